@@ -69,7 +69,21 @@ typedef enum {
                                        its fixed scratch holds */
 } molora_status;
 
-typedef enum { MOLORA_F32 = 0, MOLORA_BF16 = 1 } molora_dtype;
+/* MOLORA_E4M3 (8 bits: sign, 4 exponent, 3 fraction; largest value 448) is taken by molora_linear
+ * and as the base weights' type by molora_norm_linear_lora_apply; every other call refuses it. */
+typedef enum { MOLORA_F32 = 0, MOLORA_BF16 = 1, MOLORA_E4M3 = 2 } molora_dtype;
+
+/* Activation in molora_linear's epilogue. */
+typedef enum {
+  MOLORA_ACT_NONE = 0,
+  MOLORA_ACT_RELU = 1,
+  MOLORA_ACT_SILU = 2,      /* v / (1 + exp(-v)) */
+  MOLORA_ACT_GELU = 3,      /* v * (1 + erf(v / sqrt(2))) / 2 */
+  MOLORA_ACT_GELU_TANH = 4  /* v * (1 + tanh(u)) / 2, u = sqrt(2 / pi) * (v + 0.044715 v^3) */
+} molora_activation;
+
+/* Scores of molora_gate_topk. */
+typedef enum { MOLORA_SCORE_SOFTMAX = 0, MOLORA_SCORE_SIGMOID = 1 } molora_score;
 
 /* Which kernel family molora_lora_apply_ex uses.  AUTO, given a workspace, picks the stacked
  * path where it measured faster than dispatch + grouped (a stacked rank K*r of at least 256,
@@ -97,8 +111,12 @@ typedef enum {
 #define MOLORA_DEV_BAD_ADAPTER_ID 0x4       /* dispatch / apply: id outside [0, K); slot skipped */
 #define MOLORA_DEV_BAD_PERMUTATION 0x8      /* apply: offsets or perm inconsistent; entry skipped */
 #define MOLORA_DEV_WAIT_TIMEOUT 0x10        /* a bounded on-chip wait ran out; work abandoned */
+#define MOLORA_DEV_BAD_LOGIT 0x20           /* gate_topk: a NaN logit or bias; its expert is left out */
 
 #define MOLORA_MAX_ADAPTERS 64   /* K: hot-set size limit (the decode sweep goes to 64) */
+#define MOLORA_MAX_EXPERTS 512   /* K of molora_gate_topk: experts scored */
+#define MOLORA_MAX_GATE_K 32     /* k of molora_gate_topk: experts chosen */
+#define MOLORA_MAX_GROUPS 32     /* groups of molora_gate_topk */
 
 /* Flags of the *_ex routing calls (molora_route_vocab_ex, molora_route_vocab_dispatch_ex,
  * molora_route_vocab_lora_apply_ex): see molora_route_vocab_dispatch_ex for the promise. */
@@ -434,6 +452,112 @@ MOLORA_API molora_status molora_lora_apply_masked_pass(const void* x, molora_dty
                                             const int32_t* adapter_of, int32_t a, float scale,
                                             float* y, int32_t* err_word, molora_path path,
                                             cudaStream_t stream);
+
+/*
+ * molora_rmsnorm -- root-mean-square norm of every row, with the residual's addition before it
+ * and an optional output in 8 bits: the x that the adapter apply, the routers and the base
+ * product of a layer read.
+ *
+ *   s[t,i]    = x[t,i] + residual[t,i]                       (x alone without a residual)
+ *   sum_out   = s, rounded to dtype: the next residual
+ *   n[t,i]    = s[t,i] * rsqrt(mean_i(s[t,i]^2) + eps) * weight[i]
+ *   out       = n, rounded to dtype
+ *   scale8[t] = max(max_i |n[t,i]|, 2^-64) / 448
+ *   out8[t,i] = n[t,i] / scale8[t], rounded to e4m3 (nearest even)
+ *
+ * All in fp32 from the unrounded s.  A NaN or an infinity in a row makes its norm NaN, scale8 of
+ * that row included; so do rows whose squares overflow fp32 where s is infinite, and give 0
+ * where it is not.
+ *
+ * x        [N x d] dtype (MOLORA_BF16 or MOLORA_F32);  d >= 1
+ * residual [N x d] dtype, or NULL
+ * sum_out  [N x d] dtype, or NULL; needs residual
+ * weight   [d] dtype
+ * eps      > 0 and finite
+ * out      [N x d] dtype, or NULL;  out8 [N x d] e4m3 and scale8 fp32 [N], both or neither; out
+ *          or out8 is needed
+ * In place: each of sum_out and out may be x or residual itself (not both the same one); any
+ * other overlap of an output with another array is not allowed.
+ * One kernel, no workspace; results are reproducible bit for bit.
+ */
+MOLORA_API molora_status molora_rmsnorm(const void* x, molora_dtype dtype, int64_t N, int32_t d, const void* residual,
+                             void* sum_out, const void* weight, float eps, void* out, void* out8,
+                             float* scale8, cudaStream_t stream);
+
+/*
+ * molora_gate_topk -- expert-style gate over given logits (for a linear gate, molora_linear's
+ * x W^T): scores, a balance bias, groups, top-k and renormalised weights.
+ *
+ *   score[a]  = exp(l[a] - max l) / sum_b exp(l[b] - max l)     (MOLORA_SCORE_SOFTMAX)
+ *             = 1 / (1 + exp(-l[a]))                            (MOLORA_SCORE_SIGMOID)
+ *   choice[a] = score[a] + bias[a]; the bias moves the choice only, not the weights
+ *   groups > 1: experts [g*K/groups, (g+1)*K/groups) are group g, ranked by the sum of its
+ *             group_top (1 or 2) largest choices; the keep_groups best groups stay
+ *   ids[t]    = the k experts of the kept groups with the largest choice, descending
+ *   w[t,j]    = score[ids[t,j]], divided by the sum over the k if renormalise != 0, times scale
+ *
+ * Equal choices, and equal groups, order by the lower index first.  Scores are fp32 (the
+ * softmax's sum is exact to 46 bits and rounded once, so no result depends on an order of
+ * additions).  Without a bias, and with one group or group_top 1, the choice is the logit
+ * itself: the same order, without the ties that rounding makes.
+ * Experts with a logit of -inf (masked) or NaN, or a choice of -inf or NaN, are left out; a NaN
+ * also sets MOLORA_DEV_BAD_LOGIT.  A logit of +inf counts as the largest finite one.  A group
+ * with fewer than group_top experts left ranks behind every other.  A token with fewer than k
+ * experts left gets id -1 and weight 0 in its last slots (molora_dispatch and the applies skip
+ * those slots and set MOLORA_DEV_BAD_ADAPTER_ID).  Renormalising weights that are all 0 leaves 0.
+ *
+ * logits [N x K] dtype (MOLORA_BF16 or MOLORA_F32);  K 1..MOLORA_MAX_EXPERTS (the hot set, and
+ *        so dispatch and apply, take up to MOLORA_MAX_ADAPTERS);  bias fp32 [K] or NULL
+ * groups 1..MOLORA_MAX_GROUPS, a divisor of K with K / groups >= group_top;  keep_groups
+ *        1..groups;  k 1..MOLORA_MAX_GATE_K, at most keep_groups * K / groups;  scale finite
+ * ids int32 [N x k], w fp32 [N x k]: outputs, in molora_dispatch's and molora_lora_apply's form
+ */
+MOLORA_API molora_status molora_gate_topk(const void* logits, molora_dtype dtype, int64_t N, int32_t K, molora_score score,
+                               const float* bias, int32_t groups, int32_t keep_groups, int32_t group_top,
+                               int32_t k, int32_t renormalise, float scale, int32_t* ids, float* w,
+                               int32_t* err_word, cudaStream_t stream);
+
+/*
+ * molora_linear -- the base product of a projection, with its epilogue: the y that
+ * molora_lora_apply adds the adapters' updates to.
+ *
+ *   y[t,o] = act(x_scale[t] * w_scale[o] * sum_i x[t,i] W[o,i] + bias[o]) + residual[t,o]
+ *
+ * x [N x d_in] and W [d_out x d_in] (a row per output, the layout of stored base weights) share
+ * dtype: MOLORA_BF16, MOLORA_F32 or MOLORA_E4M3.  x_scale fp32 [N] and w_scale fp32 [d_out]: both
+ * needed with MOLORA_E4M3 (x, x_scale as molora_rmsnorm's out8, scale8), both NULL otherwise.
+ * bias fp32 [d_out] or NULL;  residual [N x d_out] of y's type or NULL, y itself allowed;
+ * y fp32 (y_bf16 = 0) or bf16 (y_bf16 = 1) [N x d_out], overwritten.
+ * Products are summed in fp32; the epilogue is fp32 and y is rounded once.  Any d_in, d_out >= 1.
+ */
+MOLORA_API molora_status molora_linear(const void* x, molora_dtype dtype, const float* x_scale, int64_t N, int32_t d_in,
+                            const void* W, const float* w_scale, int32_t d_out, const float* bias,
+                            molora_activation act, const void* residual, void* y, int32_t y_bf16,
+                            int32_t* err_word, cudaStream_t stream);
+
+/*
+ * molora_norm_linear_lora_apply -- a whole adapted projection: molora_rmsnorm, molora_linear on its
+ * output and molora_lora_apply_ex (AUTO) on both, enqueued back to back, with the results of the
+ * three calls:
+ *
+ *   sum_out, h (, h8, scale8) = molora_rmsnorm(x + residual, norm_weight, eps)
+ *   y      = h W^T + bias         or, with w_dtype = MOLORA_E4M3,  scale8 * w_scale * (h8 W^T) + bias
+ *   y[t,:] += scale * sum_j w[t,j] (h[t,:] A_{ids[t,j]}) B_{ids[t,j]}
+ *
+ * x, residual, sum_out, norm_weight, h [N x d_in], A and B: dtype, h and the others as in the three
+ * calls; sum_out needs residual, both may be NULL.  w_dtype is dtype or MOLORA_E4M3; h8 [N x d_in], scale8 fp32 [N] and
+ * w_scale fp32 [d_out] are needed with MOLORA_E4M3 and must be NULL otherwise.  h is an output: a
+ * layer's other projections read it too.  y is overwritten: fp32 (y_bf16 = 0) or bf16 (y_bf16 = 1,
+ * with molora_lora_apply_bf16y's roundings).  ids, w, k, counts, offsets, perm and ws, ws_bytes as for
+ * molora_lora_apply; only its stacked path (fp32 y) uses the workspace.
+ */
+MOLORA_API molora_status molora_norm_linear_lora_apply(
+    const void* x, molora_dtype dtype, int64_t N, int32_t d_in, const void* residual, void* sum_out,
+    const void* norm_weight, float eps, void* h, void* h8, float* scale8, const void* W, molora_dtype w_dtype,
+    const float* w_scale, int32_t d_out, const float* bias, const void* A, const void* B, int32_t K, int32_t r,
+    const int32_t* ids, const float* w, int32_t k, const int32_t* counts, const int32_t* offsets,
+    const int32_t* perm, float scale, void* y, int32_t y_bf16, void* ws, size_t* ws_bytes, int32_t* err_word,
+    cudaStream_t stream);
 
 /* The kernel family molora_lora_apply would choose for this shape when given a workspace
  * (never AUTO; without one, a STACKED choice becomes the best path that needs none). */

@@ -18,6 +18,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import math
 import os
 from typing import Optional
 
@@ -28,15 +29,17 @@ from . import build as _build
 __all__ = [
     "molora_route_vocab", "molora_router_topk", "molora_dispatch", "molora_route_vocab_dispatch",
     "molora_lora_apply", "molora_lora_apply_masked_pass", "molora_route_vocab_lora_apply",
-    "molora_router_lora_apply", "molora_select_path", "molora_workspace_bytes", "molora_lora_apply_static_ws",
+    "molora_router_lora_apply", "molora_rmsnorm", "molora_gate_topk", "molora_linear",
+    "molora_norm_linear_lora_apply", "molora_select_path", "molora_workspace_bytes", "molora_lora_apply_static_ws",
     "molora_selftest_bounded_wait", "library_path", "load_library",
     "MoloraError", "PATHS", "DEV_TOKEN_OUTSIDE_RANGES", "DEV_BAD_RANGES", "DEV_BAD_ADAPTER_ID",
-    "DEV_BAD_PERMUTATION", "DEV_WAIT_TIMEOUT", "MAX_ADAPTERS", "ROUTER_HIDDEN",
+    "DEV_BAD_PERMUTATION", "DEV_WAIT_TIMEOUT", "DEV_BAD_LOGIT", "MAX_ADAPTERS", "MAX_EXPERTS", "MAX_GATE_K",
+    "MAX_GROUPS", "ROUTER_HIDDEN", "ACTIVATIONS", "SCORES",
 ]
 
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CUDA, ERR_SCRATCH_TOO_SMALL = 0, 1, 2, 3, 4
 STATIC_SCRATCH_BYTES = 16 << 20
-F32, BF16 = 0, 1
+F32, BF16, E4M3 = 0, 1, 2
 PATHS = {"auto": 0, "scalar": 1, "grouped": 2, "dense": 3, "stacked": 4}
 PATH_NAMES = {v: k for k, v in PATHS.items()}
 DEV_TOKEN_OUTSIDE_RANGES = 0x1
@@ -44,8 +47,12 @@ DEV_BAD_RANGES = 0x2
 DEV_BAD_ADAPTER_ID = 0x4
 DEV_BAD_PERMUTATION = 0x8
 DEV_WAIT_TIMEOUT = 0x10
+DEV_BAD_LOGIT = 0x20
 INPUTS_READY = 0x1  # molora_route_vocab_dispatch_ex flag
 MAX_ADAPTERS = 64
+MAX_EXPERTS, MAX_GATE_K, MAX_GROUPS = 512, 32, 32
+ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
+SCORES = {"softmax": 0, "sigmoid": 1}
 ROUTER_HIDDEN = 64
 
 EXPORTED = ("molora_route_vocab", "molora_route_vocab_ex", "molora_router_topk", "molora_dispatch", "molora_route_vocab_dispatch",
@@ -53,7 +60,8 @@ EXPORTED = ("molora_route_vocab", "molora_route_vocab_ex", "molora_router_topk",
             "molora_lora_apply", "molora_router_lora_apply", "molora_route_vocab_lora_apply",
             "molora_lora_apply_ex", "molora_lora_apply_bf16y", "molora_lora_apply_indirect",
             "molora_lora_apply_masked_pass", "molora_select_path", "molora_status_string", "molora_version",
-            "molora_selftest_bounded_wait", "molora_lora_apply_static_ws")
+            "molora_selftest_bounded_wait", "molora_lora_apply_static_ws", "molora_rmsnorm", "molora_gate_topk",
+            "molora_linear", "molora_norm_linear_lora_apply")
 
 
 class MoloraError(RuntimeError):
@@ -102,6 +110,11 @@ def load_library(path=None):
                                                      P, P, ctypes.c_uint32, P]
     lib.molora_lora_apply_masked_pass.argtypes = [P, S, I64, I32, I32, P, P, I32, I32, P, I32, F, P, P, S, P]
     lib.molora_lora_apply_static_ws.argtypes = [P, S, I64, I32, I32, P, P, I32, I32, P, P, I32, F, P, P, P]
+    lib.molora_rmsnorm.argtypes = [P, S, I64, I32, P, P, P, F, P, P, P, P]
+    lib.molora_gate_topk.argtypes = [P, S, I64, I32, S, P, I32, I32, I32, I32, I32, F, P, P, P, P]
+    lib.molora_linear.argtypes = [P, S, P, I64, I32, P, P, I32, P, S, P, P, I32, P, P]
+    lib.molora_norm_linear_lora_apply.argtypes = [P, S, I64, I32, P, P, P, F, P, P, P, P, S, P, I32, P, P, P, I32, I32,
+                                                  P, P, I32, P, P, P, F, P, I32, P, P, P, P]
     lib.molora_select_path.argtypes = [S, I64, I32, I32, I32, I32, I32]
     lib.molora_status_string.argtypes = [S]
     lib.molora_status_string.restype = ctypes.c_char_p
@@ -111,7 +124,8 @@ def load_library(path=None):
                  "molora_route_vocab_dispatch_ex", "molora_route_vocab_lora_apply_ex", "molora_lora_apply", "molora_lora_apply_ex", "molora_lora_apply_bf16y", "molora_lora_apply_indirect",
                  "molora_router_lora_apply", "molora_route_vocab_lora_apply", "molora_lora_apply_masked_pass",
                  "molora_select_path", "molora_version", "molora_selftest_bounded_wait",
-                 "molora_lora_apply_static_ws"):
+                 "molora_lora_apply_static_ws", "molora_rmsnorm", "molora_gate_topk", "molora_linear",
+                 "molora_norm_linear_lora_apply"):
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -231,6 +245,8 @@ def _on_tensor_device(fn):
             if isinstance(a, (list, tuple)) and a and isinstance(a[0], torch.Tensor):
                 a = a[0]
             if isinstance(a, torch.Tensor) and a.is_cuda:
+                if a.device.index == torch.cuda.current_device():
+                    return fn(*args, **kwargs)
                 with torch.cuda.device(a.device):
                     return fn(*args, **kwargs)
         return fn(*args, **kwargs)
@@ -644,6 +660,231 @@ def molora_lora_apply_masked_pass(x, A, B, adapter_of, a, y, scale, err_word=Non
         _p(x), _dtype_code(x), N, d_in, d_out, _p(A), _p(B), K, r, _p(adapter_of), int(a), float(scale), _p(y),
         _p(_err_word(err_word, dev)), PATHS[path], _stream(stream, dev)))
     return y
+
+
+_TYPE_CODES = {torch.float32: F32, torch.bfloat16: BF16, torch.float8_e4m3fn: E4M3}
+
+
+def _array(t: Optional[torch.Tensor], name: str, shape, dtype, device):
+    """The device pointer of a tensor argument of this shape, dtype and device (None for None).  That
+    `device` is a GPU is checked by _on_gpu, last, so that a mis-sized argument is reported as such."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} must be a tensor")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device} (all tensors of a call share one device)")
+    return t.data_ptr()
+
+
+def _on_gpu(t: torch.Tensor, name: str):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+
+
+def _matrix(t, name: str, types):
+    """Checks a 2-D tensor argument that gives a call its sizes, and returns its dtype's code."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise ValueError(f"{name} must be a 2-D tensor")
+    if t.shape[1] < 1:
+        raise ValueError(f"{name} must have at least one column")
+    if t.dtype not in types:
+        raise ValueError(f"{name} must be one of {', '.join(str(d) for d in types)}, got {t.dtype}")
+    return _TYPE_CODES[t.dtype]
+
+
+def _named(value: str, name: str, table) -> int:
+    if value not in table:
+        raise ValueError(f"{name} must be one of {', '.join(table)}, got {value!r}")
+    return table[value]
+
+
+_FLOATS = (torch.bfloat16, torch.float32)
+
+
+def _raw_stream(stream, device) -> int:
+    if stream is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    return _stream(stream, device).value
+
+
+@_on_tensor_device
+def molora_rmsnorm(x, weight, eps=1e-6, residual=None, sum_out=None, out=None, out8=None, scale8=None, stream=None):
+    """Root-mean-square norm of x [N, d] (+ residual) by rows: returns (sum_out, out, out8, scale8).
+    ``out`` (x's dtype) is made if neither it nor out8 is given; ``sum_out`` (x + residual) is made
+    if there is a residual; out8 (float8_e4m3fn, with scale8 float32 [N]) is written if given.
+    sum_out and out may each be x or residual."""
+    code = _matrix(x, "x", _FLOATS)
+    N, d = x.shape
+    dev, dt, shape = x.device, x.dtype, x.shape
+    px = _array(x, "x", shape, dt, dev)
+    pg = _array(weight, "weight", (d,), dt, dev)
+    pr = _array(residual, "residual", shape, dt, dev)
+    if weight is None:
+        raise ValueError("weight must be a tensor")
+    if not (isinstance(eps, (int, float)) and 0.0 < eps < math.inf):
+        raise ValueError(f"eps must be positive and finite, got {eps!r}")
+    if (out8 is None) != (scale8 is None):
+        raise ValueError("out8 and scale8 go together")
+    if residual is None and sum_out is not None:
+        raise ValueError("sum_out needs a residual")
+    if residual is not None and sum_out is None:
+        sum_out = torch.empty_like(x)
+    if out is None and out8 is None:
+        out = torch.empty_like(x)
+    ps, po = _array(sum_out, "sum_out", shape, dt, dev), _array(out, "out", shape, dt, dev)
+    p8 = _array(out8, "out8", shape, torch.float8_e4m3fn, dev)
+    pc = _array(scale8, "scale8", (N,), torch.float32, dev)
+    if ps is not None and ps == po and N:
+        raise ValueError("sum_out and out must be different tensors")
+    _on_gpu(x, "x")
+    status = load_library().molora_rmsnorm(px, code, N, d, pr, ps, pg, eps, po, p8, pc, _raw_stream(stream, dev))
+    if status != OK:
+        _check("molora_rmsnorm", status)
+    return sum_out, out, out8, scale8
+
+
+@_on_tensor_device
+def molora_gate_topk(logits, k, score="softmax", bias=None, groups=1, keep_groups=1, group_top=1, renormalise=True,
+                     scale=1.0, ids=None, w=None, err_word=None, stream=None):
+    """Expert-style gate over logits [N, K] (bfloat16 or float32, K up to MAX_EXPERTS): returns
+    (ids int32 [N, k], w float32 [N, k]), the k largest of score + bias within the keep_groups best
+    of `groups` groups (each ranked by the sum of its group_top largest), with the scores as
+    weights.  A token with fewer than k experts left has id -1 and weight 0 in its last slots."""
+    code = _matrix(logits, "logits", _FLOATS)
+    N, K = logits.shape
+    dev = logits.device
+    score = _named(score, "score", SCORES)
+    if K > MAX_EXPERTS:
+        raise ValueError(f"at most {MAX_EXPERTS} experts, got {K}")
+    if not 1 <= groups <= MAX_GROUPS or K % groups:
+        raise ValueError(f"groups must be 1 to {MAX_GROUPS} and divide {K}, got {groups}")
+    if group_top not in (1, 2) or K // groups < group_top:
+        raise ValueError(f"group_top must be 1 or 2 and at most the group's {K // groups}, got {group_top}")
+    if not 1 <= keep_groups <= groups:
+        raise ValueError(f"keep_groups must be 1 to {groups}, got {keep_groups}")
+    if not 1 <= k <= min(MAX_GATE_K, keep_groups * (K // groups)):
+        raise ValueError(f"k must be 1 to {min(MAX_GATE_K, keep_groups * (K // groups))}, got {k}")
+    pl = _array(logits, "logits", logits.shape, logits.dtype, dev)
+    pb = _array(bias, "bias", (K,), torch.float32, dev)
+    if ids is None:
+        ids = torch.empty(N, k, dtype=torch.int32, device=dev)
+    if w is None:
+        w = torch.empty(N, k, dtype=torch.float32, device=dev)
+    pi, pw = _array(ids, "ids", (N, k), torch.int32, dev), _array(w, "w", (N, k), torch.float32, dev)
+    _on_gpu(logits, "logits")
+    status = load_library().molora_gate_topk(
+        pl, code, N, K, score, pb, groups, keep_groups, group_top, k, 1 if renormalise else 0, scale, pi, pw,
+        _p(_err_word(err_word, dev)), _raw_stream(stream, dev))
+    if status != OK:
+        _check("molora_gate_topk", status)
+    return ids, w
+
+
+def _y(y, N, d_out, dtype, device):
+    if y is None:
+        return torch.empty(N, d_out, dtype=dtype, device=device)
+    if not isinstance(y, torch.Tensor) or y.dtype not in _FLOATS:
+        raise ValueError("y must be a float32 or bfloat16 tensor")
+    return y
+
+
+@_on_tensor_device
+def molora_linear(x, W, y=None, x_scale=None, w_scale=None, bias=None, act="none", residual=None,
+                  out_dtype=torch.float32, err_word=None, stream=None):
+    """y = act(x W^T + bias) + residual for x [N, d_in] and W [d_out, d_in] in bfloat16, float32 or
+    float8_e4m3fn (then with float32 scales x_scale [N] and w_scale [d_out]).  ``y``: the output
+    (float32 or bfloat16, residual's dtype; residual itself is allowed), else made in ``out_dtype``."""
+    code = _matrix(x, "x", (torch.bfloat16, torch.float32, torch.float8_e4m3fn))
+    N, d_in = x.shape
+    dev = x.device
+    if not isinstance(W, torch.Tensor) or W.dim() != 2 or W.shape[0] < 1:
+        raise ValueError("W must be a 2-D tensor [d_out, d_in]")
+    d_out = W.shape[0]
+    act = _named(act, "act", ACTIVATIONS)
+    fp8 = code == E4M3
+    if fp8 != (x_scale is not None) or fp8 != (w_scale is not None):
+        raise ValueError("x_scale and w_scale are needed with float8_e4m3fn, and with nothing else")
+    px = _array(x, "x", x.shape, x.dtype, dev)
+    pw = _array(W, "W", (d_out, d_in), x.dtype, dev)
+    psx = _array(x_scale, "x_scale", (N,), torch.float32, dev)
+    psw = _array(w_scale, "w_scale", (d_out,), torch.float32, dev)
+    pb = _array(bias, "bias", (d_out,), torch.float32, dev)
+    y = _y(y, N, d_out, out_dtype, dev)
+    pres = _array(residual, "residual", (N, d_out), y.dtype, dev)
+    py = _array(y, "y", (N, d_out), y.dtype, dev)
+    _on_gpu(x, "x")
+    status = load_library().molora_linear(
+        px, code, psx, N, d_in, pw, psw, d_out, pb, act, pres, py, 1 if y.dtype == torch.bfloat16 else 0,
+        _p(_err_word(err_word, dev)), _raw_stream(stream, dev))
+    if status != OK:
+        _check("molora_linear", status)
+    return y
+
+
+@_on_tensor_device
+def molora_norm_linear_lora_apply(x, norm_weight, eps, W, A, B, ids, y, scale, w=None, counts=None, offsets=None,
+                                  perm=None, residual=None, sum_out=None, h=None, h8=None, scale8=None, w_scale=None,
+                                  bias=None, err_word=None, ws=None, stream=None):
+    """A whole adapted projection: molora_rmsnorm of x (+ residual) into h, y = h W^T + bias, then
+    molora_lora_apply of h in place on y.  With float8_e4m3fn W [d_out, d_in] (and w_scale [d_out])
+    the base product reads the norm's 8-bit output.  Returns (y, sum_out, h, h8, scale8); the
+    buffers that are not given are made."""
+    code = _matrix(x, "x", _FLOATS)
+    N, d_in = x.shape
+    dev, dt, f32, i32 = x.device, x.dtype, torch.float32, torch.int32
+    if not isinstance(W, torch.Tensor) or W.dim() != 2 or W.shape[0] < 1 or W.dtype not in (dt, torch.float8_e4m3fn):
+        raise ValueError("W must be [d_out, d_in] of x's dtype or float8_e4m3fn")
+    d_out = W.shape[0]
+    fp8 = W.dtype == torch.float8_e4m3fn
+    if not isinstance(A, torch.Tensor) or not isinstance(B, torch.Tensor) or A.dim() != 3 or B.dim() != 3:
+        raise ValueError("A must be [K, d_in, r] and B [K, r, d_out]")
+    K, r = A.shape[0], A.shape[2]
+    k = _slots(ids, N)
+    if fp8 != (w_scale is not None) or (not fp8 and (h8 is not None or scale8 is not None)):
+        raise ValueError("w_scale is needed, and h8 and scale8 are taken, with float8_e4m3fn W only")
+    if norm_weight is None:
+        raise ValueError("norm_weight must be a tensor")
+    if not (isinstance(eps, (int, float)) and 0.0 < eps < math.inf):
+        raise ValueError(f"eps must be positive and finite, got {eps!r}")
+    if residual is None and sum_out is not None:
+        raise ValueError("sum_out needs a residual")
+    if not isinstance(y, torch.Tensor) or y.dtype not in _FLOATS:
+        raise ValueError("y must be a float32 or bfloat16 tensor")
+    px = _array(x, "x", x.shape, dt, dev)
+    if residual is not None and sum_out is None:
+        sum_out = torch.empty_like(x)
+    if h is None:
+        h = torch.empty_like(x)
+    if fp8 and h8 is None:
+        h8 = torch.empty(N, d_in, dtype=torch.float8_e4m3fn, device=dev)
+    if fp8 and scale8 is None:
+        scale8 = torch.empty(N, dtype=f32, device=dev)
+    if sum_out is not None and N and h.data_ptr() == sum_out.data_ptr():
+        raise ValueError("h and sum_out must be different tensors")
+    args = (px, code, N, d_in, _array(residual, "residual", x.shape, dt, dev), _array(sum_out, "sum_out", x.shape, dt, dev),
+            _array(norm_weight, "norm_weight", (d_in,), dt, dev), eps, _array(h, "h", x.shape, dt, dev),
+            _array(h8, "h8", x.shape, torch.float8_e4m3fn, dev), _array(scale8, "scale8", (N,), f32, dev),
+            _array(W, "W", (d_out, d_in), W.dtype, dev), _TYPE_CODES[W.dtype], _array(w_scale, "w_scale", (d_out,), f32, dev),
+            d_out, _array(bias, "bias", (d_out,), f32, dev), _array(A, "A", (K, d_in, r), dt, dev),
+            _array(B, "B", (K, r, d_out), dt, dev), K, r, _array(ids, "ids", ids.shape, i32, dev),
+            _array(w, "w", ids.shape, f32, dev), k, _array(counts, "counts", (K,), i32, dev),
+            _array(offsets, "offsets", (K + 1,), i32, dev), _array(perm, "perm", (N * k,), i32, dev), scale,
+            _array(y, "y", (N, d_out), y.dtype, dev), 1 if y.dtype == torch.bfloat16 else 0)
+    _on_gpu(x, "x")
+    tail = (_p(_err_word(err_word, dev)), _raw_stream(stream, dev))
+    lib = load_library()
+
+    def call(ws_ptr, ws_bytes):
+        return lib.molora_norm_linear_lora_apply(*args, ws_ptr, ws_bytes, *tail)
+    _check("molora_norm_linear_lora_apply", _workspace(ws, dev, call))
+    return y, sum_out, h, h8, scale8
 
 
 @_on_tensor_device

@@ -156,6 +156,36 @@ static molora_status apply_impl(const void* x, molora_dtype dtype, int64_t N, in
                                       y_bf16, -1, err_word, stream, table));
 }
 
+// molora_linear's checks.  With N == 0 no pointer is looked at.
+static molora_status check_linear(const LinearArgs& a) {
+  if (!(valid_dtype(a.dtype) || a.dtype == MOLORA_E4M3) || a.N < 0 || a.N > INT32_MAX || a.d_in < 1 || a.d_out < 1 ||
+      a.act < MOLORA_ACT_NONE || a.act > MOLORA_ACT_GELU_TANH)
+    return MOLORA_ERR_INVALID_ARG;
+  if (a.N == 0) return MOLORA_OK;
+  if (!a.x || !a.W || !a.y) return MOLORA_ERR_INVALID_ARG;
+  if ((a.dtype == MOLORA_E4M3) != (a.x_scale != nullptr) || (a.dtype == MOLORA_E4M3) != (a.w_scale != nullptr))
+    return MOLORA_ERR_INVALID_ARG;
+  return MOLORA_OK;
+}
+
+static molora_status linear_impl(const LinearArgs& a, cudaStream_t stream) {
+  const molora_status st = check_linear(a);
+  if (st != MOLORA_OK || a.N == 0) return st;
+  return launched(launch_linear_scalar(a, stream));
+}
+
+static molora_status check_rmsnorm(const void* x, molora_dtype dtype, int64_t N, int32_t d, const void* residual,
+                                   const void* sum_out, const void* weight, float eps, const void* out,
+                                   const void* out8, const float* scale8) {
+  if (!valid_dtype(dtype) || N < 0 || N > INT32_MAX || d < 1 || !(eps > 0.f) || !(eps <= 3.4e38f))
+    return MOLORA_ERR_INVALID_ARG;
+  if (N == 0) return MOLORA_OK;
+  if (!x || !weight || (!out && !out8) || (out8 != nullptr) != (scale8 != nullptr) || (sum_out && !residual) ||
+      (sum_out && sum_out == out))
+    return MOLORA_ERR_INVALID_ARG;
+  return MOLORA_OK;
+}
+
 }  // namespace molora
 
 using namespace molora;
@@ -365,6 +395,74 @@ molora_status molora_lora_apply_static_ws(const void* x, molora_dtype dtype, int
   if (stacked_static_scratch(&scratch) != cudaSuccess) return MOLORA_ERR_CUDA;
   return launched(launch_lora_stacked(x, N, d_in, d_out, A, B, K, r, ids, w, k, scale, y, scratch, err_word, nullptr,
                                       nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, stream));
+}
+
+molora_status molora_rmsnorm(const void* x, molora_dtype dtype, int64_t N, int32_t d, const void* residual, void* sum_out,
+                             const void* weight, float eps, void* out, void* out8, float* scale8,
+                             cudaStream_t stream) {
+  const molora_status st = check_rmsnorm(x, dtype, N, d, residual, sum_out, weight, eps, out, out8, scale8);
+  if (st != MOLORA_OK || N == 0) return st;
+  return launched(launch_rmsnorm(x, dtype, N, d, residual, sum_out, weight, eps, out, out8, scale8, stream));
+}
+
+molora_status molora_gate_topk(const void* logits, molora_dtype dtype, int64_t N, int32_t K, molora_score score,
+                               const float* bias, int32_t groups, int32_t keep_groups, int32_t group_top, int32_t k,
+                               int32_t renormalise, float scale, int32_t* ids, float* w, int32_t* err_word,
+                               cudaStream_t stream) {
+  if (!valid_dtype(dtype) || N < 0 || N > INT32_MAX || K < 1 || K > MOLORA_MAX_EXPERTS ||
+      (score != MOLORA_SCORE_SOFTMAX && score != MOLORA_SCORE_SIGMOID) || groups < 1 || groups > MOLORA_MAX_GROUPS ||
+      K % groups || keep_groups < 1 || keep_groups > groups || (group_top != 1 && group_top != 2) ||
+      K / groups < group_top || k < 1 || k > MOLORA_MAX_GATE_K || k > keep_groups * (K / groups) ||
+      !(scale >= -3.4e38f && scale <= 3.4e38f))
+    return MOLORA_ERR_INVALID_ARG;
+  if (N == 0) return MOLORA_OK;
+  if (!logits || !ids || !w) return MOLORA_ERR_INVALID_ARG;
+  return launched(launch_gate_topk(logits, dtype, N, K, score == MOLORA_SCORE_SIGMOID, bias, groups, keep_groups,
+                                   group_top, k, renormalise != 0, scale, ids, w, err_word, stream));
+}
+
+molora_status molora_linear(const void* x, molora_dtype dtype, const float* x_scale, int64_t N, int32_t d_in,
+                            const void* W, const float* w_scale, int32_t d_out, const float* bias,
+                            molora_activation act, const void* residual, void* y, int32_t y_bf16, int32_t* err_word,
+                            cudaStream_t stream) {
+  const LinearArgs a = {x, dtype, x_scale, N, d_in, W, w_scale, d_out, bias, act, residual, y, y_bf16 != 0, err_word};
+  return linear_impl(a, stream);
+}
+
+molora_status molora_norm_linear_lora_apply(const void* x, molora_dtype dtype, int64_t N, int32_t d_in,
+                                            const void* residual, void* sum_out, const void* norm_weight, float eps,
+                                            void* h, void* h8, float* scale8, const void* W, molora_dtype w_dtype,
+                                            const float* w_scale, int32_t d_out, const float* bias, const void* A,
+                                            const void* B, int32_t K, int32_t r, const int32_t* ids, const float* w,
+                                            int32_t k, const int32_t* counts, const int32_t* offsets,
+                                            const int32_t* perm, float scale, void* y, int32_t y_bf16, void* ws,
+                                            size_t* ws_bytes, int32_t* err_word, cudaStream_t stream) {
+  const bool fp8 = w_dtype == MOLORA_E4M3;
+  if (!fp8 && w_dtype != dtype) return MOLORA_ERR_INVALID_ARG;
+  if (ws_bytes && !ws) {  // a query, as molora_lora_apply's; bf16 y takes no workspace
+    if (!y_bf16)
+      return apply_impl(nullptr, dtype, N, d_in, d_out, nullptr, nullptr, K, r, nullptr, nullptr, k, nullptr, nullptr,
+                        nullptr, scale, nullptr, false, nullptr, MOLORA_PATH_AUTO, stream, nullptr, nullptr, ws_bytes);
+    *ws_bytes = 0;
+    return check_apply_sizes(dtype, N, d_in, d_out, K, r, k);
+  }
+  // every argument of the three steps is checked before the first of them is enqueued
+  const LinearArgs lin = {fp8 ? h8 : h, w_dtype, scale8, N, d_in, W, w_scale, d_out, bias, MOLORA_ACT_NONE, nullptr, y,
+                          y_bf16 != 0, err_word};
+  molora_status st = check_rmsnorm(x, dtype, N, d_in, residual, sum_out, norm_weight, eps, h, h8, scale8);
+  if (st == MOLORA_OK) st = check_linear(lin);
+  if (st == MOLORA_OK) st = check_apply_args(h, dtype, N, d_in, d_out, A, B, K, r, ids, k, y);
+  if (st != MOLORA_OK || N == 0) return st;
+  if (ws && (reinterpret_cast<uintptr_t>(ws) & 255u)) return MOLORA_ERR_INVALID_ARG;
+  if (y_bf16 == 0 && ws_bytes && molora_select_path(dtype, N, d_in, d_out, K, r, k) == MOLORA_PATH_STACKED &&
+      *ws_bytes < stacked_workspace_bytes(N, K, r))
+    return MOLORA_ERR_INVALID_ARG;
+  if (launch_rmsnorm(x, dtype, N, d_in, residual, sum_out, norm_weight, eps, h, h8, scale8, stream) != cudaSuccess)
+    return MOLORA_ERR_CUDA;
+  st = linear_impl(lin, stream);
+  if (st != MOLORA_OK) return st;
+  return apply_impl(h, dtype, N, d_in, d_out, A, B, K, r, ids, w, k, counts, offsets, perm, scale, y, y_bf16 != 0,
+                    err_word, MOLORA_PATH_AUTO, stream, nullptr, y_bf16 ? nullptr : ws, y_bf16 ? nullptr : ws_bytes);
 }
 
 const char* molora_status_string(molora_status status) {

@@ -611,6 +611,9 @@ __device__ __forceinline__ void router_rows(const float* recv, int C, int rows, 
                          coef, tid, nthreads, store);
 }
 
+__device__ __forceinline__ float to_float(float v) { return v; }
+__device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+
 __device__ __forceinline__ float bf16_bits_to_float(uint16_t b) { return __uint_as_float(((uint32_t)b) << 16); }
 
 }  // namespace molora

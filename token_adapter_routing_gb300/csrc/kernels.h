@@ -94,6 +94,33 @@ cudaError_t launch_router_tc(const void* x, int64_t N, int32_t d_in, const void*
                              const void* W2, const float* b2, int32_t K, int32_t k, float* logits,
                              int32_t* ids, float* w, cudaStream_t stream);
 
+cudaError_t launch_rmsnorm(const void* x, molora_dtype dtype, int64_t N, int32_t d, const void* residual, void* sum_out,
+                           const void* weight, float eps, void* out, void* out8, float* scale8, cudaStream_t stream);
+
+cudaError_t launch_gate_topk(const void* logits, molora_dtype dtype, int64_t N, int32_t K, bool sigmoid,
+                             const float* bias, int32_t groups, int32_t keep, int32_t group_top, int32_t k, bool renorm,
+                             float scale, int32_t* ids, float* w, int32_t* err_word, cudaStream_t stream);
+
+// The base product's arguments (molora_linear).
+struct LinearArgs {
+  const void* x;
+  molora_dtype dtype;
+  const float* x_scale;
+  int64_t N;
+  int32_t d_in;
+  const void* W;
+  const float* w_scale;
+  int32_t d_out;
+  const float* bias;
+  molora_activation act;
+  const void* residual;
+  void* y;
+  bool y_bf16;
+  int32_t* err_word;
+};
+// CUDA-core product: any type, size and alignment.
+cudaError_t launch_linear_scalar(const LinearArgs& a, cudaStream_t stream);
+
 int num_sms();
 
 cudaError_t launch_bounded_wait_selftest(uint64_t limit_ns, int32_t* err_word, cudaStream_t stream);
