@@ -349,7 +349,8 @@ def check_linear(y, x, W, sx, sw, bias, act, res):
 
 SIZES = [(1, 64, 64), (1, 4096, 1000), (2, 128, 7), (3, 33, 5), (7, 200, 257), (8, 2048, 512), (16, 512, 129), (17, 640, 384),
          (31, 1031, 517), (33, 4096, 96), (64, 96, 64), (65, 256, 1024), (127, 512, 260), (128, 64, 128), (129, 1024, 256),
-         (200, 72, 200), (257, 2048, 320), (300, 24, 24), (513, 1, 1), (700, 136, 1032), (1024, 512, 768)]
+         (200, 72, 200), (257, 2048, 320), (300, 24, 24), (513, 1, 1), (700, 136, 1032), (1024, 512, 768),
+         (2500, 272, 2056), (3001, 1024, 1100), (4097, 64, 1333), (20000, 128, 160)]
 
 
 @pytest.mark.parametrize("N, d_in, d_out", SIZES)
@@ -370,7 +371,8 @@ def test_linear(m, N, d_in, d_out, dtype, y_dtype, bias, act, residual):
     assert (buf[N:] == 7).all()
 
 
-@pytest.mark.parametrize("N, d_in, d_out", [(1, 512, 512), (5, 64, 40), (40, 1024, 136), (130, 320, 264), (600, 4096, 512), (2, 333, 31)])
+@pytest.mark.parametrize("N, d_in, d_out", [(1, 512, 512), (5, 64, 40), (40, 1024, 136), (130, 320, 264), (600, 4096, 512), (2, 333, 31),
+                                            (2900, 160, 2100), (2600, 512, 2052), (5000, 96, 1031)])
 @pytest.mark.parametrize("dtype", [BF, FP8, F32])
 def test_linear_integers_are_exact(m, N, d_in, d_out, dtype):
     g = gen(d_in)
@@ -386,7 +388,7 @@ def test_linear_integers_are_exact(m, N, d_in, d_out, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF, FP8, F32])
-@pytest.mark.parametrize("N, d_in, d_out", [(4, 256, 96), (150, 256, 192)])
+@pytest.mark.parametrize("N, d_in, d_out", [(4, 256, 96), (150, 256, 192), (4000, 64, 1024)])
 def test_linear_unaligned_and_in_place(m, dtype, N, d_in, d_out):
     g = gen(11)
     x, W, sx, sw = linear_inputs(g, N, d_in, d_out, dtype)

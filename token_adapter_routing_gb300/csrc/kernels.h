@@ -120,6 +120,9 @@ struct LinearArgs {
 };
 // CUDA-core product: any type, size and alignment.
 cudaError_t launch_linear_scalar(const LinearArgs& a, cudaStream_t stream);
+// tcgen05 product: bf16 or e4m3 operands whose rows start on 16-byte boundaries.
+bool linear_tc_supported(const LinearArgs& a);
+cudaError_t launch_linear_tc(const LinearArgs& a, cudaStream_t stream);
 
 int num_sms();
 

@@ -1,0 +1,679 @@
+// linear_tc.cu -- the base product with its epilogue on the 5th-generation tensor cores, bf16 or
+// e4m3 operands with fp32 accumulators in TMEM:
+//
+//   y[t,o] = act(sx[t] * sw[o] * sum_i x[t,i] W[o,i] + bias[o]) + residual[t,o]
+//
+// x and W are both rows along d_in (K-major), so a stage of either is a 128-byte-swizzled box of
+// rows x 128 bytes, 64 bf16 or 128 e4m3 elements of K, and the two types differ in the MMA's kind and
+// in nothing else.  Elements past the arrays' ends are loaded as zeros and never stored.
+//
+// linear_tc_kernel (many tokens): a persistent kernel over tiles of 256 tokens x BN outputs, each made
+//   by a pair of CTAs with cta_group::2 MMAs.  Each CTA loads its 128 token rows and half of the
+//   tile's W rows: a pair reads every operand byte once from shared memory per MMA, which
+//   one CTA alone cannot feed at full rate.  A TMA warp and an MMA warp run ahead of 8 epilogue
+//   warps by two TMEM accumulators.
+// linear_skinny_kernel (few tokens): W's rows are the MMA's M (128 outputs a CTA), the tokens its N
+//   (16 .. 256), so that no MMA row is spent on tokens that are not there; d_in is split over a
+//   cluster of CTAs whose partial sums meet through distributed shared memory in rank order.
+#include <cudaTypedefs.h>
+
+#include <atomic>
+#include <mutex>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "linear.cuh"
+
+namespace molora {
+
+namespace {
+
+constexpr int kRows = 128;          // rows of a box of x (or of W in the skinny kernel) = TMEM lanes
+constexpr uint32_t kRowBytes = 128; // bytes of K per stage
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 32 * (kEpiWarps + 2);  // + TMA warp (8) + MMA warp (9)
+constexpr int kMaxStages = 8;
+constexpr size_t kMaxSmem = 227 * 1024;
+constexpr size_t kSmemSlack = 1024;
+constexpr uint32_t kBox = 4096;     // epilogue staging per warp: 32 rows x 32 columns of fp32
+
+struct __align__(8) LCtrl {
+  uint64_t full[kMaxStages];
+  uint64_t empty[kMaxStages];
+  uint64_t tfull[2];
+  uint64_t tempty[2];
+  uint64_t done;
+  uint32_t tmem_base;
+  int32_t abort;
+};
+
+// What the epilogue reads and writes.
+struct Epi {
+  const float* sx;
+  const float* sw;
+  const float* bias;
+  const void* res;
+  void* y;
+  int64_t N;
+  int32_t d_out;
+  molora_activation act;
+  bool y_bf16;
+  bool col_vec;  // sw and bias may be read in 16-byte vectors
+  bool tma_y;    // y through its tensor map, residual in 16-byte vectors
+};
+
+struct TcPlan {
+  int BN;                // outputs per tile
+  int S;                 // stages
+  int nkb;               // K blocks of 128 bytes
+  int group;             // token tiles per group of tiles (they share W's rows in L2)
+  int64_t m_tiles, tiles;
+  int32_t n_tiles;
+  uint32_t stage_bytes, off_b, off_stage, off_ctrl, tmem_cols, smem;
+};
+
+__device__ __forceinline__ void apply_act(float (&v)[32], molora_activation act) {
+  if (act == MOLORA_ACT_NONE) return;
+  if (act == MOLORA_ACT_RELU) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = activate_fast(v[i], MOLORA_ACT_RELU);
+  } else if (act == MOLORA_ACT_SILU) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = activate_fast(v[i], MOLORA_ACT_SILU);
+  } else if (act == MOLORA_ACT_GELU_TANH) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = activate_fast(v[i], MOLORA_ACT_GELU_TANH);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = activate_fast(v[i], MOLORA_ACT_GELU);
+  }
+}
+
+// v[i] = op(v[i], p[n0 + i]) over a chunk of 32 columns; p is the same for every lane.
+template <typename F>
+__device__ __forceinline__ void per_column(float (&v)[32], const float* p, int n0, int d_out, bool vec, F op) {
+  if (vec && n0 + 32 <= d_out) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float4 q = *reinterpret_cast<const float4*>(p + n0 + 4 * i);
+      v[4 * i] = op(v[4 * i], q.x), v[4 * i + 1] = op(v[4 * i + 1], q.y);
+      v[4 * i + 2] = op(v[4 * i + 2], q.z), v[4 * i + 3] = op(v[4 * i + 3], q.w);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (n0 + i < d_out) v[i] = op(v[i], p[n0 + i]);
+  }
+}
+
+// v += 32 residual columns of a row in 16-byte vectors, those past d_out left out (a multiple of
+// the vector's elements).
+__device__ __forceinline__ void add_residual(float (&v)[32], const void* res, bool bf16, int64_t at, int cols) {
+  if (bf16) {
+    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(res) + at);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (8 * i < cols) {
+        const uint4 q = p[i];
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          v[8 * i + 2 * j] += __uint_as_float(w[j] << 16);
+          v[8 * i + 2 * j + 1] += __uint_as_float(w[j] & 0xffff0000u);
+        }
+      }
+  } else {
+    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(res) + at);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (4 * i < cols) {
+        const float4 q = p[i];
+        v[4 * i] += q.x, v[4 * i + 1] += q.y, v[4 * i + 2] += q.z, v[4 * i + 3] += q.w;
+      }
+  }
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&p);
+}
+
+}  // namespace
+
+template <bool kFp8>
+__global__ void __launch_bounds__(kThreads, 1)
+    linear_tc_kernel(const Epi E, const TcPlan P, int32_t* err_word, const __grid_constant__ CUtensorMap map_x,
+                     const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_y) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  LCtrl* ctrl = reinterpret_cast<LCtrl*>(sm + P.off_ctrl);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int BN = P.BN, S = P.S, nkb = P.nkb;
+  const uint32_t rank = cluster_ctarank();
+  const int64_t pair = blockIdx.x / 2, pairs = gridDim.x / 2;
+  volatile int32_t* abort = &ctrl->abort;
+  // tiles in groups of P.group token tiles: within a group, the token tile runs fastest
+  auto tile_at = [&](int64_t pt, int32_t& m0, int32_t& n0) {
+    const int64_t span = (int64_t)P.group * P.n_tiles, grp = pt / span;
+    const int64_t first = grp * P.group, left = P.m_tiles - first, rows = left < P.group ? left : P.group;
+    const int64_t in = pt - grp * span;
+    m0 = (int32_t)((first + in % rows) * 2 * kRows + rank * kRows);
+    n0 = (int32_t)(in / rows) * BN;
+  };
+
+  if (warp == 9) {
+    tmem_alloc_pair(&ctrl->tmem_base, P.tmem_cols);
+    tmem_relinquish_pair();
+  }
+  if (warp == 8 && lane == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&ctrl->full[s], 1);
+      mbar_init(&ctrl->empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&ctrl->tfull[b], 1);
+      mbar_init(&ctrl->tempty[b], 2 * kEpiWarps);
+    }
+    mbar_init(&ctrl->done, 1);
+    ctrl->abort = 0;
+    mbar_fence_init();
+    tma_prefetch_desc(&map_x);
+    tma_prefetch_desc(&map_w);
+    if (E.tma_y) tma_prefetch_desc(&map_y);
+  }
+  pdl_wait();
+  __syncthreads();
+  // only now, with this CTA's TMEM held, may the next kernel's CTAs come and ask for theirs
+  pdl_launch_dependents();
+  tc_fence_after();
+  const uint32_t tmem = ctrl->tmem_base;
+  cluster_sync();  // both CTAs' barriers are initialised before either signals the other's
+
+  if (warp == 8) {
+    if (lane == 0) {
+      const int elems = kFp8 ? 128 : 64;  // K elements per stage
+      int s = 0, issued = 0;
+      uint32_t phase = 1;  // the first use of a stage finds it empty
+      bool ok = true;
+      for (int64_t pt = pair; pt < P.tiles && ok; pt += pairs) {
+        int32_t m0, n0;
+        tile_at(pt, m0, n0);
+        for (int kb = 0; kb < nkb; ++kb) {
+          if (issued >= S && !mbar_wait_or_abort(&ctrl->empty[s], phase, abort)) {
+            ok = false;
+            break;
+          }
+          // the leader's barrier counts both CTAs' bytes
+          const uint32_t bar = dsmem_addr(smem_u32(&ctrl->full[s]), 0);
+          if (rank == 0) mbar_arrive_expect_tx(&ctrl->full[s], 2 * P.stage_bytes);
+          uint8_t* st = sm + (size_t)s * P.stage_bytes;
+          tma_load_2d_pair(smem_u32(st), &map_x, kb * elems, m0, bar);
+          tma_load_2d_pair(smem_u32(st + P.off_b), &map_w, kb * elems, n0 + (int32_t)rank * (BN / 2), bar);
+          if (issued < S) ++issued;
+          if (++s == S) s = 0, phase ^= 1;
+        }
+      }
+      // the last fill of every stage has been consumed before the CTA leaves
+      for (int i = 0; i < issued; ++i) {
+        if (issued < S) {
+          mbar_wait(&ctrl->empty[i], 0);
+        } else {
+          mbar_wait(&ctrl->empty[s], phase);
+          if (++s == S) s = 0, phase ^= 1;
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 9) {
+    if (lane == 0 && rank == 0) {
+      const uint32_t idesc = kFp8 ? idesc_e4m3_f32(2 * kRows, (uint32_t)BN) : idesc_bf16_f32(2 * kRows, (uint32_t)BN, false, false);
+      int s = 0, tc = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int64_t pt = pair; pt < P.tiles && ok; pt += pairs, ++tc) {
+        const int buf = tc & 1;
+        if (tc >= 2 && !mbar_wait_or_abort(&ctrl->tempty[buf], (uint32_t)((tc >> 1) - 1) & 1u, abort)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d = tmem + (uint32_t)(buf * (P.tmem_cols / 2));
+        for (int kb = 0; kb < nkb; ++kb) {
+          if (!mbar_wait_or_abort(&ctrl->full[s], phase, abort)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint8_t* st = sm + (size_t)s * P.stage_bytes;
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks) {
+            const uint64_t da = smem_desc(smem_u32(st) + ks * 32, 16, 1024, kSwizzle128B);
+            const uint64_t db = smem_desc(smem_u32(st + P.off_b) + ks * 32, 16, 1024, kSwizzle128B);
+            if (kFp8)
+              umma_f8_pair(d, da, db, idesc, (kb | ks) != 0);
+            else
+              umma_f16_pair(d, da, db, idesc, (kb | ks) != 0);
+          }
+          umma_commit_pair(&ctrl->empty[s]);
+          if (++s == S) s = 0, phase ^= 1;
+        }
+        if (!ok) break;
+        umma_commit_pair(&ctrl->tfull[buf]);
+      }
+      if (!ok) report(err_word, MOLORA_DEV_WAIT_TIMEOUT);
+      umma_commit_pair(&ctrl->done);  // arrives in both CTAs once every MMA has completed
+    }
+    __syncwarp();
+  } else {
+    // epilogue: warps w and w + 4 share 32 rows and take half of the columns each
+    const int quarter = warp & 3, half = warp >> 2;
+    const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+    uint8_t* box = sm + P.off_stage + (size_t)warp * kBox;
+    int tc = 0;
+    for (int64_t pt = pair; pt < P.tiles; pt += pairs, ++tc) {
+      const int buf = tc & 1;
+      int32_t m0, n0;
+      tile_at(pt, m0, n0);
+      m0 += quarter * 32;
+      n0 += half * (BN / 2);
+      const int64_t t = (int64_t)m0 + lane;
+      const float sx = E.sx && t < E.N ? E.sx[t] : 1.f;
+      if (!__all_sync(0xffffffffu, mbar_wait_or_abort(&ctrl->tfull[buf], (uint32_t)(tc >> 1) & 1u, abort))) break;
+      tc_fence_after();
+      const uint32_t base = tmem + lanes + (uint32_t)(buf * (P.tmem_cols / 2) + half * (BN / 2));
+      const int chunks = m0 < E.N ? min(BN / 64, (E.d_out - n0 + 31) / 32) : 0;
+      for (int c = 0; c < chunks; ++c) {
+        const int col = n0 + c * 32;
+        uint32_t r[32];
+        tmem_ld32_start(base + (uint32_t)(c * 32), r);
+        tmem_ld_wait(r);
+        float v[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+        if (E.sx) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] *= sx;
+          per_column(v, E.sw, col, E.d_out, E.col_vec, [](float a, float b) { return a * b; });
+        }
+        if (E.bias) per_column(v, E.bias, col, E.d_out, E.col_vec, [](float a, float b) { return a + b; });
+        apply_act(v, E.act);
+        if (E.tma_y) {
+          if (E.res && t < E.N) add_residual(v, E.res, E.y_bf16, t * E.d_out + col, E.d_out - col);
+          if (lane == 0) bulk_wait_read<0>();  // the last store from this box has read it
+          __syncwarp();
+          if (E.y_bf16) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              *reinterpret_cast<uint4*>(box + swz_offset((uint32_t)lane, (uint32_t)i, 64)) =
+                  make_uint4(pack_bf16(v[8 * i], v[8 * i + 1]), pack_bf16(v[8 * i + 2], v[8 * i + 3]),
+                             pack_bf16(v[8 * i + 4], v[8 * i + 5]), pack_bf16(v[8 * i + 6], v[8 * i + 7]));
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              *reinterpret_cast<float4*>(box + sw128_offset((uint32_t)lane, (uint32_t)i)) =
+                  make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_2d(&map_y, smem_u32(box), col, m0);
+            bulk_commit();
+          }
+        } else {
+          // rows that are not 16-byte aligned: turned in shared memory, written a row at a time
+          float* turn = reinterpret_cast<float*>(box);
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) turn[lane * 32 + (i ^ lane)] = v[i];
+          __syncwarp();
+          for (int q = 0; q < 32 && m0 + q < E.N; ++q) {
+            if (col + lane >= E.d_out) continue;
+            const int64_t at = ((int64_t)m0 + q) * E.d_out + col + lane;
+            float o = turn[q * 32 + (lane ^ q)];
+            if (E.y_bf16) {
+              if (E.res) o += to_float(static_cast<const __nv_bfloat16*>(E.res)[at]);
+              static_cast<__nv_bfloat16*>(E.y)[at] = __float2bfloat16_rn(o);
+            } else {
+              if (E.res) o += static_cast<const float*>(E.res)[at];
+              static_cast<float*>(E.y)[at] = o;
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(dsmem_addr(smem_u32(&ctrl->tempty[buf]), 0));
+    }
+    if (lane == 0) bulk_wait_all();
+    __syncwarp();
+  }
+  if (warp == 9 && lane == 0) mbar_wait(&ctrl->done, 0);
+  __syncthreads();
+  cluster_sync();  // neither CTA leaves, nor frees its TMEM, while the other may still signal or use it
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, P.tmem_cols);
+  }
+}
+
+// ---------------------------------------------------------------------------------------------
+struct SkinnyPlan {
+  int BN;                // tokens per tile (MMA N)
+  int C;                 // CTAs of a cluster: d_in split C ways
+  int S;
+  int nkb;
+  int32_t o_tiles, t_tiles;
+  uint32_t stage_bytes, off_b, off_ctrl, tmem_cols, smem;
+};
+
+template <bool kFp8>
+__global__ void __launch_bounds__(kThreads, 1)
+    linear_skinny_kernel(const Epi E, const SkinnyPlan P, int32_t* err_word, const __grid_constant__ CUtensorMap map_x,
+                         const __grid_constant__ CUtensorMap map_w) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  LCtrl* ctrl = reinterpret_cast<LCtrl*>(sm + P.off_ctrl);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int BN = P.BN, S = P.S, C = P.C;
+  const int rank = (int)cluster_ctarank();
+  const unsigned tile = blockIdx.x / (unsigned)C;
+  const int32_t o0 = (int32_t)(tile % (unsigned)P.o_tiles) * kRows, t0 = (int32_t)(tile / (unsigned)P.o_tiles) * BN;
+  const int kb0 = (int)((int64_t)P.nkb * rank / C), kb1 = (int)((int64_t)P.nkb * (rank + 1) / C);
+  const int tokens = (int)min((int64_t)BN, E.N - t0);
+  volatile int32_t* abort = &ctrl->abort;
+
+  if (warp == 9) {
+    tmem_alloc(&ctrl->tmem_base, P.tmem_cols);
+    tmem_relinquish();
+  }
+  if (warp == 8 && lane == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&ctrl->full[s], 1);
+      mbar_init(&ctrl->empty[s], 1);
+    }
+    mbar_init(&ctrl->done, 1);
+    ctrl->abort = 0;
+    mbar_fence_init();
+    tma_prefetch_desc(&map_x);
+    tma_prefetch_desc(&map_w);
+  }
+  pdl_wait();
+  __syncthreads();
+  // only now, with this CTA's TMEM held, may the next kernel's CTAs come and ask for theirs
+  pdl_launch_dependents();
+  tc_fence_after();
+  const uint32_t tmem = ctrl->tmem_base;
+
+  if (warp == 8) {
+    if (lane == 0) {
+      const int elems = kFp8 ? 128 : 64;
+      int issued = 0;
+      for (int kb = kb0; kb < kb1; ++kb, ++issued) {
+        const int s = issued % S, use = issued / S;
+        if (use > 0 && !mbar_wait_or_abort(&ctrl->empty[s], (uint32_t)(use - 1) & 1u, abort)) break;
+        uint8_t* st = sm + (size_t)s * P.stage_bytes;
+        mbar_arrive_expect_tx(&ctrl->full[s], P.stage_bytes);
+        tma_load_2d(smem_u32(st), &map_w, kb * elems, o0, &ctrl->full[s]);
+        tma_load_2d(smem_u32(st + P.off_b), &map_x, kb * elems, t0, &ctrl->full[s]);
+      }
+      for (int s = 0; s < S && s < issued; ++s) mbar_wait(&ctrl->full[s], (uint32_t)((issued - 1 - s) / S) & 1u);
+    }
+    __syncwarp();
+  } else if (warp == 9) {
+    if (lane == 0) {
+      const uint32_t idesc = kFp8 ? idesc_e4m3_f32(kRows, (uint32_t)BN) : idesc_bf16_f32(kRows, (uint32_t)BN, false, false);
+      bool ok = true;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        const int i = kb - kb0, s = i % S;
+        if (!mbar_wait_or_abort(&ctrl->full[s], (uint32_t)(i / S) & 1u, abort)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint8_t* st = sm + (size_t)s * P.stage_bytes;
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+          const uint64_t da = smem_desc(smem_u32(st) + ks * 32, 16, 1024, kSwizzle128B);
+          const uint64_t db = smem_desc(smem_u32(st + P.off_b) + ks * 32, 16, 1024, kSwizzle128B);
+          if (kFp8)
+            umma_f8(tmem, da, db, idesc, (i | ks) != 0);
+          else
+            umma_f16(tmem, da, db, idesc, (i | ks) != 0);
+        }
+        umma_commit(&ctrl->empty[s]);
+      }
+      if (!ok) report(err_word, MOLORA_DEV_WAIT_TIMEOUT);
+      umma_commit(&ctrl->done);
+    }
+    __syncwarp();
+  }
+
+  // partial sums [token][output] in shared memory, in the ring once every load and MMA is done
+  float* part = reinterpret_cast<float*>(sm);
+  __syncthreads();  // the TMA warp has seen every load land
+  const bool have = mbar_wait(&ctrl->done, 0) && !*abort;
+  tc_fence_after();
+  const int quarter = warp & 3;
+  if (warp < 8) {
+    const uint32_t base = tmem + ((uint32_t)(quarter * 32) << 16);
+    for (int c = (warp >> 2) * 16; c < tokens; c += 32) {
+      float v[16];
+      if (__all_sync(0xffffffffu, have))
+        tmem_ld16(base + (uint32_t)c, v);
+      else
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = 0.f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (c + i < tokens) part[(c + i) * kRows + quarter * 32 + lane] = v[i];
+    }
+    tc_fence_before();
+  }
+  __syncthreads();
+  if (C > 1) cluster_sync();
+  // this CTA's share of the tile's tokens x 128 elements: the C partial sums in rank order
+  const int total = tokens * kRows;
+  for (int e = rank * 256 + tid; warp < 8 && e < total; e += C * 256) {
+    float v = 0.f;
+    if (C > 1) {
+      const uint32_t at = smem_u32(part + e);
+      float p[8];
+#pragma unroll
+      for (int c = 0; c < 8; ++c) p[c] = c < C ? dsmem_ld_f32(dsmem_addr(at, (uint32_t)c)) : 0.f;
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+        if (c < C) v = c ? v + p[c] : p[0];
+    } else {
+      v = part[e];
+    }
+    const int64_t t = t0 + e / kRows;
+    const int32_t o = o0 + e % kRows;
+    if (o >= E.d_out || !have) continue;
+    if (E.sx) v *= E.sx[t] * E.sw[o];
+    if (E.bias) v += E.bias[o];
+    v = activate_fast(v, E.act);
+    const int64_t at = t * E.d_out + o;
+    if (E.y_bf16) {
+      if (E.res) v += to_float(static_cast<const __nv_bfloat16*>(E.res)[at]);
+      static_cast<__nv_bfloat16*>(E.y)[at] = __float2bfloat16_rn(v);
+    } else {
+      if (E.res) v += static_cast<const float*>(E.res)[at];
+      static_cast<float*>(E.y)[at] = v;
+    }
+  }
+  __syncthreads();
+  if (C > 1) cluster_sync();  // no CTA leaves while another may still read its partial sums
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, P.tmem_cols);
+  }
+}
+
+// ---------------------------------------------------------------------------------------------
+namespace {
+
+PFN_cuTensorMapEncodeTiled_v12000 linear_encoder() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    cudaDriverEntryPointQueryResult q;
+    void* p = nullptr;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    else
+      cudaGetLastError();
+  });
+  return fn;
+}
+
+bool linear_map(CUtensorMap* m, CUtensorMapDataType type, uint32_t esize, const void* base, uint64_t rows, uint64_t cols,
+                uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle swz) {
+  auto enc = linear_encoder();
+  if (!enc) return false;
+  cuuint64_t dims[2] = {cols, rows};
+  cuuint64_t strides[1] = {cols * esize};
+  cuuint32_t box[2] = {box_cols, box_rows};
+  cuuint32_t es[2] = {1, 1};
+  return enc(m, type, 2, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Lets `kernel` have kMaxSmem on the current device; `done` keeps the devices where it may already.
+template <typename K>
+cudaError_t allow_smem(K kernel, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxSmem);
+  if (e == cudaSuccess)
+    done.fetch_or(bit, std::memory_order_relaxed);
+  else
+    cudaGetLastError();
+  return e;
+}
+
+bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
+
+uint32_t tmem_columns(uint32_t n) {
+  uint32_t c = 32;
+  while (c < n) c *= 2;
+  return c;
+}
+
+bool operand_map(CUtensorMap* m, const LinearArgs& a, const void* base, int64_t rows, uint32_t box_rows) {
+  const bool fp8 = a.dtype == MOLORA_E4M3;
+  return linear_map(m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, fp8 ? 1 : 2, base,
+                    (uint64_t)rows, (uint64_t)a.d_in, fp8 ? 128 : 64, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+Epi epilogue_of(const LinearArgs& a) {
+  Epi e = {a.x_scale, a.w_scale, a.bias, a.residual, a.y, a.N, a.d_out, a.act, a.y_bf16, false, false};
+  e.col_vec = aligned(a.bias, 16) && aligned(a.w_scale, 16);
+  e.tma_y = a.d_out % (a.y_bf16 ? 8 : 4) == 0 && aligned(a.y, 16) && aligned(a.residual, 16);
+  return e;
+}
+
+cudaError_t launch_tc(const LinearArgs& a, int BN, cudaStream_t stream) {
+  const bool fp8 = a.dtype == MOLORA_E4M3;
+  Epi e = epilogue_of(a);
+  TcPlan p = {};
+  p.BN = BN;
+  p.nkb = (int)(((int64_t)a.d_in * (fp8 ? 1 : 2) + kRowBytes - 1) / kRowBytes);
+  p.m_tiles = (a.N + 2 * kRows - 1) / (2 * kRows);
+  p.n_tiles = (a.d_out + BN - 1) / BN;
+  p.tiles = p.m_tiles * p.n_tiles;
+  p.group = 8;
+  p.off_b = kRows * kRowBytes;
+  p.stage_bytes = p.off_b + (uint32_t)(BN / 2) * kRowBytes;
+  p.tmem_cols = tmem_columns(2 * (uint32_t)(BN <= 64 ? 64 : BN <= 128 ? 128 : 256));
+  const size_t fixed = kEpiWarps * kBox + sizeof(LCtrl) + kSmemSlack;
+  p.S = (int)((kMaxSmem - fixed) / p.stage_bytes);
+  if (p.S > kMaxStages) p.S = kMaxStages;
+  p.off_stage = (uint32_t)p.S * p.stage_bytes;
+  p.off_ctrl = p.off_stage + kEpiWarps * kBox;
+  p.smem = (uint32_t)(p.off_ctrl + sizeof(LCtrl) + kSmemSlack);
+  // one CTA an SM, alone: an allocation of TMEM never waits for another CTA's, which could in turn
+  // be waiting for a partner that this kernel's other CTAs keep out
+  p.smem = kMaxSmem;
+  CUtensorMap mx, mw, my = {};
+  if (!operand_map(&mx, a, a.x, a.N, kRows) || !operand_map(&mw, a, a.W, a.d_out, (uint32_t)(BN / 2)))
+    return cudaErrorNotSupported;
+  if (e.tma_y &&
+      !linear_map(&my, a.y_bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, a.y_bf16 ? 2 : 4,
+                  a.y, (uint64_t)a.N, (uint64_t)a.d_out, 32, 32,
+                  a.y_bf16 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B))
+    e.tma_y = false;
+  auto kernel = fp8 ? linear_tc_kernel<true> : linear_tc_kernel<false>;
+  static std::atomic<uint64_t> allowed[2];
+  const cudaError_t set = allow_smem(kernel, allowed[fp8]);
+  if (set != cudaSuccess) return set;
+  const int64_t most = num_sms() / 2;
+  const dim3 grid((unsigned)(2 * (p.tiles < most ? p.tiles : most)));
+  return launch_kernel(kernel, grid, dim3(kThreads), p.smem, stream, 2, e, p, a.err_word, mx, mw, my);
+}
+
+cudaError_t launch_skinny(const LinearArgs& a, cudaStream_t stream) {
+  const bool fp8 = a.dtype == MOLORA_E4M3;
+  const Epi e = epilogue_of(a);
+  SkinnyPlan p = {};
+  p.BN = a.N <= 16 ? 16 : a.N <= 32 ? 32 : a.N <= 64 ? 64 : a.N <= 128 ? 128 : 256;
+  p.nkb = (int)(((int64_t)a.d_in * (fp8 ? 1 : 2) + kRowBytes - 1) / kRowBytes);
+  p.o_tiles = (a.d_out + kRows - 1) / kRows;
+  p.t_tiles = (int32_t)((a.N + p.BN - 1) / p.BN);
+  const int64_t tiles = (int64_t)p.o_tiles * p.t_tiles;
+  p.C = 1;
+  while (p.C < 8 && tiles * p.C * 2 <= num_sms() && p.nkb >= p.C * 4) p.C *= 2;
+  p.off_b = kRows * kRowBytes;
+  p.stage_bytes = p.off_b + (uint32_t)p.BN * kRowBytes;
+  p.tmem_cols = tmem_columns((uint32_t)p.BN);
+  const size_t fixed = sizeof(LCtrl) + kSmemSlack;
+  const size_t partial = (size_t)p.BN * kRows * sizeof(float);
+  const int need = (p.nkb + p.C - 1) / p.C;
+  p.S = (int)((kMaxSmem - fixed) / p.stage_bytes);
+  if (p.S > kMaxStages) p.S = kMaxStages;
+  if (p.S > need) p.S = need;
+  size_t ring = (size_t)p.S * p.stage_bytes;
+  if (ring < partial) ring = partial;
+  p.off_ctrl = (uint32_t)ring;
+  p.smem = (uint32_t)(ring + sizeof(LCtrl) + kSmemSlack);
+  // a cluster's CTAs wait for one another: none may share an SM with a CTA that takes all of TMEM
+  // (those take 116 KB or more)
+  if (p.C > 1 && p.smem < 116 * 1024) p.smem = 116 * 1024;
+  CUtensorMap mx, mw;
+  if (!operand_map(&mx, a, a.x, a.N, (uint32_t)p.BN) || !operand_map(&mw, a, a.W, a.d_out, kRows))
+    return cudaErrorNotSupported;
+  auto kernel = fp8 ? linear_skinny_kernel<true> : linear_skinny_kernel<false>;
+  static std::atomic<uint64_t> allowed[2];
+  const cudaError_t set = allow_smem(kernel, allowed[fp8]);
+  if (set != cudaSuccess) return set;
+  return launch_kernel(kernel, dim3((unsigned)(tiles * p.C)), dim3(kThreads), p.smem, stream, p.C, e, p, a.err_word, mx,
+                       mw);
+}
+
+}  // namespace
+
+bool linear_tc_supported(const LinearArgs& a) {
+  if (a.dtype != MOLORA_BF16 && a.dtype != MOLORA_E4M3) return false;
+  return a.d_in % (a.dtype == MOLORA_E4M3 ? 16 : 8) == 0 && aligned(a.x, 16) && aligned(a.W, 16) &&
+         linear_encoder() != nullptr;
+}
+
+cudaError_t launch_linear_tc(const LinearArgs& a, cudaStream_t stream) {
+  const int64_t pairs = num_sms() / 2, m_tiles = (a.N + 2 * kRows - 1) / (2 * kRows);
+  const int64_t skinny_tiles = ((int64_t)a.d_out + kRows - 1) / kRows * ((a.N + 255) / 256);
+  if (a.N <= 256 || skinny_tiles <= num_sms() / 2) return launch_skinny(a, stream);
+  // the width whose waves of tiles cost least
+  int best = 256;
+  int64_t cost = INT64_MAX;
+  for (int BN : {256, 192, 128, 64}) {
+    const int64_t tiles = m_tiles * ((a.d_out + BN - 1) / BN), waves = (tiles + pairs - 1) / pairs;
+    const int64_t c = waves * (BN < 128 ? 96 + BN / 4 : BN);
+    if (c < cost) cost = c, best = BN;
+  }
+  return launch_tc(a, best, stream);
+}
+
+}  // namespace molora
