@@ -670,6 +670,8 @@ def _array(t: Optional[torch.Tensor], name: str, shape, dtype, device):
     `device` is a GPU is checked by _on_gpu, last, so that a mis-sized argument is reported as such."""
     if t is None:
         return None
+    if (type(t) in _TENSORS and t.shape == shape and t.dtype is dtype and t.device == device and t.is_contiguous()):
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name} must be a tensor")
     if t.shape != shape:
@@ -681,6 +683,21 @@ def _array(t: Optional[torch.Tensor], name: str, shape, dtype, device):
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device} (all tensors of a call share one device)")
     return t.data_ptr()
+
+
+_TENSORS = (torch.Tensor, torch.nn.Parameter)
+
+
+def _call(name: str, device, *args):
+    """Calls the library with `device` current and raises on a status that is not OK."""
+    fn = getattr(load_library(), name)
+    if device.index == torch.cuda.current_device():
+        status = fn(*args)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args)
+    if status != OK:
+        _check(name, status)
 
 
 def _on_gpu(t: torch.Tensor, name: str):
@@ -709,12 +726,13 @@ _FLOATS = (torch.bfloat16, torch.float32)
 
 
 def _raw_stream(stream, device) -> int:
+    """The handle of the given stream, else of the device's current one (torch's own accessor for
+    compiled callers: the public one makes a Stream object, 2 us of a 6 us call)."""
     if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
-    return _stream(stream, device).value
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    return _stream(stream, device).value or 0
 
 
-@_on_tensor_device
 def molora_rmsnorm(x, weight, eps=1e-6, residual=None, sum_out=None, out=None, out8=None, scale8=None, stream=None):
     """Root-mean-square norm of x [N, d] (+ residual) by rows: returns (sum_out, out, out8, scale8).
     ``out`` (x's dtype) is made if neither it nor out8 is given; ``sum_out`` (x + residual) is made
@@ -744,13 +762,10 @@ def molora_rmsnorm(x, weight, eps=1e-6, residual=None, sum_out=None, out=None, o
     if ps is not None and ps == po and N:
         raise ValueError("sum_out and out must be different tensors")
     _on_gpu(x, "x")
-    status = load_library().molora_rmsnorm(px, code, N, d, pr, ps, pg, eps, po, p8, pc, _raw_stream(stream, dev))
-    if status != OK:
-        _check("molora_rmsnorm", status)
+    _call("molora_rmsnorm", dev, px, code, N, d, pr, ps, pg, eps, po, p8, pc, _raw_stream(stream, dev))
     return sum_out, out, out8, scale8
 
 
-@_on_tensor_device
 def molora_gate_topk(logits, k, score="softmax", bias=None, groups=1, keep_groups=1, group_top=1, renormalise=True,
                      scale=1.0, ids=None, w=None, err_word=None, stream=None):
     """Expert-style gate over logits [N, K] (bfloat16 or float32, K up to MAX_EXPERTS): returns
@@ -779,11 +794,9 @@ def molora_gate_topk(logits, k, score="softmax", bias=None, groups=1, keep_group
         w = torch.empty(N, k, dtype=torch.float32, device=dev)
     pi, pw = _array(ids, "ids", (N, k), torch.int32, dev), _array(w, "w", (N, k), torch.float32, dev)
     _on_gpu(logits, "logits")
-    status = load_library().molora_gate_topk(
-        pl, code, N, K, score, pb, groups, keep_groups, group_top, k, 1 if renormalise else 0, scale, pi, pw,
+    _call(
+        "molora_gate_topk", dev, pl, code, N, K, score, pb, groups, keep_groups, group_top, k, 1 if renormalise else 0, scale, pi, pw,
         _p(_err_word(err_word, dev)), _raw_stream(stream, dev))
-    if status != OK:
-        _check("molora_gate_topk", status)
     return ids, w
 
 
@@ -795,7 +808,6 @@ def _y(y, N, d_out, dtype, device):
     return y
 
 
-@_on_tensor_device
 def molora_linear(x, W, y=None, x_scale=None, w_scale=None, bias=None, act="none", residual=None,
                   out_dtype=torch.float32, err_word=None, stream=None):
     """y = act(x W^T + bias) + residual for x [N, d_in] and W [d_out, d_in] in bfloat16, float32 or
@@ -820,11 +832,9 @@ def molora_linear(x, W, y=None, x_scale=None, w_scale=None, bias=None, act="none
     pres = _array(residual, "residual", (N, d_out), y.dtype, dev)
     py = _array(y, "y", (N, d_out), y.dtype, dev)
     _on_gpu(x, "x")
-    status = load_library().molora_linear(
-        px, code, psx, N, d_in, pw, psw, d_out, pb, act, pres, py, 1 if y.dtype == torch.bfloat16 else 0,
+    _call(
+        "molora_linear", dev, px, code, psx, N, d_in, pw, psw, d_out, pb, act, pres, py, 1 if y.dtype == torch.bfloat16 else 0,
         _p(_err_word(err_word, dev)), _raw_stream(stream, dev))
-    if status != OK:
-        _check("molora_linear", status)
     return y
 
 
@@ -883,7 +893,10 @@ def molora_norm_linear_lora_apply(x, norm_weight, eps, W, A, B, ids, y, scale, w
 
     def call(ws_ptr, ws_bytes):
         return lib.molora_norm_linear_lora_apply(*args, ws_ptr, ws_bytes, *tail)
-    _check("molora_norm_linear_lora_apply", _workspace(ws, dev, call))
+    if y.dtype == torch.bfloat16 and ws is None:  # no path of bf16 y takes a workspace
+        _check("molora_norm_linear_lora_apply", call(None, None))
+    else:
+        _check("molora_norm_linear_lora_apply", _workspace(ws, dev, call))
     return y, sum_out, h, h8, scale8
 
 

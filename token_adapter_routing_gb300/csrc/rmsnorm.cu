@@ -122,44 +122,80 @@ __device__ __forceinline__ float row_scale(float top, float inv) {
 
 }  // namespace
 
-// `team` threads (32 .. the CTA's) a row, NC chunks of it held by each thread.
-template <typename T, bool kVec, int NC>
+// `team` threads (32 .. the CTA's) a row, up to NC chunks of it held by each thread.  kRagged: d is
+// not a multiple of the chunk, so rows start anywhere in the arrays' 16-byte grid; a row's chunks
+// are those of the grid it touches, its first and last ones handled element by element.
+template <typename T, bool kVec, int NC, bool kRagged>
 __global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormArgs<T> a, int team) {
   using C = Chunk<T, kVec>;
   __shared__ float red[64];
-  const int in_team = threadIdx.x % team, which = threadIdx.x / team, teams = blockDim.x / team;
-  const int chunks = a.d / C::n;
+  const int in_team = threadIdx.x & (team - 1), which = threadIdx.x / team, teams = blockDim.x / team;
   pdl_wait();
   pdl_launch_dependents();
   const int64_t step = (int64_t)gridDim.x * teams;
   for (int64_t t0 = (int64_t)blockIdx.x * teams; t0 < a.N; t0 += step) {
     const int64_t t = t0 + which;
     const bool live = t < a.N;
-    const int64_t base = t * a.d;
+    const int shift = kRagged ? (int)((t * a.d) & (C::n - 1)) : 0;
+    const int chunks = live ? (a.d + shift + C::n - 1) / C::n : 0;
+    const int64_t base = t * a.d - shift;  // the first chunk's place in the arrays
+    auto whole = [&](int c) { return !kRagged || (c * C::n >= shift && (c + 1) * C::n <= a.d + shift); };
+    auto inside = [&](int c, int j) { return c * C::n + j >= shift && c * C::n + j < a.d + shift; };
+    auto load = [&](const T* p, int c, float (&v)[C::n]) {
+      if (whole(c)) {
+        C::load(p + base + (int64_t)c * C::n, v);
+      } else {
+#pragma unroll
+        for (int j = 0; j < C::n; ++j) v[j] = inside(c, j) ? to_float(p[base + (int64_t)c * C::n + j]) : 0.f;
+      }
+    };
+    auto store = [&](T* p, int c, const float (&v)[C::n]) {
+      if (whole(c)) {
+        C::store(p + base + (int64_t)c * C::n, v);
+      } else {
+#pragma unroll
+        for (int j = 0; j < C::n; ++j) {
+          const float one[1] = {v[j]};
+          if (inside(c, j)) Chunk<T, false>::store(p + base + (int64_t)c * C::n + j, one);
+        }
+      }
+    };
     float s[NC][C::n];
     float sum = 0.f, top = 0.f;
+    // every load of the row is in flight before the first is used
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       const int c = in_team + i * team;
+      if (c < chunks) load(a.x, c, s[i]);
+    }
+    if (a.res) {
 #pragma unroll
-      for (int j = 0; j < C::n; ++j) s[i][j] = 0.f;
-      if (live && c < chunks) {
-        C::load(a.x + base + (int64_t)c * C::n, s[i]);
-        if (a.res) {
+      for (int i = 0; i < NC; ++i) {
+        const int c = in_team + i * team;
+        if (c < chunks) {
           float r[C::n];
-          C::load(a.res + base + (int64_t)c * C::n, r);
+          load(a.res, c, r);
 #pragma unroll
           for (int j = 0; j < C::n; ++j) s[i][j] += r[j];
         }
+      }
+      if (a.sum_out) {
+#pragma unroll
+        for (int i = 0; i < NC; ++i)
+          if (in_team + i * team < chunks) store(a.sum_out, in_team + i * team, s[i]);
       }
     }
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       const int c = in_team + i * team;
-      if (live && c < chunks) {
-        if (a.sum_out) C::store(a.sum_out + base + (int64_t)c * C::n, s[i]);
+      if (c < chunks) {
         float g[C::n];
-        C::load(a.g + (int64_t)c * C::n, g);
+        if (kRagged) {
+#pragma unroll
+          for (int j = 0; j < C::n; ++j) g[j] = inside(c, j) ? to_float(a.g[c * C::n + j - shift]) : 0.f;
+        } else {
+          C::load(a.g + (int64_t)c * C::n, g);
+        }
 #pragma unroll
         for (int j = 0; j < C::n; ++j) {
           sum = fmaf(s[i][j], s[i][j], sum);
@@ -175,11 +211,21 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormArgs<T> a, int 
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       const int c = in_team + i * team;
-      if (live && c < chunks) {
+      if (c < chunks) {
 #pragma unroll
         for (int j = 0; j < C::n; ++j) s[i][j] *= inv;
-        if (a.out) C::store(a.out + base + (int64_t)c * C::n, s[i]);
-        if (a.out8) store8(a.out8 + base + (int64_t)c * C::n, s[i], f8);
+        if (a.out) store(a.out, c, s[i]);
+        if (a.out8) {
+          if (whole(c)) {
+            store8(a.out8 + base + (int64_t)c * C::n, s[i], f8);
+          } else {
+#pragma unroll
+            for (int j = 0; j < C::n; ++j) {
+              const float one[1] = {s[i][j]};
+              if (inside(c, j)) store8(a.out8 + base + (int64_t)c * C::n + j, one, f8);
+            }
+          }
+        }
       }
     }
   }
@@ -218,19 +264,25 @@ __global__ void __launch_bounds__(1024) rmsnorm_long_kernel(const NormArgs<T> a)
 
 namespace {
 
-template <typename T, bool kVec>
+constexpr int kFew = 2;
+
+template <typename T, bool kVec, bool kRagged>
 cudaError_t launch_norm(const NormArgs<T>& a, cudaStream_t stream) {
-  const int64_t chunks = a.d / Chunk<T, kVec>::n;
+  const int64_t chunks = (a.d + Chunk<T, kVec>::n - 1) / Chunk<T, kVec>::n + (kRagged ? 1 : 0);
+  // few chunks a thread where there are few rows (one row's latency), up to kFew where there are many
   int team = 32;
-  while (team < 1024 && chunks > (int64_t)team * 2) team *= 2;
+  while (team < 1024 && chunks > (int64_t)team * kFew) team *= 2;
+  while (team < 1024 && chunks > team && a.N * team * 2 <= (int64_t)num_sms() * 1024) team *= 2;
   const int per = (int)((chunks + team - 1) / team);
   const int threads = team < 256 ? 256 : team;
   const int64_t groups = (a.N + threads / team - 1) / (threads / team);
   const int64_t most = (int64_t)num_sms() * (2048 / threads);
-  const dim3 grid((unsigned)(groups < most ? groups : most));
-  if (per <= 1) return launch_kernel(rmsnorm_kernel<T, kVec, 1>, grid, dim3(threads), 0, stream, 0, a, team);
-  if (per <= 2) return launch_kernel(rmsnorm_kernel<T, kVec, 2>, grid, dim3(threads), 0, stream, 0, a, team);
-  if (per <= 4) return launch_kernel(rmsnorm_kernel<T, kVec, 4>, grid, dim3(threads), 0, stream, 0, a, team);
+  const dim3 grid((unsigned)(groups < most ? groups : most)), block(threads);
+  if (per <= 1) return launch_kernel(rmsnorm_kernel<T, kVec, 1, kRagged>, grid, block, 0, stream, 0, a, team);
+  if (per <= 2) return launch_kernel(rmsnorm_kernel<T, kVec, 2, kRagged>, grid, block, 0, stream, 0, a, team);
+  if (per <= 4) return launch_kernel(rmsnorm_kernel<T, kVec, 4, kRagged>, grid, block, 0, stream, 0, a, team);
+  if (Chunk<T, kVec>::n <= 4 && per <= 8)
+    return launch_kernel(rmsnorm_kernel<T, kVec, Chunk<T, kVec>::n <= 4 ? 8 : 4, kRagged>, grid, block, 0, stream, 0, a, team);
   const dim3 rows((unsigned)(a.N < 2 * num_sms() ? a.N : 2 * num_sms()));
   return launch_kernel(rmsnorm_long_kernel<T>, rows, dim3(1024), 0, stream, 0, a);
 }
@@ -245,8 +297,8 @@ cudaError_t launch_norm_typed(const void* x, int64_t N, int32_t d, const void* r
   const uintptr_t bits = reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(residual) |
                          reinterpret_cast<uintptr_t>(sum_out) | reinterpret_cast<uintptr_t>(weight) |
                          reinterpret_cast<uintptr_t>(out) | reinterpret_cast<uintptr_t>(out8);
-  const bool vec = (bits & 15u) == 0 && d % (16 / (int)sizeof(T)) == 0;
-  return vec ? launch_norm<T, true>(a, stream) : launch_norm<T, false>(a, stream);
+  if (bits & 15u) return launch_norm<T, false, false>(a, stream);
+  return d % Chunk<T, true>::n ? launch_norm<T, true, true>(a, stream) : launch_norm<T, true, false>(a, stream);
 }
 
 }  // namespace
