@@ -14,7 +14,8 @@ and of e4m3 2^-4 of the value, 2^-10 below its normal range):
     the lower index.
   * product: each of the d_in additions loses at most a whole step (2 u) of a partial sum, itself
     at most S = sum |x w|: 2 u d_in S; tensor cores align products to the largest before adding,
-    which is within the same whole step for each product.  The scales, the bias and the activation
+    which is within the same whole step for each product; fp32 operands are cut into three bf16
+    planes of which the products below 2^-21 |x w| (8 u) are left out: 8 u S.  The scales, the bias and the activation
     (whose slope is at most 1.13) add 16 u of what they handle; y rounds once.  Small
     integers, whose every partial sum is exact, have to come out bit for bit.
 """
@@ -337,7 +338,7 @@ def check_linear(y, x, W, sx, sw, bias, act, res):
     xd, wd = x.double(), W.double()
     scale = torch.ones(1, 1, device="cuda", dtype=torch.float64) if sx is None else sx.double()[:, None] * sw.double()[None]
     v, S = xd @ wd.T * scale, xd.abs() @ wd.abs().T * scale
-    tol = S * (2 * U * (x.shape[1] + 16))
+    tol = S * (2 * U * (x.shape[1] + 16)) + S * (8 * U if x.dtype == F32 else 0)
     if bias is not None:
         v, tol = v + bias.double(), tol + 16 * U * bias.double().abs()
     a = ACTS[act](v)
@@ -401,16 +402,37 @@ def test_linear_unaligned_and_in_place(m, dtype, N, d_in, d_out):
     check_linear(y, x, W, sx, sw, b, "none", res)
 
 
-def test_linear_nan_and_infinity_stay_in_their_rows(m):
-    for N in (3, 140):
-        g = gen(12)
-        x, W, _, _ = linear_inputs(g, N, 256, 64, BF)
-        x[1, 3], x[2, 4] = math.nan, math.inf
-        y = m.molora_linear(x, W, act="relu")
-        assert torch.isnan(y[1]).all()
-        check_linear(y[:1], x[:1], W, None, None, None, "relu", None)
-        if N > 3:
-            check_linear(y[3:], x[3:], W, None, None, None, "relu", None)
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("N, d_in, d_out", [(3, 256, 64), (140, 256, 64), (5, 255, 33), (3000, 256, 1024), (150, 1023, 70)])
+def test_linear_nan_and_infinity_stay_in_their_rows(m, dtype, N, d_in, d_out):
+    g = gen(12)
+    x, W, _, _ = linear_inputs(g, N, d_in, d_out, dtype)
+    x[1, 3], x[2, 4] = math.nan, math.inf
+    y = m.molora_linear(x, W)
+    assert torch.isnan(y[1]).all()
+    assert torch.equal(y[2], torch.where(W[:, 4] > 0, math.inf, -math.inf))
+    rest = [0] + list(range(3, N))
+    check_linear(y[rest], x[rest], W, None, None, None, "none", None)
+    # and an infinite weight in its column
+    x, W, _, _ = linear_inputs(g, N, d_in, d_out, dtype)
+    W[5, 7] = -math.inf
+    y = m.molora_linear(x, W, act="relu")
+    assert torch.equal(y[:, 5], torch.where(x[:, 7] > 0, 0.0, math.inf))
+    cols = [i for i in range(d_out) if i != 5]
+    check_linear(y[:, cols], x, W[cols], None, None, None, "relu", None)
+
+
+def test_linear_fp32_range(m):
+    """Values next to fp32's largest and below its normal range are cut into planes without loss."""
+    g = gen(15)
+    N, d_in, d_out = 20, 96, 40
+    x, W = torch.zeros(N, d_in, device="cuda"), torch.zeros(d_out, d_in, device="cuda")
+    x[:, 0], W[:, 0] = torch.finfo(F32).max, randn(g, d_out).sign()
+    assert torch.equal(m.molora_linear(x, W), x[:, :1] * W[:, 0])
+    x[:, 0], W[:, 0] = 2.0 ** -100 * randn(g, N), 2.0 ** 90 * randn(g, d_out)
+    y = m.molora_linear(x, W).double()
+    want = x[:, :1].double() * W[:, 0].double()
+    within(y, want, want.abs() * 8 * U)
 
 
 def test_linear_no_rows(m):

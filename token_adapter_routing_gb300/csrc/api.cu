@@ -171,7 +171,7 @@ static molora_status check_linear(const LinearArgs& a) {
 static molora_status linear_impl(const LinearArgs& a, cudaStream_t stream) {
   const molora_status st = check_linear(a);
   if (st != MOLORA_OK || a.N == 0) return st;
-  return launched(linear_tc_supported(a) ? launch_linear_tc(a, stream) : launch_linear_scalar(a, stream));
+  return launched(launch_linear(a, stream));
 }
 
 static molora_status check_rmsnorm(const void* x, molora_dtype dtype, int64_t N, int32_t d, const void* residual,

@@ -118,11 +118,7 @@ struct LinearArgs {
   bool y_bf16;
   int32_t* err_word;
 };
-// CUDA-core product: any type, size and alignment.
-cudaError_t launch_linear_scalar(const LinearArgs& a, cudaStream_t stream);
-// tcgen05 product: bf16 or e4m3 operands whose rows start on 16-byte boundaries.
-bool linear_tc_supported(const LinearArgs& a);
-cudaError_t launch_linear_tc(const LinearArgs& a, cudaStream_t stream);
+cudaError_t launch_linear(const LinearArgs& a, cudaStream_t stream);
 
 int num_sms();
 

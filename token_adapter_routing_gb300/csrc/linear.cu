@@ -1,4 +1,4 @@
-// linear_tc.cu -- the base product with its epilogue on the 5th-generation tensor cores, bf16 or
+// linear.cu -- the base product with its epilogue on the 5th-generation tensor cores, bf16 or
 // e4m3 operands with fp32 accumulators in TMEM:
 //
 //   y[t,o] = act(sx[t] * sw[o] * sum_i x[t,i] W[o,i] + bias[o]) + residual[t,o]
@@ -15,6 +15,8 @@
 // linear_skinny_kernel (few tokens): W's rows are the MMA's M (128 outputs a CTA), the tokens its N
 //   (16 .. 256), so that no MMA row is spent on tokens that are not there; d_in is split over a
 //   cluster of CTAs whose partial sums meet through distributed shared memory in rank order.
+// linear_any_kernel (fp32, and rows that start anywhere): the same split, with the operands fetched and
+//   laid out by the CTA's threads.
 #include <cudaTypedefs.h>
 
 #include <atomic>
@@ -45,6 +47,7 @@ struct __align__(8) LCtrl {
   uint64_t done;
   uint32_t tmem_base;
   int32_t abort;
+  int32_t odd;  // an infinite or NaN fp32 operand was seen
 };
 
 // What the epilogue reads and writes.
@@ -76,16 +79,16 @@ __device__ __forceinline__ void apply_act(float (&v)[32], molora_activation act)
   if (act == MOLORA_ACT_NONE) return;
   if (act == MOLORA_ACT_RELU) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = activate_fast(v[i], MOLORA_ACT_RELU);
+    for (int i = 0; i < 32; ++i) v[i] = activate(v[i], MOLORA_ACT_RELU);
   } else if (act == MOLORA_ACT_SILU) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = activate_fast(v[i], MOLORA_ACT_SILU);
+    for (int i = 0; i < 32; ++i) v[i] = activate(v[i], MOLORA_ACT_SILU);
   } else if (act == MOLORA_ACT_GELU_TANH) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = activate_fast(v[i], MOLORA_ACT_GELU_TANH);
+    for (int i = 0; i < 32; ++i) v[i] = activate(v[i], MOLORA_ACT_GELU_TANH);
   } else {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = activate_fast(v[i], MOLORA_ACT_GELU);
+    for (int i = 0; i < 32; ++i) v[i] = activate(v[i], MOLORA_ACT_GELU);
   }
 }
 
@@ -136,6 +139,71 @@ __device__ __forceinline__ void add_residual(float (&v)[32], const void* res, bo
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&p);
+}
+
+// Ends a tile of 128 outputs x `tokens` tokens whose d_in was split over a cluster's C CTAs: each
+// CTA's partial sums go from TMEM to shared memory, [token][output] in the stage ring (free: every load
+// has landed, and the MMAs are waited for here); each CTA then adds its share of the elements in rank
+// order, reading the others' through distributed shared memory, and writes it.  `last(t, o, v)` has
+// the final word on a sum.  Called by all threads.
+template <typename F>
+__device__ __forceinline__ void split_epilogue(const Epi& E, LCtrl* ctrl, uint8_t* sm, uint32_t tmem, int C, int rank,
+                                               int32_t o0, int64_t t0, int tokens, F last) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  float* part = reinterpret_cast<float*>(sm);
+  const bool have = mbar_wait(&ctrl->done, 0) && !*(volatile int32_t*)&ctrl->abort;
+  tc_fence_after();
+  const int quarter = warp & 3;
+  if (warp < kEpiWarps) {
+    const uint32_t base = tmem + ((uint32_t)(quarter * 32) << 16);
+    for (int c = (warp >> 2) * 16; c < tokens; c += 32) {
+      float v[16];
+      if (__all_sync(0xffffffffu, have))
+        tmem_ld16(base + (uint32_t)c, v);
+      else
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = 0.f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (c + i < tokens) part[(c + i) * kRows + quarter * 32 + lane] = v[i];
+    }
+    tc_fence_before();
+  }
+  __syncthreads();
+  if (C > 1) cluster_sync();
+  const int total = tokens * kRows;
+  for (int e = rank * 256 + tid; warp < kEpiWarps && e < total; e += C * 256) {
+    float v;
+    if (C > 1) {
+      const uint32_t at = smem_u32(part + e);
+      float p[8];
+#pragma unroll
+      for (int c = 0; c < 8; ++c) p[c] = c < C ? dsmem_ld_f32(dsmem_addr(at, (uint32_t)c)) : 0.f;
+      v = p[0];
+#pragma unroll
+      for (int c = 1; c < 8; ++c)
+        if (c < C) v += p[c];
+    } else {
+      v = part[e];
+    }
+    const int64_t t = t0 + e / kRows;
+    const int32_t o = o0 + e % kRows;
+    if (o >= E.d_out || !have) continue;
+    v = last(t, o, v);
+    if (E.sx) v *= E.sx[t] * E.sw[o];
+    if (E.bias) v += E.bias[o];
+    v = activate(v, E.act);
+    const int64_t at = t * E.d_out + o;
+    if (E.y_bf16) {
+      if (E.res) v += to_float(static_cast<const __nv_bfloat16*>(E.res)[at]);
+      static_cast<__nv_bfloat16*>(E.y)[at] = __float2bfloat16_rn(v);
+    } else {
+      if (E.res) v += static_cast<const float*>(E.res)[at];
+      static_cast<float*>(E.y)[at] = v;
+    }
+  }
+  __syncthreads();
+  if (C > 1) cluster_sync();  // no CTA leaves while another may still read its partial sums
 }
 
 }  // namespace
@@ -448,61 +516,193 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   }
 
-  // partial sums [token][output] in shared memory, in the ring once every load and MMA is done
-  float* part = reinterpret_cast<float*>(sm);
   __syncthreads();  // the TMA warp has seen every load land
-  const bool have = mbar_wait(&ctrl->done, 0) && !*abort;
+  split_epilogue(E, ctrl, sm, tmem, C, rank, o0, t0, tokens, [](int64_t, int32_t, float v) { return v; });
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, P.tmem_cols);
+  }
+}
+
+// ---------------------------------------------------------------------------------------------
+struct AnyPlan {
+  int BN;                // tokens per tile (MMA N)
+  int C;                 // CTAs of a cluster: d_in split C ways
+  int S;
+  int nkb;               // K blocks of 64 elements
+  int32_t o_tiles;
+  bool vec;              // fp32 rows in 16-byte vectors
+  uint32_t plane, stage_bytes, off_ctrl, tmem_cols, smem;
+};
+
+namespace {
+
+// 8 consecutive elements k0 .. k0 + 7 of a row as bf16 planes (16 bytes each) whose sum they are:
+// one plane for bf16 and e4m3, whose values bf16 holds, three for fp32, by cutting its 24 bits into
+// 8 + 8 + 8.  Elements past d_in are 0.  True if an element was infinite or NaN.
+template <typename T>
+__device__ __forceinline__ bool load_planes(const T* row, int k0, int d_in, bool, uint4 (&out)[1]) {
+  float v[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = k0 + j < d_in ? to_float(row[k0 + j]) : 0.f;
+  out[0] = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+  return false;
+}
+__device__ __forceinline__ bool load_planes(const float* row, int k0, int d_in, bool vec, uint4 (&out)[3]) {
+  float v[8];
+  if (vec && k0 + 8 <= d_in) {
+    const float4 a = *reinterpret_cast<const float4*>(row + k0), b = *reinterpret_cast<const float4*>(row + k0 + 4);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = k0 + j < d_in ? row[k0 + j] : 0.f;
+  }
+  bool odd = false;
+  uint32_t w[3][4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    uint32_t cut[3][2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float f = v[2 * j + h];
+      odd |= !(fabsf(f) <= 3.4028234663852886e38f);
+      const uint32_t u1 = __float_as_uint(f) & 0xffff0000u;
+      const float r1 = f - __uint_as_float(u1);
+      const uint32_t u2 = __float_as_uint(r1) & 0xffff0000u;
+      cut[0][h] = u1, cut[1][h] = u2, cut[2][h] = __float_as_uint(r1 - __uint_as_float(u2));
+    }
+#pragma unroll
+    for (int p = 0; p < 3; ++p) w[p][j] = __byte_perm(cut[p][0], cut[p][1], 0x7632);
+  }
+#pragma unroll
+  for (int p = 0; p < 3; ++p) out[p] = make_uint4(w[p][0], w[p][1], w[p][2], w[p][3]);
+  return odd;
+}
+
+}  // namespace
+
+// Operands that TMA cannot fetch or the tensor cores do not multiply: rows that start anywhere, and fp32.
+// The orientation and the split of linear_skinny_kernel; 8 warps fetch both operands and lay them out
+// as bf16 planes in the swizzled stages.  fp32 is three planes, x = x1 + x2 + x3 exactly, and
+//   x w = x1 w1 + x1 w2 + x2 w1 + x2 w2 + x1 w3 + x3 w1 + (terms below 2^-21 of |x w|, 2^-24 of it on average)
+// which is six bf16 products with fp32 sums: an fp32 product at a sixth of the bf16 rate, four times the CUDA
+// cores'.  An infinite operand would meet the zero planes of finite ones (inf * 0): a tile that has
+// seen one sums its outputs again on the CUDA cores.
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 1)
+    linear_any_kernel(const Epi E, const AnyPlan P, const T* __restrict__ x, const T* __restrict__ W, int32_t d_in,
+                      int32_t* err_word) {
+  constexpr int kPlanes = sizeof(T) == 4 ? 3 : 1;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  LCtrl* ctrl = reinterpret_cast<LCtrl*>(sm + P.off_ctrl);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int BN = P.BN, S = P.S, C = P.C;
+  const int rank = (int)cluster_ctarank();
+  const unsigned tile = blockIdx.x / (unsigned)C;
+  const int32_t o0 = (int32_t)(tile % (unsigned)P.o_tiles) * kRows;
+  const int64_t t0 = (int64_t)(tile / (unsigned)P.o_tiles) * BN;
+  const int kb0 = (int)((int64_t)P.nkb * rank / C), kb1 = (int)((int64_t)P.nkb * (rank + 1) / C);
+  const int tokens = (int)min((int64_t)BN, E.N - t0);
+  volatile int32_t* abort = &ctrl->abort;
+
+  if (warp == 9) {
+    tmem_alloc(&ctrl->tmem_base, P.tmem_cols);
+    tmem_relinquish();
+  }
+  if (warp == 8 && lane == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&ctrl->full[s], kEpiWarps);
+      mbar_init(&ctrl->empty[s], 1);
+    }
+    mbar_init(&ctrl->done, 1);
+    ctrl->abort = 0;
+    ctrl->odd = 0;
+    mbar_fence_init();
+  }
+  pdl_wait();
+  __syncthreads();
+  pdl_launch_dependents();  // with this CTA's TMEM held (see linear_tc_kernel)
   tc_fence_after();
-  const int quarter = warp & 3;
-  if (warp < 8) {
-    const uint32_t base = tmem + ((uint32_t)(quarter * 32) << 16);
-    for (int c = (warp >> 2) * 16; c < tokens; c += 32) {
-      float v[16];
-      if (__all_sync(0xffffffffu, have))
-        tmem_ld16(base + (uint32_t)c, v);
-      else
+  const uint32_t tmem = ctrl->tmem_base;
+
+  if (warp < kEpiWarps) {
+    bool odd = false;
+    const int pieces = (kRows + BN) * 8;  // 16-byte pieces of a stage's plane: W's rows, then x's
+    for (int kb = kb0; kb < kb1; ++kb) {
+      const int i = kb - kb0, s = i % S, use = i / S;
+      if (use > 0 && !__all_sync(0xffffffffu, mbar_wait_or_abort(&ctrl->empty[s], (uint32_t)(use - 1) & 1u, abort))) break;
+      uint8_t* st = sm + (size_t)s * P.stage_bytes;
+#pragma unroll 2
+      for (int q = tid; q < pieces; q += kEpiWarps * 32) {
+        const int row = q >> 3, piece = q & 7, k0 = kb * 64 + piece * 8;
+        uint4 p[kPlanes];
+        const bool is_w = row < kRows;
+        const bool there = is_w ? o0 + row < E.d_out : row - kRows < tokens;
+        if (there) {
+          odd |= load_planes(is_w ? W + (int64_t)(o0 + row) * d_in : x + (t0 + row - kRows) * d_in, k0, d_in, P.vec, p);
+        } else {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = 0.f;
+          for (int j = 0; j < kPlanes; ++j) p[j] = make_uint4(0, 0, 0, 0);
+        }
+        const uint32_t at = sw128_offset((uint32_t)row, (uint32_t)piece);
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (c + i < tokens) part[(c + i) * kRows + quarter * 32 + lane] = v[i];
+        for (int j = 0; j < kPlanes; ++j) *reinterpret_cast<uint4*>(st + j * P.plane + at) = p[j];
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctrl->full[s]);
     }
-    tc_fence_before();
+    if (odd) ctrl->odd = 1;
+  } else if (warp == 9) {
+    if (lane == 0) {
+      const uint32_t idesc = idesc_bf16_f32(kRows, (uint32_t)BN, false, false);
+      bool ok = true;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        const int i = kb - kb0, s = i % S;
+        if (!mbar_wait_or_abort(&ctrl->full[s], (uint32_t)(i / S) & 1u, abort)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t st = smem_u32(sm + (size_t)s * P.stage_bytes);
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+          uint64_t da[kPlanes], db[kPlanes];
+#pragma unroll
+          for (int j = 0; j < kPlanes; ++j) {
+            da[j] = smem_desc(st + j * P.plane + ks * 32, 16, 1024, kSwizzle128B);
+            db[j] = smem_desc(st + j * P.plane + kRows * kRowBytes + ks * 32, 16, 1024, kSwizzle128B);
+          }
+          umma_f16(tmem, da[0], db[0], idesc, (i | ks) != 0);
+          if (kPlanes == 3) {
+            umma_f16(tmem, da[0], db[1], idesc, 1);
+            umma_f16(tmem, da[1], db[0], idesc, 1);
+            umma_f16(tmem, da[1], db[1], idesc, 1);
+            umma_f16(tmem, da[0], db[2], idesc, 1);
+            umma_f16(tmem, da[2], db[0], idesc, 1);
+          }
+        }
+        umma_commit(&ctrl->empty[s]);
+      }
+      if (!ok) report(err_word, MOLORA_DEV_WAIT_TIMEOUT);
+      umma_commit(&ctrl->done);
+    }
+    __syncwarp();
   }
   __syncthreads();
-  if (C > 1) cluster_sync();
-  // this CTA's share of the tile's tokens x 128 elements: the C partial sums in rank order
-  const int total = tokens * kRows;
-  for (int e = rank * 256 + tid; warp < 8 && e < total; e += C * 256) {
-    float v = 0.f;
-    if (C > 1) {
-      const uint32_t at = smem_u32(part + e);
-      float p[8];
-#pragma unroll
-      for (int c = 0; c < 8; ++c) p[c] = c < C ? dsmem_ld_f32(dsmem_addr(at, (uint32_t)c)) : 0.f;
-#pragma unroll
-      for (int c = 0; c < 8; ++c)
-        if (c < C) v = c ? v + p[c] : p[0];
-    } else {
-      v = part[e];
+  // an odd element of any CTA of the cluster (they hold other parts of the same rows)
+  const uint32_t seen_at = smem_u32(&ctrl->odd);
+  split_epilogue(E, ctrl, sm, tmem, C, rank, o0, t0, tokens, [&](int64_t t, int32_t o, float v) {
+    if (kPlanes == 1) return v;
+    int32_t seen = 0;
+    for (int c = 0; c < C; ++c) seen |= C > 1 ? __float_as_int(dsmem_ld_f32(dsmem_addr(seen_at, (uint32_t)c))) : ctrl->odd;
+    if (seen) {
+      v = 0.f;
+      for (int i = 0; i < d_in; ++i) v = fmaf(to_float(x[t * d_in + i]), to_float(W[(int64_t)o * d_in + i]), v);
     }
-    const int64_t t = t0 + e / kRows;
-    const int32_t o = o0 + e % kRows;
-    if (o >= E.d_out || !have) continue;
-    if (E.sx) v *= E.sx[t] * E.sw[o];
-    if (E.bias) v += E.bias[o];
-    v = activate_fast(v, E.act);
-    const int64_t at = t * E.d_out + o;
-    if (E.y_bf16) {
-      if (E.res) v += to_float(static_cast<const __nv_bfloat16*>(E.res)[at]);
-      static_cast<__nv_bfloat16*>(E.y)[at] = __float2bfloat16_rn(v);
-    } else {
-      if (E.res) v += static_cast<const float*>(E.res)[at];
-      static_cast<float*>(E.y)[at] = v;
-    }
-  }
-  __syncthreads();
-  if (C > 1) cluster_sync();  // no CTA leaves while another may still read its partial sums
+    return v;
+  });
   if (warp == 9) {
     tc_fence_after();
     tmem_dealloc(tmem, P.tmem_cols);
@@ -594,7 +794,6 @@ cudaError_t launch_tc(const LinearArgs& a, int BN, cudaStream_t stream) {
   if (p.S > kMaxStages) p.S = kMaxStages;
   p.off_stage = (uint32_t)p.S * p.stage_bytes;
   p.off_ctrl = p.off_stage + kEpiWarps * kBox;
-  p.smem = (uint32_t)(p.off_ctrl + sizeof(LCtrl) + kSmemSlack);
   // one CTA an SM, alone: an allocation of TMEM never waits for another CTA's, which could in turn
   // be waiting for a partner that this kernel's other CTAs keep out
   p.smem = kMaxSmem;
@@ -653,15 +852,53 @@ cudaError_t launch_skinny(const LinearArgs& a, cudaStream_t stream) {
                        mw);
 }
 
+template <typename T>
+cudaError_t launch_any(const LinearArgs& a, cudaStream_t stream) {
+  const Epi e = epilogue_of(a);
+  AnyPlan p = {};
+  const int planes = sizeof(T) == 4 ? 3 : 1;
+  p.nkb = (int)(((int64_t)a.d_in + 63) / 64);
+  p.o_tiles = (int32_t)(((int64_t)a.d_out + kRows - 1) / kRows);
+  auto tiles_at = [&](int BN) { return p.o_tiles * ((a.N + BN - 1) / BN); };
+  p.BN = a.N <= 16 ? 16 : a.N <= 32 ? 32 : a.N <= 64 || tiles_at(128) < num_sms() ? 64 : 128;
+  const int64_t tiles = tiles_at(p.BN);
+  p.C = 1;
+  while (p.C < 8 && tiles * p.C * 2 <= num_sms() && p.nkb >= p.C * 4) p.C *= 2;
+  p.vec = a.d_in % 4 == 0 && aligned(a.x, 16) && aligned(a.W, 16);
+  p.plane = (uint32_t)(kRows + p.BN) * kRowBytes;
+  p.stage_bytes = planes * p.plane;
+  p.tmem_cols = tmem_columns((uint32_t)p.BN);
+  const size_t fixed = sizeof(LCtrl) + kSmemSlack, partial = (size_t)p.BN * kRows * sizeof(float);
+  p.S = (int)((kMaxSmem - fixed) / p.stage_bytes);
+  if (p.S > 4) p.S = 4;
+  size_t ring = (size_t)p.S * p.stage_bytes;
+  if (ring < partial) ring = partial;
+  p.off_ctrl = (uint32_t)ring;
+  p.smem = (uint32_t)(ring + fixed);
+  if (p.C > 1 && p.smem < 116 * 1024) p.smem = 116 * 1024;  // see launch_skinny
+  auto kernel = linear_any_kernel<T>;
+  static std::atomic<uint64_t> allowed;
+  const cudaError_t set = allow_smem(kernel, allowed);
+  if (set != cudaSuccess) return set;
+  return launch_kernel(kernel, dim3((unsigned)(tiles * p.C)), dim3(kThreads), p.smem, stream, p.C, e, p,
+                       static_cast<const T*>(a.x), static_cast<const T*>(a.W), a.d_in, a.err_word);
+}
+
 }  // namespace
 
-bool linear_tc_supported(const LinearArgs& a) {
+// Whether TMA can fetch the operands: bf16 or e4m3 rows that start on 16-byte boundaries.
+static bool tma_rows(const LinearArgs& a) {
   if (a.dtype != MOLORA_BF16 && a.dtype != MOLORA_E4M3) return false;
   return a.d_in % (a.dtype == MOLORA_E4M3 ? 16 : 8) == 0 && aligned(a.x, 16) && aligned(a.W, 16) &&
          linear_encoder() != nullptr;
 }
 
-cudaError_t launch_linear_tc(const LinearArgs& a, cudaStream_t stream) {
+cudaError_t launch_linear(const LinearArgs& a, cudaStream_t stream) {
+  if (!tma_rows(a)) {
+    if (a.dtype == MOLORA_BF16) return launch_any<__nv_bfloat16>(a, stream);
+    if (a.dtype == MOLORA_E4M3) return launch_any<__nv_fp8_e4m3>(a, stream);
+    return launch_any<float>(a, stream);
+  }
   const int64_t pairs = num_sms() / 2, m_tiles = (a.N + 2 * kRows - 1) / (2 * kRows);
   const int64_t skinny_tiles = ((int64_t)a.d_out + kRows - 1) / kRows * ((a.N + 255) / 256);
   if (a.N <= 256 || skinny_tiles <= num_sms() / 2) return launch_skinny(a, stream);

@@ -10,45 +10,28 @@ namespace molora {
 
 __device__ __forceinline__ float to_float(__nv_fp8_e4m3 v) { return static_cast<float>(v); }
 
-__device__ __forceinline__ void store_as(float* p, float v) { *p = v; }
-__device__ __forceinline__ void store_as(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
-
-// act(v) in fp32.  The tanh form of GELU is v * sigmoid(2 u), u = sqrt(2 / pi) (v + 0.044715 v^3).
-__device__ __forceinline__ float activate(float v, molora_activation act) {
-  switch (act) {
-    case MOLORA_ACT_RELU:
-      return v > 0.f ? v : (v != v ? v : 0.f);
-    case MOLORA_ACT_SILU:
-      return v / (1.f + expf(-v));
-    case MOLORA_ACT_GELU:
-      return 0.5f * v * erfcf(v * -0.70710678118654752f);
-    case MOLORA_ACT_GELU_TANH: {
-      const float u = 0.79788456080286536f * (v + 0.044715f * v * v * v);
-      return v / (1.f + expf(-2.f * u));
-    }
-    default:
-      return v;
-  }
-}
+// erf's GELU, 32 of which in a row would not fit the registers inline.
+static __device__ __noinline__ float gelu_erf(float v) { return 0.5f * v * erfcf(v * -0.70710678118654752f); }
 
 // v / (1 + exp(-z)).  exp(-z) overflows below z = -88: the quotient is then 0, as for 2^-127.
 __device__ __forceinline__ float sigmoid_times(float v, float z) {
   return __fdividef(v, 1.f + __expf(-z));
 }
 
-// The same with the hardware's exponential and reciprocal, for the tensor-core kernels' epilogues:
-// a few instructions an element, so that the epilogue stays under the MMAs of the next tile.  Their
+// act(v) in fp32 with the hardware's exponential and reciprocal: a few instructions an element, so
+// that the epilogue stays under the MMAs of the next tile.  The tanh form of GELU is v * sigmoid(2 u),
+// u = sqrt(2 / pi) (v + 0.044715 v^3).  Their
 // relative errors (about 2^-22, plus 2^-24 per unit of the exponent's argument) are below one rounding
 // of the sum the value comes from, and 2^13 times below one of a bf16 y.  At large |v| the quotient
 // underflows to -0 or tends to v, as the exact forms do.
-__device__ __forceinline__ float activate_fast(float v, molora_activation act) {
+__device__ __forceinline__ float activate(float v, molora_activation act) {
   switch (act) {
     case MOLORA_ACT_RELU:
       return v > 0.f ? v : (v != v ? v : 0.f);
     case MOLORA_ACT_SILU:
       return sigmoid_times(v, v);
     case MOLORA_ACT_GELU:
-      return 0.5f * v * erfcf(v * -0.70710678118654752f);
+      return gelu_erf(v);
     case MOLORA_ACT_GELU_TANH:
       return sigmoid_times(v, 1.5957691216057308f * v * fmaf(0.044715f * v, v, 1.f));
     default:
