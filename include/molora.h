@@ -537,8 +537,7 @@ MOLORA_API molora_status molora_linear(const void* x, molora_dtype dtype, const 
 
 /*
  * molora_norm_linear_lora_apply -- a whole adapted projection: molora_rmsnorm, molora_linear on its
- * output and molora_lora_apply_ex (AUTO) on both, enqueued back to back, with the results of the
- * three calls:
+ * output and molora_lora_apply_ex (AUTO) on both, enqueued back to back:
  *
  *   sum_out, h (, h8, scale8) = molora_rmsnorm(x + residual, norm_weight, eps)
  *   y      = h W^T + bias         or, with w_dtype = MOLORA_E4M3,  scale8 * w_scale * (h8 W^T) + bias
@@ -549,7 +548,11 @@ MOLORA_API molora_status molora_linear(const void* x, molora_dtype dtype, const 
  * w_scale fp32 [d_out] are needed with MOLORA_E4M3 and must be NULL otherwise.  h is an output: a
  * layer's other projections read it too.  y is overwritten: fp32 (y_bf16 = 0) or bf16 (y_bf16 = 1,
  * with molora_lora_apply_bf16y's roundings).  ids, w, k, counts, offsets, perm and ws, ws_bytes as for
- * molora_lora_apply; only its stacked path (fp32 y) uses the workspace.
+ * molora_lora_apply; a query sizes the path this call prefers.
+ * Given a workspace, and many tokens, bf16 W and K*r <= 512, the product takes the adapters' update
+ * along as further K blocks: the stacked path's shrink writes it to the workspace as two bf16
+ * terms (relative error 2^-17), and y is written, and rounded, once.  Otherwise the results are
+ * those of the three calls.
  */
 MOLORA_API molora_status molora_norm_linear_lora_apply(
     const void* x, molora_dtype dtype, int64_t N, int32_t d_in, const void* residual, void* sum_out,

@@ -893,10 +893,7 @@ def molora_norm_linear_lora_apply(x, norm_weight, eps, W, A, B, ids, y, scale, w
 
     def call(ws_ptr, ws_bytes):
         return lib.molora_norm_linear_lora_apply(*args, ws_ptr, ws_bytes, *tail)
-    if y.dtype == torch.bfloat16 and ws is None:  # no path of bf16 y takes a workspace
-        _check("molora_norm_linear_lora_apply", call(None, None))
-    else:
-        _check("molora_norm_linear_lora_apply", _workspace(ws, dev, call))
+    _check("molora_norm_linear_lora_apply", _workspace(ws, dev, call))
     return y, sum_out, h, h8, scale8
 
 

@@ -439,26 +439,45 @@ molora_status molora_norm_linear_lora_apply(const void* x, molora_dtype dtype, i
                                             size_t* ws_bytes, int32_t* err_word, cudaStream_t stream) {
   const bool fp8 = w_dtype == MOLORA_E4M3;
   if (!fp8 && w_dtype != dtype) return MOLORA_ERR_INVALID_ARG;
-  if (ws_bytes && !ws) {  // a query, as molora_lora_apply's; bf16 y takes no workspace
-    if (!y_bf16)
-      return apply_impl(nullptr, dtype, N, d_in, d_out, nullptr, nullptr, K, r, nullptr, nullptr, k, nullptr, nullptr,
-                        nullptr, scale, nullptr, false, nullptr, MOLORA_PATH_AUTO, stream, nullptr, nullptr, ws_bytes);
-    *ws_bytes = 0;
-    return check_apply_sizes(dtype, N, d_in, d_out, K, r, k);
-  }
-  // every argument of the three steps is checked before the first of them is enqueued
   const LinearArgs lin = {fp8 ? h8 : h, w_dtype, scale8, N, d_in, W, w_scale, d_out, bias, MOLORA_ACT_NONE, nullptr, y,
                           y_bf16 != 0, err_word};
-  molora_status st = check_rmsnorm(x, dtype, N, d_in, residual, sum_out, norm_weight, eps, h, h8, scale8);
-  if (st == MOLORA_OK) st = check_linear(lin);
-  if (st == MOLORA_OK) st = check_apply_args(h, dtype, N, d_in, d_out, A, B, K, r, ids, k, y);
-  if (st != MOLORA_OK || N == 0) return st;
-  if (ws && (reinterpret_cast<uintptr_t>(ws) & 255u)) return MOLORA_ERR_INVALID_ARG;
-  if (y_bf16 == 0 && ws_bytes && molora_select_path(dtype, N, d_in, d_out, K, r, k) == MOLORA_PATH_STACKED &&
-      *ws_bytes < stacked_workspace_bytes(N, K, r))
+  const bool query = ws_bytes && !ws;
+  molora_status st = query ? check_apply_sizes(dtype, N, d_in, d_out, K, r, k) : MOLORA_OK;
+  if (st != MOLORA_OK) return st;
+  // every argument of the three steps is checked before the first of them is enqueued
+  if (!query) {
+    st = check_rmsnorm(x, dtype, N, d_in, residual, sum_out, norm_weight, eps, h, h8, scale8);
+    if (st == MOLORA_OK) st = check_linear(lin);
+    if (st == MOLORA_OK) st = check_apply_args(h, dtype, N, d_in, d_out, A, B, K, r, ids, k, y);
+    if (st != MOLORA_OK || N == 0) return st;
+    if (ws && (reinterpret_cast<uintptr_t>(ws) & 255u)) return MOLORA_ERR_INVALID_ARG;
+  }
+  // The product takes the adapters' update along (y is then written once) where it runs on CTA pairs
+  // and the shrink's planes G fit the workspace.  That is K*r/32 more K blocks of 64 on the product's
+  // d_in/64, against a pass over y: taken up to twice the product's own work for the blocks.
+  const size_t planes = stacked_workspace_bytes(N, K, r);
+  const bool update = N > 0 && !fp8 && ws_bytes && K * r <= 512 && linear_takes_update(lin, B, K * r) &&
+                      stacked_supported(dtype, N, d_in, d_out, K, r, false);
+  if (query) {
+    *ws_bytes = planes;
+    if (update) return MOLORA_OK;
+    *ws_bytes = 0;
+    if (y_bf16) return MOLORA_OK;
+    return apply_impl(nullptr, dtype, N, d_in, d_out, nullptr, nullptr, K, r, nullptr, nullptr, k, nullptr, nullptr,
+                      nullptr, scale, nullptr, false, nullptr, MOLORA_PATH_AUTO, stream, nullptr, nullptr, ws_bytes);
+  }
+  if (ws_bytes && *ws_bytes < planes &&
+      (update || (!y_bf16 && molora_select_path(dtype, N, d_in, d_out, K, r, k) == MOLORA_PATH_STACKED)))
     return MOLORA_ERR_INVALID_ARG;
   if (launch_rmsnorm(x, dtype, N, d_in, residual, sum_out, norm_weight, eps, h, h8, scale8, stream) != cudaSuccess)
     return MOLORA_ERR_CUDA;
+  if (update) {
+    if (launch_lora_stacked(h, N, d_in, d_out, A, B, K, r, ids, w, k, scale, nullptr, ws, err_word, nullptr, nullptr,
+                            nullptr, nullptr, nullptr, nullptr, nullptr, stream) != cudaSuccess)
+      return MOLORA_ERR_CUDA;
+    const LinearUpdate u = {ws, static_cast<const uint8_t*>(ws) + planes / 2, B, K * r};
+    return launched(launch_linear(lin, stream, &u));
+  }
   st = linear_impl(lin, stream);
   if (st != MOLORA_OK) return st;
   return apply_impl(h, dtype, N, d_in, d_out, A, B, K, r, ids, w, k, counts, offsets, perm, scale, y, y_bf16 != 0,

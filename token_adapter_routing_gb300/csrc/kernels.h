@@ -58,7 +58,8 @@ bool stacked_supported(molora_dtype dtype, int64_t N, int32_t d_in, int32_t d_ou
 bool stacked_preferred(molora_dtype dtype, int64_t N, int32_t d_in, int32_t d_out, int32_t K, int32_t r,
                        int32_t k, bool router);
 size_t stacked_workspace_bytes(int64_t N, int32_t K, int32_t r);
-// W1 == nullptr: ids and w are given.  Otherwise the router (W1, b1, W2, b2) runs in the shrink
+// y == nullptr: the shrink alone, G = scale * c[t,a] (x A_a) as two bf16 planes [N x K*r] in ws, the
+// second one at stacked_workspace_bytes / 2.  W1 == nullptr: ids and w are given.  Otherwise the router (W1, b1, W2, b2) runs in the shrink
 // kernel and writes logits (if non-null), ids_out and w_out.
 cudaError_t launch_lora_stacked(const void* x, int64_t N, int32_t d_in, int32_t d_out, const void* A, const void* B,
                                 int32_t K, int32_t r, const int32_t* ids, const float* w, int32_t k, float scale,
@@ -118,7 +119,17 @@ struct LinearArgs {
   bool y_bf16;
   int32_t* err_word;
 };
-cudaError_t launch_linear(const LinearArgs& a, cudaStream_t stream);
+// Adapters' updates that the product takes along: y += (g_hi + g_lo) B before the activation, for G
+// planes [N x KR] (launch_lora_stacked without y) and B [KR x d_out] in bf16.
+struct LinearUpdate {
+  const void* g_hi;
+  const void* g_lo;
+  const void* B;
+  int32_t KR;
+};
+// True if launch_linear can take updates of KR columns along for these arguments.
+bool linear_takes_update(const LinearArgs& a, const void* B, int32_t KR);
+cudaError_t launch_linear(const LinearArgs& a, cudaStream_t stream, const LinearUpdate* update = nullptr);
 
 int num_sms();
 

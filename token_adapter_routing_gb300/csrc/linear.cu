@@ -69,6 +69,7 @@ struct TcPlan {
   int BN;                // outputs per tile
   int S;                 // stages
   int nkb;               // K blocks of 128 bytes
+  int nkg;               // K blocks of 64 of the adapters' update (0: none)
   int group;             // token tiles per group of tiles (they share W's rows in L2)
   int64_t m_tiles, tiles;
   int32_t n_tiles;
@@ -211,12 +212,16 @@ __device__ __forceinline__ void split_epilogue(const Epi& E, LCtrl* ctrl, uint8_
 template <bool kFp8>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_tc_kernel(const Epi E, const TcPlan P, int32_t* err_word, const __grid_constant__ CUtensorMap map_x,
-                     const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_y) {
+                     const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_y,
+                     const __grid_constant__ CUtensorMap map_ghi, const __grid_constant__ CUtensorMap map_glo,
+                     const __grid_constant__ CUtensorMap map_b) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   LCtrl* ctrl = reinterpret_cast<LCtrl*>(sm + P.off_ctrl);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int BN = P.BN, S = P.S, nkb = P.nkb;
+  // the adapters' update is more K blocks of the same accumulators: (G_hi, B), (G_lo, B) in turn
+  const int all = kFp8 ? nkb : nkb + 2 * P.nkg;
   const uint32_t rank = cluster_ctarank();
   const int64_t pair = blockIdx.x / 2, pairs = gridDim.x / 2;
   volatile int32_t* abort = &ctrl->abort;
@@ -247,6 +252,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_fence_init();
     tma_prefetch_desc(&map_x);
     tma_prefetch_desc(&map_w);
+    if (P.nkg) {
+      tma_prefetch_desc(&map_ghi);
+      tma_prefetch_desc(&map_glo);
+      tma_prefetch_desc(&map_b);
+    }
     if (E.tma_y) tma_prefetch_desc(&map_y);
   }
   pdl_wait();
@@ -266,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int64_t pt = pair; pt < P.tiles && ok; pt += pairs) {
         int32_t m0, n0;
         tile_at(pt, m0, n0);
-        for (int kb = 0; kb < nkb; ++kb) {
+        for (int kb = 0; kb < all; ++kb) {
           if (issued >= S && !mbar_wait_or_abort(&ctrl->empty[s], phase, abort)) {
             ok = false;
             break;
@@ -275,8 +285,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t bar = dsmem_addr(smem_u32(&ctrl->full[s]), 0);
           if (rank == 0) mbar_arrive_expect_tx(&ctrl->full[s], 2 * P.stage_bytes);
           uint8_t* st = sm + (size_t)s * P.stage_bytes;
-          tma_load_2d_pair(smem_u32(st), &map_x, kb * elems, m0, bar);
-          tma_load_2d_pair(smem_u32(st + P.off_b), &map_w, kb * elems, n0 + (int32_t)rank * (BN / 2), bar);
+          const int32_t n = n0 + (int32_t)rank * (BN / 2);
+          if (kFp8 || kb < nkb) {
+            tma_load_2d_pair(smem_u32(st), &map_x, kb * elems, m0, bar);
+            tma_load_2d_pair(smem_u32(st + P.off_b), &map_w, kb * elems, n, bar);
+          } else {
+            const int g = (kb - nkb) >> 1;
+            tma_load_2d_pair(smem_u32(st), (kb - nkb) & 1 ? &map_glo : &map_ghi, g * 64, m0, bar);
+            // B's columns in boxes of 64 rows x 32 columns, as many bytes as W's box
+            for (int q = 0; q < BN / 64; ++q)
+              tma_load_2d_pair(smem_u32(st + P.off_b + q * 4096), &map_b, n + q * 32, g * 64, bar);
+          }
           if (issued < S) ++issued;
           if (++s == S) s = 0, phase ^= 1;
         }
@@ -306,13 +325,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_after();
         const uint32_t d = tmem + (uint32_t)(buf * (P.tmem_cols / 2));
-        for (int kb = 0; kb < nkb; ++kb) {
+        for (int kb = 0; kb < all; ++kb) {
           if (!mbar_wait_or_abort(&ctrl->full[s], phase, abort)) {
             ok = false;
             break;
           }
           tc_fence_after();
           const uint8_t* st = sm + (size_t)s * P.stage_bytes;
+          if (!kFp8 && kb >= nkb) {
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks) {
+              const uint64_t da = smem_desc(smem_u32(st) + ks * 32, 16, 1024, kSwizzle128B);
+              const uint64_t db = smem_desc(smem_u32(st + P.off_b) + ks * 1024, 4096, 512, kSwizzle64B);  // MN-major
+              umma_f16_pair(d, da, db, idesc | (1u << 16), 1);
+            }
+            umma_commit_pair(&ctrl->empty[s]);
+            if (++s == S) s = 0, phase ^= 1;
+            continue;
+          }
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks) {
             const uint64_t da = smem_desc(smem_u32(st) + ks * 32, 16, 1024, kSwizzle128B);
@@ -776,12 +806,13 @@ Epi epilogue_of(const LinearArgs& a) {
   return e;
 }
 
-cudaError_t launch_tc(const LinearArgs& a, int BN, cudaStream_t stream) {
+cudaError_t launch_tc(const LinearArgs& a, int BN, const LinearUpdate* u, cudaStream_t stream) {
   const bool fp8 = a.dtype == MOLORA_E4M3;
   Epi e = epilogue_of(a);
   TcPlan p = {};
   p.BN = BN;
   p.nkb = (int)(((int64_t)a.d_in * (fp8 ? 1 : 2) + kRowBytes - 1) / kRowBytes);
+  p.nkg = u ? (u->KR + 63) / 64 : 0;
   p.m_tiles = (a.N + 2 * kRows - 1) / (2 * kRows);
   p.n_tiles = (a.d_out + BN - 1) / BN;
   p.tiles = p.m_tiles * p.n_tiles;
@@ -800,6 +831,12 @@ cudaError_t launch_tc(const LinearArgs& a, int BN, cudaStream_t stream) {
   CUtensorMap mx, mw, my = {};
   if (!operand_map(&mx, a, a.x, a.N, kRows) || !operand_map(&mw, a, a.W, a.d_out, (uint32_t)(BN / 2)))
     return cudaErrorNotSupported;
+  const auto BF = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  CUtensorMap ghi = {}, glo = {}, mb = {};
+  if (u && (!linear_map(&ghi, BF, 2, u->g_hi, (uint64_t)a.N, (uint64_t)u->KR, 64, kRows, CU_TENSOR_MAP_SWIZZLE_128B) ||
+            !linear_map(&glo, BF, 2, u->g_lo, (uint64_t)a.N, (uint64_t)u->KR, 64, kRows, CU_TENSOR_MAP_SWIZZLE_128B) ||
+            !linear_map(&mb, BF, 2, u->B, (uint64_t)u->KR, (uint64_t)a.d_out, 32, 64, CU_TENSOR_MAP_SWIZZLE_64B)))
+    return cudaErrorNotSupported;
   if (e.tma_y &&
       !linear_map(&my, a.y_bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, a.y_bf16 ? 2 : 4,
                   a.y, (uint64_t)a.N, (uint64_t)a.d_out, 32, 32,
@@ -811,7 +848,7 @@ cudaError_t launch_tc(const LinearArgs& a, int BN, cudaStream_t stream) {
   if (set != cudaSuccess) return set;
   const int64_t most = num_sms() / 2;
   const dim3 grid((unsigned)(2 * (p.tiles < most ? p.tiles : most)));
-  return launch_kernel(kernel, grid, dim3(kThreads), p.smem, stream, 2, e, p, a.err_word, mx, mw, my);
+  return launch_kernel(kernel, grid, dim3(kThreads), p.smem, stream, 2, e, p, a.err_word, mx, mw, my, ghi, glo, mb);
 }
 
 cudaError_t launch_skinny(const LinearArgs& a, cudaStream_t stream) {
@@ -893,16 +930,25 @@ static bool tma_rows(const LinearArgs& a) {
          linear_encoder() != nullptr;
 }
 
-cudaError_t launch_linear(const LinearArgs& a, cudaStream_t stream) {
+// True where the CTA-pair kernel runs: more tokens than a split tile's 256, and more tiles of
+// 128 outputs x 256 tokens than half of the SMs.
+static bool many_tokens(const LinearArgs& a) {
+  return a.N > 256 && ((int64_t)a.d_out + kRows - 1) / kRows * ((a.N + 255) / 256) > num_sms() / 2;
+}
+
+bool linear_takes_update(const LinearArgs& a, const void* B, int32_t KR) {
+  return a.dtype == MOLORA_BF16 && tma_rows(a) && many_tokens(a) && a.d_out % 8 == 0 && KR % 8 == 0 && aligned(B, 16);
+}
+
+cudaError_t launch_linear(const LinearArgs& a, cudaStream_t stream, const LinearUpdate* update) {
   if (!tma_rows(a)) {
     if (a.dtype == MOLORA_BF16) return launch_any<__nv_bfloat16>(a, stream);
     if (a.dtype == MOLORA_E4M3) return launch_any<__nv_fp8_e4m3>(a, stream);
     return launch_any<float>(a, stream);
   }
-  const int64_t pairs = num_sms() / 2, m_tiles = (a.N + 2 * kRows - 1) / (2 * kRows);
-  const int64_t skinny_tiles = ((int64_t)a.d_out + kRows - 1) / kRows * ((a.N + 255) / 256);
-  if (a.N <= 256 || skinny_tiles <= num_sms() / 2) return launch_skinny(a, stream);
+  if (!many_tokens(a)) return launch_skinny(a, stream);
   // the width whose waves of tiles cost least
+  const int64_t pairs = num_sms() / 2, m_tiles = (a.N + 2 * kRows - 1) / (2 * kRows);
   int best = 256;
   int64_t cost = INT64_MAX;
   for (int BN : {256, 192, 128, 64}) {
@@ -910,7 +956,7 @@ cudaError_t launch_linear(const LinearArgs& a, cudaStream_t stream) {
     const int64_t c = waves * (BN < 128 ? 96 + BN / 4 : BN);
     if (c < cost) cost = c, best = BN;
   }
-  return launch_tc(a, best, stream);
+  return launch_tc(a, best, update, stream);
 }
 
 }  // namespace molora
