@@ -21,6 +21,9 @@
 
 #include <atomic>
 #include <mutex>
+#ifdef MOLORA_TUNING_ENV
+#include <cstdlib>
+#endif
 
 #include "common.cuh"
 #include "kernels.h"
@@ -37,7 +40,7 @@ constexpr int kThreads = 32 * (kEpiWarps + 2);  // + TMA warp (8) + MMA warp (9)
 constexpr int kMaxStages = 8;
 constexpr size_t kMaxSmem = 227 * 1024;
 constexpr size_t kSmemSlack = 1024;
-constexpr uint32_t kBox = 4096;     // epilogue staging per warp: 32 rows x 32 columns of fp32
+constexpr uint32_t kBox = 4096;     // epilogue staging per warp: two boxes of 32 rows x 64 bytes
 
 struct __align__(8) LCtrl {
   uint64_t full[kMaxStages];
@@ -67,6 +70,7 @@ struct Epi {
 
 struct TcPlan {
   int BN;                // outputs per tile
+  int MC;                // pairs of a cluster: consecutive token tiles, which share W's boxes
   int S;                 // stages
   int nkb;               // K blocks of 128 bytes
   int nkg;               // K blocks of 64 of the adapters' update (0: none)
@@ -222,15 +226,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int BN = P.BN, S = P.S, nkb = P.nkb;
   // the adapters' update is more K blocks of the same accumulators: (G_hi, B), (G_lo, B) in turn
   const int all = kFp8 ? nkb : nkb + 2 * P.nkg;
-  const uint32_t rank = cluster_ctarank();
-  const int64_t pair = blockIdx.x / 2, pairs = gridDim.x / 2;
+  const uint32_t rank = cluster_ctarank(), leader = rank & ~1u, half = rank & 1u, which = rank >> 1;
+  const uint16_t own = (uint16_t)(0x3u << leader), everyone = (uint16_t)((1u << (2 * P.MC)) - 1u);
+  const int64_t pair = blockIdx.x / (2u * P.MC), pairs = gridDim.x / (2u * P.MC);
   volatile int32_t* abort = &ctrl->abort;
   // tiles in groups of P.group token tiles: within a group, the token tile runs fastest
   auto tile_at = [&](int64_t pt, int32_t& m0, int32_t& n0) {
     const int64_t span = (int64_t)P.group * P.n_tiles, grp = pt / span;
     const int64_t first = grp * P.group, left = P.m_tiles - first, rows = left < P.group ? left : P.group;
     const int64_t in = pt - grp * span;
-    m0 = (int32_t)((first + in % rows) * 2 * kRows + rank * kRows);
+    m0 = (int32_t)((first + in % rows) * (2 * P.MC) * kRows + rank * kRows);
     n0 = (int32_t)(in / rows) * BN;
   };
 
@@ -241,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 8 && lane == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(&ctrl->full[s], 1);
-      mbar_init(&ctrl->empty[s], 1);
+      mbar_init(&ctrl->empty[s], (uint32_t)P.MC);  // freed by every pair that W's boxes went to
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&ctrl->tfull[b], 1);
@@ -265,10 +270,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_launch_dependents();
   tc_fence_after();
   const uint32_t tmem = ctrl->tmem_base;
-  cluster_sync();  // both CTAs' barriers are initialised before either signals the other's
+  cluster_sync();  // every CTA's barriers are initialised before another signals them
 
   if (warp == 8) {
-    if (lane == 0) {
+    if (elect_one()) {
       const int elems = kFp8 ? 128 : 64;  // K elements per stage
       int s = 0, issued = 0;
       uint32_t phase = 1;  // the first use of a stage finds it empty
@@ -277,24 +282,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         int32_t m0, n0;
         tile_at(pt, m0, n0);
         for (int kb = 0; kb < all; ++kb) {
-          if (issued >= S && !mbar_wait_or_abort(&ctrl->empty[s], phase, abort)) {
+          if (issued >= S && !mbar_wait_spin(&ctrl->empty[s], phase, abort)) {
             ok = false;
             break;
           }
           // the leader's barrier counts both CTAs' bytes
-          const uint32_t bar = dsmem_addr(smem_u32(&ctrl->full[s]), 0);
-          if (rank == 0) mbar_arrive_expect_tx(&ctrl->full[s], 2 * P.stage_bytes);
+          const uint32_t bar = dsmem_addr(smem_u32(&ctrl->full[s]), leader);
+          if (half == 0) mbar_arrive_expect_tx(&ctrl->full[s], 2 * P.stage_bytes);
           uint8_t* st = sm + (size_t)s * P.stage_bytes;
-          const int32_t n = n0 + (int32_t)rank * (BN / 2);
+          const int32_t n = n0 + (int32_t)half * (BN / 2);
+          // W's half tile is the same in every pair of the cluster: each pair loads a part of it for all
+          const uint16_t sharers = (uint16_t)(P.MC == 2 ? 0x5u << half : 0x1u << half);
           if (kFp8 || kb < nkb) {
             tma_load_2d_pair(smem_u32(st), &map_x, kb * elems, m0, bar);
-            tma_load_2d_pair(smem_u32(st + P.off_b), &map_w, kb * elems, n, bar);
+            if (P.MC == 1)
+              tma_load_2d_pair(smem_u32(st + P.off_b), &map_w, kb * elems, n, bar);
+            else
+              tma_load_2d_pair_multicast(smem_u32(st + P.off_b + which * (BN / 4) * kRowBytes), &map_w, kb * elems,
+                                         n + (int32_t)which * (BN / 4), bar, sharers);
           } else {
             const int g = (kb - nkb) >> 1;
             tma_load_2d_pair(smem_u32(st), (kb - nkb) & 1 ? &map_glo : &map_ghi, g * 64, m0, bar);
-            // B's columns in boxes of 64 rows x 32 columns, as many bytes as W's box
-            for (int q = 0; q < BN / 64; ++q)
-              tma_load_2d_pair(smem_u32(st + P.off_b + q * 4096), &map_b, n + q * 32, g * 64, bar);
+            // B's columns in boxes of 64 rows x 16 columns, as many bytes as W's box
+            for (int q = (int)which; q < BN / 32; q += P.MC) {
+              if (P.MC == 1)
+                tma_load_2d_pair(smem_u32(st + P.off_b + q * 2048), &map_b, n + q * 16, g * 64, bar);
+              else
+                tma_load_2d_pair_multicast(smem_u32(st + P.off_b + q * 2048), &map_b, n + q * 16, g * 64, bar, sharers);
+            }
           }
           if (issued < S) ++issued;
           if (++s == S) s = 0, phase ^= 1;
@@ -312,82 +327,72 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else if (warp == 9) {
-    if (lane == 0 && rank == 0) {
+    if (half == 0 && elect_one()) {
       const uint32_t idesc = kFp8 ? idesc_e4m3_f32(2 * kRows, (uint32_t)BN) : idesc_bf16_f32(2 * kRows, (uint32_t)BN, false, false);
+      // descriptors of stage 0: K-major operands of 128-byte rows, and the update's B (see the TMA warp)
+      const uint64_t da = smem_desc(smem_u32(sm), 16, 1024, kSwizzle128B);
+      const uint64_t db = smem_desc(smem_u32(sm + P.off_b), 16, 1024, kSwizzle128B);
+      const uint64_t dg = smem_desc(smem_u32(sm + P.off_b), 2048, 256, kSwizzle32B);
+      const uint32_t a_lo = (uint32_t)da, b_lo = (uint32_t)db, desc_hi = (uint32_t)(da >> 32);
+      const uint32_t g_lo = (uint32_t)dg, g_hi = (uint32_t)(dg >> 32);
       int s = 0, tc = 0;
       uint32_t phase = 0;
       bool ok = true;
       for (int64_t pt = pair; pt < P.tiles && ok; pt += pairs, ++tc) {
         const int buf = tc & 1;
-        if (tc >= 2 && !mbar_wait_or_abort(&ctrl->tempty[buf], (uint32_t)((tc >> 1) - 1) & 1u, abort)) {
+        if (tc >= 2 && !mbar_wait_spin(&ctrl->tempty[buf], (uint32_t)((tc >> 1) - 1) & 1u, abort)) {
           ok = false;
           break;
         }
         tc_fence_after();
         const uint32_t d = tmem + (uint32_t)(buf * (P.tmem_cols / 2));
         for (int kb = 0; kb < all; ++kb) {
-          if (!mbar_wait_or_abort(&ctrl->full[s], phase, abort)) {
+          if (!mbar_wait_spin(&ctrl->full[s], phase, abort)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint8_t* st = sm + (size_t)s * P.stage_bytes;
-          if (!kFp8 && kb >= nkb) {
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks) {
-              const uint64_t da = smem_desc(smem_u32(st) + ks * 32, 16, 1024, kSwizzle128B);
-              const uint64_t db = smem_desc(smem_u32(st + P.off_b) + ks * 1024, 4096, 512, kSwizzle64B);  // MN-major
-              umma_f16_pair(d, da, db, idesc | (1u << 16), 1);
-            }
-            umma_commit_pair(&ctrl->empty[s]);
-            if (++s == S) s = 0, phase ^= 1;
-            continue;
-          }
-#pragma unroll
-          for (int ks = 0; ks < 4; ++ks) {
-            const uint64_t da = smem_desc(smem_u32(st) + ks * 32, 16, 1024, kSwizzle128B);
-            const uint64_t db = smem_desc(smem_u32(st + P.off_b) + ks * 32, 16, 1024, kSwizzle128B);
-            if (kFp8)
-              umma_f8_pair(d, da, db, idesc, (kb | ks) != 0);
-            else
-              umma_f16_pair(d, da, db, idesc, (kb | ks) != 0);
-          }
-          umma_commit_pair(&ctrl->empty[s]);
+          const uint32_t at = (uint32_t)s * (P.stage_bytes >> 4);
+          if (!kFp8 && kb >= nkb)  // B's columns are MN-major
+            umma_stage<true, kFp8>(d, a_lo + at, g_lo + at, desc_hi, g_hi, idesc | (1u << 16), 1, 32);
+          else
+            umma_stage<true, kFp8>(d, a_lo + at, b_lo + at, desc_hi, desc_hi, idesc, kb != 0);
+          umma_commit_pair(&ctrl->empty[s], everyone);
           if (++s == S) s = 0, phase ^= 1;
         }
         if (!ok) break;
-        umma_commit_pair(&ctrl->tfull[buf]);
+        umma_commit_pair(&ctrl->tfull[buf], own);
       }
       if (!ok) report(err_word, MOLORA_DEV_WAIT_TIMEOUT);
-      umma_commit_pair(&ctrl->done);  // arrives in both CTAs once every MMA has completed
+      umma_commit_pair(&ctrl->done, own);  // arrives in both CTAs once every MMA has completed
     }
     __syncwarp();
   } else {
-    // epilogue: warps w and w + 4 share 32 rows and take half of the columns each
-    const int quarter = warp & 3, half = warp >> 2;
+    // epilogue: warps w and w + 4 share 32 rows and take chunks of 32 columns in turn
+    const int quarter = warp & 3, side = warp >> 2;
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-    uint8_t* box = sm + P.off_stage + (size_t)warp * kBox;
-    int tc = 0;
+    uint8_t* boxes = sm + P.off_stage + (size_t)warp * kBox;  // two of 32 rows x 64 bytes
+    int tc = 0, turn = 0;
     for (int64_t pt = pair; pt < P.tiles; pt += pairs, ++tc) {
       const int buf = tc & 1;
       int32_t m0, n0;
       tile_at(pt, m0, n0);
       m0 += quarter * 32;
-      n0 += half * (BN / 2);
       const int64_t t = (int64_t)m0 + lane;
       const float sx = E.sx && t < E.N ? E.sx[t] : 1.f;
-      if (!__all_sync(0xffffffffu, mbar_wait_or_abort(&ctrl->tfull[buf], (uint32_t)(tc >> 1) & 1u, abort))) break;
+      const int chunks = m0 < E.N ? min(BN / 32, (E.d_out - n0 + 31) / 32) : 0;
+      if (!__all_sync(0xffffffffu, mbar_wait_spin(&ctrl->tfull[buf], (uint32_t)(tc >> 1) & 1u, abort))) break;
       tc_fence_after();
-      const uint32_t base = tmem + lanes + (uint32_t)(buf * (P.tmem_cols / 2) + half * (BN / 2));
-      const int chunks = m0 < E.N ? min(BN / 64, (E.d_out - n0 + 31) / 32) : 0;
-      for (int c = 0; c < chunks; ++c) {
+      const uint32_t base = tmem + lanes + (uint32_t)(buf * (P.tmem_cols / 2));
+      uint32_t r[32];
+      if (side < chunks) tmem_ld32_start(base + (uint32_t)(side * 32), r);
+      for (int c = side; c < chunks; c += 2) {
         const int col = n0 + c * 32;
-        uint32_t r[32];
-        tmem_ld32_start(base + (uint32_t)(c * 32), r);
-        tmem_ld_wait(r);
         float v[32];
+        tmem_ld_wait(r);
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+        if (c + 2 < chunks) tmem_ld32_start(base + (uint32_t)((c + 2) * 32), r);
         if (E.sx) {
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] *= sx;
@@ -397,37 +402,41 @@ __global__ void __launch_bounds__(kThreads, 1)
         apply_act(v, E.act);
         if (E.tma_y) {
           if (E.res && t < E.N) add_residual(v, E.res, E.y_bf16, t * E.d_out + col, E.d_out - col);
-          if (lane == 0) bulk_wait_read<0>();  // the last store from this box has read it
-          __syncwarp();
-          if (E.y_bf16) {
+          // 64 bytes of each row at a time: 32 columns of bf16, or 16 of fp32 twice
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+          for (int part = 0; part < 2; ++part) {
+            if (part && (E.y_bf16 || col + 16 >= E.d_out)) break;
+            uint8_t* box = boxes + turn * 2048;
+            turn ^= 1;
+            if (lane == 0) bulk_wait_read<1>();  // the store before the last, from this box, has read it
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int at = part * 16 + 4 * i;
               *reinterpret_cast<uint4*>(box + swz_offset((uint32_t)lane, (uint32_t)i, 64)) =
-                  make_uint4(pack_bf16(v[8 * i], v[8 * i + 1]), pack_bf16(v[8 * i + 2], v[8 * i + 3]),
-                             pack_bf16(v[8 * i + 4], v[8 * i + 5]), pack_bf16(v[8 * i + 6], v[8 * i + 7]));
-          } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              *reinterpret_cast<float4*>(box + sw128_offset((uint32_t)lane, (uint32_t)i)) =
-                  make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            tma_store_2d(&map_y, smem_u32(box), col, m0);
-            bulk_commit();
+                  E.y_bf16 ? make_uint4(pack_bf16(v[8 * i], v[8 * i + 1]), pack_bf16(v[8 * i + 2], v[8 * i + 3]),
+                                        pack_bf16(v[8 * i + 4], v[8 * i + 5]), pack_bf16(v[8 * i + 6], v[8 * i + 7]))
+                           : make_uint4(__float_as_uint(v[at]), __float_as_uint(v[at + 1]), __float_as_uint(v[at + 2]),
+                                        __float_as_uint(v[at + 3]));
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_2d(&map_y, smem_u32(box), col + part * 16, m0);
+              bulk_commit();
+            }
           }
         } else {
           // rows that are not 16-byte aligned: turned in shared memory, written a row at a time
-          float* turn = reinterpret_cast<float*>(box);
+          float* turned = reinterpret_cast<float*>(boxes);
           __syncwarp();
 #pragma unroll
-          for (int i = 0; i < 32; ++i) turn[lane * 32 + (i ^ lane)] = v[i];
+          for (int i = 0; i < 32; ++i) turned[lane * 32 + (i ^ lane)] = v[i];
           __syncwarp();
           for (int q = 0; q < 32 && m0 + q < E.N; ++q) {
             if (col + lane >= E.d_out) continue;
             const int64_t at = ((int64_t)m0 + q) * E.d_out + col + lane;
-            float o = turn[q * 32 + (lane ^ q)];
+            float o = turned[q * 32 + (lane ^ q)];
             if (E.y_bf16) {
               if (E.res) o += to_float(static_cast<const __nv_bfloat16*>(E.res)[at]);
               static_cast<__nv_bfloat16*>(E.y)[at] = __float2bfloat16_rn(o);
@@ -440,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(dsmem_addr(smem_u32(&ctrl->tempty[buf]), 0));
+      if (lane == 0) mbar_arrive_cluster(dsmem_addr(smem_u32(&ctrl->tempty[buf]), leader));
     }
     if (lane == 0) bulk_wait_all();
     __syncwarp();
@@ -503,42 +512,40 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = ctrl->tmem_base;
 
   if (warp == 8) {
-    if (lane == 0) {
+    if (elect_one()) {
       const int elems = kFp8 ? 128 : 64;
-      int issued = 0;
+      int issued = 0, s = 0;
+      uint32_t phase = 1;  // the first use of a stage finds it empty
       for (int kb = kb0; kb < kb1; ++kb, ++issued) {
-        const int s = issued % S, use = issued / S;
-        if (use > 0 && !mbar_wait_or_abort(&ctrl->empty[s], (uint32_t)(use - 1) & 1u, abort)) break;
+        if (issued >= S && !mbar_wait_spin(&ctrl->empty[s], phase, abort)) break;
         uint8_t* st = sm + (size_t)s * P.stage_bytes;
         mbar_arrive_expect_tx(&ctrl->full[s], P.stage_bytes);
         tma_load_2d(smem_u32(st), &map_w, kb * elems, o0, &ctrl->full[s]);
         tma_load_2d(smem_u32(st + P.off_b), &map_x, kb * elems, t0, &ctrl->full[s]);
+        if (++s == S) s = 0, phase ^= 1;
       }
-      for (int s = 0; s < S && s < issued; ++s) mbar_wait(&ctrl->full[s], (uint32_t)((issued - 1 - s) / S) & 1u);
+      for (int q = 0; q < S && q < issued; ++q) mbar_wait(&ctrl->full[q], (uint32_t)((issued - 1 - q) / S) & 1u);
     }
     __syncwarp();
   } else if (warp == 9) {
-    if (lane == 0) {
+    if (elect_one()) {
       const uint32_t idesc = kFp8 ? idesc_e4m3_f32(kRows, (uint32_t)BN) : idesc_bf16_f32(kRows, (uint32_t)BN, false, false);
+      const uint64_t da = smem_desc(smem_u32(sm), 16, 1024, kSwizzle128B);
+      const uint64_t db = smem_desc(smem_u32(sm + P.off_b), 16, 1024, kSwizzle128B);
+      const uint32_t a_lo = (uint32_t)da, b_lo = (uint32_t)db, desc_hi = (uint32_t)(da >> 32);
       bool ok = true;
+      int s = 0;
+      uint32_t phase = 0;
       for (int kb = kb0; kb < kb1; ++kb) {
-        const int i = kb - kb0, s = i % S;
-        if (!mbar_wait_or_abort(&ctrl->full[s], (uint32_t)(i / S) & 1u, abort)) {
+        if (!mbar_wait_spin(&ctrl->full[s], phase, abort)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const uint8_t* st = sm + (size_t)s * P.stage_bytes;
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {
-          const uint64_t da = smem_desc(smem_u32(st) + ks * 32, 16, 1024, kSwizzle128B);
-          const uint64_t db = smem_desc(smem_u32(st + P.off_b) + ks * 32, 16, 1024, kSwizzle128B);
-          if (kFp8)
-            umma_f8(tmem, da, db, idesc, (i | ks) != 0);
-          else
-            umma_f16(tmem, da, db, idesc, (i | ks) != 0);
-        }
+        const uint32_t at = (uint32_t)s * (P.stage_bytes >> 4);
+        umma_stage<false, kFp8>(tmem, a_lo + at, b_lo + at, desc_hi, desc_hi, idesc, kb != kb0);
         umma_commit(&ctrl->empty[s]);
+        if (++s == S) s = 0, phase ^= 1;
       }
       if (!ok) report(err_word, MOLORA_DEV_WAIT_TIMEOUT);
       umma_commit(&ctrl->done);
@@ -661,7 +668,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int pieces = (kRows + BN) * 8;  // 16-byte pieces of a stage's plane: W's rows, then x's
     for (int kb = kb0; kb < kb1; ++kb) {
       const int i = kb - kb0, s = i % S, use = i / S;
-      if (use > 0 && !__all_sync(0xffffffffu, mbar_wait_or_abort(&ctrl->empty[s], (uint32_t)(use - 1) & 1u, abort))) break;
+      if (use > 0 && !__all_sync(0xffffffffu, mbar_wait_spin(&ctrl->empty[s], (uint32_t)(use - 1) & 1u, abort))) break;
       uint8_t* st = sm + (size_t)s * P.stage_bytes;
 #pragma unroll 2
       for (int q = tid; q < pieces; q += kEpiWarps * 32) {
@@ -685,33 +692,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (odd) ctrl->odd = 1;
   } else if (warp == 9) {
-    if (lane == 0) {
+    if (elect_one()) {
       const uint32_t idesc = idesc_bf16_f32(kRows, (uint32_t)BN, false, false);
+      const uint32_t first = smem_u32(sm);
+      const uint64_t da = smem_desc(first, 16, 1024, kSwizzle128B);
+      const uint32_t a_lo = (uint32_t)da, b_lo = a_lo + ((uint32_t)kRows * kRowBytes >> 4), desc_hi = (uint32_t)(da >> 32);
       bool ok = true;
       for (int kb = kb0; kb < kb1; ++kb) {
         const int i = kb - kb0, s = i % S;
-        if (!mbar_wait_or_abort(&ctrl->full[s], (uint32_t)(i / S) & 1u, abort)) {
+        if (!mbar_wait_spin(&ctrl->full[s], (uint32_t)(i / S) & 1u, abort)) {
           ok = false;
           break;
         }
         tc_fence_after();
         const uint32_t st = smem_u32(sm + (size_t)s * P.stage_bytes);
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {
-          uint64_t da[kPlanes], db[kPlanes];
-#pragma unroll
-          for (int j = 0; j < kPlanes; ++j) {
-            da[j] = smem_desc(st + j * P.plane + ks * 32, 16, 1024, kSwizzle128B);
-            db[j] = smem_desc(st + j * P.plane + kRows * kRowBytes + ks * 32, 16, 1024, kSwizzle128B);
-          }
-          umma_f16(tmem, da[0], db[0], idesc, (i | ks) != 0);
-          if (kPlanes == 3) {
-            umma_f16(tmem, da[0], db[1], idesc, 1);
-            umma_f16(tmem, da[1], db[0], idesc, 1);
-            umma_f16(tmem, da[1], db[1], idesc, 1);
-            umma_f16(tmem, da[0], db[2], idesc, 1);
-            umma_f16(tmem, da[2], db[0], idesc, 1);
-          }
+        const uint32_t at = (st - first) >> 4, step = P.plane >> 4;
+        umma_stage<false, false>(tmem, a_lo + at, b_lo + at, desc_hi, desc_hi, idesc, i != 0);
+        if (kPlanes == 3) {
+          const uint32_t a1 = a_lo + at, a2 = a1 + step, a3 = a2 + step, b1 = b_lo + at, b2 = b1 + step, b3 = b2 + step;
+          umma_stage<false, false>(tmem, a1, b2, desc_hi, desc_hi, idesc, 1);
+          umma_stage<false, false>(tmem, a2, b1, desc_hi, desc_hi, idesc, 1);
+          umma_stage<false, false>(tmem, a2, b2, desc_hi, desc_hi, idesc, 1);
+          umma_stage<false, false>(tmem, a1, b3, desc_hi, desc_hi, idesc, 1);
+          umma_stage<false, false>(tmem, a3, b1, desc_hi, desc_hi, idesc, 1);
         }
         umma_commit(&ctrl->empty[s]);
       }
@@ -806,17 +809,21 @@ Epi epilogue_of(const LinearArgs& a) {
   return e;
 }
 
-cudaError_t launch_tc(const LinearArgs& a, int BN, const LinearUpdate* u, cudaStream_t stream) {
+cudaError_t launch_tc(const LinearArgs& a, int BN, int MC, const LinearUpdate* u, cudaStream_t stream) {
   const bool fp8 = a.dtype == MOLORA_E4M3;
   Epi e = epilogue_of(a);
   TcPlan p = {};
   p.BN = BN;
+  p.MC = MC;
   p.nkb = (int)(((int64_t)a.d_in * (fp8 ? 1 : 2) + kRowBytes - 1) / kRowBytes);
   p.nkg = u ? (u->KR + 63) / 64 : 0;
-  p.m_tiles = (a.N + 2 * kRows - 1) / (2 * kRows);
+  p.m_tiles = (a.N + 2 * MC * kRows - 1) / (2 * MC * kRows);
   p.n_tiles = (a.d_out + BN - 1) / BN;
   p.tiles = p.m_tiles * p.n_tiles;
-  p.group = 8;
+  p.group = 8 / MC;
+#ifdef MOLORA_TUNING_ENV
+  if (const char* g = getenv("MOLORA_LIN_GROUP")) p.group = atoi(g);
+#endif
   p.off_b = kRows * kRowBytes;
   p.stage_bytes = p.off_b + (uint32_t)(BN / 2) * kRowBytes;
   p.tmem_cols = tmem_columns(2 * (uint32_t)(BN <= 64 ? 64 : BN <= 128 ? 128 : 256));
@@ -829,26 +836,25 @@ cudaError_t launch_tc(const LinearArgs& a, int BN, const LinearUpdate* u, cudaSt
   // be waiting for a partner that this kernel's other CTAs keep out
   p.smem = kMaxSmem;
   CUtensorMap mx, mw, my = {};
-  if (!operand_map(&mx, a, a.x, a.N, kRows) || !operand_map(&mw, a, a.W, a.d_out, (uint32_t)(BN / 2)))
+  if (!operand_map(&mx, a, a.x, a.N, kRows) || !operand_map(&mw, a, a.W, a.d_out, (uint32_t)(BN / 2 / MC)))
     return cudaErrorNotSupported;
   const auto BF = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   CUtensorMap ghi = {}, glo = {}, mb = {};
   if (u && (!linear_map(&ghi, BF, 2, u->g_hi, (uint64_t)a.N, (uint64_t)u->KR, 64, kRows, CU_TENSOR_MAP_SWIZZLE_128B) ||
             !linear_map(&glo, BF, 2, u->g_lo, (uint64_t)a.N, (uint64_t)u->KR, 64, kRows, CU_TENSOR_MAP_SWIZZLE_128B) ||
-            !linear_map(&mb, BF, 2, u->B, (uint64_t)u->KR, (uint64_t)a.d_out, 32, 64, CU_TENSOR_MAP_SWIZZLE_64B)))
+            !linear_map(&mb, BF, 2, u->B, (uint64_t)u->KR, (uint64_t)a.d_out, 16, 64, CU_TENSOR_MAP_SWIZZLE_32B)))
     return cudaErrorNotSupported;
   if (e.tma_y &&
       !linear_map(&my, a.y_bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, a.y_bf16 ? 2 : 4,
-                  a.y, (uint64_t)a.N, (uint64_t)a.d_out, 32, 32,
-                  a.y_bf16 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B))
+                  a.y, (uint64_t)a.N, (uint64_t)a.d_out, a.y_bf16 ? 32 : 16, 32, CU_TENSOR_MAP_SWIZZLE_64B))
     e.tma_y = false;
   auto kernel = fp8 ? linear_tc_kernel<true> : linear_tc_kernel<false>;
   static std::atomic<uint64_t> allowed[2];
   const cudaError_t set = allow_smem(kernel, allowed[fp8]);
   if (set != cudaSuccess) return set;
-  const int64_t most = num_sms() / 2;
-  const dim3 grid((unsigned)(2 * (p.tiles < most ? p.tiles : most)));
-  return launch_kernel(kernel, grid, dim3(kThreads), p.smem, stream, 2, e, p, a.err_word, mx, mw, my, ghi, glo, mb);
+  const int64_t most = num_sms() / (2 * MC);
+  const dim3 grid((unsigned)(2 * MC * (p.tiles < most ? p.tiles : most)));
+  return launch_kernel(kernel, grid, dim3(kThreads), p.smem, stream, 2 * MC, e, p, a.err_word, mx, mw, my, ghi, glo, mb);
 }
 
 cudaError_t launch_skinny(const LinearArgs& a, cudaStream_t stream) {
@@ -951,12 +957,18 @@ cudaError_t launch_linear(const LinearArgs& a, cudaStream_t stream, const Linear
   const int64_t pairs = num_sms() / 2, m_tiles = (a.N + 2 * kRows - 1) / (2 * kRows);
   int best = 256;
   int64_t cost = INT64_MAX;
-  for (int BN : {256, 192, 128, 64}) {
+  for (int BN : {256, 224, 192, 160, 128, 96, 64}) {
     const int64_t tiles = m_tiles * ((a.d_out + BN - 1) / BN), waves = (tiles + pairs - 1) / pairs;
-    const int64_t c = waves * (BN < 128 ? 96 + BN / 4 : BN);
+    // cycles of a stage, halved: 420 for narrow tiles, 2 BN and 90 for wide ones
+    const int64_t c = waves * (BN + 45 > 210 ? BN + 45 : 210);
     if (c < cost) cost = c, best = BN;
   }
-  return launch_tc(a, best, update, stream);
+  int MC = 1;
+#ifdef MOLORA_TUNING_ENV
+  if (const char* g = getenv("MOLORA_LIN_BN")) best = atoi(g);
+  if (const char* g = getenv("MOLORA_LIN_MC")) MC = atoi(g);
+#endif
+  return launch_tc(a, best, MC, update, stream);
 }
 
 }  // namespace molora
