@@ -64,7 +64,6 @@ struct Epi {
   int32_t d_out;
   molora_activation act;
   bool y_bf16;
-  bool col_vec;  // sw and bias may be read in 16-byte vectors
   bool tma_y;    // y through its tensor map, residual in 16-byte vectors
 };
 
@@ -97,49 +96,35 @@ __device__ __forceinline__ void apply_act(float (&v)[32], molora_activation act)
   }
 }
 
-// v[i] = op(v[i], p[n0 + i]) over a chunk of 32 columns; p is the same for every lane.
-template <typename F>
-__device__ __forceinline__ void per_column(float (&v)[32], const float* p, int n0, int d_out, bool vec, F op) {
-  if (vec && n0 + 32 <= d_out) {
+// 32 residual columns of a row, in 16-byte vectors; those past d_out (a multiple of the vector's
+// elements) are 0.
+struct Residual {
+  uint4 q[8];
+  __device__ __forceinline__ void load(const void* res, bool bf16, int64_t at, int cols) {
+    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(res) + at * (bf16 ? 2 : 4));
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float4 q = *reinterpret_cast<const float4*>(p + n0 + 4 * i);
-      v[4 * i] = op(v[4 * i], q.x), v[4 * i + 1] = op(v[4 * i + 1], q.y);
-      v[4 * i + 2] = op(v[4 * i + 2], q.z), v[4 * i + 3] = op(v[4 * i + 3], q.w);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (n0 + i < d_out) v[i] = op(v[i], p[n0 + i]);
+    for (int i = 0; i < 8; ++i) q[i] = i * (bf16 ? 8 : 4) < min(cols, 32) ? p[i] : make_uint4(0, 0, 0, 0);
   }
-}
-
-// v += 32 residual columns of a row in 16-byte vectors, those past d_out left out (a multiple of
-// the vector's elements).
-__device__ __forceinline__ void add_residual(float (&v)[32], const void* res, bool bf16, int64_t at, int cols) {
-  if (bf16) {
-    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(res) + at);
+  __device__ __forceinline__ void add(float (&v)[32], bool bf16) const {
+    if (bf16) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (8 * i < cols) {
-        const uint4 q = p[i];
-        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           v[8 * i + 2 * j] += __uint_as_float(w[j] << 16);
           v[8 * i + 2 * j + 1] += __uint_as_float(w[j] & 0xffff0000u);
         }
       }
-  } else {
-    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(res) + at);
+    } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (4 * i < cols) {
-        const float4 q = p[i];
-        v[4 * i] += q.x, v[4 * i + 1] += q.y, v[4 * i + 2] += q.z, v[4 * i + 3] += q.w;
+      for (int i = 0; i < 8; ++i) {
+        v[4 * i] += __uint_as_float(q[i].x), v[4 * i + 1] += __uint_as_float(q[i].y);
+        v[4 * i + 2] += __uint_as_float(q[i].z), v[4 * i + 3] += __uint_as_float(q[i].w);
       }
+    }
   }
-}
+};
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
@@ -381,6 +366,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int64_t t = (int64_t)m0 + lane;
       const float sx = E.sx && t < E.N ? E.sx[t] : 1.f;
       const int chunks = m0 < E.N ? min(BN / 32, (E.d_out - n0 + 31) / 32) : 0;
+      // while the tile's MMAs run: this lane's column of each of its chunks' scales and biases, which a
+      // chunk's rows get by shuffles, and the residual's rows on their way to L2
+      float cs[4], cb[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int o = n0 + (side + 2 * q) * 32 + lane;
+        const bool in = side + 2 * q < chunks && o < E.d_out;
+        cs[q] = in && E.sw ? E.sw[o] : 1.f;
+        cb[q] = in && E.bias ? E.bias[o] : 0.f;
+      }
+      if (E.res && E.tma_y && side == 0 && chunks > 0 && t < E.N) {
+        const uint32_t esize = E.y_bf16 ? 2 : 4;
+        prefetch_l2_bulk(static_cast<const uint8_t*>(E.res) + (t * E.d_out + n0) * esize,
+                         (uint32_t)min(BN, E.d_out - n0) * esize);
+      }
       if (!__all_sync(0xffffffffu, mbar_wait_spin(&ctrl->tfull[buf], (uint32_t)(tc >> 1) & 1u, abort))) break;
       tc_fence_after();
       const uint32_t base = tmem + lanes + (uint32_t)(buf * (P.tmem_cols / 2));
@@ -389,19 +389,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int c = side; c < chunks; c += 2) {
         const int col = n0 + c * 32;
         float v[32];
+        Residual res;
+        const bool add = E.tma_y && E.res && t < E.N;
+        if (add) res.load(E.res, E.y_bf16, t * E.d_out + col, E.d_out - col);
         tmem_ld_wait(r);
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
         if (c + 2 < chunks) tmem_ld32_start(base + (uint32_t)((c + 2) * 32), r);
         if (E.sx) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] *= sx;
-          per_column(v, E.sw, col, E.d_out, E.col_vec, [](float a, float b) { return a * b; });
+          for (int i = 0; i < 32; ++i)
+            v[i] = fmaf(v[i], sx * __shfl_sync(0xffffffffu, cs[0], i), __shfl_sync(0xffffffffu, cb[0], i));
+        } else if (E.bias) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] += __shfl_sync(0xffffffffu, cb[0], i);
         }
-        if (E.bias) per_column(v, E.bias, col, E.d_out, E.col_vec, [](float a, float b) { return a + b; });
+#pragma unroll
+        for (int q = 0; q < 3; ++q) cs[q] = cs[q + 1], cb[q] = cb[q + 1];
         apply_act(v, E.act);
         if (E.tma_y) {
-          if (E.res && t < E.N) add_residual(v, E.res, E.y_bf16, t * E.d_out + col, E.d_out - col);
+          if (add) res.add(v, E.y_bf16);
           // 64 bytes of each row at a time: 32 columns of bf16, or 16 of fp32 twice
 #pragma unroll
           for (int part = 0; part < 2; ++part) {
@@ -803,8 +810,7 @@ bool operand_map(CUtensorMap* m, const LinearArgs& a, const void* base, int64_t 
 }
 
 Epi epilogue_of(const LinearArgs& a) {
-  Epi e = {a.x_scale, a.w_scale, a.bias, a.residual, a.y, a.N, a.d_out, a.act, a.y_bf16, false, false};
-  e.col_vec = aligned(a.bias, 16) && aligned(a.w_scale, 16);
+  Epi e = {a.x_scale, a.w_scale, a.bias, a.residual, a.y, a.N, a.d_out, a.act, a.y_bf16, false};
   e.tma_y = a.d_out % (a.y_bf16 ? 8 : 4) == 0 && aligned(a.y, 16) && aligned(a.residual, 16);
   return e;
 }
