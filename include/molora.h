@@ -550,7 +550,7 @@ MOLORA_API molora_status molora_linear(const void* x, molora_dtype dtype, const 
  * with molora_lora_apply_bf16y's roundings).  ids, w, k, counts, offsets, perm and ws, ws_bytes as for
  * molora_lora_apply; a query sizes the path this call prefers.
  * Given a workspace, and many tokens, bf16 W and K*r <= 512, the product takes the adapters' update
- * along as further K blocks: the stacked path's shrink writes it to the workspace as two bf16
+ * along as further K blocks: a shrink writes it to the workspace as two bf16
  * terms (relative error 2^-17), and y is written, and rounded, once.  Otherwise the results are
  * those of the three calls.
  */

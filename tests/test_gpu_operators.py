@@ -476,7 +476,8 @@ def layer(g, N, d_in, d_out, K, r, k, fp8):
     (1500, 512, 512, 8, 64, 2, True), (2100, 256, 256, 4, 16, 1, False), (33, 520, 264, 3, 8, 2, False),
     # the product takes the update along: K*r of one, part of one and several K blocks, widths of every tile
     (2600, 512, 2048, 4, 16, 2, False), (4000, 256, 1544, 2, 16, 1, False), (2300, 320, 2120, 3, 32, 2, False),
-    (5000, 128, 1024, 8, 64, 3, False), (20000, 64, 160, 4, 32, 2, False)])
+    (5000, 128, 1024, 8, 64, 3, False), (20000, 64, 160, 4, 32, 2, False),
+    (2305, 1088, 1920, 7, 64, 2, False), (2900, 64, 2048, 13, 32, 1, False)])
 def test_adapted_layer(m, y_dtype, N, d_in, d_out, K, r, k, fp8):
     """Norm -> linear gate -> gate -> dispatch -> the adapted projection, as a layer runs them, against
     the formulas in 64 bits on what each call reads; and the one call against the three it chains."""

@@ -453,29 +453,28 @@ molora_status molora_norm_linear_lora_apply(const void* x, molora_dtype dtype, i
     if (ws && (reinterpret_cast<uintptr_t>(ws) & 255u)) return MOLORA_ERR_INVALID_ARG;
   }
   // The product takes the adapters' update along (y is then written once) where it runs on CTA pairs
-  // and the shrink's planes G fit the workspace.  That is K*r/32 more K blocks of 64 on the product's
-  // d_in/64, against a pass over y: taken up to twice the product's own work for the blocks.
-  const size_t planes = stacked_workspace_bytes(N, K, r);
+  // and the update's two planes fit the workspace: K*r/32 more K blocks of 64 against a pass over y.
+  const size_t plane = lora_update_bytes(N, K * r), stacked = stacked_workspace_bytes(N, K, r);
   const bool update = N > 0 && !fp8 && ws_bytes && K * r <= 512 && linear_takes_update(lin, B, K * r) &&
-                      stacked_supported(dtype, N, d_in, d_out, K, r, false);
+                      lora_update_supported(dtype, N, d_in, K, r);
   if (query) {
-    *ws_bytes = planes;
-    if (update) return MOLORA_OK;
-    *ws_bytes = 0;
-    if (y_bf16) return MOLORA_OK;
+    *ws_bytes = update ? 2 * plane : 0;
+    if (update || y_bf16) return MOLORA_OK;
     return apply_impl(nullptr, dtype, N, d_in, d_out, nullptr, nullptr, K, r, nullptr, nullptr, k, nullptr, nullptr,
                       nullptr, scale, nullptr, false, nullptr, MOLORA_PATH_AUTO, stream, nullptr, nullptr, ws_bytes);
   }
-  if (ws_bytes && *ws_bytes < planes &&
-      (update || (!y_bf16 && molora_select_path(dtype, N, d_in, d_out, K, r, k) == MOLORA_PATH_STACKED)))
+  if (ws_bytes && *ws_bytes < (update ? 2 * plane
+                               : !y_bf16 && molora_select_path(dtype, N, d_in, d_out, K, r, k) == MOLORA_PATH_STACKED
+                                   ? stacked
+                                   : 0))
     return MOLORA_ERR_INVALID_ARG;
   if (launch_rmsnorm(x, dtype, N, d_in, residual, sum_out, norm_weight, eps, h, h8, scale8, stream) != cudaSuccess)
     return MOLORA_ERR_CUDA;
   if (update) {
-    if (launch_lora_stacked(h, N, d_in, d_out, A, B, K, r, ids, w, k, scale, nullptr, ws, err_word, nullptr, nullptr,
-                            nullptr, nullptr, nullptr, nullptr, nullptr, stream) != cudaSuccess)
+    void* lo = static_cast<uint8_t*>(ws) + plane;
+    if (launch_lora_update(h, N, d_in, A, K, r, ids, w, k, scale, ws, lo, err_word, stream) != cudaSuccess)
       return MOLORA_ERR_CUDA;
-    const LinearUpdate u = {ws, static_cast<const uint8_t*>(ws) + planes / 2, B, K * r};
+    const LinearUpdate u = {ws, lo, B, K * r};
     return launched(launch_linear(lin, stream, &u));
   }
   st = linear_impl(lin, stream);

@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "molora.h"
 
 namespace molora {
@@ -58,8 +60,7 @@ bool stacked_supported(molora_dtype dtype, int64_t N, int32_t d_in, int32_t d_ou
 bool stacked_preferred(molora_dtype dtype, int64_t N, int32_t d_in, int32_t d_out, int32_t K, int32_t r,
                        int32_t k, bool router);
 size_t stacked_workspace_bytes(int64_t N, int32_t K, int32_t r);
-// y == nullptr: the shrink alone, G = scale * c[t,a] (x A_a) as two bf16 planes [N x K*r] in ws, the
-// second one at stacked_workspace_bytes / 2.  W1 == nullptr: ids and w are given.  Otherwise the router (W1, b1, W2, b2) runs in the shrink
+// W1 == nullptr: ids and w are given.  Otherwise the router (W1, b1, W2, b2) runs in the shrink
 // kernel and writes logits (if non-null), ids_out and w_out.
 cudaError_t launch_lora_stacked(const void* x, int64_t N, int32_t d_in, int32_t d_out, const void* A, const void* B,
                                 int32_t K, int32_t r, const int32_t* ids, const float* w, int32_t k, float scale,
@@ -120,13 +121,19 @@ struct LinearArgs {
   int32_t* err_word;
 };
 // Adapters' updates that the product takes along: y += (g_hi + g_lo) B before the activation, for G
-// planes [N x KR] (launch_lora_stacked without y) and B [KR x d_out] in bf16.
+// planes [N x KR] (launch_lora_update) and B [KR x d_out] in bf16.
 struct LinearUpdate {
   const void* g_hi;
   const void* g_lo;
   const void* B;
   int32_t KR;
 };
+// Bytes of one plane, a multiple of 256.
+size_t lora_update_bytes(int64_t N, int32_t KR);
+bool lora_update_supported(molora_dtype dtype, int64_t N, int32_t d_in, int32_t K, int32_t r);
+cudaError_t launch_lora_update(const void* h, int64_t N, int32_t d_in, const void* A, int32_t K, int32_t r,
+                               const int32_t* ids, const float* w, int32_t k, float scale, void* g_hi, void* g_lo,
+                               int32_t* err_word, cudaStream_t stream);
 // True if launch_linear can take updates of KR columns along for these arguments.
 bool linear_takes_update(const LinearArgs& a, const void* B, int32_t KR);
 cudaError_t launch_linear(const LinearArgs& a, cudaStream_t stream, const LinearUpdate* update = nullptr);
@@ -164,6 +171,23 @@ cudaError_t launch_kernel(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
   const cudaError_t last = cudaGetLastError();
   return e != cudaSuccess ? e : last;
+}
+
+// Lets `kernel` have `bytes` of dynamic shared memory on the current device; `done` keeps the devices
+// where it may already.
+template <typename K>
+cudaError_t allow_smem(K kernel, std::atomic<uint64_t>& done, size_t bytes) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess)
+    done.fetch_or(bit, std::memory_order_relaxed);
+  else
+    cudaGetLastError();
+  return e;
 }
 
 }  // namespace molora

@@ -779,22 +779,6 @@ bool linear_map(CUtensorMap* m, CUtensorMapDataType type, uint32_t esize, const 
              CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Lets `kernel` have kMaxSmem on the current device; `done` keeps the devices where it may already.
-template <typename K>
-cudaError_t allow_smem(K kernel, std::atomic<uint64_t>& done) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
-  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxSmem);
-  if (e == cudaSuccess)
-    done.fetch_or(bit, std::memory_order_relaxed);
-  else
-    cudaGetLastError();
-  return e;
-}
-
 bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 
 uint32_t tmem_columns(uint32_t n) {
@@ -856,7 +840,7 @@ cudaError_t launch_tc(const LinearArgs& a, int BN, int MC, const LinearUpdate* u
     e.tma_y = false;
   auto kernel = fp8 ? linear_tc_kernel<true> : linear_tc_kernel<false>;
   static std::atomic<uint64_t> allowed[2];
-  const cudaError_t set = allow_smem(kernel, allowed[fp8]);
+  const cudaError_t set = allow_smem(kernel, allowed[fp8], kMaxSmem);
   if (set != cudaSuccess) return set;
   const int64_t most = num_sms() / (2 * MC);
   const dim3 grid((unsigned)(2 * MC * (p.tiles < most ? p.tiles : most)));
@@ -895,7 +879,7 @@ cudaError_t launch_skinny(const LinearArgs& a, cudaStream_t stream) {
     return cudaErrorNotSupported;
   auto kernel = fp8 ? linear_skinny_kernel<true> : linear_skinny_kernel<false>;
   static std::atomic<uint64_t> allowed[2];
-  const cudaError_t set = allow_smem(kernel, allowed[fp8]);
+  const cudaError_t set = allow_smem(kernel, allowed[fp8], kMaxSmem);
   if (set != cudaSuccess) return set;
   return launch_kernel(kernel, dim3((unsigned)(tiles * p.C)), dim3(kThreads), p.smem, stream, p.C, e, p, a.err_word, mx,
                        mw);
@@ -927,7 +911,7 @@ cudaError_t launch_any(const LinearArgs& a, cudaStream_t stream) {
   if (p.C > 1 && p.smem < 116 * 1024) p.smem = 116 * 1024;  // see launch_skinny
   auto kernel = linear_any_kernel<T>;
   static std::atomic<uint64_t> allowed;
-  const cudaError_t set = allow_smem(kernel, allowed);
+  const cudaError_t set = allow_smem(kernel, allowed, kMaxSmem);
   if (set != cudaSuccess) return set;
   return launch_kernel(kernel, dim3((unsigned)(tiles * p.C)), dim3(kThreads), p.smem, stream, p.C, e, p,
                        static_cast<const T*>(a.x), static_cast<const T*>(a.W), a.d_in, a.err_word);

@@ -926,7 +926,7 @@ cudaError_t launch_lora_stacked(const void* x, int64_t N, int32_t d_in, int32_t 
   if (!stacked_map(&map_b, BF, 2, B, (uint64_t)KR, (uint64_t)d_out, 64, kKBlock, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
   // y [N x d_out] fp32: reduce boxes of 32 rows x 32 columns (128-byte swizzle)
-  if (y && !stacked_map(&map_y, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, y, (uint64_t)N, (uint64_t)d_out, 32, 32,
+  if (!stacked_map(&map_y, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, y, (uint64_t)N, (uint64_t)d_out, 32, 32,
                    CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
 
@@ -952,7 +952,7 @@ cudaError_t launch_lora_stacked(const void* x, int64_t N, int32_t d_in, int32_t 
   cudaError_t e = launch_kernel(router ? stacked_shrink_kernel<true> : stacked_shrink_kernel<false>,
                                 dim3((unsigned)(tiles * sp.C)), dim3(kShrThreads), sp.smem, stream, cluster, N, d_in, K,
                                 r, k, ids, w, scale, g_hi, g_lo, err_word, rio, sp, map_x, map_a, map_w1);
-  if (e != cudaSuccess || !y) return e;
+  if (e != cudaSuccess) return e;
   // persistent clusters of two CTAs over pairs of tiles (see stacked_expand_kernel)
   const int64_t exp_pairs = (tiles + 1) / 2 * ((d_out + ep.BN - 1) / ep.BN);
   const int64_t max_clusters = num_sms() / 2;
