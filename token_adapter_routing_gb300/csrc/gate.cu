@@ -5,8 +5,8 @@
 // load is of consecutive logits, whatever K and the rows' alignment.
 //
 // Everything the choice depends on is reproducible: e = expf(l - max) and 1 / (1 + expf(-l)) are
-// single fp32 operations, and the softmax's denominator is summed in two fp32 terms (error about
-// 2^-46) and rounded once, so it does not depend on the order of the sum.
+// single fp32 operations, and the softmax's denominator is a sum of integers (to 2^-44 of the largest e)
+// that is rounded once, so it does not depend on the order of the sum.
 #include "common.cuh"
 #include "kernels.h"
 
@@ -17,12 +17,14 @@ namespace {
 constexpr int kGateWarps = 8;
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr float kFloatMax = 3.4028234663852886e38f;
+constexpr float kLowest = -__builtin_huge_valf();
 
 struct GateArgs {
   int64_t N;
   int32_t K;
   const float* bias;
   int32_t G, keep, group_top;
+  int32_t group_lanes;   // lanes that look for a group's best: 32 / G rounded down to a power of two
   uint32_t per_inverse;  // ceil(2^20 / (K / G)): a * per_inverse >> 20 is expert a's group
   int32_t k;
   bool sigmoid, renorm;
@@ -32,94 +34,139 @@ struct GateArgs {
   int32_t* err_word;
 };
 
-// hi + lo += v, without losing v's low bits.  The _rn forms are never fused with the operation
-// that made an operand, so every rounding here is the one written.
-__device__ __forceinline__ void two_sum(float& hi, float& lo, float v) {
-  const float s = __fadd_rn(hi, v), b = __fsub_rn(s, hi);
-  lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(s, b)), __fsub_rn(v, b)));
-  hi = s;
-}
-
 // Order-preserving map of a float (not NaN) to an unsigned integer.
 __device__ __forceinline__ uint32_t ordered(float v) {
   const uint32_t u = __float_as_uint(v + 0.f);  // -0 and +0 are equal
   return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
-// The scores s and choices c of this lane's experts, from their logits l (-inf past K) and biases.
+__device__ __forceinline__ float from_ordered(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k);
+}
+
+// What a token's scores come from: its largest logit and, where needed, the softmax's denominator.
+struct Norms {
+  float most, total;
+};
+
+__device__ __forceinline__ float score_of(const GateArgs& a, float l, const Norms& n) {
+  if (a.sigmoid) return __frcp_rn(__fadd_rn(1.f, expf(-l)));
+  const float e = l == kLowest ? 0.f : expf(l - n.most);
+  return n.total > 0.f ? __fdiv_rn(e, n.total) : 0.f;
+}
+
+// The biases of this lane's experts, made finite or -inf.
 template <int TL, int V>
-__device__ __forceinline__ void gate_scores(const GateArgs& a, float (&l)[V], const float (&b)[V], float (&s)[V],
-                                            float (&c)[V]) {
-  const float inf = __int_as_float(0x7f800000);
-  const bool by_logit = !a.bias && (a.G == 1 || a.group_top == 1);
-  bool bad = false;
-  float m = -inf;
+__device__ __forceinline__ void gate_bias(const GateArgs& a, int sub, float (&b)[V]) {
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    bad |= l[i] != l[i] || b[i] != b[i];
-    l[i] = l[i] != l[i] ? -inf : fminf(l[i], kFloatMax);
-    m = fmaxf(m, l[i]);
+    b[i] = a.bias && sub + TL * i < a.K ? a.bias[sub + TL * i] : 0.f;
+    if (b[i] != b[i]) {
+      report(a.err_word, MOLORA_DEV_BAD_LOGIT);
+      b[i] = kLowest;
+    }
+    b[i] = fminf(b[i], kFloatMax);
   }
-  if (bad) report(a.err_word, MOLORA_DEV_BAD_LOGIT);
-  if (a.sigmoid) {
+}
+
+// The choices c of this lane's experts from their logits l (-inf past K, NaN made -inf and +inf finite
+// here) and biases.  Returns what score_of needs; the softmax's denominator is left at 1 where the
+// choice does not need it and the weights are renormalised anyway.
+template <int TL, int V>
+__device__ __forceinline__ Norms gate_choices(const GateArgs& a, float (&l)[V], const float (&b)[V], float (&c)[V]) {
+  const bool by_logit = !a.bias && (a.G == 1 || a.group_top == 1);
+  bool odd = false;
 #pragma unroll
-    for (int i = 0; i < V; ++i) s[i] = __frcp_rn(__fadd_rn(1.f, expf(-l[i])));
-  } else {
-#pragma unroll
-    for (int off = TL / 2; off; off >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, off));
-    float hi = 0.f, lo = 0.f;
+  for (int i = 0; i < V; ++i) odd |= !(l[i] <= kFloatMax);
+  if (__any_sync(kFull, odd)) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      s[i] = l[i] == -inf ? 0.f : expf(l[i] - m);
-      two_sum(hi, lo, s[i]);
+      if (l[i] != l[i]) report(a.err_word, MOLORA_DEV_BAD_LOGIT);
+      l[i] = l[i] != l[i] ? kLowest : fminf(l[i], kFloatMax);
     }
+  }
+  Norms n = {0.f, 1.f};
+  if (!a.sigmoid) {
+    float m = l[0];
 #pragma unroll
-    for (int off = TL / 2; off; off >>= 1) {
-      const float oh = __shfl_xor_sync(kFull, hi, off), ol = __shfl_xor_sync(kFull, lo, off);
-      two_sum(hi, lo, oh);
-      lo = __fadd_rn(lo, ol);
+    for (int i = 1; i < V; ++i) m = fmaxf(m, l[i]);
+#pragma unroll
+    for (int off = TL / 2; off; off >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, off));
+    n.most = m;
+    if (!by_logit || !a.renorm) {
+      // e in units of 2^-22 and 2^-44, summed as integers: exact whatever the order (the rest of an e below
+      // 2^-20 is cut), 512 experts fit 32 bits
+      uint32_t hi = 0, lo = 0;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        c[i] = l[i] == kLowest ? 0.f : expf(l[i] - m);
+        const float u = c[i] * 4194304.f;
+        const uint32_t h = __float2uint_rz(u);
+        hi += h;
+        lo += __float2uint_rz((u - (float)h) * 4194304.f);
+      }
+      if constexpr (TL == 32) {
+        hi = __reduce_add_sync(kFull, hi);
+        lo = __reduce_add_sync(kFull, lo);
+      } else {
+#pragma unroll
+        for (int off = TL / 2; off; off >>= 1) {
+          hi += __shfl_xor_sync(kFull, hi, off);
+          lo += __shfl_xor_sync(kFull, lo, off);
+        }
+      }
+      n.total = __ull2float_rn(((unsigned long long)hi << 22) + lo) * 5.6843418860808015e-14f;  // 2^-44
     }
-    // the lanes may have added in different orders: the first one's sum, rounded once, is the token's
-    const float total = __shfl_sync(kFull, __fadd_rn(hi, lo), 0, TL);
-#pragma unroll
-    for (int i = 0; i < V; ++i) s[i] = total > 0.f ? __fdiv_rn(s[i], total) : 0.f;
   }
+  if (by_logit) {
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    c[i] = l[i] == -inf ? -inf : by_logit ? l[i] : __fadd_rn(s[i], b[i]);
-    c[i] = c[i] > -inf ? fminf(c[i], kFloatMax) : -inf;
+    for (int i = 0; i < V; ++i) c[i] = l[i];
+  } else if (a.sigmoid) {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      c[i] = l[i] == kLowest ? kLowest : __fadd_rn(__frcp_rn(__fadd_rn(1.f, expf(-l[i]))), b[i]);
+  } else {
+    const bool some = n.total > 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) c[i] = l[i] == kLowest || !some ? kLowest : __fadd_rn(__fdiv_rn(c[i], n.total), b[i]);
   }
+  return n;
 }
 
 // The k largest choices by k rounds of a maximum over the token's lanes, ties to the lower index;
 // stores the token's ids and weights if `live`.
 template <int TL, int V>
-__device__ __forceinline__ void gate_rounds(const GateArgs& a, float (&c)[V], const float (&s)[V], int64_t t, bool live) {
-  const float inf = __int_as_float(0x7f800000);
+__device__ __forceinline__ void gate_rounds(const GateArgs& a, float (&c)[V], const float (&l)[V], const Norms& n,
+                                            int64_t t, bool live) {
   const int sub = threadIdx.x & (TL - 1);
   int place[V];  // the round that took expert sub + TL * i
 #pragma unroll
   for (int i = 0; i < V; ++i) place[i] = -1;
   int found = 0;
-  float sum = 0.f;
   for (int j = 0; j < a.k; ++j) {
-    float best = c[0];
+    float top = c[0];
 #pragma unroll
-    for (int i = 1; i < V; ++i) best = fmaxf(best, c[i]);
+    for (int i = 1; i < V; ++i) top = fmaxf(top, c[i]);
 #pragma unroll
-    for (int off = TL / 2; off; off >>= 1) best = fmaxf(best, __shfl_xor_sync(kFull, best, off));
+    for (int off = TL / 2; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, off));
     int at = INT32_MAX;
 #pragma unroll
     for (int i = V - 1; i >= 0; --i)
-      if (c[i] == best) at = sub + TL * i;
+      if (c[i] == top) at = sub + TL * i;
 #pragma unroll
     for (int off = TL / 2; off; off >>= 1) at = min(at, __shfl_xor_sync(kFull, at, off));
-    if (best > -inf) {
+    if (top > kLowest) {
       ++found;
 #pragma unroll
       for (int i = 0; i < V; ++i)
-        if (at == sub + TL * i) c[i] = -inf, place[i] = j, sum += s[i];
+        if (at == sub + TL * i) c[i] = kLowest, place[i] = j;
     }
+  }
+  float s[V], sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    s[i] = 0.f;
+    if (place[i] >= 0) s[i] = score_of(a, l[i], n), sum += s[i];
   }
 #pragma unroll
   for (int off = TL / 2; off; off >>= 1) sum += __shfl_xor_sync(kFull, sum, off);
@@ -134,65 +181,108 @@ __device__ __forceinline__ void gate_rounds(const GateArgs& a, float (&c)[V], co
   for (int j = found + sub; j < a.k; j += TL) a.ids[t * a.k + j] = -1, a.w[t * a.k + j] = 0.f;
 }
 
+// The same for a warp a token, with the choices as ordered integers: a maximum, and the lowest index that
+// has it, is one instruction over the warp.
+template <int V>
+__device__ __forceinline__ void gate_rounds_warp(const GateArgs& a, const float (&c)[V], const float (&l)[V],
+                                                 const Norms& n, int64_t t) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t none = ordered(kLowest);
+  uint32_t key[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) key[i] = ordered(c[i]);
+  uint32_t mine = 0;  // lane j: the expert of round j
+  int found = 0;
+  for (; found < a.k; ++found) {
+    uint32_t best = key[0];
+#pragma unroll
+    for (int i = 1; i < V; ++i) best = max(best, key[i]);
+    const uint32_t top = __reduce_max_sync(kFull, best);
+    if (top <= none) break;
+    uint32_t at = 0xffffffffu;
+#pragma unroll
+    for (int i = V - 1; i >= 0; --i)
+      if (key[i] == top) at = (uint32_t)(lane + 32 * i);
+    at = __reduce_min_sync(kFull, at);
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (at == (uint32_t)(lane + 32 * i)) key[i] = 0u;
+    if (lane == found) mine = at;
+  }
+  float logit = 0.f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const float from = __shfl_sync(kFull, l[i], mine & 31);
+    if ((int)(mine >> 5) == i) logit = from;
+  }
+  const float score = lane < found ? score_of(a, logit, n) : 0.f;
+  float sum = score;
+  if (a.renorm) {
+#pragma unroll
+    for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(kFull, sum, off);
+  }
+  if (lane < a.k) {
+    const float w = !a.renorm ? score : sum > 0.f ? score / sum : 0.f;
+    a.ids[t * a.k + lane] = lane < found ? (int32_t)mine : -1;
+    a.w[t * a.k + lane] = w * a.scale;
+  }
+}
+
 }  // namespace
 
-// Up to 64 experts in one group: TL lanes a token, so that a warp's every instruction works for
+// Up to 16 experts in one group: TL lanes a token, so that a warp's every instruction works for
 // 32 / TL tokens and a maximum over the lanes takes log2(TL) steps.
 template <typename T, int TL, int V>
-__global__ void __launch_bounds__(kGateWarps * 32) gate_small_kernel(const T* __restrict__ logits, const GateArgs a) {
+__global__ void __launch_bounds__(kGateWarps * 32, 4) gate_small_kernel(const T* __restrict__ logits, const GateArgs a) {
   constexpr int kTokens = 32 / TL;  // of a warp
   const int lane = threadIdx.x & 31, sub = lane & (TL - 1), warp = threadIdx.x >> 5;
   pdl_wait();
   pdl_launch_dependents();
   float b[V];
-#pragma unroll
-  for (int i = 0; i < V; ++i) b[i] = a.bias && sub + TL * i < a.K ? a.bias[sub + TL * i] : 0.f;
+  gate_bias<TL, V>(a, sub, b);
   for (int64_t t0 = ((int64_t)blockIdx.x * kGateWarps + warp) * kTokens; t0 < a.N;
        t0 += (int64_t)gridDim.x * kGateWarps * kTokens) {
     const int64_t t = t0 + lane / TL;
     const bool live = t < a.N;
-    float l[V], s[V], c[V];
+    float l[V], c[V];
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      l[i] = live && sub + TL * i < a.K ? to_float(logits[t * a.K + sub + TL * i]) : __int_as_float(0xff800000);
-    gate_scores<TL, V>(a, l, b, s, c);
-    gate_rounds<TL, V>(a, c, s, t, live);
+      l[i] = live && sub + TL * i < a.K ? to_float(logits[t * a.K + sub + TL * i]) : kLowest;
+    const Norms n = gate_choices<TL, V>(a, l, b, c);
+    gate_rounds<TL, V>(a, c, l, n, t, live);
   }
 }
 
-// More experts, or groups: a warp a token.  The k-th largest of the 32 lanes' own maxima is a bound
-// that the k largest choices reach and few others do; those that do (k and a few) are ranked by
-// counting, in shared memory, instead of k rounds over all of them.
+// More experts, or groups: a warp a token, 32 V experts at most.  With up to four a lane the choice is made
+// in rounds; with more, the k-th largest of the 32 lanes' own maxima is a bound that the k largest choices
+// reach and few others do, and those that do (k and a few) are ranked by counting, in shared memory.
 template <typename T, int V>
-__global__ void __launch_bounds__(kGateWarps * 32) gate_topk_kernel(const T* __restrict__ logits, const GateArgs a) {
+__global__ void __launch_bounds__(kGateWarps * 32, V <= 8 ? 4 : 2) gate_topk_kernel(const T* __restrict__ logits, const GateArgs a) {
   extern __shared__ float choices[];  // [warps][K], with groups
   __shared__ float2 cand[kGateWarps][32];  // (choice, expert) of those that reach the bound
-  __shared__ float cand_s[kGateWarps][32];
-  const float inf = __int_as_float(0x7f800000);
+  __shared__ float cand_l[kGateWarps][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t below = (1u << lane) - 1u;
   pdl_wait();
   pdl_launch_dependents();
   float b[V];
-#pragma unroll
-  for (int i = 0; i < V; ++i) b[i] = a.bias && lane + 32 * i < a.K ? a.bias[lane + 32 * i] : 0.f;
+  gate_bias<32, V>(a, lane, b);
   for (int64_t t = (int64_t)blockIdx.x * kGateWarps + warp; t < a.N; t += (int64_t)gridDim.x * kGateWarps) {
-    float l[V], s[V], c[V];
+    float l[V], c[V];
+    const T* row = logits + t * a.K + lane;
 #pragma unroll
-    for (int i = 0; i < V; ++i) l[i] = lane + 32 * i < a.K ? to_float(logits[t * a.K + lane + 32 * i]) : -inf;
-    gate_scores<32, V>(a, l, b, s, c);
+    for (int i = 0; i < V; ++i) l[i] = lane + 32 * i < a.K ? to_float(row[32 * i]) : kLowest;
+    const Norms n = gate_choices<32, V>(a, l, b, c);
     if (a.G > 1) {
-      // each group's best, or best two, by 32 / G lanes rounded down to a power of two
+      // each group's best, or best two
       float* mine = choices + (size_t)warp * a.K;
 #pragma unroll
       for (int i = 0; i < V; ++i)
         if (lane + 32 * i < a.K) mine[lane + 32 * i] = c[i];
       __syncwarp();
       const int per = a.K / a.G;
-      int lanes = 1;
-      while (lanes * 2 * a.G <= 32) lanes *= 2;
-      const int g = lane / lanes;
-      float c1 = -inf, c2 = -inf;
+      const int lanes = a.group_lanes, g = lane / lanes;
+      float c1 = kLowest, c2 = kLowest;
       if (g < a.G) {
         for (int i = lane & (lanes - 1); i < per; i += lanes) {
           const float v = mine[g * per + i];
@@ -216,8 +306,12 @@ __global__ void __launch_bounds__(kGateWarps * 32) gate_topk_kernel(const T* __r
       }
 #pragma unroll
       for (int i = 0; i < V; ++i)
-        if (!((kept >> (((lane + 32 * i) * a.per_inverse) >> 20 & 31u)) & 1u)) c[i] = -inf;
+        if (!((kept >> (((lane + 32 * i) * a.per_inverse) >> 20 & 31u)) & 1u)) c[i] = kLowest;
       __syncwarp();
+    }
+    if constexpr (V <= 4) {
+      gate_rounds_warp<V>(a, c, l, n, t);
+      continue;
     }
     float most = c[0];
 #pragma unroll
@@ -228,32 +322,35 @@ __global__ void __launch_bounds__(kGateWarps * 32) gate_topk_kernel(const T* __r
       const uint32_t same = __ballot_sync(kFull, key == bound);
       if (lane == __ffs(same) - 1) key = 0u;
     }
-    int n = 0;
+    const float least = fmaxf(from_ordered(bound), -kFloatMax);  // experts that are out are below
+    int count = 0;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const bool in = c[i] > -inf && ordered(c[i]) >= bound;
+      const bool in = c[i] >= least;
       const uint32_t who = __ballot_sync(kFull, in);
-      const int at = n + __popc(who & below);
+      const int at = count + __popc(who & below);
       if (in && at < 32) {
         cand[warp][at] = make_float2(c[i], __int_as_float(lane + 32 * i));
-        cand_s[warp][at] = s[i];
+        cand_l[warp][at] = l[i];
       }
-      n += __popc(who);
+      count += __popc(who);
     }
-    if (n > 32) {  // many equal choices
-      gate_rounds<32, V>(a, c, s, t, true);
+    if (count > 32) {  // many equal choices
+      gate_rounds_warp<V>(a, c, l, n, t);
       continue;
     }
     __syncwarp();
-    const float2 mine = cand[warp][lane < n ? lane : 0];
-    const float score = cand_s[warp][lane < n ? lane : 0];
+    const bool has = lane < count;
+    const float2 mine = cand[warp][has ? lane : 0];
     int rank = 0;
-    for (int i = 0; i < n; ++i) {
+#pragma unroll 4
+    for (int i = 0; i < count; ++i) {
       const float2 o = cand[warp][i];
       rank += o.x > mine.x || (o.x == mine.x && __float_as_int(o.y) < __float_as_int(mine.y));
     }
-    const bool chosen = lane < n && rank < a.k;
-    float sum = chosen ? score : 0.f;
+    const bool chosen = has && rank < a.k;
+    const float score = chosen ? score_of(a, cand_l[warp][lane], n) : 0.f;
+    float sum = score;
 #pragma unroll
     for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(kFull, sum, off);
     if (chosen) {
@@ -261,7 +358,7 @@ __global__ void __launch_bounds__(kGateWarps * 32) gate_topk_kernel(const T* __r
       a.ids[t * a.k + rank] = __float_as_int(mine.y);
       a.w[t * a.k + rank] = w * a.scale;
     }
-    if (lane >= n && lane < a.k) a.ids[t * a.k + lane] = -1, a.w[t * a.k + lane] = 0.f;
+    if (lane >= count && lane < a.k) a.ids[t * a.k + lane] = -1, a.w[t * a.k + lane] = 0.f;
     __syncwarp();
   }
 }
@@ -275,12 +372,12 @@ cudaError_t launch_gate_typed(const T* logits, const GateArgs& a, cudaStream_t s
     const int64_t blocks = (a.N + (int64_t)kGateWarps * tokens - 1) / (kGateWarps * tokens), most = (int64_t)num_sms() * 8;
     return dim3((unsigned)(blocks < most ? blocks : most));
   };
-  if (a.G == 1 && a.K <= 64) {
-    if (a.K <= 16) return launch_kernel(gate_small_kernel<T, 8, 2>, grid(4), block, 0, stream, 0, logits, a);
-    if (a.K <= 32) return launch_kernel(gate_small_kernel<T, 8, 4>, grid(4), block, 0, stream, 0, logits, a);
-    return launch_kernel(gate_small_kernel<T, 8, 8>, grid(4), block, 0, stream, 0, logits, a);
+  if (a.G == 1 && a.K <= 16) {
+    if (a.K <= 8) return launch_kernel(gate_small_kernel<T, 8, 1>, grid(4), block, 0, stream, 0, logits, a);
+    return launch_kernel(gate_small_kernel<T, 8, 2>, grid(4), block, 0, stream, 0, logits, a);
   }
   const size_t smem = a.G > 1 ? sizeof(float) * kGateWarps * a.K : 0;
+  if (a.K <= 32) return launch_kernel(gate_topk_kernel<T, 1>, grid(1), block, smem, stream, 0, logits, a);
   if (a.K <= 64) return launch_kernel(gate_topk_kernel<T, 2>, grid(1), block, smem, stream, 0, logits, a);
   if (a.K <= 128) return launch_kernel(gate_topk_kernel<T, 4>, grid(1), block, smem, stream, 0, logits, a);
   if (a.K <= 256) return launch_kernel(gate_topk_kernel<T, 8>, grid(1), block, smem, stream, 0, logits, a);
@@ -294,7 +391,9 @@ cudaError_t launch_gate_topk(const void* logits, molora_dtype dtype, int64_t N, 
                              float scale, int32_t* ids, float* w, int32_t* err_word, cudaStream_t stream) {
   const uint32_t per = (uint32_t)(K / groups);
   // exact for a < 512 and per <= 512: the excess a * (per_inverse - 2^20 / per) / 2^20 < 2^-11 < 1 / per
-  const GateArgs a = {N, K, bias, groups, keep, group_top, ((1u << 20) + per - 1) / per, k, sigmoid, renorm, scale,
+  int32_t lanes = 1;
+  while (lanes * 2 * groups <= 32) lanes *= 2;
+  const GateArgs a = {N, K, bias, groups, keep, group_top, lanes, ((1u << 20) + per - 1) / per, k, sigmoid, renorm, scale,
                       ids, w, err_word};
   if (dtype == MOLORA_BF16) return launch_gate_typed(static_cast<const __nv_bfloat16*>(logits), a, stream);
   return launch_gate_typed(static_cast<const float*>(logits), a, stream);
