@@ -670,7 +670,7 @@ def _array(t: Optional[torch.Tensor], name: str, shape, dtype, device):
     `device` is a GPU is checked by _on_gpu, last, so that a mis-sized argument is reported as such."""
     if t is None:
         return None
-    if (type(t) in _TENSORS and t.shape == shape and t.dtype is dtype and t.device == device and t.is_contiguous()):
+    if type(t) in _TENSORS and t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
         return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name} must be a tensor")
@@ -893,7 +893,11 @@ def molora_norm_linear_lora_apply(x, norm_weight, eps, W, A, B, ids, y, scale, w
 
     def call(ws_ptr, ws_bytes):
         return lib.molora_norm_linear_lora_apply(*args, ws_ptr, ws_bytes, *tail)
-    _check("molora_norm_linear_lora_apply", _workspace(ws, dev, call))
+    if ws is None and y.dtype == torch.bfloat16 and (fp8 or N <= 256):
+        # no path needs a workspace (they are for fp32 y, or for many tokens' update), so none is asked for
+        _check("molora_norm_linear_lora_apply", call(None, None))
+    else:
+        _check("molora_norm_linear_lora_apply", _workspace(ws, dev, call))
     return y, sum_out, h, h8, scale8
 
 

@@ -373,15 +373,6 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t sdst, const CUtensorMa
       "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
       : "memory");
 }
-// The same into every CTA of `cta_mask`, each counting it in its own pair, in the CTA of bar's parity.
-__device__ __forceinline__ void tma_load_2d_pair_multicast(uint32_t sdst, const CUtensorMap* map, int32_t c0,
-                                                           int32_t c1, uint32_t bar, uint16_t cta_mask) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster.cta_group::2 "
-      "[%0], [%1, {%2, %3}], [%4], %5;" ::"r"(sdst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar), "h"(cta_mask)
-      : "memory");
-}
 // One arrival on the mbarrier at a cluster address (dsmem_addr).
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");

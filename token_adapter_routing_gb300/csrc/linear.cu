@@ -38,6 +38,7 @@ constexpr uint32_t kRowBytes = 128; // bytes of K per stage
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 32 * (kEpiWarps + 2);  // + TMA warp (8) + MMA warp (9)
 constexpr int kMaxStages = 8;
+constexpr int kSpan = 8;            // K blocks summed in TMEM before fp32 registers take over
 constexpr size_t kMaxSmem = 227 * 1024;
 constexpr size_t kSmemSlack = 1024;
 constexpr uint32_t kBox = 4096;     // epilogue staging per warp: two boxes of 32 rows x 64 bytes
@@ -69,7 +70,6 @@ struct Epi {
 
 struct TcPlan {
   int BN;                // outputs per tile
-  int MC;                // pairs of a cluster: consecutive token tiles, which share W's boxes
   int S;                 // stages
   int nkb;               // K blocks of 128 bytes
   int nkg;               // K blocks of 64 of the adapters' update (0: none)
@@ -131,33 +131,61 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&p);
 }
 
-// Ends a tile of 128 outputs x `tokens` tokens whose d_in was split over a cluster's C CTAs: each
-// CTA's partial sums go from TMEM to shared memory, [token][output] in the stage ring (free: every load
-// has landed, and the MMAs are waited for here); each CTA then adds its share of the elements in rank
-// order, reading the others' through distributed shared memory, and writes it.  `last(t, o, v)` has
-// the final word on a sum.  Called by all threads.
-template <typename F>
-__device__ __forceinline__ void split_epilogue(const Epi& E, LCtrl* ctrl, uint8_t* sm, uint32_t tmem, int C, int rank,
-                                               int32_t o0, int64_t t0, int tokens, F last) {
+// The sums of a tile of 128 outputs x tokens that its 8 epilogue warps keep: warp w's lanes have outputs
+// 32 (w % 4) .. + 31, columns 16 (w / 4) + 32 j .. + 15.  TMEM's own are added every kSpan K blocks,
+// in two buffers of BN columns in turn (see linear_tc_kernel).
+template <int J>
+struct TileSums {
+  float v[J][16];
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[j][i] = 0.f;
+  }
+  __device__ __forceinline__ void add(uint32_t tmem, int tokens) {
+    const int warp = threadIdx.x >> 5;
+    const uint32_t base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const int c = (warp >> 2) * 16 + 32 * j;
+      if (c >= tokens) continue;
+      float p[16];
+      tmem_ld16(base + (uint32_t)c, p);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[j][i] += p[i];
+    }
+  }
+  // Span number `c`: waits for its MMAs, takes its sums and frees its buffer.
+  __device__ __forceinline__ bool take(LCtrl* ctrl, int c, uint32_t tmem, int BN, int tokens) {
+    if (!__all_sync(0xffffffffu, mbar_wait_spin(&ctrl->tfull[c & 1], (uint32_t)(c >> 1) & 1u, &ctrl->abort))) return false;
+    tc_fence_after();
+    add(tmem + (uint32_t)((c & 1) * BN), tokens);
+    tc_fence_before();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&ctrl->tempty[c & 1]);
+    return true;
+  }
+};
+
+// Ends such a tile, whose d_in was split over a cluster's C CTAs: each CTA's sums go to shared memory,
+// [token][output] in the stage ring (free: every load has landed and every MMA is done); each CTA then adds
+// its share of the elements in rank order, reading the others' through distributed shared memory, and
+// writes it.  `last(t, o, v)` has the final word on a sum.  Called by all threads; `have` is
+// false where a wait ran out.
+template <int J, typename F>
+__device__ __forceinline__ void split_epilogue(const Epi& E, const TileSums<J>& sums, bool have, uint8_t* sm, int C,
+                                               int rank, int32_t o0, int64_t t0, int tokens, F last) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   float* part = reinterpret_cast<float*>(sm);
-  const bool have = mbar_wait(&ctrl->done, 0) && !*(volatile int32_t*)&ctrl->abort;
-  tc_fence_after();
-  const int quarter = warp & 3;
   if (warp < kEpiWarps) {
-    const uint32_t base = tmem + ((uint32_t)(quarter * 32) << 16);
-    for (int c = (warp >> 2) * 16; c < tokens; c += 32) {
-      float v[16];
-      if (__all_sync(0xffffffffu, have))
-        tmem_ld16(base + (uint32_t)c, v);
-      else
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = 0.f;
+    for (int j = 0; j < J; ++j) {
+      const int c = (warp >> 2) * 16 + 32 * j;
 #pragma unroll
       for (int i = 0; i < 16; ++i)
-        if (c + i < tokens) part[(c + i) * kRows + quarter * 32 + lane] = v[i];
+        if (c + i < tokens) part[(c + i) * kRows + (warp & 3) * 32 + lane] = sums.v[j][i];
     }
-    tc_fence_before();
   }
   __syncthreads();
   if (C > 1) cluster_sync();
@@ -198,7 +226,11 @@ __device__ __forceinline__ void split_epilogue(const Epi& E, LCtrl* ctrl, uint8_
 
 }  // namespace
 
-template <bool kFp8>
+// kPromote: a tensor core cuts what its sums lose in an addition, always towards zero, so a long chain of
+// MMAs drifts: 256 of them (d_in = 4096) leave an fp32 result 4e-6 short, 40 times what rounding
+// would.  For fp32 y the epilogue warps take the sums of every 8 K blocks (32 MMAs) into registers
+// and add there.
+template <bool kFp8, bool kPromote>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_tc_kernel(const Epi E, const TcPlan P, int32_t* err_word, const __grid_constant__ CUtensorMap map_x,
                      const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_y,
@@ -211,16 +243,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int BN = P.BN, S = P.S, nkb = P.nkb;
   // the adapters' update is more K blocks of the same accumulators: (G_hi, B), (G_lo, B) in turn
   const int all = kFp8 ? nkb : nkb + 2 * P.nkg;
-  const uint32_t rank = cluster_ctarank(), leader = rank & ~1u, half = rank & 1u, which = rank >> 1;
-  const uint16_t own = (uint16_t)(0x3u << leader), everyone = (uint16_t)((1u << (2 * P.MC)) - 1u);
-  const int64_t pair = blockIdx.x / (2u * P.MC), pairs = gridDim.x / (2u * P.MC);
+  const int span = kPromote ? kSpan : all;  // K blocks summed in TMEM at a time
+  const uint32_t rank = cluster_ctarank();
+  const uint16_t both = 0x3;
+  const int64_t pair = blockIdx.x / 2, pairs = gridDim.x / 2;
   volatile int32_t* abort = &ctrl->abort;
   // tiles in groups of P.group token tiles: within a group, the token tile runs fastest
   auto tile_at = [&](int64_t pt, int32_t& m0, int32_t& n0) {
     const int64_t span = (int64_t)P.group * P.n_tiles, grp = pt / span;
     const int64_t first = grp * P.group, left = P.m_tiles - first, rows = left < P.group ? left : P.group;
     const int64_t in = pt - grp * span;
-    m0 = (int32_t)((first + in % rows) * (2 * P.MC) * kRows + rank * kRows);
+    m0 = (int32_t)((first + in % rows) * 2 * kRows + rank * kRows);
     n0 = (int32_t)(in / rows) * BN;
   };
 
@@ -231,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 8 && lane == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(&ctrl->full[s], 1);
-      mbar_init(&ctrl->empty[s], (uint32_t)P.MC);  // freed by every pair that W's boxes went to
+      mbar_init(&ctrl->empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&ctrl->tfull[b], 1);
@@ -272,29 +305,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           // the leader's barrier counts both CTAs' bytes
-          const uint32_t bar = dsmem_addr(smem_u32(&ctrl->full[s]), leader);
-          if (half == 0) mbar_arrive_expect_tx(&ctrl->full[s], 2 * P.stage_bytes);
+          const uint32_t bar = dsmem_addr(smem_u32(&ctrl->full[s]), 0);
+          if (rank == 0) mbar_arrive_expect_tx(&ctrl->full[s], 2 * P.stage_bytes);
           uint8_t* st = sm + (size_t)s * P.stage_bytes;
-          const int32_t n = n0 + (int32_t)half * (BN / 2);
-          // W's half tile is the same in every pair of the cluster: each pair loads a part of it for all
-          const uint16_t sharers = (uint16_t)(P.MC == 2 ? 0x5u << half : 0x1u << half);
+          const int32_t n = n0 + (int32_t)rank * (BN / 2);
           if (kFp8 || kb < nkb) {
             tma_load_2d_pair(smem_u32(st), &map_x, kb * elems, m0, bar);
-            if (P.MC == 1)
-              tma_load_2d_pair(smem_u32(st + P.off_b), &map_w, kb * elems, n, bar);
-            else
-              tma_load_2d_pair_multicast(smem_u32(st + P.off_b + which * (BN / 4) * kRowBytes), &map_w, kb * elems,
-                                         n + (int32_t)which * (BN / 4), bar, sharers);
+            tma_load_2d_pair(smem_u32(st + P.off_b), &map_w, kb * elems, n, bar);
           } else {
             const int g = (kb - nkb) >> 1;
             tma_load_2d_pair(smem_u32(st), (kb - nkb) & 1 ? &map_glo : &map_ghi, g * 64, m0, bar);
             // B's columns in boxes of 64 rows x 16 columns, as many bytes as W's box
-            for (int q = (int)which; q < BN / 32; q += P.MC) {
-              if (P.MC == 1)
-                tma_load_2d_pair(smem_u32(st + P.off_b + q * 2048), &map_b, n + q * 16, g * 64, bar);
-              else
-                tma_load_2d_pair_multicast(smem_u32(st + P.off_b + q * 2048), &map_b, n + q * 16, g * 64, bar, sharers);
-            }
+            for (int q = 0; q < BN / 32; ++q)
+              tma_load_2d_pair(smem_u32(st + P.off_b + q * 2048), &map_b, n + q * 16, g * 64, bar);
           }
           if (issued < S) ++issued;
           if (++s == S) s = 0, phase ^= 1;
@@ -312,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else if (warp == 9) {
-    if (half == 0 && elect_one()) {
+    if (rank == 0 && elect_one()) {
       const uint32_t idesc = kFp8 ? idesc_e4m3_f32(2 * kRows, (uint32_t)BN) : idesc_bf16_f32(2 * kRows, (uint32_t)BN, false, false);
       // descriptors of stage 0: K-major operands of 128-byte rows, and the update's B (see the TMA warp)
       const uint64_t da = smem_desc(smem_u32(sm), 16, 1024, kSwizzle128B);
@@ -323,33 +346,34 @@ __global__ void __launch_bounds__(kThreads, 1)
       int s = 0, tc = 0;
       uint32_t phase = 0;
       bool ok = true;
-      for (int64_t pt = pair; pt < P.tiles && ok; pt += pairs, ++tc) {
-        const int buf = tc & 1;
-        if (tc >= 2 && !mbar_wait_spin(&ctrl->tempty[buf], (uint32_t)((tc >> 1) - 1) & 1u, abort)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t d = tmem + (uint32_t)(buf * (P.tmem_cols / 2));
-        for (int kb = 0; kb < all; ++kb) {
-          if (!mbar_wait_spin(&ctrl->full[s], phase, abort)) {
+      for (int64_t pt = pair; pt < P.tiles && ok; pt += pairs) {
+        for (int first = 0; first < all && ok; first += span, ++tc) {
+          const int buf = tc & 1, last = min(first + span, all);
+          if (tc >= 2 && !mbar_wait_spin(&ctrl->tempty[buf], (uint32_t)((tc >> 1) - 1) & 1u, abort)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t at = (uint32_t)s * (P.stage_bytes >> 4);
-          if (!kFp8 && kb >= nkb)  // B's columns are MN-major
-            umma_stage<true, kFp8>(d, a_lo + at, g_lo + at, desc_hi, g_hi, idesc | (1u << 16), 1, 32);
-          else
-            umma_stage<true, kFp8>(d, a_lo + at, b_lo + at, desc_hi, desc_hi, idesc, kb != 0);
-          umma_commit_pair(&ctrl->empty[s], everyone);
-          if (++s == S) s = 0, phase ^= 1;
+          const uint32_t d = tmem + (uint32_t)(buf * (P.tmem_cols / 2));
+          for (int kb = first; kb < last; ++kb) {
+            if (!mbar_wait_spin(&ctrl->full[s], phase, abort)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t at = (uint32_t)s * (P.stage_bytes >> 4);
+            if (!kFp8 && kb >= nkb)  // B's columns are MN-major
+              umma_stage<true, kFp8>(d, a_lo + at, g_lo + at, desc_hi, g_hi, idesc | (1u << 16), kb != first, 32);
+            else
+              umma_stage<true, kFp8>(d, a_lo + at, b_lo + at, desc_hi, desc_hi, idesc, kb != first);
+            umma_commit_pair(&ctrl->empty[s], both);
+            if (++s == S) s = 0, phase ^= 1;
+          }
+          if (ok) umma_commit_pair(&ctrl->tfull[buf], both);
         }
-        if (!ok) break;
-        umma_commit_pair(&ctrl->tfull[buf], own);
       }
       if (!ok) report(err_word, MOLORA_DEV_WAIT_TIMEOUT);
-      umma_commit_pair(&ctrl->done, own);  // arrives in both CTAs once every MMA has completed
+      umma_commit_pair(&ctrl->done, both);  // arrives in both CTAs once every MMA has completed
     }
     __syncwarp();
   } else {
@@ -358,8 +382,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
     uint8_t* boxes = sm + P.off_stage + (size_t)warp * kBox;  // two of 32 rows x 64 bytes
     int tc = 0, turn = 0;
-    for (int64_t pt = pair; pt < P.tiles; pt += pairs, ++tc) {
-      const int buf = tc & 1;
+    bool ok = true;
+    for (int64_t pt = pair; pt < P.tiles && ok; pt += pairs) {
       int32_t m0, n0;
       tile_at(pt, m0, n0);
       m0 += quarter * 32;
@@ -381,21 +405,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         prefetch_l2_bulk(static_cast<const uint8_t*>(E.res) + (t * E.d_out + n0) * esize,
                          (uint32_t)min(BN, E.d_out - n0) * esize);
       }
-      if (!__all_sync(0xffffffffu, mbar_wait_spin(&ctrl->tfull[buf], (uint32_t)(tc >> 1) & 1u, abort))) break;
-      tc_fence_after();
-      const uint32_t base = tmem + lanes + (uint32_t)(buf * (P.tmem_cols / 2));
-      uint32_t r[32];
-      if (side < chunks) tmem_ld32_start(base + (uint32_t)(side * 32), r);
-      for (int c = side; c < chunks; c += 2) {
+      // a chunk of 32 columns from its sums to y
+      auto finish = [&](int c, float (&v)[32], const Residual& res, bool add) {
         const int col = n0 + c * 32;
-        float v[32];
-        Residual res;
-        const bool add = E.tma_y && E.res && t < E.N;
-        if (add) res.load(E.res, E.y_bf16, t * E.d_out + col, E.d_out - col);
-        tmem_ld_wait(r);
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-        if (c + 2 < chunks) tmem_ld32_start(base + (uint32_t)((c + 2) * 32), r);
         if (E.sx) {
 #pragma unroll
           for (int i = 0; i < 32; ++i)
@@ -453,10 +465,62 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
+      };
+      auto wait_sums = [&]() {  // the next buffer of sums
+        ok = __all_sync(0xffffffffu, mbar_wait_spin(&ctrl->tfull[tc & 1], (uint32_t)(tc >> 1) & 1u, abort));
+        tc_fence_after();
+        return tmem + lanes + (uint32_t)((tc & 1) * (P.tmem_cols / 2));
+      };
+      auto free_sums = [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(dsmem_addr(smem_u32(&ctrl->tempty[tc & 1]), 0));
+        ++tc;
+      };
+      const bool add = E.tma_y && E.res && t < E.N;
+      Residual res;
+      auto load_residual = [&](int c) {
+        if (add) res.load(E.res, E.y_bf16, t * E.d_out + n0 + c * 32, E.d_out - n0 - c * 32);
+      };
+      if constexpr (kPromote) {
+        float acc[3][32];
+        for (int first = 0; first < all; first += span) {
+          const uint32_t base = wait_sums();
+          if (!ok) break;
+#pragma unroll
+          for (int q = 0; q < 3; ++q) {
+            if (side + 2 * q >= chunks) continue;
+            uint32_t r[32];
+            tmem_ld32_start(base + (uint32_t)((side + 2 * q) * 32), r);
+            tmem_ld_wait(r);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) acc[q][i] = first ? acc[q][i] + __uint_as_float(r[i]) : __uint_as_float(r[i]);
+          }
+          free_sums();
+        }
+        if (!ok) break;
+#pragma unroll
+        for (int q = 0; q < 3; ++q) {
+          if (side + 2 * q >= chunks) continue;
+          load_residual(side + 2 * q);
+          finish(side + 2 * q, acc[q], res, add);
+        }
+      } else {
+        const uint32_t base = wait_sums();
+        if (!ok) break;
+        uint32_t r[32];
+        if (side < chunks) tmem_ld32_start(base + (uint32_t)(side * 32), r);
+        for (int c = side; c < chunks; c += 2) {
+          float v[32];
+          load_residual(c);
+          tmem_ld_wait(r);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+          if (c + 2 < chunks) tmem_ld32_start(base + (uint32_t)((c + 2) * 32), r);
+          finish(c, v, res, add);
+        }
+        free_sums();
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(dsmem_addr(smem_u32(&ctrl->tempty[buf]), leader));
     }
     if (lane == 0) bulk_wait_all();
     __syncwarp();
@@ -480,7 +544,8 @@ struct SkinnyPlan {
   uint32_t stage_bytes, off_b, off_ctrl, tmem_cols, smem;
 };
 
-template <bool kFp8>
+// J: columns of sums a thread keeps, 32 J tokens a tile (few: small code, which a launch fetches cold).
+template <bool kFp8, int J>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_skinny_kernel(const Epi E, const SkinnyPlan P, int32_t* err_word, const __grid_constant__ CUtensorMap map_x,
                          const __grid_constant__ CUtensorMap map_w) {
@@ -505,6 +570,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&ctrl->full[s], 1);
       mbar_init(&ctrl->empty[s], 1);
     }
+    for (int c = 0; c < 2; ++c) {
+      mbar_init(&ctrl->tfull[c], 1);
+      mbar_init(&ctrl->tempty[c], kEpiWarps);
+    }
     mbar_init(&ctrl->done, 1);
     ctrl->abort = 0;
     mbar_fence_init();
@@ -517,6 +586,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_launch_dependents();
   tc_fence_after();
   const uint32_t tmem = ctrl->tmem_base;
+  const int spans = kFp8 ? 1 : (kb1 - kb0 + kSpan - 1) / kSpan;
+  TileSums<J> sums;
+  sums.zero();
+  bool have = true;
 
   if (warp == 8) {
     if (elect_one()) {
@@ -543,25 +616,38 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       int s = 0;
       uint32_t phase = 0;
-      for (int kb = kb0; kb < kb1; ++kb) {
-        if (!mbar_wait_spin(&ctrl->full[s], phase, abort)) {
+      for (int c = 0; c < spans && ok; ++c) {
+        const int first = kb0 + (kFp8 ? 0 : c * kSpan), last = kFp8 ? kb1 : min(first + kSpan, kb1);
+        if (c >= 2 && !mbar_wait_spin(&ctrl->tempty[c & 1], (uint32_t)((c >> 1) - 1) & 1u, abort)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const uint32_t at = (uint32_t)s * (P.stage_bytes >> 4);
-        umma_stage<false, kFp8>(tmem, a_lo + at, b_lo + at, desc_hi, desc_hi, idesc, kb != kb0);
-        umma_commit(&ctrl->empty[s]);
-        if (++s == S) s = 0, phase ^= 1;
+        const uint32_t d = tmem + (uint32_t)((c & 1) * BN);
+        for (int kb = first; kb < last; ++kb) {
+          if (!mbar_wait_spin(&ctrl->full[s], phase, abort)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t at = (uint32_t)s * (P.stage_bytes >> 4);
+          umma_stage<false, kFp8>(d, a_lo + at, b_lo + at, desc_hi, desc_hi, idesc, kb != first);
+          umma_commit(&ctrl->empty[s]);
+          if (++s == S) s = 0, phase ^= 1;
+        }
+        if (ok) umma_commit(&ctrl->tfull[c & 1]);
       }
       if (!ok) report(err_word, MOLORA_DEV_WAIT_TIMEOUT);
       umma_commit(&ctrl->done);
     }
     __syncwarp();
+  } else {
+    for (int c = 0; c < spans && have; ++c) have = sums.take(ctrl, c, tmem, BN, tokens);
   }
-
-  __syncthreads();  // the TMA warp has seen every load land
-  split_epilogue(E, ctrl, sm, tmem, C, rank, o0, t0, tokens, [](int64_t, int32_t, float v) { return v; });
+  // every MMA is done; the TMA warp has seen every load land
+  have = mbar_wait(&ctrl->done, 0) && have && !*abort;
+  __syncthreads();
+  split_epilogue(E, sums, have, sm, C, rank, o0, t0, tokens, [](int64_t, int32_t, float v) { return v; });
   if (warp == 9) {
     tc_fence_after();
     tmem_dealloc(tmem, P.tmem_cols);
@@ -575,53 +661,152 @@ struct AnyPlan {
   int S;
   int nkb;               // K blocks of 64 elements
   int32_t o_tiles;
-  bool vec;              // fp32 rows in 16-byte vectors
+  bool grid;             // both arrays start on 16-byte boundaries
   uint32_t plane, stage_bytes, off_ctrl, tmem_cols, smem;
 };
 
 namespace {
 
-// 8 consecutive elements k0 .. k0 + 7 of a row as bf16 planes (16 bytes each) whose sum they are:
-// one plane for bf16 and e4m3, whose values bf16 holds, three for fp32, by cutting its 24 bits into
-// 8 + 8 + 8.  Elements past d_in are 0.  True if an element was infinite or NaN.
+// 8 consecutive elements of a row, fetched before they are needed and then cut into bf16 planes (16 bytes
+// each) whose sum they are: one plane for bf16 and e4m3, whose values bf16 holds, three for fp32, by
+// cutting its 24 bits into 8 + 8 + 8.  `at` is the first element's place in the array, `left` how many
+// there are in the row (the others are 0).  `grid`: the array starts on a 16-byte boundary, so the elements
+// are read in whole pieces of that grid, the array's last ones excepted (`total` elements).
 template <typename T>
-__device__ __forceinline__ bool load_planes(const T* row, int k0, int d_in, bool, uint4 (&out)[1]) {
-  float v[8];
+struct Piece;
+
+template <>
+struct Piece<float> {
+  static constexpr int kPlanes = 3;
+  uint4 w[3];
+  int shift;
+  __device__ __forceinline__ void load(const float* p, int64_t at, int left, int64_t total, bool grid) {
+    shift = 0;
+    const int64_t base = at & ~int64_t(3);
+    if (grid && base + 12 <= total && left > 0) {
+      shift = (int)(at - base);
+      const uint4* q = reinterpret_cast<const uint4*>(p + base);
+      w[0] = q[0], w[1] = q[1];
+      if (shift) w[2] = q[2];
+    } else {
+      uint32_t u[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = k0 + j < d_in ? to_float(row[k0 + j]) : 0.f;
-  out[0] = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
-  return false;
-}
-__device__ __forceinline__ bool load_planes(const float* row, int k0, int d_in, bool vec, uint4 (&out)[3]) {
-  float v[8];
-  if (vec && k0 + 8 <= d_in) {
-    const float4 a = *reinterpret_cast<const float4*>(row + k0), b = *reinterpret_cast<const float4*>(row + k0 + 4);
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = k0 + j < d_in ? row[k0 + j] : 0.f;
+      for (int j = 0; j < 8; ++j) u[j] = j < left ? __float_as_uint(p[at + j]) : 0u;
+      w[0] = make_uint4(u[0], u[1], u[2], u[3]), w[1] = make_uint4(u[4], u[5], u[6], u[7]);
+    }
   }
-  bool odd = false;
-  uint32_t w[3][4];
+  // True if an element is infinite or NaN.
+  __device__ __forceinline__ bool cut(int left, uint4 (&out)[3]) const {
+    uint32_t e[12] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w, w[2].x, w[2].y, w[2].z, w[2].w};
+    if (shift & 2)
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    uint32_t cut[3][2];
+      for (int j = 0; j < 10; ++j) e[j] = e[j + 2];
+    if (shift & 1)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const float f = v[2 * j + h];
-      odd |= !(fabsf(f) <= 3.4028234663852886e38f);
-      const uint32_t u1 = __float_as_uint(f) & 0xffff0000u;
-      const float r1 = f - __uint_as_float(u1);
-      const uint32_t u2 = __float_as_uint(r1) & 0xffff0000u;
-      cut[0][h] = u1, cut[1][h] = u2, cut[2][h] = __float_as_uint(r1 - __uint_as_float(u2));
+      for (int j = 0; j < 8; ++j) e[j] = e[j + 1];
+    bool odd = false;
+    uint32_t pl[3][4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint32_t part[3][2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float f = 2 * j + h < left ? __uint_as_float(e[2 * j + h]) : 0.f;
+        odd |= !(fabsf(f) <= 3.4028234663852886e38f);
+        part[0][h] = __float_as_uint(f) & 0xffff0000u;
+        const float r = f - __uint_as_float(part[0][h]);
+        part[1][h] = __float_as_uint(r) & 0xffff0000u;
+        part[2][h] = __float_as_uint(r - __uint_as_float(part[1][h]));
+      }
+#pragma unroll
+      for (int k = 0; k < 3; ++k) pl[k][j] = __byte_perm(part[k][0], part[k][1], 0x7632);
     }
 #pragma unroll
-    for (int p = 0; p < 3; ++p) w[p][j] = __byte_perm(cut[p][0], cut[p][1], 0x7632);
+    for (int k = 0; k < 3; ++k) out[k] = make_uint4(pl[k][0], pl[k][1], pl[k][2], pl[k][3]);
+    return odd;
   }
+};
+
+template <>
+struct Piece<__nv_bfloat16> {
+  static constexpr int kPlanes = 1;
+  uint4 w[2];
+  int shift;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p, int64_t at, int left, int64_t total, bool grid) {
+    shift = 0;
+    const int64_t base = at & ~int64_t(7);
+    if (grid && base + 16 <= total && left > 0) {
+      shift = (int)(at - base);
+      const uint4* q = reinterpret_cast<const uint4*>(p + base);
+      w[0] = q[0];
+      if (shift) w[1] = q[1];
+    } else {
+      uint32_t u[8];
 #pragma unroll
-  for (int p = 0; p < 3; ++p) out[p] = make_uint4(w[p][0], w[p][1], w[p][2], w[p][3]);
-  return odd;
-}
+      for (int j = 0; j < 8; ++j) u[j] = j < left ? (uint32_t)__bfloat16_as_ushort(p[at + j]) : 0u;
+      w[0] = make_uint4(u[0] | u[1] << 16, u[2] | u[3] << 16, u[4] | u[5] << 16, u[6] | u[7] << 16);
+    }
+  }
+  __device__ __forceinline__ bool cut(int left, uint4 (&out)[1]) const {
+    uint32_t e[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
+    if (shift & 4)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) e[j] = e[j + 2];
+    if (shift & 4) e[4] = e[6], e[5] = e[7];
+    if (shift & 2)
+#pragma unroll
+      for (int j = 0; j < 5; ++j) e[j] = e[j + 1];
+    if (shift & 1)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) e[j] = __funnelshift_r(e[j], e[j + 1], 16);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (2 * j >= left) e[j] = 0u;
+      if (2 * j + 1 >= left) e[j] &= 0xffffu;
+    }
+    out[0] = make_uint4(e[0], e[1], e[2], e[3]);
+    return false;
+  }
+};
+
+template <>
+struct Piece<__nv_fp8_e4m3> {
+  static constexpr int kPlanes = 1;
+  uint32_t w[3];
+  int shift;
+  __device__ __forceinline__ void load(const __nv_fp8_e4m3* p, int64_t at, int left, int64_t total, bool grid) {
+    shift = 0;
+    const int64_t base = at & ~int64_t(3);
+    const uint8_t* bytes = reinterpret_cast<const uint8_t*>(p);
+    if (grid && base + 12 <= total && left > 0) {
+      shift = (int)(at - base) * 8;
+      const uint32_t* q = reinterpret_cast<const uint32_t*>(bytes + base);
+      w[0] = q[0], w[1] = q[1], w[2] = q[2];
+    } else {
+      w[0] = w[1] = w[2] = 0u;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j < left) w[j >> 2] |= (uint32_t)bytes[at + j] << (8 * (j & 3));
+    }
+  }
+  __device__ __forceinline__ bool cut(int left, uint4 (&out)[1]) const {
+    const uint32_t e[2] = {__funnelshift_r(w[0], w[1], shift), __funnelshift_r(w[1], w[2], shift)};
+    uint32_t b[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float f[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        __nv_fp8_e4m3 v;
+        v.__x = (__nv_fp8_storage_t)((e[j >> 1] >> (16 * (j & 1) + 8 * h)) & 0xffu);
+        f[h] = 2 * j + h < left ? static_cast<float>(v) : 0.f;
+      }
+      b[j] = pack_bf16(f[0], f[1]);
+    }
+    out[0] = make_uint4(b[0], b[1], b[2], b[3]);
+    return false;
+  }
+};
 
 }  // namespace
 
@@ -630,13 +815,13 @@ __device__ __forceinline__ bool load_planes(const float* row, int k0, int d_in, 
 // as bf16 planes in the swizzled stages.  fp32 is three planes, x = x1 + x2 + x3 exactly, and
 //   x w = x1 w1 + x1 w2 + x2 w1 + x2 w2 + x1 w3 + x3 w1 + (terms below 2^-21 of |x w|, 2^-24 of it on average)
 // which is six bf16 products with fp32 sums: an fp32 product at a sixth of the bf16 rate, four times the CUDA
-// cores'.  An infinite operand would meet the zero planes of finite ones (inf * 0): a tile that has
+// cores'.  All but the first are 2^-7 of it and less, and sum apart: their long chain's drift is theirs.  An infinite operand would meet the zero planes of finite ones (inf * 0): a tile that has
 // seen one sums its outputs again on the CUDA cores.
-template <typename T>
+template <typename T, int J>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_any_kernel(const Epi E, const AnyPlan P, const T* __restrict__ x, const T* __restrict__ W, int32_t d_in,
                       int32_t* err_word) {
-  constexpr int kPlanes = sizeof(T) == 4 ? 3 : 1;
+  constexpr int kPlanes = Piece<T>::kPlanes;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   LCtrl* ctrl = reinterpret_cast<LCtrl*>(sm + P.off_ctrl);
@@ -659,6 +844,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&ctrl->full[s], kEpiWarps);
       mbar_init(&ctrl->empty[s], 1);
     }
+    for (int c = 0; c < 2; ++c) {
+      mbar_init(&ctrl->tfull[c], 1);
+      mbar_init(&ctrl->tempty[c], kEpiWarps);
+    }
     mbar_init(&ctrl->done, 1);
     ctrl->abort = 0;
     ctrl->odd = 0;
@@ -669,34 +858,52 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_launch_dependents();  // with this CTA's TMEM held (see linear_tc_kernel)
   tc_fence_after();
   const uint32_t tmem = ctrl->tmem_base;
+  const int spans = (kb1 - kb0 + kSpan - 1) / kSpan;
+  TileSums<J> sums;
+  sums.zero();
+  bool have = true;
 
   if (warp < kEpiWarps) {
+    int taken = 0;
     bool odd = false;
     const int pieces = (kRows + BN) * 8;  // 16-byte pieces of a stage's plane: W's rows, then x's
     for (int kb = kb0; kb < kb1; ++kb) {
       const int i = kb - kb0, s = i % S, use = i / S;
       if (use > 0 && !__all_sync(0xffffffffu, mbar_wait_spin(&ctrl->empty[s], (uint32_t)(use - 1) & 1u, abort))) break;
       uint8_t* st = sm + (size_t)s * P.stage_bytes;
-#pragma unroll 2
-      for (int q = tid; q < pieces; q += kEpiWarps * 32) {
-        const int row = q >> 3, piece = q & 7, k0 = kb * 64 + piece * 8;
-        uint4 p[kPlanes];
-        const bool is_w = row < kRows;
-        const bool there = is_w ? o0 + row < E.d_out : row - kRows < tokens;
-        if (there) {
-          odd |= load_planes(is_w ? W + (int64_t)(o0 + row) * d_in : x + (t0 + row - kRows) * d_in, k0, d_in, P.vec, p);
-        } else {
+      // four pieces a thread at a time: their loads are in flight together
+      for (int q0 = tid; q0 < pieces; q0 += 4 * kEpiWarps * 32) {
+        Piece<T> piece[4];
+        int left[4];
 #pragma unroll
-          for (int j = 0; j < kPlanes; ++j) p[j] = make_uint4(0, 0, 0, 0);
+        for (int j = 0; j < 4; ++j) {
+          const int q = q0 + j * kEpiWarps * 32, row = q >> 3, k0 = kb * 64 + (q & 7) * 8;
+          const bool is_w = row < kRows;
+          const bool there = q < pieces && (is_w ? o0 + row < E.d_out : row - kRows < tokens);
+          left[j] = there ? d_in - k0 : 0;
+          if (is_w)
+            piece[j].load(W, (int64_t)(o0 + row) * d_in + k0, left[j], (int64_t)E.d_out * d_in, P.grid);
+          else
+            piece[j].load(x, (t0 + row - kRows) * d_in + k0, left[j], E.N * d_in, P.grid);
         }
-        const uint32_t at = sw128_offset((uint32_t)row, (uint32_t)piece);
 #pragma unroll
-        for (int j = 0; j < kPlanes; ++j) *reinterpret_cast<uint4*>(st + j * P.plane + at) = p[j];
+        for (int j = 0; j < 4; ++j) {
+          const int q = q0 + j * kEpiWarps * 32;
+          if (q >= pieces) continue;
+          uint4 p[kPlanes];
+          odd |= piece[j].cut(left[j], p);
+          const uint32_t at = sw128_offset((uint32_t)(q >> 3), (uint32_t)(q & 7));
+#pragma unroll
+          for (int k = 0; k < kPlanes; ++k) *reinterpret_cast<uint4*>(st + k * P.plane + at) = p[k];
+        }
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctrl->full[s]);
+      // the last span's sums, with this one's first stages already filled
+      if (i >= kSpan && i % kSpan == 2 && have) have = sums.take(ctrl, taken++, tmem, BN, tokens);
     }
+    while (taken < spans && have) have = sums.take(ctrl, taken++, tmem, BN, tokens);
     if (odd) ctrl->odd = 1;
   } else if (warp == 9) {
     if (elect_one()) {
@@ -705,35 +912,53 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t da = smem_desc(first, 16, 1024, kSwizzle128B);
       const uint32_t a_lo = (uint32_t)da, b_lo = a_lo + ((uint32_t)kRows * kRowBytes >> 4), desc_hi = (uint32_t)(da >> 32);
       bool ok = true;
-      for (int kb = kb0; kb < kb1; ++kb) {
-        const int i = kb - kb0, s = i % S;
-        if (!mbar_wait_spin(&ctrl->full[s], (uint32_t)(i / S) & 1u, abort)) {
+      const uint32_t step = P.plane >> 4, cross = tmem + 2u * (uint32_t)BN;
+      int s = 0;
+      uint32_t phase = 0;
+      for (int c = 0; c < spans && ok; ++c) {
+        const int from = kb0 + c * kSpan, last = min(from + kSpan, kb1);
+        if (c >= 2 && !mbar_wait_spin(&ctrl->tempty[c & 1], (uint32_t)((c >> 1) - 1) & 1u, abort)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const uint32_t st = smem_u32(sm + (size_t)s * P.stage_bytes);
-        const uint32_t at = (st - first) >> 4, step = P.plane >> 4;
-        umma_stage<false, false>(tmem, a_lo + at, b_lo + at, desc_hi, desc_hi, idesc, i != 0);
-        if (kPlanes == 3) {
-          const uint32_t a1 = a_lo + at, a2 = a1 + step, a3 = a2 + step, b1 = b_lo + at, b2 = b1 + step, b3 = b2 + step;
-          umma_stage<false, false>(tmem, a1, b2, desc_hi, desc_hi, idesc, 1);
-          umma_stage<false, false>(tmem, a2, b1, desc_hi, desc_hi, idesc, 1);
-          umma_stage<false, false>(tmem, a2, b2, desc_hi, desc_hi, idesc, 1);
-          umma_stage<false, false>(tmem, a1, b3, desc_hi, desc_hi, idesc, 1);
-          umma_stage<false, false>(tmem, a3, b1, desc_hi, desc_hi, idesc, 1);
+        const uint32_t d = tmem + (uint32_t)((c & 1) * BN);
+        for (int kb = from; kb < last; ++kb) {
+          if (!mbar_wait_spin(&ctrl->full[s], phase, abort)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a1 = a_lo + (uint32_t)s * (P.stage_bytes >> 4), b1 = a1 + (b_lo - a_lo);
+          umma_stage<false, false>(d, a1, b1, desc_hi, desc_hi, idesc, kb != from);
+          if (kPlanes == 3) {
+            const uint32_t a2 = a1 + step, a3 = a2 + step, b2 = b1 + step, b3 = b2 + step;
+            umma_stage<false, false>(cross, a1, b2, desc_hi, desc_hi, idesc, kb != kb0);
+            umma_stage<false, false>(cross, a2, b1, desc_hi, desc_hi, idesc, 1);
+            umma_stage<false, false>(cross, a2, b2, desc_hi, desc_hi, idesc, 1);
+            umma_stage<false, false>(cross, a1, b3, desc_hi, desc_hi, idesc, 1);
+            umma_stage<false, false>(cross, a3, b1, desc_hi, desc_hi, idesc, 1);
+          }
+          umma_commit(&ctrl->empty[s]);
+          if (++s == S) s = 0, phase ^= 1;
         }
-        umma_commit(&ctrl->empty[s]);
+        if (ok) umma_commit(&ctrl->tfull[c & 1]);
       }
       if (!ok) report(err_word, MOLORA_DEV_WAIT_TIMEOUT);
       umma_commit(&ctrl->done);
     }
     __syncwarp();
   }
+  have = mbar_wait(&ctrl->done, 0) && have && !*abort;
+  if (kPlanes == 3 && warp < kEpiWarps && __all_sync(0xffffffffu, have)) {
+    tc_fence_after();
+    sums.add(tmem + 2u * (uint32_t)BN, tokens);
+    tc_fence_before();
+  }
   __syncthreads();
   // an odd element of any CTA of the cluster (they hold other parts of the same rows)
   const uint32_t seen_at = smem_u32(&ctrl->odd);
-  split_epilogue(E, ctrl, sm, tmem, C, rank, o0, t0, tokens, [&](int64_t t, int32_t o, float v) {
+  split_epilogue(E, sums, have, sm, C, rank, o0, t0, tokens, [&](int64_t t, int32_t o, float v) {
     if (kPlanes == 1) return v;
     int32_t seen = 0;
     for (int c = 0; c < C; ++c) seen |= C > 1 ? __float_as_int(dsmem_ld_f32(dsmem_addr(seen_at, (uint32_t)c))) : ctrl->odd;
@@ -799,21 +1024,17 @@ Epi epilogue_of(const LinearArgs& a) {
   return e;
 }
 
-cudaError_t launch_tc(const LinearArgs& a, int BN, int MC, const LinearUpdate* u, cudaStream_t stream) {
+cudaError_t launch_tc(const LinearArgs& a, int BN, bool promote, const LinearUpdate* u, cudaStream_t stream) {
   const bool fp8 = a.dtype == MOLORA_E4M3;
   Epi e = epilogue_of(a);
   TcPlan p = {};
   p.BN = BN;
-  p.MC = MC;
   p.nkb = (int)(((int64_t)a.d_in * (fp8 ? 1 : 2) + kRowBytes - 1) / kRowBytes);
   p.nkg = u ? (u->KR + 63) / 64 : 0;
-  p.m_tiles = (a.N + 2 * MC * kRows - 1) / (2 * MC * kRows);
+  p.m_tiles = (a.N + 2 * kRows - 1) / (2 * kRows);
   p.n_tiles = (a.d_out + BN - 1) / BN;
   p.tiles = p.m_tiles * p.n_tiles;
-  p.group = 8 / MC;
-#ifdef MOLORA_TUNING_ENV
-  if (const char* g = getenv("MOLORA_LIN_GROUP")) p.group = atoi(g);
-#endif
+  p.group = 8;
   p.off_b = kRows * kRowBytes;
   p.stage_bytes = p.off_b + (uint32_t)(BN / 2) * kRowBytes;
   p.tmem_cols = tmem_columns(2 * (uint32_t)(BN <= 64 ? 64 : BN <= 128 ? 128 : 256));
@@ -826,7 +1047,7 @@ cudaError_t launch_tc(const LinearArgs& a, int BN, int MC, const LinearUpdate* u
   // be waiting for a partner that this kernel's other CTAs keep out
   p.smem = kMaxSmem;
   CUtensorMap mx, mw, my = {};
-  if (!operand_map(&mx, a, a.x, a.N, kRows) || !operand_map(&mw, a, a.W, a.d_out, (uint32_t)(BN / 2 / MC)))
+  if (!operand_map(&mx, a, a.x, a.N, kRows) || !operand_map(&mw, a, a.W, a.d_out, (uint32_t)(BN / 2)))
     return cudaErrorNotSupported;
   const auto BF = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   CUtensorMap ghi = {}, glo = {}, mb = {};
@@ -838,13 +1059,13 @@ cudaError_t launch_tc(const LinearArgs& a, int BN, int MC, const LinearUpdate* u
       !linear_map(&my, a.y_bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, a.y_bf16 ? 2 : 4,
                   a.y, (uint64_t)a.N, (uint64_t)a.d_out, a.y_bf16 ? 32 : 16, 32, CU_TENSOR_MAP_SWIZZLE_64B))
     e.tma_y = false;
-  auto kernel = fp8 ? linear_tc_kernel<true> : linear_tc_kernel<false>;
-  static std::atomic<uint64_t> allowed[2];
-  const cudaError_t set = allow_smem(kernel, allowed[fp8], kMaxSmem);
+  auto kernel = fp8 ? linear_tc_kernel<true, false> : promote ? linear_tc_kernel<false, true> : linear_tc_kernel<false, false>;
+  static std::atomic<uint64_t> allowed[3];
+  const cudaError_t set = allow_smem(kernel, allowed[fp8 ? 2 : promote], kMaxSmem);
   if (set != cudaSuccess) return set;
-  const int64_t most = num_sms() / (2 * MC);
-  const dim3 grid((unsigned)(2 * MC * (p.tiles < most ? p.tiles : most)));
-  return launch_kernel(kernel, grid, dim3(kThreads), p.smem, stream, 2 * MC, e, p, a.err_word, mx, mw, my, ghi, glo, mb);
+  const int64_t most = num_sms() / 2;
+  const dim3 grid((unsigned)(2 * (p.tiles < most ? p.tiles : most)));
+  return launch_kernel(kernel, grid, dim3(kThreads), p.smem, stream, 2, e, p, a.err_word, mx, mw, my, ghi, glo, mb);
 }
 
 cudaError_t launch_skinny(const LinearArgs& a, cudaStream_t stream) {
@@ -860,7 +1081,7 @@ cudaError_t launch_skinny(const LinearArgs& a, cudaStream_t stream) {
   while (p.C < 8 && tiles * p.C * 2 <= num_sms() && p.nkb >= p.C * 4) p.C *= 2;
   p.off_b = kRows * kRowBytes;
   p.stage_bytes = p.off_b + (uint32_t)p.BN * kRowBytes;
-  p.tmem_cols = tmem_columns((uint32_t)p.BN);
+  p.tmem_cols = tmem_columns(2 * (uint32_t)p.BN);
   const size_t fixed = sizeof(LCtrl) + kSmemSlack;
   const size_t partial = (size_t)p.BN * kRows * sizeof(float);
   const int need = (p.nkb + p.C - 1) / p.C;
@@ -877,12 +1098,24 @@ cudaError_t launch_skinny(const LinearArgs& a, cudaStream_t stream) {
   CUtensorMap mx, mw;
   if (!operand_map(&mx, a, a.x, a.N, (uint32_t)p.BN) || !operand_map(&mw, a, a.W, a.d_out, kRows))
     return cudaErrorNotSupported;
-  auto kernel = fp8 ? linear_skinny_kernel<true> : linear_skinny_kernel<false>;
-  static std::atomic<uint64_t> allowed[2];
-  const cudaError_t set = allow_smem(kernel, allowed[fp8], kMaxSmem);
-  if (set != cudaSuccess) return set;
-  return launch_kernel(kernel, dim3((unsigned)(tiles * p.C)), dim3(kThreads), p.smem, stream, p.C, e, p, a.err_word, mx,
-                       mw);
+  auto go = [&](auto kernel, std::atomic<uint64_t>& allowed) {
+    const cudaError_t set = allow_smem(kernel, allowed, kMaxSmem);
+    if (set != cudaSuccess) return set;
+    return launch_kernel(kernel, dim3((unsigned)(tiles * p.C)), dim3(kThreads), p.smem, stream, p.C, e, p, a.err_word, mx,
+                         mw);
+  };
+  static std::atomic<uint64_t> allowed[8];
+  switch (p.BN) {
+    case 16:
+    case 32:
+      return fp8 ? go(linear_skinny_kernel<true, 1>, allowed[0]) : go(linear_skinny_kernel<false, 1>, allowed[1]);
+    case 64:
+      return fp8 ? go(linear_skinny_kernel<true, 2>, allowed[2]) : go(linear_skinny_kernel<false, 2>, allowed[3]);
+    case 128:
+      return fp8 ? go(linear_skinny_kernel<true, 4>, allowed[4]) : go(linear_skinny_kernel<false, 4>, allowed[5]);
+    default:
+      return fp8 ? go(linear_skinny_kernel<true, 8>, allowed[6]) : go(linear_skinny_kernel<false, 8>, allowed[7]);
+  }
 }
 
 template <typename T>
@@ -897,10 +1130,10 @@ cudaError_t launch_any(const LinearArgs& a, cudaStream_t stream) {
   const int64_t tiles = tiles_at(p.BN);
   p.C = 1;
   while (p.C < 8 && tiles * p.C * 2 <= num_sms() && p.nkb >= p.C * 4) p.C *= 2;
-  p.vec = a.d_in % 4 == 0 && aligned(a.x, 16) && aligned(a.W, 16);
+  p.grid = aligned(a.x, 16) && aligned(a.W, 16);
   p.plane = (uint32_t)(kRows + p.BN) * kRowBytes;
   p.stage_bytes = planes * p.plane;
-  p.tmem_cols = tmem_columns((uint32_t)p.BN);
+  p.tmem_cols = tmem_columns((planes == 3 ? 3u : 2u) * (uint32_t)p.BN);
   const size_t fixed = sizeof(LCtrl) + kSmemSlack, partial = (size_t)p.BN * kRows * sizeof(float);
   p.S = (int)((kMaxSmem - fixed) / p.stage_bytes);
   if (p.S > 4) p.S = 4;
@@ -909,12 +1142,16 @@ cudaError_t launch_any(const LinearArgs& a, cudaStream_t stream) {
   p.off_ctrl = (uint32_t)ring;
   p.smem = (uint32_t)(ring + fixed);
   if (p.C > 1 && p.smem < 116 * 1024) p.smem = 116 * 1024;  // see launch_skinny
-  auto kernel = linear_any_kernel<T>;
-  static std::atomic<uint64_t> allowed;
-  const cudaError_t set = allow_smem(kernel, allowed, kMaxSmem);
-  if (set != cudaSuccess) return set;
-  return launch_kernel(kernel, dim3((unsigned)(tiles * p.C)), dim3(kThreads), p.smem, stream, p.C, e, p,
-                       static_cast<const T*>(a.x), static_cast<const T*>(a.W), a.d_in, a.err_word);
+  auto go = [&](auto kernel, std::atomic<uint64_t>& allowed) {
+    const cudaError_t set = allow_smem(kernel, allowed, kMaxSmem);
+    if (set != cudaSuccess) return set;
+    return launch_kernel(kernel, dim3((unsigned)(tiles * p.C)), dim3(kThreads), p.smem, stream, p.C, e, p,
+                         static_cast<const T*>(a.x), static_cast<const T*>(a.W), a.d_in, a.err_word);
+  };
+  static std::atomic<uint64_t> allowed[3];
+  if (p.BN <= 32) return go(linear_any_kernel<T, 1>, allowed[0]);
+  if (p.BN == 64) return go(linear_any_kernel<T, 2>, allowed[1]);
+  return go(linear_any_kernel<T, 4>, allowed[2]);
 }
 
 }  // namespace
@@ -943,22 +1180,25 @@ cudaError_t launch_linear(const LinearArgs& a, cudaStream_t stream, const Linear
     return launch_any<float>(a, stream);
   }
   if (!many_tokens(a)) return launch_skinny(a, stream);
+  // K blocks of fp32 results that sum in registers (see linear_tc_kernel), which hold 96 columns a thread;
+  // e4m3 sums are half as many and drift a tenth as far (2e-7 at d_in = 4096)
+  const int64_t blocks = ((int64_t)a.d_in + 63) / 64 + (update ? (update->KR + 63) / 64 * 2 : 0);
+  const bool promote = a.dtype == MOLORA_BF16 && !a.y_bf16 && blocks > kSpan;
   // the width whose waves of tiles cost least
   const int64_t pairs = num_sms() / 2, m_tiles = (a.N + 2 * kRows - 1) / (2 * kRows);
-  int best = 256;
+  int best = 128;
   int64_t cost = INT64_MAX;
   for (int BN : {256, 224, 192, 160, 128, 96, 64}) {
+    if (promote && BN > 192) continue;
     const int64_t tiles = m_tiles * ((a.d_out + BN - 1) / BN), waves = (tiles + pairs - 1) / pairs;
     // cycles of a stage, halved: 420 for narrow tiles, 2 BN and 90 for wide ones
     const int64_t c = waves * (BN + 45 > 210 ? BN + 45 : 210);
     if (c < cost) cost = c, best = BN;
   }
-  int MC = 1;
 #ifdef MOLORA_TUNING_ENV
   if (const char* g = getenv("MOLORA_LIN_BN")) best = atoi(g);
-  if (const char* g = getenv("MOLORA_LIN_MC")) MC = atoi(g);
 #endif
-  return launch_tc(a, best, MC, update, stream);
+  return launch_tc(a, best, promote, update, stream);
 }
 
 }  // namespace molora
