@@ -37,6 +37,8 @@ constexpr int kRows = 128;          // rows of a box of x (or of W in the skinny
 constexpr uint32_t kRowBytes = 128; // bytes of K per stage
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 32 * (kEpiWarps + 2);  // + TMA warp (8) + MMA warp (9)
+constexpr int kAnyThreads = 512;    // linear_any_kernel: 15 warps that lay out operands + MMA warp (15)
+constexpr int kCutters = kAnyThreads - 32;
 constexpr int kMaxStages = 8;
 constexpr int kSpan = 8;            // K blocks summed in TMEM before fp32 registers take over
 constexpr size_t kMaxSmem = 227 * 1024;
@@ -670,24 +672,36 @@ namespace {
 // 8 consecutive elements of a row, fetched before they are needed and then cut into bf16 planes (16 bytes
 // each) whose sum they are: one plane for bf16 and e4m3, whose values bf16 holds, three for fp32, by
 // cutting its 24 bits into 8 + 8 + 8.  `at` is the first element's place in the array, `left` how many
-// there are in the row (the others are 0).  `grid`: the array starts on a 16-byte boundary, so the elements
-// are read in whole pieces of that grid, the array's last ones excepted (`total` elements).
-template <typename T>
+// there are in the row (the others are 0).  kVec: rows start on 16-byte boundaries.  Else, with `grid`
+// (the array starts on one), the elements are read in whole pieces of that grid, the array's last ones
+// excepted (`total` elements).  load_inside reads from the grid's boundary `sh` elements before the first
+// one; two pieces' worth from there, and four elements, have to be the array's.
+template <typename T, bool kVec>
 struct Piece;
 
-template <>
-struct Piece<float> {
+template <bool kVec>
+struct Piece<float, kVec> {
   static constexpr int kPlanes = 3;
-  uint4 w[3];
+  static constexpr int kGrid = 4;  // elements of a 16-byte piece
+  uint4 w[kVec ? 2 : 3];
   int shift;
+  __device__ __forceinline__ void load_inside(const float* p, int sh) {
+    shift = sh;
+    const uint4* q = reinterpret_cast<const uint4*>(p);
+    w[0] = q[0], w[1] = q[1];
+    if (!kVec) w[kVec ? 0 : 2] = q[2];
+  }
   __device__ __forceinline__ void load(const float* p, int64_t at, int left, int64_t total, bool grid) {
     shift = 0;
     const int64_t base = at & ~int64_t(3);
-    if (grid && base + 12 <= total && left > 0) {
+    if (kVec && left >= 8) {
+      const uint4* q = reinterpret_cast<const uint4*>(p + at);
+      w[0] = q[0], w[1] = q[1];
+    } else if (!kVec && grid && base + 12 <= total && left > 0) {
       shift = (int)(at - base);
       const uint4* q = reinterpret_cast<const uint4*>(p + base);
       w[0] = q[0], w[1] = q[1];
-      if (shift) w[2] = q[2];
+      if (shift) w[kVec ? 0 : 2] = q[2];
     } else {
       uint32_t u[8];
 #pragma unroll
@@ -697,24 +711,30 @@ struct Piece<float> {
   }
   // True if an element is infinite or NaN.
   __device__ __forceinline__ bool cut(int left, uint4 (&out)[3]) const {
-    uint32_t e[12] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w, w[2].x, w[2].y, w[2].z, w[2].w};
-    if (shift & 2)
+    const uint4 last = w[kVec ? 1 : 2];
+    uint32_t e[12] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w, last.x, last.y, last.z, last.w};
+    if (!kVec) {
+      if (shift & 2)
 #pragma unroll
-      for (int j = 0; j < 10; ++j) e[j] = e[j + 2];
-    if (shift & 1)
+        for (int j = 0; j < 10; ++j) e[j] = e[j + 2];
+      if (shift & 1)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) e[j] = e[j + 1];
-    bool odd = false;
+        for (int j = 0; j < 8; ++j) e[j] = e[j + 1];
+      if (left < 8)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) e[j] = j < left ? e[j] : 0u;
+    }
+    uint32_t top = 0;  // a maximum of the magnitudes' bits: exponents of all ones are infinite or NaN
     uint32_t pl[3][4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       uint32_t part[3][2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const float f = 2 * j + h < left ? __uint_as_float(e[2 * j + h]) : 0.f;
-        odd |= !(fabsf(f) <= 3.4028234663852886e38f);
-        part[0][h] = __float_as_uint(f) & 0xffff0000u;
-        const float r = f - __uint_as_float(part[0][h]);
+        const uint32_t f = e[2 * j + h];
+        top = max(top, f & 0x7fffffffu);
+        part[0][h] = f & 0xffff0000u;
+        const float r = __uint_as_float(f) - __uint_as_float(part[0][h]);
         part[1][h] = __float_as_uint(r) & 0xffff0000u;
         part[2][h] = __float_as_uint(r - __uint_as_float(part[1][h]));
       }
@@ -723,15 +743,21 @@ struct Piece<float> {
     }
 #pragma unroll
     for (int k = 0; k < 3; ++k) out[k] = make_uint4(pl[k][0], pl[k][1], pl[k][2], pl[k][3]);
-    return odd;
+    return top >= 0x7f800000u;
   }
 };
 
-template <>
-struct Piece<__nv_bfloat16> {
+template <bool kVec>
+struct Piece<__nv_bfloat16, kVec> {
   static constexpr int kPlanes = 1;
+  static constexpr int kGrid = 8;
   uint4 w[2];
   int shift;
+  __device__ __forceinline__ void load_inside(const __nv_bfloat16* p, int sh) {
+    shift = sh;
+    const uint4* q = reinterpret_cast<const uint4*>(p);
+    w[0] = q[0], w[1] = q[1];
+  }
   __device__ __forceinline__ void load(const __nv_bfloat16* p, int64_t at, int left, int64_t total, bool grid) {
     shift = 0;
     const int64_t base = at & ~int64_t(7);
@@ -759,21 +785,29 @@ struct Piece<__nv_bfloat16> {
     if (shift & 1)
 #pragma unroll
       for (int j = 0; j < 4; ++j) e[j] = __funnelshift_r(e[j], e[j + 1], 16);
+    if (left < 8) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (2 * j >= left) e[j] = 0u;
-      if (2 * j + 1 >= left) e[j] &= 0xffffu;
+      for (int j = 0; j < 4; ++j) {
+        if (2 * j >= left) e[j] = 0u;
+        if (2 * j + 1 >= left) e[j] &= 0xffffu;
+      }
     }
     out[0] = make_uint4(e[0], e[1], e[2], e[3]);
     return false;
   }
 };
 
-template <>
-struct Piece<__nv_fp8_e4m3> {
+template <bool kVec>
+struct Piece<__nv_fp8_e4m3, kVec> {
   static constexpr int kPlanes = 1;
+  static constexpr int kGrid = 4;  // (4-byte pieces)
   uint32_t w[3];
   int shift;
+  __device__ __forceinline__ void load_inside(const __nv_fp8_e4m3* p, int sh) {
+    shift = sh * 8;
+    const uint32_t* q = reinterpret_cast<const uint32_t*>(p);
+    w[0] = q[0], w[1] = q[1], w[2] = q[2];
+  }
   __device__ __forceinline__ void load(const __nv_fp8_e4m3* p, int64_t at, int left, int64_t total, bool grid) {
     shift = 0;
     const int64_t base = at & ~int64_t(3);
@@ -817,11 +851,16 @@ struct Piece<__nv_fp8_e4m3> {
 // which is six bf16 products with fp32 sums: an fp32 product at a sixth of the bf16 rate, four times the CUDA
 // cores'.  All but the first are 2^-7 of it and less, and sum apart: their long chain's drift is theirs.  An infinite operand would meet the zero planes of finite ones (inf * 0): a tile that has
 // seen one sums its outputs again on the CUDA cores.
-template <typename T, int J>
-__global__ void __launch_bounds__(kThreads, 1)
+//
+// Bound by the threads that cut the operands: 15 warps, with their next pieces on the way while a stage is
+// written and handed over.  1024 x 4096 x 4096 fp32 367 us (94 TFLOP/s, 577 us for the library's fp32 product);
+// of 5400 cycles a K block, the MMAs are 1500 and the operands' way from L2 1000.
+template <typename T, bool kVec, int J>
+__global__ void __launch_bounds__(kAnyThreads, 1)
     linear_any_kernel(const Epi E, const AnyPlan P, const T* __restrict__ x, const T* __restrict__ W, int32_t d_in,
                       int32_t* err_word) {
-  constexpr int kPlanes = Piece<T>::kPlanes;
+  constexpr int kPlanes = Piece<T, kVec>::kPlanes;
+  constexpr int kPieces = ((kRows + 32 * J) * 8 + kCutters - 1) / kCutters;  // of a stage, a thread
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   LCtrl* ctrl = reinterpret_cast<LCtrl*>(sm + P.off_ctrl);
@@ -835,13 +874,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tokens = (int)min((int64_t)BN, E.N - t0);
   volatile int32_t* abort = &ctrl->abort;
 
-  if (warp == 9) {
+  if (warp == 15) {
     tmem_alloc(&ctrl->tmem_base, P.tmem_cols);
     tmem_relinquish();
   }
-  if (warp == 8 && lane == 0) {
+  if (warp == 14 && lane == 0) {
     for (int s = 0; s < S; ++s) {
-      mbar_init(&ctrl->full[s], kEpiWarps);
+      mbar_init(&ctrl->full[s], kCutters / 32);
       mbar_init(&ctrl->empty[s], 1);
     }
     for (int c = 0; c < 2; ++c) {
@@ -863,49 +902,71 @@ __global__ void __launch_bounds__(kThreads, 1)
   sums.zero();
   bool have = true;
 
-  if (warp < kEpiWarps) {
+  if (warp < 15) {
     int taken = 0;
     bool odd = false;
-    const int pieces = (kRows + BN) * 8;  // 16-byte pieces of a stage's plane: W's rows, then x's
+    Piece<T, kVec> piece[kPieces];  // of the rows of W, then x, 8 pieces each
+    // rows past the last one are read as the last one: what comes of them is not stored
+    const T* src[kPieces];  // its boundary in the grid
+    uint32_t shifts = 0;    // 4 bits a piece: the elements between the boundary and the piece's first one
+    auto row_of = [&](int j) { return (tid + j * kCutters) >> 3; };
+#pragma unroll
+    for (int j = 0; j < kPieces; ++j) {
+      const int row = row_of(j);
+      const int64_t at = (row < kRows ? (int64_t)min(o0 + row, E.d_out - 1) : t0 + min(row - kRows, tokens - 1)) * d_in +
+                         ((tid + j * kCutters) & 7) * 8;
+      const uint32_t sh = kVec ? 0u : (uint32_t)(at & (Piece<T, kVec>::kGrid - 1));
+      shifts |= sh << (4 * j);
+      src[j] = (row < kRows ? W : x) + (at - sh);
+    }
+    // a block of which every piece can be read from its boundary without leaving the row
+    auto inside = [&](int kb) { return (kVec || P.grid) && (int64_t)kb * 64 + 56 + (kVec ? 8 : 16) <= d_in; };
+    auto left_of = [&](int j, int kb) { return d_in - kb * 64 - ((tid + j * kCutters) & 7) * 8; };
+    auto fetch = [&](int kb) {
+      if (inside(kb)) {
+#pragma unroll
+        for (int j = 0; j < kPieces; ++j)
+          if (row_of(j) < kRows + BN) piece[j].load_inside(src[j] + (int64_t)kb * 64, (int)(shifts >> (4 * j)) & 15);
+      } else {
+#pragma unroll
+        for (int j = 0; j < kPieces; ++j) {
+          const bool is_w = row_of(j) < kRows;
+          if (row_of(j) < kRows + BN)
+            piece[j].load(is_w ? W : x, (src[j] - (is_w ? W : x)) + ((shifts >> (4 * j)) & 15) + (int64_t)kb * 64,
+                          left_of(j, kb), is_w ? (int64_t)E.d_out * d_in : E.N * d_in, P.grid);
+        }
+      }
+    };
+    fetch(kb0);
     for (int kb = kb0; kb < kb1; ++kb) {
       const int i = kb - kb0, s = i % S, use = i / S;
       if (use > 0 && !__all_sync(0xffffffffu, mbar_wait_spin(&ctrl->empty[s], (uint32_t)(use - 1) & 1u, abort))) break;
       uint8_t* st = sm + (size_t)s * P.stage_bytes;
-      // four pieces a thread at a time: their loads are in flight together
-      for (int q0 = tid; q0 < pieces; q0 += 4 * kEpiWarps * 32) {
-        Piece<T> piece[4];
-        int left[4];
+      auto write = [&](bool whole) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int q = q0 + j * kEpiWarps * 32, row = q >> 3, k0 = kb * 64 + (q & 7) * 8;
-          const bool is_w = row < kRows;
-          const bool there = q < pieces && (is_w ? o0 + row < E.d_out : row - kRows < tokens);
-          left[j] = there ? d_in - k0 : 0;
-          if (is_w)
-            piece[j].load(W, (int64_t)(o0 + row) * d_in + k0, left[j], (int64_t)E.d_out * d_in, P.grid);
-          else
-            piece[j].load(x, (t0 + row - kRows) * d_in + k0, left[j], E.N * d_in, P.grid);
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int q = q0 + j * kEpiWarps * 32;
-          if (q >= pieces) continue;
+        for (int j = 0; j < kPieces; ++j) {
+          if (row_of(j) >= kRows + BN) continue;
           uint4 p[kPlanes];
-          odd |= piece[j].cut(left[j], p);
-          const uint32_t at = sw128_offset((uint32_t)(q >> 3), (uint32_t)(q & 7));
+          odd |= piece[j].cut(whole ? 8 : left_of(j, kb), p);
+          const uint32_t at = sw128_offset((uint32_t)row_of(j), (uint32_t)(tid + j * kCutters) & 7u);
 #pragma unroll
           for (int k = 0; k < kPlanes; ++k) *reinterpret_cast<uint4*>(st + k * P.plane + at) = p[k];
         }
-      }
+      };
+      if (inside(kb))
+        write(true);
+      else
+        write(false);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctrl->full[s]);
+      if (kb + 1 < kb1) fetch(kb + 1);
       // the last span's sums, with this one's first stages already filled
-      if (i >= kSpan && i % kSpan == 2 && have) have = sums.take(ctrl, taken++, tmem, BN, tokens);
+      if (warp < kEpiWarps && i >= kSpan && i % kSpan == 2 && have) have = sums.take(ctrl, taken++, tmem, BN, tokens);
     }
-    while (taken < spans && have) have = sums.take(ctrl, taken++, tmem, BN, tokens);
+    while (warp < kEpiWarps && taken < spans && have) have = sums.take(ctrl, taken++, tmem, BN, tokens);
     if (odd) ctrl->odd = 1;
-  } else if (warp == 9) {
+  } else {
     if (elect_one()) {
       const uint32_t idesc = idesc_bf16_f32(kRows, (uint32_t)BN, false, false);
       const uint32_t first = smem_u32(sm);
@@ -968,7 +1029,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     return v;
   });
-  if (warp == 9) {
+  if (warp == 15) {
     tc_fence_after();
     tmem_dealloc(tmem, P.tmem_cols);
   }
@@ -1118,7 +1179,7 @@ cudaError_t launch_skinny(const LinearArgs& a, cudaStream_t stream) {
   }
 }
 
-template <typename T>
+template <typename T, bool kVec>
 cudaError_t launch_any(const LinearArgs& a, cudaStream_t stream) {
   const Epi e = epilogue_of(a);
   AnyPlan p = {};
@@ -1126,8 +1187,11 @@ cudaError_t launch_any(const LinearArgs& a, cudaStream_t stream) {
   p.nkb = (int)(((int64_t)a.d_in + 63) / 64);
   p.o_tiles = (int32_t)(((int64_t)a.d_out + kRows - 1) / kRows);
   auto tiles_at = [&](int BN) { return p.o_tiles * ((a.N + BN - 1) / BN); };
-  p.BN = a.N <= 16 ? 16 : a.N <= 32 ? 32 : a.N <= 64 || tiles_at(128) < num_sms() ? 64 : 128;
+  const bool wide = (kVec || planes == 1) && a.N > 64 && tiles_at(128) >= num_sms();  // (unaligned fp32: too many registers)
+  p.BN = a.N <= 16 ? 16 : a.N <= 32 ? 32 : wide ? 128 : 64;
   const int64_t tiles = tiles_at(p.BN);
+  // (a power of two: 25 clusters of 6 do not fit the GPU's groups of SMs at once, 22.9 us against 19.7 with
+  // 25 of 4 at 257 x 1031 x 517)
   p.C = 1;
   while (p.C < 8 && tiles * p.C * 2 <= num_sms() && p.nkb >= p.C * 4) p.C *= 2;
   p.grid = aligned(a.x, 16) && aligned(a.W, 16);
@@ -1145,13 +1209,13 @@ cudaError_t launch_any(const LinearArgs& a, cudaStream_t stream) {
   auto go = [&](auto kernel, std::atomic<uint64_t>& allowed) {
     const cudaError_t set = allow_smem(kernel, allowed, kMaxSmem);
     if (set != cudaSuccess) return set;
-    return launch_kernel(kernel, dim3((unsigned)(tiles * p.C)), dim3(kThreads), p.smem, stream, p.C, e, p,
+    return launch_kernel(kernel, dim3((unsigned)(tiles * p.C)), dim3(kAnyThreads), p.smem, stream, p.C, e, p,
                          static_cast<const T*>(a.x), static_cast<const T*>(a.W), a.d_in, a.err_word);
   };
   static std::atomic<uint64_t> allowed[3];
-  if (p.BN <= 32) return go(linear_any_kernel<T, 1>, allowed[0]);
-  if (p.BN == 64) return go(linear_any_kernel<T, 2>, allowed[1]);
-  return go(linear_any_kernel<T, 4>, allowed[2]);
+  if (p.BN <= 32) return go(linear_any_kernel<T, kVec, 1>, allowed[0]);
+  if (p.BN == 64) return go(linear_any_kernel<T, kVec, 2>, allowed[1]);
+  return go(linear_any_kernel<T, kVec, 4>, allowed[2]);
 }
 
 }  // namespace
@@ -1175,9 +1239,10 @@ bool linear_takes_update(const LinearArgs& a, const void* B, int32_t KR) {
 
 cudaError_t launch_linear(const LinearArgs& a, cudaStream_t stream, const LinearUpdate* update) {
   if (!tma_rows(a)) {
-    if (a.dtype == MOLORA_BF16) return launch_any<__nv_bfloat16>(a, stream);
-    if (a.dtype == MOLORA_E4M3) return launch_any<__nv_fp8_e4m3>(a, stream);
-    return launch_any<float>(a, stream);
+    if (a.dtype == MOLORA_BF16) return launch_any<__nv_bfloat16, false>(a, stream);
+    if (a.dtype == MOLORA_E4M3) return launch_any<__nv_fp8_e4m3, false>(a, stream);
+    return a.d_in % 4 == 0 && aligned(a.x, 16) && aligned(a.W, 16) ? launch_any<float, true>(a, stream)
+                                                                    : launch_any<float, false>(a, stream);
   }
   if (!many_tokens(a)) return launch_skinny(a, stream);
   // K blocks of fp32 results that sum in registers (see linear_tc_kernel), which hold 96 columns a thread;
