@@ -549,7 +549,7 @@ MOLORA_API molora_status molora_linear(const void* x, molora_dtype dtype, const 
  * layer's other projections read it too.  y is overwritten: fp32 (y_bf16 = 0) or bf16 (y_bf16 = 1,
  * with molora_lora_apply_bf16y's roundings).  ids, w, k, counts, offsets, perm and ws, ws_bytes as for
  * molora_lora_apply; a query sizes the path this call prefers.
- * Given a workspace, and many tokens, bf16 W and K*r <= 512, the product takes the adapters' update
+ * Given a workspace, more than 256 tokens, bf16 dtype and K*r <= 512, the product takes the adapters' update
  * along as further K blocks: a shrink writes it to the workspace as two bf16
  * terms (relative error 2^-17), and y is written, and rounded, once.  Otherwise the results are
  * those of the three calls.

@@ -479,7 +479,8 @@ def layer(g, N, d_in, d_out, K, r, k, fp8):
     # the product takes the update along: K*r of one, part of one and several K blocks, widths of every tile
     (2600, 512, 2048, 4, 16, 2, False), (4000, 256, 1544, 2, 16, 1, False), (2300, 320, 2120, 3, 32, 2, False),
     (5000, 128, 1024, 8, 64, 3, False), (20000, 64, 160, 4, 32, 2, False),
-    (2305, 1088, 1920, 7, 64, 2, False), (2900, 64, 2048, 13, 32, 1, False)])
+    (2305, 1088, 1920, 7, 64, 2, False), (2900, 64, 2048, 13, 32, 1, False),
+    (2600, 512, 2048, 4, 16, 2, True), (300, 1088, 392, 3, 32, 2, True), (5000, 128, 1024, 8, 64, 3, True)])
 def test_adapted_layer(m, y_dtype, N, d_in, d_out, K, r, k, fp8):
     """Norm -> linear gate -> gate -> dispatch -> the adapted projection, as a layer runs them, against
     the formulas in 64 bits on what each call reads; and the one call against the three it chains."""
@@ -515,7 +516,7 @@ def test_adapted_layer(m, y_dtype, N, d_in, d_out, K, r, k, fp8):
     # the grouped apply adds a token's k > 1 slots in no fixed order; bf16 y takes it where fp32 y takes
     # the stacked pair
     path = m.molora_select_path(BF, N, d_in, d_out, K, r, k)
-    if not fp8 and N > 256 and -(-d_out // 128) * -(-N // 256) > 76:
+    if N > 256 and d_in % 64 == 0 and r >= 16 and K * r <= 512:
         # the product has taken the update along, whose shrink is held in two bf16 terms (2^-17)
         within(y, y2.double(), 4e-4 * rms if y_dtype == F32 else 2 * (k + 1) * 2.0 ** -8 * (mag + rms))
     elif k == 1 or path in ("scalar", "dense") or (path == "stacked" and y_dtype == F32):

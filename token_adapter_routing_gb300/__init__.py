@@ -893,7 +893,7 @@ def molora_norm_linear_lora_apply(x, norm_weight, eps, W, A, B, ids, y, scale, w
 
     def call(ws_ptr, ws_bytes):
         return lib.molora_norm_linear_lora_apply(*args, ws_ptr, ws_bytes, *tail)
-    if ws is None and y.dtype == torch.bfloat16 and (fp8 or N <= 256):
+    if ws is None and y.dtype == torch.bfloat16 and N <= 256:
         # no path needs a workspace (they are for fp32 y, or for many tokens' update), so none is asked for
         _check("molora_norm_linear_lora_apply", call(None, None))
     else:

@@ -452,10 +452,10 @@ molora_status molora_norm_linear_lora_apply(const void* x, molora_dtype dtype, i
     if (st != MOLORA_OK || N == 0) return st;
     if (ws && (reinterpret_cast<uintptr_t>(ws) & 255u)) return MOLORA_ERR_INVALID_ARG;
   }
-  // The product takes the adapters' update along (y is then written once) where it runs on CTA pairs
-  // and the update's two planes fit the workspace: K*r/32 more K blocks of 64 against a pass over y.
+  // With more than 256 tokens the product takes the adapters' update along (y is then written, and
+  // rounded, once), if its two planes fit the workspace: K*r/32 more K blocks of 64 against a pass over y.
   const size_t plane = lora_update_bytes(N, K * r), stacked = stacked_workspace_bytes(N, K, r);
-  const bool update = N > 0 && !fp8 && ws_bytes && K * r <= 512 && linear_takes_update(lin, B, K * r) &&
+  const bool update = N > 0 && ws_bytes && K * r <= 512 && linear_takes_update(lin, B, K * r) &&
                       lora_update_supported(dtype, N, d_in, K, r);
   if (query) {
     *ws_bytes = update ? 2 * plane : 0;

@@ -231,7 +231,8 @@ __device__ __forceinline__ void split_epilogue(const Epi& E, const TileSums<J>& 
 // kPromote: a tensor core cuts what its sums lose in an addition, always towards zero, so a long chain of
 // MMAs drifts: 256 of them (d_in = 4096) leave an fp32 result 4e-6 short, 40 times what rounding
 // would.  For fp32 y the epilogue warps take the sums of every 8 K blocks (32 MMAs) into registers
-// and add there.
+// and add there.  With e4m3 operands it takes the adapters' update along: the product's sums are
+// scaled in registers before the update's, which have no scales, are added.
 template <bool kFp8, bool kPromote>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_tc_kernel(const Epi E, const TcPlan P, int32_t* err_word, const __grid_constant__ CUtensorMap map_x,
@@ -243,9 +244,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   LCtrl* ctrl = reinterpret_cast<LCtrl*>(sm + P.off_ctrl);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int BN = P.BN, S = P.S, nkb = P.nkb;
-  // the adapters' update is more K blocks of the same accumulators: (G_hi, B), (G_lo, B) in turn
-  const int all = kFp8 ? nkb : nkb + 2 * P.nkg;
-  const int span = kPromote ? kSpan : all;  // K blocks summed in TMEM at a time
+  // the adapters' update is more K blocks: (G_hi, B), (G_lo, B) in turn
+  const int all = nkb + 2 * P.nkg;
+  // the end of the K blocks from `first` on that are summed in TMEM together
+  auto span_end = [&](int first) {
+    if (!kPromote) return all;
+    if (kFp8) return first < nkb ? nkb : all;
+    return min(first + kSpan, all);
+  };
   const uint32_t rank = cluster_ctarank();
   const uint16_t both = 0x3;
   const int64_t pair = blockIdx.x / 2, pairs = gridDim.x / 2;
@@ -311,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (rank == 0) mbar_arrive_expect_tx(&ctrl->full[s], 2 * P.stage_bytes);
           uint8_t* st = sm + (size_t)s * P.stage_bytes;
           const int32_t n = n0 + (int32_t)rank * (BN / 2);
-          if (kFp8 || kb < nkb) {
+          if (kb < nkb) {
             tma_load_2d_pair(smem_u32(st), &map_x, kb * elems, m0, bar);
             tma_load_2d_pair(smem_u32(st + P.off_b), &map_w, kb * elems, n, bar);
           } else {
@@ -349,8 +355,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t phase = 0;
       bool ok = true;
       for (int64_t pt = pair; pt < P.tiles && ok; pt += pairs) {
-        for (int first = 0; first < all && ok; first += span, ++tc) {
-          const int buf = tc & 1, last = min(first + span, all);
+        for (int first = 0, last; first < all && ok; first = last, ++tc) {
+          const int buf = tc & 1;
+          last = span_end(first);
           if (tc >= 2 && !mbar_wait_spin(&ctrl->tempty[buf], (uint32_t)((tc >> 1) - 1) & 1u, abort)) {
             ok = false;
             break;
@@ -364,8 +371,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tc_fence_after();
             const uint32_t at = (uint32_t)s * (P.stage_bytes >> 4);
-            if (!kFp8 && kb >= nkb)  // B's columns are MN-major
-              umma_stage<true, kFp8>(d, a_lo + at, g_lo + at, desc_hi, g_hi, idesc | (1u << 16), kb != first, 32);
+            if (kb >= nkb)  // B's columns are MN-major
+              umma_stage<true, false>(d, a_lo + at, g_lo + at, desc_hi, g_hi, idesc_bf16_f32(2 * kRows, (uint32_t)BN, false, true),
+                                      kb != first, 32);
             else
               umma_stage<true, kFp8>(d, a_lo + at, b_lo + at, desc_hi, desc_hi, idesc, kb != first);
             umma_commit_pair(&ctrl->empty[s], both);
@@ -410,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // a chunk of 32 columns from its sums to y
       auto finish = [&](int c, float (&v)[32], const Residual& res, bool add) {
         const int col = n0 + c * 32;
-        if (E.sx) {
+        if (E.sx && !kPromote) {
 #pragma unroll
           for (int i = 0; i < 32; ++i)
             v[i] = fmaf(v[i], sx * __shfl_sync(0xffffffffu, cs[0], i), __shfl_sync(0xffffffffu, cb[0], i));
@@ -486,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       if constexpr (kPromote) {
         float acc[3][32];
-        for (int first = 0; first < all; first += span) {
+        for (int first = 0; first < all; first = span_end(first)) {
           const uint32_t base = wait_sums();
           if (!ok) break;
 #pragma unroll
@@ -495,8 +503,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t r[32];
             tmem_ld32_start(base + (uint32_t)((side + 2 * q) * 32), r);
             tmem_ld_wait(r);
+            if (first) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) acc[q][i] = first ? acc[q][i] + __uint_as_float(r[i]) : __uint_as_float(r[i]);
+              for (int i = 0; i < 32; ++i) acc[q][i] += __uint_as_float(r[i]);
+            } else if (kFp8) {  // the scales belong to the product, not to the update
+#pragma unroll
+              for (int i = 0; i < 32; ++i) acc[q][i] = __uint_as_float(r[i]) * (sx * __shfl_sync(0xffffffffu, cs[q], i));
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) acc[q][i] = __uint_as_float(r[i]);
+            }
           }
           free_sums();
         }
@@ -1120,9 +1136,10 @@ cudaError_t launch_tc(const LinearArgs& a, int BN, bool promote, const LinearUpd
       !linear_map(&my, a.y_bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, a.y_bf16 ? 2 : 4,
                   a.y, (uint64_t)a.N, (uint64_t)a.d_out, a.y_bf16 ? 32 : 16, 32, CU_TENSOR_MAP_SWIZZLE_64B))
     e.tma_y = false;
-  auto kernel = fp8 ? linear_tc_kernel<true, false> : promote ? linear_tc_kernel<false, true> : linear_tc_kernel<false, false>;
-  static std::atomic<uint64_t> allowed[3];
-  const cudaError_t set = allow_smem(kernel, allowed[fp8 ? 2 : promote], kMaxSmem);
+  auto kernel = fp8 ? (promote ? linear_tc_kernel<true, true> : linear_tc_kernel<true, false>)
+                    : (promote ? linear_tc_kernel<false, true> : linear_tc_kernel<false, false>);
+  static std::atomic<uint64_t> allowed[4];
+  const cudaError_t set = allow_smem(kernel, allowed[2 * fp8 + promote], kMaxSmem);
   if (set != cudaSuccess) return set;
   const int64_t most = num_sms() / 2;
   const dim3 grid((unsigned)(2 * (p.tiles < most ? p.tiles : most)));
@@ -1234,7 +1251,7 @@ static bool many_tokens(const LinearArgs& a) {
 }
 
 bool linear_takes_update(const LinearArgs& a, const void* B, int32_t KR) {
-  return a.dtype == MOLORA_BF16 && tma_rows(a) && many_tokens(a) && a.d_out % 8 == 0 && KR % 8 == 0 && aligned(B, 16);
+  return tma_rows(a) && a.N > 256 && a.d_out % 8 == 0 && KR % 8 == 0 && aligned(B, 16);
 }
 
 cudaError_t launch_linear(const LinearArgs& a, cudaStream_t stream, const LinearUpdate* update) {
@@ -1244,11 +1261,11 @@ cudaError_t launch_linear(const LinearArgs& a, cudaStream_t stream, const Linear
     return a.d_in % 4 == 0 && aligned(a.x, 16) && aligned(a.W, 16) ? launch_any<float, true>(a, stream)
                                                                     : launch_any<float, false>(a, stream);
   }
-  if (!many_tokens(a)) return launch_skinny(a, stream);
+  if (!update && !many_tokens(a)) return launch_skinny(a, stream);
   // K blocks of fp32 results that sum in registers (see linear_tc_kernel), which hold 96 columns a thread;
   // e4m3 sums are half as many and drift a tenth as far (2e-7 at d_in = 4096)
   const int64_t blocks = ((int64_t)a.d_in + 63) / 64 + (update ? (update->KR + 63) / 64 * 2 : 0);
-  const bool promote = a.dtype == MOLORA_BF16 && !a.y_bf16 && blocks > kSpan;
+  const bool promote = a.dtype == MOLORA_E4M3 ? update != nullptr : !a.y_bf16 && blocks > kSpan;
   // the width whose waves of tiles cost least
   const int64_t pairs = num_sms() / 2, m_tiles = (a.N + 2 * kRows - 1) / (2 * kRows);
   int best = 128;
