@@ -666,11 +666,13 @@ _TYPE_CODES = {torch.float32: F32, torch.bfloat16: BF16, torch.float8_e4m3fn: E4
 
 
 def _array(t: Optional[torch.Tensor], name: str, shape, dtype, device):
-    """The device pointer of a tensor argument of this shape, dtype and device (None for None).  That
-    `device` is a GPU is checked by _on_gpu, last, so that a mis-sized argument is reported as such."""
+    """The device pointer of a tensor argument of this shape, dtype and device index (None for None).
+    That the device is a GPU is checked by _on_gpu, last, so that a mis-sized argument is reported as
+    such.  (One quick test first: a call has up to 18 of these.)"""
     if t is None:
         return None
-    if type(t) in _TENSORS and t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+    if (type(t) in _TENSORS and t.dtype is dtype and t.shape == shape and t.get_device() == device and
+            t.is_contiguous()):
         return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name} must be a tensor")
@@ -680,8 +682,9 @@ def _array(t: Optional[torch.Tensor], name: str, shape, dtype, device):
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device} (all tensors of a call share one device)")
+    if t.get_device() != device:
+        where = "the CPU" if device < 0 else f"cuda:{device}"
+        raise ValueError(f"{name} is on {t.device}, expected {where} (all tensors of a call share one device)")
     return t.data_ptr()
 
 
@@ -689,9 +692,9 @@ _TENSORS = (torch.Tensor, torch.nn.Parameter)
 
 
 def _call(name: str, device, *args):
-    """Calls the library with `device` current and raises on a status that is not OK."""
+    """Calls the library with the device of that index current and raises on a status that is not OK."""
     fn = getattr(load_library(), name)
-    if device.index == torch.cuda.current_device():
+    if device == torch._C._cuda_getDevice():
         status = fn(*args)
     else:
         with torch.cuda.device(device):
@@ -722,6 +725,10 @@ def _named(value: str, name: str, table) -> int:
     return table[value]
 
 
+def _error_word(err_word, device):
+    return None if err_word is None else _err_word(err_word, torch.device("cuda", device)).data_ptr()
+
+
 _FLOATS = (torch.bfloat16, torch.float32)
 
 
@@ -729,8 +736,8 @@ def _raw_stream(stream, device) -> int:
     """The handle of the given stream, else of the device's current one (torch's own accessor for
     compiled callers: the public one makes a Stream object, 2 us of a 6 us call)."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device.index)
-    return _stream(stream, device).value or 0
+        return torch._C._cuda_getCurrentRawStream(device)
+    return _stream(stream, torch.device("cuda", device)).value or 0
 
 
 def molora_rmsnorm(x, weight, eps=1e-6, residual=None, sum_out=None, out=None, out8=None, scale8=None, stream=None):
@@ -740,7 +747,7 @@ def molora_rmsnorm(x, weight, eps=1e-6, residual=None, sum_out=None, out=None, o
     sum_out and out may each be x or residual."""
     code = _matrix(x, "x", _FLOATS)
     N, d = x.shape
-    dev, dt, shape = x.device, x.dtype, x.shape
+    dev, dt, shape = x.get_device(), x.dtype, x.shape
     px = _array(x, "x", shape, dt, dev)
     pg = _array(weight, "weight", (d,), dt, dev)
     pr = _array(residual, "residual", shape, dt, dev)
@@ -774,7 +781,7 @@ def molora_gate_topk(logits, k, score="softmax", bias=None, groups=1, keep_group
     weights.  A token with fewer than k experts left has id -1 and weight 0 in its last slots."""
     code = _matrix(logits, "logits", _FLOATS)
     N, K = logits.shape
-    dev = logits.device
+    dev = logits.get_device()
     score = _named(score, "score", SCORES)
     if K > MAX_EXPERTS:
         raise ValueError(f"at most {MAX_EXPERTS} experts, got {K}")
@@ -789,20 +796,20 @@ def molora_gate_topk(logits, k, score="softmax", bias=None, groups=1, keep_group
     pl = _array(logits, "logits", logits.shape, logits.dtype, dev)
     pb = _array(bias, "bias", (K,), torch.float32, dev)
     if ids is None:
-        ids = torch.empty(N, k, dtype=torch.int32, device=dev)
+        ids = logits.new_empty((N, k), dtype=torch.int32)
     if w is None:
-        w = torch.empty(N, k, dtype=torch.float32, device=dev)
+        w = logits.new_empty((N, k), dtype=torch.float32)
     pi, pw = _array(ids, "ids", (N, k), torch.int32, dev), _array(w, "w", (N, k), torch.float32, dev)
     _on_gpu(logits, "logits")
     _call(
         "molora_gate_topk", dev, pl, code, N, K, score, pb, groups, keep_groups, group_top, k, 1 if renormalise else 0, scale, pi, pw,
-        _p(_err_word(err_word, dev)), _raw_stream(stream, dev))
+        _error_word(err_word, dev), _raw_stream(stream, dev))
     return ids, w
 
 
-def _y(y, N, d_out, dtype, device):
+def _y(y, N, d_out, dtype, like):
     if y is None:
-        return torch.empty(N, d_out, dtype=dtype, device=device)
+        return like.new_empty((N, d_out), dtype=dtype)
     if not isinstance(y, torch.Tensor) or y.dtype not in _FLOATS:
         raise ValueError("y must be a float32 or bfloat16 tensor")
     return y
@@ -815,7 +822,7 @@ def molora_linear(x, W, y=None, x_scale=None, w_scale=None, bias=None, act="none
     (float32 or bfloat16, residual's dtype; residual itself is allowed), else made in ``out_dtype``."""
     code = _matrix(x, "x", (torch.bfloat16, torch.float32, torch.float8_e4m3fn))
     N, d_in = x.shape
-    dev = x.device
+    dev = x.get_device()
     if not isinstance(W, torch.Tensor) or W.dim() != 2 or W.shape[0] < 1:
         raise ValueError("W must be a 2-D tensor [d_out, d_in]")
     d_out = W.shape[0]
@@ -828,13 +835,13 @@ def molora_linear(x, W, y=None, x_scale=None, w_scale=None, bias=None, act="none
     psx = _array(x_scale, "x_scale", (N,), torch.float32, dev)
     psw = _array(w_scale, "w_scale", (d_out,), torch.float32, dev)
     pb = _array(bias, "bias", (d_out,), torch.float32, dev)
-    y = _y(y, N, d_out, out_dtype, dev)
+    y = _y(y, N, d_out, out_dtype, x)
     pres = _array(residual, "residual", (N, d_out), y.dtype, dev)
     py = _array(y, "y", (N, d_out), y.dtype, dev)
     _on_gpu(x, "x")
     _call(
         "molora_linear", dev, px, code, psx, N, d_in, pw, psw, d_out, pb, act, pres, py, 1 if y.dtype == torch.bfloat16 else 0,
-        _p(_err_word(err_word, dev)), _raw_stream(stream, dev))
+        _error_word(err_word, dev), _raw_stream(stream, dev))
     return y
 
 
@@ -848,7 +855,7 @@ def molora_norm_linear_lora_apply(x, norm_weight, eps, W, A, B, ids, y, scale, w
     buffers that are not given are made."""
     code = _matrix(x, "x", _FLOATS)
     N, d_in = x.shape
-    dev, dt, f32, i32 = x.device, x.dtype, torch.float32, torch.int32
+    dev, dt, f32, i32 = x.get_device(), x.dtype, torch.float32, torch.int32
     if not isinstance(W, torch.Tensor) or W.dim() != 2 or W.shape[0] < 1 or W.dtype not in (dt, torch.float8_e4m3fn):
         raise ValueError("W must be [d_out, d_in] of x's dtype or float8_e4m3fn")
     d_out = W.shape[0]
@@ -873,9 +880,9 @@ def molora_norm_linear_lora_apply(x, norm_weight, eps, W, A, B, ids, y, scale, w
     if h is None:
         h = torch.empty_like(x)
     if fp8 and h8 is None:
-        h8 = torch.empty(N, d_in, dtype=torch.float8_e4m3fn, device=dev)
+        h8 = x.new_empty((N, d_in), dtype=torch.float8_e4m3fn)
     if fp8 and scale8 is None:
-        scale8 = torch.empty(N, dtype=f32, device=dev)
+        scale8 = x.new_empty((N,), dtype=f32)
     if sum_out is not None and N and h.data_ptr() == sum_out.data_ptr():
         raise ValueError("h and sum_out must be different tensors")
     args = (px, code, N, d_in, _array(residual, "residual", x.shape, dt, dev), _array(sum_out, "sum_out", x.shape, dt, dev),
@@ -888,16 +895,16 @@ def molora_norm_linear_lora_apply(x, norm_weight, eps, W, A, B, ids, y, scale, w
             _array(offsets, "offsets", (K + 1,), i32, dev), _array(perm, "perm", (N * k,), i32, dev), scale,
             _array(y, "y", (N, d_out), y.dtype, dev), 1 if y.dtype == torch.bfloat16 else 0)
     _on_gpu(x, "x")
-    tail = (_p(_err_word(err_word, dev)), _raw_stream(stream, dev))
+    tail = (_error_word(err_word, dev), _raw_stream(stream, dev))
     lib = load_library()
 
     def call(ws_ptr, ws_bytes):
         return lib.molora_norm_linear_lora_apply(*args, ws_ptr, ws_bytes, *tail)
-    if ws is None and y.dtype == torch.bfloat16 and N <= 256:
+    if ws is not None or y.dtype != torch.bfloat16 or N > 256:
+        _check("molora_norm_linear_lora_apply", _workspace(ws, x.device, call))
+    else:
         # no path needs a workspace (they are for fp32 y, or for many tokens' update), so none is asked for
         _check("molora_norm_linear_lora_apply", call(None, None))
-    else:
-        _check("molora_norm_linear_lora_apply", _workspace(ws, dev, call))
     return y, sum_out, h, h8, scale8
 
 

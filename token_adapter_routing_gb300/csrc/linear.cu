@@ -1170,9 +1170,9 @@ cudaError_t launch_skinny(const LinearArgs& a, cudaStream_t stream) {
   if (ring < partial) ring = partial;
   p.off_ctrl = (uint32_t)ring;
   p.smem = (uint32_t)(ring + sizeof(LCtrl) + kSmemSlack);
-  // a cluster's CTAs wait for one another: none may share an SM with a CTA that takes all of TMEM
-  // (those take 116 KB or more)
-  if (p.C > 1 && p.smem < 116 * 1024) p.smem = 116 * 1024;
+  // 116 KB at least: neither this CTA nor one that takes all of TMEM (those take as much) can then hold
+  // columns that the other waits for while it is itself waited for, by its cluster or by the next kernel
+  if (p.smem < 116 * 1024) p.smem = 116 * 1024;
   CUtensorMap mx, mw;
   if (!operand_map(&mx, a, a.x, a.N, (uint32_t)p.BN) || !operand_map(&mw, a, a.W, a.d_out, kRows))
     return cudaErrorNotSupported;
@@ -1222,7 +1222,7 @@ cudaError_t launch_any(const LinearArgs& a, cudaStream_t stream) {
   if (ring < partial) ring = partial;
   p.off_ctrl = (uint32_t)ring;
   p.smem = (uint32_t)(ring + fixed);
-  if (p.C > 1 && p.smem < 116 * 1024) p.smem = 116 * 1024;  // see launch_skinny
+  if (p.smem < 116 * 1024) p.smem = 116 * 1024;  // see launch_skinny
   auto go = [&](auto kernel, std::atomic<uint64_t>& allowed) {
     const cudaError_t set = allow_smem(kernel, allowed, kMaxSmem);
     if (set != cudaSuccess) return set;

@@ -261,9 +261,9 @@ cudaError_t launch_lora_update(const void* h, int64_t N, int32_t d_in, const voi
   if (ring < partial) ring = partial;
   p.off_ctrl = (uint32_t)ring;
   p.smem = (uint32_t)(ring + sizeof(UCtrl) + kSlack);
-  // a cluster's CTAs wait for one another: none may share an SM with a CTA that takes all of TMEM
-  // (those take 116 KB or more)
-  if (p.C > 1 && p.smem < 116 * 1024) p.smem = 116 * 1024;
+  // 116 KB at least: neither this CTA nor one that takes all of TMEM (those take as much) can then hold
+  // columns that the other waits for while it is itself waited for, by its cluster or by the next kernel
+  if (p.smem < 116 * 1024) p.smem = 116 * 1024;
   CUtensorMap map_h, map_a;
   const CUtensorMapSwizzle swz = r == 16   ? CU_TENSOR_MAP_SWIZZLE_32B
                                  : r == 32 ? CU_TENSOR_MAP_SWIZZLE_64B
