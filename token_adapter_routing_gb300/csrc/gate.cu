@@ -4,6 +4,10 @@
 // A token belongs to TL lanes of a warp; lane l of them holds experts l, l + TL, l + 2 TL, ...: every
 // load is of consecutive logits, whatever K and the rows' alignment.
 //
+// Bound by instructions, not bytes: 16384 x 256 fp32 in 8 groups takes 19.3 us (its 17.8 MB would take 2.6),
+// issuing in 75% of the cycles, about 1100 warp instructions a token, of which 230 are the sigmoids and
+// 310 the groups; 40961 x 60 bf16 with a bias 16.4 us.  32 x 64 takes 1.6 us, a launch.
+//
 // Everything the choice depends on is reproducible: e = expf(l - max) and 1 / (1 + expf(-l)) are
 // single fp32 operations, and the softmax's denominator is a sum of integers (to 2^-44 of the largest e)
 // that is rounded once, so it does not depend on the order of the sum.
@@ -231,7 +235,8 @@ __device__ __forceinline__ void gate_rounds_warp(const GateArgs& a, const float 
 }  // namespace
 
 // Up to 16 experts in one group: TL lanes a token, so that a warp's every instruction works for
-// 32 / TL tokens and a maximum over the lanes takes log2(TL) steps.
+// 32 / TL tokens and a maximum over the lanes takes log2(TL) steps.  (With 64 experts, 8 a lane, this
+// took 18 us where a warp a token takes 16, and twice as long for a few tokens.)
 template <typename T, int TL, int V>
 __global__ void __launch_bounds__(kGateWarps * 32, 4) gate_small_kernel(const T* __restrict__ logits, const GateArgs a) {
   constexpr int kTokens = 32 / TL;  // of a warp
@@ -255,7 +260,8 @@ __global__ void __launch_bounds__(kGateWarps * 32, 4) gate_small_kernel(const T*
 
 // More experts, or groups: a warp a token, 32 V experts at most.  With up to four a lane the choice is made
 // in rounds; with more, the k-th largest of the 32 lanes' own maxima is a bound that the k largest choices
-// reach and few others do, and those that do (k and a few) are ranked by counting, in shared memory.
+// reach and few others do, and those that do (k and a few) are ranked by counting, in shared memory
+// (16384 x 256, top 8 by logits: 10.5 us, 14.0 in rounds; 512 experts 31.4 against 37.7).
 template <typename T, int V>
 __global__ void __launch_bounds__(kGateWarps * 32, V <= 8 ? 4 : 2) gate_topk_kernel(const T* __restrict__ logits, const GateArgs a) {
   extern __shared__ float choices[];  // [warps][K], with groups

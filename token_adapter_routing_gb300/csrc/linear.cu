@@ -11,10 +11,14 @@
 //   by a pair of CTAs with cta_group::2 MMAs.  Each CTA loads its 128 token rows and half of the
 //   tile's W rows: a pair reads every operand byte once from shared memory per MMA, which
 //   one CTA alone cannot feed at full rate.  A TMA warp and an MMA warp run ahead of 8 epilogue
-//   warps by two TMEM accumulators.
+//   warps by two TMEM accumulators.  Bound by the tensor cores: 8192 x 4096 x 4096 bf16 141 us (1950
+//   TFLOP/s; tensor pipe active in 89% of the cycles), 150 with bias, SiLU and residual; e4m3 76 us
+//   (3600).  4096 x 2048 x 6144 e4m3 with scales, bias and GELU 42 us, 36 without: there the epilogue of
+//   224 columns is nearly as long as a tile's 16 K blocks.
 // linear_skinny_kernel (few tokens): W's rows are the MMA's M (128 outputs a CTA), the tokens its N
 //   (16 .. 256), so that no MMA row is spent on tokens that are not there; d_in is split over a
-//   cluster of CTAs whose partial sums meet through distributed shared memory in rank order.
+//   cluster of CTAs whose partial sums meet through distributed shared memory in rank order.  Bound by
+//   reading W, and the way through the kernel: one token, 4096 x 4096 bf16, 7.2 us (W's bytes: 5.0).
 // linear_any_kernel (fp32, and rows that start anywhere): the same split, with the operands fetched and
 //   laid out by the CTA's threads.
 #include <cudaTypedefs.h>

@@ -9,7 +9,8 @@
 // of the K*r columns belongs to a cluster of C CTAs that split d_in, so each reads its own columns of h
 // and rows of A and nothing twice; their partial sums meet through distributed shared memory in rank
 // order.  (Splitting the columns instead, as stacked_shrink_kernel does to exchange a router's hidden
-// units, reads h C times: 20 us against 5 at 4096 x 2048 with 4 adapters of rank 16.)
+// units, reads h C times: the whole projection of 4096 x 2048 -> 6144 with 4 adapters of rank 16 took 96 us
+// with it and takes 87 with this.)  What is left is the way through: 8 K blocks a CTA, then the join.
 #include <cudaTypedefs.h>
 
 #include <atomic>
