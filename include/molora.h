@@ -15,7 +15,8 @@
  *     against N for per-token routing).
  *
  * Workspace (ws, ws_bytes), for the calls that take it (Table 1's shared dispatch
- * infrastructure needs none; only MOLORA_PATH_STACKED does):
+ * infrastructure needs none; only MOLORA_PATH_STACKED and molora_norm_linear_lora_apply with more than
+ * 256 tokens do):
  *   - ws_bytes == NULL: no workspace.  AUTO chooses among the paths that need none, and an
  *     explicit MOLORA_PATH_STACKED returns MOLORA_ERR_INVALID_ARG.
  *   - ws == NULL, ws_bytes != NULL: a query.  *ws_bytes is set to the bytes the call would
@@ -528,7 +529,9 @@ MOLORA_API molora_status molora_gate_topk(const void* logits, molora_dtype dtype
  * needed with MOLORA_E4M3 (x, x_scale as molora_rmsnorm's out8, scale8), both NULL otherwise.
  * bias fp32 [d_out] or NULL;  residual [N x d_out] of y's type or NULL, y itself allowed;
  * y fp32 (y_bf16 = 0) or bf16 (y_bf16 = 1) [N x d_out], overwritten.
- * Products are summed in fp32; the epilogue is fp32 and y is rounded once.  Any d_in, d_out >= 1.
+ * Products are summed in fp32; the epilogue is fp32 and y is rounded once.  Any d_in, d_out >= 1; arrays
+ * start on a boundary of their element's size (rows on 16-byte boundaries are faster).  Results are
+ * reproducible bit for bit.  A wait that ran out (MOLORA_DEV_WAIT_TIMEOUT) leaves its tile of y unwritten.
  */
 MOLORA_API molora_status molora_linear(const void* x, molora_dtype dtype, const float* x_scale, int64_t N, int32_t d_in,
                             const void* W, const float* w_scale, int32_t d_out, const float* bias,
@@ -551,8 +554,9 @@ MOLORA_API molora_status molora_linear(const void* x, molora_dtype dtype, const 
  * molora_lora_apply; a query sizes the path this call prefers.
  * Given a workspace, more than 256 tokens, bf16 dtype and K*r <= 512, the product takes the adapters' update
  * along as further K blocks: a shrink writes it to the workspace as two bf16
- * terms (relative error 2^-17), and y is written, and rounded, once.  Otherwise the results are
- * those of the three calls.
+ * terms (relative error 2^-17), and y is written, and rounded, once.  It evaluates all K adapters, those
+ * that a token did not choose with weight 0, as the dense and stacked paths do: the whole hot set has to
+ * be finite.  Otherwise the results are those of the three calls.
  */
 MOLORA_API molora_status molora_norm_linear_lora_apply(
     const void* x, molora_dtype dtype, int64_t N, int32_t d_in, const void* residual, void* sum_out,

@@ -112,9 +112,10 @@ def test_norm(m, dtype, N, d, residual, fp8):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
-def test_norm_unaligned_and_in_place(m, dtype):
+@pytest.mark.parametrize("N", [37, 2500])
+def test_norm_unaligned_and_in_place(m, dtype, N):
     g = gen(3)
-    x, res, w = randn(g, 37, 512).to(dtype), randn(g, 37, 512).to(dtype), randn(g, 512).to(dtype)
+    x, res, w = randn(g, N, 512).to(dtype), randn(g, N, 512).to(dtype), randn(g, 512).to(dtype)
     _, want, _, _ = m.molora_rmsnorm(x, w, 1e-6, residual=res)
     xo, ro = off_by_one(x), off_by_one(res)
     got_sum, got, _, _ = m.molora_rmsnorm(xo, off_by_one(w), 1e-6, residual=ro, sum_out=ro, out=xo)
@@ -525,10 +526,11 @@ def test_adapted_layer(m, y_dtype, N, d_in, d_out, K, r, k, fp8):
         within(y, y2.double(), 4e-4 * rms if y_dtype == F32 else 2 * (k + 1) * 2.0 ** -8 * (mag + rms))
 
 
-def test_layer_captured_and_replayed(m):
+@pytest.mark.parametrize("N", [48, 400])
+def test_layer_captured_and_replayed(m, N):
     """The chain in a CUDA graph, replayed on new inputs, equals the eager calls; two graphs alive
     at once do not disturb one another."""
-    N, d, K, r, k = 48, 512, 8, 16, 2
+    d, K, r, k = 512, 8, 16, 2
     graphs = []
     for seed, fp8 in ((21, True), (22, False)):
         tensors = layer(gen(seed), N, d, d, K, r, k, fp8)
@@ -559,6 +561,45 @@ def test_layer_captured_and_replayed(m):
             want = step()
             for a, b in zip(out, want):
                 assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("N", [5, 300])
+def test_fp32_layer(m, N, fp8):
+    """Hidden states and adapters in fp32, base weights in fp32 or e4m3."""
+    g = gen(41 + N)
+    d_in, d_out, K, r, k = 192, 160, 3, 8, 2
+    x, nw, A, B = randn(g, N, d_in), 1 + 0.1 * randn(g, d_in), randn(g, K, d_in, r) / math.sqrt(d_in), randn(g, K, r, d_out)
+    W, sw = randn(g, d_out, d_in) / math.sqrt(d_in), None
+    if fp8:
+        W, sw = quantised(W)
+    ids, w = m.molora_gate_topk(randn(g, N, K), k)
+    buf = torch.full((N + 2, d_out), 7.0, device="cuda")
+    y, s, h, h8, scale8 = m.molora_norm_linear_lora_apply(x, nw, 1e-6, W, A, B, ids, buf[:N], 2.0, w=w, w_scale=sw)
+    assert s is None and (buf[N:] == 7).all() and (h8 is not None) == fp8
+    check_norm(x, None, nw, 1e-6, None, h, h8, scale8)
+    base = (h8.double() * scale8.double()[:, None]) @ (W.double() * sw.double()[:, None]).T if fp8 else h.double() @ W.double().T
+    for a in range(K):
+        base += 2.0 * (w.double() * (ids == a)).sum(1, keepdim=True) * ((h.double() @ A[a].double()) @ B[a].double())
+    within(y, base, 2e-4 * base.pow(2).mean().sqrt().item())
+
+
+@pytest.mark.parametrize("N", [20, 300])
+def test_layer_skips_slots_without_an_adapter(m, N):
+    """Slots of -1 (a token whose experts ran out) are skipped and reported; the others are applied."""
+    g = gen(51)
+    x, _, nw, W, _, A, B, _, _ = layer(g, N, 256, 192, 4, 16, 2, False)
+    ids = torch.randint(0, 4, (N, 2), generator=g, device="cuda", dtype=torch.int32)
+    ids[:, 1] = torch.where(torch.arange(N, device="cuda") % 3 == 0, -1, (ids[:, 0] + 1) % 4)
+    w = torch.rand(N, 2, generator=g, device="cuda")
+    e = err_word()
+    y = torch.empty(N, 192, device="cuda")
+    _, _, h, _, _ = m.molora_norm_linear_lora_apply(x, nw, 1e-6, W, A, B, ids, y, 2.0, w=w, err_word=e)
+    assert e.item() == m.DEV_BAD_ADAPTER_ID
+    want = h.double() @ W.double().T
+    for a in range(4):
+        want += 2.0 * (w.double() * (ids == a)).sum(1, keepdim=True) * ((h.double() @ A[a].double()) @ B[a].double())
+    within(y, want, 2e-4 * want.pow(2).mean().sqrt().item())
 
 
 def test_two_streams_at_once(m):

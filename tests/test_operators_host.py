@@ -79,6 +79,8 @@ def test_gate_refuses(kwargs, match):
     (dict(bias=z(5, dtype=F32)), "bias must have shape"),
     (dict(bias=z(6)), "bias must be torch.float32"),
     (dict(y=z(4, 6, dtype=torch.float16)), "y must be"),
+    (dict(out_dtype=torch.float16), "out_dtype must be"),
+    (dict(out_dtype=torch.float64), "out_dtype must be"),
     (dict(y=z(4, 6), residual=z(4, 6, dtype=F32)), "residual must be torch.bfloat16"),
     (dict(y=z(4, 6), residual=z(3, 6)), "residual must have shape"),
     (dict(), "must be a CUDA tensor"),
@@ -128,18 +130,22 @@ def test_c_abi_refuses_without_launching():
     assert norm(p, 1, 4, 8, None, None, p, 1e-6, None, q, None, None) == INVALID      # out8 without scale8
     assert norm(p, 1, 4, 8, None, q, p, 1e-6, q, None, None, None) == INVALID         # sum_out without residual
     assert norm(p, 1, 4, 8, p, q, p, 1e-6, q, None, None, None) == INVALID            # sum_out and out the same
+    assert norm(p + 1, 1, 4, 8, None, None, p, 1e-6, q, None, None, None) == INVALID  # half an element
+    assert norm(p, 0, 4, 8, None, None, p, 1e-6, q + 2, None, None, None) == INVALID
     gate = lib.molora_gate_topk
     assert gate(None, 1, 0, 8, 0, None, 1, 1, 1, 2, 1, 1.0, None, None, None, None) == 0
     for bad in [dict(K=513), dict(K=0), dict(score=2), dict(groups=3), dict(groups=64, K=512), dict(keep=2),
                 dict(groups=4, keep=0), dict(top=3), dict(groups=8, top=2), dict(k=0), dict(k=9), dict(k=33, K=64),
-                dict(scale=float("nan")), dict(dtype=2), dict(logits=None), dict(ids=None)]:
+                dict(scale=float("nan")), dict(dtype=2), dict(logits=None), dict(ids=None), dict(logits=p + 1),
+                dict(ids=p + 2)]:
         a = dict(logits=p, dtype=1, N=4, K=8, score=0, groups=1, keep=1, top=1, k=2, scale=1.0, ids=p) | bad
         assert gate(a["logits"], a["dtype"], a["N"], a["K"], a["score"], None, a["groups"], a["keep"], a["top"], a["k"], 1,
                     a["scale"], a["ids"], p, None, None) == INVALID, bad
     linear = lib.molora_linear
     assert linear(None, 1, None, 0, 8, None, None, 8, None, 0, None, None, 0, None, None) == 0
     for bad in [dict(dtype=3), dict(N=-1), dict(d_in=0), dict(d_out=0), dict(act=5), dict(act=-1), dict(x=None),
-                dict(W=None), dict(y=None), dict(sx=p), dict(sw=p), dict(dtype=2), dict(dtype=2, sx=p)]:
+                dict(W=None), dict(y=None), dict(sx=p), dict(sw=p), dict(dtype=2), dict(dtype=2, sx=p), dict(x=p + 1),
+                dict(y=q + 2), dict(dtype=2, sx=p + 1, sw=p)]:
         a = dict(x=p, dtype=1, sx=None, N=4, d_in=8, W=p, sw=None, d_out=8, act=0, y=q) | bad
         assert linear(a["x"], a["dtype"], a["sx"], a["N"], a["d_in"], a["W"], a["sw"], a["d_out"], None, a["act"], None,
                       a["y"], 0, None, None) == INVALID, bad

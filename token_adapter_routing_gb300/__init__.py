@@ -809,6 +809,8 @@ def molora_gate_topk(logits, k, score="softmax", bias=None, groups=1, keep_group
 
 def _y(y, N, d_out, dtype, like):
     if y is None:
+        if dtype not in _FLOATS:
+            raise ValueError(f"out_dtype must be torch.float32 or torch.bfloat16, got {dtype}")
         return like.new_empty((N, d_out), dtype=dtype)
     if not isinstance(y, torch.Tensor) or y.dtype not in _FLOATS:
         raise ValueError("y must be a float32 or bfloat16 tensor")

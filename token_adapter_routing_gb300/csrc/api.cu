@@ -156,6 +156,10 @@ static molora_status apply_impl(const void* x, molora_dtype dtype, int64_t N, in
                                       y_bf16, -1, err_word, stream, table));
 }
 
+static size_t size_of(molora_dtype d) { return d == MOLORA_F32 ? 4 : d == MOLORA_BF16 ? 2 : 1; }
+// Whether a pointer (NULL included) starts on a boundary of its element's size: kernels read whole elements.
+static bool on_element(const void* p, size_t size) { return (reinterpret_cast<uintptr_t>(p) & (size - 1)) == 0; }
+
 // molora_linear's checks.  With N == 0 no pointer is looked at.
 static molora_status check_linear(const LinearArgs& a) {
   if (!(valid_dtype(a.dtype) || a.dtype == MOLORA_E4M3) || a.N < 0 || a.N > INT32_MAX || a.d_in < 1 || a.d_out < 1 ||
@@ -164,6 +168,10 @@ static molora_status check_linear(const LinearArgs& a) {
   if (a.N == 0) return MOLORA_OK;
   if (!a.x || !a.W || !a.y) return MOLORA_ERR_INVALID_ARG;
   if ((a.dtype == MOLORA_E4M3) != (a.x_scale != nullptr) || (a.dtype == MOLORA_E4M3) != (a.w_scale != nullptr))
+    return MOLORA_ERR_INVALID_ARG;
+  const size_t e = size_of(a.dtype), ye = a.y_bf16 ? 2 : 4;
+  if (!on_element(a.x, e) || !on_element(a.W, e) || !on_element(a.y, ye) || !on_element(a.residual, ye) ||
+      !on_element(a.bias, 4) || !on_element(a.x_scale, 4) || !on_element(a.w_scale, 4))
     return MOLORA_ERR_INVALID_ARG;
   return MOLORA_OK;
 }
@@ -182,6 +190,10 @@ static molora_status check_rmsnorm(const void* x, molora_dtype dtype, int64_t N,
   if (N == 0) return MOLORA_OK;
   if (!x || !weight || (!out && !out8) || (out8 != nullptr) != (scale8 != nullptr) || (sum_out && !residual) ||
       (sum_out && sum_out == out))
+    return MOLORA_ERR_INVALID_ARG;
+  const size_t e = size_of(dtype);
+  if (!on_element(x, e) || !on_element(residual, e) || !on_element(sum_out, e) || !on_element(weight, e) ||
+      !on_element(out, e) || !on_element(scale8, 4))
     return MOLORA_ERR_INVALID_ARG;
   return MOLORA_OK;
 }
@@ -416,7 +428,9 @@ molora_status molora_gate_topk(const void* logits, molora_dtype dtype, int64_t N
       !(scale >= -3.4e38f && scale <= 3.4e38f))
     return MOLORA_ERR_INVALID_ARG;
   if (N == 0) return MOLORA_OK;
-  if (!logits || !ids || !w) return MOLORA_ERR_INVALID_ARG;
+  if (!logits || !ids || !w || !on_element(logits, size_of(dtype)) || !on_element(bias, 4) || !on_element(ids, 4) ||
+      !on_element(w, 4))
+    return MOLORA_ERR_INVALID_ARG;
   return launched(launch_gate_topk(logits, dtype, N, K, score == MOLORA_SCORE_SIGMOID, bias, groups, keep_groups,
                                    group_top, k, renormalise != 0, scale, ids, w, err_word, stream));
 }
