@@ -847,7 +847,18 @@ def molora_linear(x, W, y=None, x_scale=None, w_scale=None, bias=None, act="none
     return y
 
 
-@_on_tensor_device
+def _on_device_of_x(fn):
+    """_on_tensor_device for a call whose first argument is a tensor that says where the others are."""
+    @functools.wraps(fn)
+    def call(x, *args, **kwargs):
+        if isinstance(x, torch.Tensor) and x.is_cuda and x.get_device() != torch._C._cuda_getDevice():
+            with torch.cuda.device(x.device):
+                return fn(x, *args, **kwargs)
+        return fn(x, *args, **kwargs)
+    return call
+
+
+@_on_device_of_x
 def molora_norm_linear_lora_apply(x, norm_weight, eps, W, A, B, ids, y, scale, w=None, counts=None, offsets=None,
                                   perm=None, residual=None, sum_out=None, h=None, h8=None, scale8=None, w_scale=None,
                                   bias=None, err_word=None, ws=None, stream=None):

@@ -174,14 +174,59 @@ struct TileSums {
   }
 };
 
+// Four consecutive outputs o .. o + 3 of a token as the epilogue reads and writes them: in one access
+// where `vec` (rows of 4-element pieces on 16-byte boundaries), else one by one, those past d_out left out.
+struct Quad {
+  float v[4];
+  __device__ __forceinline__ void load(const float* p, int o, int d_out, bool vec) {
+    if (vec) {
+      const float4 q = *reinterpret_cast<const float4*>(p + o);
+      v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = o + i < d_out ? p[o + i] : 0.f;
+    }
+  }
+  __device__ __forceinline__ void load(const __nv_bfloat16* p, int o, int d_out, bool vec) {
+    if (vec) {
+      const uint2 q = *reinterpret_cast<const uint2*>(p + o);
+      v[0] = __uint_as_float(q.x << 16), v[1] = __uint_as_float(q.x & 0xffff0000u);
+      v[2] = __uint_as_float(q.y << 16), v[3] = __uint_as_float(q.y & 0xffff0000u);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = o + i < d_out ? __bfloat162float(p[o + i]) : 0.f;
+    }
+  }
+  __device__ __forceinline__ void store(float* p, int o, int d_out, bool vec) const {
+    if (vec) {
+      *reinterpret_cast<float4*>(p + o) = make_float4(v[0], v[1], v[2], v[3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (o + i < d_out) p[o + i] = v[i];
+    }
+  }
+  __device__ __forceinline__ void store(__nv_bfloat16* p, int o, int d_out, bool vec) const {
+    if (vec) {
+      *reinterpret_cast<uint2*>(p + o) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (o + i < d_out) p[o + i] = __float2bfloat16_rn(v[i]);
+    }
+  }
+};
+
 // Ends such a tile, whose d_in was split over a cluster's C CTAs: each CTA's sums go to shared memory,
 // [token][output] in the stage ring (free: every load has landed and every MMA is done); each CTA then adds
 // its share of the elements in rank order, reading the others' through distributed shared memory, and
-// writes it.  `last(t, o, v)` has the final word on a sum.  Called by all threads; `have` is
-// false where a wait ran out.
-template <int J, typename F>
+// writes it.  Four outputs at a time and two such quads in flight a thread: element by element, one
+// remote access after another, this was 12 of 20 us at 257 x 1031 x 517.  `redo()` says, once the
+// cluster has met, whether `again(t, o)` makes the sums anew.  Called by all threads; `have` is false
+// where a wait ran out.
+template <int J, typename R, typename F>
 __device__ __forceinline__ void split_epilogue(const Epi& E, const TileSums<J>& sums, bool have, uint8_t* sm, int C,
-                                               int rank, int32_t o0, int64_t t0, int tokens, F last) {
+                                               int rank, int32_t o0, int64_t t0, int tokens, R redo, F again) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   float* part = reinterpret_cast<float*>(sm);
   if (warp < kEpiWarps) {
@@ -195,35 +240,67 @@ __device__ __forceinline__ void split_epilogue(const Epi& E, const TileSums<J>& 
   }
   __syncthreads();
   if (C > 1) cluster_sync();
-  const int total = tokens * kRows;
-  for (int e = rank * 256 + tid; warp < kEpiWarps && e < total; e += C * 256) {
-    float v;
-    if (C > 1) {
-      const uint32_t at = smem_u32(part + e);
-      float p[8];
+  if (warp < kEpiWarps && have) {
+    const bool anew = redo();
+    const bool vec = E.tma_y;  // (d_out a multiple of 4 and y, residual aligned)
+    const bool bias_vec = vec && (reinterpret_cast<uintptr_t>(E.bias) & 15u) == 0;
+    const bool sw_vec = vec && (reinterpret_cast<uintptr_t>(E.sw) & 15u) == 0;
+    const int quads = tokens * (kRows / 4), step = C * 256;
+    for (int q0 = rank * 256 + tid; q0 < quads; q0 += 2 * step) {
+      Quad v[2], res[2];
 #pragma unroll
-      for (int c = 0; c < 8; ++c) p[c] = c < C ? dsmem_ld_f32(dsmem_addr(at, (uint32_t)c)) : 0.f;
-      v = p[0];
+      for (int u = 0; u < 2; ++u) {
+        const int q = q0 + u * step, o = o0 + (q % (kRows / 4)) * 4;
+        if (q >= quads || o >= E.d_out) continue;
+        const int64_t row = (t0 + q / (kRows / 4)) * E.d_out;
+        if (E.res) {
+          if (E.y_bf16)
+            res[u].load(static_cast<const __nv_bfloat16*>(E.res) + row, o, E.d_out, vec);
+          else
+            res[u].load(static_cast<const float*>(E.res) + row, o, E.d_out, vec);
+        }
+        float4 p[8];
+        const uint32_t at = smem_u32(part + 4 * q);
 #pragma unroll
-      for (int c = 1; c < 8; ++c)
-        if (c < C) v += p[c];
-    } else {
-      v = part[e];
-    }
-    const int64_t t = t0 + e / kRows;
-    const int32_t o = o0 + e % kRows;
-    if (o >= E.d_out || !have) continue;
-    v = last(t, o, v);
-    if (E.sx) v *= E.sx[t] * E.sw[o];
-    if (E.bias) v += E.bias[o];
-    v = activate(v, E.act);
-    const int64_t at = t * E.d_out + o;
-    if (E.y_bf16) {
-      if (E.res) v += to_float(static_cast<const __nv_bfloat16*>(E.res)[at]);
-      static_cast<__nv_bfloat16*>(E.y)[at] = __float2bfloat16_rn(v);
-    } else {
-      if (E.res) v += static_cast<const float*>(E.res)[at];
-      static_cast<float*>(E.y)[at] = v;
+        for (int c = 0; c < 8; ++c)
+          if (c < C) p[c] = C > 1 ? dsmem_ld_f4(dsmem_addr(at, (uint32_t)c)) : *reinterpret_cast<const float4*>(part + 4 * q);
+        v[u].v[0] = p[0].x, v[u].v[1] = p[0].y, v[u].v[2] = p[0].z, v[u].v[3] = p[0].w;
+#pragma unroll
+        for (int c = 1; c < 8; ++c)
+          if (c < C) v[u].v[0] += p[c].x, v[u].v[1] += p[c].y, v[u].v[2] += p[c].z, v[u].v[3] += p[c].w;
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int q = q0 + u * step, o = o0 + (q % (kRows / 4)) * 4;
+        if (q >= quads || o >= E.d_out) continue;
+        const int64_t t = t0 + q / (kRows / 4), row = t * E.d_out;
+        if (anew)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (o + i < E.d_out) v[u].v[i] = again(t, o + i);
+        if (E.sx) {
+          Quad w;
+          w.load(E.sw, o, E.d_out, sw_vec);
+          const float sx = E.sx[t];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[u].v[i] *= sx * w.v[i];
+        }
+        if (E.bias) {
+          Quad w;
+          w.load(E.bias, o, E.d_out, bias_vec);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[u].v[i] += w.v[i];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[u].v[i] = activate(v[u].v[i], E.act);
+        if (E.res)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[u].v[i] += res[u].v[i];
+        if (E.y_bf16)
+          v[u].store(static_cast<__nv_bfloat16*>(E.y) + row, o, E.d_out, vec);
+        else
+          v[u].store(static_cast<float*>(E.y) + row, o, E.d_out, vec);
+      }
     }
   }
   __syncthreads();
@@ -669,7 +746,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // every MMA is done; the TMA warp has seen every load land
   have = mbar_wait(&ctrl->done, 0) && have && !*abort;
   __syncthreads();
-  split_epilogue(E, sums, have, sm, C, rank, o0, t0, tokens, [](int64_t, int32_t, float v) { return v; });
+  split_epilogue(E, sums, have, sm, C, rank, o0, t0, tokens, []() { return false; }, [](int64_t, int32_t) { return 0.f; });
   if (warp == 9) {
     tc_fence_after();
     tmem_dealloc(tmem, P.tmem_cols);
@@ -1038,15 +1115,16 @@ __global__ void __launch_bounds__(kAnyThreads, 1)
   }
   __syncthreads();
   // an odd element of any CTA of the cluster (they hold other parts of the same rows)
-  const uint32_t seen_at = smem_u32(&ctrl->odd);
-  split_epilogue(E, sums, have, sm, C, rank, o0, t0, tokens, [&](int64_t t, int32_t o, float v) {
-    if (kPlanes == 1) return v;
+  auto odd_seen = [&]() {
     int32_t seen = 0;
-    for (int c = 0; c < C; ++c) seen |= C > 1 ? __float_as_int(dsmem_ld_f32(dsmem_addr(seen_at, (uint32_t)c))) : ctrl->odd;
-    if (seen) {
-      v = 0.f;
-      for (int i = 0; i < d_in; ++i) v = fmaf(to_float(x[t * d_in + i]), to_float(W[(int64_t)o * d_in + i]), v);
-    }
+    if (kPlanes == 3)
+      for (int c = 0; c < C; ++c)
+        seen |= C > 1 ? __float_as_int(dsmem_ld_f32(dsmem_addr(smem_u32(&ctrl->odd), (uint32_t)c))) : ctrl->odd;
+    return seen != 0;
+  };
+  split_epilogue(E, sums, have, sm, C, rank, o0, t0, tokens, odd_seen, [&](int64_t t, int32_t o) {
+    float v = 0.f;
+    for (int i = 0; i < d_in; ++i) v = fmaf(to_float(x[t * d_in + i]), to_float(W[(int64_t)o * d_in + i]), v);
     return v;
   });
   if (warp == 15) {
