@@ -43,7 +43,7 @@ constexpr int kEpiWarps = 8;
 constexpr int kThreads = 32 * (kEpiWarps + 2);  // + TMA warp (8) + MMA warp (9)
 constexpr int kAnyThreads = 512;    // linear_any_kernel: 15 warps that lay out operands + MMA warp (15)
 constexpr int kCutters = kAnyThreads - 32;
-constexpr int kMaxStages = 8;
+constexpr int kMaxStages = 12;
 constexpr int kSpan = 8;            // K blocks summed in TMEM before fp32 registers take over
 constexpr size_t kMaxSmem = 227 * 1024;
 constexpr size_t kSmemSlack = 1024;
@@ -220,11 +220,11 @@ struct Quad {
 // Ends such a tile, whose d_in was split over a cluster's C CTAs: each CTA's sums go to shared memory,
 // [token][output] in the stage ring (free: every load has landed and every MMA is done); each CTA then adds
 // its share of the elements in rank order, reading the others' through distributed shared memory, and
-// writes it.  Four outputs at a time and two such quads in flight a thread: element by element, one
+// writes it.  Four outputs at a time and U such quads in flight a thread: element by element, one
 // remote access after another, this was 12 of 20 us at 257 x 1031 x 517.  `redo()` says, once the
 // cluster has met, whether `again(t, o)` makes the sums anew.  Called by all threads; `have` is false
 // where a wait ran out.
-template <int J, typename R, typename F>
+template <int U, int J, typename R, typename F>
 __device__ __forceinline__ void split_epilogue(const Epi& E, const TileSums<J>& sums, bool have, uint8_t* sm, int C,
                                                int rank, int32_t o0, int64_t t0, int tokens, R redo, F again) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -246,10 +246,10 @@ __device__ __forceinline__ void split_epilogue(const Epi& E, const TileSums<J>& 
     const bool bias_vec = vec && (reinterpret_cast<uintptr_t>(E.bias) & 15u) == 0;
     const bool sw_vec = vec && (reinterpret_cast<uintptr_t>(E.sw) & 15u) == 0;
     const int quads = tokens * (kRows / 4), step = C * 256;
-    for (int q0 = rank * 256 + tid; q0 < quads; q0 += 2 * step) {
-      Quad v[2], res[2];
+    for (int q0 = rank * 256 + tid; q0 < quads; q0 += U * step) {
+      Quad v[U], res[U];
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
+      for (int u = 0; u < U; ++u) {
         const int q = q0 + u * step, o = o0 + (q % (kRows / 4)) * 4;
         if (q >= quads || o >= E.d_out) continue;
         const int64_t row = (t0 + q / (kRows / 4)) * E.d_out;
@@ -270,7 +270,7 @@ __device__ __forceinline__ void split_epilogue(const Epi& E, const TileSums<J>& 
           if (c < C) v[u].v[0] += p[c].x, v[u].v[1] += p[c].y, v[u].v[2] += p[c].z, v[u].v[3] += p[c].w;
       }
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
+      for (int u = 0; u < U; ++u) {
         const int q = q0 + u * step, o = o0 + (q % (kRows / 4)) * 4;
         if (q >= quads || o >= E.d_out) continue;
         const int64_t t = t0 + q / (kRows / 4), row = t * E.d_out;
@@ -746,7 +746,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // every MMA is done; the TMA warp has seen every load land
   have = mbar_wait(&ctrl->done, 0) && have && !*abort;
   __syncthreads();
-  split_epilogue(E, sums, have, sm, C, rank, o0, t0, tokens, []() { return false; }, [](int64_t, int32_t) { return 0.f; });
+  split_epilogue<J >= 2 ? 4 : 2>(E, sums, have, sm, C, rank, o0, t0, tokens, []() { return false; }, [](int64_t, int32_t) { return 0.f; });
   if (warp == 9) {
     tc_fence_after();
     tmem_dealloc(tmem, P.tmem_cols);
@@ -1122,7 +1122,7 @@ __global__ void __launch_bounds__(kAnyThreads, 1)
         seen |= C > 1 ? __float_as_int(dsmem_ld_f32(dsmem_addr(smem_u32(&ctrl->odd), (uint32_t)c))) : ctrl->odd;
     return seen != 0;
   };
-  split_epilogue(E, sums, have, sm, C, rank, o0, t0, tokens, odd_seen, [&](int64_t t, int32_t o) {
+  split_epilogue<2>(E, sums, have, sm, C, rank, o0, t0, tokens, odd_seen, [&](int64_t t, int32_t o) {
     float v = 0.f;
     for (int i = 0; i < d_in; ++i) v = fmaf(to_float(x[t * d_in + i]), to_float(W[(int64_t)o * d_in + i]), v);
     return v;
@@ -1177,10 +1177,64 @@ bool operand_map(CUtensorMap* m, const LinearArgs& a, const void* base, int64_t 
                     (uint64_t)rows, (uint64_t)a.d_in, fp8 ? 128 : 64, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+// How many clusters of 1 to 8 CTAs (one an SM) the current device holds at once: its groups of SMs are not
+// multiples of every size (on GB300's 152 SMs: 76 of 2, 36 of 4, 23 of 6, 15 of 8).  Asked for once a
+// device; one look at the current device a call, since a small product is over in 4 us.
+struct Resident {
+  int of[9];
+};
+
+int ask_resident(int C) {
+  static std::atomic<uint64_t> allowed;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(C * num_sms()));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kMaxSmem;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = (unsigned)C;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (allow_smem(linear_skinny_kernel<false, 1>, allowed, kMaxSmem) == cudaSuccess &&
+      cudaOccupancyMaxActiveClusters(&n, linear_skinny_kernel<false, 1>, &cfg) == cudaSuccess && n > 0)
+    return n;
+  cudaGetLastError();
+  return num_sms() / C * 3 / 4;
+}
+
+Resident resident_clusters() {
+  static std::atomic<int> known[64][9];
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) dev = -1;
+  Resident r = {};
+  r.of[1] = num_sms();
+  for (int C = 2; C <= 8; ++C) {
+    r.of[C] = dev >= 0 ? known[dev][C].load(std::memory_order_relaxed) : 0;
+    if (r.of[C]) continue;
+    r.of[C] = ask_resident(C);
+    if (dev >= 0) known[dev][C].store(r.of[C], std::memory_order_relaxed);
+  }
+  return r;
+}
+
+// How many CTAs share a tile's d_in of nkb blocks: as many as let every tile have its cluster at once,
+// two blocks each at least.
+int split_of(const Resident& r, int64_t tiles, int nkb) {
+  for (int C = 8; C > 1; --C)
+    if (nkb >= 2 * C && tiles <= r.of[C]) return C;
+  return 1;
+}
+
 Epi epilogue_of(const LinearArgs& a) {
   Epi e = {a.x_scale, a.w_scale, a.bias, a.residual, a.y, a.N, a.d_out, a.act, a.y_bf16, false};
   e.tma_y = a.d_out % (a.y_bf16 ? 8 : 4) == 0 && aligned(a.y, 16) && aligned(a.residual, 16);
   return e;
+}
+
+int k_blocks(const LinearArgs& a) {
+  return (int)(((int64_t)a.d_in * (a.dtype == MOLORA_E4M3 ? 1 : 2) + kRowBytes - 1) / kRowBytes);
 }
 
 cudaError_t launch_tc(const LinearArgs& a, int BN, bool promote, const LinearUpdate* u, cudaStream_t stream) {
@@ -1188,7 +1242,7 @@ cudaError_t launch_tc(const LinearArgs& a, int BN, bool promote, const LinearUpd
   Epi e = epilogue_of(a);
   TcPlan p = {};
   p.BN = BN;
-  p.nkb = (int)(((int64_t)a.d_in * (fp8 ? 1 : 2) + kRowBytes - 1) / kRowBytes);
+  p.nkb = k_blocks(a);
   p.nkg = u ? (u->KR + 63) / 64 : 0;
   p.m_tiles = (a.N + 2 * kRows - 1) / (2 * kRows);
   p.n_tiles = (a.d_out + BN - 1) / BN;
@@ -1228,17 +1282,33 @@ cudaError_t launch_tc(const LinearArgs& a, int BN, bool promote, const LinearUpd
   return launch_kernel(kernel, grid, dim3(kThreads), p.smem, stream, 2, e, p, a.err_word, mx, mw, my, ghi, glo, mb);
 }
 
-cudaError_t launch_skinny(const LinearArgs& a, cudaStream_t stream) {
+// Cycles that linear_skinny_kernel takes in tiles of BN tokens, and linear_tc_kernel in tiles of BN outputs, as
+// measured on GB300 with 64 to 6144 outputs, d_in 1024 to 4096 and 1 to 4096 tokens (within 20%): what
+// a K block takes, a join or a last epilogue that grows with the tile, and the way through.  The split
+// product is 7.7 us for 16 tokens of 4096 x 4096, 16.5 for 256 and 23.4 for 512, the pairs' 16.6, 17.1 and 17.6.
+int64_t skinny_cycles(const LinearArgs& a, const Resident& r, int BN) {
+  const int64_t tiles = (((int64_t)a.d_out + kRows - 1) / kRows) * ((a.N + BN - 1) / BN);
+  const int nkb = k_blocks(a), C = split_of(r, tiles, nkb);
+  const int64_t waves = (tiles + r.of[C] - 1) / r.of[C];
+  return 6500 + waves * ((nkb + C - 1) / C * (420 + BN * 3 / 2) + 48 * BN);
+}
+
+int64_t tc_cycles(const LinearArgs& a, const Resident& r, int BN, int blocks) {
+  const int64_t m_tiles = (a.N + 2 * kRows - 1) / (2 * kRows);
+  const int64_t tiles = m_tiles * ((a.d_out + BN - 1) / BN), waves = (tiles + r.of[2] - 1) / r.of[2];
+  return 8000 + waves * blocks * (2 * BN + 90 > 420 ? 2 * BN + 90 : 420);
+}
+
+cudaError_t launch_skinny(const LinearArgs& a, const Resident& r, int BN, cudaStream_t stream) {
   const bool fp8 = a.dtype == MOLORA_E4M3;
   const Epi e = epilogue_of(a);
   SkinnyPlan p = {};
-  p.BN = a.N <= 16 ? 16 : a.N <= 32 ? 32 : a.N <= 64 ? 64 : a.N <= 128 ? 128 : 256;
-  p.nkb = (int)(((int64_t)a.d_in * (fp8 ? 1 : 2) + kRowBytes - 1) / kRowBytes);
+  p.BN = BN;
+  p.nkb = k_blocks(a);
   p.o_tiles = (a.d_out + kRows - 1) / kRows;
   p.t_tiles = (int32_t)((a.N + p.BN - 1) / p.BN);
   const int64_t tiles = (int64_t)p.o_tiles * p.t_tiles;
-  p.C = 1;
-  while (p.C < 8 && tiles * p.C * 2 <= num_sms() && p.nkb >= p.C * 4) p.C *= 2;
+  p.C = split_of(r, tiles, p.nkb);
   p.off_b = kRows * kRowBytes;
   p.stage_bytes = p.off_b + (uint32_t)p.BN * kRowBytes;
   p.tmem_cols = tmem_columns(2 * (uint32_t)p.BN);
@@ -1289,10 +1359,7 @@ cudaError_t launch_any(const LinearArgs& a, cudaStream_t stream) {
   const bool wide = (kVec || planes == 1) && a.N > 64 && tiles_at(128) >= num_sms();  // (unaligned fp32: too many registers)
   p.BN = a.N <= 16 ? 16 : a.N <= 32 ? 32 : wide ? 128 : 64;
   const int64_t tiles = tiles_at(p.BN);
-  // (a power of two: 25 clusters of 6 do not fit the GPU's groups of SMs at once, 22.9 us against 19.7 with
-  // 25 of 4 at 257 x 1031 x 517)
-  p.C = 1;
-  while (p.C < 8 && tiles * p.C * 2 <= num_sms() && p.nkb >= p.C * 4) p.C *= 2;
+  p.C = split_of(resident_clusters(), tiles, p.nkb);
   p.grid = aligned(a.x, 16) && aligned(a.W, 16);
   p.plane = (uint32_t)(kRows + p.BN) * kRowBytes;
   p.stage_bytes = planes * p.plane;
@@ -1326,12 +1393,6 @@ static bool tma_rows(const LinearArgs& a) {
          linear_encoder() != nullptr;
 }
 
-// True where the CTA-pair kernel runs: more tokens than a split tile's 256, and more tiles of
-// 128 outputs x 256 tokens than half of the SMs.
-static bool many_tokens(const LinearArgs& a) {
-  return a.N > 256 && ((int64_t)a.d_out + kRows - 1) / kRows * ((a.N + 255) / 256) > num_sms() / 2;
-}
-
 bool linear_takes_update(const LinearArgs& a, const void* B, int32_t KR) {
   return tma_rows(a) && a.N > 256 && a.d_out % 8 == 0 && KR % 8 == 0 && aligned(B, 16);
 }
@@ -1343,26 +1404,27 @@ cudaError_t launch_linear(const LinearArgs& a, cudaStream_t stream, const Linear
     return a.d_in % 4 == 0 && aligned(a.x, 16) && aligned(a.W, 16) ? launch_any<float, true>(a, stream)
                                                                     : launch_any<float, false>(a, stream);
   }
-  if (!update && !many_tokens(a)) return launch_skinny(a, stream);
   // K blocks of fp32 results that sum in registers (see linear_tc_kernel), which hold 96 columns a thread;
   // e4m3 sums are half as many and drift a tenth as far (2e-7 at d_in = 4096)
-  const int64_t blocks = ((int64_t)a.d_in + 63) / 64 + (update ? (update->KR + 63) / 64 * 2 : 0);
+  const int blocks = k_blocks(a) + (update ? (update->KR + 63) / 64 * 2 : 0);
   const bool promote = a.dtype == MOLORA_E4M3 ? update != nullptr : !a.y_bf16 && blocks > kSpan;
-  // the width whose waves of tiles cost least
-  const int64_t pairs = num_sms() / 2, m_tiles = (a.N + 2 * kRows - 1) / (2 * kRows);
-  int best = 128;
+  const Resident r = resident_clusters();
+  int best = 128, split = 0;
   int64_t cost = INT64_MAX;
   for (int BN : {256, 224, 192, 160, 128, 96, 64}) {
-    if (promote && BN > 192) continue;
-    const int64_t tiles = m_tiles * ((a.d_out + BN - 1) / BN), waves = (tiles + pairs - 1) / pairs;
-    // cycles of a stage, halved: 420 for narrow tiles, 2 BN and 90 for wide ones
-    const int64_t c = waves * (BN + 45 > 210 ? BN + 45 : 210);
+    const int64_t c = promote && BN > 192 ? INT64_MAX : tc_cycles(a, r, BN, blocks);
     if (c < cost) cost = c, best = BN;
+  }
+  for (int BN : {16, 32, 64, 128, 256}) {
+    if (update || (BN > 16 && BN / 2 >= a.N)) continue;
+    const int64_t c = skinny_cycles(a, r, BN);
+    if (c < cost) cost = c, split = BN;
   }
 #ifdef MOLORA_TUNING_ENV
   if (const char* g = getenv("MOLORA_LIN_BN")) best = atoi(g);
+  if (const char* g = getenv("MOLORA_LIN_SKINNY")) split = atoi(g);
 #endif
-  return launch_tc(a, best, promote, update, stream);
+  return split ? launch_skinny(a, r, split, stream) : launch_tc(a, best, promote, update, stream);
 }
 
 }  // namespace molora
