@@ -233,7 +233,9 @@ def check_gate(logits, ids, w, k, score, bias, groups, keep, group_top, renorm, 
     (257, 60, 6, "softmax", True, 1, 1, 1), (1000, 256, 8, "sigmoid", True, 8, 4, 2), (63, 512, 32, "softmax", True, 1, 1, 1),
     (100, 512, 8, "sigmoid", False, 32, 3, 2), (77, 66, 5, "softmax", False, 6, 2, 1), (129, 30, 3, "sigmoid", False, 5, 5, 1),
     (64, 255, 7, "softmax", True, 3, 1, 2), (200, 33, 33 - 1, "sigmoid", False, 1, 1, 1), (50, 16, 2, "softmax", True, 8, 1, 2),
-    (513, 128, 6, "softmax", False, 1, 1, 1), (90, 48, 4, "softmax", True, 16, 4, 1), (40, 250, 9, "sigmoid", True, 25, 20, 2)])
+    (513, 128, 6, "softmax", False, 1, 1, 1), (90, 48, 4, "softmax", True, 16, 4, 1), (40, 250, 9, "sigmoid", True, 25, 20, 2),
+    (70, 32, 5, "softmax", True, 32, 9, 1), (45, 64, 6, "sigmoid", True, 2, 1, 2), (91, 128, 32, "softmax", True, 4, 3, 2),
+    (37, 512, 8, "softmax", True, 16, 5, 2), (21, 256, 12, "softmax", False, 8, 2, 1)])
 @pytest.mark.parametrize("renorm", [False, True])
 def test_gate(m, dtype, N, K, k, score, bias, groups, keep, top, renorm):
     g = gen(N + K)
@@ -250,7 +252,8 @@ def test_gate(m, dtype, N, K, k, score, bias, groups, keep, top, renorm):
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
-@pytest.mark.parametrize("K, groups, top", [(16, 1, 1), (60, 1, 1), (256, 8, 2), (64, 4, 1), (500, 1, 1)])
+@pytest.mark.parametrize("K, groups, top", [(16, 1, 1), (60, 1, 1), (256, 8, 2), (64, 4, 1), (500, 1, 1),
+                                            (512, 4, 2), (96, 4, 2)])
 def test_gate_ties_go_to_the_lower_index(m, score, K, groups, top):
     """Logits of three values only: among equal experts, and equal groups, the lower index comes first."""
     g = gen(K)

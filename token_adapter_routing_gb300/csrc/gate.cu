@@ -4,13 +4,16 @@
 // A token belongs to TL lanes of a warp; lane l of them holds experts l, l + TL, l + 2 TL, ...: every
 // load is of consecutive logits, whatever K and the rows' alignment.
 //
-// Bound by instructions, not bytes: 16384 x 256 fp32 in 8 groups takes 19.3 us (its 17.8 MB would take 2.6),
-// issuing in 75% of the cycles, about 1100 warp instructions a token, of which 230 are the sigmoids and
-// 310 the groups; 40961 x 60 bf16 with a bias 16.4 us.  32 x 64 takes 1.6 us, a launch.
+// Bound by instructions, not bytes: 16384 x 256 fp32 in 8 groups takes 18.1 us (its 17.8 MB would take 2.6),
+// about 1000 warp instructions a token: the sigmoids 2.5 us of it, the bound 1.0, the candidates 2.3, their
+// ranks 2.0.  Fetching the next token's logits ahead, or other grids, gained nothing.  40961 x 60 bf16 with a
+// bias takes 16.4 us, 32 x 64 1.6 us, a launch.
 //
 // Everything the choice depends on is reproducible: e = expf(l - max) and 1 / (1 + expf(-l)) are
 // single fp32 operations, and the softmax's denominator is a sum of integers (to 2^-44 of the largest e)
 // that is rounded once, so it does not depend on the order of the sum.
+#include <type_traits>
+
 #include "common.cuh"
 #include "kernels.h"
 
@@ -59,12 +62,12 @@ __device__ __forceinline__ float score_of(const GateArgs& a, float l, const Norm
   return n.total > 0.f ? __fdiv_rn(e, n.total) : 0.f;
 }
 
-// The biases of this lane's experts, made finite or -inf.
-template <int TL, int V>
-__device__ __forceinline__ void gate_bias(const GateArgs& a, int sub, float (&b)[V]) {
+// The biases of this lane's experts first, first + step, ..., made finite or -inf.
+template <int V>
+__device__ __forceinline__ void gate_bias(const GateArgs& a, int first, int step, float (&b)[V]) {
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    b[i] = a.bias && sub + TL * i < a.K ? a.bias[sub + TL * i] : 0.f;
+    b[i] = a.bias && first + step * i < a.K ? a.bias[first + step * i] : 0.f;
     if (b[i] != b[i]) {
       report(a.err_word, MOLORA_DEV_BAD_LOGIT);
       b[i] = kLowest;
@@ -185,12 +188,30 @@ __device__ __forceinline__ void gate_rounds(const GateArgs& a, float (&c)[V], co
   for (int j = found + sub; j < a.k; j += TL) a.ids[t * a.k + j] = -1, a.w[t * a.k + j] = 0.f;
 }
 
+// Stores the ids and weights of a token whose found experts, best first, stand with their scores in the warp's
+// first lanes: the sum of the scores depends on their order alone.
+__device__ __forceinline__ void gate_store(const GateArgs& a, float score, int id, int found, int64_t t) {
+  const int lane = threadIdx.x & 31;
+  if (lane >= found) score = 0.f, id = -1;
+  float sum = score;
+  if (a.renorm) {
+#pragma unroll
+    for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(kFull, sum, off);
+  }
+  if (lane < a.k) {
+    const float w = !a.renorm ? score : sum > 0.f ? score / sum : 0.f;
+    a.ids[t * a.k + lane] = id;
+    a.w[t * a.k + lane] = w * a.scale;
+  }
+}
+
 // The same for a warp a token, with the choices as ordered integers: a maximum, and the lowest index that
 // has it, is one instruction over the warp.
-template <int V>
+template <int V, bool kBlocked>
 __device__ __forceinline__ void gate_rounds_warp(const GateArgs& a, const float (&c)[V], const float (&l)[V],
                                                  const Norms& n, int64_t t) {
   const int lane = threadIdx.x & 31;
+  auto expert = [&](int i) { return (uint32_t)(kBlocked ? V * lane + i : lane + 32 * i); };
   const uint32_t none = ordered(kLowest);
   uint32_t key[V];
 #pragma unroll
@@ -206,30 +227,20 @@ __device__ __forceinline__ void gate_rounds_warp(const GateArgs& a, const float 
     uint32_t at = 0xffffffffu;
 #pragma unroll
     for (int i = V - 1; i >= 0; --i)
-      if (key[i] == top) at = (uint32_t)(lane + 32 * i);
+      if (key[i] == top) at = expert(i);
     at = __reduce_min_sync(kFull, at);
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if (at == (uint32_t)(lane + 32 * i)) key[i] = 0u;
+      if (at == expert(i)) key[i] = 0u;
     if (lane == found) mine = at;
   }
   float logit = 0.f;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const float from = __shfl_sync(kFull, l[i], mine & 31);
-    if ((int)(mine >> 5) == i) logit = from;
+    const float from = __shfl_sync(kFull, l[i], kBlocked ? mine / V : mine & 31);
+    if ((int)(kBlocked ? mine % V : mine >> 5) == i) logit = from;
   }
-  const float score = lane < found ? score_of(a, logit, n) : 0.f;
-  float sum = score;
-  if (a.renorm) {
-#pragma unroll
-    for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(kFull, sum, off);
-  }
-  if (lane < a.k) {
-    const float w = !a.renorm ? score : sum > 0.f ? score / sum : 0.f;
-    a.ids[t * a.k + lane] = lane < found ? (int32_t)mine : -1;
-    a.w[t * a.k + lane] = w * a.scale;
-  }
+  gate_store(a, lane < found ? score_of(a, logit, n) : 0.f, (int)mine, found, t);
 }
 
 }  // namespace
@@ -244,7 +255,7 @@ __global__ void __launch_bounds__(kGateWarps * 32, 4) gate_small_kernel(const T*
   pdl_wait();
   pdl_launch_dependents();
   float b[V];
-  gate_bias<TL, V>(a, sub, b);
+  gate_bias<V>(a, sub, TL, b);
   for (int64_t t0 = ((int64_t)blockIdx.x * kGateWarps + warp) * kTokens; t0 < a.N;
        t0 += (int64_t)gridDim.x * kGateWarps * kTokens) {
     const int64_t t = t0 + lane / TL;
@@ -262,38 +273,64 @@ __global__ void __launch_bounds__(kGateWarps * 32, 4) gate_small_kernel(const T*
 // in rounds; with more, the k-th largest of the 32 lanes' own maxima is a bound that the k largest choices
 // reach and few others do, and those that do (k and a few) are ranked by counting, in shared memory
 // (16384 x 256, top 8 by logits: 10.5 us, 14.0 in rounds; 512 experts 31.4 against 37.7).
-template <typename T, int V>
+//
+// kBlocked: groups of 32 / G whole lanes, which hold V consecutive experts each (32 V experts in a power of
+// two of groups): a group's best two come from registers and a few shuffles, and a lane stays or goes as one
+// (16384 x 256 in 8 groups 18.1 us; 19.3 through shared memory, which other sizes take).
+template <typename T, int V, bool kBlocked>
 __global__ void __launch_bounds__(kGateWarps * 32, V <= 8 ? 4 : 2) gate_topk_kernel(const T* __restrict__ logits, const GateArgs a) {
-  extern __shared__ float choices[];  // [warps][K], with groups
+  extern __shared__ float choices[];  // [warps][K], with groups that do not follow the lanes
   __shared__ float2 cand[kGateWarps][32];  // (choice, expert) of those that reach the bound
   __shared__ float cand_l[kGateWarps][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t below = (1u << lane) - 1u;
+  auto expert = [&](int i) { return kBlocked ? V * lane + i : lane + 32 * i; };
   pdl_wait();
   pdl_launch_dependents();
   float b[V];
-  gate_bias<32, V>(a, lane, b);
+  gate_bias<V>(a, expert(0), kBlocked ? 1 : 32, b);
   for (int64_t t = (int64_t)blockIdx.x * kGateWarps + warp; t < a.N; t += (int64_t)gridDim.x * kGateWarps) {
     float l[V], c[V];
-    const T* row = logits + t * a.K + lane;
+    const T* row = logits + t * a.K;
+    if constexpr (kBlocked) {
+      constexpr int kBytes = V * sizeof(T) < 16 ? V * sizeof(T) : 16, kEach = kBytes / sizeof(T);
+      struct alignas(kBytes) Run {
+        T v[kEach];
+      };
 #pragma unroll
-    for (int i = 0; i < V; ++i) l[i] = lane + 32 * i < a.K ? to_float(row[32 * i]) : kLowest;
+      for (int i = 0; i < V; i += kEach) {
+        const Run run = *reinterpret_cast<const Run*>(row + expert(i));
+#pragma unroll
+        for (int j = 0; j < kEach; ++j) l[i + j] = to_float(run.v[j]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) l[i] = expert(i) < a.K ? to_float(row[expert(i)]) : kLowest;
+    }
     const Norms n = gate_choices<32, V>(a, l, b, c);
-    if (a.G > 1) {
+    if (kBlocked || a.G > 1) {
       // each group's best, or best two
       float* mine = choices + (size_t)warp * a.K;
-#pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (lane + 32 * i < a.K) mine[lane + 32 * i] = c[i];
-      __syncwarp();
-      const int per = a.K / a.G;
       const int lanes = a.group_lanes, g = lane / lanes;
       float c1 = kLowest, c2 = kLowest;
-      if (g < a.G) {
-        for (int i = lane & (lanes - 1); i < per; i += lanes) {
-          const float v = mine[g * per + i];
-          c2 = fmaxf(c2, fminf(c1, v));
-          c1 = fmaxf(c1, v);
+      if constexpr (kBlocked) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          c2 = fmaxf(c2, fminf(c1, c[i]));
+          c1 = fmaxf(c1, c[i]);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (expert(i) < a.K) mine[expert(i)] = c[i];
+        __syncwarp();
+        const int per = a.K / a.G;
+        if (g < a.G) {
+          for (int i = lane & (lanes - 1); i < per; i += lanes) {
+            const float v = mine[g * per + i];
+            c2 = fmaxf(c2, fminf(c1, v));
+            c1 = fmaxf(c1, v);
+          }
         }
       }
       for (int off = 1; off < lanes; off <<= 1) {
@@ -310,13 +347,19 @@ __global__ void __launch_bounds__(kGateWarps * 32, V <= 8 ? 4 : 2) gate_topk_ker
         kept |= 1u << (win / lanes);
         if (lane == win) key = 0u;
       }
+      if constexpr (kBlocked) {
+        if (!((kept >> g) & 1u))
 #pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (!((kept >> (((lane + 32 * i) * a.per_inverse) >> 20 & 31u)) & 1u)) c[i] = kLowest;
-      __syncwarp();
+          for (int i = 0; i < V; ++i) c[i] = kLowest;
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (!((kept >> ((expert(i) * a.per_inverse) >> 20 & 31u)) & 1u)) c[i] = kLowest;
+        __syncwarp();
+      }
     }
     if constexpr (V <= 4) {
-      gate_rounds_warp<V>(a, c, l, n, t);
+      gate_rounds_warp<V, kBlocked>(a, c, l, n, t);
       continue;
     }
     float most = c[0];
@@ -336,13 +379,13 @@ __global__ void __launch_bounds__(kGateWarps * 32, V <= 8 ? 4 : 2) gate_topk_ker
       const uint32_t who = __ballot_sync(kFull, in);
       const int at = count + __popc(who & below);
       if (in && at < 32) {
-        cand[warp][at] = make_float2(c[i], __int_as_float(lane + 32 * i));
+        cand[warp][at] = make_float2(c[i], __int_as_float(expert(i)));
         cand_l[warp][at] = l[i];
       }
       count += __popc(who);
     }
     if (count > 32) {  // many equal choices
-      gate_rounds_warp<V>(a, c, l, n, t);
+      gate_rounds_warp<V, kBlocked>(a, c, l, n, t);
       continue;
     }
     __syncwarp();
@@ -356,15 +399,10 @@ __global__ void __launch_bounds__(kGateWarps * 32, V <= 8 ? 4 : 2) gate_topk_ker
     }
     const bool chosen = has && rank < a.k;
     const float score = chosen ? score_of(a, cand_l[warp][lane], n) : 0.f;
-    float sum = score;
-#pragma unroll
-    for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(kFull, sum, off);
-    if (chosen) {
-      const float w = !a.renorm ? score : sum > 0.f ? score / sum : 0.f;
-      a.ids[t * a.k + rank] = __float_as_int(mine.y);
-      a.w[t * a.k + rank] = w * a.scale;
-    }
-    if (lane >= count && lane < a.k) a.ids[t * a.k + lane] = -1, a.w[t * a.k + lane] = 0.f;
+    __syncwarp();
+    if (chosen) cand[warp][rank] = make_float2(score, mine.y);
+    __syncwarp();
+    gate_store(a, cand[warp][lane].x, __float_as_int(cand[warp][lane].y), min(count, a.k), t);
     __syncwarp();
   }
 }
@@ -382,12 +420,18 @@ cudaError_t launch_gate_typed(const T* logits, const GateArgs& a, cudaStream_t s
     if (a.K <= 8) return launch_kernel(gate_small_kernel<T, 8, 1>, grid(4), block, 0, stream, 0, logits, a);
     return launch_kernel(gate_small_kernel<T, 8, 2>, grid(4), block, 0, stream, 0, logits, a);
   }
-  const size_t smem = a.G > 1 ? sizeof(float) * kGateWarps * a.K : 0;
-  if (a.K <= 32) return launch_kernel(gate_topk_kernel<T, 1>, grid(1), block, smem, stream, 0, logits, a);
-  if (a.K <= 64) return launch_kernel(gate_topk_kernel<T, 2>, grid(1), block, smem, stream, 0, logits, a);
-  if (a.K <= 128) return launch_kernel(gate_topk_kernel<T, 4>, grid(1), block, smem, stream, 0, logits, a);
-  if (a.K <= 256) return launch_kernel(gate_topk_kernel<T, 8>, grid(1), block, smem, stream, 0, logits, a);
-  return launch_kernel(gate_topk_kernel<T, 16>, grid(1), block, smem, stream, 0, logits, a);
+  auto go = [&](auto blocked) {
+    constexpr bool kB = decltype(blocked)::value;
+    const size_t smem = a.G > 1 && !kB ? sizeof(float) * kGateWarps * a.K : 0;
+    if (a.K <= 32) return launch_kernel(gate_topk_kernel<T, 1, kB>, grid(1), block, smem, stream, 0, logits, a);
+    if (a.K <= 64) return launch_kernel(gate_topk_kernel<T, 2, kB>, grid(1), block, smem, stream, 0, logits, a);
+    if (a.K <= 128) return launch_kernel(gate_topk_kernel<T, 4, kB>, grid(1), block, smem, stream, 0, logits, a);
+    if (a.K <= 256) return launch_kernel(gate_topk_kernel<T, 8, kB>, grid(1), block, smem, stream, 0, logits, a);
+    return launch_kernel(gate_topk_kernel<T, 16, kB>, grid(1), block, smem, stream, 0, logits, a);
+  };
+  const bool powers = a.K >= 32 && (a.K & (a.K - 1)) == 0 && a.G > 1 && (a.G & (a.G - 1)) == 0;
+  if (powers && (reinterpret_cast<uintptr_t>(logits) & 15) == 0) return go(std::true_type());
+  return go(std::false_type());
 }
 
 }  // namespace

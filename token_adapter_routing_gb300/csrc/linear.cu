@@ -1380,8 +1380,10 @@ cudaError_t launch_any(const LinearArgs& a, cudaStream_t stream) {
   };
   static std::atomic<uint64_t> allowed[3];
   if (p.BN <= 32) return go(linear_any_kernel<T, kVec, 1>, allowed[0]);
-  if (p.BN == 64) return go(linear_any_kernel<T, kVec, 2>, allowed[1]);
-  return go(linear_any_kernel<T, kVec, 4>, allowed[2]);
+  if constexpr (kVec || sizeof(T) != 4) {
+    if (p.BN == 128) return go(linear_any_kernel<T, kVec, 4>, allowed[2]);
+  }
+  return go(linear_any_kernel<T, kVec, 2>, allowed[1]);
 }
 
 }  // namespace
