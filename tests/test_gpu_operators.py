@@ -32,7 +32,8 @@ BF, F32, FP8 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
 HALF = {BF: 2.0 ** -8, F32: U}
 ACTS = {"none": lambda v: v, "relu": torch.relu, "silu": lambda v: v * torch.sigmoid(v),
         "gelu": lambda v: 0.5 * v * torch.erfc(-v / math.sqrt(2)),
-        "gelu_tanh": lambda v: 0.5 * v * (1 + torch.tanh(math.sqrt(2 / math.pi) * (v + 0.044715 * v ** 3)))}
+        # (1 + tanh(u)) / 2 = sigmoid(2 u), without the cancellation at u < 0
+        "gelu_tanh": lambda v: v * torch.sigmoid(2 * math.sqrt(2 / math.pi) * (v + 0.044715 * v ** 3))}
 
 
 @pytest.fixture(scope="module")
@@ -352,6 +353,28 @@ def check_linear(y, x, W, sx, sw, bias, act, res):
     if res is not None:
         a, tol = a + res.double(), tol + 2 * U * res.double().abs()
     within(y, a, tol + a.abs() * (HALF[y.dtype] + 2 * U) + 2.0 ** -120)
+
+
+@pytest.mark.parametrize("act", sorted(ACTS))
+def test_linear_activation_curves(m, act):
+    """act over its whole range, the sums exact (d_in = 1, W = 1): a power and a reciprocal are good to 2^-22
+    and 2^-23, an exponent's rounding costs 2 U of it; below the normal numbers they are 0.  So are the lower two
+    of an operand's three bf16 parts where they are below 2^-126, which is less than 2^-125 together.  v / (1 + e)
+    takes the sum's rounding (U), the reciprocal (2^-23 = 2 U) and the product's (U): under 5 U of the result."""
+    v = torch.cat([s * torch.logspace(-38, 38, 3001, device="cuda") for s in (1, -1)] +
+                  [torch.linspace(-16, 16, 8001, device="cuda"), torch.zeros(1, device="cuda")])
+    y = m.molora_linear(v[:, None], torch.ones(1, 1, device="cuda"), act=act, out_dtype=F32)[:, 0]
+    d = v.double()
+    want = ACTS[act](d)
+    want[(d < -100) & (act != "none")] = 0
+    exponent = {"silu": d.abs(), "gelu": d * d, "gelu_tanh": 1.6 * d.abs() + 0.072 * d.abs() ** 3}.get(act, 0 * d)
+    tail = want - d.clamp_min(0) if act != "none" else 0 * d   # what the power makes
+    within(y, want, 5 * U * want.abs() + tail.abs() * (2.0 ** -20 + 4 * U * exponent) + d.abs().clamp(1, 100) * 2.0 ** -125)
+    odd = torch.tensor([[math.inf], [math.nan], [-math.inf]], device="cuda")
+    y = m.molora_linear(odd, torch.ones(1, 1, device="cuda"), act=act, out_dtype=F32)[:, 0].tolist()
+    assert y[0] == math.inf and math.isnan(y[1])
+    if act in ("relu", "gelu"):
+        assert y[2] == 0
 
 
 SIZES = [(1, 64, 64), (1, 4096, 1000), (2, 128, 7), (3, 33, 5), (7, 200, 257), (8, 2048, 512), (16, 512, 129), (17, 640, 384),

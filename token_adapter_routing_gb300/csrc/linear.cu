@@ -497,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                          (uint32_t)min(BN, E.d_out - n0) * esize);
       }
       // a chunk of 32 columns from its sums to y
-      auto finish = [&](int c, float (&v)[32], const Residual& res, bool add) {
+      auto finish = [&](int c, float (&v)[32], const Residual& res, bool add, auto next) {
         const int col = n0 + c * 32;
         if (E.sx && !kPromote) {
 #pragma unroll
@@ -512,6 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         apply_act(v, E.act);
         if (E.tma_y) {
           if (add) res.add(v, E.y_bf16);
+          next();
           // 64 bytes of each row at a time: 32 columns of bf16, or 16 of fp32 twice
 #pragma unroll
           for (int part = 0; part < 2; ++part) {
@@ -569,9 +570,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++tc;
       };
       const bool add = E.tma_y && E.res && t < E.N;
-      Residual res;
+      Residual res;  // a chunk ahead: its way from L2 is under the chunk before
       auto load_residual = [&](int c) {
-        if (add) res.load(E.res, E.y_bf16, t * E.d_out + n0 + c * 32, E.d_out - n0 - c * 32);
+        if (add && c < chunks) res.load(E.res, E.y_bf16, t * E.d_out + n0 + c * 32, E.d_out - n0 - c * 32);
       };
       if constexpr (kPromote) {
         float acc[3][32];
@@ -598,25 +599,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           free_sums();
         }
         if (!ok) break;
+        load_residual(side);
 #pragma unroll
         for (int q = 0; q < 3; ++q) {
           if (side + 2 * q >= chunks) continue;
-          load_residual(side + 2 * q);
-          finish(side + 2 * q, acc[q], res, add);
+          finish(side + 2 * q, acc[q], res, add, [&] { load_residual(side + 2 * q + 2); });
         }
       } else {
+        load_residual(side);
         const uint32_t base = wait_sums();
         if (!ok) break;
         uint32_t r[32];
         if (side < chunks) tmem_ld32_start(base + (uint32_t)(side * 32), r);
         for (int c = side; c < chunks; c += 2) {
           float v[32];
-          load_residual(c);
           tmem_ld_wait(r);
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
           if (c + 2 < chunks) tmem_ld32_start(base + (uint32_t)((c + 2) * 32), r);
-          finish(c, v, res, add);
+          finish(c, v, res, add, [&] { load_residual(c + 2); });
         }
         free_sums();
       }

@@ -10,15 +10,35 @@ namespace molora {
 
 __device__ __forceinline__ float to_float(__nv_fp8_e4m3 v) { return static_cast<float>(v); }
 
-// erf's GELU, 32 of which in a row would not fit the registers inline.
-static __device__ __noinline__ float gelu_erf(float v) { return 0.5f * v * erfcf(v * -0.70710678118654752f); }
-
 // v / (1 + 2^z) by the hardware's power and reciprocal.  Where 2^z overflows the result is v * 0.
 __device__ __forceinline__ float over_one_plus_exp2(float v, float z) {
   float e, r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z));
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
   return v * r;
+}
+
+// GELU, v (1 + erf(v / sqrt(2))) / 2 = max(v, 0) - z Q(z) with z = |v| and Q(z) = erfc(z / sqrt(2)) / 2, the
+// normal distribution's tail.  Q(z) e^(z^2 / 2) falls smoothly from 1/2 and is a polynomial of degree 8 in
+// t = 1 / (1 + 0.3 z), fitted here for the least relative error over 0 <= z <= 13.5 (5.7e-8); past that z Q(z)
+// is below the smallest normal number.  No cancellation: of v < 0 only the second term is left.  17
+// instructions an element; the library's erfcf took 4096 x 2048 -> 6144 in e4m3 from 43 us to 115.
+__device__ __forceinline__ float gelu_erf(float v) {
+  const float z = fminf(fabsf(v), 14.f);
+  float t, e, most;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(fmaf(0.3f, z, 1.f)));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * (-0.72134752f * z)));
+  asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(most) : "f"(v));
+  float q = 0.0383342616f;
+  q = fmaf(q, t, -0.168951929f);
+  q = fmaf(q, t, 0.228217259f);
+  q = fmaf(q, t, -0.0759995431f);
+  q = fmaf(q, t, 0.142185017f);
+  q = fmaf(q, t, 0.094832994f);
+  q = fmaf(q, t, 0.121882051f);
+  q = fmaf(q, t, 0.119493067f);
+  q = fmaf(q, t, 6.85289888e-06f);
+  return fmaf(-z * q, e, most);
 }
 
 // act(v) in fp32 with a few instructions an element, so that the epilogue stays under the MMAs of the
