@@ -47,7 +47,7 @@ constexpr int kMaxStages = 12;
 constexpr int kSpan = 8;            // K blocks summed in TMEM before fp32 registers take over
 constexpr size_t kMaxSmem = 227 * 1024;
 constexpr size_t kSmemSlack = 1024;
-constexpr uint32_t kBox = 4096;     // epilogue staging per warp: two boxes of 32 rows x 64 bytes
+constexpr uint32_t kBox = 2048;     // of the epilogue's staging: 32 rows x 64 bytes
 
 struct __align__(8) LCtrl {
   uint64_t full[kMaxStages];
@@ -55,6 +55,7 @@ struct __align__(8) LCtrl {
   uint64_t tfull[2];
   uint64_t tempty[2];
   uint64_t done;
+  uint64_t res_full[kEpiWarps][2];
   uint32_t tmem_base;
   int32_t abort;
   int32_t odd;  // an infinite or NaN fp32 operand was seen
@@ -71,7 +72,7 @@ struct Epi {
   int32_t d_out;
   molora_activation act;
   bool y_bf16;
-  bool tma_y;    // y through its tensor map, residual in 16-byte vectors
+  bool tma_y;    // rows of y and residual on 16-byte boundaries: linear_tc_kernel moves them by TMA
 };
 
 struct TcPlan {
@@ -101,36 +102,6 @@ __device__ __forceinline__ void apply_act(float (&v)[32], molora_activation act)
     for (int i = 0; i < 32; ++i) v[i] = activate(v[i], MOLORA_ACT_GELU);
   }
 }
-
-// 32 residual columns of a row, in 16-byte vectors; those past d_out (a multiple of the vector's
-// elements) are 0.
-struct Residual {
-  uint4 q[8];
-  __device__ __forceinline__ void load(const void* res, bool bf16, int64_t at, int cols) {
-    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(res) + at * (bf16 ? 2 : 4));
-#pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = i * (bf16 ? 8 : 4) < min(cols, 32) ? p[i] : make_uint4(0, 0, 0, 0);
-  }
-  __device__ __forceinline__ void add(float (&v)[32], bool bf16) const {
-    if (bf16) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          v[8 * i + 2 * j] += __uint_as_float(w[j] << 16);
-          v[8 * i + 2 * j + 1] += __uint_as_float(w[j] & 0xffff0000u);
-        }
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        v[4 * i] += __uint_as_float(q[i].x), v[4 * i + 1] += __uint_as_float(q[i].y);
-        v[4 * i + 2] += __uint_as_float(q[i].z), v[4 * i + 3] += __uint_as_float(q[i].w);
-      }
-    }
-  }
-};
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
@@ -314,12 +285,14 @@ __device__ __forceinline__ void split_epilogue(const Epi& E, const TileSums<J>& 
 // would.  For fp32 y the epilogue warps take the sums of every 8 K blocks (32 MMAs) into registers
 // and add there.  With e4m3 operands it takes the adapters' update along: the product's sums are
 // scaled in registers before the update's, which have no scales, are added.
-template <bool kFp8, bool kPromote>
+template <bool kFp8, bool kPromote, bool kY16>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_tc_kernel(const Epi E, const TcPlan P, int32_t* err_word, const __grid_constant__ CUtensorMap map_x,
                      const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_y,
                      const __grid_constant__ CUtensorMap map_ghi, const __grid_constant__ CUtensorMap map_glo,
-                     const __grid_constant__ CUtensorMap map_b) {
+                     const __grid_constant__ CUtensorMap map_b, const __grid_constant__ CUtensorMap map_r) {
+  constexpr int kParts = kY16 ? 1 : 2;  // boxes of a chunk of 32 columns of y
+  constexpr uint32_t kSet = kParts * kBox;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   LCtrl* ctrl = reinterpret_cast<LCtrl*>(sm + P.off_ctrl);
@@ -360,6 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&ctrl->tempty[b], 2 * kEpiWarps);
     }
     mbar_init(&ctrl->done, 1);
+    for (int b = 0; b < 2 * kEpiWarps; ++b) mbar_init(&ctrl->res_full[b / 2][b & 1], 1);
     ctrl->abort = 0;
     mbar_fence_init();
     tma_prefetch_desc(&map_x);
@@ -370,6 +344,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tma_prefetch_desc(&map_b);
     }
     if (E.tma_y) tma_prefetch_desc(&map_y);
+    if (E.tma_y && E.res) tma_prefetch_desc(&map_r);
   }
   pdl_wait();
   __syncthreads();
@@ -471,8 +446,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     // epilogue: warps w and w + 4 share 32 rows and take chunks of 32 columns in turn
     const int quarter = warp & 3, side = warp >> 2;
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-    uint8_t* boxes = sm + P.off_stage + (size_t)warp * kBox;  // two of 32 rows x 64 bytes
-    int tc = 0, turn = 0;
+    // two sets of boxes of 32 rows x 64 bytes, for the chunks in turn: one box of bf16, two of fp32.  The
+    // residual's chunk is fetched into its set while the chunk before is worked on, is read from
+    // there and makes room for y's.  (Loaded into registers, a row a lane, it took 141 -> 147 us at
+    // 8192 x 4096 x 4096 and 37 -> 50 at 4096 x 2048 -> 6144 in e4m3.)
+    uint8_t* boxes = sm + P.off_stage + (size_t)warp * 2 * kSet;
+    const bool add = E.tma_y && E.res;
+    int tc = 0, chunk = 0, asked = 0;  // chunks done, and residual chunks on their way or taken
+    auto ask = [&](int32_t col, int32_t m0) {
+      if (lane == 0) {
+        bulk_wait_read<1>();  // the store before the last, from this set, has read it
+        uint64_t* bar = &ctrl->res_full[warp][asked & 1];
+        mbar_arrive_expect_tx(bar, kSet);
+        for (int q = 0; q < kParts; ++q)  // (past d_out there is nothing: zeros)
+          tma_load_2d(smem_u32(boxes + (asked & 1) * kSet + q * kBox), &map_r, col + q * 16, m0, bar);
+      }
+      ++asked;
+    };
     bool ok = true;
     for (int64_t pt = pair; pt < P.tiles && ok; pt += pairs) {
       int32_t m0, n0;
@@ -491,13 +481,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         cs[q] = in && E.sw ? E.sw[o] : 1.f;
         cb[q] = in && E.bias ? E.bias[o] : 0.f;
       }
-      if (E.res && E.tma_y && side == 0 && chunks > 0 && t < E.N) {
-        const uint32_t esize = E.y_bf16 ? 2 : 4;
+      if (add && side == 0 && chunks > 0 && t < E.N) {
+        const uint32_t esize = kY16 ? 2 : 4;
         prefetch_l2_bulk(static_cast<const uint8_t*>(E.res) + (t * E.d_out + n0) * esize,
                          (uint32_t)min(BN, E.d_out - n0) * esize);
       }
       // a chunk of 32 columns from its sums to y
-      auto finish = [&](int c, float (&v)[32], const Residual& res, bool add, auto next) {
+      auto finish = [&](int c, float (&v)[32]) {
         const int col = n0 + c * 32;
         if (E.sx && !kPromote) {
 #pragma unroll
@@ -511,32 +501,53 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int q = 0; q < 3; ++q) cs[q] = cs[q + 1], cb[q] = cb[q + 1];
         apply_act(v, E.act);
         if (E.tma_y) {
-          if (add) res.add(v, E.y_bf16);
-          next();
-          // 64 bytes of each row at a time: 32 columns of bf16, or 16 of fp32 twice
-#pragma unroll
-          for (int part = 0; part < 2; ++part) {
-            if (part && (E.y_bf16 || col + 16 >= E.d_out)) break;
-            uint8_t* box = boxes + turn * 2048;
-            turn ^= 1;
-            if (lane == 0) bulk_wait_read<1>();  // the store before the last, from this box, has read it
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int at = part * 16 + 4 * i;
-              *reinterpret_cast<uint4*>(box + swz_offset((uint32_t)lane, (uint32_t)i, 64)) =
-                  E.y_bf16 ? make_uint4(pack_bf16(v[8 * i], v[8 * i + 1]), pack_bf16(v[8 * i + 2], v[8 * i + 3]),
-                                        pack_bf16(v[8 * i + 4], v[8 * i + 5]), pack_bf16(v[8 * i + 6], v[8 * i + 7]))
-                           : make_uint4(__float_as_uint(v[at]), __float_as_uint(v[at + 1]), __float_as_uint(v[at + 2]),
-                                        __float_as_uint(v[at + 3]));
+          uint8_t* set = boxes + (chunk & 1) * kSet;
+          auto piece = [&](int i) { return set + (i >> 2) * kBox + swz_offset((uint32_t)lane, (uint32_t)i & 3u, 64); };
+          if (add) {
+            if (!__all_sync(0xffffffffu, mbar_wait(&ctrl->res_full[warp][chunk & 1], (uint32_t)(chunk >> 1) & 1u))) {
+              ok = false;
+              return;
             }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              tma_store_2d(&map_y, smem_u32(box), col + part * 16, m0);
-              bulk_commit();
+            uint4 q[4 * kParts];
+#pragma unroll
+            for (int i = 0; i < 4 * kParts; ++i) q[i] = *reinterpret_cast<const uint4*>(piece(i));
+#pragma unroll
+            for (int i = 0; i < 4 * kParts; ++i) {
+              const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                if constexpr (kY16) {
+                  v[8 * i + 2 * j] += __uint_as_float(w[j] << 16);
+                  v[8 * i + 2 * j + 1] += __uint_as_float(w[j] & 0xffff0000u);
+                } else {
+                  v[4 * i + j] += __uint_as_float(w[j]);
+                }
+              }
             }
+          } else {
+            if (lane == 0) bulk_wait_read<1>();  // the store before the last, from this set, has read it
+            __syncwarp();
           }
+#pragma unroll
+          for (int i = 0; i < 4 * kParts; ++i) {
+            uint4 q;
+            if constexpr (kY16)
+              q = make_uint4(pack_bf16(v[8 * i], v[8 * i + 1]), pack_bf16(v[8 * i + 2], v[8 * i + 3]),
+                             pack_bf16(v[8 * i + 4], v[8 * i + 5]), pack_bf16(v[8 * i + 6], v[8 * i + 7]));
+            else
+              q = make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]), __float_as_uint(v[4 * i + 2]),
+                             __float_as_uint(v[4 * i + 3]));
+            *reinterpret_cast<uint4*>(piece(i)) = q;
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            for (int q = 0; q < kParts && col + q * 16 < E.d_out; ++q)
+              tma_store_2d(&map_y, smem_u32(set + q * kBox), col + q * 16, m0);
+            bulk_commit();
+          }
+          ++chunk;
+          if (add && c + 2 < chunks) ask(col + 64, m0);
         } else {
           // rows that are not 16-byte aligned: turned in shared memory, written a row at a time
           float* turned = reinterpret_cast<float*>(boxes);
@@ -548,7 +559,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (col + lane >= E.d_out) continue;
             const int64_t at = ((int64_t)m0 + q) * E.d_out + col + lane;
             float o = turned[q * 32 + (lane ^ q)];
-            if (E.y_bf16) {
+            if constexpr (kY16) {
               if (E.res) o += to_float(static_cast<const __nv_bfloat16*>(E.res)[at]);
               static_cast<__nv_bfloat16*>(E.y)[at] = __float2bfloat16_rn(o);
             } else {
@@ -569,11 +580,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive_cluster(dsmem_addr(smem_u32(&ctrl->tempty[tc & 1]), 0));
         ++tc;
       };
-      const bool add = E.tma_y && E.res && t < E.N;
-      Residual res;  // a chunk ahead: its way from L2 is under the chunk before
-      auto load_residual = [&](int c) {
-        if (add && c < chunks) res.load(E.res, E.y_bf16, t * E.d_out + n0 + c * 32, E.d_out - n0 - c * 32);
-      };
+      if (add && side < chunks) ask(n0 + side * 32, m0);
       if constexpr (kPromote) {
         float acc[3][32];
         for (int first = 0; first < all; first = span_end(first)) {
@@ -599,28 +606,31 @@ __global__ void __launch_bounds__(kThreads, 1)
           free_sums();
         }
         if (!ok) break;
-        load_residual(side);
 #pragma unroll
         for (int q = 0; q < 3; ++q) {
           if (side + 2 * q >= chunks) continue;
-          finish(side + 2 * q, acc[q], res, add, [&] { load_residual(side + 2 * q + 2); });
+          if (ok) finish(side + 2 * q, acc[q]);
         }
       } else {
-        load_residual(side);
         const uint32_t base = wait_sums();
         if (!ok) break;
         uint32_t r[32];
         if (side < chunks) tmem_ld32_start(base + (uint32_t)(side * 32), r);
-        for (int c = side; c < chunks; c += 2) {
+        for (int c = side; c < chunks && ok; c += 2) {
           float v[32];
           tmem_ld_wait(r);
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
           if (c + 2 < chunks) tmem_ld32_start(base + (uint32_t)((c + 2) * 32), r);
-          finish(c, v, res, add, [&] { load_residual(c + 2); });
+          finish(c, v);
         }
         free_sums();
       }
+    }
+    if (!ok) {
+      if (asked > chunk) mbar_wait(&ctrl->res_full[warp][chunk & 1], (uint32_t)(chunk >> 1) & 1u);
+      *abort = 1;
+      if (lane == 0) report(err_word, MOLORA_DEV_WAIT_TIMEOUT);
     }
     if (lane == 0) bulk_wait_all();
     __syncwarp();
@@ -1252,11 +1262,11 @@ cudaError_t launch_tc(const LinearArgs& a, int BN, bool promote, const LinearUpd
   p.off_b = kRows * kRowBytes;
   p.stage_bytes = p.off_b + (uint32_t)(BN / 2) * kRowBytes;
   p.tmem_cols = tmem_columns(2 * (uint32_t)(BN <= 64 ? 64 : BN <= 128 ? 128 : 256));
-  const size_t fixed = kEpiWarps * kBox + sizeof(LCtrl) + kSmemSlack;
+  const size_t boxes = kEpiWarps * 2 * (a.y_bf16 ? kBox : 2 * kBox), fixed = boxes + sizeof(LCtrl) + kSmemSlack;
   p.S = (int)((kMaxSmem - fixed) / p.stage_bytes);
   if (p.S > kMaxStages) p.S = kMaxStages;
   p.off_stage = (uint32_t)p.S * p.stage_bytes;
-  p.off_ctrl = p.off_stage + kEpiWarps * kBox;
+  p.off_ctrl = p.off_stage + (uint32_t)boxes;
   // one CTA an SM, alone: an allocation of TMEM never waits for another CTA's, which could in turn
   // be waiting for a partner that this kernel's other CTAs keep out
   p.smem = kMaxSmem;
@@ -1269,18 +1279,24 @@ cudaError_t launch_tc(const LinearArgs& a, int BN, bool promote, const LinearUpd
             !linear_map(&glo, BF, 2, u->g_lo, (uint64_t)a.N, (uint64_t)u->KR, 64, kRows, CU_TENSOR_MAP_SWIZZLE_128B) ||
             !linear_map(&mb, BF, 2, u->B, (uint64_t)u->KR, (uint64_t)a.d_out, 16, 64, CU_TENSOR_MAP_SWIZZLE_32B)))
     return cudaErrorNotSupported;
-  if (e.tma_y &&
-      !linear_map(&my, a.y_bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, a.y_bf16 ? 2 : 4,
-                  a.y, (uint64_t)a.N, (uint64_t)a.d_out, a.y_bf16 ? 32 : 16, 32, CU_TENSOR_MAP_SWIZZLE_64B))
-    e.tma_y = false;
-  auto kernel = fp8 ? (promote ? linear_tc_kernel<true, true> : linear_tc_kernel<true, false>)
-                    : (promote ? linear_tc_kernel<false, true> : linear_tc_kernel<false, false>);
-  static std::atomic<uint64_t> allowed[4];
-  const cudaError_t set = allow_smem(kernel, allowed[2 * fp8 + promote], kMaxSmem);
+  CUtensorMap mr = {};
+  auto rows_map = [&](CUtensorMap* m, const void* base) {
+    return linear_map(m, a.y_bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, a.y_bf16 ? 2 : 4, base,
+                      (uint64_t)a.N, (uint64_t)a.d_out, a.y_bf16 ? 32 : 16, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+  };
+  if (e.tma_y && (!rows_map(&my, a.y) || (a.residual && !rows_map(&mr, a.residual)))) e.tma_y = false;
+  const bool y16 = a.y_bf16;
+  auto kernel = fp8 ? promote ? y16 ? linear_tc_kernel<true, true, true> : linear_tc_kernel<true, true, false>
+                              : y16 ? linear_tc_kernel<true, false, true> : linear_tc_kernel<true, false, false>
+                : promote ? linear_tc_kernel<false, true, false>  // (for fp32 y only)
+                          : y16 ? linear_tc_kernel<false, false, true> : linear_tc_kernel<false, false, false>;
+  static std::atomic<uint64_t> allowed[8];
+  const cudaError_t set = allow_smem(kernel, allowed[4 * fp8 + 2 * promote + y16], kMaxSmem);
   if (set != cudaSuccess) return set;
   const int64_t most = num_sms() / 2;
   const dim3 grid((unsigned)(2 * (p.tiles < most ? p.tiles : most)));
-  return launch_kernel(kernel, grid, dim3(kThreads), p.smem, stream, 2, e, p, a.err_word, mx, mw, my, ghi, glo, mb);
+  return launch_kernel(kernel, grid, dim3(kThreads), p.smem, stream, 2, e, p, a.err_word, mx, mw, my, ghi, glo, mb,
+                       mr);
 }
 
 // Cycles that linear_skinny_kernel takes in tiles of BN tokens, and linear_tc_kernel in tiles of BN outputs, as
