@@ -45,6 +45,7 @@ constexpr int kAnyThreads = 512;    // linear_any_kernel: 15 warps that lay out 
 constexpr int kCutters = kAnyThreads - 32;
 constexpr int kMaxStages = 12;
 constexpr int kSpan = 8;            // K blocks summed in TMEM before fp32 registers take over
+constexpr uint32_t kTurn = 4096;    // 32 x 32 values of fp32 y
 constexpr size_t kMaxSmem = 227 * 1024;
 constexpr size_t kSmemSlack = 1024;
 constexpr uint32_t kBox = 2048;     // of the epilogue's staging: 32 rows x 64 bytes
@@ -55,7 +56,7 @@ struct __align__(8) LCtrl {
   uint64_t tfull[2];
   uint64_t tempty[2];
   uint64_t done;
-  uint64_t res_full[kEpiWarps][2];
+  uint64_t res_full[12];
   uint32_t tmem_base;
   int32_t abort;
   int32_t odd;  // an infinite or NaN fp32 operand was seen
@@ -280,19 +281,24 @@ __device__ __forceinline__ void split_epilogue(const Epi& E, const TileSums<J>& 
 
 }  // namespace
 
+// linear_tc_kernel's epilogue: groups of 4 warps that share a tile's chunks, and the CTA's threads.
+constexpr int tc_sides(bool fp8, bool promote) { return promote ? 2 : 3; }
+constexpr int tc_threads(bool fp8, bool promote) { return 32 * (4 * tc_sides(fp8, promote) + 2); }
+
 // kPromote: a tensor core cuts what its sums lose in an addition, always towards zero, so a long chain of
 // MMAs drifts: 256 of them (d_in = 4096) leave an fp32 result 4e-6 short, 40 times what rounding
 // would.  For fp32 y the epilogue warps take the sums of every 8 K blocks (32 MMAs) into registers
 // and add there.  With e4m3 operands it takes the adapters' update along: the product's sums are
 // scaled in registers before the update's, which have no scales, are added.
 template <bool kFp8, bool kPromote, bool kY16>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(tc_threads(kFp8, kPromote), 1)
     linear_tc_kernel(const Epi E, const TcPlan P, int32_t* err_word, const __grid_constant__ CUtensorMap map_x,
                      const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_y,
                      const __grid_constant__ CUtensorMap map_ghi, const __grid_constant__ CUtensorMap map_glo,
                      const __grid_constant__ CUtensorMap map_b, const __grid_constant__ CUtensorMap map_r) {
   constexpr int kParts = kY16 ? 1 : 2;  // boxes of a chunk of 32 columns of y
   constexpr uint32_t kSet = kParts * kBox;
+  constexpr int kSides = tc_sides(kFp8, kPromote), kWarps = 4 * kSides, kMine = (8 + kSides - 1) / kSides;  // chunks a warp
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   LCtrl* ctrl = reinterpret_cast<LCtrl*>(sm + P.off_ctrl);
@@ -319,21 +325,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     n0 = (int32_t)(in / rows) * BN;
   };
 
-  if (warp == 9) {
+  if (warp == kWarps + 1) {
     tmem_alloc_pair(&ctrl->tmem_base, P.tmem_cols);
     tmem_relinquish_pair();
   }
-  if (warp == 8 && lane == 0) {
+  if (warp == kWarps && lane == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(&ctrl->full[s], 1);
       mbar_init(&ctrl->empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&ctrl->tfull[b], 1);
-      mbar_init(&ctrl->tempty[b], 2 * kEpiWarps);
+      mbar_init(&ctrl->tempty[b], 2 * kWarps);
     }
     mbar_init(&ctrl->done, 1);
-    for (int b = 0; b < 2 * kEpiWarps; ++b) mbar_init(&ctrl->res_full[b / 2][b & 1], 1);
+    for (int b = 0; b < kWarps; ++b) mbar_init(&ctrl->res_full[b], 1);
     ctrl->abort = 0;
     mbar_fence_init();
     tma_prefetch_desc(&map_x);
@@ -354,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = ctrl->tmem_base;
   cluster_sync();  // every CTA's barriers are initialised before another signals them
 
-  if (warp == 8) {
+  if (warp == kWarps) {
     if (elect_one()) {
       const int elems = kFp8 ? 128 : 64;  // K elements per stage
       int s = 0, issued = 0;
@@ -398,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp == 9) {
+  } else if (warp == kWarps + 1) {
     if (rank == 0 && elect_one()) {
       const uint32_t idesc = kFp8 ? idesc_e4m3_f32(2 * kRows, (uint32_t)BN) : idesc_bf16_f32(2 * kRows, (uint32_t)BN, false, false);
       // descriptors of stage 0: K-major operands of 128-byte rows, and the update's B (see the TMA warp)
@@ -443,23 +449,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else {
-    // epilogue: warps w and w + 4 share 32 rows and take chunks of 32 columns in turn
+    // epilogue: warps w, w + 4, ... share 32 rows and take chunks of 32 columns in turn
     const int quarter = warp & 3, side = warp >> 2;
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-    // two sets of boxes of 32 rows x 64 bytes, for the chunks in turn: one box of bf16, two of fp32.  The
-    // residual's chunk is fetched into its set while the chunk before is worked on, is read from
-    // there and makes room for y's.  (Loaded into registers, a row a lane, it took 141 -> 147 us at
-    // 8192 x 4096 x 4096 and 37 -> 50 at 4096 x 2048 -> 6144 in e4m3.)
-    uint8_t* boxes = sm + P.off_stage + (size_t)warp * 2 * kSet;
+    // y leaves through boxes of 32 rows x 64 bytes: one of bf16, two of fp32.  The residual's chunk is fetched
+    // into them while the chunk's sums are awaited and worked on, is read from there and makes room for
+    // y's.  (Loaded into registers, a row a lane, it took fp32 y from 230 to 310 us at 8192 x 4096 x 4096,
+    // now to 250.)  One set of boxes a warp: the store before has long read it, and a second would take
+    // a stage from the ring (140 -> 145 us).
+    uint8_t* set = sm + P.off_stage + (size_t)warp * kSet;
     const bool add = E.tma_y && E.res;
     int tc = 0, chunk = 0, asked = 0;  // chunks done, and residual chunks on their way or taken
     auto ask = [&](int32_t col, int32_t m0) {
       if (lane == 0) {
-        bulk_wait_read<1>();  // the store before the last, from this set, has read it
-        uint64_t* bar = &ctrl->res_full[warp][asked & 1];
-        mbar_arrive_expect_tx(bar, kSet);
+        bulk_wait_read<0>();  // the last store has read the boxes
+        mbar_arrive_expect_tx(&ctrl->res_full[warp], kSet);
         for (int q = 0; q < kParts; ++q)  // (past d_out there is nothing: zeros)
-          tma_load_2d(smem_u32(boxes + (asked & 1) * kSet + q * kBox), &map_r, col + q * 16, m0, bar);
+          tma_load_2d(smem_u32(set + q * kBox), &map_r, col + q * 16, m0, &ctrl->res_full[warp]);
       }
       ++asked;
     };
@@ -473,11 +479,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int chunks = m0 < E.N ? min(BN / 32, (E.d_out - n0 + 31) / 32) : 0;
       // while the tile's MMAs run: this lane's column of each of its chunks' scales and biases, which a
       // chunk's rows get by shuffles, and the residual's rows on their way to L2
-      float cs[4], cb[4];
+      float cs[kMine], cb[kMine];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int o = n0 + (side + 2 * q) * 32 + lane;
-        const bool in = side + 2 * q < chunks && o < E.d_out;
+      for (int q = 0; q < kMine; ++q) {
+        const int o = n0 + (side + kSides * q) * 32 + lane;
+        const bool in = side + kSides * q < chunks && o < E.d_out;
         cs[q] = in && E.sw ? E.sw[o] : 1.f;
         cb[q] = in && E.bias ? E.bias[o] : 0.f;
       }
@@ -489,6 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // a chunk of 32 columns from its sums to y
       auto finish = [&](int c, float (&v)[32]) {
         const int col = n0 + c * 32;
+        if (add && asked == chunk) ask(col, m0);
         if (E.sx && !kPromote) {
 #pragma unroll
           for (int i = 0; i < 32; ++i)
@@ -498,13 +505,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < 32; ++i) v[i] += __shfl_sync(0xffffffffu, cb[0], i);
         }
 #pragma unroll
-        for (int q = 0; q < 3; ++q) cs[q] = cs[q + 1], cb[q] = cb[q + 1];
+        for (int q = 0; q < kMine - 1; ++q) cs[q] = cs[q + 1], cb[q] = cb[q + 1];
         apply_act(v, E.act);
         if (E.tma_y) {
-          uint8_t* set = boxes + (chunk & 1) * kSet;
           auto piece = [&](int i) { return set + (i >> 2) * kBox + swz_offset((uint32_t)lane, (uint32_t)i & 3u, 64); };
           if (add) {
-            if (!__all_sync(0xffffffffu, mbar_wait(&ctrl->res_full[warp][chunk & 1], (uint32_t)(chunk >> 1) & 1u))) {
+            if (!__all_sync(0xffffffffu, mbar_wait(&ctrl->res_full[warp], (uint32_t)chunk & 1u))) {
               ok = false;
               return;
             }
@@ -525,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           } else {
-            if (lane == 0) bulk_wait_read<1>();  // the store before the last, from this set, has read it
+            if (lane == 0) bulk_wait_read<0>();  // the last store has read the boxes
             __syncwarp();
           }
 #pragma unroll
@@ -547,10 +553,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             bulk_commit();
           }
           ++chunk;
-          if (add && c + 2 < chunks) ask(col + 64, m0);
         } else {
           // rows that are not 16-byte aligned: turned in shared memory, written a row at a time
-          float* turned = reinterpret_cast<float*>(boxes);
+          float* turned = reinterpret_cast<float*>(sm + P.off_stage + (size_t)warp * kTurn);
           __syncwarp();
 #pragma unroll
           for (int i = 0; i < 32; ++i) turned[lane * 32 + (i ^ lane)] = v[i];
@@ -588,9 +593,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
 #pragma unroll
           for (int q = 0; q < 3; ++q) {
-            if (side + 2 * q >= chunks) continue;
+            if (side + kSides * q >= chunks) continue;
             uint32_t r[32];
-            tmem_ld32_start(base + (uint32_t)((side + 2 * q) * 32), r);
+            tmem_ld32_start(base + (uint32_t)((side + kSides * q) * 32), r);
             tmem_ld_wait(r);
             if (first) {
 #pragma unroll
@@ -608,37 +613,37 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
 #pragma unroll
         for (int q = 0; q < 3; ++q) {
-          if (side + 2 * q >= chunks) continue;
-          if (ok) finish(side + 2 * q, acc[q]);
+          if (side + kSides * q >= chunks) continue;
+          if (ok) finish(side + kSides * q, acc[q]);
         }
       } else {
         const uint32_t base = wait_sums();
         if (!ok) break;
         uint32_t r[32];
         if (side < chunks) tmem_ld32_start(base + (uint32_t)(side * 32), r);
-        for (int c = side; c < chunks && ok; c += 2) {
+        for (int c = side; c < chunks && ok; c += kSides) {
           float v[32];
           tmem_ld_wait(r);
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-          if (c + 2 < chunks) tmem_ld32_start(base + (uint32_t)((c + 2) * 32), r);
+          if (c + kSides < chunks) tmem_ld32_start(base + (uint32_t)((c + kSides) * 32), r);
           finish(c, v);
         }
         free_sums();
       }
     }
     if (!ok) {
-      if (asked > chunk) mbar_wait(&ctrl->res_full[warp][chunk & 1], (uint32_t)(chunk >> 1) & 1u);
+      if (asked > chunk) mbar_wait(&ctrl->res_full[warp], (uint32_t)chunk & 1u);
       *abort = 1;
       if (lane == 0) report(err_word, MOLORA_DEV_WAIT_TIMEOUT);
     }
     if (lane == 0) bulk_wait_all();
     __syncwarp();
   }
-  if (warp == 9 && lane == 0) mbar_wait(&ctrl->done, 0);
+  if (warp == kWarps + 1 && lane == 0) mbar_wait(&ctrl->done, 0);
   __syncthreads();
   cluster_sync();  // neither CTA leaves, nor frees its TMEM, while the other may still signal or use it
-  if (warp == 9) {
+  if (warp == kWarps + 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, P.tmem_cols);
   }
@@ -1262,15 +1267,21 @@ cudaError_t launch_tc(const LinearArgs& a, int BN, bool promote, const LinearUpd
   p.off_b = kRows * kRowBytes;
   p.stage_bytes = p.off_b + (uint32_t)(BN / 2) * kRowBytes;
   p.tmem_cols = tmem_columns(2 * (uint32_t)(BN <= 64 ? 64 : BN <= 128 ? 128 : 256));
-  const size_t boxes = kEpiWarps * 2 * (a.y_bf16 ? kBox : 2 * kBox), fixed = boxes + sizeof(LCtrl) + kSmemSlack;
+  CUtensorMap mx, mw, my = {}, mr = {};
+  auto rows_map = [&](CUtensorMap* m, const void* base) {
+    return linear_map(m, a.y_bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, a.y_bf16 ? 2 : 4, base,
+                      (uint64_t)a.N, (uint64_t)a.d_out, a.y_bf16 ? 32 : 16, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+  };
+  if (e.tma_y && (!rows_map(&my, a.y) || (a.residual && !rows_map(&mr, a.residual)))) e.tma_y = false;
+  const uint32_t boxes = 4 * tc_sides(fp8, promote) * (e.tma_y && a.y_bf16 ? kBox : kTurn);
+  const size_t fixed = boxes + sizeof(LCtrl) + kSmemSlack;
   p.S = (int)((kMaxSmem - fixed) / p.stage_bytes);
   if (p.S > kMaxStages) p.S = kMaxStages;
   p.off_stage = (uint32_t)p.S * p.stage_bytes;
-  p.off_ctrl = p.off_stage + (uint32_t)boxes;
+  p.off_ctrl = p.off_stage + boxes;
   // one CTA an SM, alone: an allocation of TMEM never waits for another CTA's, which could in turn
   // be waiting for a partner that this kernel's other CTAs keep out
   p.smem = kMaxSmem;
-  CUtensorMap mx, mw, my = {};
   if (!operand_map(&mx, a, a.x, a.N, kRows) || !operand_map(&mw, a, a.W, a.d_out, (uint32_t)(BN / 2)))
     return cudaErrorNotSupported;
   const auto BF = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
@@ -1279,12 +1290,6 @@ cudaError_t launch_tc(const LinearArgs& a, int BN, bool promote, const LinearUpd
             !linear_map(&glo, BF, 2, u->g_lo, (uint64_t)a.N, (uint64_t)u->KR, 64, kRows, CU_TENSOR_MAP_SWIZZLE_128B) ||
             !linear_map(&mb, BF, 2, u->B, (uint64_t)u->KR, (uint64_t)a.d_out, 16, 64, CU_TENSOR_MAP_SWIZZLE_32B)))
     return cudaErrorNotSupported;
-  CUtensorMap mr = {};
-  auto rows_map = [&](CUtensorMap* m, const void* base) {
-    return linear_map(m, a.y_bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, a.y_bf16 ? 2 : 4, base,
-                      (uint64_t)a.N, (uint64_t)a.d_out, a.y_bf16 ? 32 : 16, 32, CU_TENSOR_MAP_SWIZZLE_64B);
-  };
-  if (e.tma_y && (!rows_map(&my, a.y) || (a.residual && !rows_map(&mr, a.residual)))) e.tma_y = false;
   const bool y16 = a.y_bf16;
   auto kernel = fp8 ? promote ? y16 ? linear_tc_kernel<true, true, true> : linear_tc_kernel<true, true, false>
                               : y16 ? linear_tc_kernel<true, false, true> : linear_tc_kernel<true, false, false>
@@ -1295,7 +1300,7 @@ cudaError_t launch_tc(const LinearArgs& a, int BN, bool promote, const LinearUpd
   if (set != cudaSuccess) return set;
   const int64_t most = num_sms() / 2;
   const dim3 grid((unsigned)(2 * (p.tiles < most ? p.tiles : most)));
-  return launch_kernel(kernel, grid, dim3(kThreads), p.smem, stream, 2, e, p, a.err_word, mx, mw, my, ghi, glo, mb,
+  return launch_kernel(kernel, grid, dim3(tc_threads(fp8, promote)), p.smem, stream, 2, e, p, a.err_word, mx, mw, my, ghi, glo, mb,
                        mr);
 }
 
