@@ -10,11 +10,11 @@
 // linear_tc_kernel (many tokens): a persistent kernel over tiles of 256 tokens x BN outputs, each made
 //   by a pair of CTAs with cta_group::2 MMAs.  Each CTA loads its 128 token rows and half of the
 //   tile's W rows: a pair reads every operand byte once from shared memory per MMA, which
-//   one CTA alone cannot feed at full rate.  A TMA warp and an MMA warp run ahead of 8 epilogue
-//   warps by two TMEM accumulators.  Bound by the tensor cores: 8192 x 4096 x 4096 bf16 141 us (1950
-//   TFLOP/s; tensor pipe active in 89% of the cycles), 150 with bias, SiLU and residual; e4m3 76 us
-//   (3600).  4096 x 2048 x 6144 e4m3 with scales, bias and GELU 42 us, 36 without: there the epilogue of
-//   224 columns is nearly as long as a tile's 16 K blocks.
+//   one CTA alone cannot feed at full rate.  A TMA warp and an MMA warp run ahead of 12 (or 8, see
+//   tc_sides) epilogue warps by two TMEM accumulators.  Bound by the tensor cores: 8192 x 4096 x 4096 bf16
+//   142 us (1940 TFLOP/s; tensor pipe active in 89% of the cycles), 148 with bias, SiLU and residual; e4m3
+//   78 us (3500).  4096 x 2048 x 6144 e4m3 with scales, bias and GELU's tanh form 40 us, 36 without: there
+//   the epilogue of 224 columns is nearly as long as a tile's 16 K blocks.
 // linear_skinny_kernel (few tokens): W's rows are the MMA's M (128 outputs a CTA), the tokens its N
 //   (16 .. 256), so that no MMA row is spent on tokens that are not there; d_in is split over a
 //   cluster of CTAs whose partial sums meet through distributed shared memory in rank order.  Bound by
@@ -43,7 +43,9 @@ constexpr int kEpiWarps = 8;
 constexpr int kThreads = 32 * (kEpiWarps + 2);  // + TMA warp (8) + MMA warp (9)
 constexpr int kAnyThreads = 512;    // linear_any_kernel: 15 warps that lay out operands + MMA warp (15)
 constexpr int kCutters = kAnyThreads - 32;
-constexpr int kMaxStages = 12;
+// More bytes in flight take longer to come: one token, 4096 x 4096 bf16 from HBM 9.4 us with 4 stages, 8.8
+// with 8, 10.0 with 12 (from L2 7.1, 7.4, 8.2).
+constexpr int kMaxStages = 8;
 constexpr int kSpan = 8;            // K blocks summed in TMEM before fp32 registers take over
 constexpr uint32_t kTurn = 4096;    // 32 x 32 values of fp32 y
 constexpr size_t kMaxSmem = 227 * 1024;
@@ -281,9 +283,12 @@ __device__ __forceinline__ void split_epilogue(const Epi& E, const TileSums<J>& 
 
 }  // namespace
 
-// linear_tc_kernel's epilogue: groups of 4 warps that share a tile's chunks, and the CTA's threads.
-constexpr int tc_sides(bool fp8, bool promote) { return promote ? 2 : 3; }
-constexpr int tc_threads(bool fp8, bool promote) { return 32 * (4 * tc_sides(fp8, promote) + 2); }
+// linear_tc_kernel's epilogue: groups of 4 warps that share a tile's chunks, and the CTA's threads.  Three groups
+// where a chunk's registers allow it: 8192 x 1024 -> 4096 e4m3 with two 43 us, with three 39, and with GELU 56
+// and 52; 4096 x 1024 -> 4096 bf16 with GELU's tanh form 34 and 31.  Where K is long the tensor cores bound both
+// (8192 x 4096 x 4096 bf16 141 and 142).
+constexpr int tc_sides(bool promote) { return promote ? 2 : 3; }
+constexpr int tc_threads(bool promote) { return 32 * (4 * tc_sides(promote) + 2); }
 
 // kPromote: a tensor core cuts what its sums lose in an addition, always towards zero, so a long chain of
 // MMAs drifts: 256 of them (d_in = 4096) leave an fp32 result 4e-6 short, 40 times what rounding
@@ -291,14 +296,14 @@ constexpr int tc_threads(bool fp8, bool promote) { return 32 * (4 * tc_sides(fp8
 // and add there.  With e4m3 operands it takes the adapters' update along: the product's sums are
 // scaled in registers before the update's, which have no scales, are added.
 template <bool kFp8, bool kPromote, bool kY16>
-__global__ void __launch_bounds__(tc_threads(kFp8, kPromote), 1)
+__global__ void __launch_bounds__(tc_threads(kPromote), 1)
     linear_tc_kernel(const Epi E, const TcPlan P, int32_t* err_word, const __grid_constant__ CUtensorMap map_x,
                      const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_y,
                      const __grid_constant__ CUtensorMap map_ghi, const __grid_constant__ CUtensorMap map_glo,
                      const __grid_constant__ CUtensorMap map_b, const __grid_constant__ CUtensorMap map_r) {
   constexpr int kParts = kY16 ? 1 : 2;  // boxes of a chunk of 32 columns of y
   constexpr uint32_t kSet = kParts * kBox;
-  constexpr int kSides = tc_sides(kFp8, kPromote), kWarps = 4 * kSides, kMine = (8 + kSides - 1) / kSides;  // chunks a warp
+  constexpr int kSides = tc_sides(kPromote), kWarps = 4 * kSides, kMine = (8 + kSides - 1) / kSides;  // chunks a warp
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   LCtrl* ctrl = reinterpret_cast<LCtrl*>(sm + P.off_ctrl);
@@ -966,7 +971,7 @@ struct Piece<__nv_fp8_e4m3, kVec> {
 // seen one sums its outputs again on the CUDA cores.
 //
 // Bound by the threads that cut the operands: 15 warps, with their next pieces on the way while a stage is
-// written and handed over.  1024 x 4096 x 4096 fp32 367 us (94 TFLOP/s, 577 us for the library's fp32 product);
+// written and handed over.  1024 x 4096 x 4096 fp32 343 us (100 TFLOP/s, 577 us for the library's fp32 product);
 // of 5400 cycles a K block, the MMAs are 1500 and the operands' way from L2 1000.
 template <typename T, bool kVec, int J>
 __global__ void __launch_bounds__(kAnyThreads, 1)
@@ -1273,7 +1278,7 @@ cudaError_t launch_tc(const LinearArgs& a, int BN, bool promote, const LinearUpd
                       (uint64_t)a.N, (uint64_t)a.d_out, a.y_bf16 ? 32 : 16, 32, CU_TENSOR_MAP_SWIZZLE_64B);
   };
   if (e.tma_y && (!rows_map(&my, a.y) || (a.residual && !rows_map(&mr, a.residual)))) e.tma_y = false;
-  const uint32_t boxes = 4 * tc_sides(fp8, promote) * (e.tma_y && a.y_bf16 ? kBox : kTurn);
+  const uint32_t boxes = 4 * tc_sides(promote) * (e.tma_y && a.y_bf16 ? kBox : kTurn);
   const size_t fixed = boxes + sizeof(LCtrl) + kSmemSlack;
   p.S = (int)((kMaxSmem - fixed) / p.stage_bytes);
   if (p.S > kMaxStages) p.S = kMaxStages;
@@ -1300,14 +1305,14 @@ cudaError_t launch_tc(const LinearArgs& a, int BN, bool promote, const LinearUpd
   if (set != cudaSuccess) return set;
   const int64_t most = num_sms() / 2;
   const dim3 grid((unsigned)(2 * (p.tiles < most ? p.tiles : most)));
-  return launch_kernel(kernel, grid, dim3(tc_threads(fp8, promote)), p.smem, stream, 2, e, p, a.err_word, mx, mw, my, ghi, glo, mb,
+  return launch_kernel(kernel, grid, dim3(tc_threads(promote)), p.smem, stream, 2, e, p, a.err_word, mx, mw, my, ghi, glo, mb,
                        mr);
 }
 
 // Cycles that linear_skinny_kernel takes in tiles of BN tokens, and linear_tc_kernel in tiles of BN outputs, as
 // measured on GB300 with 64 to 6144 outputs, d_in 1024 to 4096 and 1 to 4096 tokens (within 20%): what
 // a K block takes, a join or a last epilogue that grows with the tile, and the way through.  The split
-// product is 7.7 us for 16 tokens of 4096 x 4096, 16.5 for 256 and 23.4 for 512, the pairs' 16.6, 17.1 and 17.6.
+// product is 7.7 us for 16 tokens of 4096 x 4096, 16.4 for 256 and 23.4 for 512, the pairs' 16.6, 17.1 and 17.5.
 int64_t skinny_cycles(const LinearArgs& a, const Resident& r, int BN) {
   const int64_t tiles = (((int64_t)a.d_out + kRows - 1) / kRows) * ((a.N + BN - 1) / BN);
   const int nkb = k_blocks(a), C = split_of(r, tiles, nkb);
@@ -1435,14 +1440,16 @@ cudaError_t launch_linear(const LinearArgs& a, cudaStream_t stream, const Linear
   const Resident r = resident_clusters();
   int best = 128, split = 0;
   int64_t cost = INT64_MAX;
-  for (int BN : {256, 224, 192, 160, 128, 96, 64}) {
-    const int64_t c = promote && BN > 192 ? INT64_MAX : tc_cycles(a, r, BN, blocks);
-    if (c < cost) cost = c, best = BN;
-  }
   for (int BN : {16, 32, 64, 128, 256}) {
-    if (update || (BN > 16 && BN / 2 >= a.N)) continue;
+    if (update || (BN > 16 && BN / 2 >= a.N)) break;
     const int64_t c = skinny_cycles(a, r, BN);
     if (c < cost) cost = c, split = BN;
+  }
+  // up to 32 tokens the pairs' 256 rows were never faster, and the call is the host's
+  for (int BN : {256, 224, 192, 160, 128, 96, 64}) {
+    if ((split && a.N <= 32) || (promote && BN > 192)) continue;
+    const int64_t c = tc_cycles(a, r, BN, blocks);
+    if (c < cost) cost = c, best = BN, split = 0;
   }
 #ifdef MOLORA_TUNING_ENV
   if (const char* g = getenv("MOLORA_LIN_BN")) best = atoi(g);
