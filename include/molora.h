@@ -470,7 +470,7 @@ MOLORA_API molora_status molora_lora_apply_masked_pass(const void* x, molora_dty
  * that row included; so do rows whose squares overflow fp32 where s is infinite, and give 0
  * where it is not.
  *
- * x        [N x d] dtype (MOLORA_BF16 or MOLORA_F32);  d >= 1
+ * x        [N x d] dtype (MOLORA_BF16 or MOLORA_F32);  d >= 1, N and d up to 2^31 - 1024
  * residual [N x d] dtype, or NULL
  * sum_out  [N x d] dtype, or NULL; needs residual
  * weight   [d] dtype
@@ -478,7 +478,7 @@ MOLORA_API molora_status molora_lora_apply_masked_pass(const void* x, molora_dty
  * out      [N x d] dtype, or NULL;  out8 [N x d] e4m3 and scale8 fp32 [N], both or neither; out
  *          or out8 is needed
  * In place: each of sum_out and out may be x or residual itself (not both the same one); any
- * other overlap of an output with another array is not allowed.
+ * other overlap of an output with another array is refused.
  * One kernel, no workspace; results are reproducible bit for bit.
  */
 MOLORA_API molora_status molora_rmsnorm(const void* x, molora_dtype dtype, int64_t N, int32_t d, const void* residual,
@@ -512,6 +512,7 @@ MOLORA_API molora_status molora_rmsnorm(const void* x, molora_dtype dtype, int64
  * groups 1..MOLORA_MAX_GROUPS, a divisor of K with K / groups >= group_top;  keep_groups
  *        1..groups;  k 1..MOLORA_MAX_GATE_K, at most keep_groups * K / groups;  scale finite
  * ids int32 [N x k], w fp32 [N x k]: outputs, in molora_dispatch's and molora_lora_apply's form
+ * (sharing memory with no other array)
  */
 MOLORA_API molora_status molora_gate_topk(const void* logits, molora_dtype dtype, int64_t N, int32_t K, molora_score score,
                                const float* bias, int32_t groups, int32_t keep_groups, int32_t group_top,
@@ -528,8 +529,9 @@ MOLORA_API molora_status molora_gate_topk(const void* logits, molora_dtype dtype
  * dtype: MOLORA_BF16, MOLORA_F32 or MOLORA_E4M3.  x_scale fp32 [N] and w_scale fp32 [d_out]: both
  * needed with MOLORA_E4M3 (x, x_scale as molora_rmsnorm's out8, scale8), both NULL otherwise.
  * bias fp32 [d_out] or NULL;  residual [N x d_out] of y's type or NULL, y itself allowed;
- * y fp32 (y_bf16 = 0) or bf16 (y_bf16 = 1) [N x d_out], overwritten.
- * Products are summed in fp32; the epilogue is fp32 and y is rounded once.  Any d_in, d_out >= 1; arrays
+ * y fp32 (y_bf16 = 0) or bf16 (y_bf16 = 1) [N x d_out], overwritten; it may share no memory
+ * with the other arrays (refused).
+ * Products are summed in fp32; the epilogue is fp32 and y is rounded once.  Any N, d_in, d_out up to 2^31 - 1024; arrays
  * start on a boundary of their element's size (rows on 16-byte boundaries are faster).  Results are
  * reproducible bit for bit.  A wait that ran out (MOLORA_DEV_WAIT_TIMEOUT) leaves its tile of y unwritten.
  */
@@ -549,7 +551,8 @@ MOLORA_API molora_status molora_linear(const void* x, molora_dtype dtype, const 
  * x, residual, sum_out, norm_weight, h [N x d_in], A and B: dtype, h and the others as in the three
  * calls; sum_out needs residual, both may be NULL.  w_dtype is dtype or MOLORA_E4M3; h8 [N x d_in], scale8 fp32 [N] and
  * w_scale fp32 [d_out] are needed with MOLORA_E4M3 and must be NULL otherwise.  h is an output: a
- * layer's other projections read it too.  y is overwritten: fp32 (y_bf16 = 0) or bf16 (y_bf16 = 1,
+ * layer's other projections read it too.  y shares memory with none
+ * of h, h8, sum_out, W, A and B (refused), and is overwritten: fp32 (y_bf16 = 0) or bf16 (y_bf16 = 1,
  * with molora_lora_apply_bf16y's roundings).  ids, w, k, counts, offsets, perm and ws, ws_bytes as for
  * molora_lora_apply; a query sizes the path this call prefers.
  * Given a workspace, more than 256 tokens, bf16 dtype and K*r <= 512, the product takes the adapters' update

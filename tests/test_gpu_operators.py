@@ -628,6 +628,32 @@ def test_layer_skips_slots_without_an_adapter(m, N):
     within(y, want, 2e-4 * want.pow(2).mean().sqrt().item())
 
 
+@pytest.mark.parametrize("y_dtype", [BF, F32])
+def test_buffers_of_a_call_on_another_stream(m, y_dtype):
+    """What a call on a given stream makes for itself stays its own until that stream is done: buffers
+    made and dropped on the current stream meanwhile get other memory."""
+    g = gen(37)
+    N, d, K, r = 600, 512, 4, 16
+    x, _, nw, W, sw, A, B, Wg, _ = layer(g, N, d, d, K, r, 2, True)
+    ids, w = m.molora_gate_topk(m.molora_linear(x, Wg), 2)
+    want = torch.empty(N, d, device="cuda", dtype=y_dtype)
+    m.molora_norm_linear_lora_apply(x, nw, 1e-6, W, A, B, ids, want, 2.0, w=w, w_scale=sw)
+    y = torch.empty_like(want)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        torch.cuda._sleep(50_000_000)           # the call's kernels wait for this
+    m.molora_norm_linear_lora_apply(x, nw, 1e-6, W, A, B, ids, y, 2.0, w=w, w_scale=sw, stream=st)
+    h = m.molora_rmsnorm(x, nw, stream=st)[1]
+    logits = m.molora_linear(h, Wg, stream=st)
+    others = [torch.full((n,), 255, dtype=torch.uint8, device="cuda") for n in (N * d * 2, N * d, N * 4, N * K * r * 4) * 4]
+    st.synchronize()
+    assert torch.equal(y, want)
+    assert torch.equal(h, m.molora_rmsnorm(x, nw)[1])
+    assert torch.equal(logits, m.molora_linear(h, Wg))
+    assert all((o == 255).all() for o in others)
+
+
 def test_two_streams_at_once(m):
     g = gen(31)
     x, W, _, _ = linear_inputs(g, 300, 1024, 512, BF)

@@ -132,28 +132,40 @@ def test_c_abi_refuses_without_launching():
     assert norm(p, 1, 4, 8, p, q, p, 1e-6, q, None, None, None) == INVALID            # sum_out and out the same
     assert norm(p + 1, 1, 4, 8, None, None, p, 1e-6, q, None, None, None) == INVALID  # half an element
     assert norm(p, 0, 4, 8, None, None, p, 1e-6, q + 2, None, None, None) == INVALID
+    most = 2 ** 31 - 1024
+    assert norm(p, 1, most + 1, 8, None, None, p, 1e-6, q, None, None, None) == INVALID
+    assert norm(p, 1, 1, most + 1, None, None, p, 1e-6, q, None, None, None) == INVALID
+    # outputs that share memory with an input in part, with one another, or with the weight
+    for bad in [dict(out=p + 16), dict(out=p + 62, residual=q), dict(sum_out=q + 16), dict(out=0x40000), dict(out=0x40000 - 62),
+                dict(out8=p), dict(out8=p + 63), dict(out8=q), dict(out8=0x50000), dict(out8=0x50000 - 31), dict(out8=0x4000c),
+                dict(scale8=0x30010), dict(scale8=p), dict(sum_out=0x50010), dict(sum_out=0x60000), dict(sum_out=0x30010)]:
+        a = dict(x=p, residual=q, sum_out=q, weight=0x40000, out=0x50000, out8=0x30000, scale8=0x60000) | bad
+        assert norm(a["x"], 1, 4, 8, a["residual"], a["sum_out"], a["weight"], 1e-6, a["out"], a["out8"], a["scale8"], None) == INVALID, bad
     gate = lib.molora_gate_topk
     assert gate(None, 1, 0, 8, 0, None, 1, 1, 1, 2, 1, 1.0, None, None, None, None) == 0
     for bad in [dict(K=513), dict(K=0), dict(score=2), dict(groups=3), dict(groups=64, K=512), dict(keep=2),
                 dict(groups=4, keep=0), dict(top=3), dict(groups=8, top=2), dict(k=0), dict(k=9), dict(k=33, K=64),
                 dict(scale=float("nan")), dict(dtype=2), dict(logits=None), dict(ids=None), dict(logits=p + 1),
-                dict(ids=p + 2)]:
-        a = dict(logits=p, dtype=1, N=4, K=8, score=0, groups=1, keep=1, top=1, k=2, scale=1.0, ids=p) | bad
+                dict(ids=p + 2), dict(ids=p + 60), dict(ids=q + 28), dict(logits=q + 16)]:
+        a = dict(logits=p, dtype=1, N=4, K=8, score=0, groups=1, keep=1, top=1, k=2, scale=1.0, ids=0x30000) | bad
         assert gate(a["logits"], a["dtype"], a["N"], a["K"], a["score"], None, a["groups"], a["keep"], a["top"], a["k"], 1,
-                    a["scale"], a["ids"], p, None, None) == INVALID, bad
+                    a["scale"], a["ids"], q, None, None) == INVALID, bad
     linear = lib.molora_linear
     assert linear(None, 1, None, 0, 8, None, None, 8, None, 0, None, None, 0, None, None) == 0
     for bad in [dict(dtype=3), dict(N=-1), dict(d_in=0), dict(d_out=0), dict(act=5), dict(act=-1), dict(x=None),
                 dict(W=None), dict(y=None), dict(sx=p), dict(sw=p), dict(dtype=2), dict(dtype=2, sx=p), dict(x=p + 1),
-                dict(y=q + 2), dict(dtype=2, sx=p + 1, sw=p)]:
-        a = dict(x=p, dtype=1, sx=None, N=4, d_in=8, W=p, sw=None, d_out=8, act=0, y=q) | bad
-        assert linear(a["x"], a["dtype"], a["sx"], a["N"], a["d_in"], a["W"], a["sw"], a["d_out"], None, a["act"], None,
+                dict(y=q + 2), dict(dtype=2, sx=p + 1, sw=p), dict(N=most + 1), dict(d_in=most + 1), dict(d_out=most + 1),
+                dict(y=p), dict(y=p + 60), dict(y=p - 124), dict(y=0x30040), dict(bias=q + 124), dict(bias=q - 28),
+                dict(res=q + 4), dict(res=q - 124), dict(dtype=2, sx=q + 16, sw=p), dict(dtype=2, sx=p, sw=q - 16)]:
+        a = dict(x=p, dtype=1, sx=None, N=4, d_in=8, W=0x30000, sw=None, d_out=8, bias=None, act=0, res=None, y=q) | bad
+        assert linear(a["x"], a["dtype"], a["sx"], a["N"], a["d_in"], a["W"], a["sw"], a["d_out"], a["bias"], a["act"], a["res"],
                       a["y"], 0, None, None) == INVALID, bad
     step = lib.molora_norm_linear_lora_apply
     size = ctypes.c_size_t(99)
     for bad in [dict(w_dtype=0), dict(w_dtype=2), dict(h=None), dict(h8=p), dict(W=None), dict(A=None), dict(ids=None),
-                dict(k=3), dict(r=12), dict(y=0x10004), dict(eps=0.0), dict(sum_out=q), dict(ws=0x10001)]:
-        a = dict(w_dtype=1, h=p, h8=None, W=p, A=p, ids=p, k=1, r=16, y=q, eps=1e-6, sum_out=None, ws=None) | bad
+                dict(k=3), dict(r=12), dict(y=0x10004), dict(eps=0.0), dict(sum_out=q), dict(ws=0x10001),
+                dict(h=q), dict(W=q + 64), dict(A=q + 1020), dict(B=q - 4094)]:
+        a = dict(w_dtype=1, h=0x30000, h8=None, W=p, A=p, B=p, ids=p, k=1, r=16, y=q, eps=1e-6, sum_out=None, ws=None) | bad
         assert step(p, 1, 4, 64, None, a["sum_out"], p, a["eps"], a["h"], a["h8"], None, a["W"], a["w_dtype"], None, 64, None,
-                    a["A"], p, 2, a["r"], a["ids"], None, a["k"], None, None, None, 1.0, a["y"], 0, a["ws"],
+                    a["A"], a["B"], 2, a["r"], a["ids"], None, a["k"], None, None, None, 1.0, a["y"], 0, a["ws"],
                     ctypes.byref(size) if a["ws"] else None, None, None) == INVALID, bad

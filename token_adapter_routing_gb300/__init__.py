@@ -216,11 +216,11 @@ def _slots(ids: torch.Tensor, N: int, name: str = "ids"):
     return 1 if ids.dim() == 1 else ids.shape[1]
 
 
-def _workspace(ws: Optional[torch.Tensor], device, call) -> int:
+def _workspace(ws: Optional[torch.Tensor], device, call, stream=None) -> int:
     """Runs `call(ws_ptr, ws_bytes_ptr)` under the library's workspace convention and returns
     its status: with no caller buffer it first queries the size and, if one is needed,
     allocates it on `device` (torch's caching allocator; inside a CUDA graph capture the
-    graph's pool)."""
+    graph's pool; of `stream`'s memory if given)."""
     size = ctypes.c_size_t(0)
     if ws is None:
         status = call(None, ctypes.byref(size))
@@ -228,7 +228,8 @@ def _workspace(ws: Optional[torch.Tensor], device, call) -> int:
             return status
         if size.value == 0:
             return call(None, None)
-        ws = torch.empty(size.value, dtype=torch.uint8, device=device)
+        with torch.cuda.stream(stream):
+            ws = torch.empty(size.value, dtype=torch.uint8, device=device)
     else:
         _cuda(ws, "ws", torch.uint8, device=device)
     size.value = ws.numel()
@@ -740,6 +741,15 @@ def _raw_stream(stream, device) -> int:
     return _stream(stream, torch.device("cuda", device)).value or 0
 
 
+def _new(like, shape, dtype, stream):
+    """An output or workspace that a call makes for kernels on `stream`: from that stream's memory, so
+    that neither work before it on the current stream nor whoever gets its memory next can meet them."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    with torch.cuda.stream(stream):
+        return like.new_empty(shape, dtype=dtype)
+
+
 def molora_rmsnorm(x, weight, eps=1e-6, residual=None, sum_out=None, out=None, out8=None, scale8=None, stream=None):
     """Root-mean-square norm of x [N, d] (+ residual) by rows: returns (sum_out, out, out8, scale8).
     ``out`` (x's dtype) is made if neither it nor out8 is given; ``sum_out`` (x + residual) is made
@@ -760,9 +770,9 @@ def molora_rmsnorm(x, weight, eps=1e-6, residual=None, sum_out=None, out=None, o
     if residual is None and sum_out is not None:
         raise ValueError("sum_out needs a residual")
     if residual is not None and sum_out is None:
-        sum_out = torch.empty_like(x)
+        sum_out = _new(x, shape, dt, stream)
     if out is None and out8 is None:
-        out = torch.empty_like(x)
+        out = _new(x, shape, dt, stream)
     ps, po = _array(sum_out, "sum_out", shape, dt, dev), _array(out, "out", shape, dt, dev)
     p8 = _array(out8, "out8", shape, torch.float8_e4m3fn, dev)
     pc = _array(scale8, "scale8", (N,), torch.float32, dev)
@@ -796,9 +806,9 @@ def molora_gate_topk(logits, k, score="softmax", bias=None, groups=1, keep_group
     pl = _array(logits, "logits", logits.shape, logits.dtype, dev)
     pb = _array(bias, "bias", (K,), torch.float32, dev)
     if ids is None:
-        ids = logits.new_empty((N, k), dtype=torch.int32)
+        ids = _new(logits, (N, k), torch.int32, stream)
     if w is None:
-        w = logits.new_empty((N, k), dtype=torch.float32)
+        w = _new(logits, (N, k), torch.float32, stream)
     pi, pw = _array(ids, "ids", (N, k), torch.int32, dev), _array(w, "w", (N, k), torch.float32, dev)
     _on_gpu(logits, "logits")
     _call(
@@ -807,11 +817,11 @@ def molora_gate_topk(logits, k, score="softmax", bias=None, groups=1, keep_group
     return ids, w
 
 
-def _y(y, N, d_out, dtype, like):
+def _y(y, N, d_out, dtype, like, stream):
     if y is None:
         if dtype not in _FLOATS:
             raise ValueError(f"out_dtype must be torch.float32 or torch.bfloat16, got {dtype}")
-        return like.new_empty((N, d_out), dtype=dtype)
+        return _new(like, (N, d_out), dtype, stream)
     if not isinstance(y, torch.Tensor) or y.dtype not in _FLOATS:
         raise ValueError("y must be a float32 or bfloat16 tensor")
     return y
@@ -837,7 +847,7 @@ def molora_linear(x, W, y=None, x_scale=None, w_scale=None, bias=None, act="none
     psx = _array(x_scale, "x_scale", (N,), torch.float32, dev)
     psw = _array(w_scale, "w_scale", (d_out,), torch.float32, dev)
     pb = _array(bias, "bias", (d_out,), torch.float32, dev)
-    y = _y(y, N, d_out, out_dtype, x)
+    y = _y(y, N, d_out, out_dtype, x, stream)
     pres = _array(residual, "residual", (N, d_out), y.dtype, dev)
     py = _array(y, "y", (N, d_out), y.dtype, dev)
     _on_gpu(x, "x")
@@ -868,7 +878,7 @@ def molora_norm_linear_lora_apply(x, norm_weight, eps, W, A, B, ids, y, scale, w
     buffers that are not given are made."""
     code = _matrix(x, "x", _FLOATS)
     N, d_in = x.shape
-    dev, dt, f32, i32 = x.get_device(), x.dtype, torch.float32, torch.int32
+    dev, dt, shape, f32, i32 = x.get_device(), x.dtype, x.shape, torch.float32, torch.int32
     if not isinstance(W, torch.Tensor) or W.dim() != 2 or W.shape[0] < 1 or W.dtype not in (dt, torch.float8_e4m3fn):
         raise ValueError("W must be [d_out, d_in] of x's dtype or float8_e4m3fn")
     d_out = W.shape[0]
@@ -889,13 +899,13 @@ def molora_norm_linear_lora_apply(x, norm_weight, eps, W, A, B, ids, y, scale, w
         raise ValueError("y must be a float32 or bfloat16 tensor")
     px = _array(x, "x", x.shape, dt, dev)
     if residual is not None and sum_out is None:
-        sum_out = torch.empty_like(x)
+        sum_out = _new(x, shape, dt, stream)
     if h is None:
-        h = torch.empty_like(x)
+        h = _new(x, shape, dt, stream)
     if fp8 and h8 is None:
-        h8 = x.new_empty((N, d_in), dtype=torch.float8_e4m3fn)
+        h8 = _new(x, shape, torch.float8_e4m3fn, stream)
     if fp8 and scale8 is None:
-        scale8 = x.new_empty((N,), dtype=f32)
+        scale8 = _new(x, (N,), f32, stream)
     if sum_out is not None and N and h.data_ptr() == sum_out.data_ptr():
         raise ValueError("h and sum_out must be different tensors")
     args = (px, code, N, d_in, _array(residual, "residual", x.shape, dt, dev), _array(sum_out, "sum_out", x.shape, dt, dev),
@@ -914,7 +924,7 @@ def molora_norm_linear_lora_apply(x, norm_weight, eps, W, A, B, ids, y, scale, w
     def call(ws_ptr, ws_bytes):
         return lib.molora_norm_linear_lora_apply(*args, ws_ptr, ws_bytes, *tail)
     if ws is not None or y.dtype != torch.bfloat16 or N > 256:
-        _check("molora_norm_linear_lora_apply", _workspace(ws, x.device, call))
+        _check("molora_norm_linear_lora_apply", _workspace(ws, x.device, call, stream))
     else:
         # no path needs a workspace (they are for fp32 y, or for many tokens' update), so none is asked for
         _check("molora_norm_linear_lora_apply", call(None, None))

@@ -159,11 +159,28 @@ static molora_status apply_impl(const void* x, molora_dtype dtype, int64_t N, in
 static size_t size_of(molora_dtype d) { return d == MOLORA_F32 ? 4 : d == MOLORA_BF16 ? 2 : 1; }
 // Whether a pointer (NULL included) starts on a boundary of its element's size: kernels read whole elements.
 static bool on_element(const void* p, size_t size) { return (reinterpret_cast<uintptr_t>(p) & (size - 1)) == 0; }
+// The most rows, and columns, of the norm's and the product's arrays: kernels count to a tile past the end
+// in 32 bits.
+static constexpr int32_t kMostSize = INT32_MAX - 1023;
+
+// Rows x columns of `size` bytes at p.  An absent array shares nothing with another.
+struct Span {
+  const void* p;
+  int64_t rows, cols;
+  size_t size;
+  bool shares(const Span& o) const {
+    if (!p || !o.p) return false;
+    const unsigned __int128 a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(o.p);
+    return a < b + (unsigned __int128)o.rows * o.cols * o.size && b < a + (unsigned __int128)rows * cols * size;
+  }
+  // as an output that may be the other array itself
+  bool shares_part(const Span& o) const { return p != o.p && shares(o); }
+};
 
 // molora_linear's checks.  With N == 0 no pointer is looked at.
 static molora_status check_linear(const LinearArgs& a) {
-  if (!(valid_dtype(a.dtype) || a.dtype == MOLORA_E4M3) || a.N < 0 || a.N > INT32_MAX || a.d_in < 1 || a.d_out < 1 ||
-      a.act < MOLORA_ACT_NONE || a.act > MOLORA_ACT_GELU_TANH)
+  if (!(valid_dtype(a.dtype) || a.dtype == MOLORA_E4M3) || a.N < 0 || a.N > kMostSize || a.d_in < 1 ||
+      a.d_in > kMostSize || a.d_out < 1 || a.d_out > kMostSize || a.act < MOLORA_ACT_NONE || a.act > MOLORA_ACT_GELU_TANH)
     return MOLORA_ERR_INVALID_ARG;
   if (a.N == 0) return MOLORA_OK;
   if (!a.x || !a.W || !a.y) return MOLORA_ERR_INVALID_ARG;
@@ -172,6 +189,11 @@ static molora_status check_linear(const LinearArgs& a) {
   const size_t e = size_of(a.dtype), ye = a.y_bf16 ? 2 : 4;
   if (!on_element(a.x, e) || !on_element(a.W, e) || !on_element(a.y, ye) || !on_element(a.residual, ye) ||
       !on_element(a.bias, 4) || !on_element(a.x_scale, 4) || !on_element(a.w_scale, 4))
+    return MOLORA_ERR_INVALID_ARG;
+  const Span y = {a.y, a.N, a.d_out, ye};
+  if (y.shares({a.x, a.N, a.d_in, e}) || y.shares({a.W, a.d_out, a.d_in, e}) || y.shares({a.x_scale, a.N, 1, 4}) ||
+      y.shares({a.w_scale, a.d_out, 1, 4}) || y.shares({a.bias, a.d_out, 1, 4}) ||
+      y.shares_part({a.residual, a.N, a.d_out, ye}))
     return MOLORA_ERR_INVALID_ARG;
   return MOLORA_OK;
 }
@@ -185,17 +207,22 @@ static molora_status linear_impl(const LinearArgs& a, cudaStream_t stream) {
 static molora_status check_rmsnorm(const void* x, molora_dtype dtype, int64_t N, int32_t d, const void* residual,
                                    const void* sum_out, const void* weight, float eps, const void* out,
                                    const void* out8, const float* scale8) {
-  if (!valid_dtype(dtype) || N < 0 || N > INT32_MAX || d < 1 || !(eps > 0.f) || !(eps <= 3.4e38f))
+  if (!valid_dtype(dtype) || N < 0 || N > kMostSize || d < 1 || d > kMostSize || !(eps > 0.f) || !(eps <= 3.4e38f))
     return MOLORA_ERR_INVALID_ARG;
   if (N == 0) return MOLORA_OK;
-  if (!x || !weight || (!out && !out8) || (out8 != nullptr) != (scale8 != nullptr) || (sum_out && !residual) ||
-      (sum_out && sum_out == out))
+  if (!x || !weight || (!out && !out8) || (out8 != nullptr) != (scale8 != nullptr) || (sum_out && !residual))
     return MOLORA_ERR_INVALID_ARG;
   const size_t e = size_of(dtype);
   if (!on_element(x, e) || !on_element(residual, e) || !on_element(sum_out, e) || !on_element(weight, e) ||
       !on_element(out, e) || !on_element(scale8, 4))
     return MOLORA_ERR_INVALID_ARG;
-  return MOLORA_OK;
+  const Span xs = {x, N, d, e}, rs = {residual, N, d, e}, ws = {weight, 1, d, e}, ss = {sum_out, N, d, e}, os = {out, N, d, e},
+             os8 = {out8, N, d, 1}, sc = {scale8, N, 1, 4};
+  for (const Span& o : {ss, os})
+    if (o.shares_part(xs) || o.shares_part(rs) || o.shares(ws) || o.shares(os8) || o.shares(sc)) return MOLORA_ERR_INVALID_ARG;
+  for (const Span& o : {os8, sc})
+    if (o.shares(xs) || o.shares(rs) || o.shares(ws)) return MOLORA_ERR_INVALID_ARG;
+  return ss.shares(os) || os8.shares(sc) ? MOLORA_ERR_INVALID_ARG : MOLORA_OK;
 }
 
 }  // namespace molora
@@ -431,6 +458,8 @@ molora_status molora_gate_topk(const void* logits, molora_dtype dtype, int64_t N
   if (!logits || !ids || !w || !on_element(logits, size_of(dtype)) || !on_element(bias, 4) || !on_element(ids, 4) ||
       !on_element(w, 4))
     return MOLORA_ERR_INVALID_ARG;
+  const Span ls = {logits, N, K, size_of(dtype)}, bs = {bias, 1, K, 4}, is = {ids, N, k, 4}, ws = {w, N, k, 4};
+  if (is.shares(ls) || is.shares(bs) || is.shares(ws) || ws.shares(ls) || ws.shares(bs)) return MOLORA_ERR_INVALID_ARG;
   return launched(launch_gate_topk(logits, dtype, N, K, score == MOLORA_SCORE_SIGMOID, bias, groups, keep_groups,
                                    group_top, k, renormalise != 0, scale, ids, w, err_word, stream));
 }
@@ -465,6 +494,11 @@ molora_status molora_norm_linear_lora_apply(const void* x, molora_dtype dtype, i
     if (st == MOLORA_OK) st = check_apply_args(h, dtype, N, d_in, d_out, A, B, K, r, ids, k, y);
     if (st != MOLORA_OK || N == 0) return st;
     if (ws && (reinterpret_cast<uintptr_t>(ws) & 255u)) return MOLORA_ERR_INVALID_ARG;
+    const size_t e = size_of(dtype);
+    const Span ys = {y, N, d_out, y_bf16 ? size_t(2) : size_t(4)};
+    if (ys.shares({h, N, d_in, e}) || ys.shares({sum_out, N, d_in, e}) || ys.shares({A, (int64_t)K * d_in, r, e}) ||
+        ys.shares({B, (int64_t)K * r, d_out, e}))
+      return MOLORA_ERR_INVALID_ARG;
   }
   // With more than 256 tokens the product takes the adapters' update along (y is then written, and
   // rounded, once), if its two planes fit the workspace: K*r/32 more K blocks of 64 against a pass over y.
