@@ -21,6 +21,7 @@
 //   reading W, and the way through the kernel: one token, 4096 x 4096 bf16, 7.2 us (W's bytes: 5.0).
 // linear_any_kernel (fp32, and rows that start anywhere): the same split, with the operands fetched and
 //   laid out by the CTA's threads.
+// linear_few_kernel (a token of little W or of rows that start anywhere, a few of fp32): the CUDA cores.
 #include <cudaTypedefs.h>
 
 #include <atomic>
@@ -1155,6 +1156,76 @@ __global__ void __launch_bounds__(kAnyThreads, 1)
 }
 
 // ---------------------------------------------------------------------------------------------
+constexpr int kFewWarps = 4;
+
+// A token or a few: R outputs a warp on the CUDA cores, W's rows straight into registers, U loads of 16 bytes
+// (kVec: rows on 16-byte boundaries) or of an element of each row in flight a lane; x comes from L1.  Bound by
+// those loads (one token, 4096 x 4096 fp32 from HBM 12.0 us, 5600 GB/s) and, with each further token, by the
+// instructions that multiply.
+template <typename T, bool kVec, int NT, int R>
+__global__ void __launch_bounds__(kFewWarps * 32)
+    linear_few_kernel(const Epi E, const T* __restrict__ x, const T* __restrict__ W, int32_t d_in) {
+  constexpr uint32_t n = kVec ? 16 / sizeof(T) : 1;
+  constexpr int U = kVec ? 4 : 8;
+  struct alignas(kVec ? 16 : sizeof(T)) Run {
+    T v[n];
+  };
+  const int lane = threadIdx.x & 31;
+  const int64_t o0 = ((int64_t)blockIdx.x * kFewWarps + (threadIdx.x >> 5)) * R;
+  pdl_wait();
+  pdl_launch_dependents();
+  if (o0 >= E.d_out) return;
+  const T* rows[R];
+#pragma unroll
+  for (int q = 0; q < R; ++q) rows[q] = W + min(o0 + q, (int64_t)E.d_out - 1) * d_in;
+  float sum[R][NT] = {};
+  for (uint32_t i = lane * n; i < (uint32_t)d_in; i += 32 * n * U) {
+    Run w[U][R];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int q = 0; q < R; ++q)
+        if (i + 32 * n * u < (uint32_t)d_in) w[u][q] = *reinterpret_cast<const Run*>(rows[q] + i + 32 * n * u);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (i + 32 * n * u >= (uint32_t)d_in) continue;
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        if (NT > 1 && t >= E.N) continue;
+        const Run a = *reinterpret_cast<const Run*>(x + (int64_t)t * d_in + i + 32 * n * u);
+#pragma unroll
+        for (int j = 0; j < (int)n; ++j) {
+          const float v = to_float(a.v[j]);
+#pragma unroll
+          for (int q = 0; q < R; ++q) sum[q][t] = fmaf(v, to_float(w[u][q].v[j]), sum[q][t]);
+        }
+      }
+    }
+  }
+  float v = 0.f;  // of lane q * NT + t
+#pragma unroll
+  for (int q = 0; q < R; ++q)
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+#pragma unroll
+      for (int off = 16; off; off >>= 1) sum[q][t] += __shfl_xor_sync(0xffffffffu, sum[q][t], off);
+      if (lane == q * NT + t) v = sum[q][t];
+    }
+  const int64_t o = o0 + lane / NT, t = lane % NT, at = t * E.d_out + o;
+  if (lane >= R * NT || o >= E.d_out || t >= E.N) return;
+  if (E.sx) v *= E.sx[t] * E.sw[o];
+  if (E.bias) v += E.bias[o];
+  v = activate(v, E.act);
+  if (E.y_bf16) {
+    if (E.res) v += to_float(static_cast<const __nv_bfloat16*>(E.res)[at]);
+    static_cast<__nv_bfloat16*>(E.y)[at] = __float2bfloat16_rn(v);
+  } else {
+    if (E.res) v += static_cast<const float*>(E.res)[at];
+    static_cast<float*>(E.y)[at] = v;
+  }
+}
+
+// ---------------------------------------------------------------------------------------------
 namespace {
 
 PFN_cuTensorMapEncodeTiled_v12000 linear_encoder() {
@@ -1415,6 +1486,27 @@ cudaError_t launch_any(const LinearArgs& a, cudaStream_t stream) {
 
 }  // namespace
 
+namespace {
+
+template <typename T, bool kVec, int NT, int R>
+cudaError_t launch_few(const LinearArgs& a, cudaStream_t stream) {
+  const dim3 grid((unsigned)(((int64_t)a.d_out + kFewWarps * R - 1) / (kFewWarps * R)));
+  return launch_kernel(linear_few_kernel<T, kVec, NT, R>, grid, dim3(kFewWarps * 32), 0, stream, 0, epilogue_of(a),
+                       static_cast<const T*>(a.x), static_cast<const T*>(a.W), a.d_in);
+}
+
+// fp32, up to four tokens.  With outputs enough to fill the GPU, several a warp share x (4096 x 4096, one token
+// 6.7 us, 8.5 with one output a warp; four tokens 13.3 with four outputs, 14.5 with one; 1024 -> 1024 the other
+// way, 2.4 and 2.3, 3.9 and 3.6).
+cudaError_t launch_few_fp32(const LinearArgs& a, cudaStream_t stream) {
+  const bool wide = a.d_out >= 2048;
+  if (a.N == 1) return wide ? launch_few<float, true, 1, 2>(a, stream) : launch_few<float, true, 1, 1>(a, stream);
+  if (a.N == 2) return wide ? launch_few<float, true, 2, 2>(a, stream) : launch_few<float, true, 2, 1>(a, stream);
+  return wide ? launch_few<float, true, 4, 4>(a, stream) : launch_few<float, true, 4, 1>(a, stream);
+}
+
+}  // namespace
+
 // Whether TMA can fetch the operands: bf16 or e4m3 rows that start on 16-byte boundaries.
 static bool tma_rows(const LinearArgs& a) {
   if (a.dtype != MOLORA_BF16 && a.dtype != MOLORA_E4M3) return false;
@@ -1427,6 +1519,22 @@ bool linear_takes_update(const LinearArgs& a, const void* B, int32_t KR) {
 }
 
 cudaError_t launch_linear(const LinearArgs& a, cudaStream_t stream, const LinearUpdate* update) {
+  // linear_few_kernel, where it was the faster one (us):
+  //   fp32, up to 4 tokens:  4096 x 4096, 1, 2, 4 and 8 tokens 6.7, 11, 13 and 22 against 21 on the tensor cores
+  //   rows that start anywhere, one token:  4095 x 4096 fp32 8.2 against 26, bf16 8.9 against 14, e4m3 8.7
+  //     against 16; but two tokens, element by element, 32 against 26, 33 against 14, 34 against 16
+  //   bf16 and e4m3 rows up to 8 KB, one token, up to 2 MB of W:  1024 x 1024 bf16 2.5 against 4.2, 4096 -> 512
+  //     e4m3 4.0 against 4.6; 4096 -> 4096 bf16 7.5 against 7.5, e4m3 7.6 against 6.5
+  const int64_t row_bytes = (int64_t)a.d_in * (a.dtype == MOLORA_F32 ? 4 : a.dtype == MOLORA_BF16 ? 2 : 1);
+  const bool vec = row_bytes % 16 == 0 && aligned(a.x, 16) && aligned(a.W, 16);
+  if (!update && a.dtype == MOLORA_F32 && vec && a.N <= 4) return launch_few_fp32(a, stream);
+  if (!update && a.N == 1 && !vec) {
+    if (a.dtype == MOLORA_BF16) return launch_few<__nv_bfloat16, false, 1, 1>(a, stream);
+    if (a.dtype == MOLORA_E4M3) return launch_few<__nv_fp8_e4m3, false, 1, 1>(a, stream);
+    return launch_few<float, false, 1, 1>(a, stream);
+  }
+  if (!update && a.N == 1 && a.dtype != MOLORA_F32 && row_bytes <= 8192 && row_bytes * a.d_out <= 2 << 20)
+    return a.dtype == MOLORA_BF16 ? launch_few<__nv_bfloat16, true, 1, 1>(a, stream) : launch_few<__nv_fp8_e4m3, true, 1, 1>(a, stream);
   if (!tma_rows(a)) {
     if (a.dtype == MOLORA_BF16) return launch_any<__nv_bfloat16, false>(a, stream);
     if (a.dtype == MOLORA_E4M3) return launch_any<__nv_fp8_e4m3, false>(a, stream);
