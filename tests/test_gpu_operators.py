@@ -381,7 +381,8 @@ SIZES = [(1, 64, 64), (1, 4096, 1000), (2, 128, 7), (3, 33, 5), (7, 200, 257), (
          (31, 1031, 517), (33, 4096, 96), (64, 96, 64), (65, 256, 1024), (127, 512, 260), (128, 64, 128), (129, 1024, 256),
          (200, 72, 200), (257, 2048, 320), (300, 24, 24), (513, 1, 1), (700, 136, 1032), (1024, 512, 768),
          (2500, 272, 2056), (3001, 1024, 1100), (4097, 64, 1333), (20000, 128, 160),
-         (1, 260, 2100), (1, 1031, 517), (1, 4096, 257), (1, 8, 3), (2, 512, 2305), (4, 516, 2051), (3, 128, 4097), (4, 4100, 65)]
+         (1, 260, 2100), (1, 1031, 517), (1, 4096, 257), (1, 8, 3), (2, 512, 2305), (4, 516, 2051), (3, 128, 4097), (4, 4100, 65),
+         (1, 1024, 33), (2, 1024, 1000), (4, 1024, 513), (3, 512, 2048), (2, 333, 2049), (3, 1031, 34), (4, 77, 2050)]
 
 
 @pytest.mark.parametrize("N, d_in, d_out", SIZES)

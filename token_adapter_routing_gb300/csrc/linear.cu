@@ -1178,6 +1178,10 @@ __global__ void __launch_bounds__(kFewWarps * 32)
   const T* rows[R];
 #pragma unroll
   for (int q = 0; q < R; ++q) rows[q] = W + min(o0 + q, (int64_t)E.d_out - 1) * d_in;
+  // past the last token the last one again: a test in the loop would keep its loads from running ahead
+  const T* tokens[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) tokens[t] = x + (NT > 2 ? min((int64_t)t, E.N - 1) : (int64_t)t) * d_in;
   float sum[R][NT] = {};
   for (uint32_t i = lane * n; i < (uint32_t)d_in; i += 32 * n * U) {
     Run w[U][R];
@@ -1191,8 +1195,7 @@ __global__ void __launch_bounds__(kFewWarps * 32)
       if (i + 32 * n * u >= (uint32_t)d_in) continue;
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        if (NT > 1 && t >= E.N) continue;
-        const Run a = *reinterpret_cast<const Run*>(x + (int64_t)t * d_in + i + 32 * n * u);
+        const Run a = *reinterpret_cast<const Run*>(tokens[t] + i + 32 * n * u);
 #pragma unroll
         for (int j = 0; j < (int)n; ++j) {
           const float v = to_float(a.v[j]);
@@ -1495,14 +1498,39 @@ cudaError_t launch_few(const LinearArgs& a, cudaStream_t stream) {
                        static_cast<const T*>(a.x), static_cast<const T*>(a.W), a.d_in);
 }
 
-// fp32, up to four tokens.  With outputs enough to fill the GPU, several a warp share x (4096 x 4096, one token
-// 6.7 us, 8.5 with one output a warp; four tokens 13.3 with four outputs, 14.5 with one; 1024 -> 1024 the other
-// way, 2.4 and 2.3, 3.9 and 3.6).
-cudaError_t launch_few_fp32(const LinearArgs& a, cudaStream_t stream) {
-  const bool wide = a.d_out >= 2048;
-  if (a.N == 1) return wide ? launch_few<float, true, 1, 2>(a, stream) : launch_few<float, true, 1, 1>(a, stream);
-  if (a.N == 2) return wide ? launch_few<float, true, 2, 2>(a, stream) : launch_few<float, true, 2, 1>(a, stream);
-  return wide ? launch_few<float, true, 4, 4>(a, stream) : launch_few<float, true, 4, 1>(a, stream);
+// Whether linear_few_kernel is the faster one, and in which form (us here, on the tensor cores):
+//   fp32, up to 4 tokens:  4096 x 4096, 1, 2 and 4 tokens 6.6, 10 and 12, 21; 1024 x 1024 2.3, 2.5 and 3.0, 7.1.
+//     For one or two tokens, outputs enough to fill the GPU share x, two a warp (one token of 4096 x 4096 6.6, with
+//     one output a warp 8.3; of 1024 x 1024 2.4 and 2.3)
+//   rows that start anywhere, two tokens, four of fp32:  4095 x 4096 fp32 8.2, 10 and 17, 26; bf16 8.7 and 12.5, 14;
+//     e4m3 8.7 and 12.6, 16; but four tokens of bf16 17, 14
+//   bf16 and e4m3, up to four tokens that are 8 KB together, up to 2 MB of W:  1024 x 1024 bf16 2.5, 2.5 and 2.7,
+//     4.2; e4m3 2.4 to 2.8, 3.8; one token of 4096 -> 512 bf16 5.4, 5.7; of 4096 -> 4096 e4m3 7.6, 6.5
+// Returns cudaErrorNotSupported where it is not.
+cudaError_t try_few(const LinearArgs& a, cudaStream_t stream) {
+  using F = float;
+  using B = __nv_bfloat16;
+  using Q = __nv_fp8_e4m3;
+  if (a.N > 4) return cudaErrorNotSupported;
+  const int64_t row_bytes = (int64_t)a.d_in * (a.dtype == MOLORA_F32 ? 4 : a.dtype == MOLORA_BF16 ? 2 : 1);
+  const bool vec = row_bytes % 16 == 0 && aligned(a.x, 16) && aligned(a.W, 16), wide = a.d_out >= 2048;
+  if (a.dtype == MOLORA_F32) {
+    if (vec && a.N == 1) return wide ? launch_few<F, true, 1, 2>(a, stream) : launch_few<F, true, 1, 1>(a, stream);
+    if (vec && a.N == 2) return wide ? launch_few<F, true, 2, 2>(a, stream) : launch_few<F, true, 2, 1>(a, stream);
+    if (vec) return launch_few<F, true, 4, 1>(a, stream);
+    if (a.N == 1) return launch_few<F, false, 1, 1>(a, stream);
+    return a.N == 2 ? launch_few<F, false, 2, 2>(a, stream) : launch_few<F, false, 4, 2>(a, stream);
+  }
+  const bool bf16 = a.dtype == MOLORA_BF16;
+  if (!vec) {
+    if (a.N == 1) return bf16 ? launch_few<B, false, 1, 1>(a, stream) : launch_few<Q, false, 1, 1>(a, stream);
+    if (a.N == 2) return bf16 ? launch_few<B, false, 2, 2>(a, stream) : launch_few<Q, false, 2, 2>(a, stream);
+    return cudaErrorNotSupported;
+  }
+  if (row_bytes * a.N > 8192 || row_bytes * a.d_out > 2 << 20) return cudaErrorNotSupported;
+  if (a.N == 1) return bf16 ? launch_few<B, true, 1, 1>(a, stream) : launch_few<Q, true, 1, 1>(a, stream);
+  if (a.N == 2) return bf16 ? launch_few<B, true, 2, 2>(a, stream) : launch_few<Q, true, 2, 1>(a, stream);
+  return bf16 ? launch_few<B, true, 4, 2>(a, stream) : launch_few<Q, true, 4, 1>(a, stream);
 }
 
 }  // namespace
@@ -1519,22 +1547,10 @@ bool linear_takes_update(const LinearArgs& a, const void* B, int32_t KR) {
 }
 
 cudaError_t launch_linear(const LinearArgs& a, cudaStream_t stream, const LinearUpdate* update) {
-  // linear_few_kernel, where it was the faster one (us):
-  //   fp32, up to 4 tokens:  4096 x 4096, 1, 2, 4 and 8 tokens 6.7, 11, 13 and 22 against 21 on the tensor cores
-  //   rows that start anywhere, one token:  4095 x 4096 fp32 8.2 against 26, bf16 8.9 against 14, e4m3 8.7
-  //     against 16; but two tokens, element by element, 32 against 26, 33 against 14, 34 against 16
-  //   bf16 and e4m3 rows up to 8 KB, one token, up to 2 MB of W:  1024 x 1024 bf16 2.5 against 4.2, 4096 -> 512
-  //     e4m3 4.0 against 4.6; 4096 -> 4096 bf16 7.5 against 7.5, e4m3 7.6 against 6.5
-  const int64_t row_bytes = (int64_t)a.d_in * (a.dtype == MOLORA_F32 ? 4 : a.dtype == MOLORA_BF16 ? 2 : 1);
-  const bool vec = row_bytes % 16 == 0 && aligned(a.x, 16) && aligned(a.W, 16);
-  if (!update && a.dtype == MOLORA_F32 && vec && a.N <= 4) return launch_few_fp32(a, stream);
-  if (!update && a.N == 1 && !vec) {
-    if (a.dtype == MOLORA_BF16) return launch_few<__nv_bfloat16, false, 1, 1>(a, stream);
-    if (a.dtype == MOLORA_E4M3) return launch_few<__nv_fp8_e4m3, false, 1, 1>(a, stream);
-    return launch_few<float, false, 1, 1>(a, stream);
+  if (!update) {
+    const cudaError_t few = try_few(a, stream);
+    if (few != cudaErrorNotSupported) return few;
   }
-  if (!update && a.N == 1 && a.dtype != MOLORA_F32 && row_bytes <= 8192 && row_bytes * a.d_out <= 2 << 20)
-    return a.dtype == MOLORA_BF16 ? launch_few<__nv_bfloat16, true, 1, 1>(a, stream) : launch_few<__nv_fp8_e4m3, true, 1, 1>(a, stream);
   if (!tma_rows(a)) {
     if (a.dtype == MOLORA_BF16) return launch_any<__nv_bfloat16, false>(a, stream);
     if (a.dtype == MOLORA_E4M3) return launch_any<__nv_fp8_e4m3, false>(a, stream);
