@@ -86,6 +86,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = ctrl->tmem_base;
 
+  // of the join below: 8 columns of a token a thread (one adapter's, since r >= 16), the CTA's share of the rows
+  const int per_row = NA / 8, first = kRows * rank / C, rows = kRows * (rank + 1) / C - first;
+  auto coefficient = [&](int q) {
+    const int64_t t = t0 + first + q / per_row;
+    const int c0 = (q % per_row) * 8, a = a0 + c0 / r;
+    float coef = 0.f;
+    if (q >= rows * per_row || t >= N || a >= K) return coef;
+    for (int j = 0; j < k; ++j) {
+      const int32_t id = ids[t * k + j];
+      if (id == a) coef += w ? w[t * k + j] : 1.f;
+      if ((id < 0 || id >= K) && a == 0 && c0 == 0) report(err_word, MOLORA_DEV_BAD_ADAPTER_ID);
+    }
+    return coef * scale;
+  };
+  float coef = warp < kEpiWarps ? coefficient(tid) : 0.f;  // on its way under the MMAs
+
   if (warp == 8) {
     if (elect_one()) {
       int issued = 0, s = 0;
@@ -156,8 +172,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   __syncthreads();
   if (C > 1) cluster_sync();
-  // 8 columns of a token a thread (one adapter's, since r >= 16), the CTA's share of the rows
-  const int per_row = NA / 8, first = kRows * rank / C, rows = kRows * (rank + 1) / C - first;
   for (int q = tid; warp < kEpiWarps && q < rows * per_row; q += kEpiWarps * 32) {
     const int row = first + q / per_row, c0 = (q % per_row) * 8;
     const int64_t t = t0 + row;
@@ -171,13 +185,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       v[0] += p0.x, v[1] += p0.y, v[2] += p0.z, v[3] += p0.w;
       v[4] += p1.x, v[5] += p1.y, v[6] += p1.z, v[7] += p1.w;
     }
-    float coef = 0.f;
-    for (int j = 0; j < k; ++j) {
-      const int32_t id = ids[t * k + j];
-      if (id == a) coef += w ? w[t * k + j] : 1.f;
-      if ((id < 0 || id >= K) && a == 0 && c0 == 0) report(err_word, MOLORA_DEV_BAD_ADAPTER_ID);
-    }
-    coef *= scale;
+    if (q != tid) coef = coefficient(q);
     uint32_t hi[4], lo[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
