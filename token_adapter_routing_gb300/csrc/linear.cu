@@ -18,7 +18,7 @@
 // linear_skinny_kernel (few tokens): W's rows are the MMA's M (128 outputs a CTA), the tokens its N
 //   (16 .. 256), so that no MMA row is spent on tokens that are not there; d_in is split over a
 //   cluster of CTAs whose partial sums meet through distributed shared memory in rank order.  Bound by
-//   reading W, and the way through the kernel: one token, 4096 x 4096 bf16, 7.2 us (W's bytes: 5.0).
+//   reading W, and the way through the kernel: one token, 4096 x 4096 bf16, 7.4 us (W's bytes: 5.0).
 // linear_any_kernel (fp32, and rows that start anywhere): the same split, with the operands fetched and
 //   laid out by the CTA's threads.
 // linear_few_kernel (a token of little W or of rows that start anywhere, a few of fp32): the CUDA cores.
@@ -968,8 +968,9 @@ struct Piece<__nv_fp8_e4m3, kVec> {
 // as bf16 planes in the swizzled stages.  fp32 is three planes, x = x1 + x2 + x3 exactly, and
 //   x w = x1 w1 + x1 w2 + x2 w1 + x2 w2 + x1 w3 + x3 w1 + (terms below 2^-21 of |x w|, 2^-24 of it on average)
 // which is six bf16 products with fp32 sums: an fp32 product at a sixth of the bf16 rate, four times the CUDA
-// cores'.  All but the first are 2^-7 of it and less, and sum apart: their long chain's drift is theirs.  An infinite operand would meet the zero planes of finite ones (inf * 0): a tile that has
-// seen one sums its outputs again on the CUDA cores.
+// cores'.  All but the first are 2^-7 of it and less, and sum apart: their long chain's drift is theirs.  An
+// infinite operand would meet the zero planes of finite ones (inf * 0): a tile that has seen one sums its outputs
+// again on the CUDA cores.
 //
 // Bound by the threads that cut the operands: 15 warps, with their next pieces on the way while a stage is
 // written and handed over.  1024 x 4096 x 4096 fp32 343 us (100 TFLOP/s, 577 us for the library's fp32 product);
