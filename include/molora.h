@@ -533,7 +533,8 @@ MOLORA_API molora_status molora_gate_topk(const void* logits, molora_dtype dtype
  * with the other arrays (refused).
  * Products are summed in fp32; the epilogue is fp32 and y is rounded once.  Any N, d_in, d_out up to 2^31 - 1024; arrays
  * start on a boundary of their element's size (rows on 16-byte boundaries are faster).  Results are
- * reproducible bit for bit.  A wait that ran out (MOLORA_DEV_WAIT_TIMEOUT) leaves its tile of y unwritten.
+ * reproducible bit for bit.  Outputs that a wait that ran out (MOLORA_DEV_WAIT_TIMEOUT) left without their sums are NaN,
+ * or stay as they were; the others are right.
  */
 MOLORA_API molora_status molora_linear(const void* x, molora_dtype dtype, const float* x_scale, int64_t N, int32_t d_in,
                             const void* W, const float* w_scale, int32_t d_out, const float* bias,
