@@ -560,7 +560,8 @@ MOLORA_API molora_status molora_linear(const void* x, molora_dtype dtype, const 
  * along as further K blocks: a shrink writes it to the workspace as two bf16
  * terms (relative error 2^-17), and y is written, and rounded, once.  It evaluates all K adapters, those
  * that a token did not choose with weight 0, as the dense and stacked paths do: the whole hot set has to
- * be finite.  Otherwise the results are those of the three calls.
+ * be finite.  Tokens whose update a wait that ran out has lost are NaN.  Otherwise the results are those of the three
+ * calls.
  */
 MOLORA_API molora_status molora_norm_linear_lora_apply(
     const void* x, molora_dtype dtype, int64_t N, int32_t d_in, const void* residual, void* sum_out,

@@ -30,7 +30,7 @@ def libs(tmp_path_factory):
         subprocess.run([build._nvcc(), *build.ARCH, *build.NVCC_FLAGS, f'-DMOLORA_SOURCE="{name}.cu"',
                         f"-DMOLORA_SET=lost_in_{name}", "-c", here, "-o", obj], check=True)
         return obj
-    names = ("linear",)
+    names = ("linear", "lora_update")
     with concurrent.futures.ThreadPoolExecutor() as ex:
         objs = list(ex.map(compile_one, names))
     objs += [os.path.join(build.BUILD, os.path.basename(s)[:-3] + ".o") for s in build.sources()
@@ -38,7 +38,8 @@ def libs(tmp_path_factory):
     path = str(out / "libmolora_lost.so")
     subprocess.run([build._nvcc(), *build.ARCH, "-shared", "-o", path, *objs], check=True)
     lost = ctypes.CDLL(path)
-    lost.molora_linear.argtypes = lib.molora_linear.argtypes
+    for name in ("molora_linear", "molora_norm_linear_lora_apply"):
+        getattr(lost, name).argtypes = getattr(lib, name).argtypes
     return m, lib, lost
 
 
@@ -123,3 +124,42 @@ def test_pair_product_writes_nothing_wrong(libs, y_dtype, cta, warp):
     assert e.item() == m.DEV_WAIT_TIMEOUT
     assert ((y == want) | (y == OLD)).all()
     assert (y == OLD).any()
+
+
+@pytest.mark.parametrize("K, r", [(4, 16), (7, 64)])
+@pytest.mark.parametrize("cta, warp", [(0, 0), (1, 0), (1, 9), (0, 9), (1, 8)])
+def test_update_that_was_lost_is_nan(libs, K, r, cta, warp):
+    """The tokens whose update a shrink's run-out wait lost are NaN, whatever the workspace held; the others are right."""
+    m, lib, _ = libs
+    g = gen(K)
+    N, d = 300, 512
+    x, nw = randn(g, N, d).to(BF), torch.ones(d, dtype=BF, device="cuda")
+    W = (randn(g, d, d) / d ** 0.5).to(BF)
+    A, B = (randn(g, K, d, r) / d ** 0.5).to(BF), randn(g, K, r, d).to(BF)
+    ids = (torch.arange(N, device="cuda") % K).to(torch.int32)
+    w = torch.rand(N, generator=g, device="cuda")
+    ws = torch.zeros(2 * ((N * K * r * 2 + 255) // 256 * 256), dtype=torch.uint8, device="cuda")
+
+    def run(lib):
+        h, y = torch.empty_like(x), torch.full((N, d), OLD, device="cuda")
+        e = torch.zeros(1, dtype=torch.int32, device="cuda")
+        size = ctypes.c_size_t(ws.numel())
+        p = [t.data_ptr() for t in (x, nw, h, W, A, B, ids, w, y, ws, e)]
+        status = lib.molora_norm_linear_lora_apply(
+            p[0], 1, N, d, None, None, p[1], 1e-6, p[2], None, None, p[3], 1, None, d, None, p[4], p[5], K, r, p[6], p[7], 1,
+            None, None, None, 2.0, p[8], 0, p[9], ctypes.byref(size), p[10], torch.cuda.current_stream().cuda_stream)
+        assert status == 0
+        torch.cuda.synchronize()
+        return y, e.item()
+    want, e = run(lib)
+    assert e == 0
+    for stale in (0, 63):  # of bf16, 0 and 0.747
+        ws.fill_(stale)
+        out = []
+        call_with_lost(libs, "lora_update", cta, warp, lambda lost: out.append(run(lost)))
+        y, e = out[0]
+        assert e == m.DEV_WAIT_TIMEOUT
+        assert ((y == want) | torch.isnan(y)).all()
+        assert torch.equal(y[128:], want[128:])  # tile 0 is 128 tokens; warp 0 has its first 32
+        if warp in (0, 9):
+            assert torch.isnan(y[:32 if warp == 0 else 128]).all()

@@ -151,7 +151,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   // partial sums [token][NA + 4] in the ring (the padding spreads the rows over the banks)
   float* part = reinterpret_cast<float*>(sm);
   const int stride = NA + 4;
+  // a thread whose wait ran out has NaN for its sums, and so has all that is made of them, the tokens' y at last
   const bool have = mbar_wait(&ctrl->done, 0) && !*abort;
+  if (!have) report(err_word, MOLORA_DEV_WAIT_TIMEOUT);
   tc_fence_after();
   if (warp < kEpiWarps) {
     const int quarter = warp & 3, row = quarter * 32 + lane;
@@ -162,7 +164,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld16(base + (uint32_t)c, v);
       else
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = 0.f;
+        for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(0x7fffffffu);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         *reinterpret_cast<float4*>(part + row * stride + c + 4 * i) =
@@ -176,7 +178,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = first + q / per_row, c0 = (q % per_row) * 8;
     const int64_t t = t0 + row;
     const int a = a0 + c0 / r;
-    if (t >= N || a >= K || !have) continue;
+    if (t >= N || a >= K) continue;
     float v[8] = {};
     const uint32_t at = smem_u32(part + row * stride + c0);
     for (int c = 0; c < C; ++c) {
