@@ -101,6 +101,13 @@ struct NormArgs {
   float eps;
 };
 
+// The larger one, or NaN if either is: a row with a NaN has no largest value to scale by.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float m;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+  return m;
+}
+
 // Sum and maximum over the `warps` warps of a team; red holds 2 floats per warp of the CTA, the
 // team's first at red[2 * warp0].  Called by every thread of the CTA; two calls in a row take different
 // arrays (a thread may still read one while others write the next).
@@ -108,14 +115,14 @@ __device__ __forceinline__ void team_reduce(float& sum, float& top, int warps, i
 #pragma unroll
   for (int off = 16; off; off >>= 1) {
     sum += __shfl_xor_sync(0xffffffffu, sum, off);
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+    top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, off));
   }
   if (warps == 1) return;
   const int warp = threadIdx.x >> 5;
   if ((threadIdx.x & 31) == 0) red[2 * warp] = sum, red[2 * warp + 1] = top;
   __syncthreads();
   sum = 0.f, top = 0.f;
-  for (int i = 0; i < warps; ++i) sum += red[2 * (warp0 + i)], top = fmaxf(top, red[2 * (warp0 + i) + 1]);
+  for (int i = 0; i < warps; ++i) sum += red[2 * (warp0 + i)], top = max_nan(top, red[2 * (warp0 + i) + 1]);
 }
 
 // The 8-bit scale of a row whose largest |s * g| is `top`.  A NaN stays one.
@@ -234,7 +241,7 @@ __global__ void __launch_bounds__(kAhead ? 256 : 1024) rmsnorm_kernel(const Norm
       for (int j = 0; j < C::n; ++j) {
         part = fmaf(s[i][j], s[i][j], part);
         s[i][j] *= g[j];
-        top = fmaxf(top, fabsf(s[i][j]));
+        top = max_nan(top, fabsf(s[i][j]));
       }
       sum += part;
     }
@@ -280,7 +287,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_long_kernel(const NormArgs<T> a)
       float s = to_float(a.x[base + c]);
       if (a.res) s += to_float(a.res[base + c]);
       sum = fmaf(s, s, sum);
-      top = fmaxf(top, fabsf(s * to_float(a.g[c])));
+      top = max_nan(top, fabsf(s * to_float(a.g[c])));
     }
     team_reduce(sum, top, blockDim.x / 32, 0, red[turn ^= 1]);
     const float inv = 1.f / sqrtf(sum / (float)a.d + a.eps);
