@@ -466,9 +466,10 @@ MOLORA_API molora_status molora_lora_apply_masked_pass(const void* x, molora_dty
  *   scale8[t] = max(max_i |n[t,i]|, 2^-64) / 448
  *   out8[t,i] = n[t,i] / scale8[t], rounded to e4m3 (nearest even)
  *
- * All in fp32 from the unrounded s.  A NaN or an infinity in a row makes its norm NaN, scale8 of
- * that row included; so do rows whose squares overflow fp32 where s is infinite, and give 0
- * where it is not.
+ * All in fp32 from the unrounded s, as the formulas say for NaN and infinities too.  A NaN in a row makes all its outputs
+ * but sum_out NaN.  An infinity makes the row's root infinite: n is NaN at the infinity and 0 elsewhere, scale8 and all
+ * of out8 are NaN.  A row of finite s whose squares pass fp32's range gives 0.  A NaN in weight makes its column, every
+ * scale8 and all of out8 NaN.
  *
  * x        [N x d] dtype (MOLORA_BF16 or MOLORA_F32);  d >= 1, N and d up to 2^31 - 1024
  * residual [N x d] dtype, or NULL

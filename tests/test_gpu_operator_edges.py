@@ -63,3 +63,27 @@ def test_norm_weight_nan_and_infinity(m, dtype, N, d, unaligned):
         o8 = out8.float()
         assert torch.isnan(o8[:, at]).all() and torch.isnan(o8).sum().item() == N
         assert (o8.nan_to_num(0.0) == 0).all()
+
+
+@pytest.mark.parametrize("unaligned", [False, True])
+@pytest.mark.parametrize("dtype, N, d", NORMS)
+def test_norm_infinite_rows(m, dtype, N, d, unaligned):
+    """An infinity makes the row's root infinite: NaN at the infinity itself, 0 at the finite elements, and a NaN
+    scale, with which the whole row in 8 bits is NaN.  The other rows are what they are without it."""
+    g = gen(N * 3 + d)
+    x, w = randn(g, N, d).to(dtype), (1 + 0.1 * randn(g, d)).to(dtype)
+    x = off_by_one(x) if unaligned else x
+
+    def call():
+        out8, scale8 = torch.empty(N, d, dtype=FP8, device="cuda"), torch.empty(N, device="cuda")
+        out = m.molora_rmsnorm(x, w, out=torch.empty(N, d, dtype=dtype, device="cuda"), out8=out8, scale8=scale8)[1]
+        return out, out8.float(), scale8
+    plain = call()
+    x[1, 7] = -math.inf
+    out, out8, scale8 = call()
+    assert torch.isnan(out[1, 7]) and torch.isnan(out).sum().item() == 1
+    assert (out[1, :7] == 0).all() and (out[1, 8:] == 0).all()
+    assert torch.isnan(scale8[1]) and torch.isnan(out8[1]).all()
+    rest = [0] + list(range(2, N))
+    for a, b in zip((out, out8, scale8), plain):
+        assert torch.equal(a[rest], b[rest])
