@@ -464,7 +464,8 @@ MOLORA_API molora_status molora_lora_apply_masked_pass(const void* x, molora_dty
  *   n[t,i]    = s[t,i] * rsqrt(mean_i(s[t,i]^2) + eps) * weight[i]
  *   out       = n, rounded to dtype
  *   scale8[t] = max(max_i |n[t,i]|, 2^-64) / 448
- *   out8[t,i] = n[t,i] / scale8[t], rounded to e4m3 (nearest even)
+ *   out8[t,i] = n[t,i] * (1 / scale8[t]), the reciprocal and the product rounded to fp32 (so within 2^-23 of the
+ *               quotient), then to e4m3 (nearest even)
  *
  * All in fp32 from the unrounded s, as the formulas say for NaN and infinities too.  A NaN in a row makes all its outputs
  * but sum_out NaN.  An infinity makes the row's root infinite: n is NaN at the infinity and 0 elsewhere, scale8 and all

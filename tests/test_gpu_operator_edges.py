@@ -87,3 +87,15 @@ def test_norm_infinite_rows(m, dtype, N, d, unaligned):
     rest = [0] + list(range(2, N))
     for a, b in zip((out, out8, scale8), plain):
         assert torch.equal(a[rest], b[rest])
+
+
+@pytest.mark.parametrize("N, d", [(4096, 2048), (3000, 2049), (40, 40000)])
+def test_norm_out8_is_the_product_with_the_reciprocal(m, N, d):
+    """out8 is e4m3(n * (1 / scale8)) of the fp32 n and scale8 that the call returns, to the bit."""
+    g = gen(N)
+    x, w = randn(g, N, d), 1 + 0.1 * randn(g, d)
+    out8, scale8 = torch.empty(N, d, dtype=FP8, device="cuda"), torch.empty(N, device="cuda")
+    out = m.molora_rmsnorm(x, w, out=torch.empty_like(x), out8=out8, scale8=scale8)[1]
+    q = out.cpu() * (1.0 / scale8.cpu())[:, None]
+    want = q.clamp(-448, 448).to(FP8)
+    assert torch.equal(out8.cpu().view(torch.uint8), want.view(torch.uint8))

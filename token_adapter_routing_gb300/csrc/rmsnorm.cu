@@ -3,7 +3,11 @@
 //
 //   s = x + residual                      (fp32; sum_out = s rounded to x's type)
 //   n = s * rsqrt(mean(s^2) + eps) * g    (fp32; out = n rounded to x's type)
-//   scale8 = max(max |n|, 2^-64) / 448,   out8 = e4m3(n / scale8)
+//   scale8 = max(max |n|, 2^-64) / 448,   out8 = e4m3(n * (1 / scale8))
+//
+// A product with the rounded reciprocal, not a quotient: the two differ by 2^-23, so an element that close to a border
+// of e4m3, whose own steps are 2^-3, may go to its other side.  A division takes 8192 x 4096 bf16 from 49.0 to 57.5 us
+// (with e4m3 alone out from 26.1 to 39.3); a product with one correction, 26.1 to 28.0.
 //
 // A row is read once: s stays in registers between the reduction and the outputs.  The norm uses
 // the unrounded s, so rounding sum_out does not reach the other outputs.
