@@ -99,3 +99,25 @@ def test_norm_out8_is_the_product_with_the_reciprocal(m, N, d):
     q = out.cpu() * (1.0 / scale8.cpu())[:, None]
     want = q.clamp(-448, 448).to(FP8)
     assert torch.equal(out8.cpu().view(torch.uint8), want.view(torch.uint8))
+
+
+@pytest.mark.parametrize("N, d_in, d_out", [(5, 255, 33), (140, 256, 64), (64, 1024, 300), (1100, 512, 1032), (150, 1023, 70)])
+def test_infinities_leave_the_neighbours_bits(m, N, d_in, d_out):
+    """fp32: an infinity or NaN in one token, or one output's weights, changes no bit of the others."""
+    g = gen(N + d_in)
+    x, W = randn(g, N, d_in), randn(g, d_out, d_in) / math.sqrt(d_in)
+    plain = m.molora_linear(x, W)
+    bad = x.clone()
+    bad[2, 4], bad[4, d_in - 1] = math.inf, math.nan
+    bad.view(torch.int32)[1, 3] = 0x7f800001  # a NaN of low bits only
+    y = m.molora_linear(bad, W)
+    rest = [0, 3] + list(range(5, N))
+    assert torch.equal(y[rest], plain[rest])
+    assert torch.isnan(y[1]).all() and torch.isnan(y[4]).all()
+    assert torch.equal(y[2], torch.where(W[:, 4] > 0, math.inf, -math.inf))
+    V = W.clone()
+    V[5, 7] = -math.inf
+    y = m.molora_linear(x, V)
+    cols = [i for i in range(d_out) if i != 5]
+    assert torch.equal(y[:, cols], plain[:, cols])
+    assert torch.equal(y[:, 5], torch.where(x[:, 7] > 0, -math.inf, math.inf))

@@ -62,7 +62,6 @@ struct __align__(8) LCtrl {
   uint64_t res_full[12];
   uint32_t tmem_base;
   int32_t abort;
-  int32_t odd;  // an infinite or NaN fp32 operand was seen
 };
 
 // What the epilogue reads and writes.
@@ -196,13 +195,13 @@ struct Quad {
 // [token][output] in the stage ring (free: every load has landed and every MMA is done); each CTA then adds
 // its share of the elements in rank order, reading the others' through distributed shared memory, and
 // writes it.  Four outputs at a time and U such quads in flight a thread: element by element, one
-// remote access after another, this was 12 of 20 us at 257 x 1031 x 517.  `redo()` says, once the
-// cluster has met, whether `again(t, o)` makes the sums anew.  Called by all threads; `have` is false
+// remote access after another, this was 12 of 20 us at 257 x 1031 x 517.  kAgain: a sum that is NaN is made anew by
+// `again(t, o)`.  Called by all threads; `have` is false
 // where a wait ran out: such a thread's sums are NaN, and so is what any CTA of the cluster makes of them.  (Leaving
 // their outputs unwritten takes a flag of the cluster: 0.1 to 0.4 us a call, however it is passed on.)
-template <int U, int J, typename R, typename F>
+template <int U, bool kAgain, int J, typename F>
 __device__ __forceinline__ void split_epilogue(const Epi& E, TileSums<J>& sums, bool have, uint8_t* sm, int C, int rank,
-                                               int32_t o0, int64_t t0, int tokens, int32_t* err_word, R redo, F again) {
+                                               int32_t o0, int64_t t0, int tokens, int32_t* err_word, F again) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   float* part = reinterpret_cast<float*>(sm);
   if (!have) {
@@ -221,7 +220,6 @@ __device__ __forceinline__ void split_epilogue(const Epi& E, TileSums<J>& sums, 
   __syncthreads();
   if (C > 1) cluster_sync();
   if (warp < kEpiWarps) {
-    const bool anew = redo();
     const bool vec = E.tma_y;  // (d_out a multiple of 4 and y, residual aligned)
     const bool bias_vec = vec && (reinterpret_cast<uintptr_t>(E.bias) & 15u) == 0;
     const bool sw_vec = vec && (reinterpret_cast<uintptr_t>(E.sw) & 15u) == 0;
@@ -254,10 +252,11 @@ __device__ __forceinline__ void split_epilogue(const Epi& E, TileSums<J>& sums, 
         const int q = q0 + u * step, o = o0 + (q % (kRows / 4)) * 4;
         if (q >= quads || o >= E.d_out) continue;
         const int64_t t = t0 + q / (kRows / 4), row = t * E.d_out;
-        if (anew)
+        if constexpr (kAgain) {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            if (o + i < E.d_out) v[u].v[i] = again(t, o + i);
+            if (o + i < E.d_out && v[u].v[i] != v[u].v[i]) v[u].v[i] = again(t, o + i);
+        }
         if (E.sx) {
           Quad w;
           w.load(E.sw, o, E.d_out, sw_vec);
@@ -773,8 +772,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   // every MMA is done; the TMA warp has seen every load land
   have = mbar_wait(&ctrl->done, 0) && have && !*abort;
   __syncthreads();
-  split_epilogue<J >= 2 ? 4 : 2>(E, sums, have, sm, C, rank, o0, t0, tokens, err_word, []() { return false; },
-                                 [](int64_t, int32_t) { return 0.f; });
+  split_epilogue<J >= 2 ? 4 : 2, false>(E, sums, have, sm, C, rank, o0, t0, tokens, err_word,
+                                        [](int64_t, int32_t) { return 0.f; });
   if (warp == 9) {
     tc_fence_after();
     tmem_dealloc(tmem, P.tmem_cols);
@@ -834,8 +833,7 @@ struct Piece<float, kVec> {
       w[0] = make_uint4(u[0], u[1], u[2], u[3]), w[1] = make_uint4(u[4], u[5], u[6], u[7]);
     }
   }
-  // True if an element is infinite or NaN.
-  __device__ __forceinline__ bool cut(int left, uint4 (&out)[3]) const {
+  __device__ __forceinline__ void cut(int left, uint4 (&out)[3]) const {
     const uint4 last = w[kVec ? 1 : 2];
     uint32_t e[12] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w, last.x, last.y, last.z, last.w};
     if (!kVec) {
@@ -849,7 +847,6 @@ struct Piece<float, kVec> {
 #pragma unroll
         for (int j = 0; j < 8; ++j) e[j] = j < left ? e[j] : 0u;
     }
-    uint32_t top = 0;  // a maximum of the magnitudes' bits: exponents of all ones are infinite or NaN
     uint32_t pl[3][4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -857,7 +854,6 @@ struct Piece<float, kVec> {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const uint32_t f = e[2 * j + h];
-        top = max(top, f & 0x7fffffffu);
         part[0][h] = f & 0xffff0000u;
         const float r = __uint_as_float(f) - __uint_as_float(part[0][h]);
         part[1][h] = __float_as_uint(r) & 0xffff0000u;
@@ -868,7 +864,6 @@ struct Piece<float, kVec> {
     }
 #pragma unroll
     for (int k = 0; k < 3; ++k) out[k] = make_uint4(pl[k][0], pl[k][1], pl[k][2], pl[k][3]);
-    return top >= 0x7f800000u;
   }
 };
 
@@ -898,7 +893,7 @@ struct Piece<__nv_bfloat16, kVec> {
       w[0] = make_uint4(u[0] | u[1] << 16, u[2] | u[3] << 16, u[4] | u[5] << 16, u[6] | u[7] << 16);
     }
   }
-  __device__ __forceinline__ bool cut(int left, uint4 (&out)[1]) const {
+  __device__ __forceinline__ void cut(int left, uint4 (&out)[1]) const {
     uint32_t e[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
     if (shift & 4)
 #pragma unroll
@@ -918,7 +913,6 @@ struct Piece<__nv_bfloat16, kVec> {
       }
     }
     out[0] = make_uint4(e[0], e[1], e[2], e[3]);
-    return false;
   }
 };
 
@@ -948,7 +942,7 @@ struct Piece<__nv_fp8_e4m3, kVec> {
         if (j < left) w[j >> 2] |= (uint32_t)bytes[at + j] << (8 * (j & 3));
     }
   }
-  __device__ __forceinline__ bool cut(int left, uint4 (&out)[1]) const {
+  __device__ __forceinline__ void cut(int left, uint4 (&out)[1]) const {
     const uint32_t e[2] = {__funnelshift_r(w[0], w[1], shift), __funnelshift_r(w[1], w[2], shift)};
     uint32_t b[4];
 #pragma unroll
@@ -963,7 +957,6 @@ struct Piece<__nv_fp8_e4m3, kVec> {
       b[j] = pack_bf16(f[0], f[1]);
     }
     out[0] = make_uint4(b[0], b[1], b[2], b[3]);
-    return false;
   }
 };
 
@@ -974,9 +967,9 @@ struct Piece<__nv_fp8_e4m3, kVec> {
 // as bf16 planes in the swizzled stages.  fp32 is three planes, x = x1 + x2 + x3 exactly, and
 //   x w = x1 w1 + x1 w2 + x2 w1 + x2 w2 + x1 w3 + x3 w1 + (terms below 2^-21 of |x w|, 2^-24 of it on average)
 // which is six bf16 products with fp32 sums: an fp32 product at a sixth of the bf16 rate, four times the CUDA
-// cores'.  All but the first are 2^-7 of it and less, and sum apart: their long chain's drift is theirs.  An
-// infinite operand would meet the zero planes of finite ones (inf * 0): a tile that has seen one sums its outputs
-// again on the CUDA cores.
+// cores'.  All but the first are 2^-7 of it and less, and sum apart: their long chain's drift is theirs.  The second
+// plane of an infinity is NaN (inf - inf), as a NaN's is: every output that reads one comes out NaN, and outputs that
+// are NaN, no others, are summed again on the CUDA cores, so that no token's bits or time depend on its neighbours'.
 //
 // Bound by the threads that cut the operands: 15 warps, with their next pieces on the way while a stage is
 // written and handed over.  1024 x 4096 x 4096 fp32 343 us (100 TFLOP/s, 577 us for the library's fp32 product);
@@ -1015,7 +1008,6 @@ __global__ void __launch_bounds__(kAnyThreads, 1)
     }
     mbar_init(&ctrl->done, 1);
     ctrl->abort = 0;
-    ctrl->odd = 0;
     mbar_fence_init();
   }
   pdl_wait();
@@ -1030,7 +1022,6 @@ __global__ void __launch_bounds__(kAnyThreads, 1)
 
   if (warp < 15) {
     int taken = 0;
-    bool odd = false;
     Piece<T, kVec> piece[kPieces];  // of the rows of W, then x, 8 pieces each
     // rows past the last one are read as the last one: what comes of them is not stored
     const T* src[kPieces];  // its boundary in the grid
@@ -1073,7 +1064,7 @@ __global__ void __launch_bounds__(kAnyThreads, 1)
         for (int j = 0; j < kPieces; ++j) {
           if (row_of(j) >= kRows + BN) continue;
           uint4 p[kPlanes];
-          odd |= piece[j].cut(whole ? 8 : left_of(j, kb), p);
+          piece[j].cut(whole ? 8 : left_of(j, kb), p);
           const uint32_t at = sw128_offset((uint32_t)row_of(j), (uint32_t)(tid + j * kCutters) & 7u);
 #pragma unroll
           for (int k = 0; k < kPlanes; ++k) *reinterpret_cast<uint4*>(st + k * P.plane + at) = p[k];
@@ -1091,7 +1082,6 @@ __global__ void __launch_bounds__(kAnyThreads, 1)
       if (warp < kEpiWarps && i >= kSpan && i % kSpan == 2 && have) have = sums.take(ctrl, taken++, tmem, BN, tokens);
     }
     while (warp < kEpiWarps && taken < spans && have) have = sums.take(ctrl, taken++, tmem, BN, tokens);
-    if (odd) ctrl->odd = 1;
   } else {
     if (elect_one()) {
       const uint32_t idesc = idesc_bf16_f32(kRows, (uint32_t)BN, false, false);
@@ -1143,15 +1133,7 @@ __global__ void __launch_bounds__(kAnyThreads, 1)
     tc_fence_before();
   }
   __syncthreads();
-  // an odd element of any CTA of the cluster (they hold other parts of the same rows)
-  auto odd_seen = [&]() {
-    int32_t seen = 0;
-    if (kPlanes == 3)
-      for (int c = 0; c < C; ++c)
-        seen |= C > 1 ? __float_as_int(dsmem_ld_f32(dsmem_addr(smem_u32(&ctrl->odd), (uint32_t)c))) : ctrl->odd;
-    return seen != 0;
-  };
-  split_epilogue<2>(E, sums, have, sm, C, rank, o0, t0, tokens, err_word, odd_seen, [&](int64_t t, int32_t o) {
+  split_epilogue<2, kPlanes == 3>(E, sums, have, sm, C, rank, o0, t0, tokens, err_word, [&](int64_t t, int32_t o) {
     float v = 0.f;
     for (int i = 0; i < d_in; ++i) v = fmaf(to_float(x[t * d_in + i]), to_float(W[(int64_t)o * d_in + i]), v);
     return v;
