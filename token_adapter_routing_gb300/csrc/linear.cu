@@ -117,11 +117,11 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 template <int J>
 struct TileSums {
   float v[J][16];
-  __device__ __forceinline__ void fill(float all) {
+  __device__ __forceinline__ void zero() {
 #pragma unroll
     for (int j = 0; j < J; ++j)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) v[j][i] = all;
+      for (int i = 0; i < 16; ++i) v[j][i] = 0.f;
   }
   __device__ __forceinline__ void add(uint32_t tmem, int tokens) {
     const int warp = threadIdx.x >> 5;
@@ -200,21 +200,18 @@ struct Quad {
 // where a wait ran out: such a thread's sums are NaN, and so is what any CTA of the cluster makes of them.  (Leaving
 // their outputs unwritten takes a flag of the cluster: 0.1 to 0.4 us a call, however it is passed on.)
 template <int U, bool kAgain, int J, typename F>
-__device__ __forceinline__ void split_epilogue(const Epi& E, TileSums<J>& sums, bool have, uint8_t* sm, int C, int rank,
+__device__ __forceinline__ void split_epilogue(const Epi& E, const TileSums<J>& sums, bool have, uint8_t* sm, int C, int rank,
                                                int32_t o0, int64_t t0, int tokens, int32_t* err_word, F again) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   float* part = reinterpret_cast<float*>(sm);
-  if (!have) {
-    sums.fill(__uint_as_float(0x7fffffffu));
-    report(err_word, MOLORA_DEV_WAIT_TIMEOUT);
-  }
+  if (!have) report(err_word, MOLORA_DEV_WAIT_TIMEOUT);
   if (warp < kEpiWarps) {
 #pragma unroll
     for (int j = 0; j < J; ++j) {
       const int c = (warp >> 2) * 16 + 32 * j;
 #pragma unroll
       for (int i = 0; i < 16; ++i)
-        if (c + i < tokens) part[(c + i) * kRows + (warp & 3) * 32 + lane] = sums.v[j][i];
+        if (c + i < tokens) part[(c + i) * kRows + (warp & 3) * 32 + lane] = have ? sums.v[j][i] : __uint_as_float(0x7fffffffu);
     }
   }
   __syncthreads();
@@ -713,7 +710,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = ctrl->tmem_base;
   const int spans = kFp8 ? 1 : (kb1 - kb0 + kSpan - 1) / kSpan;
   TileSums<J> sums;
-  sums.fill(0.f);
+  sums.zero();
   bool have = true;
 
   if (warp == 8) {
@@ -1017,7 +1014,7 @@ __global__ void __launch_bounds__(kAnyThreads, 1)
   const uint32_t tmem = ctrl->tmem_base;
   const int spans = (kb1 - kb0 + kSpan - 1) / kSpan;
   TileSums<J> sums;
-  sums.fill(0.f);
+  sums.zero();
   bool have = true;
 
   if (warp < 15) {
