@@ -554,8 +554,9 @@ MOLORA_API molora_status molora_linear(const void* x, molora_dtype dtype, const 
  * x, residual, sum_out, norm_weight, h [N x d_in], A and B: dtype, h and the others as in the three
  * calls; sum_out needs residual, both may be NULL.  w_dtype is dtype or MOLORA_E4M3; h8 [N x d_in], scale8 fp32 [N] and
  * w_scale fp32 [d_out] are needed with MOLORA_E4M3 and must be NULL otherwise.  h is an output: a
- * layer's other projections read it too.  y shares memory with none
- * of h, h8, sum_out, W, A and B (refused), and is overwritten: fp32 (y_bf16 = 0) or bf16 (y_bf16 = 1,
+ * layer's other projections read it too.  y, h, h8, scale8, sum_out and the workspace share memory with none of W,
+ * w_scale, bias, A, B, ids, w, counts, offsets and perm, nor with one another (refused; h and sum_out may each be x
+ * or residual).  y is overwritten: fp32 (y_bf16 = 0) or bf16 (y_bf16 = 1,
  * with molora_lora_apply_bf16y's roundings).  ids, w, k, counts, offsets, perm and ws, ws_bytes as for
  * molora_lora_apply; a query sizes the path this call prefers.
  * Given a workspace, more than 256 tokens, bf16 dtype and K*r <= 512, the product takes the adapters' update

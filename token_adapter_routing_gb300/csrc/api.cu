@@ -494,11 +494,20 @@ molora_status molora_norm_linear_lora_apply(const void* x, molora_dtype dtype, i
     if (st == MOLORA_OK) st = check_apply_args(h, dtype, N, d_in, d_out, A, B, K, r, ids, k, y);
     if (st != MOLORA_OK || N == 0) return st;
     if (ws && (reinterpret_cast<uintptr_t>(ws) & 255u)) return MOLORA_ERR_INVALID_ARG;
+    // what a step writes shares nothing with what a later one reads, nor with another output
     const size_t e = size_of(dtype);
-    const Span ys = {y, N, d_out, y_bf16 ? size_t(2) : size_t(4)};
-    if (ys.shares({h, N, d_in, e}) || ys.shares({sum_out, N, d_in, e}) || ys.shares({A, (int64_t)K * d_in, r, e}) ||
-        ys.shares({B, (int64_t)K * r, d_out, e}))
-      return MOLORA_ERR_INVALID_ARG;
+    const Span ys = {y, N, d_out, y_bf16 ? size_t(2) : size_t(4)}, hs = {h, N, d_in, e}, sums = {sum_out, N, d_in, e},
+               h8s = {h8, N, d_in, 1}, scales = {scale8, N, 1, 4},
+               wss = {ws_bytes ? ws : nullptr, 1, ws_bytes ? (int64_t)*ws_bytes : 0, 1};
+    const Span read[] = {{W, d_out, d_in, size_of(w_dtype)}, {w_scale, d_out, 1, 4}, {bias, d_out, 1, 4},
+                         {A, (int64_t)K * d_in, r, e}, {B, (int64_t)K * r, d_out, e}, {ids, N, k, 4}, {w, N, k, 4},
+                         {counts, K, 1, 4}, {offsets, K + 1, 1, 4}, {perm, N, k, 4}};
+    for (const Span& in : read)
+      for (const Span* out : {&ys, &hs, &sums, &h8s, &scales, &wss})
+        if (out->shares(in)) return MOLORA_ERR_INVALID_ARG;
+    if (ys.shares(hs) || ys.shares(sums)) return MOLORA_ERR_INVALID_ARG;  // (h8 and scale8 are the product's inputs)
+    for (const Span* out : {&ys, &hs, &sums, &h8s, &scales})
+      if (wss.shares(*out)) return MOLORA_ERR_INVALID_ARG;
   }
   // With more than 256 tokens the product takes the adapters' update along (y is then written, and
   // rounded, once), if its two planes fit the workspace: K*r/32 more K blocks of 64 against a pass over y.
