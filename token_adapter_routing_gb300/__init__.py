@@ -692,6 +692,14 @@ def _array(t: Optional[torch.Tensor], name: str, shape, dtype, device):
 _TENSORS = (torch.Tensor, torch.nn.Parameter)
 
 
+def _slot_array(t: Optional[torch.Tensor], name: str, shape, dtype, device, rows=None):
+    """_array for an argument that may have any shape with the elements of `shape` (and `rows` rows), as
+    molora_lora_apply takes its slots' and its dispatch's arrays."""
+    if isinstance(t, torch.Tensor) and t.numel() == math.prod(shape) and (rows is None or (t.dim() and t.shape[0] == rows)):
+        shape = t.shape
+    return _array(t, name, shape, dtype, device)
+
+
 def _call(name: str, device, *args):
     """Calls the library with the device of that index current and raises on a status that is not OK."""
     fn = getattr(load_library(), name)
@@ -914,8 +922,8 @@ def molora_norm_linear_lora_apply(x, norm_weight, eps, W, A, B, ids, y, scale, w
             _array(W, "W", (d_out, d_in), W.dtype, dev), _TYPE_CODES[W.dtype], _array(w_scale, "w_scale", (d_out,), f32, dev),
             d_out, _array(bias, "bias", (d_out,), f32, dev), _array(A, "A", (K, d_in, r), dt, dev),
             _array(B, "B", (K, r, d_out), dt, dev), K, r, _array(ids, "ids", ids.shape, i32, dev),
-            _array(w, "w", ids.shape, f32, dev), k, _array(counts, "counts", (K,), i32, dev),
-            _array(offsets, "offsets", (K + 1,), i32, dev), _array(perm, "perm", (N * k,), i32, dev), scale,
+            _slot_array(w, "w", ids.shape, f32, dev, N), k, _slot_array(counts, "counts", (K,), i32, dev),
+            _slot_array(offsets, "offsets", (K + 1,), i32, dev), _slot_array(perm, "perm", (N * k,), i32, dev), scale,
             _array(y, "y", (N, d_out), y.dtype, dev), 1 if y.dtype == torch.bfloat16 else 0)
     _on_gpu(x, "x")
     tail = (_error_word(err_word, dev), _raw_stream(stream, dev))
