@@ -10,8 +10,8 @@
 // bias takes 16.4 us, 32 x 64 1.6 us, a launch.
 //
 // Everything the choice depends on is reproducible: e = expf(l - max) and 1 / (1 + expf(-l)) are
-// single fp32 operations, and the softmax's denominator is a sum of integers (to 2^-44 of the largest e)
-// that is rounded once, so it does not depend on the order of the sum.
+// single fp32 operations, and the softmax's denominator is a sum of integers (each e in units of 2^-44 of the
+// largest) that is rounded once, so it does not depend on the order of the sum.
 #include <type_traits>
 
 #include "common.cuh"
@@ -101,8 +101,8 @@ __device__ __forceinline__ Norms gate_choices(const GateArgs& a, float (&l)[V], 
     for (int off = TL / 2; off; off >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, off));
     n.most = m;
     if (!by_logit || !a.renorm) {
-      // e in units of 2^-22 and 2^-44, summed as integers: exact whatever the order (the rest of an e below
-      // 2^-20 is cut), 512 experts fit 32 bits
+      // e in units of 2^-22 and 2^-44, summed as integers: exact whatever the order (what an e below 2^-21
+      // has under 2^-44 is cut: 512 experts lose less than 2^-35), 512 experts fit 32 bits
       uint32_t hi = 0, lo = 0;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
