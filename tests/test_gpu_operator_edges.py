@@ -121,3 +121,21 @@ def test_infinities_leave_the_neighbours_bits(m, N, d_in, d_out):
     cols = [i for i in range(d_out) if i != 5]
     assert torch.equal(y[:, cols], plain[:, cols])
     assert torch.equal(y[:, 5], torch.where(x[:, 7] > 0, -math.inf, math.inf))
+
+
+@pytest.mark.parametrize("dtype, N, d_in, d_out", [
+    (BF, 4096, 4096, 2048), (BF, 16, 4096, 10240), (F32, 1000, 4096, 4096), (BF, 1000, 4095, 4096), (F32, 1000, 4095, 4096),
+    # d_in over several CTAs, and the CUDA cores
+    (BF, 16, 4096, 4096), (BF, 300, 4096, 512), (F32, 64, 4096, 1024), (F32, 2, 4096, 1024)])
+def test_long_sums_do_not_drift(m, dtype, N, d_in, d_out):
+    """fp32 y of positive products, whose partial sums only grow.  A tensor core cuts what an addition loses, half a
+    step (2^-24 of the sum or less) on the mean.  Sums of 32 MMAs that registers add lose 2^-24 sum_j j / 32 =
+    1.0e-6 at most, and fp32's further products, 2^-7 of the first, 640 in a chain, 3e-7; one chain of 256 would
+    lose 2^-25 sum_j j / 256 = 3.8e-6 at least."""
+    g = gen(d_in)
+    x = (0.5 + 0.5 * torch.rand(N, d_in, generator=g, device="cuda")).to(dtype)
+    W = (0.5 + 0.5 * torch.rand(d_out, d_in, generator=g, device="cuda")).to(dtype)
+    y = m.molora_linear(x, W).double()
+    want = x.double() @ W.double().T
+    drift = ((y - want) / want).mean().abs().item()
+    assert drift <= 1.5e-6, drift
