@@ -501,8 +501,8 @@ MOLORA_API molora_status molora_rmsnorm(const void* x, molora_dtype dtype, int64
  *
  * Equal choices, and equal groups, order by the lower index first.  Scores are fp32 (each of the
  * softmax's exponentials is cut to a multiple of 2^-44; their sum, 1 or more and so within 2^-35 of the whole one's,
- * is exact and rounded once, so that no result depends on an order of additions).  Without a bias, and with one group or group_top 1, the choice is the logit
- * itself: the same order, without the ties that rounding makes.
+ * is exact and rounded once, so that no result depends on an order of additions).  Without a bias, and with one group
+ * or group_top 1, the choice is the logit itself: the same order, without the ties that rounding makes.
  * Experts with a logit of -inf (masked) or NaN, or a choice of -inf or NaN, are left out; a NaN
  * also sets MOLORA_DEV_BAD_LOGIT.  A logit of +inf counts as the largest finite one.  A group
  * with fewer than group_top experts left ranks behind every other.  A token with fewer than k

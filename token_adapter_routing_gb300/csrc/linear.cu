@@ -960,7 +960,7 @@ struct Piece<__nv_fp8_e4m3, kVec> {
 }  // namespace
 
 // Operands that TMA cannot fetch or the tensor cores do not multiply: rows that start anywhere, and fp32.
-// The orientation and the split of linear_skinny_kernel; 8 warps fetch both operands and lay them out
+// The orientation and the split of linear_skinny_kernel; 15 warps fetch both operands and lay them out
 // as bf16 planes in the swizzled stages.  fp32 is three planes, x = x1 + x2 + x3 exactly, and
 //   x w = x1 w1 + x1 w2 + x2 w1 + x2 w2 + x1 w3 + x3 w1 + (terms below 2^-21 of |x w|, 2^-24 of it on average)
 // which is six bf16 products with fp32 sums: an fp32 product at a sixth of the bf16 rate, four times the CUDA
