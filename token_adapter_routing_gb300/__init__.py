@@ -666,10 +666,11 @@ def molora_lora_apply_masked_pass(x, A, B, adapter_of, a, y, scale, err_word=Non
 _TYPE_CODES = {torch.float32: F32, torch.bfloat16: BF16, torch.float8_e4m3fn: E4M3}
 
 
-def _array(t: Optional[torch.Tensor], name: str, shape, dtype, device):
+def _array(t: Optional[torch.Tensor], name: str, shape, dtype, device, rows=None):
     """The device pointer of a tensor argument of this shape, dtype and device index (None for None).
     That the device is a GPU is checked by _on_gpu, last, so that a mis-sized argument is reported as
-    such.  (One quick test first: a call has up to 18 of these.)"""
+    such.  With `rows`, any shape of as many elements and that many rows (0: whatever the rows) will do, as
+    molora_lora_apply takes its slots' and its dispatch's arrays.  (One quick test first: a call has up to 18 of these.)"""
     if t is None:
         return None
     if (type(t) in _TENSORS and t.dtype is dtype and t.shape == shape and t.get_device() == device and
@@ -677,7 +678,7 @@ def _array(t: Optional[torch.Tensor], name: str, shape, dtype, device):
         return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name} must be a tensor")
-    if t.shape != shape:
+    if t.shape != shape and (rows is None or t.numel() != math.prod(shape) or (rows and t.shape[:1] != (rows,))):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
@@ -690,14 +691,6 @@ def _array(t: Optional[torch.Tensor], name: str, shape, dtype, device):
 
 
 _TENSORS = (torch.Tensor, torch.nn.Parameter)
-
-
-def _slot_array(t: Optional[torch.Tensor], name: str, shape, dtype, device, rows=None):
-    """_array for an argument that may have any shape with the elements of `shape` (and `rows` rows), as
-    molora_lora_apply takes its slots' and its dispatch's arrays."""
-    if isinstance(t, torch.Tensor) and t.numel() == math.prod(shape) and (rows is None or (t.dim() and t.shape[0] == rows)):
-        shape = t.shape
-    return _array(t, name, shape, dtype, device)
 
 
 def _call(name: str, device, *args):
@@ -922,8 +915,8 @@ def molora_norm_linear_lora_apply(x, norm_weight, eps, W, A, B, ids, y, scale, w
             _array(W, "W", (d_out, d_in), W.dtype, dev), _TYPE_CODES[W.dtype], _array(w_scale, "w_scale", (d_out,), f32, dev),
             d_out, _array(bias, "bias", (d_out,), f32, dev), _array(A, "A", (K, d_in, r), dt, dev),
             _array(B, "B", (K, r, d_out), dt, dev), K, r, _array(ids, "ids", ids.shape, i32, dev),
-            _slot_array(w, "w", ids.shape, f32, dev, N), k, _slot_array(counts, "counts", (K,), i32, dev),
-            _slot_array(offsets, "offsets", (K + 1,), i32, dev), _slot_array(perm, "perm", (N * k,), i32, dev), scale,
+            _array(w, "w", ids.shape, f32, dev, N), k, _array(counts, "counts", (K,), i32, dev, 0),
+            _array(offsets, "offsets", (K + 1,), i32, dev, 0), _array(perm, "perm", (N * k,), i32, dev, 0), scale,
             _array(y, "y", (N, d_out), y.dtype, dev), 1 if y.dtype == torch.bfloat16 else 0)
     _on_gpu(x, "x")
     tail = (_error_word(err_word, dev), _raw_stream(stream, dev))

@@ -163,16 +163,13 @@ static bool on_element(const void* p, size_t size) { return (reinterpret_cast<ui
 // in 32 bits.
 static constexpr int32_t kMostSize = INT32_MAX - 1023;
 
-// Rows x columns of `size` bytes at p.  An absent array shares nothing with another.
+// Rows x columns of `size` bytes at p.  An absent or empty array shares nothing with another.
 struct Span {
   const void* p;
-  int64_t rows, cols;
-  size_t size;
-  bool shares(const Span& o) const {
-    if (!p || !o.p) return false;
-    const unsigned __int128 a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(o.p);
-    return a < b + (unsigned __int128)o.rows * o.cols * o.size && b < a + (unsigned __int128)rows * cols * size;
-  }
+  unsigned __int128 first, last;
+  Span(const void* at, int64_t rows, int64_t cols, size_t size)
+      : p(at), first(reinterpret_cast<uintptr_t>(at)), last(at && rows && cols ? first + (unsigned __int128)rows * cols * size : 0) {}
+  bool shares(const Span& o) const { return first < o.last && o.first < last; }
   // as an output that may be the other array itself
   bool shares_part(const Span& o) const { return p != o.p && shares(o); }
 };
