@@ -139,3 +139,24 @@ def test_long_sums_do_not_drift(m, dtype, N, d_in, d_out):
     want = x.double() @ W.double().T
     drift = ((y - want) / want).mean().abs().item()
     assert drift <= 1.5e-6, drift
+
+
+@pytest.mark.parametrize("N", [16, 300])
+def test_an_empty_workspace_is_none(m, N):
+    """A buffer of the 0 bytes that a size query may give: the calls run, as they do without one."""
+    g = gen(N)
+    d, K, r = 256, 4, 16
+    x, nw = randn(g, N, d).to(BF), torch.ones(d, dtype=BF, device="cuda")
+    W, A, B = randn(g, d, d).to(BF), randn(g, K, d, r).to(BF), randn(g, K, r, d).to(BF)
+    ids = (torch.arange(N, device="cuda") % K).to(torch.int32)
+    none = torch.empty(0, dtype=torch.uint8, device="cuda")
+    y, want = torch.ones(N, d, device="cuda"), torch.ones(N, d, device="cuda")
+    m.molora_lora_apply(x, A, B, ids, want, 2.0, path="scalar")
+    m.molora_lora_apply(x, A, B, ids, y, 2.0, path="scalar", ws=none)
+    assert torch.equal(y, want) and not (y == 1).all()
+    y.fill_(7.0)
+    _, _, h, _, _ = m.molora_norm_linear_lora_apply(x, nw, 1e-6, W, A, B, ids, y, 2.0, ws=none)
+    want = h.double() @ W.double().T
+    for a in range(K):
+        want += 2.0 * (ids == a).double()[:, None] * ((h.double() @ A[a].double()) @ B[a].double())
+    assert (y.double() - want).abs().max() <= 2e-4 * want.pow(2).mean().sqrt()  # the apply's own bar

@@ -220,7 +220,8 @@ def _workspace(ws: Optional[torch.Tensor], device, call, stream=None) -> int:
     """Runs `call(ws_ptr, ws_bytes_ptr)` under the library's workspace convention and returns
     its status: with no caller buffer it first queries the size and, if one is needed,
     allocates it on `device` (torch's caching allocator; inside a CUDA graph capture the
-    graph's pool; of `stream`'s memory if given)."""
+    graph's pool; of `stream`'s memory if given).  An empty buffer (what a size of 0 makes; it has no address, which
+    would be a query) is none."""
     size = ctypes.c_size_t(0)
     if ws is None:
         status = call(None, ctypes.byref(size))
@@ -232,6 +233,8 @@ def _workspace(ws: Optional[torch.Tensor], device, call, stream=None) -> int:
             ws = torch.empty(size.value, dtype=torch.uint8, device=device)
     else:
         _cuda(ws, "ws", torch.uint8, device=device)
+        if ws.numel() == 0:
+            return call(None, None)
     size.value = ws.numel()
     return call(_p(ws), ctypes.byref(size))
 
