@@ -12,8 +12,8 @@
 //   tile's W rows: a pair reads every operand byte once from shared memory per MMA, which
 //   one CTA alone cannot feed at full rate.  A TMA warp and an MMA warp run ahead of 12 (or 8, see
 //   tc_sides) epilogue warps by two TMEM accumulators.  Bound by the tensor cores: 8192 x 4096 x 4096 bf16
-//   142 us (1940 TFLOP/s; tensor pipe active in 89% of the cycles), 148 with bias, SiLU and residual; e4m3
-//   78 us (3500).  4096 x 2048 x 6144 e4m3 with scales, bias and GELU's tanh form 40 us, 36 without: there
+//   143 us (1920 TFLOP/s; tensor pipe active in 89% of the cycles), 151 with bias, SiLU and residual (165 and 174 in
+//   a long loop, at the power limit); e4m3 76 us (3600).  4096 x 2048 x 6144 e4m3 with scales, bias and GELU's tanh form 40 us, 36 without: there
 //   the epilogue of 224 columns is nearly as long as a tile's 16 K blocks.
 // linear_skinny_kernel (few tokens): W's rows are the MMA's M (128 outputs a CTA), the tokens its N
 //   (16 .. 256), so that no MMA row is spent on tokens that are not there; d_in is split over a
@@ -969,8 +969,8 @@ struct Piece<__nv_fp8_e4m3, kVec> {
 // are NaN, no others, are summed again on the CUDA cores, so that no token's bits or time depend on its neighbours'.
 //
 // Bound by the threads that cut the operands: 15 warps, with their next pieces on the way while a stage is
-// written and handed over.  1024 x 4096 x 4096 fp32 343 us (100 TFLOP/s, 577 us for the library's fp32 product);
-// of 5400 cycles a K block, the MMAs are 1500 and the operands' way from L2 1000.
+// written and handed over.  1024 x 4096 x 4096 fp32 324 us (106 TFLOP/s, 577 us for the library's fp32 product);
+// of 5100 cycles a K block, the MMAs are 1500 and the operands' way from L2 1000.
 template <typename T, bool kVec, int J>
 __global__ void __launch_bounds__(kAnyThreads, 1)
     linear_any_kernel(const Epi E, const AnyPlan P, const T* __restrict__ x, const T* __restrict__ W, int32_t d_in,
@@ -1491,7 +1491,8 @@ cudaError_t launch_few(const LinearArgs& a, cudaStream_t stream) {
 //   rows that start anywhere, two tokens, four of fp32:  4095 x 4096 fp32 8.2, 10 and 17, 26; bf16 8.7 and 12.5, 14;
 //     e4m3 8.7 and 12.6, 16; but four tokens of bf16 17, 14
 //   bf16 and e4m3, up to four tokens that are 8 KB together, up to 2 MB of W:  1024 x 1024 bf16 2.5, 2.5 and 2.7,
-//     4.2; e4m3 2.4 to 2.8, 3.8; one token of 4096 -> 512 bf16 5.4, 5.7; of 4096 -> 4096 e4m3 7.6, 6.5
+//     4.2; e4m3 2.4 to 2.8, 3.8; one token of 4096 -> 512 bf16 5.4, 5.7; of 4096 -> 4096 e4m3 7.6, 6.5, bf16 7.2, 7.4
+//     with W in L2 and 12.3, 9.3 from HBM
 // Returns cudaErrorNotSupported where it is not.
 cudaError_t try_few(const LinearArgs& a, cudaStream_t stream) {
   using F = float;
