@@ -38,20 +38,11 @@ namespace molora {
 
 namespace {
 
-constexpr int kRows = 128;          // rows of a box of x (or of W in the skinny kernel) = TMEM lanes
-constexpr uint32_t kRowBytes = 128; // bytes of K per stage
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 32 * (kEpiWarps + 2);  // + TMA warp (8) + MMA warp (9)
 constexpr int kAnyThreads = 512;    // linear_any_kernel: 15 warps that lay out operands + MMA warp (15)
 constexpr int kCutters = kAnyThreads - 32;
-// More bytes in flight take longer to come: one token, 4096 x 4096 bf16 from HBM 9.4 us with 4 stages, 8.8
-// with 8, 10.0 with 12 (from L2 7.1, 7.4, 8.2).
-constexpr int kMaxStages = 8;
 constexpr int kSpan = 8;            // K blocks summed in TMEM before fp32 registers take over
-constexpr uint32_t kTurn = 4096;    // 32 x 32 values of fp32 y
-constexpr size_t kMaxSmem = 227 * 1024;
-constexpr size_t kSmemSlack = 1024;
-constexpr uint32_t kBox = 2048;     // of the epilogue's staging: 32 rows x 64 bytes
 
 struct __align__(8) LCtrl {
   uint64_t full[kMaxStages];
@@ -89,28 +80,6 @@ struct TcPlan {
   uint32_t stage_bytes, off_b, off_stage, off_ctrl, tmem_cols, smem;
 };
 
-__device__ __forceinline__ void apply_act(float (&v)[32], molora_activation act) {
-  if (act == MOLORA_ACT_NONE) return;
-  if (act == MOLORA_ACT_RELU) {
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = activate(v[i], MOLORA_ACT_RELU);
-  } else if (act == MOLORA_ACT_SILU) {
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = activate(v[i], MOLORA_ACT_SILU);
-  } else if (act == MOLORA_ACT_GELU_TANH) {
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = activate(v[i], MOLORA_ACT_GELU_TANH);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = activate(v[i], MOLORA_ACT_GELU);
-  }
-}
-
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-  const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&p);
-}
-
 // The sums of a tile of 128 outputs x tokens that its 8 epilogue warps keep: warp w's lanes have outputs
 // 32 (w % 4) .. + 31, columns 16 (w / 4) + 32 j .. + 15.  TMEM's own are added every kSpan K blocks,
 // in two buffers of BN columns in turn (see linear_tc_kernel).
@@ -145,49 +114,6 @@ struct TileSums {
     __syncwarp();
     if ((threadIdx.x & 31) == 0) mbar_arrive(&ctrl->tempty[c & 1]);
     return true;
-  }
-};
-
-// Four consecutive outputs o .. o + 3 of a token as the epilogue reads and writes them: in one access
-// where `vec` (rows of 4-element pieces on 16-byte boundaries), else one by one, those past d_out left out.
-struct Quad {
-  float v[4];
-  __device__ __forceinline__ void load(const float* p, int o, int d_out, bool vec) {
-    if (vec) {
-      const float4 q = *reinterpret_cast<const float4*>(p + o);
-      v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = o + i < d_out ? p[o + i] : 0.f;
-    }
-  }
-  __device__ __forceinline__ void load(const __nv_bfloat16* p, int o, int d_out, bool vec) {
-    if (vec) {
-      const uint2 q = *reinterpret_cast<const uint2*>(p + o);
-      v[0] = __uint_as_float(q.x << 16), v[1] = __uint_as_float(q.x & 0xffff0000u);
-      v[2] = __uint_as_float(q.y << 16), v[3] = __uint_as_float(q.y & 0xffff0000u);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = o + i < d_out ? __bfloat162float(p[o + i]) : 0.f;
-    }
-  }
-  __device__ __forceinline__ void store(float* p, int o, int d_out, bool vec) const {
-    if (vec) {
-      *reinterpret_cast<float4*>(p + o) = make_float4(v[0], v[1], v[2], v[3]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (o + i < d_out) p[o + i] = v[i];
-    }
-  }
-  __device__ __forceinline__ void store(__nv_bfloat16* p, int o, int d_out, bool vec) const {
-    if (vec) {
-      *reinterpret_cast<uint2*>(p + o) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (o + i < d_out) p[o + i] = __float2bfloat16_rn(v[i]);
-    }
   }
 };
 
@@ -1232,6 +1158,8 @@ PFN_cuTensorMapEncodeTiled_v12000 linear_encoder() {
   return fn;
 }
 
+}  // namespace
+
 bool linear_map(CUtensorMap* m, CUtensorMapDataType type, uint32_t esize, const void* base, uint64_t rows, uint64_t cols,
                 uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle swz) {
   auto enc = linear_encoder();
@@ -1244,26 +1172,25 @@ bool linear_map(CUtensorMap* m, CUtensorMapDataType type, uint32_t esize, const 
              CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
-
-uint32_t tmem_columns(uint32_t n) {
-  uint32_t c = 32;
-  while (c < n) c *= 2;
-  return c;
+bool linear_map_3d(CUtensorMap* m, CUtensorMapDataType type, const void* base, const uint64_t (&size)[3],
+                   const uint64_t (&step)[2], const uint32_t (&box)[3], CUtensorMapSwizzle swz) {
+  auto enc = linear_encoder();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {size[0], size[1], size[2]};
+  cuuint64_t strides[2] = {step[0], step[1]};
+  cuuint32_t boxes[3] = {box[0], box[1], box[2]};
+  cuuint32_t es[3] = {1, 1, 1};
+  return enc(m, type, 3, const_cast<void*>(base), dims, strides, boxes, es, CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+
+namespace {
 
 bool operand_map(CUtensorMap* m, const LinearArgs& a, const void* base, int64_t rows, uint32_t box_rows) {
   const bool fp8 = a.dtype == MOLORA_E4M3;
   return linear_map(m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, fp8 ? 1 : 2, base,
                     (uint64_t)rows, (uint64_t)a.d_in, fp8 ? 128 : 64, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
 }
-
-// How many clusters of 1 to 8 CTAs (one an SM) the current device holds at once: its groups of SMs are not
-// multiples of every size (on GB300's 152 SMs: 76 of 2, 36 of 4, 23 of 6, 15 of 8).  Asked for once a
-// device; one look at the current device a call, since a small product is over in 4 us.
-struct Resident {
-  int of[9];
-};
 
 int ask_resident(int C) {
   static std::atomic<uint64_t> allowed;
@@ -1285,6 +1212,8 @@ int ask_resident(int C) {
   return num_sms() / C * 3 / 4;
 }
 
+}  // namespace
+
 Resident resident_clusters() {
   static std::atomic<int> known[64][9];
   int dev = -1;
@@ -1300,13 +1229,7 @@ Resident resident_clusters() {
   return r;
 }
 
-// How many CTAs share a tile's d_in of nkb blocks: as many as let every tile have its cluster at once,
-// two blocks each at least.
-int split_of(const Resident& r, int64_t tiles, int nkb) {
-  for (int C = 8; C > 1; --C)
-    if (nkb >= 2 * C && tiles <= r.of[C]) return C;
-  return 1;
-}
+namespace {
 
 Epi epilogue_of(const LinearArgs& a) {
   Epi e = {a.x_scale, a.w_scale, a.bias, a.residual, a.y, a.N, a.d_out, a.act, a.y_bf16, false};

@@ -1,10 +1,12 @@
-// linear.cuh -- what the kernels of the base product share: the epilogue's activation and the
-// conversions of its element types.
+// linear.cuh -- what the kernels of the products share: the epilogue's activation, the conversions of its
+// element types and its pieces of four outputs, the boxes that operands and outputs move in, tensor maps, and
+// how a product splits over clusters.
 #pragma once
 
 #include <cuda_fp8.h>
 
 #include "common.cuh"
+#include "kernels.h"
 
 namespace molora {
 
@@ -94,5 +96,113 @@ __device__ __forceinline__ void umma_stage(uint32_t d, uint32_t a, uint32_t b, u
     MOLORA_UMMA4("1", "f16");
 }
 #undef MOLORA_UMMA4
+
+constexpr int kRows = 128;          // rows of a box of x (or of W in the skinny kernels) = TMEM lanes
+constexpr uint32_t kRowBytes = 128; // bytes of K per stage
+// More bytes in flight take longer to come: one token, 4096 x 4096 bf16 from HBM 9.4 us with 4 stages, 8.8
+// with 8, 10.0 with 12 (from L2 7.1, 7.4, 8.2).
+constexpr int kMaxStages = 8;
+constexpr uint32_t kTurn = 4096;    // 32 x 32 values of fp32 y
+constexpr size_t kMaxSmem = 227 * 1024;
+constexpr size_t kSmemSlack = 1024;
+constexpr uint32_t kBox = 2048;     // of the epilogue's staging: 32 rows x 64 bytes
+
+__device__ __forceinline__ void apply_act(float (&v)[32], molora_activation act) {
+  if (act == MOLORA_ACT_NONE) return;
+  if (act == MOLORA_ACT_RELU) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = activate(v[i], MOLORA_ACT_RELU);
+  } else if (act == MOLORA_ACT_SILU) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = activate(v[i], MOLORA_ACT_SILU);
+  } else if (act == MOLORA_ACT_GELU_TANH) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = activate(v[i], MOLORA_ACT_GELU_TANH);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = activate(v[i], MOLORA_ACT_GELU);
+  }
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&p);
+}
+
+// Four consecutive outputs o .. o + 3 of a token as the epilogue reads and writes them: in one access
+// where `vec` (rows of 4-element pieces on 16-byte boundaries), else one by one, those past d_out left out.
+struct Quad {
+  float v[4];
+  __device__ __forceinline__ void load(const float* p, int o, int d_out, bool vec) {
+    if (vec) {
+      const float4 q = *reinterpret_cast<const float4*>(p + o);
+      v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = o + i < d_out ? p[o + i] : 0.f;
+    }
+  }
+  __device__ __forceinline__ void load(const __nv_bfloat16* p, int o, int d_out, bool vec) {
+    if (vec) {
+      const uint2 q = *reinterpret_cast<const uint2*>(p + o);
+      v[0] = __uint_as_float(q.x << 16), v[1] = __uint_as_float(q.x & 0xffff0000u);
+      v[2] = __uint_as_float(q.y << 16), v[3] = __uint_as_float(q.y & 0xffff0000u);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = o + i < d_out ? __bfloat162float(p[o + i]) : 0.f;
+    }
+  }
+  __device__ __forceinline__ void store(float* p, int o, int d_out, bool vec) const {
+    if (vec) {
+      *reinterpret_cast<float4*>(p + o) = make_float4(v[0], v[1], v[2], v[3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (o + i < d_out) p[o + i] = v[i];
+    }
+  }
+  __device__ __forceinline__ void store(__nv_bfloat16* p, int o, int d_out, bool vec) const {
+    if (vec) {
+      *reinterpret_cast<uint2*>(p + o) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (o + i < d_out) p[o + i] = __float2bfloat16_rn(v[i]);
+    }
+  }
+};
+
+inline bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
+
+inline uint32_t tmem_columns(uint32_t n) {
+  uint32_t c = 32;
+  while (c < n) c *= 2;
+  return c;
+}
+
+// A tensor map of `rows` dense rows of `cols` elements of esize bytes, in boxes of box_rows x box_cols.  False if the
+// driver makes none of it.
+bool linear_map(CUtensorMap* m, CUtensorMapDataType type, uint32_t esize, const void* base, uint64_t rows, uint64_t cols,
+                uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle swz);
+// The same of three dimensions, the densest first; step: the bytes from one element of the second, and of the third, to
+// the next.
+bool linear_map_3d(CUtensorMap* m, CUtensorMapDataType type, const void* base, const uint64_t (&size)[3],
+                   const uint64_t (&step)[2], const uint32_t (&box)[3], CUtensorMapSwizzle swz);
+
+// How many clusters of 1 to 8 CTAs (one an SM) the current device holds at once: its groups of SMs are not
+// multiples of every size (on GB300's 152 SMs: 76 of 2, 36 of 4, 23 of 6, 15 of 8).  Asked for once a
+// device; one look at the current device a call, since a small product is over in 4 us.
+struct Resident {
+  int of[9];
+};
+Resident resident_clusters();
+
+// How many CTAs share a tile's d_in of nkb blocks: as many as let every tile have its cluster at once,
+// two blocks each at least.
+inline int split_of(const Resident& r, int64_t tiles, int nkb) {
+  for (int C = 8; C > 1; --C)
+    if (nkb >= 2 * C && tiles <= r.of[C]) return C;
+  return 1;
+}
 
 }  // namespace molora

@@ -24,7 +24,7 @@ namespace molora {
 
 namespace {
 
-constexpr int kRows = 128, kKBlock = 64;
+constexpr int kKBlock = 64;
 constexpr int kEpiWarps = 8, kThreads = 32 * (kEpiWarps + 2);
 constexpr int kStages = 6;
 constexpr size_t kSlack = 1024, kSmemLimit = 227 * 1024;
