@@ -70,11 +70,13 @@ typedef enum {
                                        its fixed scratch holds */
 } molora_status;
 
-/* MOLORA_E4M3 (8 bits: sign, 4 exponent, 3 fraction; largest value 448) is taken by molora_linear
- * and as the base weights' type by molora_norm_linear_lora_apply; every other call refuses it. */
+/* MOLORA_E4M3 (8 bits: sign, 4 exponent, 3 fraction; largest value 448) is taken by molora_linear and
+ * molora_gated_linear and as the base weights' type by molora_norm_linear_lora_apply; every other call that
+ * takes a type refuses it. */
 typedef enum { MOLORA_F32 = 0, MOLORA_BF16 = 1, MOLORA_E4M3 = 2 } molora_dtype;
 
-/* Activation in molora_linear's epilogue. */
+/* Activation in the products' epilogues (molora_linear, molora_linear_blocks), and of the gate in
+ * molora_gated_linear. */
 typedef enum {
   MOLORA_ACT_NONE = 0,
   MOLORA_ACT_RELU = 1,
@@ -118,6 +120,7 @@ typedef enum {
 #define MOLORA_MAX_EXPERTS 512   /* K of molora_gate_topk: experts scored */
 #define MOLORA_MAX_GATE_K 32     /* k of molora_gate_topk: experts chosen */
 #define MOLORA_MAX_GROUPS 32     /* groups of molora_gate_topk */
+#define MOLORA_SCALE_BLOCK 128   /* columns (and, of weights, rows) that share a scale in the block-scaled calls */
 
 /* Flags of the *_ex routing calls (molora_route_vocab_ex, molora_route_vocab_dispatch_ex,
  * molora_route_vocab_lora_apply_ex): see molora_route_vocab_dispatch_ex for the promise. */
@@ -573,6 +576,79 @@ MOLORA_API molora_status molora_norm_linear_lora_apply(
     const int32_t* ids, const float* w, int32_t k, const int32_t* counts, const int32_t* offsets,
     const int32_t* perm, float scale, void* y, int32_t y_bf16, void* ws, size_t* ws_bytes, int32_t* err_word,
     cudaStream_t stream);
+
+/*
+ * molora_quantise_blocks -- e4m3 of every row with a scale for each block of 128 columns (the last block may be
+ * shorter): the x that molora_linear_blocks and molora_gated_linear read.
+ *
+ *   scale8[t,b] = max(max_{i in block b} |x[t,i]|, 2^-64) / 448
+ *   out8[t,i]   = x[t,i] * (1 / scale8[t,b]), as molora_rmsnorm's out8
+ *
+ * A NaN in a block makes its scale and all its values NaN; an infinity makes its scale infinite and itself NaN, the
+ * block's other values 0.
+ *
+ * x [N x d] dtype (MOLORA_BF16 or MOLORA_F32);  out8 [N x d] e4m3;  scale8 fp32 [N x ceil(d / 128)];  d >= 1, N and d up to
+ * 2^31 - 1024.  Arrays start on a boundary of their element's size (rows on 16-byte boundaries are faster).  No array
+ * shares memory with another (refused).
+ */
+MOLORA_API molora_status molora_quantise_blocks(const void* x, molora_dtype dtype, int64_t N, int32_t d, void* out8,
+                                     float* scale8, cudaStream_t stream);
+
+/*
+ * molora_linear_blocks -- the base product of weights stored in e4m3 with a scale for each block of 128 x 128:
+ *
+ *   y[t,o] = act(sum_b x_scale[t,b] * w_scale[o / 128, b] * sum_{i in block b} x[t,i] W[o,i] + bias[o]) + residual[t,o]
+ *
+ * x [N x d_in] and W [d_out x d_in] e4m3;  x_scale fp32 [N x ceil(d_in / 128)] (x and x_scale as molora_quantise_blocks
+ * makes them);  w_scale fp32 [ceil(d_out / 128) x ceil(d_in / 128)].  bias, act, residual, y and y_bf16 as for molora_linear.
+ * A block's products are summed by the tensor cores, the scaled blocks in fp32 in order; the epilogue is fp32 and y is rounded
+ * once.  d_in is a multiple of 16 (else MOLORA_ERR_UNSUPPORTED); N, d_in, d_out up to 2^31 - 1024; x and W are 16-byte aligned,
+ * the other arrays start on a boundary of their element's size.  y shares no memory with another array but may be the
+ * residual.  Results are reproducible bit for bit.  Outputs that a wait that ran out (MOLORA_DEV_WAIT_TIMEOUT) left without
+ * their sums are NaN, or stay as they were; the others are right.
+ */
+MOLORA_API molora_status molora_linear_blocks(const void* x, const float* x_scale, int64_t N, int32_t d_in, const void* W,
+                                   const float* w_scale, int32_t d_out, const float* bias, molora_activation act,
+                                   const void* residual, void* y, int32_t y_bf16, int32_t* err_word,
+                                   cudaStream_t stream);
+
+/*
+ * molora_gated_linear -- the gated half of a feed-forward block: both projections, the activation and their product
+ * in one kernel.
+ *
+ *   g = x Wg^T,  u = x Wu^T,  h[t,f] = act(g[t,f]) * u[t,f]
+ *
+ * x [N x d_in] and W [2 d_ff x d_in], the d_ff rows of Wg before those of Wu, share dtype: MOLORA_BF16, or MOLORA_E4M3
+ * with a scale for each block of 128: x_scale fp32 [N x ceil(d_in / 128)] and w_scale fp32
+ * [2 ceil(d_ff / 128) x ceil(d_in / 128)], Wg's blocks of rows before Wu's; both NULL with MOLORA_BF16.  h bf16 [N x d_ff].
+ * proj (MOLORA_BF16 only) bf16 [N x 2 x roundup8(d_ff)] or NULL: g and u, rounded, for the backward pass; columns from
+ * d_ff on are unspecified.  h is made of the unrounded g and u in fp32 and rounded once.
+ * d_in is a multiple of 8 (MOLORA_BF16) or 16 (MOLORA_E4M3), else MOLORA_ERR_UNSUPPORTED; d_ff up to 2^30 - 1024, N and d_in
+ * up to 2^31 - 1024; x, W and proj are 16-byte aligned, the other arrays start on a boundary of their element's size.
+ * h and proj share no memory with another array.  Results are reproducible bit for bit.  Lost waits as for molora_linear_blocks.
+ * The way back to the model's width is molora_linear (or molora_quantise_blocks and molora_linear_blocks) with the residual.
+ */
+MOLORA_API molora_status molora_gated_linear(const void* x, molora_dtype dtype, const float* x_scale, int64_t N, int32_t d_in,
+                                  const void* W, const float* w_scale, int32_t d_ff, molora_activation act, void* h,
+                                  void* proj, int32_t* err_word, cudaStream_t stream);
+
+/*
+ * molora_gated_linear_backward -- the gradients of molora_gated_linear (MOLORA_BF16) from that of h:
+ *
+ *   dg = dh * u * act'(g),  du = dh * act(g)
+ *   dx = dg Wg + du Wu,     dW = [dg^T x; du^T x]
+ *
+ * proj: as molora_gated_linear wrote it;  dh bf16 [N x d_ff];  dproj bf16 [N x 2 x roundup8(d_ff)]: dg and du, rounded,
+ * which the two products read, an output (proj itself allowed);  dx bf16 [N x d_in] or NULL (the weights' gradient
+ * alone);  dW bf16 [2 d_ff x d_in] or NULL (frozen weights, as when adapters are trained through them).  x may be NULL
+ * without dW, W without dx.  Outputs are overwritten, not added to; N == 0 makes dW zero.
+ * act' of RELU is 0 at 0.  Sums are fp32, outputs rounded once.  Sizes and alignment as for molora_gated_linear; dproj, dx and
+ * dW are 16-byte aligned too.  No output shares memory with another array, but dproj may be proj.  Results are reproducible
+ * bit for bit.  Outputs that a wait that ran out left without their sums stay as they were.
+ */
+MOLORA_API molora_status molora_gated_linear_backward(const void* x, molora_dtype dtype, int64_t N, int32_t d_in, const void* W,
+                                           int32_t d_ff, molora_activation act, const void* proj, const void* dh,
+                                           void* dproj, void* dx, void* dW, int32_t* err_word, cudaStream_t stream);
 
 /* The kernel family molora_lora_apply would choose for this shape when given a workspace
  * (never AUTO; without one, a STACKED choice becomes the best path that needs none). */

@@ -30,11 +30,12 @@ __all__ = [
     "molora_route_vocab", "molora_router_topk", "molora_dispatch", "molora_route_vocab_dispatch",
     "molora_lora_apply", "molora_lora_apply_masked_pass", "molora_route_vocab_lora_apply",
     "molora_router_lora_apply", "molora_rmsnorm", "molora_gate_topk", "molora_linear",
-    "molora_norm_linear_lora_apply", "molora_select_path", "molora_workspace_bytes", "molora_lora_apply_static_ws",
+    "molora_norm_linear_lora_apply", "molora_quantise_blocks", "molora_linear_blocks", "molora_gated_linear",
+    "molora_gated_linear_backward", "molora_select_path", "molora_workspace_bytes", "molora_lora_apply_static_ws",
     "molora_selftest_bounded_wait", "library_path", "load_library",
     "MoloraError", "PATHS", "DEV_TOKEN_OUTSIDE_RANGES", "DEV_BAD_RANGES", "DEV_BAD_ADAPTER_ID",
     "DEV_BAD_PERMUTATION", "DEV_WAIT_TIMEOUT", "DEV_BAD_LOGIT", "MAX_ADAPTERS", "MAX_EXPERTS", "MAX_GATE_K",
-    "MAX_GROUPS", "ROUTER_HIDDEN", "ACTIVATIONS", "SCORES",
+    "MAX_GROUPS", "SCALE_BLOCK", "ROUTER_HIDDEN", "ACTIVATIONS", "SCORES",
 ]
 
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CUDA, ERR_SCRATCH_TOO_SMALL = 0, 1, 2, 3, 4
@@ -54,6 +55,7 @@ MAX_EXPERTS, MAX_GATE_K, MAX_GROUPS = 512, 32, 32
 ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 SCORES = {"softmax": 0, "sigmoid": 1}
 ROUTER_HIDDEN = 64
+SCALE_BLOCK = 128  # columns (and, of weights, rows) that share a scale in the block-scaled calls
 
 EXPORTED = ("molora_route_vocab", "molora_route_vocab_ex", "molora_router_topk", "molora_dispatch", "molora_route_vocab_dispatch",
             "molora_route_vocab_dispatch_ex", "molora_route_vocab_lora_apply_ex",
@@ -61,7 +63,8 @@ EXPORTED = ("molora_route_vocab", "molora_route_vocab_ex", "molora_router_topk",
             "molora_lora_apply_ex", "molora_lora_apply_bf16y", "molora_lora_apply_indirect",
             "molora_lora_apply_masked_pass", "molora_select_path", "molora_status_string", "molora_version",
             "molora_selftest_bounded_wait", "molora_lora_apply_static_ws", "molora_rmsnorm", "molora_gate_topk",
-            "molora_linear", "molora_norm_linear_lora_apply")
+            "molora_linear", "molora_norm_linear_lora_apply", "molora_quantise_blocks", "molora_linear_blocks",
+            "molora_gated_linear", "molora_gated_linear_backward")
 
 
 class MoloraError(RuntimeError):
@@ -115,6 +118,10 @@ def load_library(path=None):
     lib.molora_linear.argtypes = [P, S, P, I64, I32, P, P, I32, P, S, P, P, I32, P, P]
     lib.molora_norm_linear_lora_apply.argtypes = [P, S, I64, I32, P, P, P, F, P, P, P, P, S, P, I32, P, P, P, I32, I32,
                                                   P, P, I32, P, P, P, F, P, I32, P, P, P, P]
+    lib.molora_quantise_blocks.argtypes = [P, S, I64, I32, P, P, P]
+    lib.molora_linear_blocks.argtypes = [P, P, I64, I32, P, P, I32, P, S, P, P, I32, P, P]
+    lib.molora_gated_linear.argtypes = [P, S, P, I64, I32, P, P, I32, S, P, P, P, P]
+    lib.molora_gated_linear_backward.argtypes = [P, S, I64, I32, P, I32, S, P, P, P, P, P, P, P]
     lib.molora_select_path.argtypes = [S, I64, I32, I32, I32, I32, I32]
     lib.molora_status_string.argtypes = [S]
     lib.molora_status_string.restype = ctypes.c_char_p
@@ -125,7 +132,8 @@ def load_library(path=None):
                  "molora_router_lora_apply", "molora_route_vocab_lora_apply", "molora_lora_apply_masked_pass",
                  "molora_select_path", "molora_version", "molora_selftest_bounded_wait",
                  "molora_lora_apply_static_ws", "molora_rmsnorm", "molora_gate_topk", "molora_linear",
-                 "molora_norm_linear_lora_apply"):
+                 "molora_norm_linear_lora_apply", "molora_quantise_blocks", "molora_linear_blocks", "molora_gated_linear",
+                 "molora_gated_linear_backward"):
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -933,6 +941,127 @@ def molora_norm_linear_lora_apply(x, norm_weight, eps, W, A, B, ids, y, scale, w
         # no path needs a workspace (they are for fp32 y, or for many tokens' update), so none is asked for
         _check("molora_norm_linear_lora_apply", call(None, None))
     return y, sum_out, h, h8, scale8
+
+
+def _scale_blocks(n):
+    return -(-n // SCALE_BLOCK)
+
+
+def molora_quantise_blocks(x, out8=None, scale8=None, stream=None):
+    """x [N, d] (bfloat16 or float32) in float8_e4m3fn with a scale for each row's block of SCALE_BLOCK columns: returns
+    (out8 [N, d], scale8 float32 [N, ceil(d / SCALE_BLOCK)]), made if not given."""
+    code = _matrix(x, "x", _FLOATS)
+    N, d = x.shape
+    dev, blocks = x.get_device(), (N, _scale_blocks(d))
+    px = _array(x, "x", x.shape, x.dtype, dev)
+    if out8 is None:
+        out8 = _new(x, x.shape, torch.float8_e4m3fn, stream)
+    if scale8 is None:
+        scale8 = _new(x, blocks, torch.float32, stream)
+    po, ps = _array(out8, "out8", x.shape, torch.float8_e4m3fn, dev), _array(scale8, "scale8", blocks, torch.float32, dev)
+    _on_gpu(x, "x")
+    _call("molora_quantise_blocks", dev, px, code, N, d, po, ps, _raw_stream(stream, dev))
+    return out8, scale8
+
+
+def molora_linear_blocks(x, x_scale, W, w_scale, y=None, bias=None, act="none", residual=None, out_dtype=torch.float32,
+                         err_word=None, stream=None):
+    """y = act(x W^T + bias) + residual for x [N, d_in] and W [d_out, d_in] in float8_e4m3fn with a scale for each block of
+    SCALE_BLOCK: x_scale float32 [N, blocks of d_in] (molora_quantise_blocks), w_scale float32 [blocks of d_out, blocks of
+    d_in].  d_in is a multiple of 16.  y, bias, act, residual and out_dtype as for molora_linear."""
+    _matrix(x, "x", (torch.float8_e4m3fn,))
+    N, d_in = x.shape
+    dev, f32 = x.get_device(), torch.float32
+    if not isinstance(W, torch.Tensor) or W.dim() != 2 or W.shape[0] < 1:
+        raise ValueError("W must be a 2-D tensor [d_out, d_in]")
+    d_out, blocks = W.shape[0], _scale_blocks(d_in)
+    act = _named(act, "act", ACTIVATIONS)
+    if x_scale is None or w_scale is None:
+        raise ValueError("x_scale and w_scale must be tensors")
+    px = _array(x, "x", x.shape, x.dtype, dev)
+    pw = _array(W, "W", (d_out, d_in), x.dtype, dev)
+    psx = _array(x_scale, "x_scale", (N, blocks), f32, dev)
+    psw = _array(w_scale, "w_scale", (_scale_blocks(d_out), blocks), f32, dev)
+    pb = _array(bias, "bias", (d_out,), f32, dev)
+    y = _y(y, N, d_out, out_dtype, x, stream)
+    pres = _array(residual, "residual", (N, d_out), y.dtype, dev)
+    py = _array(y, "y", (N, d_out), y.dtype, dev)
+    _on_gpu(x, "x")
+    _call("molora_linear_blocks", dev, px, psx, N, d_in, pw, psw, d_out, pb, act, pres, py,
+          1 if y.dtype == torch.bfloat16 else 0, _error_word(err_word, dev), _raw_stream(stream, dev))
+    return y
+
+
+def _gated_weights(W, d_in):
+    """d_ff of W [2 d_ff, d_in]: the gate's rows before the up projection's."""
+    if not isinstance(W, torch.Tensor) or W.dim() != 2 or W.shape[0] < 2 or W.shape[0] % 2:
+        raise ValueError("W must be a 2-D tensor [2 * d_ff, d_in]")
+    return W.shape[0] // 2
+
+
+def _proj_shape(N, d_ff):
+    return (N, 2, (d_ff + 7) // 8 * 8)
+
+
+def molora_gated_linear(x, W, h=None, act="silu", x_scale=None, w_scale=None, proj=None, want_proj=False, err_word=None,
+                        stream=None):
+    """The gated half of a feed-forward block: h = act(x Wg^T) * (x Wu^T), bfloat16 [N, d_ff], for x [N, d_in] and
+    W = [Wg; Wu] [2 d_ff, d_in] in bfloat16 (d_in a multiple of 8), or in float8_e4m3fn (of 16) with a scale for each block of
+    SCALE_BLOCK: x_scale float32 [N, blocks of d_in] and w_scale float32 [2 * blocks of d_ff, blocks of d_in].  Returns
+    (h, proj).  ``proj`` (bfloat16 [N, 2, d_ff rounded up to 8], bfloat16 x only): both projections, as
+    molora_gated_linear_backward reads them, written if given or if want_proj, else None."""
+    code = _matrix(x, "x", (torch.bfloat16, torch.float8_e4m3fn))
+    N, d_in = x.shape
+    dev, bf16, f32 = x.get_device(), torch.bfloat16, torch.float32
+    d_ff, blocks = _gated_weights(W, d_in), _scale_blocks(d_in)
+    act = _named(act, "act", ACTIVATIONS)
+    fp8 = code == E4M3
+    if fp8 != (x_scale is not None) or fp8 != (w_scale is not None):
+        raise ValueError("x_scale and w_scale are needed with float8_e4m3fn, and with nothing else")
+    if fp8 and (want_proj or proj is not None):
+        raise ValueError("proj is for bfloat16 x")
+    px = _array(x, "x", x.shape, x.dtype, dev)
+    pw = _array(W, "W", (2 * d_ff, d_in), x.dtype, dev)
+    psx = _array(x_scale, "x_scale", (N, blocks), f32, dev)
+    psw = _array(w_scale, "w_scale", (2 * _scale_blocks(d_ff), blocks), f32, dev)
+    if h is None:
+        h = _new(x, (N, d_ff), bf16, stream)
+    if proj is None and want_proj:
+        proj = _new(x, _proj_shape(N, d_ff), bf16, stream)
+    ph, pp = _array(h, "h", (N, d_ff), bf16, dev), _array(proj, "proj", _proj_shape(N, d_ff), bf16, dev)
+    _on_gpu(x, "x")
+    _call("molora_gated_linear", dev, px, code, psx, N, d_in, pw, psw, d_ff, act, ph, pp, _error_word(err_word, dev),
+          _raw_stream(stream, dev))
+    return h, proj
+
+
+def molora_gated_linear_backward(x, W, proj, dh, act="silu", dx=None, dW=None, dproj=None, want_dx=True, want_dW=True,
+                                 err_word=None, stream=None):
+    """The gradients of molora_gated_linear's bfloat16 form from that of h, dh [N, d_ff], and its proj: returns (dx, dW,
+    dproj), dx [N, d_in] and dW [2 d_ff, d_in], made if not given unless want_dx or want_dW is false (frozen weights need no
+    dW).  ``dproj`` (proj's shape, proj itself allowed) is the projections' gradient, made if not given."""
+    code = _matrix(x, "x", (torch.bfloat16,))
+    N, d_in = x.shape
+    dev, bf16 = x.get_device(), torch.bfloat16
+    d_ff = _gated_weights(W, d_in)
+    act = _named(act, "act", ACTIVATIONS)
+    if proj is None or dh is None:
+        raise ValueError("proj and dh must be tensors")
+    px = _array(x, "x", x.shape, bf16, dev)
+    pw = _array(W, "W", (2 * d_ff, d_in), bf16, dev)
+    pp, pdh = _array(proj, "proj", _proj_shape(N, d_ff), bf16, dev), _array(dh, "dh", (N, d_ff), bf16, dev)
+    if dx is None and want_dx:
+        dx = _new(x, x.shape, bf16, stream)
+    if dW is None and want_dW:
+        dW = _new(x, W.shape, bf16, stream)
+    if dproj is None:
+        dproj = _new(x, _proj_shape(N, d_ff), bf16, stream)
+    pdx, pdw = _array(dx, "dx", x.shape, bf16, dev), _array(dW, "dW", W.shape, bf16, dev)
+    pdp = _array(dproj, "dproj", _proj_shape(N, d_ff), bf16, dev)
+    _on_gpu(x, "x")
+    _call("molora_gated_linear_backward", dev, px, code, N, d_in, pw, d_ff, act, pp, pdh, pdp, pdx, pdw,
+          _error_word(err_word, dev), _raw_stream(stream, dev))
+    return dx, dW, dproj
 
 
 @_on_tensor_device

@@ -1,0 +1,902 @@
+// feed_forward.cu -- the products of a layer's feed-forward half on the 5th-generation tensor cores:
+//
+//   blocks:  y[t,o] = act(sum_b sx[t,b] sw[o/128,b] sum_{i in b} x[t,i] W[o,i] + bias[o]) + residual[t,o]
+//            e4m3 operands with one fp32 scale for each 128 columns of a row of x, and each 128 x 128 of W
+//   gated:   h[t,f] = act(g[t,f]) u[t,f],  [g | u] = x [Wg; Wu]^T, in bf16, or in e4m3 with such scales
+//
+// Both projections of the gated block are one product: a tile's columns are as many rows of Wg as of Wu, so that the
+// sums of g[t,f] and u[t,f] meet in the registers of one thread and neither goes to memory (unless asked for, as
+// the backward pass reads them).
+//
+// ff_tc_kernel (many tokens): linear_tc_kernel's pipeline (linear.cu): persistent pairs of CTAs with tiles of 256 tokens x
+//   BN rows of W, a TMA warp and an MMA warp ahead of 8 epilogue warps by two TMEM accumulators.  Scales change with
+//   every K block of 128, so with e4m3 an accumulator holds one K block, and the epilogue warps
+//   add it, scaled, to fp32 registers (128 a thread) while the next one's MMAs run.
+// ff_skinny_kernel (few tokens): W's rows are the MMA's M, the tokens its N, d_in split over a cluster; bound by reading W.
+#include <cudaTypedefs.h>
+
+#include <atomic>
+#ifdef MOLORA_TUNING_ENV
+#include <cstdlib>
+#endif
+
+#include "common.cuh"
+#include "kernels.h"
+#include "linear.cuh"
+
+namespace molora {
+
+namespace {
+
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 32 * (kEpiWarps + 2);  // + TMA warp (8) + MMA warp (9)
+// ff_tc_kernel: 8 epilogue warps, the TMA warp (8), the MMA warp (9) and two that only make up the warpgroup.  With e4m3 the
+// epilogue's 128 sums a thread take more than the 168 registers that 384 threads are launched with, so the
+// last warpgroup gives up its own: 256 x 224 + 128 x 56 = 384 x 168.
+constexpr int kTcThreads = 384, kEpiRegisters = 224, kOtherRegisters = 56;
+constexpr int kMaxSets = 4;  // staging boxes an epilogue warp has at most
+constexpr int kSpan = 8;     // bf16, few tokens: K blocks summed in TMEM before fp32 registers take over
+
+struct __align__(8) FCtrl {
+  uint64_t full[kMaxStages];
+  uint64_t empty[kMaxStages];
+  uint64_t tfull[2];
+  uint64_t tempty[2];
+  uint64_t done;
+  uint64_t res_full[kEpiWarps * kMaxSets];
+  uint32_t tmem_base;
+  int32_t abort;
+};
+
+// What the epilogue reads and writes.
+struct FEpi {
+  const float* sx;   // [N x nkb]
+  const float* sw;   // [blocks of W's rows x nkb]
+  const float* bias;
+  const void* res;
+  void* y;
+  void* proj;
+  int64_t N;
+  int32_t d_out;     // outputs; gated: d_ff
+  int32_t up;        // gated: Wu's first block of rows in sw
+  molora_activation act;
+  bool y_bf16;
+  bool tma_y;        // rows of y and residual on 16-byte boundaries
+};
+
+struct FPlan {
+  int BN;                // rows of W a tile
+  int S;                 // stages
+  int sets;              // staging boxes a warp
+  int nkb;               // K blocks of 128 bytes
+  int group;             // token tiles per group of tiles (they share W's rows in L2)
+  int64_t m_tiles, tiles;
+  int32_t n_tiles;
+  uint32_t stage_bytes, off_b, off_stage, off_ctrl, tmem_cols, smem;
+};
+
+}  // namespace
+
+template <bool kFp8, bool kGated, bool kY16>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    ff_tc_kernel(const FEpi E, const FPlan P, int32_t* err_word, const __grid_constant__ CUtensorMap map_x,
+                 const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_y,
+                 const __grid_constant__ CUtensorMap map_r, const __grid_constant__ CUtensorMap map_p) {
+  constexpr int kParts = kY16 ? 1 : 2;  // boxes of a chunk of 32 columns of y
+  constexpr uint32_t kSet = kParts * kBox;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  FCtrl* ctrl = reinterpret_cast<FCtrl*>(sm + P.off_ctrl);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int BN = P.BN, S = P.S, nkb = P.nkb, width = kGated ? BN / 2 : BN;  // outputs a tile
+  const uint32_t rank = cluster_ctarank();
+  const uint16_t both = 0x3;
+  const int64_t pair = blockIdx.x / 2, pairs = gridDim.x / 2;
+  volatile int32_t* abort = &ctrl->abort;
+  // tiles in groups of P.group token tiles: within a group, the token tile runs fastest
+  auto tile_at = [&](int64_t pt, int32_t& m0, int32_t& n0) {
+    const int64_t span = (int64_t)P.group * P.n_tiles, grp = pt / span;
+    const int64_t first = grp * P.group, left = P.m_tiles - first, rows = left < P.group ? left : P.group;
+    const int64_t in = pt - grp * span;
+    m0 = (int32_t)((first + in % rows) * 2 * kRows + rank * kRows);
+    n0 = (int32_t)(in / rows) * width;
+  };
+
+  if (warp == kEpiWarps + 1) {
+    tmem_alloc_pair(&ctrl->tmem_base, P.tmem_cols);
+    tmem_relinquish_pair();
+  }
+  if (warp == kEpiWarps && lane == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&ctrl->full[s], 1);
+      mbar_init(&ctrl->empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&ctrl->tfull[b], 1);
+      mbar_init(&ctrl->tempty[b], 2 * kEpiWarps);
+    }
+    mbar_init(&ctrl->done, 1);
+    for (int b = 0; b < kEpiWarps * kMaxSets; ++b) mbar_init(&ctrl->res_full[b], 1);
+    ctrl->abort = 0;
+    mbar_fence_init();
+    tma_prefetch_desc(&map_x);
+    tma_prefetch_desc(&map_w);
+    if (E.tma_y) tma_prefetch_desc(&map_y);
+    if (E.tma_y && E.res) tma_prefetch_desc(&map_r);
+    if (E.proj) tma_prefetch_desc(&map_p);
+  }
+  pdl_wait();
+  __syncthreads();
+  // only now, with this CTA's TMEM held, may the next kernel's CTAs come and ask for theirs
+  pdl_launch_dependents();
+  tc_fence_after();
+  const uint32_t tmem = ctrl->tmem_base;
+  cluster_sync();  // every CTA's barriers are initialised before another signals them
+
+  if (warp >= kEpiWarps) {
+    if constexpr (kFp8) registers_down<kOtherRegisters>();
+    if (warp == kEpiWarps && elect_one()) {
+      const int elems = kFp8 ? 128 : 64;  // K elements per stage
+      int s = 0, issued = 0;
+      uint32_t phase = 1;  // the first use of a stage finds it empty
+      bool ok = true;
+      for (int64_t pt = pair; pt < P.tiles && ok; pt += pairs) {
+        int32_t m0, n0;
+        tile_at(pt, m0, n0);
+        // the pair's halves of the MMA's columns: gated, one CTA brings rows of Wg and the other of Wu
+        const int32_t n = kGated ? n0 + (int32_t)rank * E.d_out : n0 + (int32_t)rank * (BN / 2);
+        for (int kb = 0; kb < nkb; ++kb) {
+          if (issued >= S && !mbar_wait_spin(&ctrl->empty[s], phase, abort)) {
+            ok = false;
+            break;
+          }
+          // the leader's barrier counts both CTAs' bytes
+          const uint32_t bar = dsmem_addr(smem_u32(&ctrl->full[s]), 0);
+          if (rank == 0) mbar_arrive_expect_tx(&ctrl->full[s], 2 * P.stage_bytes);
+          uint8_t* st = sm + (size_t)s * P.stage_bytes;
+          tma_load_2d_pair(smem_u32(st), &map_x, kb * elems, m0, bar);
+          tma_load_2d_pair(smem_u32(st + P.off_b), &map_w, kb * elems, n, bar);
+          if (issued < S) ++issued;
+          if (++s == S) s = 0, phase ^= 1;
+        }
+      }
+      // the last fill of every stage has been consumed before the CTA leaves
+      for (int i = 0; i < issued; ++i) {
+        if (issued < S) {
+          mbar_wait(&ctrl->empty[i], 0);
+        } else {
+          mbar_wait(&ctrl->empty[s], phase);
+          if (++s == S) s = 0, phase ^= 1;
+        }
+      }
+    }
+    if (warp == kEpiWarps + 1 && rank == 0 && elect_one()) {
+      const uint32_t idesc = kFp8 ? idesc_e4m3_f32(2 * kRows, (uint32_t)BN) : idesc_bf16_f32(2 * kRows, (uint32_t)BN, false, false);
+      const uint64_t da = smem_desc(smem_u32(sm), 16, 1024, kSwizzle128B);
+      const uint64_t db = smem_desc(smem_u32(sm + P.off_b), 16, 1024, kSwizzle128B);
+      const uint32_t a_lo = (uint32_t)da, b_lo = (uint32_t)db, desc_hi = (uint32_t)(da >> 32);
+      const int span = kFp8 ? 1 : nkb;  // K blocks an accumulator holds
+      int s = 0, tc = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int64_t pt = pair; pt < P.tiles && ok; pt += pairs) {
+        for (int first = 0; first < nkb && ok; first += span, ++tc) {
+          const int buf = tc & 1;
+          if (tc >= 2 && !mbar_wait_spin(&ctrl->tempty[buf], (uint32_t)((tc >> 1) - 1) & 1u, abort)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t d = tmem + (uint32_t)(buf * (P.tmem_cols / 2));
+          for (int kb = first; kb < first + span; ++kb) {
+            if (!mbar_wait_spin(&ctrl->full[s], phase, abort)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t at = (uint32_t)s * (P.stage_bytes >> 4);
+            umma_stage<true, kFp8>(d, a_lo + at, b_lo + at, desc_hi, desc_hi, idesc, kb != first);
+            umma_commit_pair(&ctrl->empty[s], both);
+            if (++s == S) s = 0, phase ^= 1;
+          }
+          if (ok) umma_commit_pair(&ctrl->tfull[buf], both);
+        }
+      }
+      if (!ok) report(err_word, MOLORA_DEV_WAIT_TIMEOUT);
+      umma_commit_pair(&ctrl->done, both);  // arrives in both CTAs once every MMA has completed
+    }
+    __syncwarp();
+  } else {
+    if constexpr (kFp8) registers_up<kEpiRegisters>();
+    // epilogue: warps w and w + 4 share 32 rows and take chunks of 32 outputs in turn
+    const int quarter = warp & 3, side = warp >> 2;
+    const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+    // Outputs leave through a ring of P.sets staging boxes, into which the residual's chunks come before.
+    uint8_t* ring = sm + P.off_stage + (size_t)warp * P.sets * kSet;
+    const bool add = !kGated && E.tma_y && E.res;
+    int tc = 0, used = 0, asked = 0;  // boxes written, and residual chunks on their way or taken
+    auto box_of = [&](int n) { return ring + (size_t)(n & (P.sets - 1)) * kSet; };
+    auto parity_of = [&](int n) { return (uint32_t)(n / P.sets) & 1u; };
+    auto ask = [&](int32_t col, int32_t m0) {
+      if (lane == 0) {
+        uint64_t* bar = &ctrl->res_full[warp * kMaxSets + (asked & (P.sets - 1))];
+        // the store that last left the box has read it
+        if (asked >= P.sets) bulk_wait_read_upto(used + P.sets - 1 - asked);
+        mbar_arrive_expect_tx(bar, kSet);
+        for (int q = 0; q < kParts; ++q)  // (past d_out there is nothing: zeros)
+          tma_load_2d(smem_u32(box_of(asked) + q * kBox), &map_r, col + q * 16, m0, bar);
+      }
+      ++asked;
+    };
+    auto piece = [&](uint8_t* box, int i) { return box + (i >> 2) * kBox + swz_offset((uint32_t)lane, (uint32_t)i & 3u, 64); };
+    // 32 columns of this warp's rows into a box, ready to be stored by lane 0
+    auto stage = [&](const float (&v)[32]) {
+      uint8_t* box = box_of(used);
+      if (!add) {
+        if (lane == 0) bulk_wait_read_upto(P.sets - 1);  // the store that last left the box has read it
+        __syncwarp();
+      }
+#pragma unroll
+      for (int i = 0; i < 4 * kParts; ++i) {
+        uint4 q;
+        if constexpr (kY16)
+          q = make_uint4(pack_bf16(v[8 * i], v[8 * i + 1]), pack_bf16(v[8 * i + 2], v[8 * i + 3]),
+                         pack_bf16(v[8 * i + 4], v[8 * i + 5]), pack_bf16(v[8 * i + 6], v[8 * i + 7]));
+        else
+          q = make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]), __float_as_uint(v[4 * i + 2]),
+                         __float_as_uint(v[4 * i + 3]));
+        *reinterpret_cast<uint4*>(piece(box, i)) = q;
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      ++used;
+      return box;
+    };
+    bool ok = true;
+    for (int64_t pt = pair; pt < P.tiles && ok; pt += pairs) {
+      int32_t m0, n0;
+      tile_at(pt, m0, n0);
+      m0 += quarter * 32;
+      const int64_t t = (int64_t)m0 + lane;
+      const int chunks = m0 < E.N ? min(width / 32, (E.d_out - n0 + 31) / 32) : 0;
+      const int mine = side < chunks ? (chunks - side + 1) / 2 : 0;  // chunks side, side + 2, ...
+      auto column = [&](int q) { return n0 + (side + 2 * q) * 32; };
+      // y's chunk from its finished values
+      auto put = [&](float (&v)[32], int32_t col) {
+        if (E.tma_y) {
+          if (add) {
+            if (!__all_sync(0xffffffffu, mbar_wait(&ctrl->res_full[warp * kMaxSets + (used & (P.sets - 1))], parity_of(used)))) {
+              ok = false;
+              return;
+            }
+            uint8_t* box = box_of(used);
+#pragma unroll
+            for (int i = 0; i < 4 * kParts; ++i) {
+              const uint4 q = *reinterpret_cast<const uint4*>(piece(box, i));
+              const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                if constexpr (kY16) {
+                  v[8 * i + 2 * j] += __uint_as_float(w[j] << 16);
+                  v[8 * i + 2 * j + 1] += __uint_as_float(w[j] & 0xffff0000u);
+                } else {
+                  v[4 * i + j] += __uint_as_float(w[j]);
+                }
+              }
+            }
+          }
+          const uint8_t* box = stage(v);
+          if (lane == 0) {
+            for (int q = 0; q < kParts && col + q * 16 < E.d_out; ++q)
+              tma_store_2d(&map_y, smem_u32(box + q * kBox), col + q * 16, m0);
+            bulk_commit();
+          }
+        } else {
+          // rows that are not 16-byte aligned: turned in shared memory, written a row at a time, 8 rows' residuals
+          // on their way together
+          if (E.proj) {
+            if (lane == 0) bulk_wait_read<0>();  // (the projections leave through the same boxes)
+          }
+          float* turned = reinterpret_cast<float*>(ring);
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) turned[lane * 32 + (i ^ lane)] = v[i];
+          __syncwarp();
+          const bool in = col + lane < E.d_out;
+#pragma unroll 1
+          for (int q0 = 0; q0 < 32 && m0 + q0 < E.N; q0 += 8) {
+            float o[8];
+            const int64_t at = ((int64_t)m0 + q0) * E.d_out + col + lane;
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              o[q] = 0.f;
+              if (!kGated && E.res && in && m0 + q0 + q < E.N) {
+                if constexpr (kY16)
+                  o[q] = to_float(static_cast<const __nv_bfloat16*>(E.res)[at + (int64_t)q * E.d_out]);
+                else
+                  o[q] = static_cast<const float*>(E.res)[at + (int64_t)q * E.d_out];
+              }
+            }
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              if (!in || m0 + q0 + q >= E.N) continue;
+              const float w = turned[(q0 + q) * 32 + (lane ^ (q0 + q))] + o[q];
+              if constexpr (kY16)
+                static_cast<__nv_bfloat16*>(E.y)[at + (int64_t)q * E.d_out] = __float2bfloat16_rn(w);
+              else
+                static_cast<float*>(E.y)[at + (int64_t)q * E.d_out] = w;
+            }
+          }
+          __syncwarp();
+        }
+      };
+      auto wait_sums = [&]() {  // the next accumulator
+        ok = __all_sync(0xffffffffu, mbar_wait_spin(&ctrl->tfull[tc & 1], (uint32_t)(tc >> 1) & 1u, abort));
+        tc_fence_after();
+        return tmem + lanes + (uint32_t)((tc & 1) * (P.tmem_cols / 2));
+      };
+      auto free_sums = [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(dsmem_addr(smem_u32(&ctrl->tempty[tc & 1]), 0));
+        ++tc;
+      };
+      if (add)
+        for (int q = 0; q < mine && q < P.sets; ++q) ask(column(q), m0);
+      if constexpr (kFp8) {
+        // 4 pieces of 32 columns of TMEM: linear, this warp's chunks; gated, gate and up of its two chunks in turn
+        float acc[4][32];
+        const int pieces = kGated ? 2 * mine : mine;
+        float cb[4], next[4], row;
+        const float* ps[4];
+        const float* px = E.sx + (t < E.N ? t * nkb : 0);
+        row = px[0];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int32_t col = column(kGated ? q >> 1 : q);
+          ps[q] = E.sw + (q < pieces ? (int64_t)(col / 128 + (kGated && (q & 1) ? E.up : 0)) * nkb : 0);
+          next[q] = ps[q][0];
+          cb[q] = !kGated && E.bias && q < pieces && col + lane < E.d_out ? E.bias[col + lane] : 0.f;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) acc[q][i] = 0.f;
+        }
+        for (int kb = 0; kb < nkb; ++kb) {
+          float sc[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) sc[q] = row * next[q];
+          if (kb + 1 < nkb) {  // on their way while this block's sums are awaited
+            row = px[kb + 1];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) next[q] = ps[q][kb + 1];
+          }
+          const uint32_t base = wait_sums();
+          if (!ok) break;
+          auto at = [&](int h) {  // the h-th 16 columns
+            const int q = h >> 1;
+            const int c = kGated ? (q & 1) * width + (side + 2 * (q >> 1)) * 32 : (side + 2 * q) * 32;
+            return base + (uint32_t)(c + (h & 1) * 16);
+          };
+          uint32_t r[2][16];
+          if (pieces > 0)
+            tmem_ld16_start(at(0), r[0]);
+          else
+            free_sums();
+#pragma unroll
+          for (int h = 0; h < 8; ++h) {
+            if (h >= 2 * pieces) continue;
+            tmem_ld_wait(r[h & 1]);
+            if (h + 1 < 2 * pieces) {
+              if (h + 1 < 8) tmem_ld16_start(at(h + 1), r[(h + 1) & 1]);
+            } else {
+              free_sums();
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              acc[h >> 1][(h & 1) * 16 + i] = fmaf(__uint_as_float(r[h & 1][i]), sc[h >> 1], acc[h >> 1][(h & 1) * 16 + i]);
+          }
+        }
+        if (!ok) break;
+#pragma unroll
+        for (int q = 0; q < (kGated ? 2 : 4); ++q) {
+          if (q >= mine || !ok) continue;
+          if constexpr (kGated) {
+            apply_act(acc[2 * q], E.act);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) acc[2 * q][i] *= acc[2 * q + 1][i];
+            put(acc[2 * q], column(q));
+          } else {
+            if (E.bias) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) acc[q][i] += __shfl_sync(0xffffffffu, cb[q], i);
+            }
+            apply_act(acc[q], E.act);
+            put(acc[q], column(q));
+            if (add && q + P.sets < mine) ask(column(q + P.sets), m0);
+          }
+        }
+      } else {
+        const uint32_t base = wait_sums();
+        if (!ok) break;
+        for (int q = 0; q < mine; ++q) {
+          uint32_t rg[32], ru[32];
+          tmem_ld32_start(base + (uint32_t)((side + 2 * q) * 32), rg);
+          tmem_ld32_start(base + (uint32_t)(width + (side + 2 * q) * 32), ru);
+          tmem_ld_wait(rg);
+          tmem_ld_bind(ru);
+          if (q + 1 == mine) free_sums();
+          float g[32], u[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) g[i] = __uint_as_float(rg[i]), u[i] = __uint_as_float(ru[i]);
+          const int32_t col = column(q);
+          if (E.proj) {
+            const uint8_t* box = stage(g);
+            if (lane == 0) {
+              tma_store_3d(&map_p, smem_u32(box), col, 0, m0);
+              bulk_commit();
+            }
+            box = stage(u);
+            if (lane == 0) {
+              tma_store_3d(&map_p, smem_u32(box), col, 1, m0);
+              bulk_commit();
+            }
+          }
+          apply_act(g, E.act);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) g[i] *= u[i];
+          put(g, col);
+        }
+        if (mine == 0) free_sums();
+      }
+    }
+    if (!ok) {
+      for (int n = used; n < asked; ++n)  // no copy is left in flight
+        mbar_wait(&ctrl->res_full[warp * kMaxSets + (n & (P.sets - 1))], parity_of(n));
+      *abort = 1;
+      if (lane == 0) report(err_word, MOLORA_DEV_WAIT_TIMEOUT);
+    }
+    if (lane == 0) bulk_wait_all();
+    __syncwarp();
+  }
+  if (warp == kEpiWarps + 1 && lane == 0) mbar_wait(&ctrl->done, 0);
+  __syncthreads();
+  cluster_sync();  // neither CTA leaves, nor frees its TMEM, while the other may still signal or use it
+  if (warp == kEpiWarps + 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, P.tmem_cols);
+  }
+}
+
+// ---------------------------------------------------------------------------------------------
+namespace {
+
+struct FSkinnyPlan {
+  int BN;                // tokens per tile (MMA N)
+  int C;                 // CTAs of a cluster: d_in split C ways
+  int S;
+  int nkb;
+  int32_t o_tiles, t_tiles;
+  uint32_t stage_bytes, off_b, off_ctrl, tmem_cols, smem;
+};
+
+// Ends a tile whose d_in was split over a cluster's C CTAs (as linear.cu's split_epilogue does): each CTA's sums
+// [token][row of W] go to shared memory, each CTA adds its share of the outputs in rank order, reading the others'
+// through distributed shared memory, and writes it.  Where `have` is false a wait ran out: such a thread's sums are
+// NaN, and so is what any CTA of the cluster makes of them.
+template <bool kGated, int U, int J>
+__device__ __forceinline__ void ff_join(const FEpi& E, const float (&sums)[J][16], bool have, uint8_t* sm, int C, int rank,
+                                        int32_t o0, int64_t t0, int tokens, int32_t* err_word) {
+  constexpr int kParts = kGated ? 2 : 1, kQuads = kRows / 4 / kParts;  // quads of outputs a token
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  float* part = reinterpret_cast<float*>(sm);
+  if (!have) report(err_word, MOLORA_DEV_WAIT_TIMEOUT);
+  if (warp < kEpiWarps) {
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const int c = (warp >> 2) * 16 + 32 * j;
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (c + i < tokens) part[(c + i) * kRows + (warp & 3) * 32 + lane] = have ? sums[j][i] : __uint_as_float(0x7fffffffu);
+    }
+  }
+  __syncthreads();
+  if (C > 1) cluster_sync();
+  if (warp < kEpiWarps) {
+    const bool vec = E.tma_y;  // (d_out a multiple of 4 and y, residual aligned)
+    const bool bias_vec = vec && (reinterpret_cast<uintptr_t>(E.bias) & 15u) == 0;
+    const int quads = tokens * kQuads, step = C * 256;
+    const int64_t half = (E.d_out + 7) & ~7;  // gated: elements of a row of one projection
+    for (int q0 = rank * 256 + tid; q0 < quads; q0 += U * step) {
+      Quad v[U][kParts], res[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int q = q0 + u * step, o = o0 + (q % kQuads) * 4;
+        if (q >= quads || o >= E.d_out) continue;
+        const int64_t row = (t0 + q / kQuads) * E.d_out;
+        if (!kGated && E.res) {
+          if (E.y_bf16)
+            res[u].load(static_cast<const __nv_bfloat16*>(E.res) + row, o, E.d_out, vec);
+          else
+            res[u].load(static_cast<const float*>(E.res) + row, o, E.d_out, vec);
+        }
+#pragma unroll
+        for (int h = 0; h < kParts; ++h) {
+          float4 p[8];
+          const float* mine = part + (q / kQuads) * kRows + h * (kRows / 2) + (q % kQuads) * 4;
+          const uint32_t at = smem_u32(mine);
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            if (c < C) p[c] = C > 1 ? dsmem_ld_f4(dsmem_addr(at, (uint32_t)c)) : *reinterpret_cast<const float4*>(mine);
+          float(&s)[4] = v[u][h].v;
+          s[0] = p[0].x, s[1] = p[0].y, s[2] = p[0].z, s[3] = p[0].w;
+#pragma unroll
+          for (int c = 1; c < 8; ++c)
+            if (c < C) s[0] += p[c].x, s[1] += p[c].y, s[2] += p[c].z, s[3] += p[c].w;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int q = q0 + u * step, o = o0 + (q % kQuads) * 4;
+        if (q >= quads || o >= E.d_out) continue;
+        const int64_t t = t0 + q / kQuads, row = t * E.d_out;
+        Quad& y = v[u][0];
+        if constexpr (kGated) {
+          if (E.proj) {  // (rows of whole quads: past d_ff they are padding)
+            __nv_bfloat16* p = static_cast<__nv_bfloat16*>(E.proj) + t * 2 * half;
+            v[u][0].store(p, o, E.d_out, true);
+            v[u][1].store(p + half, o, E.d_out, true);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) y.v[i] = activate(y.v[i], E.act) * v[u][kParts - 1].v[i];
+        } else {
+          if (E.bias) {
+            Quad b;
+            b.load(E.bias, o, E.d_out, bias_vec);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) y.v[i] += b.v[i];
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) y.v[i] = activate(y.v[i], E.act);
+          if (E.res)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) y.v[i] += res[u].v[i];
+        }
+        if (E.y_bf16)
+          y.store(static_cast<__nv_bfloat16*>(E.y) + row, o, E.d_out, vec);
+        else
+          y.store(static_cast<float*>(E.y) + row, o, E.d_out, vec);
+      }
+    }
+  }
+  __syncthreads();
+  if (C > 1) cluster_sync();  // no CTA leaves while another may still read its partial sums
+}
+
+}  // namespace
+
+// J: columns of sums a thread keeps, 32 J tokens a tile.  Warp w's lanes have rows 32 (w % 4) .. + 31 of the tile's 128
+// of W, columns 16 (w / 4) + 32 j .. + 15 of its tokens.
+template <bool kFp8, bool kGated, int J>
+__global__ void __launch_bounds__(kThreads, 1)
+    ff_skinny_kernel(const FEpi E, const FSkinnyPlan P, int32_t* err_word, const __grid_constant__ CUtensorMap map_x,
+                     const __grid_constant__ CUtensorMap map_w) {
+  constexpr int kWidth = kGated ? kRows / 2 : kRows;  // outputs a tile
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  FCtrl* ctrl = reinterpret_cast<FCtrl*>(sm + P.off_ctrl);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int BN = P.BN, S = P.S, C = P.C;
+  const int rank = (int)cluster_ctarank();
+  const unsigned tile = blockIdx.x / (unsigned)C;
+  const int32_t o0 = (int32_t)(tile % (unsigned)P.o_tiles) * kWidth, t0 = (int32_t)(tile / (unsigned)P.o_tiles) * BN;
+  const int kb0 = (int)((int64_t)P.nkb * rank / C), kb1 = (int)((int64_t)P.nkb * (rank + 1) / C);
+  const int tokens = (int)min((int64_t)BN, E.N - t0);
+  volatile int32_t* abort = &ctrl->abort;
+
+  if (warp == 9) {
+    tmem_alloc(&ctrl->tmem_base, P.tmem_cols);
+    tmem_relinquish();
+  }
+  if (warp == 8 && lane == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&ctrl->full[s], 1);
+      mbar_init(&ctrl->empty[s], 1);
+    }
+    for (int c = 0; c < 2; ++c) {
+      mbar_init(&ctrl->tfull[c], 1);
+      mbar_init(&ctrl->tempty[c], kEpiWarps);
+    }
+    mbar_init(&ctrl->done, 1);
+    ctrl->abort = 0;
+    mbar_fence_init();
+    tma_prefetch_desc(&map_x);
+    tma_prefetch_desc(&map_w);
+  }
+  pdl_wait();
+  __syncthreads();
+  // only now, with this CTA's TMEM held, may the next kernel's CTAs come and ask for theirs
+  pdl_launch_dependents();
+  tc_fence_after();
+  const uint32_t tmem = ctrl->tmem_base;
+  constexpr int kEach = kFp8 ? 1 : kSpan;  // K blocks an accumulator holds
+  const int spans = (kb1 - kb0 + kEach - 1) / kEach;
+  float sums[J][16];
+#pragma unroll
+  for (int j = 0; j < J; ++j)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) sums[j][i] = 0.f;
+  bool have = true;
+
+  if (warp == 8) {
+    if (elect_one()) {
+      const int elems = kFp8 ? 128 : 64;
+      int issued = 0, s = 0;
+      uint32_t phase = 1;  // the first use of a stage finds it empty
+      for (int kb = kb0; kb < kb1; ++kb, ++issued) {
+        if (issued >= S && !mbar_wait_spin(&ctrl->empty[s], phase, abort)) break;
+        uint8_t* st = sm + (size_t)s * P.stage_bytes;
+        mbar_arrive_expect_tx(&ctrl->full[s], P.stage_bytes);
+        tma_load_2d(smem_u32(st), &map_w, kb * elems, o0, &ctrl->full[s]);
+        if (kGated) tma_load_2d(smem_u32(st + kWidth * kRowBytes), &map_w, kb * elems, E.d_out + o0, &ctrl->full[s]);
+        tma_load_2d(smem_u32(st + P.off_b), &map_x, kb * elems, t0, &ctrl->full[s]);
+        if (++s == S) s = 0, phase ^= 1;
+      }
+      for (int q = 0; q < S && q < issued; ++q) mbar_wait(&ctrl->full[q], (uint32_t)((issued - 1 - q) / S) & 1u);
+    }
+    __syncwarp();
+  } else if (warp == 9) {
+    if (elect_one()) {
+      const uint32_t idesc = kFp8 ? idesc_e4m3_f32(kRows, (uint32_t)BN) : idesc_bf16_f32(kRows, (uint32_t)BN, false, false);
+      const uint64_t da = smem_desc(smem_u32(sm), 16, 1024, kSwizzle128B);
+      const uint64_t db = smem_desc(smem_u32(sm + P.off_b), 16, 1024, kSwizzle128B);
+      const uint32_t a_lo = (uint32_t)da, b_lo = (uint32_t)db, desc_hi = (uint32_t)(da >> 32);
+      bool ok = true;
+      int s = 0;
+      uint32_t phase = 0;
+      for (int c = 0; c < spans && ok; ++c) {
+        const int first = kb0 + c * kEach, last = min(first + kEach, kb1);
+        if (c >= 2 && !mbar_wait_spin(&ctrl->tempty[c & 1], (uint32_t)((c >> 1) - 1) & 1u, abort)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d = tmem + (uint32_t)((c & 1) * BN);
+        for (int kb = first; kb < last; ++kb) {
+          if (!mbar_wait_spin(&ctrl->full[s], phase, abort)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t at = (uint32_t)s * (P.stage_bytes >> 4);
+          umma_stage<false, kFp8>(d, a_lo + at, b_lo + at, desc_hi, desc_hi, idesc, kb != first);
+          umma_commit(&ctrl->empty[s]);
+          if (++s == S) s = 0, phase ^= 1;
+        }
+        if (ok) umma_commit(&ctrl->tfull[c & 1]);
+      }
+      if (!ok) report(err_word, MOLORA_DEV_WAIT_TIMEOUT);
+      umma_commit(&ctrl->done);
+    }
+    __syncwarp();
+  } else {
+    const uint32_t base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const int c0 = (warp >> 2) * 16;
+    // e4m3: the K block's scales, of this warp's rows of W, and lane i of the i-th token of each 16
+    const float* pw = nullptr;
+    const float* px[J];
+    float row = 0.f, col[J];
+    if constexpr (kFp8) {
+      const int32_t block = o0 / 128 + (kGated && (warp & 2) ? E.up : 0);
+      pw = E.sw + (int64_t)block * P.nkb;
+      row = pw[kb0];
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        const int64_t t = t0 + c0 + 32 * j + (lane & 15);
+        px[j] = E.sx + (t < E.N ? t : 0) * P.nkb;
+        col[j] = px[j][kb0];
+      }
+    }
+    for (int c = 0; c < spans && have; ++c) {
+      float sc[J];
+      if constexpr (kFp8) {
+#pragma unroll
+        for (int j = 0; j < J; ++j) sc[j] = row * col[j];
+        if (c + 1 < spans) {
+          row = pw[kb0 + c + 1];
+#pragma unroll
+          for (int j = 0; j < J; ++j) col[j] = px[j][kb0 + c + 1];
+        }
+      }
+      have = __all_sync(0xffffffffu, mbar_wait_spin(&ctrl->tfull[c & 1], (uint32_t)(c >> 1) & 1u, abort));
+      if (!have) break;
+      tc_fence_after();
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        if (c0 + 32 * j >= tokens) continue;
+        float p[16];
+        tmem_ld16(base + (uint32_t)((c & 1) * BN + c0 + 32 * j), p);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          if constexpr (kFp8)
+            sums[j][i] = fmaf(p[i], __shfl_sync(0xffffffffu, sc[j], i), sums[j][i]);
+          else
+            sums[j][i] += p[i];
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctrl->tempty[c & 1]);
+    }
+  }
+  // every MMA is done; the TMA warp has seen every load land
+  have = mbar_wait(&ctrl->done, 0) && have && !*abort;
+  __syncthreads();
+  ff_join<kGated, J >= 2 && !kGated ? 4 : 2>(E, sums, have, sm, C, rank, o0, t0, tokens, err_word);
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, P.tmem_cols);
+  }
+}
+
+// ---------------------------------------------------------------------------------------------
+namespace {
+
+FEpi epilogue_of(const FeedForwardArgs& a) {
+  FEpi e = {a.x_scale, a.w_scale, a.bias, a.residual, a.y, a.proj, a.N, a.d_out, (a.d_out + 127) / 128, a.act, a.y_bf16, false};
+  e.tma_y = a.d_out % (a.y_bf16 ? 8 : 4) == 0 && aligned(a.y, 16) && aligned(a.residual, 16);
+  return e;
+}
+
+int64_t rows_of_w(const FeedForwardArgs& a) { return (int64_t)a.d_out * (a.gated ? 2 : 1); }
+
+int k_blocks(const FeedForwardArgs& a) {
+  return (int)(((int64_t)a.d_in * (a.dtype == MOLORA_E4M3 ? 1 : 2) + kRowBytes - 1) / kRowBytes);
+}
+
+bool operand_map(CUtensorMap* m, const FeedForwardArgs& a, const void* base, int64_t rows, uint32_t box_rows) {
+  const bool fp8 = a.dtype == MOLORA_E4M3;
+  return linear_map(m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, fp8 ? 1 : 2, base,
+                    (uint64_t)rows, (uint64_t)a.d_in, fp8 ? 128 : 64, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+cudaError_t launch_tc(const FeedForwardArgs& a, int BN, cudaStream_t stream) {
+  const bool fp8 = a.dtype == MOLORA_E4M3;
+  FEpi e = epilogue_of(a);
+  FPlan p = {};
+  const int width = a.gated ? BN / 2 : BN;
+  p.BN = BN;
+  p.nkb = k_blocks(a);
+  p.m_tiles = (a.N + 2 * kRows - 1) / (2 * kRows);
+  p.n_tiles = (int32_t)(((int64_t)a.d_out + width - 1) / width);
+  p.tiles = p.m_tiles * p.n_tiles;
+  p.group = 8;
+  p.off_b = kRows * kRowBytes;
+  p.stage_bytes = p.off_b + (uint32_t)(BN / 2) * kRowBytes;
+  p.tmem_cols = tmem_columns(2 * (uint32_t)(BN <= 64 ? 64 : BN <= 128 ? 128 : 256));
+  CUtensorMap mx, mw, my = {}, mr = {}, mp = {};
+  auto rows_map = [&](CUtensorMap* m, const void* base) {
+    return linear_map(m, a.y_bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, a.y_bf16 ? 2 : 4, base,
+                      (uint64_t)a.N, (uint64_t)a.d_out, a.y_bf16 ? 32 : 16, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+  };
+  if (e.tma_y && (!rows_map(&my, a.y) || (a.residual && !rows_map(&mr, a.residual)))) e.tma_y = false;
+  if (a.proj) {
+    const uint64_t half = ((uint64_t)a.d_out + 7) & ~uint64_t(7);
+    if (!linear_map_3d(&mp, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.proj, {half, 2, (uint64_t)a.N}, {2 * half, 4 * half}, {32, 1, 32},
+                       CU_TENSOR_MAP_SWIZZLE_64B))
+      return cudaErrorNotSupported;
+  }
+  // boxes: two a warp; where the residual comes through them, four of bf16, so that all of a tile's come ahead
+  p.sets = a.residual && e.tma_y && a.y_bf16 ? 4 : 2;
+  const uint32_t boxes = kEpiWarps * (uint32_t)p.sets * (a.y_bf16 ? 1 : 2) * kBox;
+  static_assert(2 * kBox >= kTurn, "a warp's boxes hold a turned chunk");
+  const size_t fixed = boxes + sizeof(FCtrl) + kSmemSlack;
+  p.S = (int)((kMaxSmem - fixed) / p.stage_bytes);
+  if (p.S > kMaxStages) p.S = kMaxStages;
+  p.off_stage = (uint32_t)p.S * p.stage_bytes;
+  p.off_ctrl = p.off_stage + boxes;
+  // one CTA an SM, alone: an allocation of TMEM never waits for another CTA's (see linear.cu)
+  p.smem = kMaxSmem;
+  if (!operand_map(&mx, a, a.x, a.N, kRows) || !operand_map(&mw, a, a.W, rows_of_w(a), (uint32_t)(BN / 2)))
+    return cudaErrorNotSupported;
+  auto kernel = !fp8 ? ff_tc_kernel<false, true, true>
+                : a.gated ? ff_tc_kernel<true, true, true>
+                          : a.y_bf16 ? ff_tc_kernel<true, false, true> : ff_tc_kernel<true, false, false>;
+  static std::atomic<uint64_t> allowed[4];
+  const cudaError_t set = allow_smem(kernel, allowed[!fp8 ? 0 : a.gated ? 1 : a.y_bf16 ? 2 : 3], kMaxSmem);
+  if (set != cudaSuccess) return set;
+  const int64_t most = num_sms() / 2;
+  const dim3 grid((unsigned)(2 * (p.tiles < most ? p.tiles : most)));
+  return launch_kernel(kernel, grid, dim3(kTcThreads), p.smem, stream, 2, e, p, a.err_word, mx, mw, my, mr, mp);
+}
+
+cudaError_t launch_skinny(const FeedForwardArgs& a, const Resident& r, int BN, cudaStream_t stream) {
+  const FEpi e = epilogue_of(a);
+  FSkinnyPlan p = {};
+  const int width = a.gated ? kRows / 2 : kRows;
+  p.BN = BN;
+  p.nkb = k_blocks(a);
+  p.o_tiles = (int32_t)(((int64_t)a.d_out + width - 1) / width);
+  p.t_tiles = (int32_t)((a.N + p.BN - 1) / p.BN);
+  const int64_t tiles = (int64_t)p.o_tiles * p.t_tiles;
+  p.C = split_of(r, tiles, p.nkb);
+  p.off_b = kRows * kRowBytes;
+  p.stage_bytes = p.off_b + (uint32_t)p.BN * kRowBytes;
+  p.tmem_cols = tmem_columns(2 * (uint32_t)p.BN);
+  const size_t fixed = sizeof(FCtrl) + kSmemSlack;
+  const size_t partial = (size_t)p.BN * kRows * sizeof(float);
+  const int need = (p.nkb + p.C - 1) / p.C;
+  p.S = (int)((kMaxSmem - fixed) / p.stage_bytes);
+  if (p.S > kMaxStages) p.S = kMaxStages;
+  if (p.S > need) p.S = need;
+  size_t ring = (size_t)p.S * p.stage_bytes;
+  if (ring < partial) ring = partial;
+  p.off_ctrl = (uint32_t)ring;
+  p.smem = (uint32_t)(ring + fixed);
+  if (p.smem < 116 * 1024) p.smem = 116 * 1024;  // no two CTAs that could wait for each other's TMEM share an SM (see linear.cu)
+  CUtensorMap mx, mw;
+  if (!operand_map(&mx, a, a.x, a.N, (uint32_t)p.BN) || !operand_map(&mw, a, a.W, rows_of_w(a), (uint32_t)width))
+    return cudaErrorNotSupported;
+  auto go = [&](auto kernel, std::atomic<uint64_t>& allowed) {
+    const cudaError_t set = allow_smem(kernel, allowed, kMaxSmem);
+    if (set != cudaSuccess) return set;
+    return launch_kernel(kernel, dim3((unsigned)(tiles * p.C)), dim3(kThreads), p.smem, stream, p.C, e, p, a.err_word, mx, mw);
+  };
+  static std::atomic<uint64_t> allowed[12];
+  const bool fp8 = a.dtype == MOLORA_E4M3;
+  auto pick = [&](auto j, int n) {
+    constexpr int J = decltype(j)::value;
+    return !fp8 ? go(ff_skinny_kernel<false, true, J>, allowed[3 * n])
+           : a.gated ? go(ff_skinny_kernel<true, true, J>, allowed[3 * n + 1])
+                     : go(ff_skinny_kernel<true, false, J>, allowed[3 * n + 2]);
+  };
+  switch (p.BN) {
+    case 16:
+    case 32:
+      return pick(std::integral_constant<int, 1>{}, 0);
+    case 64:
+      return pick(std::integral_constant<int, 2>{}, 1);
+    case 128:
+      return pick(std::integral_constant<int, 4>{}, 2);
+    default:
+      return pick(std::integral_constant<int, 8>{}, 3);
+  }
+}
+
+// Cycles that the kernels take in tiles of BN tokens, and of BN rows of W (see linear.cu's).
+int64_t skinny_cycles(const FeedForwardArgs& a, const Resident& r, int BN) {
+  const int64_t tiles = ((rows_of_w(a) + kRows - 1) / kRows) * ((a.N + BN - 1) / BN);
+  const int nkb = k_blocks(a), C = split_of(r, tiles, nkb);
+  const int64_t waves = (tiles + r.of[C] - 1) / r.of[C];
+  return 6500 + waves * ((nkb + C - 1) / C * (420 + BN * 3 / 2) + 48 * BN);
+}
+
+int64_t tc_cycles(const FeedForwardArgs& a, const Resident& r, int BN) {
+  const int width = a.gated ? BN / 2 : BN;
+  const int64_t m_tiles = (a.N + 2 * kRows - 1) / (2 * kRows);
+  const int64_t tiles = m_tiles * (((int64_t)a.d_out + width - 1) / width), waves = (tiles + r.of[2] - 1) / r.of[2];
+  return 8000 + waves * k_blocks(a) * (2 * BN + 90 > 420 ? 2 * BN + 90 : 420);
+}
+
+}  // namespace
+
+cudaError_t launch_feed_forward(const FeedForwardArgs& a, cudaStream_t stream) {
+  const Resident r = resident_clusters();
+  int best = 128, split = 0;
+  int64_t cost = INT64_MAX;
+  for (int BN : {16, 32, 64, 128, 256}) {
+    if (BN > 16 && BN / 2 >= a.N) break;
+    const int64_t c = skinny_cycles(a, r, BN);
+    if (c < cost) cost = c, split = BN;
+  }
+  for (int BN : {256, 192, 128, 64}) {
+    if (split && a.N <= 32) continue;
+    const int64_t c = tc_cycles(a, r, BN);
+    if (c < cost) cost = c, best = BN, split = 0;
+  }
+#ifdef MOLORA_TUNING_ENV
+  if (const char* g = getenv("MOLORA_FF_BN")) best = atoi(g);
+  if (const char* g = getenv("MOLORA_FF_SKINNY")) split = atoi(g);
+#endif
+  return split ? launch_skinny(a, r, split, stream) : launch_tc(a, best, stream);
+}
+
+}  // namespace molora

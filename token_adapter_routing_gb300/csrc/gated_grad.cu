@@ -1,0 +1,474 @@
+// gated_grad.cu -- the backward pass of the gated feed-forward block h = act(g) u, [g | u] = x [Wg; Wu]^T:
+//
+//   dg = dh u act'(g),  du = dh act(g)        gated_slope_kernel: one pass over proj = [g | u] and dh, bound by HBM
+//   dx = dg Wg + du Wu                        grad_tc_kernel: 2 d_ff terms an element
+//   dWg = dg^T x,  dWu = du^T x               grad_tc_kernel: N terms an element
+//
+// Both products are tiles of one persistent kernel of CTA pairs (linear.cu's pipeline: a TMA warp and an MMA warp ahead of
+// the epilogue by two TMEM accumulators), so that the second's tiles fill the pairs that the first leaves idle.
+// No operand is transposed in memory: what is not K-major (W in dx, both operands in dW) is read by the tensor
+// cores as it lies, MN-major, in boxes of 64 columns x 64 rows of K.  Bound by the tensor cores.
+#include <cudaTypedefs.h>
+
+#include <atomic>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "linear.cuh"
+
+namespace molora {
+
+namespace {
+
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 32 * (kEpiWarps + 2);  // + TMA warp (8) + MMA warp (9)
+constexpr int kSets = 2;                        // staging boxes an epilogue warp
+constexpr uint32_t kAtom = 64 * kRowBytes;      // a box of 64 columns x 64 rows of K
+constexpr uint32_t kStageA = kRows * kRowBytes;
+
+struct __align__(8) GCtrl {
+  uint64_t full[kMaxStages];
+  uint64_t empty[kMaxStages];
+  uint64_t tfull[2];
+  uint64_t tempty[2];
+  uint64_t done;
+  uint32_t tmem_base;
+  int32_t abort;
+};
+
+// The tiles: dx's first (their sums are the longest), then dW's, gate and up rows in turn.
+struct GPlan {
+  int BN;                    // columns a tile
+  int S;
+  int64_t tiles_x, tiles;    // dx's, all
+  int32_t n_tiles;           // tiles across d_in
+  int64_t m_tiles_x, m_tiles_w;  // down N, down d_ff
+  int32_t kb_half, kb_x, kb_w;   // K blocks of 64: of one projection, of a tile of dx, of one of dW
+  int32_t group;
+  int64_t N;
+  int32_t d_in, d_ff;
+  uint32_t stage_bytes, off_stage, off_ctrl, tmem_cols;
+};
+
+struct GTile {
+  bool x;          // of dx
+  int32_t plane;   // of dW: 0 gate, 1 up
+  int32_t m0, n0;  // this CTA's first row, the tile's first column
+  int32_t kbs;
+};
+
+__device__ __forceinline__ GTile tile_at(const GPlan& P, int64_t i, uint32_t rank) {
+  GTile t;
+  t.x = i < P.tiles_x;
+  if (!t.x) i -= P.tiles_x;
+  const int64_t m_tiles = t.x ? P.m_tiles_x : 2 * P.m_tiles_w;
+  // groups of row tiles that share the other operand's columns in L2: within one the row tile runs fastest
+  const int64_t span = (int64_t)P.group * P.n_tiles, grp = i / span;
+  const int64_t first = grp * P.group, left = m_tiles - first, rows = left < P.group ? left : P.group;
+  const int64_t in = i - grp * span;
+  int64_t m = first + in % rows;
+  t.plane = !t.x && m >= P.m_tiles_w;
+  if (t.plane) m -= P.m_tiles_w;
+  t.m0 = (int32_t)(m * 2 * kRows + rank * kRows);
+  t.n0 = (int32_t)(in / rows) * P.BN;
+  t.kbs = t.x ? P.kb_x : P.kb_w;
+  return t;
+}
+
+// The MMAs of one stage, as umma_stage, with the 16-byte units between the steps of A too.
+__device__ __forceinline__ void umma_stage_steps(uint32_t d, uint32_t a, uint32_t b, uint32_t a_hi, uint32_t b_hi, uint32_t idesc,
+                                                 uint32_t accumulate, uint32_t a_step, uint32_t b_step) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t.reg .b32 al, bl;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "mov.b64 da, {%1, %3};\n\tmov.b64 db, {%2, %4};\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %5, p;\n\t"
+      "setp.eq.b32 p, 0, 0;\n\t"
+      "add.u32 al, %1, %7;\n\tadd.u32 bl, %2, %8;\n\tmov.b64 da, {al, %3};\n\tmov.b64 db, {bl, %4};\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %5, p;\n\t"
+      "add.u32 al, al, %7;\n\tadd.u32 bl, bl, %8;\n\tmov.b64 da, {al, %3};\n\tmov.b64 db, {bl, %4};\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %5, p;\n\t"
+      "add.u32 al, al, %7;\n\tadd.u32 bl, bl, %8;\n\tmov.b64 da, {al, %3};\n\tmov.b64 db, {bl, %4};\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %5, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(a_hi), "r"(b_hi), "r"(idesc), "r"(accumulate), "r"(a_step), "r"(b_step)
+      : "memory");
+}
+
+}  // namespace
+
+// map_pk, map_pm: dproj [N x 2 x d_ff] in boxes of 128 tokens x 64 columns (K-major rows of dx's product), and of 64
+// tokens x 64 (MN-major rows of dW's).  map_b[0], map_b[1]: W [2 x d_ff x d_in] and x [1 x N x d_in] in boxes of 64 x 64.
+// map_dx, map_dw: the outputs, [1 x N x d_in] and [2 x d_ff x d_in].
+__global__ void __launch_bounds__(kThreads, 1)
+    grad_tc_kernel(const GPlan P, int32_t* err_word, const __grid_constant__ CUtensorMap map_pk,
+                   const __grid_constant__ CUtensorMap map_pm, const __grid_constant__ CUtensorMap map_w,
+                   const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_dx,
+                   const __grid_constant__ CUtensorMap map_dw) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  GCtrl* ctrl = reinterpret_cast<GCtrl*>(sm + P.off_ctrl);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int BN = P.BN, S = P.S;
+  const uint32_t rank = cluster_ctarank();
+  const uint16_t both = 0x3;
+  const int64_t pair = blockIdx.x / 2, pairs = gridDim.x / 2;
+  volatile int32_t* abort = &ctrl->abort;
+
+  if (warp == kEpiWarps + 1) {
+    tmem_alloc_pair(&ctrl->tmem_base, P.tmem_cols);
+    tmem_relinquish_pair();
+  }
+  if (warp == kEpiWarps && lane == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&ctrl->full[s], 1);
+      mbar_init(&ctrl->empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&ctrl->tfull[b], 1);
+      mbar_init(&ctrl->tempty[b], 2 * kEpiWarps);
+    }
+    mbar_init(&ctrl->done, 1);
+    ctrl->abort = 0;
+    mbar_fence_init();
+    if (P.tiles_x) {
+      tma_prefetch_desc(&map_pk);
+      tma_prefetch_desc(&map_w);
+      tma_prefetch_desc(&map_dx);
+    }
+    if (P.tiles > P.tiles_x) {
+      tma_prefetch_desc(&map_pm);
+      tma_prefetch_desc(&map_x);
+      tma_prefetch_desc(&map_dw);
+    }
+  }
+  pdl_wait();
+  __syncthreads();
+  // only now, with this CTA's TMEM held, may the next kernel's CTAs come and ask for theirs
+  pdl_launch_dependents();
+  tc_fence_after();
+  const uint32_t tmem = ctrl->tmem_base;
+  cluster_sync();  // every CTA's barriers are initialised before another signals them
+
+  if (warp == kEpiWarps) {
+    if (elect_one()) {
+      int s = 0, issued = 0;
+      uint32_t phase = 1;  // the first use of a stage finds it empty
+      bool ok = true;
+      for (int64_t i = pair; i < P.tiles && ok; i += pairs) {
+        const GTile t = tile_at(P, i, rank);
+        const CUtensorMap* map_b = t.x ? &map_w : &map_x;
+        const int32_t n = t.n0 + (int32_t)rank * (BN / 2);
+        for (int kb = 0; kb < t.kbs; ++kb) {
+          if (issued >= S && !mbar_wait_spin(&ctrl->empty[s], phase, abort)) {
+            ok = false;
+            break;
+          }
+          // the leader's barrier counts both CTAs' bytes
+          const uint32_t bar = dsmem_addr(smem_u32(&ctrl->full[s]), 0);
+          if (rank == 0) mbar_arrive_expect_tx(&ctrl->full[s], 2 * P.stage_bytes);
+          const uint32_t st = smem_u32(sm + (size_t)s * P.stage_bytes);
+          int32_t k, plane = 0;
+          if (t.x) {  // K runs over the gate's columns of dproj, then the up's
+            plane = kb >= P.kb_half;
+            k = (kb - (plane ? P.kb_half : 0)) * 64;
+            tma_load_3d_pair(st, &map_pk, k, plane, t.m0, bar);
+          } else {  // K runs over tokens
+            k = kb * 64;
+            tma_load_3d_pair(st, &map_pm, t.m0, t.plane, k, bar);
+            tma_load_3d_pair(st + kAtom, &map_pm, t.m0 + 64, t.plane, k, bar);
+          }
+          for (int q = 0; q < BN / 128; ++q) tma_load_3d_pair(st + kStageA + q * kAtom, map_b, n + q * 64, k, plane, bar);
+          if (issued < S) ++issued;
+          if (++s == S) s = 0, phase ^= 1;
+        }
+      }
+      // the last fill of every stage has been consumed before the CTA leaves
+      for (int i = 0; i < issued; ++i) {
+        if (issued < S) {
+          mbar_wait(&ctrl->empty[i], 0);
+        } else {
+          mbar_wait(&ctrl->empty[s], phase);
+          if (++s == S) s = 0, phase ^= 1;
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == kEpiWarps + 1) {
+    if (rank == 0 && elect_one()) {
+      // K-major rows of 128 bytes; MN-major boxes of 64 columns, kAtom bytes apart, groups of 8 rows of K 1024
+      const uint64_t dk = smem_desc(smem_u32(sm), 16, 1024, kSwizzle128B), dm = smem_desc(smem_u32(sm), kAtom, 1024, kSwizzle128B);
+      const uint32_t k_lo = (uint32_t)dk, m_lo = (uint32_t)dm, hi = (uint32_t)(dk >> 32);
+      int s = 0, tc = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int64_t i = pair; i < P.tiles && ok; i += pairs, ++tc) {
+        const GTile t = tile_at(P, i, rank);
+        const uint32_t idesc = idesc_bf16_f32(2 * kRows, (uint32_t)BN, !t.x, true);
+        const uint32_t a_lo = t.x ? k_lo : m_lo, a_step = t.x ? 2 : 16 * kRowBytes / 16;
+        const int buf = tc & 1;
+        if (tc >= 2 && !mbar_wait_spin(&ctrl->tempty[buf], (uint32_t)((tc >> 1) - 1) & 1u, abort)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d = tmem + (uint32_t)(buf * (P.tmem_cols / 2));
+        for (int kb = 0; kb < t.kbs; ++kb) {
+          if (!mbar_wait_spin(&ctrl->full[s], phase, abort)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t at = (uint32_t)s * (P.stage_bytes >> 4);
+          umma_stage_steps(d, a_lo + at, m_lo + (kStageA >> 4) + at, hi, hi, idesc, kb != 0, a_step, 16 * kRowBytes / 16);
+          umma_commit_pair(&ctrl->empty[s], both);
+          if (++s == S) s = 0, phase ^= 1;
+        }
+        if (ok) umma_commit_pair(&ctrl->tfull[buf], both);
+      }
+      if (!ok) report(err_word, MOLORA_DEV_WAIT_TIMEOUT);
+      umma_commit_pair(&ctrl->done, both);  // arrives in both CTAs once every MMA has completed
+    }
+    __syncwarp();
+  } else {
+    // epilogue: warps w and w + 4 share 32 rows and take chunks of 32 columns in turn
+    const int quarter = warp & 3, side = warp >> 2;
+    const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+    uint8_t* ring = sm + P.off_stage + (size_t)warp * kSets * kBox;
+    int tc = 0, used = 0;
+    bool ok = true;
+    for (int64_t i = pair; i < P.tiles && ok; i += pairs) {
+      const GTile t = tile_at(P, i, rank);
+      const int32_t row = t.m0 + quarter * 32;
+      const int64_t rows = t.x ? P.N : P.d_ff;
+      const int chunks = row < rows ? min(BN / 32, (P.d_in - t.n0 + 31) / 32) : 0;
+      ok = __all_sync(0xffffffffu, mbar_wait_spin(&ctrl->tfull[tc & 1], (uint32_t)(tc >> 1) & 1u, abort));
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t base = tmem + lanes + (uint32_t)((tc & 1) * (P.tmem_cols / 2));
+      uint32_t r[32];
+      if (side < chunks) tmem_ld32_start(base + (uint32_t)(side * 32), r);
+      for (int c = side; c < chunks; c += 2) {
+        tmem_ld_wait(r);
+        uint4 v[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          v[q] = make_uint4(pack_bf16(__uint_as_float(r[8 * q]), __uint_as_float(r[8 * q + 1])),
+                            pack_bf16(__uint_as_float(r[8 * q + 2]), __uint_as_float(r[8 * q + 3])),
+                            pack_bf16(__uint_as_float(r[8 * q + 4]), __uint_as_float(r[8 * q + 5])),
+                            pack_bf16(__uint_as_float(r[8 * q + 6]), __uint_as_float(r[8 * q + 7])));
+        if (c + 2 < chunks) tmem_ld32_start(base + (uint32_t)((c + 2) * 32), r);
+        uint8_t* box = ring + (size_t)(used & (kSets - 1)) * kBox;
+        if (lane == 0) bulk_wait_read<kSets - 1>();  // the store that last left the box has read it
+        __syncwarp();
+#pragma unroll
+        for (int q = 0; q < 4; ++q) *reinterpret_cast<uint4*>(box + swz_offset((uint32_t)lane, (uint32_t)q, 64)) = v[q];
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tma_store_3d(t.x ? &map_dx : &map_dw, smem_u32(box), t.n0 + c * 32, row, t.plane);
+          bulk_commit();
+        }
+        ++used;
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(dsmem_addr(smem_u32(&ctrl->tempty[tc & 1]), 0));
+      ++tc;
+    }
+    if (!ok) {
+      *abort = 1;
+      if (lane == 0) report(err_word, MOLORA_DEV_WAIT_TIMEOUT);
+    }
+    if (lane == 0) bulk_wait_all();
+    __syncwarp();
+  }
+  if (warp == kEpiWarps + 1 && lane == 0) mbar_wait(&ctrl->done, 0);
+  __syncthreads();
+  cluster_sync();  // neither CTA leaves, nor frees its TMEM, while the other may still signal or use it
+  if (warp == kEpiWarps + 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, P.tmem_cols);
+  }
+}
+
+// ---------------------------------------------------------------------------------------------
+namespace {
+
+__device__ __forceinline__ float exp2_fast(float z) {
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z));
+  return e;
+}
+__device__ __forceinline__ float rcp_fast(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+// act(v) and act'(v) together, from one power each (see activate):
+//   SiLU        p = 1 / (1 + 2^(-v log2 e)):  v p,  p + v p (1 - p)
+//   GELU        Phi(v) the normal distribution, phi(v) its density:  v Phi(v),  Phi(v) + v phi(v)
+//   GELU, tanh  p = 1 / (1 + 2^(-2 u log2 e)):  v p,  p + v p (1 - p) 2 u',  u' = sqrt(2 / pi) (1 + 0.134145 v^2)
+// 1 - p is the power times p where p is near 1, which leaves nothing to cancel.  Where 2^z overflows p is 0, and so are
+// both; v^2 is kept finite, so that nothing there is 0 times infinity.
+__device__ __forceinline__ void act_and_slope(float v, molora_activation act, float& a, float& s) {
+  switch (act) {
+    case MOLORA_ACT_RELU:
+      a = v > 0.f ? v : (v != v ? v : 0.f);
+      s = v > 0.f ? 1.f : (v != v ? v : 0.f);
+      return;
+    case MOLORA_ACT_SILU: {
+      const float e = exp2_fast(-1.4426950408889634f * v), p = rcp_fast(1.f + e);
+      a = v * p;
+      s = fmaf(a, e < 1.f ? e * p : 1.f - p, p);
+      return;
+    }
+    case MOLORA_ACT_GELU_TANH: {
+      const float e = exp2_fast(v * fmaf(-0.10294324f * v, v, -2.3022082f)), p = rcp_fast(1.f + e);
+      a = v * p;
+      s = fmaf(a, (e < 1.f ? e * p : 1.f - p) * fmaf(0.21406859f, fminf(v * v, 1e30f), 1.5957691f), p);
+      return;
+    }
+    case MOLORA_ACT_GELU: {
+      a = gelu_erf(v);
+      const float z = fminf(fabsf(v), 14.f), density = 0.3989422804f * exp2_fast(z * (-0.72134752f * z));
+      const float tail = 0.5f * erfcf(z * 0.70710678f);
+      s = fmaf(copysignf(z, v), density, v > 0.f ? 1.f - tail : tail);
+      if (v != v) s = v;
+      return;
+    }
+    default:
+      a = v;
+      s = 1.f;
+  }
+}
+
+constexpr int kSlopeThreads = 256;
+
+}  // namespace
+
+// dproj from proj and dh, 8 columns a thread and kUnits such pieces in flight.  proj and dproj [N x 2 x half], half = d_ff rounded
+// up to 8; dproj may be proj.  kVec: dh's rows start on 16-byte boundaries (d_ff = half).
+template <bool kVec, int kUnits>
+__global__ void __launch_bounds__(kSlopeThreads)
+    gated_slope_kernel(const __nv_bfloat16* proj, const __nv_bfloat16* __restrict__ dh, __nv_bfloat16* dproj, int64_t N, int32_t d_ff,
+                       molora_activation act) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int32_t pieces = (int32_t)(((int64_t)d_ff + 7) / 8);
+  const int64_t half = (int64_t)pieces * 8, all = N * pieces;
+  const int64_t first = (int64_t)blockIdx.x * (kSlopeThreads * kUnits) + threadIdx.x;
+  uint4 g[kUnits], u[kUnits], d[kUnits];
+  int64_t at[kUnits];
+#pragma unroll
+  for (int k = 0; k < kUnits; ++k) {
+    const int64_t i = first + k * kSlopeThreads;
+    if (i >= all) continue;
+    const int64_t n = all <= UINT32_MAX ? (uint32_t)i / (uint32_t)pieces : i / pieces;
+    const int32_t c = (int32_t)(i - n * pieces) * 8;
+    at[k] = n * 2 * half + c;
+    g[k] = *reinterpret_cast<const uint4*>(proj + at[k]);
+    u[k] = *reinterpret_cast<const uint4*>(proj + at[k] + half);
+    const __nv_bfloat16* p = dh + n * d_ff + c;
+    if (kVec) {
+      d[k] = *reinterpret_cast<const uint4*>(p);
+    } else {
+      uint32_t w[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[j] = c + j < d_ff ? (uint32_t)__bfloat16_as_ushort(p[j]) : 0u;
+      d[k] = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kUnits; ++k) {
+    if (first + k * kSlopeThreads >= all) continue;
+    const uint32_t gw[4] = {g[k].x, g[k].y, g[k].z, g[k].w}, uw[4] = {u[k].x, u[k].y, u[k].z, u[k].w},
+                   dw[4] = {d[k].x, d[k].y, d[k].z, d[k].w};
+    uint32_t og[4], ou[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float r[2][2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        auto value = [&](uint32_t w) { return __uint_as_float(h ? w & 0xffff0000u : w << 16); };
+        float a, s;
+        act_and_slope(value(gw[j]), act, a, s);
+        const float v = value(dw[j]);
+        r[0][h] = v * value(uw[j]) * s;
+        r[1][h] = v * a;
+      }
+      og[j] = pack_bf16(r[0][0], r[0][1]);
+      ou[j] = pack_bf16(r[1][0], r[1][1]);
+    }
+    *reinterpret_cast<uint4*>(dproj + at[k]) = make_uint4(og[0], og[1], og[2], og[3]);
+    *reinterpret_cast<uint4*>(dproj + at[k] + half) = make_uint4(ou[0], ou[1], ou[2], ou[3]);
+  }
+}
+
+namespace {
+
+cudaError_t launch_slope(const GatedGradArgs& a, cudaStream_t stream) {
+  const auto* proj = static_cast<const __nv_bfloat16*>(a.proj);
+  const auto* dh = static_cast<const __nv_bfloat16*>(a.dh);
+  auto* dproj = static_cast<__nv_bfloat16*>(a.dproj);
+  const int64_t all = a.N * (((int64_t)a.d_ff + 7) / 8);
+  constexpr int kUnits = 2;
+  const int64_t grid = (all + kSlopeThreads * kUnits - 1) / (kSlopeThreads * kUnits);
+  if (grid > INT32_MAX) return cudaErrorNotSupported;
+  auto kernel = a.d_ff % 8 == 0 && aligned(dh, 16) ? gated_slope_kernel<true, kUnits> : gated_slope_kernel<false, kUnits>;
+  return launch_kernel(kernel, dim3((unsigned)grid), dim3(kSlopeThreads), 0, stream, 0, proj, dh, dproj, a.N, a.d_ff, a.act);
+}
+
+}  // namespace
+
+cudaError_t launch_gated_grad(const GatedGradArgs& a, cudaStream_t stream) {
+  const cudaError_t slope = launch_slope(a, stream);
+  if (slope != cudaSuccess || (!a.dx && !a.dW)) return slope;
+  const uint64_t N = (uint64_t)a.N, F = (uint64_t)a.d_ff, D = (uint64_t)a.d_in, half = (F + 7) & ~uint64_t(7);
+  GPlan p = {};
+  p.N = a.N;
+  p.d_in = a.d_in;
+  p.d_ff = a.d_ff;
+  p.m_tiles_x = (a.N + 2 * kRows - 1) / (2 * kRows);
+  p.m_tiles_w = ((int64_t)a.d_ff + 2 * kRows - 1) / (2 * kRows);
+  p.kb_half = (int32_t)((F + 63) / 64);
+  p.kb_x = 2 * p.kb_half;
+  p.kb_w = (int32_t)((N + 63) / 64);
+  p.group = 8;
+  const int64_t pairs = resident_clusters().of[2];
+  auto plan = [&](int BN) {
+    p.BN = BN;
+    p.n_tiles = (int32_t)(((int64_t)a.d_in + BN - 1) / BN);
+    p.tiles_x = a.dx ? p.m_tiles_x * p.n_tiles : 0;
+    p.tiles = p.tiles_x + (a.dW ? 2 * p.m_tiles_w * p.n_tiles : 0);
+  };
+  plan(256);
+  if (p.tiles < pairs) plan(128);
+  p.stage_bytes = kStageA + (uint32_t)(p.BN / 128) * kAtom;
+  const uint32_t boxes = kEpiWarps * kSets * kBox;
+  p.S = (int)((kMaxSmem - boxes - sizeof(GCtrl) - kSmemSlack) / p.stage_bytes);
+  if (p.S > kMaxStages) p.S = kMaxStages;
+  p.off_stage = (uint32_t)p.S * p.stage_bytes;
+  p.off_ctrl = p.off_stage + boxes;
+  p.tmem_cols = 2 * (uint32_t)p.BN;
+  const auto BF = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const auto S128 = CU_TENSOR_MAP_SWIZZLE_128B, S64 = CU_TENSOR_MAP_SWIZZLE_64B;
+  CUtensorMap pk = {}, pm = {}, w = {}, x = {}, dx = {}, dw = {};
+  if (a.dx && (!linear_map_3d(&pk, BF, a.dproj, {F, 2, N}, {2 * half, 4 * half}, {64, 1, 128}, S128) ||
+               !linear_map_3d(&w, BF, a.W, {D, F, 2}, {2 * D, 2 * F * D}, {64, 64, 1}, S128) ||
+               !linear_map_3d(&dx, BF, a.dx, {D, N, 1}, {2 * D, 2 * N * D}, {32, 32, 1}, S64)))
+    return cudaErrorNotSupported;
+  if (a.dW && (!linear_map_3d(&pm, BF, a.dproj, {F, 2, N}, {2 * half, 4 * half}, {64, 1, 64}, S128) ||
+               !linear_map_3d(&x, BF, a.x, {D, N, 1}, {2 * D, 2 * N * D}, {64, 64, 1}, S128) ||
+               !linear_map_3d(&dw, BF, a.dW, {D, F, 2}, {2 * D, 2 * F * D}, {32, 32, 1}, S64)))
+    return cudaErrorNotSupported;
+  static std::atomic<uint64_t> allowed;
+  const cudaError_t set = allow_smem(grad_tc_kernel, allowed, kMaxSmem);
+  if (set != cudaSuccess) return set;
+  const int64_t most = num_sms() / 2;
+  const dim3 grid((unsigned)(2 * (p.tiles < most ? p.tiles : most)));
+  // one CTA an SM, alone: an allocation of TMEM never waits for another CTA's (see linear.cu)
+  return launch_kernel(grad_tc_kernel, grid, dim3(kThreads), kMaxSmem, stream, 2, p, a.err_word, pk, pm, w, x, dx, dw);
+}
+
+}  // namespace molora

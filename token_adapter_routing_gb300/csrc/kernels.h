@@ -138,6 +138,48 @@ cudaError_t launch_lora_update(const void* h, int64_t N, int32_t d_in, const voi
 bool linear_takes_update(const LinearArgs& a, const void* B, int32_t KR);
 cudaError_t launch_linear(const LinearArgs& a, cudaStream_t stream, const LinearUpdate* update = nullptr);
 
+// e4m3 of x [N x d] with a scale for each row's block of 128 columns.
+cudaError_t launch_quantise_blocks(const void* x, molora_dtype dtype, int64_t N, int32_t d, void* out8, float* scale8,
+                                   cudaStream_t stream);
+
+// The products of a feed-forward block: molora_linear_blocks (gated = false) and molora_gated_linear.
+struct FeedForwardArgs {
+  bool gated;
+  const void* x;
+  molora_dtype dtype;      // MOLORA_E4M3 (with scales for each block), or MOLORA_BF16 if gated
+  const float* x_scale;
+  int64_t N;
+  int32_t d_in;
+  const void* W;           // [d_out x d_in]; gated: [2 d_out x d_in], gate rows first
+  const float* w_scale;
+  int32_t d_out;
+  const float* bias;
+  molora_activation act;
+  const void* residual;
+  void* y;
+  bool y_bf16;
+  void* proj;              // gated bf16: [N x 2 x roundup8(d_out)] or nullptr
+  int32_t* err_word;
+};
+cudaError_t launch_feed_forward(const FeedForwardArgs& a, cudaStream_t stream);
+
+// The gated block's backward pass: dproj from proj and dh, then dx and dW (each may be nullptr).
+struct GatedGradArgs {
+  const void* x;
+  int64_t N;
+  int32_t d_in;
+  const void* W;
+  int32_t d_ff;
+  molora_activation act;
+  const void* proj;
+  const void* dh;
+  void* dproj;
+  void* dx;
+  void* dW;
+  int32_t* err_word;
+};
+cudaError_t launch_gated_grad(const GatedGradArgs& a, cudaStream_t stream);
+
 int num_sms();
 
 cudaError_t launch_bounded_wait_selftest(uint64_t limit_ns, int32_t* err_word, cudaStream_t stream);
