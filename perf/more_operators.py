@@ -172,10 +172,9 @@ def _own(s):
     if s["op"] == "blocks":
         return m.molora_linear_blocks(s["x"], s["sx"], s["W"], s["sw"], y=s["buf"], bias=s["b"], act=s["act"], residual=s["res"])
     if s["op"] == "gated":
-        h, _ = m.molora_gated_linear(s["x"], s["W"], h=s["h"], act=s["act"], x_scale=s["sx"], w_scale=s["sw"])
-        return h
-    h, proj = m.molora_gated_linear(s["x"], s["W"], h=s["h"], act=s["act"], proj=s["proj"])
-    dx, dW, _ = m.molora_gated_linear_backward(s["x"], s["W"], proj, s["dh"], act=s["act"], dx=s["dx"], dW=s["dW"], dproj=proj)
+        return m.molora_gated_linear(s["x"], s["W"], h=s["h"], act=s["act"], x_scale=s["sx"], w_scale=s["sw"])
+    h = m.molora_gated_linear(s["x"], s["W"], h=s["h"], act=s["act"])
+    dx, dW, _ = m.molora_gated_linear_backward(s["x"], s["W"], s["dh"], act=s["act"], dx=s["dx"], dW=s["dW"], dproj=s["proj"])
     return [h, dx, dW]
 
 
