@@ -621,34 +621,34 @@ MOLORA_API molora_status molora_linear_blocks(const void* x, const float* x_scal
  * x [N x d_in] and W [2 d_ff x d_in], the d_ff rows of Wg before those of Wu, share dtype: MOLORA_BF16, or MOLORA_E4M3
  * with a scale for each block of 128: x_scale fp32 [N x ceil(d_in / 128)] and w_scale fp32
  * [2 ceil(d_ff / 128) x ceil(d_in / 128)], Wg's blocks of rows before Wu's; both NULL with MOLORA_BF16.  h bf16 [N x d_ff].
- * proj (MOLORA_BF16 only) bf16 [N x 2 x roundup8(d_ff)] or NULL: g and u, rounded, for the backward pass; columns from
- * d_ff on are unspecified.  h is made of the unrounded g and u in fp32 and rounded once.
- * d_in is a multiple of 8 (MOLORA_BF16) or 16 (MOLORA_E4M3), else MOLORA_ERR_UNSUPPORTED; d_ff up to 2^30 - 1024, N and d_in
- * up to 2^31 - 1024; x, W and proj are 16-byte aligned, the other arrays start on a boundary of their element's size.
- * h and proj share no memory with another array.  Results are reproducible bit for bit.  Lost waits as for molora_linear_blocks.
+ * g and u stay in fp32; h is made of them unrounded and rounded once.
+ * d_in is a multiple of 8 (MOLORA_BF16) or 16 (MOLORA_E4M3), else MOLORA_ERR_UNSUPPORTED; d_ff up to 2^30 - 512, N and d_in
+ * up to 2^31 - 1024; x and W are 16-byte aligned, the other arrays start on a boundary of their element's size.  h shares no
+ * memory with another array.  Results are reproducible bit for bit.  Lost waits as for molora_linear_blocks.
  * The way back to the model's width is molora_linear (or molora_quantise_blocks and molora_linear_blocks) with the residual.
  */
 MOLORA_API molora_status molora_gated_linear(const void* x, molora_dtype dtype, const float* x_scale, int64_t N, int32_t d_in,
                                   const void* W, const float* w_scale, int32_t d_ff, molora_activation act, void* h,
-                                  void* proj, int32_t* err_word, cudaStream_t stream);
+                                  int32_t* err_word, cudaStream_t stream);
 
 /*
  * molora_gated_linear_backward -- the gradients of molora_gated_linear (MOLORA_BF16) from that of h:
  *
- *   dg = dh * u * act'(g),  du = dh * act(g)
+ *   dg = dh * u * act'(g),  du = dh * act(g),  with g = x Wg^T and u = x Wu^T made again, in fp32
  *   dx = dg Wg + du Wu,     dW = [dg^T x; du^T x]
  *
- * proj: as molora_gated_linear wrote it;  dh bf16 [N x d_ff];  dproj bf16 [N x 2 x roundup8(d_ff)]: dg and du, rounded,
- * which the two products read, an output (proj itself allowed);  dx bf16 [N x d_in] or NULL (the weights' gradient
- * alone);  dW bf16 [2 d_ff x d_in] or NULL (frozen weights, as when adapters are trained through them).  x may be NULL
- * without dW, W without dx.  Outputs are overwritten, not added to; N == 0 makes dW zero.
- * act' of RELU is 0 at 0.  Sums are fp32, outputs rounded once.  Sizes and alignment as for molora_gated_linear; dproj, dx and
- * dW are 16-byte aligned too.  No output shares memory with another array, but dproj may be proj.  Results are reproducible
- * bit for bit.  Outputs that a wait that ran out left without their sums stay as they were.
+ * The forward pass leaves nothing but x behind (its g and u, rounded to 16 bits, would put as much error into dx and dW as
+ * the rounding of dproj does).
+ * dh bf16 [N x d_ff];  dproj bf16 [N x 2 x roundup8(d_ff)]: dg and du, rounded, which the two products read, an output
+ * (columns from d_ff on are unspecified);  dx bf16 [N x d_in] or NULL (the weights' gradient alone);  dW bf16
+ * [2 d_ff x d_in] or NULL (frozen weights, as when adapters are trained through them).  Outputs are overwritten, not added
+ * to; N == 0 makes dW zero.  act' of RELU is 0 at 0.  Sums are fp32, outputs rounded once.  Sizes and alignment as for
+ * molora_gated_linear; dproj, dx and dW are 16-byte aligned too.  No output shares memory with another array.  Results are
+ * reproducible bit for bit.  Outputs that a wait that ran out left without their sums stay as they were.
  */
 MOLORA_API molora_status molora_gated_linear_backward(const void* x, molora_dtype dtype, int64_t N, int32_t d_in, const void* W,
-                                           int32_t d_ff, molora_activation act, const void* proj, const void* dh,
-                                           void* dproj, void* dx, void* dW, int32_t* err_word, cudaStream_t stream);
+                                           int32_t d_ff, molora_activation act, const void* dh, void* dproj, void* dx,
+                                           void* dW, int32_t* err_word, cudaStream_t stream);
 
 /* The kernel family molora_lora_apply would choose for this shape when given a workspace
  * (never AUTO; without one, a STACKED choice becomes the best path that needs none). */

@@ -66,12 +66,9 @@ def test_linear_blocks_refuses(kwargs, match):
     (dict(act="swish"), "act must be one of"),
     (dict(h=z(4, 12)), "h must have shape"),
     (dict(h=z(4, 6, dtype=F32)), "h must be torch.bfloat16"),
-    (dict(proj=z(4, 2, 6)), "proj must have shape"),
     (dict(x_scale=z(4, 1, dtype=F32)), "x_scale and w_scale"),
     (dict(x=z(4, 16, dtype=FP8), W=z(12, 16, dtype=FP8)), "x_scale and w_scale"),
     (dict(x=z(4, 16, dtype=FP8), W=z(12, 16, dtype=FP8), x_scale=z(4, 1, dtype=F32), w_scale=z(1, 1, dtype=F32)), "w_scale must have shape"),
-    (dict(x=z(4, 16, dtype=FP8), W=z(12, 16, dtype=FP8), x_scale=z(4, 1, dtype=F32), w_scale=z(2, 1, dtype=F32), want_proj=True),
-     "proj is for bfloat16"),
     (dict(), "must be a CUDA tensor"),
 ])
 def test_gated_refuses(kwargs, match):
@@ -82,10 +79,7 @@ def test_gated_refuses(kwargs, match):
 @pytest.mark.parametrize("kwargs, match", [
     (dict(x=z(4, 16, dtype=FP8)), "x must be one of"),
     (dict(W=z(13, 16)), "W must be a 2-D"),
-    (dict(proj=None), "must be tensors"),
-    (dict(dh=None), "must be tensors"),
-    (dict(proj=z(4, 2, 6)), "proj must have shape"),
-    (dict(proj=z(4, 16)), "proj must have shape"),
+    (dict(dh=None), "must be a tensor"),
     (dict(dh=z(4, 8)), "dh must have shape"),
     (dict(dh=z(4, 6, dtype=F32)), "dh must be torch.bfloat16"),
     (dict(dx=z(4, 8)), "dx must have shape"),
@@ -97,7 +91,7 @@ def test_gated_refuses(kwargs, match):
 ])
 def test_gated_backward_refuses(kwargs, match):
     with pytest.raises(ValueError, match=match):
-        m.molora_gated_linear_backward(**(dict(x=z(4, 16), W=z(12, 16), proj=z(4, 2, 8), dh=z(4, 6)) | kwargs))
+        m.molora_gated_linear_backward(**(dict(x=z(4, 16), W=z(12, 16), dh=z(4, 6)) | kwargs))
 
 
 OK, INVALID, UNSUPPORTED = 0, 1, 2
@@ -142,16 +136,15 @@ def test_c_abi_linear_blocks(lib):
 @needs_nvcc
 def test_c_abi_gated(lib):
     f = lib.molora_gated_linear
-    good = dict(x=X, dtype=B, sx=None, N=4, d_in=64, W=WT, sw=None, d_ff=50, act=2, h=Y, proj=P)
+    good = dict(x=X, dtype=B, sx=None, N=4, d_in=64, W=WT, sw=None, d_ff=50, act=2, h=Y)
 
     def call(**kw):
         return f(*(good | kw).values(), None, None)
-    fp8 = dict(dtype=Q, sx=SX, sw=SW, proj=None)
-    assert call(N=0, x=None, W=None, h=None, proj=None) == OK and call(N=0, **fp8) == OK
+    fp8 = dict(dtype=Q, sx=SX, sw=SW)
+    assert call(N=0, x=None, W=None, h=None) == OK and call(N=0, **fp8) == OK
     for bad in [dict(dtype=F), dict(dtype=3), dict(N=-1), dict(d_in=0), dict(d_ff=0), dict(act=9), dict(x=None), dict(W=None),
-                dict(h=None), dict(sx=SX), dict(sw=SW), dict(x=X + 2), dict(W=WT + 8), dict(proj=P + 8), dict(h=Y + 1), dict(h=X),
-                dict(proj=X), dict(h=WT + 2 * 99 * 64), dict(proj=Y), dict(proj=Y + 16), dict(h=P + 2 * 2 * 56 * 3), dict(d_ff=2 ** 30),
-                fp8 | dict(proj=P), fp8 | dict(sx=None), fp8 | dict(sw=None), fp8 | dict(h=SX), fp8 | dict(h=SW)]:
+                dict(h=None), dict(sx=SX), dict(sw=SW), dict(x=X + 2), dict(W=WT + 8), dict(h=Y + 1), dict(h=X),
+                dict(h=WT + 2 * 99 * 64), dict(d_ff=2 ** 30), fp8 | dict(sx=None), fp8 | dict(sw=None), fp8 | dict(h=SX), fp8 | dict(h=SW)]:
         assert call(**bad) == INVALID, bad
     assert call(d_in=63) == UNSUPPORTED and call(d_in=4) == UNSUPPORTED and call(**(fp8 | dict(d_in=72))) == UNSUPPORTED
 
@@ -159,14 +152,13 @@ def test_c_abi_gated(lib):
 @needs_nvcc
 def test_c_abi_gated_backward(lib):
     f = lib.molora_gated_linear_backward
-    good = dict(x=X, dtype=B, N=4, d_in=64, W=WT, d_ff=50, act=2, proj=P, dh=SX, dproj=P, dx=Y, dW=R)
+    good = dict(x=X, dtype=B, N=4, d_in=64, W=WT, d_ff=50, act=2, dh=SX, dproj=P, dx=Y, dW=R)
 
     def call(**kw):
         return f(*(good | kw).values(), None, None)
-    assert call(N=0, x=None, W=None, proj=None, dh=None, dproj=None, dx=None, dW=None) == OK
+    assert call(N=0, x=None, W=None, dh=None, dproj=None, dx=None, dW=None) == OK
     for bad in [dict(dtype=F), dict(dtype=Q), dict(N=-1), dict(d_in=0), dict(d_ff=0), dict(act=5), dict(x=None), dict(W=None),
-                dict(proj=None), dict(dh=None), dict(dproj=None), dict(x=X + 2), dict(W=WT + 2), dict(proj=P + 2), dict(dproj=P + 16),
-                dict(dx=Y + 8), dict(dW=R + 2), dict(dh=SX + 1), dict(dx=X), dict(dx=P), dict(dW=WT), dict(dW=X), dict(dx=SX),
+                dict(dh=None), dict(dproj=None), dict(x=X + 2), dict(W=WT + 2), dict(dproj=P + 2), dict(dx=Y + 8), dict(dW=R + 2), dict(dh=SX + 1), dict(dx=X), dict(dx=P), dict(dW=WT), dict(dW=X), dict(dx=SX),
                 dict(dproj=SX), dict(dproj=X), dict(dproj=WT), dict(dx=R), dict(dW=Y), dict(dproj=Y), dict(dproj=R + 128)]:
         assert call(**bad) == INVALID, bad
     assert call(d_in=60) == UNSUPPORTED and call(N=0, d_in=60) == UNSUPPORTED

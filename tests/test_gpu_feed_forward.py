@@ -9,9 +9,10 @@ Tolerances, derived from the arithmetic (u = 2^-24, half a step of fp32; half a 
     (2 u 128 + u (blocks + 4)) S, with S of the scaled operands.
   * epilogue: bias and activation (whose slope is at most 1.13) add 16 u of what they handle; outputs round once.
   * gated: with errors eg, eu of g and u, act(g) u is off by 1.13 eg (|u| + eu) + |act(g)| eu + 32 u |h|.
-  * backward, from proj as stored: act' is a sum of two terms that are 3 together at most, each within 256 u (an
-    exponent of up to 126 and its factors within 2 u each); dproj rounds once.  dx and dW are sums of 2 d_ff and N products
-    of dproj as stored.
+  * backward: act' is a sum of two terms that are 3 together at most, each within 256 u (an exponent of up to 126 and its
+    factors within 2 u each); act'' is at most 1.2.  dg = dh u act'(g) is off by |dh| (|u| (768 u + 1.2 eg) + 1.13 eu),
+    du = dh act(g) by |dh| (1.13 eg + 256 u |act(g)|); both round once.  dx and dW are sums of 2 d_ff and N products of
+    dproj as stored.
 Small integers, whose every partial sum is exact, have to come out bit for bit."""
 
 import math
@@ -282,24 +283,15 @@ SIZES = [(1, 16, 1), (1, 2048, 640), (2, 128, 7), (16, 64, 33), (7, 1040, 64), (
 def test_gated_linear(m, dtype, N, d, F, act):
     g = gen(N + d + F)
     x, sx, W, sw = gated_inputs(g, dtype, N, d, F)
-    want, gate, up, tol, eg, eu = gated64(x, sx, W, sw, act)
+    want, _, _, tol, _, _ = gated64(x, sx, W, sw, act)
     e = err_word()
     out, free = guarded((N, F), BF)
     scales = {} if dtype == BF else dict(x_scale=beside_nan(sx), w_scale=beside_nan(sw))
-    h, proj = m.molora_gated_linear(beside_nan(x), beside_nan(W), h=out, act=act, err_word=e, **scales)
-    assert h is out and proj is None and e.item() == 0
+    h = m.molora_gated_linear(beside_nan(x), beside_nan(W), h=out, act=act, err_word=e, **scales)
+    assert h is out and e.item() == 0
     within(h, want, tol + (want.abs() + tol) * HALF[BF])
     free()
-    if dtype == BF:
-        p, free = guarded((N, 2, (F + 7) // 8 * 8), BF)
-        again, proj = m.molora_gated_linear(x, W, act=act, proj=p)
-        assert torch.equal(again, h) and proj is p
-        within(p[:, 0, :F], gate, eg + (gate.abs() + eg) * HALF[BF])
-        within(p[:, 1, :F], up, eu + (up.abs() + eu) * HALF[BF])
-        free()
-    else:
-        again, _ = m.molora_gated_linear(x, W, act=act, x_scale=sx, w_scale=sw)
-        assert torch.equal(again, h)
+    assert torch.equal(m.molora_gated_linear(x, W, act=act, x_scale=sx, w_scale=sw), h)
 
 
 @pytest.mark.parametrize("act", ["none", "relu", "gelu"])
@@ -309,7 +301,7 @@ def test_gated_linear_activations(m, act, dtype, N):
     g = gen(N)
     x, sx, W, sw = gated_inputs(g, dtype, N, 256, 520)
     want, _, _, tol, _, _ = gated64(x, sx, W, sw, act)
-    h, _ = m.molora_gated_linear(x, W, act=act, x_scale=sx, w_scale=sw)
+    h = m.molora_gated_linear(x, W, act=act, x_scale=sx, w_scale=sw)
     within(h, want, tol + (want.abs() + tol) * HALF[BF])
 
 
@@ -324,7 +316,7 @@ def test_gated_linear_exact_integers(m, dtype, N, d, F):
         sx = torch.exp2(torch.randint(0, 2, (N, blocks(d)), generator=g, device="cuda").float())
         sw = torch.exp2(torch.randint(0, 2, (2 * blocks(F), blocks(d)), generator=g, device="cuda").float())
     want, gate, up, _, _, _ = gated64(x, sx, W, sw, "relu")
-    h, _ = m.molora_gated_linear(x, W, act="relu", x_scale=sx, w_scale=sw)
+    h = m.molora_gated_linear(x, W, act="relu", x_scale=sx, w_scale=sw)
     assert gate.abs().max() < 2 ** 20
     # relu(g) u rounds to fp32, then to bf16
     assert torch.equal(h, (torch.relu(gate.float()) * up.float()).to(BF))
@@ -336,17 +328,16 @@ def test_gated_linear_unaligned_and_nan(m, dtype, N):
     g = gen(N)
     x, sx, W, sw = gated_inputs(g, dtype, N, 256, 264)
     kw = {} if dtype == BF else dict(x_scale=sx, w_scale=sw)
-    want, _ = m.molora_gated_linear(x, W, **kw)
+    want = m.molora_gated_linear(x, W, **kw)
     out, free = guarded((N, 264), BF, shift=1)
-    proj = None if dtype == FP8 else torch.empty(N, 2, 264, dtype=BF, device="cuda")
-    m.molora_gated_linear(x, W, h=out, proj=proj, **kw)
+    m.molora_gated_linear(x, W, h=out, **kw)
     assert torch.equal(out, want)
     free()
     x2, W2 = x.clone(), W.clone()
     x2[2, 7] = math.nan
     W2[11, 3] = math.nan        # a gate's row
     W2[264 + 40, 250] = math.nan  # an up projection's
-    h, _ = m.molora_gated_linear(x2, W2, **kw)
+    h = m.molora_gated_linear(x2, W2, **kw)
     lost = torch.zeros_like(want, dtype=torch.bool)
     lost[2], lost[:, 11], lost[:, 40] = True, True, True
     assert torch.isnan(h[lost]).all() and torch.equal(h[~lost], want[~lost])
@@ -359,27 +350,32 @@ def slope64(v, act):
     return v.grad
 
 
-def check_backward(m, x, W, proj, dh, act, **kw):
+def check_backward(m, x, W, dh, act, **kw):
     N, d = x.shape
     F = W.shape[0] // 2
     e = err_word()
-    g, u = proj[:, 0, :F].double().clone(), proj[:, 1, :F].double().clone()
-    dx, dW, dproj = m.molora_gated_linear_backward(x, W, proj, dh, act=act, err_word=e, **kw)
+    _, g, u, _, eg, eu = gated64(x, None, W, None, act)
+    dx, dW, dproj = m.molora_gated_linear_backward(x, W, dh, act=act, err_word=e, **kw)
     assert e.item() == 0
-    dhu, s, a = dh.double() * u, slope64(g, act), ACTS[act](g)
+    dh, s, a, tiny = dh.double(), slope64(g, act), ACTS[act](g), 2.0 ** -118
     dg, du = dproj[:, 0, :F], dproj[:, 1, :F]
-    tol = 3 * 256 * U * dhu.abs() + 2.0 ** -130
-    within(dg, dhu * s, tol + (dhu * s).abs() * (HALF[BF] + 4 * U))
-    within(du, dh.double() * a, (dh.double() * a).abs() * (HALF[BF] + 256 * U) + 2.0 ** -130)
-    dp = torch.cat([dg, du], dim=1).double()
+    if act == "relu":  # a gate within eg of 0 may fall on either side of it
+        s, near = torch.where(g.abs() <= eg, torch.nan, s), g.abs() <= eg
+        dg = torch.where(near, 0.0, dg.double())
+        s = torch.where(near, 0.0, s)
+    tol = dh.abs() * (u.abs() * (768 * U + 1.2 * eg) + 1.13 * eu)
+    within(dg, dh * u * s, tol + ((dh * u * s).abs() + tol) * HALF[BF] + tiny)
+    tol = dh.abs() * (1.13 * eg + 256 * U * a.abs())
+    within(du, dh * a, tol + ((dh * a).abs() + tol) * HALF[BF] + tiny)
+    dp = torch.cat([dproj[:, 0, :F], du], dim=1).double()
     if dx is not None:
         want, S = dp @ W.double(), dp.abs() @ W.double().abs()
         tol = 2 * U * 2 * F * S
-        within(dx, want, tol + (want.abs() + tol) * HALF[BF] + 2.0 ** -130)
+        within(dx, want, tol + (want.abs() + tol) * HALF[BF] + tiny)
     if dW is not None:
         want, S = dp.T @ x.double(), dp.abs().T @ x.double().abs()
         tol = 2 * U * N * S
-        within(dW, want, tol + (want.abs() + tol) * HALF[BF] + 2.0 ** -130)
+        within(dW, want, tol + (want.abs() + tol) * HALF[BF] + tiny)
     return dx, dW, dproj
 
 
@@ -390,74 +386,75 @@ def test_gated_backward(m, N, d, F, act):
     g = gen(N + d + F)
     x, _, W, _ = gated_inputs(g, BF, N, d, F)
     dh = randn(g, N, F).to(BF)
-    _, proj = m.molora_gated_linear(x, W, act=act, want_proj=True)
     dx, free_x = guarded((N, d), BF)
     dW, free_w = guarded((2 * F, d), BF)
-    out = check_backward(m, beside_nan(x), beside_nan(W), proj, beside_nan(dh), act, dx=dx, dW=dW)
-    free_x(), free_w()
-    # in place, and one of the two alone: the same bits
-    mine = proj.clone()
-    a, none, dp = m.molora_gated_linear_backward(x, W, mine, dh, act=act, dproj=mine, want_dW=False)
-    assert none is None and dp is mine and torch.equal(a, out[0]) and torch.equal(dp[:, :, :F], out[2][:, :, :F])
-    none, b, _ = m.molora_gated_linear_backward(x, W, proj, dh, act=act, want_dx=False)
-    assert none is None and torch.equal(b, out[1])
+    dproj, free_p = guarded((N, 2, (F + 7) // 8 * 8), BF)
+    out = check_backward(m, beside_nan(x), beside_nan(W), beside_nan(dh), act, dx=dx, dW=dW, dproj=dproj)
+    free_x(), free_w(), free_p()
+    # one of the two alone, and dh off 16-byte boundaries: the same bits
+    a, none, _ = m.molora_gated_linear_backward(x, W, dh, act=act, want_dW=False)
+    assert none is None and torch.equal(a, out[0])
+    off = torch.empty(N * F + 1, dtype=BF, device="cuda")[1:].view(N, F)
+    off.copy_(dh)
+    none, b, dp = m.molora_gated_linear_backward(x, W, off, act=act, want_dx=False)
+    assert none is None and torch.equal(b, out[1]) and torch.equal(dp[:, :, :F], out[2][:, :, :F])
 
 
 @pytest.mark.parametrize("act", ["none", "relu", "gelu"])
 def test_gated_backward_activations(m, act):
     g = gen(3)
     x, _, W, _ = gated_inputs(g, BF, 200, 256, 520)
-    _, proj = m.molora_gated_linear(x, W, act=act, want_proj=True)
-    check_backward(m, x, W, proj, randn(g, 200, 520).to(BF), act)
+    check_backward(m, x, W, randn(g, 200, 520).to(BF), act)
 
 
 @pytest.mark.parametrize("act", list(ACTS))
 def test_slopes_over_the_whole_range(m, act):
-    """dproj where the activation saturates, overflows or underflows: every finite bf16 gate."""
+    """dproj where the activation saturates, overflows or underflows: every finite bf16 gate, as one product with 1."""
     v = torch.arange(1 << 16, dtype=torch.int32, device="cuda").to(torch.int16).view(BF)
     v = v[torch.isfinite(v)]
     v = v[(v == 0) | (v.abs() >= 2.0 ** -120)]  # (fp32 powers flush what is smaller)
-    F = v.numel() // 8 * 8
-    v = v[:F]
-    proj = torch.ones(1, 2, F, dtype=BF, device="cuda")
-    proj[0, 0] = v
+    F = v.numel()
+    x = torch.zeros(1, 8, dtype=BF, device="cuda")
+    x[0, 0] = 1
+    W = torch.zeros(2 * F, 8, dtype=BF, device="cuda")
+    W[:F, 0], W[F:, 0] = v, 1
     dh = torch.ones(1, F, dtype=BF, device="cuda")
-    x, W = torch.zeros(1, 8, dtype=BF, device="cuda"), torch.zeros(2 * F, 8, dtype=BF, device="cuda")
-    _, _, dproj = m.molora_gated_linear_backward(x, W, proj, dh, act=act, want_dW=False)
+    _, _, dproj = m.molora_gated_linear_backward(x, W, dh, act=act, want_dW=False)
     a, s = ACTS[act](v.double()), slope64(v.double(), act)
     if act == "gelu_tanh":  # (v^3 past fp64's square of it, 0 times infinity in the formula's gradient: saturated)
         s = torch.where(torch.isfinite(s), s, (v > 0).double())
-    within(dproj[0, 0], s, 3 * 256 * U + s.abs() * HALF[BF])
+    within(dproj[0, 0, :F], s, 3 * 256 * U + s.abs() * HALF[BF])
     # p within 256 u of itself, but flushed below 2^-126, where v p is below 2^-119
-    within(dproj[0, 1], a, a.abs() * (HALF[BF] + 256 * U) + 2.0 ** -118)
+    within(dproj[0, 1, :F], a, a.abs() * (HALF[BF] + 256 * U) + 2.0 ** -118)
 
 
 @pytest.mark.parametrize("N, d, F", [(5, 64, 24), (200, 264, 136), (900, 136, 1000), (2000, 512, 256)])
 def test_gated_backward_exact_integers(m, N, d, F):
+    """Sparse small integers, so that the projections, dproj (below 256) and the sums are exact."""
     g = gen(N)
-    ints = lambda lo, hi, *s: torch.randint(lo, hi, s, generator=g, device="cuda").to(BF)  # noqa: E731
-    x, W, dh = ints(-1, 2, N, d), ints(-1, 2, 2 * F, d), ints(-1, 2, N, F)
-    proj = ints(-2, 3, N, 2, (F + 7) // 8 * 8)
-    dx, dW, dproj = m.molora_gated_linear_backward(x, W, proj, dh, act="relu")
-    dg = (dh * proj[:, 1, :F] * (proj[:, 0, :F] > 0)).double()
-    du = (dh * torch.relu(proj[:, 0, :F])).double()
-    assert torch.equal(dproj[:, 0, :F].double(), dg) and torch.equal(dproj[:, 1, :F].double(), du)
-    dp = torch.cat([dg, du], dim=1)
+
+    def ints(*s):
+        return (torch.randint(-1, 2, s, generator=g, device="cuda") * (torch.rand(s, generator=g, device="cuda") < 0.1)).to(BF)
+    x, W, dh = ints(N, d), ints(2 * F, d), torch.randint(-1, 2, (N, F), generator=g, device="cuda").to(BF)
+    dx, dW, dproj = m.molora_gated_linear_backward(x, W, dh, act="relu")
+    gate, up = (x.double() @ W.double().T).split(F, dim=1)
+    dp = torch.cat([dh.double() * up * (gate > 0), dh.double() * torch.relu(gate)], dim=1)
+    assert dp.abs().max() <= 256
+    assert torch.equal(torch.cat([dproj[:, 0, :F], dproj[:, 1, :F]], dim=1).double(), dp)
     assert torch.equal(dx, (dp @ W.double()).float().to(BF))
     assert torch.equal(dW, (dp.T @ x.double()).float().to(BF))
 
 
 def test_gated_gradient_against_differences(m):
     """<dx, v> + <dW, V> against (L(x + e v, W + e V) - L(x - e v, W - e V)) / 2 e of L = sum h dh in 64 bits.  The central
-    difference is off by e^2 / 6 of a third derivative, 1e-9 here; dx and dW by the roundings to bf16 of proj, dproj and
-    themselves, 2^-8 each of their terms."""
+    difference is off by e^2 / 6 of a third derivative, 1e-9 here, and by 2^-53 of L / e.  dproj, dx and dW round to bf16, by
+    2^-8 of themselves at most and in either direction: six deviations of what these roundings sum to."""
     g = gen(8)
     N, d, F = 48, 64, 40
     x, _, W, _ = gated_inputs(g, BF, N, d, F)
     dh = randn(g, N, F).to(BF)
     for act in ("silu", "gelu", "gelu_tanh"):
-        _, proj = m.molora_gated_linear(x, W, act=act, want_proj=True)
-        dx, dW, dproj = m.molora_gated_linear_backward(x, W, proj, dh, act=act)
+        dx, dW, dproj = m.molora_gated_linear_backward(x, W, dh, act=act)
         v, V = randn(g, N, d).double(), randn(g, 2 * F, d).double() / math.sqrt(d)
 
         def loss(e):
@@ -466,26 +463,19 @@ def test_gated_gradient_against_differences(m):
         e = 1e-5
         want = (loss(e) - loss(-e)) / (2 * e)
         got = (dx.double() * v).sum() + (dW.double() * V).sum()
-        dp = torch.cat([dproj[:, 0, :F], dproj[:, 1, :F]], dim=1).double().abs()
-        # a rounded g moves dg by |dh u act''| |g| 2^-8, and du by |dh act'| |g| 2^-8; act'' and act' are at most 1.2
-        gate, up = proj[:, 0, :F].double().abs(), proj[:, 1, :F].double().abs()
-        moved = dh.double().abs() * 1.2 * torch.cat([up * gate + up, gate], dim=1)
-        terms = (v.abs() * (dp @ W.double().abs())).sum() + (V.abs() * (dp.T @ x.double().abs())).sum()
-        moved = (v.abs() * (moved @ W.double().abs())).sum() + (V.abs() * (moved.T @ x.double().abs())).sum()
-        assert abs(got - want) <= HALF[BF] * (2 * terms + moved) + 1e-6
-        # and far closer than that worst case, as roundings of either sign cancel: a wrong factor of one term would show
-        scale = ((dx.double() * v).pow(2).sum() + (dW.double() * V).pow(2).sum()).sqrt()
-        assert abs(got - want) <= 8 * 2.0 ** -8 * scale
+        dp = torch.cat([dproj[:, 0, :F], dproj[:, 1, :F]], dim=1).double()
+        rounded = [dp * (v @ W.double().T + x.double() @ V.T), dx.double() * v, dW.double() * V]
+        deviation = HALF[BF] * sum(r.pow(2).sum() for r in rounded).sqrt()
+        assert abs(got - want) <= 6 * deviation + 1e-6
 
 
 def test_gated_backward_of_nothing(m):
     W = torch.randn(48, 16, device="cuda").to(BF)
     x, dh = torch.empty(0, 16, dtype=BF, device="cuda"), torch.empty(0, 24, dtype=BF, device="cuda")
-    h, proj = m.molora_gated_linear(x, W, want_proj=True)
-    assert h.shape == (0, 24) and proj.shape == (0, 2, 24)
+    assert m.molora_gated_linear(x, W).shape == (0, 24)
     dW = torch.ones_like(W)
-    dx, dW, _ = m.molora_gated_linear_backward(x, W, proj, dh, dW=dW)
-    assert dx.shape == (0, 16) and (dW == 0).all()
+    dx, dW, dproj = m.molora_gated_linear_backward(x, W, dh, dW=dW)
+    assert dx.shape == (0, 16) and dproj.shape == (0, 2, 24) and (dW == 0).all()
     x8 = torch.empty(0, 16, dtype=FP8, device="cuda")
     assert m.molora_linear_blocks(x8, torch.empty(0, 1, device="cuda"), W.to(FP8), torch.ones(1, 1, device="cuda")).shape == (0, 48)
     assert m.molora_quantise_blocks(x)[0].shape == (0, 16)
@@ -513,13 +503,13 @@ def test_feed_forward_half_in_bf16_and_in_blocks(m):
 
     def half16(x):
         _, n, _, _ = m.molora_rmsnorm(x, nw)
-        h, _ = m.molora_gated_linear(n, W.to(BF))
+        h = m.molora_gated_linear(n, W.to(BF))
         return m.molora_linear(h, Wd.to(BF), residual=x, out_dtype=BF)
 
     def half8(x):
         _, n, _, _ = m.molora_rmsnorm(x, nw)
         n8, ns = m.molora_quantise_blocks(n)
-        h, _ = m.molora_gated_linear(n8, W8, x_scale=ns, w_scale=ws)
+        h = m.molora_gated_linear(n8, W8, x_scale=ns, w_scale=ws)
         h8, hs = m.molora_quantise_blocks(h)
         return m.molora_linear_blocks(h8, hs, d8, ds, residual=x, out_dtype=BF)
 
@@ -559,12 +549,12 @@ def test_adapters_train_through_a_frozen_block(m):
     x, _, W, _ = gated_inputs(g, BF, N, d, F)
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
-    h, proj = m.molora_gated_linear(x, W, want_proj=True, stream=side)
+    h = m.molora_gated_linear(x, W, stream=side)
     dh = randn(g, N, F).to(BF)
     side.wait_stream(torch.cuda.current_stream())
-    dx, dW, dproj = m.molora_gated_linear_backward(x, W, proj, dh, want_dW=False, stream=side)
+    dx, dW, dproj = m.molora_gated_linear_backward(x, W, dh, want_dW=False, stream=side)
     torch.cuda.current_stream().wait_stream(side)
-    for t in (h, proj, dx, dproj):
+    for t in (h, dx, dproj):
         t.record_stream(torch.cuda.current_stream())
-    want, _, _ = m.molora_gated_linear_backward(x, W, proj, dh)
+    want, _, _ = m.molora_gated_linear_backward(x, W, dh)
     assert dW is None and torch.equal(dx, want)

@@ -120,8 +120,8 @@ def load_library(path=None):
                                                   P, P, I32, P, P, P, F, P, I32, P, P, P, P]
     lib.molora_quantise_blocks.argtypes = [P, S, I64, I32, P, P, P]
     lib.molora_linear_blocks.argtypes = [P, P, I64, I32, P, P, I32, P, S, P, P, I32, P, P]
-    lib.molora_gated_linear.argtypes = [P, S, P, I64, I32, P, P, I32, S, P, P, P, P]
-    lib.molora_gated_linear_backward.argtypes = [P, S, I64, I32, P, I32, S, P, P, P, P, P, P, P]
+    lib.molora_gated_linear.argtypes = [P, S, P, I64, I32, P, P, I32, S, P, P, P]
+    lib.molora_gated_linear_backward.argtypes = [P, S, I64, I32, P, I32, S, P, P, P, P, P, P]
     lib.molora_select_path.argtypes = [S, I64, I32, I32, I32, I32, I32]
     lib.molora_status_string.argtypes = [S]
     lib.molora_status_string.restype = ctypes.c_char_p
@@ -999,17 +999,10 @@ def _gated_weights(W, d_in):
     return W.shape[0] // 2
 
 
-def _proj_shape(N, d_ff):
-    return (N, 2, (d_ff + 7) // 8 * 8)
-
-
-def molora_gated_linear(x, W, h=None, act="silu", x_scale=None, w_scale=None, proj=None, want_proj=False, err_word=None,
-                        stream=None):
+def molora_gated_linear(x, W, h=None, act="silu", x_scale=None, w_scale=None, err_word=None, stream=None):
     """The gated half of a feed-forward block: h = act(x Wg^T) * (x Wu^T), bfloat16 [N, d_ff], for x [N, d_in] and
     W = [Wg; Wu] [2 d_ff, d_in] in bfloat16 (d_in a multiple of 8), or in float8_e4m3fn (of 16) with a scale for each block of
-    SCALE_BLOCK: x_scale float32 [N, blocks of d_in] and w_scale float32 [2 * blocks of d_ff, blocks of d_in].  Returns
-    (h, proj).  ``proj`` (bfloat16 [N, 2, d_ff rounded up to 8], bfloat16 x only): both projections, as
-    molora_gated_linear_backward reads them, written if given or if want_proj, else None."""
+    SCALE_BLOCK: x_scale float32 [N, blocks of d_in] and w_scale float32 [2 * blocks of d_ff, blocks of d_in]."""
     code = _matrix(x, "x", (torch.bfloat16, torch.float8_e4m3fn))
     N, d_in = x.shape
     dev, bf16, f32 = x.get_device(), torch.bfloat16, torch.float32
@@ -1018,48 +1011,46 @@ def molora_gated_linear(x, W, h=None, act="silu", x_scale=None, w_scale=None, pr
     fp8 = code == E4M3
     if fp8 != (x_scale is not None) or fp8 != (w_scale is not None):
         raise ValueError("x_scale and w_scale are needed with float8_e4m3fn, and with nothing else")
-    if fp8 and (want_proj or proj is not None):
-        raise ValueError("proj is for bfloat16 x")
     px = _array(x, "x", x.shape, x.dtype, dev)
     pw = _array(W, "W", (2 * d_ff, d_in), x.dtype, dev)
     psx = _array(x_scale, "x_scale", (N, blocks), f32, dev)
     psw = _array(w_scale, "w_scale", (2 * _scale_blocks(d_ff), blocks), f32, dev)
     if h is None:
         h = _new(x, (N, d_ff), bf16, stream)
-    if proj is None and want_proj:
-        proj = _new(x, _proj_shape(N, d_ff), bf16, stream)
-    ph, pp = _array(h, "h", (N, d_ff), bf16, dev), _array(proj, "proj", _proj_shape(N, d_ff), bf16, dev)
+    ph = _array(h, "h", (N, d_ff), bf16, dev)
     _on_gpu(x, "x")
-    _call("molora_gated_linear", dev, px, code, psx, N, d_in, pw, psw, d_ff, act, ph, pp, _error_word(err_word, dev),
+    _call("molora_gated_linear", dev, px, code, psx, N, d_in, pw, psw, d_ff, act, ph, _error_word(err_word, dev),
           _raw_stream(stream, dev))
-    return h, proj
+    return h
 
 
-def molora_gated_linear_backward(x, W, proj, dh, act="silu", dx=None, dW=None, dproj=None, want_dx=True, want_dW=True,
+def molora_gated_linear_backward(x, W, dh, act="silu", dx=None, dW=None, dproj=None, want_dx=True, want_dW=True,
                                  err_word=None, stream=None):
-    """The gradients of molora_gated_linear's bfloat16 form from that of h, dh [N, d_ff], and its proj: returns (dx, dW,
-    dproj), dx [N, d_in] and dW [2 d_ff, d_in], made if not given unless want_dx or want_dW is false (frozen weights need no
-    dW).  ``dproj`` (proj's shape, proj itself allowed) is the projections' gradient, made if not given."""
+    """The gradients of molora_gated_linear's bfloat16 form from that of h, dh [N, d_ff]; the projections are made again.
+    Returns (dx, dW, dproj): dx [N, d_in] and dW [2 d_ff, d_in], made if not given unless want_dx or want_dW is false
+    (frozen weights need no dW), and dproj [N, 2, d_ff rounded up to 8], the projections' gradient (columns from d_ff on are
+    unspecified), made if not given."""
     code = _matrix(x, "x", (torch.bfloat16,))
     N, d_in = x.shape
     dev, bf16 = x.get_device(), torch.bfloat16
     d_ff = _gated_weights(W, d_in)
     act = _named(act, "act", ACTIVATIONS)
-    if proj is None or dh is None:
-        raise ValueError("proj and dh must be tensors")
+    if dh is None:
+        raise ValueError("dh must be a tensor")
     px = _array(x, "x", x.shape, bf16, dev)
     pw = _array(W, "W", (2 * d_ff, d_in), bf16, dev)
-    pp, pdh = _array(proj, "proj", _proj_shape(N, d_ff), bf16, dev), _array(dh, "dh", (N, d_ff), bf16, dev)
+    pdh = _array(dh, "dh", (N, d_ff), bf16, dev)
     if dx is None and want_dx:
         dx = _new(x, x.shape, bf16, stream)
     if dW is None and want_dW:
         dW = _new(x, W.shape, bf16, stream)
+    proj = (N, 2, (d_ff + 7) // 8 * 8)
     if dproj is None:
-        dproj = _new(x, _proj_shape(N, d_ff), bf16, stream)
+        dproj = _new(x, proj, bf16, stream)
     pdx, pdw = _array(dx, "dx", x.shape, bf16, dev), _array(dW, "dW", W.shape, bf16, dev)
-    pdp = _array(dproj, "dproj", _proj_shape(N, d_ff), bf16, dev)
+    pdp = _array(dproj, "dproj", proj, bf16, dev)
     _on_gpu(x, "x")
-    _call("molora_gated_linear_backward", dev, px, code, N, d_in, pw, d_ff, act, pp, pdh, pdp, pdx, pdw,
+    _call("molora_gated_linear_backward", dev, px, code, N, d_in, pw, d_ff, act, pdh, pdp, pdx, pdw,
           _error_word(err_word, dev), _raw_stream(stream, dev))
     return dx, dW, dproj
 

@@ -202,29 +202,27 @@ static molora_status linear_impl(const LinearArgs& a, cudaStream_t stream) {
 }
 
 static int32_t scale_blocks(int32_t n) { return n / MOLORA_SCALE_BLOCK + (n % MOLORA_SCALE_BLOCK != 0); }
-static int64_t proj_width(int32_t d_ff) { return 2 * (((int64_t)d_ff + 7) & ~int64_t(7)); }
 
 // The checks of molora_linear_blocks and molora_gated_linear.  With N == 0 no pointer is looked at.
 static molora_status check_feed_forward(const FeedForwardArgs& a) {
   const bool fp8 = a.dtype == MOLORA_E4M3;
   if (!(fp8 || (a.gated && a.dtype == MOLORA_BF16)) || a.N < 0 || a.N > kMostSize || a.d_in < 1 || a.d_in > kMostSize ||
-      a.d_out < 1 || a.d_out > (a.gated ? kMostSize / 2 : kMostSize) || a.act < MOLORA_ACT_NONE || a.act > MOLORA_ACT_GELU_TANH ||
-      (a.proj && fp8))
+      a.d_out < 1 || a.d_out > (a.gated ? kMostSize / 2 : kMostSize) || a.act < MOLORA_ACT_NONE || a.act > MOLORA_ACT_GELU_TANH)
     return MOLORA_ERR_INVALID_ARG;
   const size_t e = size_of(a.dtype), ye = a.y_bf16 ? 2 : 4;
   if (a.N > 0) {
     if (!a.x || !a.W || !a.y || fp8 != (a.x_scale != nullptr) || fp8 != (a.w_scale != nullptr)) return MOLORA_ERR_INVALID_ARG;
-    if (!aligned16(a.x) || !aligned16(a.W) || !aligned16(a.proj) || !on_element(a.y, ye) || !on_element(a.residual, ye) ||
+    if (!aligned16(a.x) || !aligned16(a.W) || !on_element(a.y, ye) || !on_element(a.residual, ye) ||
         !on_element(a.bias, 4) || !on_element(a.x_scale, 4) || !on_element(a.w_scale, 4))
       return MOLORA_ERR_INVALID_ARG;
     const int32_t blocks = scale_blocks(a.d_in);
     const int64_t rows = (int64_t)a.d_out * (a.gated ? 2 : 1), row_blocks = (int64_t)scale_blocks(a.d_out) * (a.gated ? 2 : 1);
-    const Span y = {a.y, a.N, a.d_out, ye}, p = {a.proj, a.N, proj_width(a.d_out), 2};
+    const Span y = {a.y, a.N, a.d_out, ye};
     const Span read[] = {{a.x, a.N, a.d_in, e}, {a.W, rows, a.d_in, e}, {a.x_scale, a.N, blocks, 4},
                          {a.w_scale, row_blocks, blocks, 4}, {a.bias, a.d_out, 1, 4}};
     for (const Span& in : read)
-      if (y.shares(in) || p.shares(in)) return MOLORA_ERR_INVALID_ARG;
-    if (y.shares(p) || y.shares_part({a.residual, a.N, a.d_out, ye})) return MOLORA_ERR_INVALID_ARG;
+      if (y.shares(in)) return MOLORA_ERR_INVALID_ARG;
+    if (y.shares_part({a.residual, a.N, a.d_out, ye})) return MOLORA_ERR_INVALID_ARG;
   }
   return a.d_in % (fp8 ? 16 : 8) ? MOLORA_ERR_UNSUPPORTED : MOLORA_OK;
 }
@@ -239,18 +237,16 @@ static molora_status check_gated_grad(const GatedGradArgs& a, molora_dtype dtype
   if (dtype != MOLORA_BF16 || a.N < 0 || a.N > kMostSize || a.d_in < 1 || a.d_in > kMostSize || a.d_ff < 1 ||
       a.d_ff > kMostSize / 2 || a.act < MOLORA_ACT_NONE || a.act > MOLORA_ACT_GELU_TANH)
     return MOLORA_ERR_INVALID_ARG;
-  if (a.N > 0 && (!a.proj || !a.dh || !a.dproj || (a.dW && !a.x) || (a.dx && !a.W))) return MOLORA_ERR_INVALID_ARG;
-  if (!aligned16(a.x) || !aligned16(a.W) || !aligned16(a.proj) || !aligned16(a.dproj) || !aligned16(a.dx) || !aligned16(a.dW) ||
-      !on_element(a.dh, 2))
+  if (a.N > 0 && (!a.x || !a.W || !a.dh || !a.dproj)) return MOLORA_ERR_INVALID_ARG;
+  if (!aligned16(a.x) || !aligned16(a.W) || !aligned16(a.dproj) || !aligned16(a.dx) || !aligned16(a.dW) || !on_element(a.dh, 2))
     return MOLORA_ERR_INVALID_ARG;
-  const Span ps = {a.proj, a.N, proj_width(a.d_ff), 2}, dps = {a.dproj, a.N, proj_width(a.d_ff), 2},
-             dxs = {a.dx, a.N, a.d_in, 2}, dws = {a.dW, 2 * (int64_t)a.d_ff, a.d_in, 2};
+  const Span dps = {a.dproj, a.N, 2 * (((int64_t)a.d_ff + 7) & ~int64_t(7)), 2}, dxs = {a.dx, a.N, a.d_in, 2},
+             dws = {a.dW, 2 * (int64_t)a.d_ff, a.d_in, 2};
   const Span read[] = {{a.x, a.N, a.d_in, 2}, {a.W, 2 * (int64_t)a.d_ff, a.d_in, 2}, {a.dh, a.N, a.d_ff, 2}};
   for (const Span* out : {&dps, &dxs, &dws})
     for (const Span& in : read)
       if (out->shares(in)) return MOLORA_ERR_INVALID_ARG;
-  if (dps.shares_part(ps) || dxs.shares(ps) || dws.shares(ps) || dxs.shares(dps) || dws.shares(dps) || dxs.shares(dws))
-    return MOLORA_ERR_INVALID_ARG;
+  if (dxs.shares(dps) || dws.shares(dps) || dxs.shares(dws)) return MOLORA_ERR_INVALID_ARG;
   return a.d_in % 8 ? MOLORA_ERR_UNSUPPORTED : MOLORA_OK;
 }
 
@@ -536,21 +532,21 @@ molora_status molora_linear_blocks(const void* x, const float* x_scale, int64_t 
                                    const float* w_scale, int32_t d_out, const float* bias, molora_activation act,
                                    const void* residual, void* y, int32_t y_bf16, int32_t* err_word, cudaStream_t stream) {
   const FeedForwardArgs a = {false, x, MOLORA_E4M3, x_scale, N, d_in, W, w_scale, d_out, bias, act, residual, y,
-                             y_bf16 != 0, nullptr, err_word};
+                             y_bf16 != 0, err_word};
   return feed_forward_impl(a, stream);
 }
 
 molora_status molora_gated_linear(const void* x, molora_dtype dtype, const float* x_scale, int64_t N, int32_t d_in,
                                   const void* W, const float* w_scale, int32_t d_ff, molora_activation act, void* h,
-                                  void* proj, int32_t* err_word, cudaStream_t stream) {
-  const FeedForwardArgs a = {true, x, dtype, x_scale, N, d_in, W, w_scale, d_ff, nullptr, act, nullptr, h, true, proj, err_word};
+                                  int32_t* err_word, cudaStream_t stream) {
+  const FeedForwardArgs a = {true, x, dtype, x_scale, N, d_in, W, w_scale, d_ff, nullptr, act, nullptr, h, true, err_word};
   return feed_forward_impl(a, stream);
 }
 
 molora_status molora_gated_linear_backward(const void* x, molora_dtype dtype, int64_t N, int32_t d_in, const void* W,
-                                           int32_t d_ff, molora_activation act, const void* proj, const void* dh,
-                                           void* dproj, void* dx, void* dW, int32_t* err_word, cudaStream_t stream) {
-  const GatedGradArgs a = {x, N, d_in, W, d_ff, act, proj, dh, dproj, dx, dW, err_word};
+                                           int32_t d_ff, molora_activation act, const void* dh, void* dproj,
+                                           void* dx, void* dW, int32_t* err_word, cudaStream_t stream) {
+  const GatedGradArgs a = {x, N, d_in, W, d_ff, act, dh, dproj, dx, dW, err_word};
   const molora_status st = check_gated_grad(a, dtype);
   if (st != MOLORA_OK) return st;
   if (N == 0) return dW ? launched(cudaMemsetAsync(dW, 0, (size_t)4 * d_ff * d_in, stream)) : MOLORA_OK;

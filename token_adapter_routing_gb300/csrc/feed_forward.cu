@@ -3,10 +3,11 @@
 //   blocks:  y[t,o] = act(sum_b sx[t,b] sw[o/128,b] sum_{i in b} x[t,i] W[o,i] + bias[o]) + residual[t,o]
 //            e4m3 operands with one fp32 scale for each 128 columns of a row of x, and each 128 x 128 of W
 //   gated:   h[t,f] = act(g[t,f]) u[t,f],  [g | u] = x [Wg; Wu]^T, in bf16, or in e4m3 with such scales
+//   slopes:  dproj = [dh u act'(g) | dh act(g)], the first step of the gated block's backward pass (gated_grad.cu)
 //
 // Both projections of the gated block are one product: a tile's columns are as many rows of Wg as of Wu, so that the
-// sums of g[t,f] and u[t,f] meet in the registers of one thread and neither goes to memory (unless asked for, as
-// the backward pass reads them).
+// sums of g[t,f] and u[t,f] meet in the registers of one thread and neither goes to memory.  The backward pass makes
+// them again: at 4096 x 2048 -> 6144 their 200 MB in fp32, written and read back, would take as long.
 //
 // ff_tc_kernel (many tokens): linear_tc_kernel's pipeline (linear.cu): persistent pairs of CTAs with tiles of 256 tokens x
 //   BN rows of W, a TMA warp and an MMA warp ahead of 8 epilogue warps by two TMEM accumulators.  Scales change with
@@ -35,6 +36,7 @@ constexpr int kThreads = 32 * (kEpiWarps + 2);  // + TMA warp (8) + MMA warp (9)
 // last warpgroup gives up its own: 256 x 224 + 128 x 56 = 384 x 168.
 constexpr int kTcThreads = 384, kEpiRegisters = 224, kOtherRegisters = 56;
 constexpr int kMaxSets = 4;  // staging boxes an epilogue warp has at most
+enum Mode { kLinear, kGated, kSlopes };
 constexpr int kSpan = 8;     // bf16, few tokens: K blocks summed in TMEM before fp32 registers take over
 
 struct __align__(8) FCtrl {
@@ -53,15 +55,15 @@ struct FEpi {
   const float* sx;   // [N x nkb]
   const float* sw;   // [blocks of W's rows x nkb]
   const float* bias;
-  const void* res;
-  void* y;
-  void* proj;
+  const void* res;   // slopes: dh
+  void* y;           // slopes: dproj
   int64_t N;
   int32_t d_out;     // outputs; gated: d_ff
   int32_t up;        // gated: Wu's first block of rows in sw
   molora_activation act;
   bool y_bf16;
-  bool tma_y;        // rows of y and residual on 16-byte boundaries
+  bool tma_y;        // rows of y on 16-byte boundaries
+  bool tma_res;      // the residual comes through the staging boxes (slopes: dh does, by TMA)
 };
 
 struct FPlan {
@@ -77,18 +79,19 @@ struct FPlan {
 
 }  // namespace
 
-template <bool kFp8, bool kGated, bool kY16>
+template <bool kFp8, Mode kMode, bool kY16>
 __global__ void __launch_bounds__(kTcThreads, 1)
     ff_tc_kernel(const FEpi E, const FPlan P, int32_t* err_word, const __grid_constant__ CUtensorMap map_x,
                  const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_y,
-                 const __grid_constant__ CUtensorMap map_r, const __grid_constant__ CUtensorMap map_p) {
+                 const __grid_constant__ CUtensorMap map_r) {
+  constexpr bool kPaired = kMode != kLinear;  // gate and up projection side by side
   constexpr int kParts = kY16 ? 1 : 2;  // boxes of a chunk of 32 columns of y
   constexpr uint32_t kSet = kParts * kBox;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   FCtrl* ctrl = reinterpret_cast<FCtrl*>(sm + P.off_ctrl);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int BN = P.BN, S = P.S, nkb = P.nkb, width = kGated ? BN / 2 : BN;  // outputs a tile
+  const int BN = P.BN, S = P.S, nkb = P.nkb, width = kPaired ? BN / 2 : BN;  // outputs a tile
   const uint32_t rank = cluster_ctarank();
   const uint16_t both = 0x3;
   const int64_t pair = blockIdx.x / 2, pairs = gridDim.x / 2;
@@ -122,8 +125,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     tma_prefetch_desc(&map_x);
     tma_prefetch_desc(&map_w);
     if (E.tma_y) tma_prefetch_desc(&map_y);
-    if (E.tma_y && E.res) tma_prefetch_desc(&map_r);
-    if (E.proj) tma_prefetch_desc(&map_p);
+    if (E.tma_res) tma_prefetch_desc(&map_r);
   }
   pdl_wait();
   __syncthreads();
@@ -144,7 +146,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         int32_t m0, n0;
         tile_at(pt, m0, n0);
         // the pair's halves of the MMA's columns: gated, one CTA brings rows of Wg and the other of Wu
-        const int32_t n = kGated ? n0 + (int32_t)rank * E.d_out : n0 + (int32_t)rank * (BN / 2);
+        const int32_t n = kPaired ? n0 + (int32_t)rank * E.d_out : n0 + (int32_t)rank * (BN / 2);
         for (int kb = 0; kb < nkb; ++kb) {
           if (issued >= S && !mbar_wait_spin(&ctrl->empty[s], phase, abort)) {
             ok = false;
@@ -212,27 +214,34 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int quarter = warp & 3, side = warp >> 2;
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
     // Outputs leave through a ring of P.sets staging boxes, into which the residual's chunks come before.
-    uint8_t* ring = sm + P.off_stage + (size_t)warp * P.sets * kSet;
-    const bool add = !kGated && E.tma_y && E.res;
-    int tc = 0, used = 0, asked = 0;  // boxes written, and residual chunks on their way or taken
+    // dh's chunks come through a ring of their own, of two boxes.
+    constexpr int kOwn = kMode == kSlopes ? 2 : 0;
+    uint8_t* in_ring = sm + P.off_stage + (size_t)warp * (P.sets + kOwn) * kSet;
+    uint8_t* ring = in_ring + kOwn * kSet;
+    const int in_sets = kOwn ? kOwn : P.sets;
+    int tc = 0, used = 0, asked = 0, taken = 0;  // boxes written; residual chunks on their way or taken, and taken
     auto box_of = [&](int n) { return ring + (size_t)(n & (P.sets - 1)) * kSet; };
-    auto parity_of = [&](int n) { return (uint32_t)(n / P.sets) & 1u; };
+    auto in_box = [&](int n) { return in_ring + (size_t)(n & (in_sets - 1)) * kSet; };
     auto ask = [&](int32_t col, int32_t m0) {
       if (lane == 0) {
-        uint64_t* bar = &ctrl->res_full[warp * kMaxSets + (asked & (P.sets - 1))];
-        // the store that last left the box has read it
-        if (asked >= P.sets) bulk_wait_read_upto(used + P.sets - 1 - asked);
+        uint64_t* bar = &ctrl->res_full[warp * kMaxSets + (asked & (in_sets - 1))];
+        // the store that last left the box has read it (dh's boxes: the lanes have, see below)
+        if (!kOwn && asked >= P.sets) bulk_wait_read_upto(used + P.sets - 1 - asked);
         mbar_arrive_expect_tx(bar, kSet);
         for (int q = 0; q < kParts; ++q)  // (past d_out there is nothing: zeros)
-          tma_load_2d(smem_u32(box_of(asked) + q * kBox), &map_r, col + q * 16, m0, bar);
+          tma_load_2d(smem_u32(in_box(asked) + q * kBox), &map_r, col + q * 16, m0, bar);
       }
       ++asked;
+    };
+    // the next chunk that was asked for; false where the wait ran out
+    auto await = [&]() {
+      return __all_sync(0xffffffffu, mbar_wait(&ctrl->res_full[warp * kMaxSets + (taken & (in_sets - 1))], (uint32_t)(taken / in_sets) & 1u));
     };
     auto piece = [&](uint8_t* box, int i) { return box + (i >> 2) * kBox + swz_offset((uint32_t)lane, (uint32_t)i & 3u, 64); };
     // 32 columns of this warp's rows into a box, ready to be stored by lane 0
     auto stage = [&](const float (&v)[32]) {
       uint8_t* box = box_of(used);
-      if (!add) {
+      if (kOwn || !E.tma_res) {
         if (lane == 0) bulk_wait_read_upto(P.sets - 1);  // the store that last left the box has read it
         __syncwarp();
       }
@@ -264,12 +273,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       // y's chunk from its finished values
       auto put = [&](float (&v)[32], int32_t col) {
         if (E.tma_y) {
-          if (add) {
-            if (!__all_sync(0xffffffffu, mbar_wait(&ctrl->res_full[warp * kMaxSets + (used & (P.sets - 1))], parity_of(used)))) {
+          if (kMode == kLinear && E.tma_res) {
+            if (!await()) {
               ok = false;
               return;
             }
-            uint8_t* box = box_of(used);
+            uint8_t* box = in_box(taken);
 #pragma unroll
             for (int i = 0; i < 4 * kParts; ++i) {
               const uint4 q = *reinterpret_cast<const uint4*>(piece(box, i));
@@ -284,6 +293,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
               }
             }
+            ++taken;
           }
           const uint8_t* box = stage(v);
           if (lane == 0) {
@@ -294,9 +304,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         } else {
           // rows that are not 16-byte aligned: turned in shared memory, written a row at a time, 8 rows' residuals
           // on their way together
-          if (E.proj) {
-            if (lane == 0) bulk_wait_read<0>();  // (the projections leave through the same boxes)
-          }
           float* turned = reinterpret_cast<float*>(ring);
           __syncwarp();
 #pragma unroll
@@ -310,7 +317,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
               o[q] = 0.f;
-              if (!kGated && E.res && in && m0 + q0 + q < E.N) {
+              if (kMode == kLinear && E.res && in && m0 + q0 + q < E.N) {
                 if constexpr (kY16)
                   o[q] = to_float(static_cast<const __nv_bfloat16*>(E.res)[at + (int64_t)q * E.d_out]);
                 else
@@ -341,22 +348,22 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (lane == 0) mbar_arrive_cluster(dsmem_addr(smem_u32(&ctrl->tempty[tc & 1]), 0));
         ++tc;
       };
-      if (add)
-        for (int q = 0; q < mine && q < P.sets; ++q) ask(column(q), m0);
+      if (E.tma_res)
+        for (int q = 0; q < mine && q < in_sets; ++q) ask(column(q), m0);
       if constexpr (kFp8) {
         // 4 pieces of 32 columns of TMEM: linear, this warp's chunks; gated, gate and up of its two chunks in turn
         float acc[4][32];
-        const int pieces = kGated ? 2 * mine : mine;
+        const int pieces = kPaired ? 2 * mine : mine;
         float cb[4], next[4], row;
         const float* ps[4];
         const float* px = E.sx + (t < E.N ? t * nkb : 0);
         row = px[0];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const int32_t col = column(kGated ? q >> 1 : q);
-          ps[q] = E.sw + (q < pieces ? (int64_t)(col / 128 + (kGated && (q & 1) ? E.up : 0)) * nkb : 0);
+          const int32_t col = column(kPaired ? q >> 1 : q);
+          ps[q] = E.sw + (q < pieces ? (int64_t)(col / 128 + (kPaired && (q & 1) ? E.up : 0)) * nkb : 0);
           next[q] = ps[q][0];
-          cb[q] = !kGated && E.bias && q < pieces && col + lane < E.d_out ? E.bias[col + lane] : 0.f;
+          cb[q] = !kPaired && E.bias && q < pieces && col + lane < E.d_out ? E.bias[col + lane] : 0.f;
 #pragma unroll
           for (int i = 0; i < 32; ++i) acc[q][i] = 0.f;
         }
@@ -373,7 +380,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           if (!ok) break;
           auto at = [&](int h) {  // the h-th 16 columns
             const int q = h >> 1;
-            const int c = kGated ? (q & 1) * width + (side + 2 * (q >> 1)) * 32 : (side + 2 * q) * 32;
+            const int c = kPaired ? (q & 1) * width + (side + 2 * (q >> 1)) * 32 : (side + 2 * q) * 32;
             return base + (uint32_t)(c + (h & 1) * 16);
           };
           uint32_t r[2][16];
@@ -397,9 +404,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         if (!ok) break;
 #pragma unroll
-        for (int q = 0; q < (kGated ? 2 : 4); ++q) {
+        for (int q = 0; q < (kPaired ? 2 : 4); ++q) {
           if (q >= mine || !ok) continue;
-          if constexpr (kGated) {
+          if constexpr (kPaired) {
             apply_act(acc[2 * q], E.act);
 #pragma unroll
             for (int i = 0; i < 32; ++i) acc[2 * q][i] *= acc[2 * q + 1][i];
@@ -411,7 +418,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
             apply_act(acc[q], E.act);
             put(acc[q], column(q));
-            if (add && q + P.sets < mine) ask(column(q + P.sets), m0);
+            if (E.tma_res && q + P.sets < mine) ask(column(q + P.sets), m0);
           }
         }
       } else {
@@ -428,29 +435,58 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
           for (int i = 0; i < 32; ++i) g[i] = __uint_as_float(rg[i]), u[i] = __uint_as_float(ru[i]);
           const int32_t col = column(q);
-          if (E.proj) {
-            const uint8_t* box = stage(g);
+          if constexpr (kMode == kGated) {
+            apply_act(g, E.act);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) g[i] *= u[i];
+            put(g, col);
+          } else {
+            uint8_t* box = in_box(taken);
+            if (E.tma_res) {
+              if (!(ok = await())) break;
+            } else {  // rows of dh that start anywhere: a lane a column, turned into the same box
+              __syncwarp();
+              const __nv_bfloat16* dh = static_cast<const __nv_bfloat16*>(E.res) + (int64_t)m0 * E.d_out + col + lane;
+#pragma unroll 8
+              for (int r = 0; r < 32; ++r) {
+                const bool in = m0 + r < E.N && col + lane < E.d_out;
+                *reinterpret_cast<__nv_bfloat16*>(box + swz_offset((uint32_t)r, (uint32_t)lane >> 3, 64) + (lane & 7) * 2) =
+                    in ? dh[(int64_t)r * E.d_out] : __float2bfloat16_rn(0.f);
+              }
+              __syncwarp();
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint4 d = *reinterpret_cast<const uint4*>(piece(box, i));
+              const uint32_t w[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                const float dh = __uint_as_float(j & 1 ? w[j / 2] & 0xffff0000u : w[j / 2] << 16);
+                float a, s;
+                act_and_slope(g[8 * i + j], E.act, a, s);
+                g[8 * i + j] = dh * u[8 * i + j] * s;
+                u[8 * i + j] = dh * a;
+              }
+            }
+            ++taken;
+            if (!E.tma_res) ++asked;
+            const uint8_t* from = stage(g);  // (after its __syncwarp every lane has read dh's box)
             if (lane == 0) {
-              tma_store_3d(&map_p, smem_u32(box), col, 0, m0);
+              tma_store_3d(&map_y, smem_u32(from), col, 0, m0);
               bulk_commit();
             }
-            box = stage(u);
+            from = stage(u);
             if (lane == 0) {
-              tma_store_3d(&map_p, smem_u32(box), col, 1, m0);
+              tma_store_3d(&map_y, smem_u32(from), col, 1, m0);
               bulk_commit();
             }
           }
-          apply_act(g, E.act);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) g[i] *= u[i];
-          put(g, col);
         }
         if (mine == 0) free_sums();
       }
     }
     if (!ok) {
-      for (int n = used; n < asked; ++n)  // no copy is left in flight
-        mbar_wait(&ctrl->res_full[warp * kMaxSets + (n & (P.sets - 1))], parity_of(n));
+      for (; E.tma_res && taken < asked; ++taken) await();  // no copy is left in flight
       *abort = 1;
       if (lane == 0) report(err_word, MOLORA_DEV_WAIT_TIMEOUT);
     }
@@ -482,10 +518,10 @@ struct FSkinnyPlan {
 // [token][row of W] go to shared memory, each CTA adds its share of the outputs in rank order, reading the others'
 // through distributed shared memory, and writes it.  Where `have` is false a wait ran out: such a thread's sums are
 // NaN, and so is what any CTA of the cluster makes of them.
-template <bool kGated, int U, int J>
+template <Mode kMode, int U, int J>
 __device__ __forceinline__ void ff_join(const FEpi& E, const float (&sums)[J][16], bool have, uint8_t* sm, int C, int rank,
                                         int32_t o0, int64_t t0, int tokens, int32_t* err_word) {
-  constexpr int kParts = kGated ? 2 : 1, kQuads = kRows / 4 / kParts;  // quads of outputs a token
+  constexpr int kParts = kMode == kGated ? 2 : 1, kQuads = kRows / 4 / kParts;  // quads of outputs a token
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   float* part = reinterpret_cast<float*>(sm);
   if (!have) report(err_word, MOLORA_DEV_WAIT_TIMEOUT);
@@ -504,7 +540,6 @@ __device__ __forceinline__ void ff_join(const FEpi& E, const float (&sums)[J][16
     const bool vec = E.tma_y;  // (d_out a multiple of 4 and y, residual aligned)
     const bool bias_vec = vec && (reinterpret_cast<uintptr_t>(E.bias) & 15u) == 0;
     const int quads = tokens * kQuads, step = C * 256;
-    const int64_t half = (E.d_out + 7) & ~7;  // gated: elements of a row of one projection
     for (int q0 = rank * 256 + tid; q0 < quads; q0 += U * step) {
       Quad v[U][kParts], res[U];
 #pragma unroll
@@ -512,7 +547,7 @@ __device__ __forceinline__ void ff_join(const FEpi& E, const float (&sums)[J][16
         const int q = q0 + u * step, o = o0 + (q % kQuads) * 4;
         if (q >= quads || o >= E.d_out) continue;
         const int64_t row = (t0 + q / kQuads) * E.d_out;
-        if (!kGated && E.res) {
+        if (kMode == kLinear && E.res) {
           if (E.y_bf16)
             res[u].load(static_cast<const __nv_bfloat16*>(E.res) + row, o, E.d_out, vec);
           else
@@ -539,12 +574,7 @@ __device__ __forceinline__ void ff_join(const FEpi& E, const float (&sums)[J][16
         if (q >= quads || o >= E.d_out) continue;
         const int64_t t = t0 + q / kQuads, row = t * E.d_out;
         Quad& y = v[u][0];
-        if constexpr (kGated) {
-          if (E.proj) {  // (rows of whole quads: past d_ff they are padding)
-            __nv_bfloat16* p = static_cast<__nv_bfloat16*>(E.proj) + t * 2 * half;
-            v[u][0].store(p, o, E.d_out, true);
-            v[u][1].store(p + half, o, E.d_out, true);
-          }
+        if constexpr (kMode == kGated) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) y.v[i] = activate(y.v[i], E.act) * v[u][kParts - 1].v[i];
         } else {
@@ -575,11 +605,11 @@ __device__ __forceinline__ void ff_join(const FEpi& E, const float (&sums)[J][16
 
 // J: columns of sums a thread keeps, 32 J tokens a tile.  Warp w's lanes have rows 32 (w % 4) .. + 31 of the tile's 128
 // of W, columns 16 (w / 4) + 32 j .. + 15 of its tokens.
-template <bool kFp8, bool kGated, int J>
+template <bool kFp8, Mode kMode, int J>
 __global__ void __launch_bounds__(kThreads, 1)
     ff_skinny_kernel(const FEpi E, const FSkinnyPlan P, int32_t* err_word, const __grid_constant__ CUtensorMap map_x,
                      const __grid_constant__ CUtensorMap map_w) {
-  constexpr int kWidth = kGated ? kRows / 2 : kRows;  // outputs a tile
+  constexpr int kWidth = kMode == kGated ? kRows / 2 : kRows;  // outputs a tile
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   FCtrl* ctrl = reinterpret_cast<FCtrl*>(sm + P.off_ctrl);
@@ -636,7 +666,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint8_t* st = sm + (size_t)s * P.stage_bytes;
         mbar_arrive_expect_tx(&ctrl->full[s], P.stage_bytes);
         tma_load_2d(smem_u32(st), &map_w, kb * elems, o0, &ctrl->full[s]);
-        if (kGated) tma_load_2d(smem_u32(st + kWidth * kRowBytes), &map_w, kb * elems, E.d_out + o0, &ctrl->full[s]);
+        if (kMode == kGated) tma_load_2d(smem_u32(st + kWidth * kRowBytes), &map_w, kb * elems, E.d_out + o0, &ctrl->full[s]);
         tma_load_2d(smem_u32(st + P.off_b), &map_x, kb * elems, t0, &ctrl->full[s]);
         if (++s == S) s = 0, phase ^= 1;
       }
@@ -685,7 +715,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float* px[J];
     float row = 0.f, col[J];
     if constexpr (kFp8) {
-      const int32_t block = o0 / 128 + (kGated && (warp & 2) ? E.up : 0);
+      const int32_t block = o0 / 128 + (kMode == kGated && (warp & 2) ? E.up : 0);
       pw = E.sw + (int64_t)block * P.nkb;
       row = pw[kb0];
 #pragma unroll
@@ -730,7 +760,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // every MMA is done; the TMA warp has seen every load land
   have = mbar_wait(&ctrl->done, 0) && have && !*abort;
   __syncthreads();
-  ff_join<kGated, J >= 2 && !kGated ? 4 : 2>(E, sums, have, sm, C, rank, o0, t0, tokens, err_word);
+  ff_join<kMode, J >= 2 && kMode == kLinear ? 4 : 2>(E, sums, have, sm, C, rank, o0, t0, tokens, err_word);
   if (warp == 9) {
     tc_fence_after();
     tmem_dealloc(tmem, P.tmem_cols);
@@ -741,7 +771,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 namespace {
 
 FEpi epilogue_of(const FeedForwardArgs& a) {
-  FEpi e = {a.x_scale, a.w_scale, a.bias, a.residual, a.y, a.proj, a.N, a.d_out, (a.d_out + 127) / 128, a.act, a.y_bf16, false};
+  FEpi e = {a.x_scale, a.w_scale, a.bias, a.residual, a.y, a.N, a.d_out, (a.d_out + 127) / 128, a.act, a.y_bf16, false, false};
   e.tma_y = a.d_out % (a.y_bf16 ? 8 : 4) == 0 && aligned(a.y, 16) && aligned(a.residual, 16);
   return e;
 }
@@ -758,7 +788,7 @@ bool operand_map(CUtensorMap* m, const FeedForwardArgs& a, const void* base, int
                     (uint64_t)rows, (uint64_t)a.d_in, fp8 ? 128 : 64, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-cudaError_t launch_tc(const FeedForwardArgs& a, int BN, cudaStream_t stream) {
+cudaError_t launch_tc(const FeedForwardArgs& a, Mode mode, int BN, cudaStream_t stream) {
   const bool fp8 = a.dtype == MOLORA_E4M3;
   FEpi e = epilogue_of(a);
   FPlan p = {};
@@ -772,21 +802,25 @@ cudaError_t launch_tc(const FeedForwardArgs& a, int BN, cudaStream_t stream) {
   p.off_b = kRows * kRowBytes;
   p.stage_bytes = p.off_b + (uint32_t)(BN / 2) * kRowBytes;
   p.tmem_cols = tmem_columns(2 * (uint32_t)(BN <= 64 ? 64 : BN <= 128 ? 128 : 256));
-  CUtensorMap mx, mw, my = {}, mr = {}, mp = {};
+  CUtensorMap mx, mw, my = {}, mr = {};
   auto rows_map = [&](CUtensorMap* m, const void* base) {
     return linear_map(m, a.y_bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, a.y_bf16 ? 2 : 4, base,
                       (uint64_t)a.N, (uint64_t)a.d_out, a.y_bf16 ? 32 : 16, 32, CU_TENSOR_MAP_SWIZZLE_64B);
   };
-  if (e.tma_y && (!rows_map(&my, a.y) || (a.residual && !rows_map(&mr, a.residual)))) e.tma_y = false;
-  if (a.proj) {
+  if (mode == kSlopes) {
     const uint64_t half = ((uint64_t)a.d_out + 7) & ~uint64_t(7);
-    if (!linear_map_3d(&mp, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.proj, {half, 2, (uint64_t)a.N}, {2 * half, 4 * half}, {32, 1, 32},
+    if (!linear_map_3d(&my, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.y, {half, 2, (uint64_t)a.N}, {2 * half, 4 * half}, {32, 1, 32},
                        CU_TENSOR_MAP_SWIZZLE_64B))
       return cudaErrorNotSupported;
+    e.tma_res = a.d_out % 8 == 0 && aligned(a.residual, 16) && rows_map(&mr, a.residual);
+  } else {
+    if (e.tma_y && (!rows_map(&my, a.y) || (a.residual && !rows_map(&mr, a.residual)))) e.tma_y = false;
+    e.tma_res = e.tma_y && a.residual;
   }
-  // boxes: two a warp; where the residual comes through them, four of bf16, so that all of a tile's come ahead
-  p.sets = a.residual && e.tma_y && a.y_bf16 ? 4 : 2;
-  const uint32_t boxes = kEpiWarps * (uint32_t)p.sets * (a.y_bf16 ? 1 : 2) * kBox;
+  // boxes: two a warp to store from; where the residual comes through them, four of bf16, so that all of a tile's come
+  // ahead; two more for dh
+  p.sets = mode == kLinear && e.tma_res && a.y_bf16 ? 4 : 2;
+  const uint32_t boxes = kEpiWarps * (uint32_t)(p.sets + (mode == kSlopes ? 2 : 0)) * (a.y_bf16 ? 1 : 2) * kBox;
   static_assert(2 * kBox >= kTurn, "a warp's boxes hold a turned chunk");
   const size_t fixed = boxes + sizeof(FCtrl) + kSmemSlack;
   p.S = (int)((kMaxSmem - fixed) / p.stage_bytes);
@@ -797,15 +831,18 @@ cudaError_t launch_tc(const FeedForwardArgs& a, int BN, cudaStream_t stream) {
   p.smem = kMaxSmem;
   if (!operand_map(&mx, a, a.x, a.N, kRows) || !operand_map(&mw, a, a.W, rows_of_w(a), (uint32_t)(BN / 2)))
     return cudaErrorNotSupported;
-  auto kernel = !fp8 ? ff_tc_kernel<false, true, true>
-                : a.gated ? ff_tc_kernel<true, true, true>
-                          : a.y_bf16 ? ff_tc_kernel<true, false, true> : ff_tc_kernel<true, false, false>;
-  static std::atomic<uint64_t> allowed[4];
-  const cudaError_t set = allow_smem(kernel, allowed[!fp8 ? 0 : a.gated ? 1 : a.y_bf16 ? 2 : 3], kMaxSmem);
-  if (set != cudaSuccess) return set;
-  const int64_t most = num_sms() / 2;
-  const dim3 grid((unsigned)(2 * (p.tiles < most ? p.tiles : most)));
-  return launch_kernel(kernel, grid, dim3(kTcThreads), p.smem, stream, 2, e, p, a.err_word, mx, mw, my, mr, mp);
+  auto go = [&](auto kernel, std::atomic<uint64_t>& allowed) {
+    const cudaError_t set = allow_smem(kernel, allowed, kMaxSmem);
+    if (set != cudaSuccess) return set;
+    const int64_t most = num_sms() / 2;
+    const dim3 grid((unsigned)(2 * (p.tiles < most ? p.tiles : most)));
+    return launch_kernel(kernel, grid, dim3(kTcThreads), p.smem, stream, 2, e, p, a.err_word, mx, mw, my, mr);
+  };
+  static std::atomic<uint64_t> allowed[5];
+  if (mode == kSlopes) return go(ff_tc_kernel<false, kSlopes, true>, allowed[0]);
+  if (!fp8) return go(ff_tc_kernel<false, kGated, true>, allowed[1]);
+  if (a.gated) return go(ff_tc_kernel<true, kGated, true>, allowed[2]);
+  return a.y_bf16 ? go(ff_tc_kernel<true, kLinear, true>, allowed[3]) : go(ff_tc_kernel<true, kLinear, false>, allowed[4]);
 }
 
 cudaError_t launch_skinny(const FeedForwardArgs& a, const Resident& r, int BN, cudaStream_t stream) {
@@ -844,9 +881,9 @@ cudaError_t launch_skinny(const FeedForwardArgs& a, const Resident& r, int BN, c
   const bool fp8 = a.dtype == MOLORA_E4M3;
   auto pick = [&](auto j, int n) {
     constexpr int J = decltype(j)::value;
-    return !fp8 ? go(ff_skinny_kernel<false, true, J>, allowed[3 * n])
-           : a.gated ? go(ff_skinny_kernel<true, true, J>, allowed[3 * n + 1])
-                     : go(ff_skinny_kernel<true, false, J>, allowed[3 * n + 2]);
+    return !fp8 ? go(ff_skinny_kernel<false, kGated, J>, allowed[3 * n])
+           : a.gated ? go(ff_skinny_kernel<true, kGated, J>, allowed[3 * n + 1])
+                     : go(ff_skinny_kernel<true, kLinear, J>, allowed[3 * n + 2]);
   };
   switch (p.BN) {
     case 16:
@@ -876,27 +913,41 @@ int64_t tc_cycles(const FeedForwardArgs& a, const Resident& r, int BN) {
   return 8000 + waves * k_blocks(a) * (2 * BN + 90 > 420 ? 2 * BN + 90 : 420);
 }
 
+// The pairs' tile of the least cost, if that is below `cost`, else 0.
+int best_tc(const FeedForwardArgs& a, const Resident& r, int64_t cost) {
+  int best = 0;
+  for (int BN : {256, 192, 128, 64}) {
+    const int64_t c = tc_cycles(a, r, BN);
+    if (c < cost) cost = c, best = BN;
+  }
+#ifdef MOLORA_TUNING_ENV
+  if (const char* g = getenv("MOLORA_FF_BN")) best = atoi(g);
+#endif
+  return best;
+}
+
 }  // namespace
 
 cudaError_t launch_feed_forward(const FeedForwardArgs& a, cudaStream_t stream) {
   const Resident r = resident_clusters();
-  int best = 128, split = 0;
+  int split = 0;
   int64_t cost = INT64_MAX;
   for (int BN : {16, 32, 64, 128, 256}) {
     if (BN > 16 && BN / 2 >= a.N) break;
     const int64_t c = skinny_cycles(a, r, BN);
     if (c < cost) cost = c, split = BN;
   }
-  for (int BN : {256, 192, 128, 64}) {
-    if (split && a.N <= 32) continue;
-    const int64_t c = tc_cycles(a, r, BN);
-    if (c < cost) cost = c, best = BN, split = 0;
-  }
 #ifdef MOLORA_TUNING_ENV
-  if (const char* g = getenv("MOLORA_FF_BN")) best = atoi(g);
-  if (const char* g = getenv("MOLORA_FF_SKINNY")) split = atoi(g);
+  if (const char* g = getenv("MOLORA_FF_SKINNY")) split = atoi(g), cost = split ? 0 : INT64_MAX;
 #endif
-  return split ? launch_skinny(a, r, split, stream) : launch_tc(a, best, stream);
+  const int pairs = a.N <= 32 && cost < INT64_MAX ? 0 : best_tc(a, r, cost);
+  return pairs ? launch_tc(a, a.gated ? kGated : kLinear, pairs, stream) : launch_skinny(a, r, split, stream);
+}
+
+cudaError_t launch_gated_slope(const GatedGradArgs& g, cudaStream_t stream) {
+  const FeedForwardArgs a = {true, g.x, MOLORA_BF16, nullptr, g.N, g.d_in, g.W, nullptr, g.d_ff, nullptr, g.act, g.dh, g.dproj, true,
+                             g.err_word};
+  return launch_tc(a, kSlopes, best_tc(a, resident_clusters(), INT64_MAX), stream);
 }
 
 }  // namespace molora

@@ -1,8 +1,8 @@
-// gated_grad.cu -- the backward pass of the gated feed-forward block h = act(g) u, [g | u] = x [Wg; Wu]^T:
+// gated_grad.cu -- the gradients of the gated feed-forward block h = act(g) u, [g | u] = x [Wg; Wu]^T, from those of its
+// projections, dproj = [dg | du] (feed_forward.cu):
 //
-//   dg = dh u act'(g),  du = dh act(g)        gated_slope_kernel: one pass over proj = [g | u] and dh, bound by HBM
-//   dx = dg Wg + du Wu                        grad_tc_kernel: 2 d_ff terms an element
-//   dWg = dg^T x,  dWu = du^T x               grad_tc_kernel: N terms an element
+//   dx = dg Wg + du Wu            2 d_ff terms an element
+//   dWg = dg^T x,  dWu = du^T x   N terms an element
 //
 // Both products are tiles of one persistent kernel of CTA pairs (linear.cu's pipeline: a TMA warp and an MMA warp ahead of
 // the epilogue by two TMEM accumulators), so that the second's tiles fill the pairs that the first leaves idle.
@@ -292,137 +292,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ---------------------------------------------------------------------------------------------
-namespace {
-
-__device__ __forceinline__ float exp2_fast(float z) {
-  float e;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z));
-  return e;
-}
-__device__ __forceinline__ float rcp_fast(float v) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-  return r;
-}
-
-// act(v) and act'(v) together, from one power each (see activate):
-//   SiLU        p = 1 / (1 + 2^(-v log2 e)):  v p,  p + v p (1 - p)
-//   GELU        Phi(v) the normal distribution, phi(v) its density:  v Phi(v),  Phi(v) + v phi(v)
-//   GELU, tanh  p = 1 / (1 + 2^(-2 u log2 e)):  v p,  p + v p (1 - p) 2 u',  u' = sqrt(2 / pi) (1 + 0.134145 v^2)
-// 1 - p is the power times p where p is near 1, which leaves nothing to cancel.  Where 2^z overflows p is 0, and so are
-// both; v^2 is kept finite, so that nothing there is 0 times infinity.
-__device__ __forceinline__ void act_and_slope(float v, molora_activation act, float& a, float& s) {
-  switch (act) {
-    case MOLORA_ACT_RELU:
-      a = v > 0.f ? v : (v != v ? v : 0.f);
-      s = v > 0.f ? 1.f : (v != v ? v : 0.f);
-      return;
-    case MOLORA_ACT_SILU: {
-      const float e = exp2_fast(-1.4426950408889634f * v), p = rcp_fast(1.f + e);
-      a = v * p;
-      s = fmaf(a, e < 1.f ? e * p : 1.f - p, p);
-      return;
-    }
-    case MOLORA_ACT_GELU_TANH: {
-      const float e = exp2_fast(v * fmaf(-0.10294324f * v, v, -2.3022082f)), p = rcp_fast(1.f + e);
-      a = v * p;
-      s = fmaf(a, (e < 1.f ? e * p : 1.f - p) * fmaf(0.21406859f, fminf(v * v, 1e30f), 1.5957691f), p);
-      return;
-    }
-    case MOLORA_ACT_GELU: {
-      a = gelu_erf(v);
-      const float z = fminf(fabsf(v), 14.f), density = 0.3989422804f * exp2_fast(z * (-0.72134752f * z));
-      const float tail = 0.5f * erfcf(z * 0.70710678f);
-      s = fmaf(copysignf(z, v), density, v > 0.f ? 1.f - tail : tail);
-      if (v != v) s = v;
-      return;
-    }
-    default:
-      a = v;
-      s = 1.f;
-  }
-}
-
-constexpr int kSlopeThreads = 256;
-
-}  // namespace
-
-// dproj from proj and dh, 8 columns a thread and kUnits such pieces in flight.  proj and dproj [N x 2 x half], half = d_ff rounded
-// up to 8; dproj may be proj.  kVec: dh's rows start on 16-byte boundaries (d_ff = half).
-template <bool kVec, int kUnits>
-__global__ void __launch_bounds__(kSlopeThreads)
-    gated_slope_kernel(const __nv_bfloat16* proj, const __nv_bfloat16* __restrict__ dh, __nv_bfloat16* dproj, int64_t N, int32_t d_ff,
-                       molora_activation act) {
-  pdl_wait();
-  pdl_launch_dependents();
-  const int32_t pieces = (int32_t)(((int64_t)d_ff + 7) / 8);
-  const int64_t half = (int64_t)pieces * 8, all = N * pieces;
-  const int64_t first = (int64_t)blockIdx.x * (kSlopeThreads * kUnits) + threadIdx.x;
-  uint4 g[kUnits], u[kUnits], d[kUnits];
-  int64_t at[kUnits];
-#pragma unroll
-  for (int k = 0; k < kUnits; ++k) {
-    const int64_t i = first + k * kSlopeThreads;
-    if (i >= all) continue;
-    const int64_t n = all <= UINT32_MAX ? (uint32_t)i / (uint32_t)pieces : i / pieces;
-    const int32_t c = (int32_t)(i - n * pieces) * 8;
-    at[k] = n * 2 * half + c;
-    g[k] = *reinterpret_cast<const uint4*>(proj + at[k]);
-    u[k] = *reinterpret_cast<const uint4*>(proj + at[k] + half);
-    const __nv_bfloat16* p = dh + n * d_ff + c;
-    if (kVec) {
-      d[k] = *reinterpret_cast<const uint4*>(p);
-    } else {
-      uint32_t w[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) w[j] = c + j < d_ff ? (uint32_t)__bfloat16_as_ushort(p[j]) : 0u;
-      d[k] = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
-    }
-  }
-#pragma unroll
-  for (int k = 0; k < kUnits; ++k) {
-    if (first + k * kSlopeThreads >= all) continue;
-    const uint32_t gw[4] = {g[k].x, g[k].y, g[k].z, g[k].w}, uw[4] = {u[k].x, u[k].y, u[k].z, u[k].w},
-                   dw[4] = {d[k].x, d[k].y, d[k].z, d[k].w};
-    uint32_t og[4], ou[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      float r[2][2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        auto value = [&](uint32_t w) { return __uint_as_float(h ? w & 0xffff0000u : w << 16); };
-        float a, s;
-        act_and_slope(value(gw[j]), act, a, s);
-        const float v = value(dw[j]);
-        r[0][h] = v * value(uw[j]) * s;
-        r[1][h] = v * a;
-      }
-      og[j] = pack_bf16(r[0][0], r[0][1]);
-      ou[j] = pack_bf16(r[1][0], r[1][1]);
-    }
-    *reinterpret_cast<uint4*>(dproj + at[k]) = make_uint4(og[0], og[1], og[2], og[3]);
-    *reinterpret_cast<uint4*>(dproj + at[k] + half) = make_uint4(ou[0], ou[1], ou[2], ou[3]);
-  }
-}
-
-namespace {
-
-cudaError_t launch_slope(const GatedGradArgs& a, cudaStream_t stream) {
-  const auto* proj = static_cast<const __nv_bfloat16*>(a.proj);
-  const auto* dh = static_cast<const __nv_bfloat16*>(a.dh);
-  auto* dproj = static_cast<__nv_bfloat16*>(a.dproj);
-  const int64_t all = a.N * (((int64_t)a.d_ff + 7) / 8);
-  constexpr int kUnits = 2;
-  const int64_t grid = (all + kSlopeThreads * kUnits - 1) / (kSlopeThreads * kUnits);
-  if (grid > INT32_MAX) return cudaErrorNotSupported;
-  auto kernel = a.d_ff % 8 == 0 && aligned(dh, 16) ? gated_slope_kernel<true, kUnits> : gated_slope_kernel<false, kUnits>;
-  return launch_kernel(kernel, dim3((unsigned)grid), dim3(kSlopeThreads), 0, stream, 0, proj, dh, dproj, a.N, a.d_ff, a.act);
-}
-
-}  // namespace
-
 cudaError_t launch_gated_grad(const GatedGradArgs& a, cudaStream_t stream) {
-  const cudaError_t slope = launch_slope(a, stream);
+  const cudaError_t slope = launch_gated_slope(a, stream);
   if (slope != cudaSuccess || (!a.dx && !a.dW)) return slope;
   const uint64_t N = (uint64_t)a.N, F = (uint64_t)a.d_ff, D = (uint64_t)a.d_in, half = (F + 7) & ~uint64_t(7);
   GPlan p = {};

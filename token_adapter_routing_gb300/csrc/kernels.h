@@ -158,12 +158,11 @@ struct FeedForwardArgs {
   const void* residual;
   void* y;
   bool y_bf16;
-  void* proj;              // gated bf16: [N x 2 x roundup8(d_out)] or nullptr
   int32_t* err_word;
 };
 cudaError_t launch_feed_forward(const FeedForwardArgs& a, cudaStream_t stream);
 
-// The gated block's backward pass: dproj from proj and dh, then dx and dW (each may be nullptr).
+// The gated block's backward pass: dproj [N x 2 x roundup8(d_ff)] from x, W and dh, then dx and dW (each may be nullptr).
 struct GatedGradArgs {
   const void* x;
   int64_t N;
@@ -171,13 +170,13 @@ struct GatedGradArgs {
   const void* W;
   int32_t d_ff;
   molora_activation act;
-  const void* proj;
   const void* dh;
   void* dproj;
   void* dx;
   void* dW;
   int32_t* err_word;
 };
+cudaError_t launch_gated_slope(const GatedGradArgs& a, cudaStream_t stream);  // dproj alone
 cudaError_t launch_gated_grad(const GatedGradArgs& a, cudaStream_t stream);
 
 int num_sms();
