@@ -396,6 +396,11 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t sdst, const CUtensorMa
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+// The same, ordering only what this CTA sees: enough where the waiting thread overwrites what this one has read into
+// registers (TMEM), not where it reads what this one wrote.  Releasing to the whole cluster first waits for every load in flight.
+__device__ __forceinline__ void mbar_arrive_cluster_read(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
 // smem box -> global through a tensor map; rows and columns outside the tensor are skipped.
 // Completes as a bulk group of the issuing thread.
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t ssrc, int32_t c0, int32_t c1) {

@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       auto free_sums = [&]() {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(dsmem_addr(smem_u32(&ctrl->tempty[tc & 1]), 0));
+        if (lane == 0) mbar_arrive_cluster_read(dsmem_addr(smem_u32(&ctrl->tempty[tc & 1]), 0));
         ++tc;
       };
       if (E.tma_res)

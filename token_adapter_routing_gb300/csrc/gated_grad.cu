@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(dsmem_addr(smem_u32(&ctrl->tempty[tc & 1]), 0));
+      if (lane == 0) mbar_arrive_cluster_read(dsmem_addr(smem_u32(&ctrl->tempty[tc & 1]), 0));
       ++tc;
     }
     if (!ok) {
