@@ -152,6 +152,9 @@ __device__ __forceinline__ void cp_async_16_hint(uint32_t sdst, const void* gsrc
                "r"(src_bytes), "l"(policy)
                : "memory");
 }
+__device__ __forceinline__ void cp_async_4(uint32_t sdst, const void* gsrc) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(sdst), "l"(gsrc) : "memory");
+}
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // One arrival on `bar` once every cp.async this thread issued so far has landed (the
 // barrier's expected count includes this arrival).
@@ -163,6 +166,26 @@ __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wai
 template <int N>
 __device__ __forceinline__ void cp_async_wait_group() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Shared memory by its address, in the order of the waits around it.
+__device__ __forceinline__ float lds_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float2 lds_f32x2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+
+// (a, b) += (x, y) * s, two fp32 multiply-adds (each rounded as fmaf is) in one instruction.
+__device__ __forceinline__ void fma_pair(float& a, float& b, float x, float y, float s) {
+  asm("{\n\t.reg .b64 p, q, r;\n\tmov.b64 p, {%2, %3};\n\tmov.b64 q, {%4, %4};\n\tmov.b64 r, {%0, %1};\n\t"
+      "fma.rn.f32x2 r, p, q, r;\n\tmov.b64 {%0, %1}, r;\n\t}"
+      : "+f"(a), "+f"(b)
+      : "f"(x), "f"(y), "f"(s));
 }
 
 // ------------------------------------------------------------------ proxies / bulk async
@@ -396,10 +419,10 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t sdst, const CUtensorMa
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// The same, ordering only what this CTA sees: enough where the waiting thread overwrites what this one has read into
-// registers (TMEM), not where it reads what this one wrote.  Releasing to the whole cluster first waits for every load in flight.
+// The same without ordering memory: enough where the waiting thread's MMAs overwrite what this one has read from TMEM
+// into registers (tcgen05.wait::ld), and nothing that it wrote.  A release waits for every load in flight.
 __device__ __forceinline__ void mbar_arrive_cluster_read(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 // smem box -> global through a tensor map; rows and columns outside the tensor are skipped.
 // Completes as a bulk group of the issuing thread.

@@ -12,7 +12,7 @@
 // ff_tc_kernel (many tokens): linear_tc_kernel's pipeline (linear.cu): persistent pairs of CTAs with tiles of 256 tokens x
 //   BN rows of W, a TMA warp and an MMA warp ahead of 8 epilogue warps by two TMEM accumulators.  Scales change with
 //   every K block of 128, so with e4m3 an accumulator holds one K block, and the epilogue warps
-//   add it, scaled, to fp32 registers (128 a thread) while the next one's MMAs run.
+//   add it, scaled, to fp32 registers (64 a thread) while the next one's MMAs run.
 // ff_skinny_kernel (few tokens): W's rows are the MMA's M, the tokens its N, d_in split over a cluster; bound by reading W.
 #include <cudaTypedefs.h>
 
@@ -31,11 +31,23 @@ namespace {
 
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 32 * (kEpiWarps + 2);  // + TMA warp (8) + MMA warp (9)
-// ff_tc_kernel: 8 epilogue warps, the TMA warp (8), the MMA warp (9) and two that only make up the warpgroup.  With e4m3 the
-// epilogue's 128 sums a thread take more than the 168 registers that 384 threads are launched with, so the
-// last warpgroup gives up its own: 256 x 224 + 128 x 56 = 384 x 168.
-constexpr int kTcThreads = 384, kEpiRegisters = 224, kOtherRegisters = 56;
-constexpr int kMaxSets = 4;  // staging boxes an epilogue warp has at most
+// ff_tc_kernel: groups of 4 epilogue warps that share a tile's chunks, then the TMA warp, the MMA warp and two that only make up
+// the warpgroup.  With e4m3 a K block's sums have 512 cycles, the next one's MMAs, to leave TMEM: four warps on each
+// scheduler hide one another's waits (8192 x 4096 -> 4096 with two 218 us, with four TODO).  Their 64 sums a thread
+// and what they work with take more than the 96 registers that 640 threads are launched with, so the last warpgroup
+// gives up its own: 512 x 104 + 128 x 64 = 640 x 96.
+constexpr int tc_sides(bool fp8) { return fp8 ? 4 : 2; }
+constexpr int tc_threads(bool fp8) { return 32 * (4 * tc_sides(fp8) + 4); }
+constexpr int kEpiRegisters = 104, kOtherRegisters = 64;
+constexpr int kMaxSets = 2;  // staging boxes that an epilogue warp reads into at most
+// The scales of kScaleSpan K blocks of a tile, which two warps gather ahead of the epilogue, K block by K block: of the CTA's
+// 128 tokens (x's scales lie token by token, so gathered by the epilogue's warps each K block's take 32 lines of L1 a warp,
+// 512 cycles an SM), and of the 8 pieces of 32 columns of the accumulator, c and c + 4 together.
+constexpr int kScaleSpan = 16, kScaleStride = kRows + 1;
+struct __align__(8) Scales {
+  float x[kScaleSpan * kScaleStride];
+  float w[kScaleSpan * 8];
+};
 enum Mode { kLinear, kGated, kSlopes };
 constexpr int kSpan = 8;     // bf16, few tokens: K blocks summed in TMEM before fp32 registers take over
 
@@ -44,8 +56,10 @@ struct __align__(8) FCtrl {
   uint64_t empty[kMaxStages];
   uint64_t tfull[2];
   uint64_t tempty[2];
+  uint64_t sfull[2];
+  uint64_t sempty[2];
   uint64_t done;
-  uint64_t res_full[kEpiWarps * kMaxSets];
+  uint64_t res_full[16 * kMaxSets];
   uint32_t tmem_base;
   int32_t abort;
 };
@@ -72,54 +86,58 @@ struct FPlan {
   int sets;              // staging boxes a warp
   int nkb;               // K blocks of 128 bytes
   int group;             // token tiles per group of tiles (they share W's rows in L2)
-  int64_t m_tiles, tiles;
-  int32_t n_tiles;
-  uint32_t stage_bytes, off_b, off_stage, off_ctrl, tmem_cols, smem;
+  // (32 bits: 2^27 tiles would be an output of 10^13 bytes)
+  int32_t m_tiles, n_tiles, tiles;
+  uint32_t stage_bytes, off_b, off_stage, off_scales, off_ctrl, tmem_cols, smem;
 };
 
 }  // namespace
 
 template <bool kFp8, Mode kMode, bool kY16>
-__global__ void __launch_bounds__(kTcThreads, 1)
+__global__ void __launch_bounds__(tc_threads(kFp8), 1)
     ff_tc_kernel(const FEpi E, const FPlan P, int32_t* err_word, const __grid_constant__ CUtensorMap map_x,
                  const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_y,
                  const __grid_constant__ CUtensorMap map_r) {
   constexpr bool kPaired = kMode != kLinear;  // gate and up projection side by side
   constexpr int kParts = kY16 ? 1 : 2;  // boxes of a chunk of 32 columns of y
   constexpr uint32_t kSet = kParts * kBox;
+  constexpr int kSides = tc_sides(kFp8), kWarps = 4 * kSides;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   FCtrl* ctrl = reinterpret_cast<FCtrl*>(sm + P.off_ctrl);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // (the warp's number, and the like, from lane 0: in uniform registers)
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int BN = P.BN, S = P.S, nkb = P.nkb, width = kPaired ? BN / 2 : BN;  // outputs a tile
   const uint32_t rank = cluster_ctarank();
   const uint16_t both = 0x3;
-  const int64_t pair = blockIdx.x / 2, pairs = gridDim.x / 2;
+  const int32_t pair = blockIdx.x / 2, pairs = gridDim.x / 2;
   volatile int32_t* abort = &ctrl->abort;
   // tiles in groups of P.group token tiles: within a group, the token tile runs fastest
-  auto tile_at = [&](int64_t pt, int32_t& m0, int32_t& n0) {
-    const int64_t span = (int64_t)P.group * P.n_tiles, grp = pt / span;
-    const int64_t first = grp * P.group, left = P.m_tiles - first, rows = left < P.group ? left : P.group;
-    const int64_t in = pt - grp * span;
-    m0 = (int32_t)((first + in % rows) * 2 * kRows + rank * kRows);
-    n0 = (int32_t)(in / rows) * width;
+  auto tile_at = [&](int32_t pt, int32_t& m0, int32_t& n0) {
+    const int32_t span = P.group * P.n_tiles, grp = pt / span;
+    const int32_t first = grp * P.group, left = P.m_tiles - first, rows = left < P.group ? left : P.group;
+    const int32_t in = pt - grp * span;
+    m0 = (first + in % rows) * 2 * kRows + (int32_t)rank * kRows;
+    n0 = in / rows * width;
   };
 
-  if (warp == kEpiWarps + 1) {
+  if (warp == kWarps + 1) {
     tmem_alloc_pair(&ctrl->tmem_base, P.tmem_cols);
     tmem_relinquish_pair();
   }
-  if (warp == kEpiWarps && lane == 0) {
+  if (warp == kWarps && lane == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(&ctrl->full[s], 1);
       mbar_init(&ctrl->empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&ctrl->tfull[b], 1);
-      mbar_init(&ctrl->tempty[b], 2 * kEpiWarps);
+      mbar_init(&ctrl->tempty[b], 2 * kWarps);
+      mbar_init(&ctrl->sfull[b], 64);
+      mbar_init(&ctrl->sempty[b], kWarps);
     }
     mbar_init(&ctrl->done, 1);
-    for (int b = 0; b < kEpiWarps * kMaxSets; ++b) mbar_init(&ctrl->res_full[b], 1);
+    for (int b = 0; b < kWarps * kMaxSets; ++b) mbar_init(&ctrl->res_full[b], 1);
     ctrl->abort = 0;
     mbar_fence_init();
     tma_prefetch_desc(&map_x);
@@ -132,17 +150,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   // only now, with this CTA's TMEM held, may the next kernel's CTAs come and ask for theirs
   pdl_launch_dependents();
   tc_fence_after();
-  const uint32_t tmem = ctrl->tmem_base;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, ctrl->tmem_base, 0);
   cluster_sync();  // every CTA's barriers are initialised before another signals them
 
-  if (warp >= kEpiWarps) {
+  if (warp >= kWarps) {
     if constexpr (kFp8) registers_down<kOtherRegisters>();
-    if (warp == kEpiWarps && elect_one()) {
+    if (warp == kWarps && elect_one()) {
       const int elems = kFp8 ? 128 : 64;  // K elements per stage
       int s = 0, issued = 0;
       uint32_t phase = 1;  // the first use of a stage finds it empty
       bool ok = true;
-      for (int64_t pt = pair; pt < P.tiles && ok; pt += pairs) {
+      for (int32_t pt = pair; pt < P.tiles && ok; pt += pairs) {
         int32_t m0, n0;
         tile_at(pt, m0, n0);
         // the pair's halves of the MMA's columns: gated, one CTA brings rows of Wg and the other of Wu
@@ -172,7 +190,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
       }
     }
-    if (warp == kEpiWarps + 1 && rank == 0 && elect_one()) {
+    if (warp == kWarps + 1 && rank == 0 && elect_one()) {
       const uint32_t idesc = kFp8 ? idesc_e4m3_f32(2 * kRows, (uint32_t)BN) : idesc_bf16_f32(2 * kRows, (uint32_t)BN, false, false);
       const uint64_t da = smem_desc(smem_u32(sm), 16, 1024, kSwizzle128B);
       const uint64_t db = smem_desc(smem_u32(sm + P.off_b), 16, 1024, kSwizzle128B);
@@ -181,7 +199,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       int s = 0, tc = 0;
       uint32_t phase = 0;
       bool ok = true;
-      for (int64_t pt = pair; pt < P.tiles && ok; pt += pairs) {
+      for (int32_t pt = pair; pt < P.tiles && ok; pt += pairs) {
         for (int first = 0; first < nkb && ok; first += span, ++tc) {
           const int buf = tc & 1;
           if (tc >= 2 && !mbar_wait_spin(&ctrl->tempty[buf], (uint32_t)((tc >> 1) - 1) & 1u, abort)) {
@@ -198,19 +216,49 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             tc_fence_after();
             const uint32_t at = (uint32_t)s * (P.stage_bytes >> 4);
             umma_stage<true, kFp8>(d, a_lo + at, b_lo + at, desc_hi, desc_hi, idesc, kb != first);
-            umma_commit_pair(&ctrl->empty[s], both);
+            umma_commit_pair(&ctrl->empty[s], both);  // e4m3: for the epilogue too
             if (++s == S) s = 0, phase ^= 1;
           }
-          if (ok) umma_commit_pair(&ctrl->tfull[buf], both);
+          if (!kFp8 && ok) umma_commit_pair(&ctrl->tfull[buf], both);
         }
       }
       if (!ok) report(err_word, MOLORA_DEV_WAIT_TIMEOUT);
       umma_commit_pair(&ctrl->done, both);  // arrives in both CTAs once every MMA has completed
     }
+    if constexpr (kFp8) {
+      if (warp >= kWarps + 2) {  // the scales' two warps: 16 lanes a token, a K block each
+        const int l = (warp - kWarps - 2) * 32 + lane, k = l & 15;
+        int n = 0;
+        bool ok = true;
+        for (int32_t pt = pair; pt < P.tiles && ok; pt += pairs) {
+          int32_t m0, n0;
+          tile_at(pt, m0, n0);
+          for (int kb = 0; kb < nkb; kb += kScaleSpan, ++n) {
+            if (n >= 2 && !mbar_wait_spin(&ctrl->sempty[n & 1], (uint32_t)((n >> 1) - 1) & 1u, abort)) {
+              ok = false;
+              break;
+            }
+            Scales* to = reinterpret_cast<Scales*>(sm + P.off_scales) + (n & 1);
+            if (kb + k < nkb) {
+              for (int r = l >> 4; r < kRows && m0 + r < E.N; r += 4)
+                cp_async_4(smem_u32(to->x + k * kScaleStride + r), E.sx + (int64_t)(m0 + r) * nkb + kb + k);
+              for (int c = l >> 4; c < 8; c += 4) {
+                const int32_t col = n0 + (kPaired ? c & 3 : c) * 32;
+                if (col < E.d_out)
+                  cp_async_4(smem_u32(to->w + k * 8 + (c & 3) * 2 + (c >> 2)),
+                             E.sw + (int64_t)(col / 128 + (kPaired && c >= 4 ? E.up : 0)) * nkb + kb + k);
+              }
+            }
+            cp_async_mbar_arrive(&ctrl->sfull[n & 1]);
+          }
+        }
+        cp_async_wait_all();
+      }
+    }
     __syncwarp();
   } else {
     if constexpr (kFp8) registers_up<kEpiRegisters>();
-    // epilogue: warps w and w + 4 share 32 rows and take chunks of 32 outputs in turn
+    // epilogue: warps w, w + 4, ... share 32 rows and take chunks of 32 outputs in turn
     const int quarter = warp & 3, side = warp >> 2;
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
     // Outputs leave through a ring of P.sets staging boxes, into which the residual's chunks come before.
@@ -219,7 +267,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     uint8_t* in_ring = sm + P.off_stage + (size_t)warp * (P.sets + kOwn) * kSet;
     uint8_t* ring = in_ring + kOwn * kSet;
     const int in_sets = kOwn ? kOwn : P.sets;
-    int tc = 0, used = 0, asked = 0, taken = 0;  // boxes written; residual chunks on their way or taken, and taken
+    int tc = 0, spans = 0;                  // accumulators, and spans of scales, done with
+    int used = 0, asked = 0, taken = 0;  // boxes written; residual chunks on their way or taken, and taken
     auto box_of = [&](int n) { return ring + (size_t)(n & (P.sets - 1)) * kSet; };
     auto in_box = [&](int n) { return in_ring + (size_t)(n & (in_sets - 1)) * kSet; };
     auto ask = [&](int32_t col, int32_t m0) {
@@ -261,15 +310,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       ++used;
       return box;
     };
+    const uint32_t tempty = dsmem_addr(smem_u32(&ctrl->tempty[0]), 0);
+    int s = 0;  // e4m3: the stage of the next K block
+    uint32_t phase = 0;
     bool ok = true;
-    for (int64_t pt = pair; pt < P.tiles && ok; pt += pairs) {
+    for (int32_t pt = pair; pt < P.tiles && ok; pt += pairs) {
       int32_t m0, n0;
       tile_at(pt, m0, n0);
       m0 += quarter * 32;
-      const int64_t t = (int64_t)m0 + lane;
       const int chunks = m0 < E.N ? min(width / 32, (E.d_out - n0 + 31) / 32) : 0;
-      const int mine = side < chunks ? (chunks - side + 1) / 2 : 0;  // chunks side, side + 2, ...
-      auto column = [&](int q) { return n0 + (side + 2 * q) * 32; };
+      const int mine = side < chunks ? (chunks - side + kSides - 1) / kSides : 0;  // chunks side, side + kSides, ...
+      auto column = [&](int q) { return n0 + (side + kSides * q) * 32; };
       // y's chunk from its finished values
       auto put = [&](float (&v)[32], int32_t col) {
         if (E.tma_y) {
@@ -338,79 +389,83 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
       };
       auto wait_sums = [&]() {  // the next accumulator
-        ok = __all_sync(0xffffffffu, mbar_wait_spin(&ctrl->tfull[tc & 1], (uint32_t)(tc >> 1) & 1u, abort));
+        if constexpr (kFp8) {
+          ok = __all_sync(0xffffffffu, mbar_wait_spin(&ctrl->empty[s], phase, abort));
+          if (++s == S) s = 0, phase ^= 1;
+        } else {
+          ok = __all_sync(0xffffffffu, mbar_wait_spin(&ctrl->tfull[tc & 1], (uint32_t)(tc >> 1) & 1u, abort));
+        }
         tc_fence_after();
-        return tmem + lanes + (uint32_t)((tc & 1) * (P.tmem_cols / 2));
+        return tmem + (uint32_t)((tc & 1) * (P.tmem_cols / 2));
       };
       auto free_sums = [&]() {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster_read(dsmem_addr(smem_u32(&ctrl->tempty[tc & 1]), 0));
+        if (lane == 0) mbar_arrive_cluster_read(tempty + (tc & 1) * 8);
         ++tc;
       };
       if (E.tma_res)
         for (int q = 0; q < mine && q < in_sets; ++q) ask(column(q), m0);
       if constexpr (kFp8) {
-        // 4 pieces of 32 columns of TMEM: linear, this warp's chunks; gated, gate and up of its two chunks in turn
-        float acc[4][32];
+        // two pieces of 32 columns of TMEM, side and side + 4 of 8: linear, this warp's chunks; gated, gate and up
+        // projection of its chunk
+        float acc[2][32];
         const int pieces = kPaired ? 2 * mine : mine;
-        float cb[4], next[4], row;
-        const float* ps[4];
-        const float* px = E.sx + (t < E.N ? t * nkb : 0);
-        row = px[0];
+        const uint32_t at[2] = {lanes + (uint32_t)(side * 32), lanes + (uint32_t)((kPaired ? width : 128) + side * 32)};
+        float cb[2];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int32_t col = column(kPaired ? q >> 1 : q);
-          ps[q] = E.sw + (q < pieces ? (int64_t)(col / 128 + (kPaired && (q & 1) ? E.up : 0)) * nkb : 0);
-          next[q] = ps[q][0];
+        for (int q = 0; q < 2; ++q) {
+          const int32_t col = column(kPaired ? 0 : q);
           cb[q] = !kPaired && E.bias && q < pieces && col + lane < E.d_out ? E.bias[col + lane] : 0.f;
 #pragma unroll
           for (int i = 0; i < 32; ++i) acc[q][i] = 0.f;
         }
-        for (int kb = 0; kb < nkb; ++kb) {
-          float sc[4];
+        // K blocks of a span of scales, whose sums are added with as few instructions as they come down to: 64 fmas a warp
+        // and K block, four warps a scheduler, in the 512 cycles of the next K block's MMAs
+        auto add_span = [&](auto count, int blocks, uint32_t sx, uint32_t sw) {
+          constexpr int kPieces = decltype(count)::value;
+          for (; blocks > 0; --blocks, sx += kScaleStride * 4, sw += 32) {
+            const float row = lds_f32(sx);
+            const float2 w = lds_f32x2(sw);
+            const float sc[2] = {row * w.x, row * w.y};
+            const uint32_t base = wait_sums();
+            if (!ok) return;
 #pragma unroll
-          for (int q = 0; q < 4; ++q) sc[q] = row * next[q];
-          if (kb + 1 < nkb) {  // on their way while this block's sums are awaited
-            row = px[kb + 1];
+            for (int h = 0; h < 2 * kPieces; ++h) {
+              float r[16];
+              tmem_ld16(base + at[h >> 1] + (h & 1) * 16, r);
+              if (h == 2 * kPieces - 1) free_sums();
 #pragma unroll
-            for (int q = 0; q < 4; ++q) next[q] = ps[q][kb + 1];
-          }
-          const uint32_t base = wait_sums();
-          if (!ok) break;
-          auto at = [&](int h) {  // the h-th 16 columns
-            const int q = h >> 1;
-            const int c = kPaired ? (q & 1) * width + (side + 2 * (q >> 1)) * 32 : (side + 2 * q) * 32;
-            return base + (uint32_t)(c + (h & 1) * 16);
-          };
-          uint32_t r[2][16];
-          if (pieces > 0)
-            tmem_ld16_start(at(0), r[0]);
-          else
-            free_sums();
-#pragma unroll
-          for (int h = 0; h < 8; ++h) {
-            if (h >= 2 * pieces) continue;
-            tmem_ld_wait(r[h & 1]);
-            if (h + 1 < 2 * pieces) {
-              if (h + 1 < 8) tmem_ld16_start(at(h + 1), r[(h + 1) & 1]);
-            } else {
-              free_sums();
+              for (int i = 0; i < 16; i += 2)
+                fma_pair(acc[h >> 1][(h & 1) * 16 + i], acc[h >> 1][(h & 1) * 16 + i + 1], r[i], r[i + 1], sc[h >> 1]);
             }
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              acc[h >> 1][(h & 1) * 16 + i] = fmaf(__uint_as_float(r[h & 1][i]), sc[h >> 1], acc[h >> 1][(h & 1) * 16 + i]);
+            if (kPieces == 0) free_sums();
           }
+        };
+        for (int kb = 0; kb < nkb && ok; kb += kScaleSpan, ++spans) {
+          ok = __all_sync(0xffffffffu, mbar_wait_spin(&ctrl->sfull[spans & 1], (uint32_t)(spans >> 1) & 1u, abort));
+          if (!ok) break;
+          const uint32_t scales = smem_u32(sm + P.off_scales) + (spans & 1) * (uint32_t)sizeof(Scales);
+          const uint32_t sx = scales + (quarter * 32 + lane) * 4, sw = scales + kScaleSpan * kScaleStride * 4 + side * 8;
+          const int blocks = min(nkb - kb, kScaleSpan);
+          if (pieces == 2)
+            add_span(std::integral_constant<int, 2>{}, blocks, sx, sw);
+          else if (pieces == 1)
+            add_span(std::integral_constant<int, 1>{}, blocks, sx, sw);
+          else
+            add_span(std::integral_constant<int, 0>{}, blocks, sx, sw);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ctrl->sempty[spans & 1]);
         }
         if (!ok) break;
 #pragma unroll
-        for (int q = 0; q < (kPaired ? 2 : 4); ++q) {
+        for (int q = 0; q < (kPaired ? 1 : 2); ++q) {
           if (q >= mine || !ok) continue;
           if constexpr (kPaired) {
-            apply_act(acc[2 * q], E.act);
+            apply_act(acc[0], E.act);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) acc[2 * q][i] *= acc[2 * q + 1][i];
-            put(acc[2 * q], column(q));
+            for (int i = 0; i < 32; ++i) acc[0][i] *= acc[1][i];
+            put(acc[0], column(0));
           } else {
             if (E.bias) {
 #pragma unroll
@@ -422,12 +477,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
         }
       } else {
-        const uint32_t base = wait_sums();
+        const uint32_t base = wait_sums() + lanes;
         if (!ok) break;
         for (int q = 0; q < mine; ++q) {
           uint32_t rg[32], ru[32];
-          tmem_ld32_start(base + (uint32_t)((side + 2 * q) * 32), rg);
-          tmem_ld32_start(base + (uint32_t)(width + (side + 2 * q) * 32), ru);
+          tmem_ld32_start(base + (uint32_t)((side + kSides * q) * 32), rg);
+          tmem_ld32_start(base + (uint32_t)(width + (side + kSides * q) * 32), ru);
           tmem_ld_wait(rg);
           tmem_ld_bind(ru);
           if (q + 1 == mine) free_sums();
@@ -493,10 +548,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (lane == 0) bulk_wait_all();
     __syncwarp();
   }
-  if (warp == kEpiWarps + 1 && lane == 0) mbar_wait(&ctrl->done, 0);
+  if (warp == kWarps + 1 && lane == 0) mbar_wait(&ctrl->done, 0);
   __syncthreads();
   cluster_sync();  // neither CTA leaves, nor frees its TMEM, while the other may still signal or use it
-  if (warp == kEpiWarps + 1) {
+  if (warp == kWarps + 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, P.tmem_cols);
   }
@@ -795,8 +850,10 @@ cudaError_t launch_tc(const FeedForwardArgs& a, Mode mode, int BN, cudaStream_t 
   const int width = a.gated ? BN / 2 : BN;
   p.BN = BN;
   p.nkb = k_blocks(a);
-  p.m_tiles = (a.N + 2 * kRows - 1) / (2 * kRows);
-  p.n_tiles = (int32_t)(((int64_t)a.d_out + width - 1) / width);
+  const int64_t m_tiles = (a.N + 2 * kRows - 1) / (2 * kRows), n_tiles = ((int64_t)a.d_out + width - 1) / width;
+  if (m_tiles * n_tiles > INT32_MAX / 16) return cudaErrorNotSupported;
+  p.m_tiles = (int32_t)m_tiles;
+  p.n_tiles = (int32_t)n_tiles;
   p.tiles = p.m_tiles * p.n_tiles;
   p.group = 8;
   p.off_b = kRows * kRowBytes;
@@ -817,16 +874,19 @@ cudaError_t launch_tc(const FeedForwardArgs& a, Mode mode, int BN, cudaStream_t 
     if (e.tma_y && (!rows_map(&my, a.y) || (a.residual && !rows_map(&mr, a.residual)))) e.tma_y = false;
     e.tma_res = e.tma_y && a.residual;
   }
-  // boxes: two a warp to store from; where the residual comes through them, four of bf16, so that all of a tile's come
-  // ahead; two more for dh
-  p.sets = mode == kLinear && e.tma_res && a.y_bf16 ? 4 : 2;
-  const uint32_t boxes = kEpiWarps * (uint32_t)(p.sets + (mode == kSlopes ? 2 : 0)) * (a.y_bf16 ? 1 : 2) * kBox;
-  static_assert(2 * kBox >= kTurn, "a warp's boxes hold a turned chunk");
-  const size_t fixed = boxes + sizeof(FCtrl) + kSmemSlack;
+  // boxes that a warp stores from, through which the residual comes too: both chunks of a tile where they are of bf16, so that no
+  // store is waited for (all tiles of a wave end together: with one box, 4800 cycles a tile of 28700); one where they
+  // are of fp32, of which two would leave two stages.  Two more for dh.
+  const int warps = 4 * tc_sides(fp8);
+  p.sets = a.y_bf16 ? 2 : 1;
+  const uint32_t boxes = (uint32_t)(warps * (p.sets + (mode == kSlopes ? 2 : 0)) * (a.y_bf16 ? 1 : 2)) * kBox;
+  static_assert(2 * kBox >= kTurn, "two boxes of bf16, or one of fp32, hold a turned chunk");
+  const size_t scales = fp8 ? 2 * sizeof(Scales) : 0, fixed = boxes + scales + sizeof(FCtrl) + kSmemSlack;
   p.S = (int)((kMaxSmem - fixed) / p.stage_bytes);
   if (p.S > kMaxStages) p.S = kMaxStages;
   p.off_stage = (uint32_t)p.S * p.stage_bytes;
-  p.off_ctrl = p.off_stage + boxes;
+  p.off_scales = p.off_stage + boxes;
+  p.off_ctrl = p.off_scales + (uint32_t)scales;
   // one CTA an SM, alone: an allocation of TMEM never waits for another CTA's (see linear.cu)
   p.smem = kMaxSmem;
   if (!operand_map(&mx, a, a.x, a.N, kRows) || !operand_map(&mw, a, a.W, rows_of_w(a), (uint32_t)(BN / 2)))
@@ -834,9 +894,9 @@ cudaError_t launch_tc(const FeedForwardArgs& a, Mode mode, int BN, cudaStream_t 
   auto go = [&](auto kernel, std::atomic<uint64_t>& allowed) {
     const cudaError_t set = allow_smem(kernel, allowed, kMaxSmem);
     if (set != cudaSuccess) return set;
-    const int64_t most = num_sms() / 2;
+    const int32_t most = num_sms() / 2;
     const dim3 grid((unsigned)(2 * (p.tiles < most ? p.tiles : most)));
-    return launch_kernel(kernel, grid, dim3(kTcThreads), p.smem, stream, 2, e, p, a.err_word, mx, mw, my, mr);
+    return launch_kernel(kernel, grid, dim3(tc_threads(fp8)), p.smem, stream, 2, e, p, a.err_word, mx, mw, my, mr);
   };
   static std::atomic<uint64_t> allowed[5];
   if (mode == kSlopes) return go(ff_tc_kernel<false, kSlopes, true>, allowed[0]);
