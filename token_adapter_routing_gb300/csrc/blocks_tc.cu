@@ -1,0 +1,500 @@
+// blocks_tc.cu -- many tokens times weights in e4m3, with scales for each block of 128: molora_linear_blocks, and
+// molora_gated_linear's e4m3 form (see feed_forward.cu).
+//
+// Scales change with every K block of 128, so an accumulator in TMEM holds one K block and the epilogue warps add it,
+// scaled, to sums in fp32 registers while the next one's MMAs run.  That takes one fma an element and K block beside the
+// tensor cores' 128 multiply-adds: 256 cycles of a scheduler's pipe, in pairs half as many instructions, against the
+// 512 cycles of the MMAs, and everything else in the loop competes with it.  What it came down to, by what it cost
+// (8192 x 4096 -> 4096 in us, one after the other):
+//   * giving an accumulator back without a release: 331 -> 218 (a cluster-wide one waits for every load in flight)
+//   * four epilogue warps a scheduler instead of two, x's scales gathered ahead into shared memory by two warps of their
+//     own (they lie token by token: 32 lines of L1 a warp and K block), registers enough for the MMA warp: 218 -> 129
+//   * the loop's few instructions (addresses that flip by xor, one vote a wait, fmas in pairs): 129 -> 123
+//   * accumulators made, read and given back in halves of 128 columns, so that the next K block's first half is on
+//     the tensor cores while this one's second half is read, and a tile's outputs leaving together: TODO
+#include <cudaTypedefs.h>
+
+#include <atomic>
+
+#include "feed_forward.cuh"
+
+namespace molora {
+
+namespace {
+
+constexpr int kSides = 2, kWarps = 4 * kSides;   // epilogue warps: groups of four share 32 rows each
+constexpr int kThreadsB = 32 * (kWarps + 4);     // + TMA warp, MMA warp, two that gather scales
+// 128 sums a thread, 64 more on their way from TMEM and what the epilogue works with take more than the 168 registers that
+// 384 threads are launched with, so the last warpgroup gives up its own: 256 x 232 + 128 x 40 = 384 x 168.
+constexpr int kEpiRegisters = 232, kOtherRegisters = 40;
+
+// The scales of kScaleSpan K blocks of a tile: for each K block the 4 pieces' of each side, and the CTA's 128 tokens'.
+constexpr int kScaleSpan = 16, kScaleStride = kRows + 1;
+struct __align__(16) Scales {
+  float w[kScaleSpan][8];
+  float x[kScaleSpan * kScaleStride];
+};
+
+struct __align__(16) BCtrl {
+  uint64_t tfull[2];   // (one's address and the other's differ in one bit)
+  uint64_t tempty[2];
+  uint64_t full[kMaxStages];
+  uint64_t empty[kMaxStages];
+  uint64_t sfull[2];
+  uint64_t sempty[2];
+  uint64_t done;
+  uint64_t res_full[kWarps];
+  uint32_t tmem_base;
+  int32_t abort;
+};
+
+struct BPlan {
+  int BN;                // rows of W a tile
+  int S;                 // stages
+  int nkb;               // K blocks of 128
+  int group;             // token tiles per group of tiles (they share W's rows in L2)
+  // (32 bits: 2^27 tiles would be an output of 10^13 bytes)
+  int32_t m_tiles, n_tiles, tiles;
+  uint32_t box;          // bytes of staging a warp
+  uint32_t stage_bytes, off_b, off_stage, off_scales, off_ctrl, tmem_cols, smem;
+};
+
+// The h-th piece of 32 columns of a side's warps: its columns of TMEM, and of the outputs (from the tile's first).  Gated,
+// pieces come in pairs, of the gate's rows of W and the up projection's.
+template <bool kGated>
+__device__ __forceinline__ int piece_column(const BPlan& P, int side, int h) {
+  return kGated ? (h & 1) * (P.BN / 2) + (side + kSides * (h >> 1)) * 32 : (side + kSides * h) * 32;
+}
+template <bool kGated>
+__device__ __forceinline__ int piece_output(int side, int h) {
+  return (side + kSides * (kGated ? h >> 1 : h)) * 32;
+}
+// How many pieces a side has.
+template <bool kGated>
+__device__ __forceinline__ int pieces_of(const BPlan& P, int side) {
+  const int chunks = P.BN / (kGated ? 64 : 32);
+  return (chunks - side + kSides - 1) / kSides * (kGated ? 2 : 1);
+}
+
+}  // namespace
+
+template <bool kGated, bool kY16>
+__global__ void __launch_bounds__(kThreadsB, 1)
+    blocks_tc_kernel(const FEpi E, const BPlan P, int32_t* err_word, const __grid_constant__ CUtensorMap map_x,
+                     const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_y,
+                     const __grid_constant__ CUtensorMap map_r) {
+  constexpr int kOut = kGated ? 2 : 4;               // output pieces of 32 columns a warp
+  constexpr int kParts = kY16 ? 1 : 2;               // one's boxes: 32 rows of 64 bytes
+  constexpr uint32_t kPiece = kParts * kBox;
+  constexpr int kRound = kY16 ? kOut : 2;            // pieces that leave together
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  BCtrl* ctrl = reinterpret_cast<BCtrl*>(sm + P.off_ctrl);
+  // (the warp's number, and the like, from lane 0: in uniform registers)
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  const int BN = P.BN, S = P.S, nkb = P.nkb, width = kGated ? BN / 2 : BN;  // outputs a tile
+  const uint32_t rank = cluster_ctarank();
+  const uint16_t both = 0x3;
+  const int32_t pair = blockIdx.x / 2, pairs = gridDim.x / 2;
+  volatile int32_t* abort = &ctrl->abort;
+  // tiles in groups of P.group token tiles: within a group, the token tile runs fastest
+  auto tile_at = [&](int32_t pt, int32_t& m0, int32_t& n0) {
+    const int32_t span = P.group * P.n_tiles, grp = pt / span;
+    const int32_t first = grp * P.group, left = P.m_tiles - first, rows = left < P.group ? left : P.group;
+    const int32_t in = pt - grp * span;
+    m0 = (first + in % rows) * 2 * kRows + (int32_t)rank * kRows;
+    n0 = in / rows * width;
+  };
+
+  if (warp == kWarps + 1) {
+    tmem_alloc_pair(&ctrl->tmem_base, P.tmem_cols);
+    tmem_relinquish_pair();
+  }
+  if (warp == kWarps && lane == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&ctrl->full[s], 1);
+      mbar_init(&ctrl->empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&ctrl->tfull[b], 1);
+      mbar_init(&ctrl->tempty[b], 2 * kWarps);
+      mbar_init(&ctrl->sfull[b], 64);
+      mbar_init(&ctrl->sempty[b], kWarps);
+    }
+    mbar_init(&ctrl->done, 1);
+    for (int b = 0; b < kWarps; ++b) mbar_init(&ctrl->res_full[b], 1);
+    ctrl->abort = 0;
+    mbar_fence_init();
+    tma_prefetch_desc(&map_x);
+    tma_prefetch_desc(&map_w);
+    if (E.tma_y) tma_prefetch_desc(&map_y);
+    if (E.tma_res) tma_prefetch_desc(&map_r);
+  }
+  pdl_wait();
+  __syncthreads();
+  // only now, with this CTA's TMEM held, may the next kernel's CTAs come and ask for theirs
+  pdl_launch_dependents();
+  tc_fence_after();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, ctrl->tmem_base, 0);
+  cluster_sync();  // every CTA's barriers are initialised before another signals them
+
+  if (warp >= kWarps) {
+    registers_down<kOtherRegisters>();
+    if (warp == kWarps && elect_one()) {
+      int s = 0, issued = 0;
+      uint32_t phase = 1;  // the first use of a stage finds it empty
+      bool ok = true;
+      for (int32_t pt = pair; pt < P.tiles && ok; pt += pairs) {
+        int32_t m0, n0;
+        tile_at(pt, m0, n0);
+        // the pair's halves of the MMA's columns: gated, one CTA brings rows of Wg and the other of Wu
+        const int32_t n = kGated ? n0 + (int32_t)rank * E.d_out : n0 + (int32_t)rank * (BN / 2);
+        for (int kb = 0; kb < nkb; ++kb) {
+          if (issued >= S && !mbar_wait_spin(&ctrl->empty[s], phase, abort)) {
+            ok = false;
+            break;
+          }
+          // the leader's barrier counts both CTAs' bytes
+          const uint32_t bar = dsmem_addr(smem_u32(&ctrl->full[s]), 0);
+          if (rank == 0) mbar_arrive_expect_tx(&ctrl->full[s], 2 * P.stage_bytes);
+          uint8_t* st = sm + (size_t)s * P.stage_bytes;
+          tma_load_2d_pair(smem_u32(st), &map_x, kb * 128, m0, bar);
+          tma_load_2d_pair(smem_u32(st + P.off_b), &map_w, kb * 128, n, bar);
+          if (issued < S) ++issued;
+          if (++s == S) s = 0, phase ^= 1;
+        }
+      }
+      // the last fill of every stage has been consumed before the CTA leaves
+      for (int i = 0; i < issued; ++i) {
+        if (issued < S) {
+          mbar_wait(&ctrl->empty[i], 0);
+        } else {
+          mbar_wait(&ctrl->empty[s], phase);
+          if (++s == S) s = 0, phase ^= 1;
+        }
+      }
+    }
+    if (warp == kWarps + 1 && rank == 0 && elect_one()) {
+      const uint32_t idesc = idesc_e4m3_f32(2 * kRows, (uint32_t)BN);
+      const uint64_t da = smem_desc(smem_u32(sm), 16, 1024, kSwizzle128B);
+      const uint64_t db = smem_desc(smem_u32(sm + P.off_b), 16, 1024, kSwizzle128B);
+      const uint32_t a_lo = (uint32_t)da, b_lo = (uint32_t)db, desc_hi = (uint32_t)(da >> 32);
+      int s = 0, tc = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int32_t pt = pair; pt < P.tiles && ok; pt += pairs) {
+        for (int kb = 0; kb < nkb && ok; ++kb, ++tc) {
+          const int buf = tc & 1;
+          if (tc >= 2 && !(ok = mbar_wait_spin(&ctrl->tempty[buf], (uint32_t)((tc >> 1) - 1) & 1u, abort))) break;
+          if (!(ok = mbar_wait_spin(&ctrl->full[s], phase, abort))) break;
+          tc_fence_after();
+          const uint32_t at = (uint32_t)s * (P.stage_bytes >> 4);
+          umma_stage<true, true>(tmem + (uint32_t)buf * (P.tmem_cols / 2), a_lo + at, b_lo + at, desc_hi, desc_hi, idesc, 0);
+          umma_commit_pair(&ctrl->tfull[buf], both);
+          umma_commit_pair(&ctrl->empty[s], both);
+          if (++s == S) s = 0, phase ^= 1;
+        }
+      }
+      if (!ok) report(err_word, MOLORA_DEV_WAIT_TIMEOUT);
+      umma_commit_pair(&ctrl->done, both);  // arrives in both CTAs once every MMA has completed
+    }
+    if (warp >= kWarps + 2) {  // the scales: 16 lanes a token, a K block each
+      const int l = (warp - kWarps - 2) * 32 + lane, k = l & 15;
+      int n = 0;
+      bool ok = true;
+      for (int32_t pt = pair; pt < P.tiles && ok; pt += pairs) {
+        int32_t m0, n0;
+        tile_at(pt, m0, n0);
+        for (int kb = 0; kb < nkb; kb += kScaleSpan, ++n) {
+          if (n >= 2 && !mbar_wait_spin(&ctrl->sempty[n & 1], (uint32_t)((n >> 1) - 1) & 1u, abort)) {
+            ok = false;
+            break;
+          }
+          Scales* to = reinterpret_cast<Scales*>(sm + P.off_scales) + (n & 1);
+          if (kb + k < nkb) {
+            for (int r = l >> 4; r < kRows && m0 + r < E.N; r += 4)
+              cp_async_4(smem_u32(to->x + k * kScaleStride + r), E.sx + (int64_t)(m0 + r) * nkb + kb + k);
+            for (int c = l >> 4; c < 8; c += 4) {  // piece c & 3 of side c / 4
+              const int32_t col = n0 + piece_output<kGated>(c >> 2, c & 3);
+              if (col < E.d_out)
+                cp_async_4(smem_u32(&to->w[k][c]), E.sw + (int64_t)(col / 128 + (kGated && (c & 1) ? E.up : 0)) * nkb + kb + k);
+            }
+          }
+          cp_async_mbar_arrive(&ctrl->sfull[n & 1]);
+        }
+      }
+      cp_async_wait_all();
+    }
+    __syncwarp();
+  } else {
+    registers_up<kEpiRegisters>();
+    const int quarter = warp & 3, side = warp >> 2;
+    uint8_t* box = sm + P.off_stage + (size_t)warp * P.box;
+    const uint32_t tempty = dsmem_addr(smem_u32(&ctrl->tempty[0]), 0), tfull = smem_u32(&ctrl->tfull[0]);
+    const int pieces = pieces_of<kGated>(P, side);
+    uint32_t at[4];
+#pragma unroll
+    for (int h = 0; h < 4; ++h) at[h] = ((uint32_t)(quarter * 32) << 16) + (uint32_t)piece_column<kGated>(P, side, h);
+    int tc = 0, spans = 0;     // accumulators, and spans of scales, done with
+    int asked = 0, taken = 0;  // rounds of the residual on their way or taken, and taken
+    bool ok = true;
+    for (int32_t pt = pair; pt < P.tiles && ok; pt += pairs) {
+      int32_t m0, n0;
+      tile_at(pt, m0, n0);
+      m0 += quarter * 32;
+      // output piece o's first column; it is the outputs' where that is below d_out, in the tile and for rows that are there
+      auto column = [&](int o) { return n0 + piece_output<kGated>(side, kGated ? 2 * o : o); };
+      auto there = [&](int o) { return o < (kGated ? pieces / 2 : pieces) && column(o) < E.d_out && m0 < E.N; };
+      // the residual's pieces of a round come into the boxes that the outputs' leave from
+      auto ask = [&](int round) {
+        if (lane == 0) {
+          bulk_wait_read<0>();  // the last stores have read the boxes
+          uint32_t bytes = 0;
+#pragma unroll
+          for (int o = 0; o < kRound; ++o) bytes += there(round * kRound + o) ? kPiece : 0u;
+          mbar_arrive_expect_tx(&ctrl->res_full[warp], bytes);
+#pragma unroll
+          for (int o = 0; o < kRound; ++o)
+            if (there(round * kRound + o))
+              for (int q = 0; q < kParts; ++q)
+                tma_load_2d(smem_u32(box + o * kPiece + q * kBox), &map_r, column(round * kRound + o) + q * 16, m0, &ctrl->res_full[warp]);
+        }
+        ++asked;
+      };
+      if (!kGated && E.tma_res) ask(0);
+      float acc[4][32];
+#pragma unroll
+      for (int h = 0; h < 4; ++h)
+#pragma unroll
+        for (int i = 0; i < 32; ++i) acc[h][i] = 0.f;
+      // K blocks of a span of scales, with as few instructions as they come down to
+      auto add_span = [&](auto count, int blocks, uint32_t sx, uint32_t sw) {
+        constexpr int kPieces = decltype(count)::value;
+        uint32_t buf = (uint32_t)tc & 1u, parity = (uint32_t)(tc >> 1) & 1u;
+        const uint32_t flip = P.tmem_cols / 2;
+        uint32_t from = tmem + buf * flip, full_at = tfull + buf * 8, free_at = tempty + buf * 8;
+        tc += blocks;
+        for (; blocks > 0; --blocks, sx += kScaleStride * 4, sw += 32) {
+          const float row = lds_f32(sx);
+          const float4 w = lds_f32x4(sw);
+          if (!mbar_try_wait_all(full_at, parity)) {
+            ok = __all_sync(0xffffffffu, mbar_wait_spin(&ctrl->tfull[buf], parity, abort));
+            if (!ok) return;
+          }
+          tc_fence_after();
+          // a piece is on its way from TMEM while the one before it is added
+          uint32_t r[2][32];
+          tmem_ld32_start(from + at[0], r[0]);
+#pragma unroll
+          for (int h = 0; h < kPieces; ++h) {
+            tmem_ld_wait(r[h & 1]);
+            if (h + 1 < kPieces) {
+              tmem_ld32_start(from + at[h + 1], r[(h + 1) & 1]);
+            } else {
+              tc_fence_before();
+              if (lane == 0) mbar_arrive_cluster_read(free_at);
+            }
+            const float scale = row * (h == 0 ? w.x : h == 1 ? w.y : h == 2 ? w.z : w.w);
+#pragma unroll
+            for (int i = 0; i < 32; i += 2)
+              fma_pair(acc[h][i], acc[h][i + 1], __uint_as_float(r[h & 1][i]), __uint_as_float(r[h & 1][i + 1]), scale);
+          }
+          parity ^= buf, buf ^= 1;
+          from = tmem + (buf ? flip : 0u), full_at ^= 8, free_at ^= 8;
+        }
+      };
+      for (int kb = 0; kb < nkb && ok; kb += kScaleSpan, ++spans) {
+        ok = __all_sync(0xffffffffu, mbar_wait_spin(&ctrl->sfull[spans & 1], (uint32_t)(spans >> 1) & 1u, abort));
+        if (!ok) break;
+        const uint32_t sw = smem_u32(sm + P.off_scales) + (spans & 1) * (uint32_t)sizeof(Scales) + side * 16;
+        const uint32_t sx = sw - side * 16 + kScaleSpan * 32 + (quarter * 32 + lane) * 4;
+        const int blocks = min(nkb - kb, kScaleSpan);
+        if (pieces == 4)
+          add_span(std::integral_constant<int, 4>{}, blocks, sx, sw);
+        else if (!kGated && pieces == 3)
+          add_span(std::integral_constant<int, 3>{}, blocks, sx, sw);
+        else
+          add_span(std::integral_constant<int, 2>{}, blocks, sx, sw);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctrl->sempty[spans & 1]);
+      }
+      if (!ok) break;
+      if constexpr (kGated) {
+#pragma unroll
+        for (int o = 0; o < 2; ++o) {
+          apply_act(acc[2 * o], E.act);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) acc[o][i] = acc[2 * o][i] * acc[2 * o + 1][i];
+        }
+      } else {
+#pragma unroll
+        for (int o = 0; o < 4; ++o) {
+          if (E.bias) {
+            const float b = there(o) && column(o) + lane < E.d_out ? E.bias[column(o) + lane] : 0.f;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) acc[o][i] += __shfl_sync(0xffffffffu, b, i);
+          }
+          apply_act(acc[o], E.act);
+        }
+      }
+      if (E.tma_y) {
+        auto chunk = [&](int o, int i) { return box + o * kPiece + (i >> 2) * kBox + swz_offset((uint32_t)lane, (uint32_t)i & 3u, 64); };
+#pragma unroll
+        for (int round = 0; round < kOut / kRound; ++round) {
+          if (!kGated && E.tma_res) {
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait(&ctrl->res_full[warp], (uint32_t)taken & 1u)))) break;
+            ++taken;
+#pragma unroll
+            for (int o = 0; o < kRound; ++o) {
+              float(&v)[32] = acc[round * kRound + o];
+              if (!there(round * kRound + o)) continue;
+#pragma unroll
+              for (int i = 0; i < 4 * kParts; ++i) {
+                const uint4 q = *reinterpret_cast<const uint4*>(chunk(o, i));
+                const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  if constexpr (kY16) {
+                    v[8 * i + 2 * j] += __uint_as_float(w[j] << 16);
+                    v[8 * i + 2 * j + 1] += __uint_as_float(w[j] & 0xffff0000u);
+                  } else {
+                    v[4 * i + j] += __uint_as_float(w[j]);
+                  }
+                }
+              }
+            }
+          } else {
+            if (lane == 0) bulk_wait_read<0>();  // the last stores have read the boxes
+            __syncwarp();
+          }
+#pragma unroll
+          for (int o = 0; o < kRound; ++o) {
+            const float(&v)[32] = acc[round * kRound + o];
+#pragma unroll
+            for (int i = 0; i < 4 * kParts; ++i) {
+              uint4 q;
+              if constexpr (kY16)
+                q = make_uint4(pack_bf16(v[8 * i], v[8 * i + 1]), pack_bf16(v[8 * i + 2], v[8 * i + 3]),
+                               pack_bf16(v[8 * i + 4], v[8 * i + 5]), pack_bf16(v[8 * i + 6], v[8 * i + 7]));
+              else
+                q = make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]), __float_as_uint(v[4 * i + 2]),
+                               __float_as_uint(v[4 * i + 3]));
+              *reinterpret_cast<uint4*>(chunk(o, i)) = q;
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+#pragma unroll
+            for (int o = 0; o < kRound; ++o)
+              if (there(round * kRound + o))
+                for (int q = 0; q < kParts && column(round * kRound + o) + q * 16 < E.d_out; ++q)
+                  tma_store_2d(&map_y, smem_u32(box + o * kPiece + q * kBox), column(round * kRound + o) + q * 16, m0);
+            bulk_commit();
+          }
+          if (!kGated && E.tma_res && round + 1 < kOut / kRound) ask(round + 1);
+        }
+      } else {
+        // rows that are not 16-byte aligned: turned in shared memory, written a row at a time, 8 rows' residuals on their way
+        // together
+        float* turned = reinterpret_cast<float*>(box);
+#pragma unroll
+        for (int o = 0; o < kOut; ++o) {
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) turned[lane * 32 + (i ^ lane)] = acc[o][i];
+          __syncwarp();
+          const int32_t col = column(o) + lane;
+          const bool in = there(o) && col < E.d_out;
+#pragma unroll 1
+          for (int q0 = 0; q0 < 32 && m0 + q0 < E.N; q0 += 8) {
+            float add[8];
+            const int64_t to = ((int64_t)m0 + q0) * E.d_out + col;
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              add[q] = 0.f;
+              if (!kGated && E.res && in && m0 + q0 + q < E.N) {
+                if constexpr (kY16)
+                  add[q] = to_float(static_cast<const __nv_bfloat16*>(E.res)[to + (int64_t)q * E.d_out]);
+                else
+                  add[q] = static_cast<const float*>(E.res)[to + (int64_t)q * E.d_out];
+              }
+            }
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              if (!in || m0 + q0 + q >= E.N) continue;
+              const float v = turned[(q0 + q) * 32 + (lane ^ (q0 + q))] + add[q];
+              if constexpr (kY16)
+                static_cast<__nv_bfloat16*>(E.y)[to + (int64_t)q * E.d_out] = __float2bfloat16_rn(v);
+              else
+                static_cast<float*>(E.y)[to + (int64_t)q * E.d_out] = v;
+            }
+          }
+        }
+      }
+    }
+    if (!ok) {
+      // no copy is left in flight
+      if (taken < asked) mbar_wait(&ctrl->res_full[warp], (uint32_t)taken & 1u);
+      *abort = 1;
+      if (lane == 0) report(err_word, MOLORA_DEV_WAIT_TIMEOUT);
+    }
+    if (lane == 0) bulk_wait_all();
+    __syncwarp();
+  }
+  if (warp == kWarps + 1 && lane == 0) mbar_wait(&ctrl->done, 0);
+  __syncthreads();
+  cluster_sync();  // neither CTA leaves, nor frees its TMEM, while the other may still signal or use it
+  if (warp == kWarps + 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, P.tmem_cols);
+  }
+}
+
+cudaError_t launch_blocks_tc(const FeedForwardArgs& a, int BN, cudaStream_t stream) {
+  FEpi e = ff_epilogue_of(a);
+  BPlan p = {};
+  const int width = a.gated ? BN / 2 : BN;
+  const int64_t m_tiles = (a.N + 2 * kRows - 1) / (2 * kRows), n_tiles = ((int64_t)a.d_out + width - 1) / width;
+  if (m_tiles * n_tiles > INT32_MAX / 16) return cudaErrorNotSupported;
+  p.BN = BN;
+  p.nkb = ff_k_blocks(a);
+  p.m_tiles = (int32_t)m_tiles;
+  p.n_tiles = (int32_t)n_tiles;
+  p.tiles = p.m_tiles * p.n_tiles;
+  p.group = 8;
+  p.off_b = kRows * kRowBytes;
+  p.stage_bytes = p.off_b + (uint32_t)(BN / 2) * kRowBytes;
+  p.tmem_cols = tmem_columns(2 * (uint32_t)(BN <= 128 ? 128 : 256));
+  CUtensorMap mx, mw, my = {}, mr = {};
+  auto rows_map = [&](CUtensorMap* m, const void* base) {
+    return linear_map(m, a.y_bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, a.y_bf16 ? 2 : 4, base,
+                      (uint64_t)a.N, (uint64_t)a.d_out, a.y_bf16 ? 32 : 16, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+  };
+  if (e.tma_y && (!rows_map(&my, a.y) || (a.residual && !rows_map(&mr, a.residual)))) e.tma_y = false;
+  e.tma_res = e.tma_y && a.residual;
+  p.box = (a.gated ? 2 : 4) * kBox;  // all of a tile's pieces of bf16, half of them of fp32
+  static_assert(kTurn <= 2 * kBox, "a warp's boxes hold a turned piece");
+  const size_t boxes = (size_t)kWarps * p.box, fixed = boxes + 2 * sizeof(Scales) + sizeof(BCtrl) + kSmemSlack;
+  p.S = (int)((kMaxSmem - fixed) / p.stage_bytes);
+  if (p.S > kMaxStages) p.S = kMaxStages;
+  p.off_stage = (uint32_t)p.S * p.stage_bytes;
+  p.off_scales = p.off_stage + (uint32_t)boxes;
+  p.off_ctrl = p.off_scales + 2 * (uint32_t)sizeof(Scales);
+  // one CTA an SM, alone: an allocation of TMEM never waits for another CTA's (see linear.cu)
+  p.smem = kMaxSmem;
+  if (!ff_operand_map(&mx, a, a.x, a.N, kRows) || !ff_operand_map(&mw, a, a.W, ff_rows_of_w(a), (uint32_t)(BN / 2)))
+    return cudaErrorNotSupported;
+  auto go = [&](auto kernel, std::atomic<uint64_t>& allowed) {
+    const cudaError_t set = allow_smem(kernel, allowed, kMaxSmem);
+    if (set != cudaSuccess) return set;
+    const int32_t most = num_sms() / 2;
+    const dim3 grid((unsigned)(2 * (p.tiles < most ? p.tiles : most)));
+    return launch_kernel(kernel, grid, dim3(kThreadsB), p.smem, stream, 2, e, p, a.err_word, mx, mw, my, mr);
+  };
+  static std::atomic<uint64_t> allowed[3];
+  if (a.gated) return go(blocks_tc_kernel<true, true>, allowed[0]);
+  return a.y_bf16 ? go(blocks_tc_kernel<false, true>, allowed[1]) : go(blocks_tc_kernel<false, false>, allowed[2]);
+}
+
+}  // namespace molora

@@ -9,10 +9,9 @@
 // sums of g[t,f] and u[t,f] meet in the registers of one thread and neither goes to memory.  The backward pass makes
 // them again: at 4096 x 2048 -> 6144 their 200 MB in fp32, written and read back, would take as long.
 //
-// ff_tc_kernel (many tokens): linear_tc_kernel's pipeline (linear.cu): persistent pairs of CTAs with tiles of 256 tokens x
-//   BN rows of W, a TMA warp and an MMA warp ahead of 8 epilogue warps by two TMEM accumulators.  Scales change with
-//   every K block of 128, so with e4m3 an accumulator holds one K block, and the epilogue warps
-//   add it, scaled, to fp32 registers (64 a thread) while the next one's MMAs run.
+// ff_tc_kernel (bf16, many tokens): linear_tc_kernel's pipeline (linear.cu): persistent pairs of CTAs with tiles of 256 tokens x
+//   BN rows of W, a TMA warp and an MMA warp ahead of 8 epilogue warps by two TMEM accumulators.
+// blocks_tc_kernel (e4m3, many tokens): blocks_tc.cu.
 // ff_skinny_kernel (few tokens): W's rows are the MMA's M, the tokens its N, d_in split over a cluster; bound by reading W.
 #include <cudaTypedefs.h>
 
@@ -21,9 +20,7 @@
 #include <cstdlib>
 #endif
 
-#include "common.cuh"
-#include "kernels.h"
-#include "linear.cuh"
+#include "feed_forward.cuh"
 
 namespace molora {
 
@@ -31,23 +28,6 @@ namespace {
 
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 32 * (kEpiWarps + 2);  // + TMA warp (8) + MMA warp (9)
-// ff_tc_kernel: groups of 4 epilogue warps that share a tile's chunks, then the TMA warp, the MMA warp and two that only make up
-// the warpgroup.  With e4m3 a K block's sums have 512 cycles, the next one's MMAs, to leave TMEM: four warps on each
-// scheduler hide one another's waits (8192 x 4096 -> 4096 with two 218 us, with four TODO).  Their 64 sums a thread
-// and what they work with take more than the 96 registers that 640 threads are launched with, so the last warpgroup
-// gives up its own: 512 x 104 + 128 x 64 = 640 x 96.
-constexpr int tc_sides(bool fp8) { return fp8 ? 4 : 2; }
-constexpr int tc_threads(bool fp8) { return 32 * (4 * tc_sides(fp8) + 4); }
-constexpr int kEpiRegisters = 104, kOtherRegisters = 64;
-constexpr int kMaxSets = 2;  // staging boxes that an epilogue warp reads into at most
-// The scales of kScaleSpan K blocks of a tile, which two warps gather ahead of the epilogue, K block by K block: of the CTA's
-// 128 tokens (x's scales lie token by token, so gathered by the epilogue's warps each K block's take 32 lines of L1 a warp,
-// 512 cycles an SM), and of the 8 pieces of 32 columns of the accumulator, c and c + 4 together.
-constexpr int kScaleSpan = 16, kScaleStride = kRows + 1;
-struct __align__(8) Scales {
-  float x[kScaleSpan * kScaleStride];
-  float w[kScaleSpan * 8];
-};
 enum Mode { kLinear, kGated, kSlopes };
 constexpr int kSpan = 8;     // bf16, few tokens: K blocks summed in TMEM before fp32 registers take over
 
@@ -56,58 +36,36 @@ struct __align__(8) FCtrl {
   uint64_t empty[kMaxStages];
   uint64_t tfull[2];
   uint64_t tempty[2];
-  uint64_t sfull[2];
-  uint64_t sempty[2];
   uint64_t done;
-  uint64_t res_full[16 * kMaxSets];
+  uint64_t res_full[kEpiWarps * 2];
   uint32_t tmem_base;
   int32_t abort;
-};
-
-// What the epilogue reads and writes.
-struct FEpi {
-  const float* sx;   // [N x nkb]
-  const float* sw;   // [blocks of W's rows x nkb]
-  const float* bias;
-  const void* res;   // slopes: dh
-  void* y;           // slopes: dproj
-  int64_t N;
-  int32_t d_out;     // outputs; gated: d_ff
-  int32_t up;        // gated: Wu's first block of rows in sw
-  molora_activation act;
-  bool y_bf16;
-  bool tma_y;        // rows of y on 16-byte boundaries
-  bool tma_res;      // the residual comes through the staging boxes (slopes: dh does, by TMA)
 };
 
 struct FPlan {
   int BN;                // rows of W a tile
   int S;                 // stages
-  int sets;              // staging boxes a warp
   int nkb;               // K blocks of 128 bytes
   int group;             // token tiles per group of tiles (they share W's rows in L2)
   // (32 bits: 2^27 tiles would be an output of 10^13 bytes)
   int32_t m_tiles, n_tiles, tiles;
-  uint32_t stage_bytes, off_b, off_stage, off_scales, off_ctrl, tmem_cols, smem;
+  uint32_t stage_bytes, off_b, off_stage, off_ctrl, tmem_cols, smem;
 };
 
 }  // namespace
 
-template <bool kFp8, Mode kMode, bool kY16>
-__global__ void __launch_bounds__(tc_threads(kFp8), 1)
+template <Mode kMode>
+__global__ void __launch_bounds__(kThreads, 1)
     ff_tc_kernel(const FEpi E, const FPlan P, int32_t* err_word, const __grid_constant__ CUtensorMap map_x,
                  const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_y,
                  const __grid_constant__ CUtensorMap map_r) {
-  constexpr bool kPaired = kMode != kLinear;  // gate and up projection side by side
-  constexpr int kParts = kY16 ? 1 : 2;  // boxes of a chunk of 32 columns of y
-  constexpr uint32_t kSet = kParts * kBox;
-  constexpr int kSides = tc_sides(kFp8), kWarps = 4 * kSides;
+  constexpr int kWarps = kEpiWarps;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   FCtrl* ctrl = reinterpret_cast<FCtrl*>(sm + P.off_ctrl);
   // (the warp's number, and the like, from lane 0: in uniform registers)
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-  const int BN = P.BN, S = P.S, nkb = P.nkb, width = kPaired ? BN / 2 : BN;  // outputs a tile
+  const int BN = P.BN, S = P.S, nkb = P.nkb, width = BN / 2;  // outputs a tile
   const uint32_t rank = cluster_ctarank();
   const uint16_t both = 0x3;
   const int32_t pair = blockIdx.x / 2, pairs = gridDim.x / 2;
@@ -133,11 +91,9 @@ __global__ void __launch_bounds__(tc_threads(kFp8), 1)
     for (int b = 0; b < 2; ++b) {
       mbar_init(&ctrl->tfull[b], 1);
       mbar_init(&ctrl->tempty[b], 2 * kWarps);
-      mbar_init(&ctrl->sfull[b], 64);
-      mbar_init(&ctrl->sempty[b], kWarps);
     }
     mbar_init(&ctrl->done, 1);
-    for (int b = 0; b < kWarps * kMaxSets; ++b) mbar_init(&ctrl->res_full[b], 1);
+    for (int b = 0; b < kWarps * 2; ++b) mbar_init(&ctrl->res_full[b], 1);
     ctrl->abort = 0;
     mbar_fence_init();
     tma_prefetch_desc(&map_x);
@@ -153,18 +109,15 @@ __global__ void __launch_bounds__(tc_threads(kFp8), 1)
   const uint32_t tmem = __shfl_sync(0xffffffffu, ctrl->tmem_base, 0);
   cluster_sync();  // every CTA's barriers are initialised before another signals them
 
-  if (warp >= kWarps) {
-    if constexpr (kFp8) registers_down<kOtherRegisters>();
-    if (warp == kWarps && elect_one()) {
-      const int elems = kFp8 ? 128 : 64;  // K elements per stage
+  if (warp == kWarps) {
+    if (elect_one()) {
       int s = 0, issued = 0;
       uint32_t phase = 1;  // the first use of a stage finds it empty
       bool ok = true;
       for (int32_t pt = pair; pt < P.tiles && ok; pt += pairs) {
         int32_t m0, n0;
         tile_at(pt, m0, n0);
-        // the pair's halves of the MMA's columns: gated, one CTA brings rows of Wg and the other of Wu
-        const int32_t n = kPaired ? n0 + (int32_t)rank * E.d_out : n0 + (int32_t)rank * (BN / 2);
+        const int32_t n = n0 + (int32_t)rank * E.d_out;  // one CTA brings rows of Wg and the other of Wu
         for (int kb = 0; kb < nkb; ++kb) {
           if (issued >= S && !mbar_wait_spin(&ctrl->empty[s], phase, abort)) {
             ok = false;
@@ -174,8 +127,8 @@ __global__ void __launch_bounds__(tc_threads(kFp8), 1)
           const uint32_t bar = dsmem_addr(smem_u32(&ctrl->full[s]), 0);
           if (rank == 0) mbar_arrive_expect_tx(&ctrl->full[s], 2 * P.stage_bytes);
           uint8_t* st = sm + (size_t)s * P.stage_bytes;
-          tma_load_2d_pair(smem_u32(st), &map_x, kb * elems, m0, bar);
-          tma_load_2d_pair(smem_u32(st + P.off_b), &map_w, kb * elems, n, bar);
+          tma_load_2d_pair(smem_u32(st), &map_x, kb * 64, m0, bar);
+          tma_load_2d_pair(smem_u32(st + P.off_b), &map_w, kb * 64, n, bar);
           if (issued < S) ++issued;
           if (++s == S) s = 0, phase ^= 1;
         }
@@ -190,306 +143,129 @@ __global__ void __launch_bounds__(tc_threads(kFp8), 1)
         }
       }
     }
-    if (warp == kWarps + 1 && rank == 0 && elect_one()) {
-      const uint32_t idesc = kFp8 ? idesc_e4m3_f32(2 * kRows, (uint32_t)BN) : idesc_bf16_f32(2 * kRows, (uint32_t)BN, false, false);
+    __syncwarp();
+  } else if (warp == kWarps + 1) {
+    if (rank == 0 && elect_one()) {
+      const uint32_t idesc = idesc_bf16_f32(2 * kRows, (uint32_t)BN, false, false);
       const uint64_t da = smem_desc(smem_u32(sm), 16, 1024, kSwizzle128B);
       const uint64_t db = smem_desc(smem_u32(sm + P.off_b), 16, 1024, kSwizzle128B);
       const uint32_t a_lo = (uint32_t)da, b_lo = (uint32_t)db, desc_hi = (uint32_t)(da >> 32);
-      const int span = kFp8 ? 1 : nkb;  // K blocks an accumulator holds
       int s = 0, tc = 0;
       uint32_t phase = 0;
       bool ok = true;
-      for (int32_t pt = pair; pt < P.tiles && ok; pt += pairs) {
-        for (int first = 0; first < nkb && ok; first += span, ++tc) {
-          const int buf = tc & 1;
-          if (tc >= 2 && !mbar_wait_spin(&ctrl->tempty[buf], (uint32_t)((tc >> 1) - 1) & 1u, abort)) {
+      for (int32_t pt = pair; pt < P.tiles && ok; pt += pairs, ++tc) {
+        const int buf = tc & 1;
+        if (tc >= 2 && !mbar_wait_spin(&ctrl->tempty[buf], (uint32_t)((tc >> 1) - 1) & 1u, abort)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d = tmem + (uint32_t)(buf * (P.tmem_cols / 2));
+        for (int kb = 0; kb < nkb; ++kb) {
+          if (!mbar_wait_spin(&ctrl->full[s], phase, abort)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t d = tmem + (uint32_t)(buf * (P.tmem_cols / 2));
-          for (int kb = first; kb < first + span; ++kb) {
-            if (!mbar_wait_spin(&ctrl->full[s], phase, abort)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            const uint32_t at = (uint32_t)s * (P.stage_bytes >> 4);
-            umma_stage<true, kFp8>(d, a_lo + at, b_lo + at, desc_hi, desc_hi, idesc, kb != first);
-            umma_commit_pair(&ctrl->empty[s], both);  // e4m3: for the epilogue too
-            if (++s == S) s = 0, phase ^= 1;
-          }
-          if (!kFp8 && ok) umma_commit_pair(&ctrl->tfull[buf], both);
+          const uint32_t at = (uint32_t)s * (P.stage_bytes >> 4);
+          umma_stage<true, false>(d, a_lo + at, b_lo + at, desc_hi, desc_hi, idesc, kb != 0);
+          umma_commit_pair(&ctrl->empty[s], both);
+          if (++s == S) s = 0, phase ^= 1;
         }
+        if (ok) umma_commit_pair(&ctrl->tfull[buf], both);
       }
       if (!ok) report(err_word, MOLORA_DEV_WAIT_TIMEOUT);
       umma_commit_pair(&ctrl->done, both);  // arrives in both CTAs once every MMA has completed
     }
-    if constexpr (kFp8) {
-      if (warp >= kWarps + 2) {  // the scales' two warps: 16 lanes a token, a K block each
-        const int l = (warp - kWarps - 2) * 32 + lane, k = l & 15;
-        int n = 0;
-        bool ok = true;
-        for (int32_t pt = pair; pt < P.tiles && ok; pt += pairs) {
-          int32_t m0, n0;
-          tile_at(pt, m0, n0);
-          for (int kb = 0; kb < nkb; kb += kScaleSpan, ++n) {
-            if (n >= 2 && !mbar_wait_spin(&ctrl->sempty[n & 1], (uint32_t)((n >> 1) - 1) & 1u, abort)) {
-              ok = false;
-              break;
-            }
-            Scales* to = reinterpret_cast<Scales*>(sm + P.off_scales) + (n & 1);
-            if (kb + k < nkb) {
-              for (int r = l >> 4; r < kRows && m0 + r < E.N; r += 4)
-                cp_async_4(smem_u32(to->x + k * kScaleStride + r), E.sx + (int64_t)(m0 + r) * nkb + kb + k);
-              for (int c = l >> 4; c < 8; c += 4) {
-                const int32_t col = n0 + (kPaired ? c & 3 : c) * 32;
-                if (col < E.d_out)
-                  cp_async_4(smem_u32(to->w + k * 8 + (c & 3) * 2 + (c >> 2)),
-                             E.sw + (int64_t)(col / 128 + (kPaired && c >= 4 ? E.up : 0)) * nkb + kb + k);
-              }
-            }
-            cp_async_mbar_arrive(&ctrl->sfull[n & 1]);
-          }
-        }
-        cp_async_wait_all();
-      }
-    }
     __syncwarp();
   } else {
-    if constexpr (kFp8) registers_up<kEpiRegisters>();
-    // epilogue: warps w, w + 4, ... share 32 rows and take chunks of 32 outputs in turn
+    // epilogue: warps w and w + 4 share 32 rows and take chunks of 32 outputs in turn
     const int quarter = warp & 3, side = warp >> 2;
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-    // Outputs leave through a ring of P.sets staging boxes, into which the residual's chunks come before.
-    // dh's chunks come through a ring of their own, of two boxes.
+    // Outputs leave through a ring of two staging boxes; dh's chunks come through two of their own.
     constexpr int kOwn = kMode == kSlopes ? 2 : 0;
-    uint8_t* in_ring = sm + P.off_stage + (size_t)warp * (P.sets + kOwn) * kSet;
-    uint8_t* ring = in_ring + kOwn * kSet;
-    const int in_sets = kOwn ? kOwn : P.sets;
-    int tc = 0, spans = 0;                  // accumulators, and spans of scales, done with
-    int used = 0, asked = 0, taken = 0;  // boxes written; residual chunks on their way or taken, and taken
-    auto box_of = [&](int n) { return ring + (size_t)(n & (P.sets - 1)) * kSet; };
-    auto in_box = [&](int n) { return in_ring + (size_t)(n & (in_sets - 1)) * kSet; };
-    auto ask = [&](int32_t col, int32_t m0) {
+    uint8_t* in_ring = sm + P.off_stage + (size_t)warp * (2 + kOwn) * kBox;
+    uint8_t* ring = in_ring + kOwn * kBox;
+    int tc = 0, used = 0, asked = 0, taken = 0;  // accumulators done with, boxes written; dh's chunks on their way or taken, and taken
+    auto in_box = [&](int n) { return in_ring + (size_t)(n & 1) * kBox; };
+    auto ask = [&](int32_t col, int32_t m0) {  // (the box's last chunk has been read by every lane, see below)
       if (lane == 0) {
-        uint64_t* bar = &ctrl->res_full[warp * kMaxSets + (asked & (in_sets - 1))];
-        // the store that last left the box has read it (dh's boxes: the lanes have, see below)
-        if (!kOwn && asked >= P.sets) bulk_wait_read_upto(used + P.sets - 1 - asked);
-        mbar_arrive_expect_tx(bar, kSet);
-        for (int q = 0; q < kParts; ++q)  // (past d_out there is nothing: zeros)
-          tma_load_2d(smem_u32(in_box(asked) + q * kBox), &map_r, col + q * 16, m0, bar);
+        uint64_t* bar = &ctrl->res_full[warp * 2 + (asked & 1)];
+        mbar_arrive_expect_tx(bar, kBox);
+        tma_load_2d(smem_u32(in_box(asked)), &map_r, col, m0, bar);
       }
       ++asked;
     };
     // the next chunk that was asked for; false where the wait ran out
     auto await = [&]() {
-      return __all_sync(0xffffffffu, mbar_wait(&ctrl->res_full[warp * kMaxSets + (taken & (in_sets - 1))], (uint32_t)(taken / in_sets) & 1u));
+      return __all_sync(0xffffffffu, mbar_wait(&ctrl->res_full[warp * 2 + (taken & 1)], (uint32_t)(taken / 2) & 1u));
     };
-    auto piece = [&](uint8_t* box, int i) { return box + (i >> 2) * kBox + swz_offset((uint32_t)lane, (uint32_t)i & 3u, 64); };
+    auto piece = [&](uint8_t* box, int i) { return box + swz_offset((uint32_t)lane, (uint32_t)i, 64); };
     // 32 columns of this warp's rows into a box, ready to be stored by lane 0
     auto stage = [&](const float (&v)[32]) {
-      uint8_t* box = box_of(used);
-      if (kOwn || !E.tma_res) {
-        if (lane == 0) bulk_wait_read_upto(P.sets - 1);  // the store that last left the box has read it
-        __syncwarp();
-      }
+      uint8_t* box = ring + (size_t)(used & 1) * kBox;
+      if (lane == 0) bulk_wait_read<1>();  // the store that last left the box has read it
+      __syncwarp();
 #pragma unroll
-      for (int i = 0; i < 4 * kParts; ++i) {
-        uint4 q;
-        if constexpr (kY16)
-          q = make_uint4(pack_bf16(v[8 * i], v[8 * i + 1]), pack_bf16(v[8 * i + 2], v[8 * i + 3]),
-                         pack_bf16(v[8 * i + 4], v[8 * i + 5]), pack_bf16(v[8 * i + 6], v[8 * i + 7]));
-        else
-          q = make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]), __float_as_uint(v[4 * i + 2]),
-                         __float_as_uint(v[4 * i + 3]));
-        *reinterpret_cast<uint4*>(piece(box, i)) = q;
-      }
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<uint4*>(piece(box, i)) =
+            make_uint4(pack_bf16(v[8 * i], v[8 * i + 1]), pack_bf16(v[8 * i + 2], v[8 * i + 3]),
+                       pack_bf16(v[8 * i + 4], v[8 * i + 5]), pack_bf16(v[8 * i + 6], v[8 * i + 7]));
       fence_proxy_async_smem();
       __syncwarp();
       ++used;
       return box;
     };
     const uint32_t tempty = dsmem_addr(smem_u32(&ctrl->tempty[0]), 0);
-    int s = 0;  // e4m3: the stage of the next K block
-    uint32_t phase = 0;
     bool ok = true;
     for (int32_t pt = pair; pt < P.tiles && ok; pt += pairs) {
       int32_t m0, n0;
       tile_at(pt, m0, n0);
       m0 += quarter * 32;
       const int chunks = m0 < E.N ? min(width / 32, (E.d_out - n0 + 31) / 32) : 0;
-      const int mine = side < chunks ? (chunks - side + kSides - 1) / kSides : 0;  // chunks side, side + kSides, ...
-      auto column = [&](int q) { return n0 + (side + kSides * q) * 32; };
-      // y's chunk from its finished values
+      // h's chunk from its finished values
       auto put = [&](float (&v)[32], int32_t col) {
         if (E.tma_y) {
-          if (kMode == kLinear && E.tma_res) {
-            if (!await()) {
-              ok = false;
-              return;
-            }
-            uint8_t* box = in_box(taken);
-#pragma unroll
-            for (int i = 0; i < 4 * kParts; ++i) {
-              const uint4 q = *reinterpret_cast<const uint4*>(piece(box, i));
-              const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                if constexpr (kY16) {
-                  v[8 * i + 2 * j] += __uint_as_float(w[j] << 16);
-                  v[8 * i + 2 * j + 1] += __uint_as_float(w[j] & 0xffff0000u);
-                } else {
-                  v[4 * i + j] += __uint_as_float(w[j]);
-                }
-              }
-            }
-            ++taken;
-          }
           const uint8_t* box = stage(v);
           if (lane == 0) {
-            for (int q = 0; q < kParts && col + q * 16 < E.d_out; ++q)
-              tma_store_2d(&map_y, smem_u32(box + q * kBox), col + q * 16, m0);
+            tma_store_2d(&map_y, smem_u32(box), col, m0);
             bulk_commit();
           }
         } else {
-          // rows that are not 16-byte aligned: turned in shared memory, written a row at a time, 8 rows' residuals
-          // on their way together
+          // rows that are not 16-byte aligned: turned in shared memory, written a row at a time
           float* turned = reinterpret_cast<float*>(ring);
           __syncwarp();
 #pragma unroll
           for (int i = 0; i < 32; ++i) turned[lane * 32 + (i ^ lane)] = v[i];
           __syncwarp();
-          const bool in = col + lane < E.d_out;
-#pragma unroll 1
-          for (int q0 = 0; q0 < 32 && m0 + q0 < E.N; q0 += 8) {
-            float o[8];
-            const int64_t at = ((int64_t)m0 + q0) * E.d_out + col + lane;
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-              o[q] = 0.f;
-              if (kMode == kLinear && E.res && in && m0 + q0 + q < E.N) {
-                if constexpr (kY16)
-                  o[q] = to_float(static_cast<const __nv_bfloat16*>(E.res)[at + (int64_t)q * E.d_out]);
-                else
-                  o[q] = static_cast<const float*>(E.res)[at + (int64_t)q * E.d_out];
-              }
-            }
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-              if (!in || m0 + q0 + q >= E.N) continue;
-              const float w = turned[(q0 + q) * 32 + (lane ^ (q0 + q))] + o[q];
-              if constexpr (kY16)
-                static_cast<__nv_bfloat16*>(E.y)[at + (int64_t)q * E.d_out] = __float2bfloat16_rn(w);
-              else
-                static_cast<float*>(E.y)[at + (int64_t)q * E.d_out] = w;
-            }
-          }
-          __syncwarp();
+          __nv_bfloat16* y = static_cast<__nv_bfloat16*>(E.y) + (int64_t)m0 * E.d_out + col + lane;
+          for (int q = 0; q < 32 && m0 + q < E.N; ++q)
+            if (col + lane < E.d_out) y[(int64_t)q * E.d_out] = __float2bfloat16_rn(turned[q * 32 + (lane ^ q)]);
         }
       };
-      auto wait_sums = [&]() {  // the next accumulator
-        if constexpr (kFp8) {
-          ok = __all_sync(0xffffffffu, mbar_wait_spin(&ctrl->empty[s], phase, abort));
-          if (++s == S) s = 0, phase ^= 1;
-        } else {
-          ok = __all_sync(0xffffffffu, mbar_wait_spin(&ctrl->tfull[tc & 1], (uint32_t)(tc >> 1) & 1u, abort));
-        }
-        tc_fence_after();
-        return tmem + (uint32_t)((tc & 1) * (P.tmem_cols / 2));
-      };
+      if (E.tma_res)
+        for (int c = side; c < chunks; c += 2) ask(n0 + c * 32, m0);
+      ok = __all_sync(0xffffffffu, mbar_wait_spin(&ctrl->tfull[tc & 1], (uint32_t)(tc >> 1) & 1u, abort));
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t base = tmem + lanes + (uint32_t)((tc & 1) * (P.tmem_cols / 2));
       auto free_sums = [&]() {
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster_read(tempty + (tc & 1) * 8);
-        ++tc;
       };
-      if (E.tma_res)
-        for (int q = 0; q < mine && q < in_sets; ++q) ask(column(q), m0);
-      if constexpr (kFp8) {
-        // two pieces of 32 columns of TMEM, side and side + 4 of 8: linear, this warp's chunks; gated, gate and up
-        // projection of its chunk
-        float acc[2][32];
-        const int pieces = kPaired ? 2 * mine : mine;
-        const uint32_t at[2] = {lanes + (uint32_t)(side * 32), lanes + (uint32_t)((kPaired ? width : 128) + side * 32)};
-        float cb[2];
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const int32_t col = column(kPaired ? 0 : q);
-          cb[q] = !kPaired && E.bias && q < pieces && col + lane < E.d_out ? E.bias[col + lane] : 0.f;
-#pragma unroll
-          for (int i = 0; i < 32; ++i) acc[q][i] = 0.f;
-        }
-        // K blocks of a span of scales, whose sums are added with as few instructions as they come down to: 64 fmas a warp
-        // and K block, four warps a scheduler, in the 512 cycles of the next K block's MMAs
-        auto add_span = [&](auto count, int blocks, uint32_t sx, uint32_t sw) {
-          constexpr int kPieces = decltype(count)::value;
-          for (; blocks > 0; --blocks, sx += kScaleStride * 4, sw += 32) {
-            const float row = lds_f32(sx);
-            const float2 w = lds_f32x2(sw);
-            const float sc[2] = {row * w.x, row * w.y};
-            const uint32_t base = wait_sums();
-            if (!ok) return;
-#pragma unroll
-            for (int h = 0; h < 2 * kPieces; ++h) {
-              float r[16];
-              tmem_ld16(base + at[h >> 1] + (h & 1) * 16, r);
-              if (h == 2 * kPieces - 1) free_sums();
-#pragma unroll
-              for (int i = 0; i < 16; i += 2)
-                fma_pair(acc[h >> 1][(h & 1) * 16 + i], acc[h >> 1][(h & 1) * 16 + i + 1], r[i], r[i + 1], sc[h >> 1]);
-            }
-            if (kPieces == 0) free_sums();
-          }
-        };
-        for (int kb = 0; kb < nkb && ok; kb += kScaleSpan, ++spans) {
-          ok = __all_sync(0xffffffffu, mbar_wait_spin(&ctrl->sfull[spans & 1], (uint32_t)(spans >> 1) & 1u, abort));
-          if (!ok) break;
-          const uint32_t scales = smem_u32(sm + P.off_scales) + (spans & 1) * (uint32_t)sizeof(Scales);
-          const uint32_t sx = scales + (quarter * 32 + lane) * 4, sw = scales + kScaleSpan * kScaleStride * 4 + side * 8;
-          const int blocks = min(nkb - kb, kScaleSpan);
-          if (pieces == 2)
-            add_span(std::integral_constant<int, 2>{}, blocks, sx, sw);
-          else if (pieces == 1)
-            add_span(std::integral_constant<int, 1>{}, blocks, sx, sw);
-          else
-            add_span(std::integral_constant<int, 0>{}, blocks, sx, sw);
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&ctrl->sempty[spans & 1]);
-        }
-        if (!ok) break;
-#pragma unroll
-        for (int q = 0; q < (kPaired ? 1 : 2); ++q) {
-          if (q >= mine || !ok) continue;
-          if constexpr (kPaired) {
-            apply_act(acc[0], E.act);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) acc[0][i] *= acc[1][i];
-            put(acc[0], column(0));
-          } else {
-            if (E.bias) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) acc[q][i] += __shfl_sync(0xffffffffu, cb[q], i);
-            }
-            apply_act(acc[q], E.act);
-            put(acc[q], column(q));
-            if (E.tma_res && q + P.sets < mine) ask(column(q + P.sets), m0);
-          }
-        }
-      } else {
-        const uint32_t base = wait_sums() + lanes;
-        if (!ok) break;
-        for (int q = 0; q < mine; ++q) {
+      if (side >= chunks) free_sums();
+      for (int c = side; c < chunks; c += 2) {
           uint32_t rg[32], ru[32];
-          tmem_ld32_start(base + (uint32_t)((side + kSides * q) * 32), rg);
-          tmem_ld32_start(base + (uint32_t)(width + (side + kSides * q) * 32), ru);
+          tmem_ld32_start(base + (uint32_t)(c * 32), rg);
+          tmem_ld32_start(base + (uint32_t)(width + c * 32), ru);
           tmem_ld_wait(rg);
           tmem_ld_bind(ru);
-          if (q + 1 == mine) free_sums();
+          if (c + 2 >= chunks) free_sums();
           float g[32], u[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i) g[i] = __uint_as_float(rg[i]), u[i] = __uint_as_float(ru[i]);
-          const int32_t col = column(q);
+          const int32_t col = n0 + c * 32;
           if constexpr (kMode == kGated) {
             apply_act(g, E.act);
 #pragma unroll
@@ -537,8 +313,7 @@ __global__ void __launch_bounds__(tc_threads(kFp8), 1)
             }
           }
         }
-        if (mine == 0) free_sums();
-      }
+      ++tc;
     }
     if (!ok) {
       for (; E.tma_res && taken < asked; ++taken) await();  // no copy is left in flight
@@ -825,33 +600,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ---------------------------------------------------------------------------------------------
 namespace {
 
-FEpi epilogue_of(const FeedForwardArgs& a) {
-  FEpi e = {a.x_scale, a.w_scale, a.bias, a.residual, a.y, a.N, a.d_out, (a.d_out + 127) / 128, a.act, a.y_bf16, false, false};
-  e.tma_y = a.d_out % (a.y_bf16 ? 8 : 4) == 0 && aligned(a.y, 16) && aligned(a.residual, 16);
-  return e;
-}
-
-int64_t rows_of_w(const FeedForwardArgs& a) { return (int64_t)a.d_out * (a.gated ? 2 : 1); }
-
-int k_blocks(const FeedForwardArgs& a) {
-  return (int)(((int64_t)a.d_in * (a.dtype == MOLORA_E4M3 ? 1 : 2) + kRowBytes - 1) / kRowBytes);
-}
-
-bool operand_map(CUtensorMap* m, const FeedForwardArgs& a, const void* base, int64_t rows, uint32_t box_rows) {
-  const bool fp8 = a.dtype == MOLORA_E4M3;
-  return linear_map(m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, fp8 ? 1 : 2, base,
-                    (uint64_t)rows, (uint64_t)a.d_in, fp8 ? 128 : 64, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
-}
-
 cudaError_t launch_tc(const FeedForwardArgs& a, Mode mode, int BN, cudaStream_t stream) {
-  const bool fp8 = a.dtype == MOLORA_E4M3;
-  FEpi e = epilogue_of(a);
+  FEpi e = ff_epilogue_of(a);
   FPlan p = {};
-  const int width = a.gated ? BN / 2 : BN;
-  p.BN = BN;
-  p.nkb = k_blocks(a);
+  const int width = BN / 2;
   const int64_t m_tiles = (a.N + 2 * kRows - 1) / (2 * kRows), n_tiles = ((int64_t)a.d_out + width - 1) / width;
   if (m_tiles * n_tiles > INT32_MAX / 16) return cudaErrorNotSupported;
+  p.BN = BN;
+  p.nkb = ff_k_blocks(a);
   p.m_tiles = (int32_t)m_tiles;
   p.n_tiles = (int32_t)n_tiles;
   p.tiles = p.m_tiles * p.n_tiles;
@@ -860,57 +616,46 @@ cudaError_t launch_tc(const FeedForwardArgs& a, Mode mode, int BN, cudaStream_t 
   p.stage_bytes = p.off_b + (uint32_t)(BN / 2) * kRowBytes;
   p.tmem_cols = tmem_columns(2 * (uint32_t)(BN <= 64 ? 64 : BN <= 128 ? 128 : 256));
   CUtensorMap mx, mw, my = {}, mr = {};
+  const auto BF = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   auto rows_map = [&](CUtensorMap* m, const void* base) {
-    return linear_map(m, a.y_bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, a.y_bf16 ? 2 : 4, base,
-                      (uint64_t)a.N, (uint64_t)a.d_out, a.y_bf16 ? 32 : 16, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+    return linear_map(m, BF, 2, base, (uint64_t)a.N, (uint64_t)a.d_out, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
   };
   if (mode == kSlopes) {
     const uint64_t half = ((uint64_t)a.d_out + 7) & ~uint64_t(7);
-    if (!linear_map_3d(&my, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.y, {half, 2, (uint64_t)a.N}, {2 * half, 4 * half}, {32, 1, 32},
-                       CU_TENSOR_MAP_SWIZZLE_64B))
+    if (!linear_map_3d(&my, BF, a.y, {half, 2, (uint64_t)a.N}, {2 * half, 4 * half}, {32, 1, 32}, CU_TENSOR_MAP_SWIZZLE_64B))
       return cudaErrorNotSupported;
     e.tma_res = a.d_out % 8 == 0 && aligned(a.residual, 16) && rows_map(&mr, a.residual);
-  } else {
-    if (e.tma_y && (!rows_map(&my, a.y) || (a.residual && !rows_map(&mr, a.residual)))) e.tma_y = false;
-    e.tma_res = e.tma_y && a.residual;
+  } else if (e.tma_y && !rows_map(&my, a.y)) {
+    e.tma_y = false;
   }
-  // boxes that a warp stores from, through which the residual comes too: both chunks of a tile where they are of bf16, so that no
-  // store is waited for (all tiles of a wave end together: with one box, 4800 cycles a tile of 28700); one where they
-  // are of fp32, of which two would leave two stages.  Two more for dh.
-  const int warps = 4 * tc_sides(fp8);
-  p.sets = a.y_bf16 ? 2 : 1;
-  const uint32_t boxes = (uint32_t)(warps * (p.sets + (mode == kSlopes ? 2 : 0)) * (a.y_bf16 ? 1 : 2)) * kBox;
-  static_assert(2 * kBox >= kTurn, "two boxes of bf16, or one of fp32, hold a turned chunk");
-  const size_t scales = fp8 ? 2 * sizeof(Scales) : 0, fixed = boxes + scales + sizeof(FCtrl) + kSmemSlack;
+  const uint32_t boxes = kEpiWarps * (mode == kSlopes ? 4 : 2) * kBox;
+  static_assert(2 * kBox >= kTurn, "a warp's boxes hold a turned chunk");
+  const size_t fixed = boxes + sizeof(FCtrl) + kSmemSlack;
   p.S = (int)((kMaxSmem - fixed) / p.stage_bytes);
   if (p.S > kMaxStages) p.S = kMaxStages;
   p.off_stage = (uint32_t)p.S * p.stage_bytes;
-  p.off_scales = p.off_stage + boxes;
-  p.off_ctrl = p.off_scales + (uint32_t)scales;
+  p.off_ctrl = p.off_stage + boxes;
   // one CTA an SM, alone: an allocation of TMEM never waits for another CTA's (see linear.cu)
   p.smem = kMaxSmem;
-  if (!operand_map(&mx, a, a.x, a.N, kRows) || !operand_map(&mw, a, a.W, rows_of_w(a), (uint32_t)(BN / 2)))
+  if (!ff_operand_map(&mx, a, a.x, a.N, kRows) || !ff_operand_map(&mw, a, a.W, ff_rows_of_w(a), (uint32_t)(BN / 2)))
     return cudaErrorNotSupported;
   auto go = [&](auto kernel, std::atomic<uint64_t>& allowed) {
     const cudaError_t set = allow_smem(kernel, allowed, kMaxSmem);
     if (set != cudaSuccess) return set;
     const int32_t most = num_sms() / 2;
     const dim3 grid((unsigned)(2 * (p.tiles < most ? p.tiles : most)));
-    return launch_kernel(kernel, grid, dim3(tc_threads(fp8)), p.smem, stream, 2, e, p, a.err_word, mx, mw, my, mr);
+    return launch_kernel(kernel, grid, dim3(kThreads), p.smem, stream, 2, e, p, a.err_word, mx, mw, my, mr);
   };
-  static std::atomic<uint64_t> allowed[5];
-  if (mode == kSlopes) return go(ff_tc_kernel<false, kSlopes, true>, allowed[0]);
-  if (!fp8) return go(ff_tc_kernel<false, kGated, true>, allowed[1]);
-  if (a.gated) return go(ff_tc_kernel<true, kGated, true>, allowed[2]);
-  return a.y_bf16 ? go(ff_tc_kernel<true, kLinear, true>, allowed[3]) : go(ff_tc_kernel<true, kLinear, false>, allowed[4]);
+  static std::atomic<uint64_t> allowed[2];
+  return mode == kSlopes ? go(ff_tc_kernel<kSlopes>, allowed[0]) : go(ff_tc_kernel<kGated>, allowed[1]);
 }
 
 cudaError_t launch_skinny(const FeedForwardArgs& a, const Resident& r, int BN, cudaStream_t stream) {
-  const FEpi e = epilogue_of(a);
+  const FEpi e = ff_epilogue_of(a);
   FSkinnyPlan p = {};
   const int width = a.gated ? kRows / 2 : kRows;
   p.BN = BN;
-  p.nkb = k_blocks(a);
+  p.nkb = ff_k_blocks(a);
   p.o_tiles = (int32_t)(((int64_t)a.d_out + width - 1) / width);
   p.t_tiles = (int32_t)((a.N + p.BN - 1) / p.BN);
   const int64_t tiles = (int64_t)p.o_tiles * p.t_tiles;
@@ -930,7 +675,7 @@ cudaError_t launch_skinny(const FeedForwardArgs& a, const Resident& r, int BN, c
   p.smem = (uint32_t)(ring + fixed);
   if (p.smem < 116 * 1024) p.smem = 116 * 1024;  // no two CTAs that could wait for each other's TMEM share an SM (see linear.cu)
   CUtensorMap mx, mw;
-  if (!operand_map(&mx, a, a.x, a.N, (uint32_t)p.BN) || !operand_map(&mw, a, a.W, rows_of_w(a), (uint32_t)width))
+  if (!ff_operand_map(&mx, a, a.x, a.N, (uint32_t)p.BN) || !ff_operand_map(&mw, a, a.W, ff_rows_of_w(a), (uint32_t)width))
     return cudaErrorNotSupported;
   auto go = [&](auto kernel, std::atomic<uint64_t>& allowed) {
     const cudaError_t set = allow_smem(kernel, allowed, kMaxSmem);
@@ -960,8 +705,8 @@ cudaError_t launch_skinny(const FeedForwardArgs& a, const Resident& r, int BN, c
 
 // Cycles that the kernels take in tiles of BN tokens, and of BN rows of W (see linear.cu's).
 int64_t skinny_cycles(const FeedForwardArgs& a, const Resident& r, int BN) {
-  const int64_t tiles = ((rows_of_w(a) + kRows - 1) / kRows) * ((a.N + BN - 1) / BN);
-  const int nkb = k_blocks(a), C = split_of(r, tiles, nkb);
+  const int64_t tiles = ((ff_rows_of_w(a) + kRows - 1) / kRows) * ((a.N + BN - 1) / BN);
+  const int nkb = ff_k_blocks(a), C = split_of(r, tiles, nkb);
   const int64_t waves = (tiles + r.of[C] - 1) / r.of[C];
   return 6500 + waves * ((nkb + C - 1) / C * (420 + BN * 3 / 2) + 48 * BN);
 }
@@ -970,13 +715,14 @@ int64_t tc_cycles(const FeedForwardArgs& a, const Resident& r, int BN) {
   const int width = a.gated ? BN / 2 : BN;
   const int64_t m_tiles = (a.N + 2 * kRows - 1) / (2 * kRows);
   const int64_t tiles = m_tiles * (((int64_t)a.d_out + width - 1) / width), waves = (tiles + r.of[2] - 1) / r.of[2];
-  return 8000 + waves * k_blocks(a) * (2 * BN + 90 > 420 ? 2 * BN + 90 : 420);
+  return 8000 + waves * ff_k_blocks(a) * (2 * BN + 90 > 420 ? 2 * BN + 90 : 420);
 }
 
 // The pairs' tile of the least cost, if that is below `cost`, else 0.
 int best_tc(const FeedForwardArgs& a, const Resident& r, int64_t cost) {
   int best = 0;
   for (int BN : {256, 192, 128, 64}) {
+    if (BN == 64 && a.dtype == MOLORA_E4M3) continue;
     const int64_t c = tc_cycles(a, r, BN);
     if (c < cost) cost = c, best = BN;
   }
@@ -1001,7 +747,8 @@ cudaError_t launch_feed_forward(const FeedForwardArgs& a, cudaStream_t stream) {
   if (const char* g = getenv("MOLORA_FF_SKINNY")) split = atoi(g), cost = split ? 0 : INT64_MAX;
 #endif
   const int pairs = a.N <= 32 && cost < INT64_MAX ? 0 : best_tc(a, r, cost);
-  return pairs ? launch_tc(a, a.gated ? kGated : kLinear, pairs, stream) : launch_skinny(a, r, split, stream);
+  if (!pairs) return launch_skinny(a, r, split, stream);
+  return a.dtype == MOLORA_E4M3 ? launch_blocks_tc(a, pairs, stream) : launch_tc(a, kGated, pairs, stream);
 }
 
 cudaError_t launch_gated_slope(const GatedGradArgs& g, cudaStream_t stream) {

@@ -159,20 +159,21 @@ constexpr size_t kMaxSmem = 227 * 1024;
 constexpr size_t kSmemSlack = 1024;
 constexpr uint32_t kBox = 2048;     // of the epilogue's staging: 32 rows x 64 bytes
 
-__device__ __forceinline__ void apply_act(float (&v)[32], molora_activation act) {
+template <int N>
+__device__ __forceinline__ void apply_act(float (&v)[N], molora_activation act) {
   if (act == MOLORA_ACT_NONE) return;
   if (act == MOLORA_ACT_RELU) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = activate(v[i], MOLORA_ACT_RELU);
+    for (int i = 0; i < N; ++i) v[i] = activate(v[i], MOLORA_ACT_RELU);
   } else if (act == MOLORA_ACT_SILU) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = activate(v[i], MOLORA_ACT_SILU);
+    for (int i = 0; i < N; ++i) v[i] = activate(v[i], MOLORA_ACT_SILU);
   } else if (act == MOLORA_ACT_GELU_TANH) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = activate(v[i], MOLORA_ACT_GELU_TANH);
+    for (int i = 0; i < N; ++i) v[i] = activate(v[i], MOLORA_ACT_GELU_TANH);
   } else {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = activate(v[i], MOLORA_ACT_GELU);
+    for (int i = 0; i < N; ++i) v[i] = activate(v[i], MOLORA_ACT_GELU);
   }
 }
 
