@@ -395,7 +395,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
           if (!kGated && E.tma_res && round + 1 < kOut / kRound) ask(round + 1);
         }
       } else {
-        // rows that are not 16-byte aligned: turned in shared memory, written a row at a time, 8 rows' residuals on their way
+        // rows that are not 16-byte aligned: turned in shared memory, written a row at a time, 16 rows' residuals on their way
         // together
         float* turned = reinterpret_cast<float*>(box);
 #pragma unroll
@@ -407,11 +407,11 @@ __global__ void __launch_bounds__(kThreadsB, 1)
           const int32_t col = column(o) + lane;
           const bool in = there(o) && col < E.d_out;
 #pragma unroll 1
-          for (int q0 = 0; q0 < 32 && m0 + q0 < E.N; q0 += 8) {
-            float add[8];
+          for (int q0 = 0; q0 < 32 && m0 + q0 < E.N; q0 += 16) {
+            float add[16];
             const int64_t to = ((int64_t)m0 + q0) * E.d_out + col;
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
+            for (int q = 0; q < 16; ++q) {
               add[q] = 0.f;
               if (!kGated && E.res && in && m0 + q0 + q < E.N) {
                 if constexpr (kY16)
@@ -421,7 +421,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
               }
             }
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
+            for (int q = 0; q < 16; ++q) {
               if (!in || m0 + q0 + q >= E.N) continue;
               const float v = turned[(q0 + q) * 32 + (lane ^ (q0 + q))] + add[q];
               if constexpr (kY16)
