@@ -278,11 +278,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else {  // rows of dh that start anywhere: a lane a column, turned into the same box
               __syncwarp();
               const __nv_bfloat16* dh = static_cast<const __nv_bfloat16*>(E.res) + (int64_t)m0 * E.d_out + col + lane;
-#pragma unroll 8
-              for (int r = 0; r < 32; ++r) {
-                const bool in = m0 + r < E.N && col + lane < E.d_out;
-                *reinterpret_cast<__nv_bfloat16*>(box + swz_offset((uint32_t)r, (uint32_t)lane >> 3, 64) + (lane & 7) * 2) =
-                    in ? dh[(int64_t)r * E.d_out] : __float2bfloat16_rn(0.f);
+              const bool in = col + lane < E.d_out;
+#pragma unroll
+              for (int r0 = 0; r0 < 32; r0 += 16) {  // (loads before stores: these could be to the same memory)
+                __nv_bfloat16 v[16];
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                  v[r] = in && m0 + r0 + r < E.N ? dh[(int64_t)(r0 + r) * E.d_out] : __float2bfloat16_rn(0.f);
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                  *reinterpret_cast<__nv_bfloat16*>(box + swz_offset((uint32_t)(r0 + r), (uint32_t)lane >> 3, 64) + (lane & 7) * 2) = v[r];
               }
               __syncwarp();
             }
