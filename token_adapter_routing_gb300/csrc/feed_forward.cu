@@ -218,7 +218,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     const uint32_t tempty = dsmem_addr(smem_u32(&ctrl->tempty[0]), 0);
     bool ok = true;
-    for (int32_t pt = pair; pt < P.tiles && ok; pt += pairs) {
+    int32_t pt = pair;
+    for (; pt < P.tiles && ok; pt += ok ? pairs : 0) {
       int32_t m0, n0;
       tile_at(pt, m0, n0);
       m0 += quarter * 32;
@@ -256,74 +257,93 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       if (side >= chunks) free_sums();
       for (int c = side; c < chunks; c += 2) {
-          uint32_t rg[32], ru[32];
-          tmem_ld32_start(base + (uint32_t)(c * 32), rg);
-          tmem_ld32_start(base + (uint32_t)(width + c * 32), ru);
-          tmem_ld_wait(rg);
-          tmem_ld_bind(ru);
-          if (c + 2 >= chunks) free_sums();
-          float g[32], u[32];
+        uint32_t rg[32], ru[32];
+        tmem_ld32_start(base + (uint32_t)(c * 32), rg);
+        tmem_ld32_start(base + (uint32_t)(width + c * 32), ru);
+        tmem_ld_wait(rg);
+        tmem_ld_bind(ru);
+        if (c + 2 >= chunks) free_sums();
+        float g[32], u[32];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) g[i] = __uint_as_float(rg[i]), u[i] = __uint_as_float(ru[i]);
-          const int32_t col = n0 + c * 32;
-          if constexpr (kMode == kGated) {
-            apply_act(g, E.act);
+        for (int i = 0; i < 32; ++i) g[i] = __uint_as_float(rg[i]), u[i] = __uint_as_float(ru[i]);
+        const int32_t col = n0 + c * 32;
+        if constexpr (kMode == kGated) {
+          apply_act(g, E.act);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) g[i] *= u[i];
-            put(g, col);
-          } else {
-            uint8_t* box = in_box(taken);
-            if (E.tma_res) {
-              if (!(ok = await())) break;
-            } else {  // rows of dh that start anywhere: a lane a column, turned into the same box
-              __syncwarp();
-              const __nv_bfloat16* dh = static_cast<const __nv_bfloat16*>(E.res) + (int64_t)m0 * E.d_out + col + lane;
-              const bool in = col + lane < E.d_out;
+          for (int i = 0; i < 32; ++i) g[i] *= u[i];
+          put(g, col);
+        } else {
+          uint8_t* box = in_box(taken);
+          if (E.tma_res) {
+            if (!(ok = await())) break;
+          } else {  // rows of dh that start anywhere: a lane a column, turned into the same box
+            __syncwarp();
+            const __nv_bfloat16* dh = static_cast<const __nv_bfloat16*>(E.res) + (int64_t)m0 * E.d_out + col + lane;
+            const bool in = col + lane < E.d_out;
 #pragma unroll
-              for (int r0 = 0; r0 < 32; r0 += 16) {  // (loads before stores: these could be to the same memory)
-                __nv_bfloat16 v[16];
+            for (int r0 = 0; r0 < 32; r0 += 16) {  // (loads before stores: these could be to the same memory)
+              __nv_bfloat16 v[16];
 #pragma unroll
-                for (int r = 0; r < 16; ++r)
-                  v[r] = in && m0 + r0 + r < E.N ? dh[(int64_t)(r0 + r) * E.d_out] : __float2bfloat16_rn(0.f);
+              for (int r = 0; r < 16; ++r)
+                v[r] = in && m0 + r0 + r < E.N ? dh[(int64_t)(r0 + r) * E.d_out] : __float2bfloat16_rn(0.f);
 #pragma unroll
-                for (int r = 0; r < 16; ++r)
-                  *reinterpret_cast<__nv_bfloat16*>(box + swz_offset((uint32_t)(r0 + r), (uint32_t)lane >> 3, 64) + (lane & 7) * 2) = v[r];
-              }
-              __syncwarp();
+              for (int r = 0; r < 16; ++r)
+                *reinterpret_cast<__nv_bfloat16*>(box + swz_offset((uint32_t)(r0 + r), (uint32_t)lane >> 3, 64) + (lane & 7) * 2) = v[r];
             }
+            __syncwarp();
+          }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint4 d = *reinterpret_cast<const uint4*>(piece(box, i));
-              const uint32_t w[4] = {d.x, d.y, d.z, d.w};
+          for (int i = 0; i < 4; ++i) {
+            const uint4 d = *reinterpret_cast<const uint4*>(piece(box, i));
+            const uint32_t w[4] = {d.x, d.y, d.z, d.w};
 #pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                const float dh = __uint_as_float(j & 1 ? w[j / 2] & 0xffff0000u : w[j / 2] << 16);
-                float a, s;
-                act_and_slope(g[8 * i + j], E.act, a, s);
-                g[8 * i + j] = dh * u[8 * i + j] * s;
-                u[8 * i + j] = dh * a;
-              }
-            }
-            ++taken;
-            if (!E.tma_res) ++asked;
-            const uint8_t* from = stage(g);  // (after its __syncwarp every lane has read dh's box)
-            if (lane == 0) {
-              tma_store_3d(&map_y, smem_u32(from), col, 0, m0);
-              bulk_commit();
-            }
-            from = stage(u);
-            if (lane == 0) {
-              tma_store_3d(&map_y, smem_u32(from), col, 1, m0);
-              bulk_commit();
+            for (int j = 0; j < 8; ++j) {
+              const float dh = __uint_as_float(j & 1 ? w[j / 2] & 0xffff0000u : w[j / 2] << 16);
+              float a, s;
+              act_and_slope(g[8 * i + j], E.act, a, s);
+              g[8 * i + j] = dh * u[8 * i + j] * s;
+              u[8 * i + j] = dh * a;
             }
           }
+          ++taken;
+          if (!E.tma_res) ++asked;
+          const uint8_t* from = stage(g);  // (after its __syncwarp every lane has read dh's box)
+          if (lane == 0) {
+            tma_store_3d(&map_y, smem_u32(from), col, 0, m0);
+            bulk_commit();
+          }
+          from = stage(u);
+          if (lane == 0) {
+            tma_store_3d(&map_y, smem_u32(from), col, 1, m0);
+            bulk_commit();
+          }
         }
+      }
       ++tc;
     }
     if (!ok) {
       for (; E.tma_res && taken < asked; ++taken) await();  // no copy is left in flight
       *abort = 1;
       if (lane == 0) report(err_word, MOLORA_DEV_WAIT_TIMEOUT);
+      if constexpr (kMode == kSlopes) {
+        // what is lost of dproj is NaN, and so is what the products after this kernel make of it
+        float lost[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) lost[i] = __uint_as_float(0x7fffffffu);
+        for (; pt < P.tiles; pt += pairs) {
+          int32_t m0, n0;
+          tile_at(pt, m0, n0);
+          m0 += quarter * 32;
+          for (int c = side; m0 < E.N && c < width / 32 && n0 + c * 32 < E.d_out; c += 2) {
+            const uint8_t* from = stage(lost);
+            if (lane == 0) {
+              tma_store_3d(&map_y, smem_u32(from), n0 + c * 32, 0, m0);
+              tma_store_3d(&map_y, smem_u32(from), n0 + c * 32, 1, m0);
+              bulk_commit();
+            }
+          }
+        }
+      }
     }
     if (lane == 0) bulk_wait_all();
     __syncwarp();
@@ -708,19 +728,24 @@ cudaError_t launch_skinny(const FeedForwardArgs& a, const Resident& r, int BN, c
   }
 }
 
-// Cycles that the kernels take in tiles of BN tokens, and of BN rows of W (see linear.cu's).
+// Cycles that ff_skinny_kernel takes in tiles of BN tokens, and the pairs' kernels in tiles of BN rows of W: what a K block takes,
+// what ends a tile, and the way through.  Fitted to 130 sizes on GB300 (1 to 2048 tokens, d_in 1024 to 4096, 1024 to 12288
+// rows of W): the choice is 0.6% off the fastest on average, 14% at most.  With e4m3 a K block of many tokens takes
+// long, as its sums are scaled: 200 tokens of 1024 -> 1024 gated 6.1 us in tiles of 32, 7.7 in tiles of 128.
 int64_t skinny_cycles(const FeedForwardArgs& a, const Resident& r, int BN) {
   const int64_t tiles = ((ff_rows_of_w(a) + kRows - 1) / kRows) * ((a.N + BN - 1) / BN);
   const int nkb = ff_k_blocks(a), C = split_of(r, tiles, nkb);
-  const int64_t waves = (tiles + r.of[C] - 1) / r.of[C];
-  return 6500 + waves * ((nkb + C - 1) / C * (420 + BN * 3 / 2) + 48 * BN);
+  const int64_t waves = (tiles + r.of[C] - 1) / r.of[C], blocks = (nkb + C - 1) / C;
+  if (a.dtype == MOLORA_E4M3) return 4000 + waves * (blocks * (450 + 5 * BN) + 60 * BN);
+  return 6600 + waves * (blocks * (730 + BN * 3 / 5) + 38 * BN);
 }
 
 int64_t tc_cycles(const FeedForwardArgs& a, const Resident& r, int BN) {
   const int width = a.gated ? BN / 2 : BN;
   const int64_t m_tiles = (a.N + 2 * kRows - 1) / (2 * kRows);
   const int64_t tiles = m_tiles * (((int64_t)a.d_out + width - 1) / width), waves = (tiles + r.of[2] - 1) / r.of[2];
-  return 8000 + waves * ff_k_blocks(a) * (2 * BN + 90 > 420 ? 2 * BN + 90 : 420);
+  if (a.dtype == MOLORA_E4M3) return 9200 + waves * (ff_k_blocks(a) * (200 + BN * 33 / 20) + 5400);
+  return 6300 + waves * (ff_k_blocks(a) * (160 + BN * 8 / 5) + 450);
 }
 
 // The pairs' tile of the least cost, if that is below `cost`, else 0.
