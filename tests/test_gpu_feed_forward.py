@@ -558,3 +558,80 @@ def test_adapters_train_through_a_frozen_block(m):
         t.record_stream(torch.cuda.current_stream())
     want, _, _ = m.molora_gated_linear_backward(x, W, dh)
     assert dW is None and torch.equal(dx, want)
+
+
+@pytest.mark.parametrize("kind", ["quantise", "blocks", "gated", "gated_fp8", "backward"])
+def test_offsets_past_32_bits(m, kind):
+    """Outputs (and, of the quantiser, inputs) of more than 2^31 elements: the first, the middle and the last rows."""
+    g = gen(50)
+    rows = lambda N: torch.tensor([0, 1, N // 2 - 1, N // 2, N // 2 + 1, N - 2, N - 1], device="cuda")  # noqa: E731
+    if kind == "quantise":
+        N, d = 530000, 4096
+        x = torch.zeros(N, d, dtype=BF, device="cuda")
+        at = rows(N)
+        x[at] = randn(g, 7, d).to(BF)
+        out8, scale8 = m.molora_quantise_blocks(x)
+        a, b = m.molora_quantise_blocks(x[at].contiguous())
+        assert torch.equal(out8[at].view(torch.uint8), a.view(torch.uint8)) and torch.equal(scale8[at], b)
+        return
+    if kind == "backward":
+        N, d, F = 280000, 64, 4096
+        x, _, W, _ = gated_inputs(g, BF, N, d, F)
+        dh = torch.zeros(N, F, dtype=BF, device="cuda")
+        at = rows(N)
+        dh[at] = randn(g, 7, F).to(BF)
+        dx, dW, dproj = m.molora_gated_linear_backward(x, W, dh)
+        a, b, c = m.molora_gated_linear_backward(x[at].contiguous(), W, dh[at].contiguous())
+        assert torch.equal(dx[at], a) and torch.equal(dproj[at], c) and (dx[2:1000] == 0).all()
+        within(dW, b.double(), 2 * (b.double().abs() * HALF[BF]) + 2.0 ** -20)  # (the same 7 terms, in two orders of additions)
+        return
+    N, d, F = 530000, 128, 4096
+    if kind == "blocks":
+        x, sx = e4m3(g, N, d, N)
+        W, sw = e4m3(g, F, d, blocks(F))
+        run = lambda i: m.molora_linear_blocks(x[i].contiguous(), sx[i].contiguous(), W, sw, out_dtype=BF)  # noqa: E731
+    else:
+        x, sx, W, sw = gated_inputs(g, FP8 if kind == "gated_fp8" else BF, N, d, F)
+        run = lambda i: m.molora_gated_linear(x[i].contiguous(), W, x_scale=None if sx is None else sx[i].contiguous(), w_scale=sw)  # noqa: E731
+    y = run(slice(None))
+    few = run(rows(N))
+    # (few and many tokens take other kernels: sums in another order, and a rounding of either)
+    within(y[rows(N)], few.double(), few.double().abs() * 2 * HALF[BF] + 2.0 ** -10 * few.double().abs().mean())
+
+
+def test_two_streams_and_two_graphs_at_once(m):
+    """Calls on two streams at once, and two captured graphs of them replayed in turn, keep to their own buffers."""
+    g = gen(60)
+    jobs = []
+    for N in (2000, 1100):
+        x, sx = e4m3(g, N, 512, N)
+        W, sw = e4m3(g, 1024, 512, 8)
+        b, _, V, _ = gated_inputs(g, BF, N, 256, 768)
+        dh = randn(g, N, 768).to(BF)
+
+        def run(x=x, sx=sx, W=W, sw=sw, b=b, V=V, dh=dh):
+            return [m.molora_linear_blocks(x, sx, W, sw), m.molora_gated_linear(b, V), *m.molora_gated_linear_backward(b, V, dh)]
+        jobs.append(run)
+    want = [run() for run in jobs]
+    streams = [torch.cuda.Stream() for _ in jobs]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = []
+        for s, run in zip(streams, jobs):
+            with torch.cuda.stream(s):
+                got.append(run())
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for w, v in zip(want, got) for a, b in zip(w, v))
+    graphs = []
+    for run in jobs:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = run()
+        graphs.append((graph, out))
+    for _ in range(2):
+        for graph, out in graphs:
+            for t in out:
+                t.zero_()
+            graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for w, (_, v) in zip(want, graphs) for a, b in zip(w, v))

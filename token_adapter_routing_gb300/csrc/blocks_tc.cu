@@ -1,17 +1,21 @@
 // blocks_tc.cu -- many tokens times weights in e4m3, with scales for each block of 128: molora_linear_blocks, and
 // molora_gated_linear's e4m3 form (see feed_forward.cu).
 //
-// Scales change with every K block of 128, so an accumulator in TMEM holds one K block and the epilogue warps add it,
-// scaled, to sums in fp32 registers while the next one's MMAs run.  That takes one fma an element and K block beside the
-// tensor cores' 128 multiply-adds: 256 cycles of a scheduler's pipe, in pairs half as many instructions, against the
-// 512 cycles of the MMAs, and everything else in the loop competes with it.  What it came down to, by what it cost
-// (8192 x 4096 -> 4096 in us, one after the other):
-//   * giving an accumulator back without a release: 331 -> 218 (a cluster-wide one waits for every load in flight)
-//   * four epilogue warps a scheduler instead of two, x's scales gathered ahead into shared memory by two warps of their
-//     own (they lie token by token: 32 lines of L1 a warp and K block), registers enough for the MMA warp: 218 -> 129
-//   * the loop's few instructions (addresses that flip by xor, one vote a wait, fmas in pairs): 129 -> 123
-//   * accumulators made, read and given back in halves of 128 columns, so that the next K block's first half is on
-//     the tensor cores while this one's second half is read, and a tile's outputs leaving together: TODO
+// A persistent kernel of CTA pairs as linear_tc_kernel (linear.cu) is.  Scales change with every K block of 128, so an
+// accumulator in TMEM holds one K block, and the epilogue warps add it, scaled, to sums in fp32 registers while the next
+// one's MMAs run.  That is one fma an element and K block, 280 cycles an SM, and as much again to read TMEM, against the
+// 512 cycles of the MMAs: it fits beside them only if little else is done, and what is done one after the other (a wait,
+// a load, the sums, a hand-back: 800 to 900 cycles now) is what bounds the kernel.  What it came down to, in us at
+// 8192 x 4096 -> 4096 bf16 y:
+//   * accumulators given back without a release, which waits for every load in flight: 331 -> 218
+//   * x's scales gathered ahead into shared memory by two warps of their own (they lie token by token, 32 lines of L1 a
+//     warp and K block), registers enough for the warp that issues the MMAs: 218 -> 129
+//   * few instructions in the loop (addresses that flip by xor, one vote a wait, fmas in pairs), loads of 32 columns
+//     with the next under way, a box for every piece a tile's outputs leave by: 129 -> 121 (110 without a residual)
+// A product without scales takes 76: the finishing of a tile (1.1 to 2 us, under which the next tile's first two K
+// blocks run, then the tensor cores wait) and the chain above are the difference.
+// Tried and left: four warps a scheduler with half the sums each (126); accumulators in halves of 128 columns, which the
+// tensor cores make less quickly (141); the next K block's first load before the last sums (more registers than there are).
 #include <cudaTypedefs.h>
 
 #include <atomic>
@@ -74,6 +78,26 @@ template <bool kGated>
 __device__ __forceinline__ int pieces_of(const BPlan& P, int side) {
   const int chunks = P.BN / (kGated ? 64 : 32);
   return (chunks - side + kSides - 1) / kSides * (kGated ? 2 : 1);
+}
+
+// SiLU, and the tanh form of GELU, of 32 values (see activate) with one reciprocal for two: 1 / a = b / (a b).  A tile's
+// activations are not under any MMA here, and their powers and reciprocals are what bounds them (gated 4096 x 2048 ->
+// 6144 96.0 -> 93.9 us).  Where 1 + 2^z passes 2^60 its reciprocal counts as 0, so that no product overflows.
+__device__ __forceinline__ void activate_pairs(float (&v)[32], bool silu) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 2) {
+    float z[2], d[2], r;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const float x = v[i + j];
+      z[j] = silu ? -1.4426950408889634f * x : x * fmaf(-0.10294324f * x, x, -2.3022082f);
+      asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(d[j]) : "f"(fminf(z[j], 60.f)));
+      d[j] += 1.f;
+    }
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d[0] * d[1]));
+    v[i] *= z[0] > 60.f ? 0.f : r * d[1];
+    v[i + 1] *= z[1] > 60.f ? 0.f : r * d[0];
+  }
 }
 
 }  // namespace
@@ -322,7 +346,12 @@ __global__ void __launch_bounds__(kThreadsB, 1)
       if constexpr (kGated) {
 #pragma unroll
         for (int o = 0; o < 2; ++o) {
-          apply_act(acc[2 * o], E.act);
+          if (E.act == MOLORA_ACT_SILU)
+            activate_pairs(acc[2 * o], true);
+          else if (E.act == MOLORA_ACT_GELU_TANH)
+            activate_pairs(acc[2 * o], false);
+          else
+            apply_act(acc[2 * o], E.act);
 #pragma unroll
           for (int i = 0; i < 32; ++i) acc[o][i] = acc[2 * o][i] * acc[2 * o + 1][i];
         }

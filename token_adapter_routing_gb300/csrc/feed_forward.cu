@@ -327,20 +327,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) report(err_word, MOLORA_DEV_WAIT_TIMEOUT);
       if constexpr (kMode == kSlopes) {
         // what is lost of dproj is NaN, and so is what the products after this kernel make of it
-        float lost[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) lost[i] = __uint_as_float(0x7fffffffu);
-        for (; pt < P.tiles; pt += pairs) {
+        if (lane == 0) bulk_wait_read<0>();
+        __syncwarp();
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<uint4*>(piece(ring, i)) = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
+        fence_proxy_async_smem();
+        __syncwarp();
+#pragma unroll 1
+        for (; pt < P.tiles && lane == 0; pt += pairs) {
           int32_t m0, n0;
           tile_at(pt, m0, n0);
           m0 += quarter * 32;
+#pragma unroll 1
           for (int c = side; m0 < E.N && c < width / 32 && n0 + c * 32 < E.d_out; c += 2) {
-            const uint8_t* from = stage(lost);
-            if (lane == 0) {
-              tma_store_3d(&map_y, smem_u32(from), n0 + c * 32, 0, m0);
-              tma_store_3d(&map_y, smem_u32(from), n0 + c * 32, 1, m0);
-              bulk_commit();
-            }
+            tma_store_3d(&map_y, smem_u32(ring), n0 + c * 32, 0, m0);
+            tma_store_3d(&map_y, smem_u32(ring), n0 + c * 32, 1, m0);
+            bulk_commit();
           }
         }
       }

@@ -36,15 +36,18 @@ struct __align__(8) GCtrl {
   int32_t abort;
 };
 
-// The tiles: dx's first (their sums are the longest), then dW's, gate and up rows in turn.
+// dx's tiles (the longer sums, where N < 2 d_ff) go round the pairs, then dW's: as many of them to each pair that is a tile
+// of dx short as take no longer than one, the rest round the pairs again, these first.
 struct GPlan {
   int BN;                    // columns a tile
   int S;
-  int64_t tiles_x, tiles;    // dx's, all
+  int64_t tiles_x, tiles_w;  // dx's, dW's (gate and up rows)
   int32_t n_tiles;           // tiles across d_in
   int64_t m_tiles_x, m_tiles_w;  // down N, down d_ff
   int32_t kb_half, kb_x, kb_w;   // K blocks of 64: of one projection, of a tile of dx, of one of dW
   int32_t group;
+  int32_t pairs;             // of CTAs
+  int32_t full, ahead;       // pairs with one tile of dx more than the others, and dW's tiles that the others get first
   int64_t N;
   int32_t d_in, d_ff;
   uint32_t stage_bytes, off_stage, off_ctrl, tmem_cols;
@@ -57,10 +60,24 @@ struct GTile {
   int32_t kbs;
 };
 
-__device__ __forceinline__ GTile tile_at(const GPlan& P, int64_t i, uint32_t rank) {
-  GTile t;
-  t.x = i < P.tiles_x;
-  if (!t.x) i -= P.tiles_x;
+// The j-th tile of a pair; false if it has no more.
+__device__ __forceinline__ bool tile_at(const GPlan& P, int32_t pair, int64_t j, uint32_t rank, GTile& t) {
+  const bool full = pair < P.full;
+  const int64_t mine = P.tiles_x / P.pairs + full;
+  t.x = j < mine;
+  int64_t i;
+  if (t.x) {
+    i = pair + j * P.pairs;
+  } else {
+    j -= mine;
+    if (!full && j < P.ahead) {
+      i = (int64_t)(pair - P.full) * P.ahead + j;
+    } else {
+      if (!full) j -= P.ahead;
+      i = (int64_t)(P.pairs - P.full) * P.ahead + (full ? pair + P.pairs : pair) - P.full + j * P.pairs;
+    }
+    if (i >= P.tiles_w) return false;
+  }
   const int64_t m_tiles = t.x ? P.m_tiles_x : 2 * P.m_tiles_w;
   // groups of row tiles that share the other operand's columns in L2: within one the row tile runs fastest
   const int64_t span = (int64_t)P.group * P.n_tiles, grp = i / span;
@@ -72,7 +89,7 @@ __device__ __forceinline__ GTile tile_at(const GPlan& P, int64_t i, uint32_t ran
   t.m0 = (int32_t)(m * 2 * kRows + rank * kRows);
   t.n0 = (int32_t)(in / rows) * P.BN;
   t.kbs = t.x ? P.kb_x : P.kb_w;
-  return t;
+  return true;
 }
 
 // The MMAs of one stage, as umma_stage, with the 16-byte units between the steps of A too.
@@ -111,7 +128,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int BN = P.BN, S = P.S;
   const uint32_t rank = cluster_ctarank();
   const uint16_t both = 0x3;
-  const int64_t pair = blockIdx.x / 2, pairs = gridDim.x / 2;
+  const int32_t pair = blockIdx.x / 2;
   volatile int32_t* abort = &ctrl->abort;
 
   if (warp == kEpiWarps + 1) {
@@ -135,7 +152,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tma_prefetch_desc(&map_w);
       tma_prefetch_desc(&map_dx);
     }
-    if (P.tiles > P.tiles_x) {
+    if (P.tiles_w) {
       tma_prefetch_desc(&map_pm);
       tma_prefetch_desc(&map_x);
       tma_prefetch_desc(&map_dw);
@@ -154,8 +171,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       int s = 0, issued = 0;
       uint32_t phase = 1;  // the first use of a stage finds it empty
       bool ok = true;
-      for (int64_t i = pair; i < P.tiles && ok; i += pairs) {
-        const GTile t = tile_at(P, i, rank);
+      GTile t;
+      for (int64_t i = 0; ok && tile_at(P, pair, i, rank, t); ++i) {
         const CUtensorMap* map_b = t.x ? &map_w : &map_x;
         const int32_t n = t.n0 + (int32_t)rank * (BN / 2);
         for (int kb = 0; kb < t.kbs; ++kb) {
@@ -201,8 +218,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       int s = 0, tc = 0;
       uint32_t phase = 0;
       bool ok = true;
-      for (int64_t i = pair; i < P.tiles && ok; i += pairs, ++tc) {
-        const GTile t = tile_at(P, i, rank);
+      GTile t;
+      for (; ok && tile_at(P, pair, tc, rank, t); ++tc) {
         const uint32_t idesc = idesc_bf16_f32(2 * kRows, (uint32_t)BN, !t.x, true);
         const uint32_t a_lo = t.x ? k_lo : m_lo, a_step = t.x ? 2 : 16 * kRowBytes / 16;
         const int buf = tc & 1;
@@ -236,8 +253,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* ring = sm + P.off_stage + (size_t)warp * kSets * kBox;
     int tc = 0, used = 0;
     bool ok = true;
-    for (int64_t i = pair; i < P.tiles && ok; i += pairs) {
-      const GTile t = tile_at(P, i, rank);
+    GTile t;
+    for (int64_t i = 0; ok && tile_at(P, pair, i, rank, t); ++i) {
       const int32_t row = t.m0 + quarter * 32;
       const int64_t rows = t.x ? P.N : P.d_ff;
       const int chunks = row < rows ? min(BN / 32, (P.d_in - t.n0 + 31) / 32) : 0;
@@ -306,15 +323,27 @@ cudaError_t launch_gated_grad(const GatedGradArgs& a, cudaStream_t stream) {
   p.kb_x = 2 * p.kb_half;
   p.kb_w = (int32_t)((N + 63) / 64);
   p.group = 8;
-  const int64_t pairs = resident_clusters().of[2];
+  const int64_t most = num_sms() / 2;
+  // The wider tiles where they are over first: a K block of a tile takes 600 cycles at 256 columns, 420 at 128.
+  // Returns those of the longest pair.
   auto plan = [&](int BN) {
     p.BN = BN;
     p.n_tiles = (int32_t)(((int64_t)a.d_in + BN - 1) / BN);
     p.tiles_x = a.dx ? p.m_tiles_x * p.n_tiles : 0;
-    p.tiles = p.tiles_x + (a.dW ? 2 * p.m_tiles_w * p.n_tiles : 0);
+    p.tiles_w = a.dW ? 2 * p.m_tiles_w * p.n_tiles : 0;
+    const int64_t tiles = p.tiles_x + p.tiles_w;
+    p.pairs = (int32_t)(tiles < most ? tiles : most);
+    p.full = (int32_t)(p.tiles_x % p.pairs);
+    const int64_t others = p.pairs - p.full, long_as = p.kb_x / p.kb_w, share = p.tiles_w / others;
+    p.ahead = p.full ? (int32_t)(long_as < share ? long_as : share) : 0;
+    const int64_t rest = p.tiles_w - others * p.ahead, extra = rest % p.pairs;
+    const int64_t all = p.tiles_x / p.pairs * p.kb_x + rest / p.pairs * p.kb_w;
+    const int64_t of_full = p.full ? all + p.kb_x + (extra > others ? p.kb_w : 0) : 0;
+    const int64_t of_others = all + (int64_t)p.ahead * p.kb_w + (extra ? p.kb_w : 0);
+    return (of_full > of_others ? of_full : of_others) * (BN == 256 ? 600 : 420);
   };
-  plan(256);
-  if (p.tiles < pairs) plan(128);
+  const int64_t narrow = plan(128);
+  if (plan(256) > narrow) plan(128);
   p.stage_bytes = kStageA + (uint32_t)(p.BN / 128) * kAtom;
   const uint32_t boxes = kEpiWarps * kSets * kBox;
   p.S = (int)((kMaxSmem - boxes - sizeof(GCtrl) - kSmemSlack) / p.stage_bytes);
@@ -336,8 +365,7 @@ cudaError_t launch_gated_grad(const GatedGradArgs& a, cudaStream_t stream) {
   static std::atomic<uint64_t> allowed;
   const cudaError_t set = allow_smem(grad_tc_kernel, allowed, kMaxSmem);
   if (set != cudaSuccess) return set;
-  const int64_t most = num_sms() / 2;
-  const dim3 grid((unsigned)(2 * (p.tiles < most ? p.tiles : most)));
+  const dim3 grid((unsigned)(2 * p.pairs));
   // one CTA an SM, alone: an allocation of TMEM never waits for another CTA's (see linear.cu)
   return launch_kernel(grad_tc_kernel, grid, dim3(kThreads), kMaxSmem, stream, 2, p, a.err_word, pk, pm, w, x, dx, dw);
 }
