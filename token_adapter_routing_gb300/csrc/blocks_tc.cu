@@ -11,11 +11,13 @@
 //   * x's scales gathered ahead into shared memory by two warps of their own (they lie token by token, 32 lines of L1 a
 //     warp and K block), registers enough for the warp that issues the MMAs: 218 -> 129
 //   * few instructions in the loop (addresses that flip by xor, one vote a wait, fmas in pairs), loads of 32 columns
-//     with the next under way, a box for every piece a tile's outputs leave by: 129 -> 121 (110 without a residual)
-// A product without scales takes 76: the finishing of a tile (1.1 to 2 us, under which the next tile's first two K
+//     with the next under way, a box for every piece a tile's outputs leave by: 129 -> 121
+//   * no register spilled (a piece's columns by a constant offset, not a table): 121 -> 112 (103 without a residual)
+// A product without scales takes 76: the finishing of a tile (1 to 2 us, under which the next tile's first two K
 // blocks run, then the tensor cores wait) and the chain above are the difference.
 // Tried and left: four warps a scheduler with half the sums each (126); accumulators in halves of 128 columns, which the
-// tensor cores make less quickly (141); the next K block's first load before the last sums (more registers than there are).
+// tensor cores make less quickly (141); loads of 64 columns (118), the next K block's scales, or the look whether it is
+// there, before the last sums (123, 131: more registers than there are); the residual asked for in mid-tile (115).
 #include <cudaTypedefs.h>
 
 #include <atomic>
@@ -63,21 +65,15 @@ struct BPlan {
   uint32_t stage_bytes, off_b, off_stage, off_scales, off_ctrl, tmem_cols, smem;
 };
 
-// The h-th piece of 32 columns of a side's warps: its columns of TMEM, and of the outputs (from the tile's first).  Gated,
-// pieces come in pairs, of the gate's rows of W and the up projection's.
+// The h-th piece of 32 columns of a side's warps: its columns of TMEM from the side's first (side * 32), and of the outputs from
+// the tile's first.  Gated, pieces come in pairs, of the gate's rows of W and the up projection's.
 template <bool kGated>
-__device__ __forceinline__ int piece_column(const BPlan& P, int side, int h) {
-  return kGated ? (h & 1) * (P.BN / 2) + (side + kSides * (h >> 1)) * 32 : (side + kSides * h) * 32;
+__device__ __forceinline__ uint32_t piece_column(const BPlan& P, int h) {
+  return kGated ? (h & 1) * ((uint32_t)P.BN / 2) + (h >> 1) * kSides * 32 : h * kSides * 32;
 }
 template <bool kGated>
 __device__ __forceinline__ int piece_output(int side, int h) {
   return (side + kSides * (kGated ? h >> 1 : h)) * 32;
-}
-// How many pieces a side has.
-template <bool kGated>
-__device__ __forceinline__ int pieces_of(const BPlan& P, int side) {
-  const int chunks = P.BN / (kGated ? 64 : 32);
-  return (chunks - side + kSides - 1) / kSides * (kGated ? 2 : 1);
 }
 
 // SiLU, and the tanh form of GELU, of 32 values (see activate) with one reciprocal for two: 1 / a = b / (a b).  A tile's
@@ -255,10 +251,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     const int quarter = warp & 3, side = warp >> 2;
     uint8_t* box = sm + P.off_stage + (size_t)warp * P.box;
     const uint32_t tempty = dsmem_addr(smem_u32(&ctrl->tempty[0]), 0), tfull = smem_u32(&ctrl->tfull[0]);
-    const int pieces = pieces_of<kGated>(P, side);
-    uint32_t at[4];
-#pragma unroll
-    for (int h = 0; h < 4; ++h) at[h] = ((uint32_t)(quarter * 32) << 16) + (uint32_t)piece_column<kGated>(P, side, h);
+    const uint32_t first = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)side * 32;  // this warp's columns of an accumulator
     int tc = 0, spans = 0;     // accumulators, and spans of scales, done with
     int asked = 0, taken = 0;  // rounds of the residual on their way or taken, and taken
     bool ok = true;
@@ -268,7 +261,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
       m0 += quarter * 32;
       // output piece o's first column; it is the outputs' where that is below d_out, in the tile and for rows that are there
       auto column = [&](int o) { return n0 + piece_output<kGated>(side, kGated ? 2 * o : o); };
-      auto there = [&](int o) { return o < (kGated ? pieces / 2 : pieces) && column(o) < E.d_out && m0 < E.N; };
+      auto there = [&](int o) { return column(o) < n0 + width && column(o) < E.d_out && m0 < E.N; };
       // the residual's pieces of a round come into the boxes that the outputs' leave from
       auto ask = [&](int round) {
         if (lane == 0) {
@@ -296,7 +289,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         constexpr int kPieces = decltype(count)::value;
         uint32_t buf = (uint32_t)tc & 1u, parity = (uint32_t)(tc >> 1) & 1u;
         const uint32_t flip = P.tmem_cols / 2;
-        uint32_t from = tmem + buf * flip, full_at = tfull + buf * 8, free_at = tempty + buf * 8;
+        uint32_t from = first + buf * flip, full_at = tfull + buf * 8, free_at = tempty + buf * 8;
         tc += blocks;
         for (; blocks > 0; --blocks, sx += kScaleStride * 4, sw += 32) {
           const float row = lds_f32(sx);
@@ -308,12 +301,12 @@ __global__ void __launch_bounds__(kThreadsB, 1)
           tc_fence_after();
           // a piece is on its way from TMEM while the one before it is added
           uint32_t r[2][32];
-          tmem_ld32_start(from + at[0], r[0]);
+          tmem_ld32_start(from + piece_column<kGated>(P, 0), r[0]);
 #pragma unroll
           for (int h = 0; h < kPieces; ++h) {
             tmem_ld_wait(r[h & 1]);
             if (h + 1 < kPieces) {
-              tmem_ld32_start(from + at[h + 1], r[(h + 1) & 1]);
+              tmem_ld32_start(from + piece_column<kGated>(P, h + 1), r[(h + 1) & 1]);
             } else {
               tc_fence_before();
               if (lane == 0) mbar_arrive_cluster_read(free_at);
@@ -324,7 +317,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
               fma_pair(acc[h][i], acc[h][i + 1], __uint_as_float(r[h & 1][i]), __uint_as_float(r[h & 1][i + 1]), scale);
           }
           parity ^= buf, buf ^= 1;
-          from = tmem + (buf ? flip : 0u), full_at ^= 8, free_at ^= 8;
+          from = first + (buf ? flip : 0u), full_at ^= 8, free_at ^= 8;
         }
       };
       for (int kb = 0; kb < nkb && ok; kb += kScaleSpan, ++spans) {
@@ -333,9 +326,9 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         const uint32_t sw = smem_u32(sm + P.off_scales) + (spans & 1) * (uint32_t)sizeof(Scales) + side * 16;
         const uint32_t sx = sw - side * 16 + kScaleSpan * 32 + (quarter * 32 + lane) * 4;
         const int blocks = min(nkb - kb, kScaleSpan);
-        if (pieces == 4)
+        if (BN == 256 || (kGated && BN == 192 && side == 0))
           add_span(std::integral_constant<int, 4>{}, blocks, sx, sw);
-        else if (!kGated && pieces == 3)
+        else if (!kGated && BN == 192)
           add_span(std::integral_constant<int, 3>{}, blocks, sx, sw);
         else
           add_span(std::integral_constant<int, 2>{}, blocks, sx, sw);

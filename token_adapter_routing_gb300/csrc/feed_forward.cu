@@ -733,7 +733,7 @@ cudaError_t launch_skinny(const FeedForwardArgs& a, const Resident& r, int BN, c
 
 // Cycles that ff_skinny_kernel takes in tiles of BN tokens, and the pairs' kernels in tiles of BN rows of W: what a K block takes,
 // what ends a tile, and the way through.  Fitted to 130 sizes on GB300 (1 to 2048 tokens, d_in 1024 to 4096, 1024 to 12288
-// rows of W): the choice is 0.6% off the fastest on average, 14% at most.  With e4m3 a K block of many tokens takes
+// rows of W): the choice is 0.8% off the fastest on average, 15% at most.  With e4m3 a K block of many tokens takes
 // long, as its sums are scaled: 200 tokens of 1024 -> 1024 gated 6.1 us in tiles of 32, 7.7 in tiles of 128.
 int64_t skinny_cycles(const FeedForwardArgs& a, const Resident& r, int BN) {
   const int64_t tiles = ((ff_rows_of_w(a) + kRows - 1) / kRows) * ((a.N + BN - 1) / BN);
