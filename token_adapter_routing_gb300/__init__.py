@@ -706,7 +706,7 @@ _TENSORS = (torch.Tensor, torch.nn.Parameter)
 
 def _call(name: str, device, *args):
     """Calls the library with the device of that index current and raises on a status that is not OK."""
-    fn = getattr(load_library(), name)
+    fn = getattr(_lib or load_library(), name)
     if device == torch._C._cuda_getDevice():
         status = fn(*args)
     else:
@@ -743,6 +743,7 @@ def _error_word(err_word, device):
 
 
 _FLOATS = (torch.bfloat16, torch.float32)
+_E4M3, _BF16, _BF16_E4M3 = (torch.float8_e4m3fn,), (torch.bfloat16,), (torch.bfloat16, torch.float8_e4m3fn)
 
 
 def _raw_stream(stream, device) -> int:
@@ -947,18 +948,27 @@ def _scale_blocks(n):
     return -(-n // SCALE_BLOCK)
 
 
+def _rows(x, types):
+    """x, the 2-D tensor argument that gives a call its sizes: its data pointer, dtype's code, sizes and device index."""
+    if type(x) not in _TENSORS or x.dtype not in types or x.dim() != 2 or not x.is_contiguous():
+        code = _matrix(x, "x", types)
+        return _array(x, "x", x.shape, x.dtype, x.get_device()), code, *x.shape, x.get_device()
+    N, d = x.shape
+    if d < 1:
+        raise ValueError("x must have at least one column")
+    return x.data_ptr(), _TYPE_CODES[x.dtype], N, d, x.get_device()
+
+
 def molora_quantise_blocks(x, out8=None, scale8=None, stream=None):
     """x [N, d] (bfloat16 or float32) in float8_e4m3fn with a scale for each row's block of SCALE_BLOCK columns: returns
     (out8 [N, d], scale8 float32 [N, ceil(d / SCALE_BLOCK)]), made if not given."""
-    code = _matrix(x, "x", _FLOATS)
-    N, d = x.shape
-    dev, blocks = x.get_device(), (N, _scale_blocks(d))
-    px = _array(x, "x", x.shape, x.dtype, dev)
+    px, code, N, d, dev = _rows(x, _FLOATS)
+    shape, blocks = (N, d), (N, _scale_blocks(d))
     if out8 is None:
-        out8 = _new(x, x.shape, torch.float8_e4m3fn, stream)
+        out8 = _new(x, shape, torch.float8_e4m3fn, stream)
     if scale8 is None:
         scale8 = _new(x, blocks, torch.float32, stream)
-    po, ps = _array(out8, "out8", x.shape, torch.float8_e4m3fn, dev), _array(scale8, "scale8", blocks, torch.float32, dev)
+    po, ps = _array(out8, "out8", shape, torch.float8_e4m3fn, dev), _array(scale8, "scale8", blocks, torch.float32, dev)
     _on_gpu(x, "x")
     _call("molora_quantise_blocks", dev, px, code, N, d, po, ps, _raw_stream(stream, dev))
     return out8, scale8
@@ -969,17 +979,15 @@ def molora_linear_blocks(x, x_scale, W, w_scale, y=None, bias=None, act="none", 
     """y = act(x W^T + bias) + residual for x [N, d_in] and W [d_out, d_in] in float8_e4m3fn with a scale for each block of
     SCALE_BLOCK: x_scale float32 [N, blocks of d_in] (molora_quantise_blocks), w_scale float32 [blocks of d_out, blocks of
     d_in].  d_in is a multiple of 16.  y, bias, act, residual and out_dtype as for molora_linear."""
-    _matrix(x, "x", (torch.float8_e4m3fn,))
-    N, d_in = x.shape
-    dev, f32 = x.get_device(), torch.float32
+    px, _, N, d_in, dev = _rows(x, _E4M3)
+    f32 = torch.float32
     if not isinstance(W, torch.Tensor) or W.dim() != 2 or W.shape[0] < 1:
         raise ValueError("W must be a 2-D tensor [d_out, d_in]")
     d_out, blocks = W.shape[0], _scale_blocks(d_in)
     act = _named(act, "act", ACTIVATIONS)
     if x_scale is None or w_scale is None:
         raise ValueError("x_scale and w_scale must be tensors")
-    px = _array(x, "x", x.shape, x.dtype, dev)
-    pw = _array(W, "W", (d_out, d_in), x.dtype, dev)
+    pw = _array(W, "W", (d_out, d_in), torch.float8_e4m3fn, dev)
     psx = _array(x_scale, "x_scale", (N, blocks), f32, dev)
     psw = _array(w_scale, "w_scale", (_scale_blocks(d_out), blocks), f32, dev)
     pb = _array(bias, "bias", (d_out,), f32, dev)
@@ -1003,15 +1011,13 @@ def molora_gated_linear(x, W, h=None, act="silu", x_scale=None, w_scale=None, er
     """The gated half of a feed-forward block: h = act(x Wg^T) * (x Wu^T), bfloat16 [N, d_ff], for x [N, d_in] and
     W = [Wg; Wu] [2 d_ff, d_in] in bfloat16 (d_in a multiple of 8), or in float8_e4m3fn (of 16) with a scale for each block of
     SCALE_BLOCK: x_scale float32 [N, blocks of d_in] and w_scale float32 [2 * blocks of d_ff, blocks of d_in]."""
-    code = _matrix(x, "x", (torch.bfloat16, torch.float8_e4m3fn))
-    N, d_in = x.shape
-    dev, bf16, f32 = x.get_device(), torch.bfloat16, torch.float32
+    px, code, N, d_in, dev = _rows(x, _BF16_E4M3)
+    bf16, f32 = torch.bfloat16, torch.float32
     d_ff, blocks = _gated_weights(W, d_in), _scale_blocks(d_in)
     act = _named(act, "act", ACTIVATIONS)
     fp8 = code == E4M3
     if fp8 != (x_scale is not None) or fp8 != (w_scale is not None):
         raise ValueError("x_scale and w_scale are needed with float8_e4m3fn, and with nothing else")
-    px = _array(x, "x", x.shape, x.dtype, dev)
     pw = _array(W, "W", (2 * d_ff, d_in), x.dtype, dev)
     psx = _array(x_scale, "x_scale", (N, blocks), f32, dev)
     psw = _array(w_scale, "w_scale", (2 * _scale_blocks(d_ff), blocks), f32, dev)
@@ -1030,14 +1036,12 @@ def molora_gated_linear_backward(x, W, dh, act="silu", dx=None, dW=None, dproj=N
     Returns (dx, dW, dproj): dx [N, d_in] and dW [2 d_ff, d_in], made if not given unless want_dx or want_dW is false
     (frozen weights need no dW), and dproj [N, 2, d_ff rounded up to 8], the projections' gradient (columns from d_ff on are
     unspecified), made if not given."""
-    code = _matrix(x, "x", (torch.bfloat16,))
-    N, d_in = x.shape
-    dev, bf16 = x.get_device(), torch.bfloat16
+    px, code, N, d_in, dev = _rows(x, _BF16)
+    bf16 = torch.bfloat16
     d_ff = _gated_weights(W, d_in)
     act = _named(act, "act", ACTIVATIONS)
     if dh is None:
         raise ValueError("dh must be a tensor")
-    px = _array(x, "x", x.shape, bf16, dev)
     pw = _array(W, "W", (2 * d_ff, d_in), bf16, dev)
     pdh = _array(dh, "dh", (N, d_ff), bf16, dev)
     if dx is None and want_dx:
