@@ -978,7 +978,7 @@ def molora_linear_blocks(x, x_scale, W, w_scale, y=None, bias=None, act="none", 
                          err_word=None, stream=None):
     """y = act(x W^T + bias) + residual for x [N, d_in] and W [d_out, d_in] in float8_e4m3fn with a scale for each block of
     SCALE_BLOCK: x_scale float32 [N, blocks of d_in] (molora_quantise_blocks), w_scale float32 [blocks of d_out, blocks of
-    d_in].  d_in is a multiple of 16.  y, bias, act, residual and out_dtype as for molora_linear."""
+    d_in].  d_in is a multiple of 16, x and W are 16-byte aligned.  y, bias, act, residual and out_dtype as for molora_linear."""
     px, _, N, d_in, dev = _rows(x, _E4M3)
     f32 = torch.float32
     if not isinstance(W, torch.Tensor) or W.dim() != 2 or W.shape[0] < 1:
@@ -1010,7 +1010,8 @@ def _gated_weights(W, d_in):
 def molora_gated_linear(x, W, h=None, act="silu", x_scale=None, w_scale=None, err_word=None, stream=None):
     """The gated half of a feed-forward block: h = act(x Wg^T) * (x Wu^T), bfloat16 [N, d_ff], for x [N, d_in] and
     W = [Wg; Wu] [2 d_ff, d_in] in bfloat16 (d_in a multiple of 8), or in float8_e4m3fn (of 16) with a scale for each block of
-    SCALE_BLOCK: x_scale float32 [N, blocks of d_in] and w_scale float32 [2 * blocks of d_ff, blocks of d_in]."""
+    SCALE_BLOCK: x_scale float32 [N, blocks of d_in] and w_scale float32 [2 * blocks of d_ff, blocks of d_in].  x and W are
+    16-byte aligned."""
     px, code, N, d_in, dev = _rows(x, _BF16_E4M3)
     bf16, f32 = torch.bfloat16, torch.float32
     d_ff, blocks = _gated_weights(W, d_in), _scale_blocks(d_in)

@@ -65,8 +65,8 @@ struct BPlan {
   uint32_t stage_bytes, off_b, off_stage, off_scales, off_ctrl, tmem_cols, smem;
 };
 
-// The h-th piece of 32 columns of a side's warps: its columns of TMEM from the side's first (side * 32), and of the outputs from
-// the tile's first.  Gated, pieces come in pairs, of the gate's rows of W and the up projection's.
+// The h-th piece of 32 columns of a side's warps: its columns of TMEM from the side's first (side * 32), and of the outputs
+// from the tile's first.  Gated, pieces come in pairs, of the gate's rows of W and the up projection's.
 template <bool kGated>
 __device__ __forceinline__ uint32_t piece_column(const BPlan& P, int h) {
   return kGated ? (h & 1) * ((uint32_t)P.BN / 2) + (h >> 1) * kSides * 32 : h * kSides * 32;
