@@ -13,6 +13,9 @@
 //   * few instructions in the loop (addresses that flip by xor, one vote a wait, fmas in pairs), loads of 32 columns
 //     with the next under way, a box for every piece a tile's outputs leave by: 129 -> 121
 //   * no register spilled (a piece's columns by a constant offset, not a table): 121 -> 112 (103 without a residual)
+//   * the bias by way of shared memory, no work on pieces that are not there, kernels of their own for rows that TMA cannot
+//     write (nothing spilled): 113.8 -> 110.8; such rows 16 at a time without a branch for each: fp32 5000 x 2064 -> 4097
+//     145 -> 107; the first scales gathered by the eight warps that wait for them: 1024 x 4096 -> 1024 14.5 -> 13.8
 // A product without scales takes 76: the finishing of a tile (1 to 2 us, under which the next tile's first two K
 // blocks run, then the tensor cores wait) and the chain above are the difference.
 // Tried and left: four warps a scheduler with half the sums each (126); accumulators in halves of 128 columns, which the
@@ -34,10 +37,12 @@ constexpr int kThreadsB = 32 * (kWarps + 4);     // + TMA warp, MMA warp, two th
 // 384 threads are launched with, so the last warpgroup gives up its own: 256 x 232 + 128 x 40 = 384 x 168.
 constexpr int kEpiRegisters = 232, kOtherRegisters = 40;
 
-// The scales of kScaleSpan K blocks of a tile: for each K block the 4 pieces' of each side, and the CTA's 128 tokens'.
+// The scales of kScaleSpan K blocks of a tile: for each K block the 4 pieces' of each side, and the CTA's 128 tokens'; and
+// what is added to the tile's columns.
 constexpr int kScaleSpan = 16, kScaleStride = kRows + 1;
 struct __align__(16) Scales {
   float w[kScaleSpan][8];
+  float bias[256];     // (a tile's last span's)
   float x[kScaleSpan * kScaleStride];
 };
 
@@ -98,7 +103,8 @@ __device__ __forceinline__ void activate_pairs(float (&v)[32], bool silu) {
 
 }  // namespace
 
-template <bool kGated, bool kY16>
+// kTma: y (and the residual) move by TMA.
+template <bool kGated, bool kY16, bool kTma>
 __global__ void __launch_bounds__(kThreadsB, 1)
     blocks_tc_kernel(const FEpi E, const BPlan P, int32_t* err_word, const __grid_constant__ CUtensorMap map_x,
                      const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_y,
@@ -147,10 +153,26 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     mbar_fence_init();
     tma_prefetch_desc(&map_x);
     tma_prefetch_desc(&map_w);
-    if (E.tma_y) tma_prefetch_desc(&map_y);
+    if (kTma) tma_prefetch_desc(&map_y);
     if (E.tma_res) tma_prefetch_desc(&map_r);
   }
   pdl_wait();
+  if (warp < kWarps) {  // the first span of scales, by all the warps that would wait for it
+    int32_t m0, n0;
+    tile_at(pair, m0, n0);
+    Scales* to = reinterpret_cast<Scales*>(sm + P.off_scales);
+    const int k = tid & 15, c = tid >> 4, col = n0 + piece_output<kGated>(c >> 2, c & 3);
+    if (k < nkb) {
+      for (int r = c; r < kRows && m0 + r < E.N; r += 2 * kWarps)
+        cp_async_4(smem_u32(to->x + k * kScaleStride + r), E.sx + (int64_t)(m0 + r) * nkb + k);
+      if (c < 8 && col < E.d_out)
+        cp_async_4(smem_u32(&to->w[k][c]), E.sw + (int64_t)(col / 128 + (kGated && (c & 1) ? E.up : 0)) * nkb + k);
+    }
+    if (!kGated && E.bias && nkb <= kScaleSpan && tid < width) {
+      const bool in = n0 + tid < E.d_out;  // (the others are 0, as activations go by pairs)
+      cp_async_4(smem_u32(&to->bias[tid]), E.bias + (in ? n0 + tid : 0), in ? 4 : 0);
+    }
+  }
   __syncthreads();
   // only now, with this CTA's TMEM held, may the next kernel's CTAs come and ask for theirs
   pdl_launch_dependents();
@@ -231,7 +253,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
             break;
           }
           Scales* to = reinterpret_cast<Scales*>(sm + P.off_scales) + (n & 1);
-          if (kb + k < nkb) {
+          if (n > 0 && kb + k < nkb) {  // (the first span: above)
             for (int r = l >> 4; r < kRows && m0 + r < E.N; r += 4)
               cp_async_4(smem_u32(to->x + k * kScaleStride + r), E.sx + (int64_t)(m0 + r) * nkb + kb + k);
             for (int c = l >> 4; c < 8; c += 4) {  // piece c & 3 of side c / 4
@@ -240,6 +262,11 @@ __global__ void __launch_bounds__(kThreadsB, 1)
                 cp_async_4(smem_u32(&to->w[k][c]), E.sw + (int64_t)(col / 128 + (kGated && (c & 1) ? E.up : 0)) * nkb + kb + k);
             }
           }
+          if (!kGated && E.bias && n > 0 && kb + kScaleSpan >= nkb)
+            for (int c = l; c < width; c += 64) {
+              const bool in = n0 + c < E.d_out;
+              cp_async_4(smem_u32(&to->bias[c]), E.bias + (in ? n0 + c : 0), in ? 4 : 0);
+            }
           cp_async_mbar_arrive(&ctrl->sfull[n & 1]);
         }
       }
@@ -248,6 +275,8 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     __syncwarp();
   } else {
     registers_up<kEpiRegisters>();
+    cp_async_wait_all();
+    named_barrier(1, 32 * kWarps);
     const int quarter = warp & 3, side = warp >> 2;
     uint8_t* box = sm + P.off_stage + (size_t)warp * P.box;
     const uint32_t tempty = dsmem_addr(smem_u32(&ctrl->tempty[0]), 0), tfull = smem_u32(&ctrl->tfull[0]);
@@ -278,7 +307,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         }
         ++asked;
       };
-      if (!kGated && E.tma_res) ask(0);
+      if (!kGated && kTma && E.tma_res) ask(0);
       float acc[4][32];
 #pragma unroll
       for (int h = 0; h < 4; ++h)
@@ -324,7 +353,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         ok = __all_sync(0xffffffffu, mbar_wait_spin(&ctrl->sfull[spans & 1], (uint32_t)(spans >> 1) & 1u, abort));
         if (!ok) break;
         const uint32_t sw = smem_u32(sm + P.off_scales) + (spans & 1) * (uint32_t)sizeof(Scales) + side * 16;
-        const uint32_t sx = sw - side * 16 + kScaleSpan * 32 + (quarter * 32 + lane) * 4;
+        const uint32_t sx = sw - side * 16 + (uint32_t)offsetof(Scales, x) + (quarter * 32 + lane) * 4;
         const int blocks = min(nkb - kb, kScaleSpan);
         if (BN == 256 || (kGated && BN == 192 && side == 0))
           add_span(std::integral_constant<int, 4>{}, blocks, sx, sw);
@@ -333,7 +362,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         else
           add_span(std::integral_constant<int, 2>{}, blocks, sx, sw);
         __syncwarp();
-        if (lane == 0) mbar_arrive(&ctrl->sempty[spans & 1]);
+        if (lane == 0 && (kGated || kb + kScaleSpan < nkb)) mbar_arrive(&ctrl->sempty[spans & 1]);
       }
       if (!ok) break;
       if constexpr (kGated) {
@@ -349,21 +378,32 @@ __global__ void __launch_bounds__(kThreadsB, 1)
           for (int i = 0; i < 32; ++i) acc[o][i] = acc[2 * o][i] * acc[2 * o + 1][i];
         }
       } else {
+        const uint32_t bias = smem_u32(&(reinterpret_cast<Scales*>(sm + P.off_scales) + ((spans - 1) & 1))->bias[side * 32]);
+        if (E.bias || E.act != MOLORA_ACT_NONE) {
 #pragma unroll
-        for (int o = 0; o < 4; ++o) {
-          if (E.bias) {
-            const float b = there(o) && column(o) + lane < E.d_out ? E.bias[column(o) + lane] : 0.f;
+          for (int o = 0; o < 4; ++o) {
+            if (!there(o)) continue;
+            if (E.bias) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) acc[o][i] += __shfl_sync(0xffffffffu, b, i);
+              for (int i = 0; i < 32; i += 4) {
+                const float4 b = lds_f32x4(bias + (o * kSides * 32 + i) * 4);
+                acc[o][i] += b.x, acc[o][i + 1] += b.y, acc[o][i + 2] += b.z, acc[o][i + 3] += b.w;
+              }
+            }
+            if (E.act == MOLORA_ACT_SILU || E.act == MOLORA_ACT_GELU_TANH)
+              activate_pairs(acc[o], E.act == MOLORA_ACT_SILU);
+            else
+              apply_act(acc[o], E.act);
           }
-          apply_act(acc[o], E.act);
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctrl->sempty[(spans - 1) & 1]);
       }
-      if (E.tma_y) {
+      if constexpr (kTma) {
         auto chunk = [&](int o, int i) { return box + o * kPiece + (i >> 2) * kBox + swz_offset((uint32_t)lane, (uint32_t)i & 3u, 64); };
 #pragma unroll
         for (int round = 0; round < kOut / kRound; ++round) {
-          if (!kGated && E.tma_res) {
+          if (!kGated && kTma && E.tma_res) {
             if (!(ok = __all_sync(0xffffffffu, mbar_wait(&ctrl->res_full[warp], (uint32_t)taken & 1u)))) break;
             ++taken;
 #pragma unroll
@@ -414,43 +454,50 @@ __global__ void __launch_bounds__(kThreadsB, 1)
                   tma_store_2d(&map_y, smem_u32(box + o * kPiece + q * kBox), column(round * kRound + o) + q * 16, m0);
             bulk_commit();
           }
-          if (!kGated && E.tma_res && round + 1 < kOut / kRound) ask(round + 1);
+          if (!kGated && kTma && E.tma_res && round + 1 < kOut / kRound) ask(round + 1);
         }
       } else {
         // rows that are not 16-byte aligned: turned in shared memory, written a row at a time, 16 rows' residuals on their way
         // together
         float* turned = reinterpret_cast<float*>(box);
+        const int rows = E.N - m0 < 32 ? (int)(E.N - m0) : 32;
+        auto residual = [&](int64_t at) {
+          if constexpr (kGated)
+            return 0.f;
+          else if constexpr (kY16)
+            return to_float(static_cast<const __nv_bfloat16*>(E.res)[at]);
+          else
+            return static_cast<const float*>(E.res)[at];
+        };
+        auto put = [&](int64_t at, float v) {
+          if constexpr (kY16)
+            static_cast<__nv_bfloat16*>(E.y)[at] = __float2bfloat16_rn(v);
+          else
+            static_cast<float*>(E.y)[at] = v;
+        };
+        const bool res = !kGated && E.res;
 #pragma unroll
         for (int o = 0; o < kOut; ++o) {
+          if (!there(o)) continue;
           __syncwarp();
 #pragma unroll
           for (int i = 0; i < 32; ++i) turned[lane * 32 + (i ^ lane)] = acc[o][i];
           __syncwarp();
-          const int32_t col = column(o) + lane;
-          const bool in = there(o) && col < E.d_out;
+          if (column(o) + lane >= E.d_out) continue;
+          int64_t to = (int64_t)m0 * E.d_out + column(o) + lane;
+          if (rows == 32) {
 #pragma unroll 1
-          for (int q0 = 0; q0 < 32 && m0 + q0 < E.N; q0 += 16) {
-            float add[16];
-            const int64_t to = ((int64_t)m0 + q0) * E.d_out + col;
+            for (int q0 = 0; q0 < 32; q0 += 16, to += 16 * (int64_t)E.d_out) {
+              float v[16];
 #pragma unroll
-            for (int q = 0; q < 16; ++q) {
-              add[q] = 0.f;
-              if (!kGated && E.res && in && m0 + q0 + q < E.N) {
-                if constexpr (kY16)
-                  add[q] = to_float(static_cast<const __nv_bfloat16*>(E.res)[to + (int64_t)q * E.d_out]);
-                else
-                  add[q] = static_cast<const float*>(E.res)[to + (int64_t)q * E.d_out];
-              }
-            }
+              for (int q = 0; q < 16; ++q) v[q] = res ? residual(to + q * (int64_t)E.d_out) : 0.f;
 #pragma unroll
-            for (int q = 0; q < 16; ++q) {
-              if (!in || m0 + q0 + q >= E.N) continue;
-              const float v = turned[(q0 + q) * 32 + (lane ^ (q0 + q))] + add[q];
-              if constexpr (kY16)
-                static_cast<__nv_bfloat16*>(E.y)[to + (int64_t)q * E.d_out] = __float2bfloat16_rn(v);
-              else
-                static_cast<float*>(E.y)[to + (int64_t)q * E.d_out] = v;
+              for (int q = 0; q < 16; ++q) v[q] += turned[(q0 + q) * 32 + (lane ^ (q0 + q))];
+#pragma unroll
+              for (int q = 0; q < 16; ++q) put(to + q * (int64_t)E.d_out, v[q]);
             }
+          } else {
+            for (int q = 0; q < rows; ++q, to += E.d_out) put(to, turned[q * 32 + (lane ^ q)] + (res ? residual(to) : 0.f));
           }
         }
       }
@@ -514,9 +561,10 @@ cudaError_t launch_blocks_tc(const FeedForwardArgs& a, int BN, cudaStream_t stre
     const dim3 grid((unsigned)(2 * (p.tiles < most ? p.tiles : most)));
     return launch_kernel(kernel, grid, dim3(kThreadsB), p.smem, stream, 2, e, p, a.err_word, mx, mw, my, mr);
   };
-  static std::atomic<uint64_t> allowed[3];
-  if (a.gated) return go(blocks_tc_kernel<true, true>, allowed[0]);
-  return a.y_bf16 ? go(blocks_tc_kernel<false, true>, allowed[1]) : go(blocks_tc_kernel<false, false>, allowed[2]);
+  static std::atomic<uint64_t> allowed[6];
+  if (a.gated) return e.tma_y ? go(blocks_tc_kernel<true, true, true>, allowed[0]) : go(blocks_tc_kernel<true, true, false>, allowed[1]);
+  if (a.y_bf16) return e.tma_y ? go(blocks_tc_kernel<false, true, true>, allowed[2]) : go(blocks_tc_kernel<false, true, false>, allowed[3]);
+  return e.tma_y ? go(blocks_tc_kernel<false, false, true>, allowed[4]) : go(blocks_tc_kernel<false, false, false>, allowed[5]);
 }
 
 }  // namespace molora

@@ -169,6 +169,10 @@ __device__ __forceinline__ void cp_async_16_hint(uint32_t sdst, const void* gsrc
 __device__ __forceinline__ void cp_async_4(uint32_t sdst, const void* gsrc) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(sdst), "l"(gsrc) : "memory");
 }
+// As cp_async_4 with src_bytes 4; with 0, nothing is read and the word becomes 0.
+__device__ __forceinline__ void cp_async_4(uint32_t sdst, const void* gsrc, uint32_t src_bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(sdst), "l"(gsrc), "r"(src_bytes) : "memory");
+}
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // One arrival on `bar` once every cp.async this thread issued so far has landed (the
 // barrier's expected count includes this arrival).
@@ -427,6 +431,13 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t sdst, const CUtensorMa
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, "
       "%3, %4}], [%5];" ::"r"(sdst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_3d(uint32_t sdst, const CUtensorMap* map, int32_t c0, int32_t c1, int32_t c2,
+                                            uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(sdst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
       : "memory");
 }
 // One arrival on the mbarrier at a cluster address (dsmem_addr).
