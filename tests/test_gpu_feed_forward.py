@@ -582,7 +582,12 @@ def test_offsets_past_32_bits(m, kind):
         dh[at] = randn(g, 7, F).to(BF)
         dx, dW, dproj = m.molora_gated_linear_backward(x, W, dh)
         a, b, c = m.molora_gated_linear_backward(x[at].contiguous(), W, dh[at].contiguous())
-        assert torch.equal(dx[at], a) and torch.equal(dproj[at], c) and (dx[2:1000] == 0).all()
+        assert torch.equal(dproj[at], c) and (dx[2:1000] == 0).all()
+        # (few and many tokens' dx take other kernels: fp32 sums of 2 F terms in another order, and a rounding of either)
+        dp = torch.cat([c[:, 0], c[:, 1]], dim=1).double()
+        want, tol = dp @ W.double(), 2 * U * 2 * F * (dp.abs() @ W.double().abs())
+        for got in (dx[at], a):
+            within(got, want, tol + (want.abs() + tol) * HALF[BF] + 2.0 ** -118)
         within(dW, b.double(), 2 * (b.double().abs() * HALF[BF]) + 2.0 ** -20)  # (the same 7 terms, in two orders of additions)
         return
     N, d, F = 530000, 128, 4096

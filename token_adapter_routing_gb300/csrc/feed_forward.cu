@@ -13,6 +13,8 @@
 //   BN rows of W, a TMA warp and an MMA warp ahead of 8 epilogue warps by two TMEM accumulators.
 // blocks_tc_kernel (e4m3, many tokens): blocks_tc.cu.
 // ff_skinny_kernel (few tokens): W's rows are the MMA's M, the tokens its N, d_in split over a cluster; bound by reading W.
+//   The gated block's dx = [dg | du] [Wg; Wu] is such a product too: W's columns are M, read as they lie (MN-major), and
+//   2 d_ff is what is split.
 #include <cudaTypedefs.h>
 
 #include <atomic>
@@ -28,7 +30,7 @@ namespace {
 
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 32 * (kEpiWarps + 2);  // + TMA warp (8) + MMA warp (9)
-enum Mode { kLinear, kGated, kSlopes };
+enum Mode { kLinear, kGated, kSlopes, kInput };  // (kInput: dx of the gated block)
 constexpr int kSpan = 8;     // bf16, few tokens: K blocks summed in TMEM before fp32 registers take over
 
 struct __align__(8) FCtrl {
@@ -523,6 +525,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (issued >= S && !mbar_wait_spin(&ctrl->empty[s], phase, abort)) break;
         uint8_t* st = sm + (size_t)s * P.stage_bytes;
         mbar_arrive_expect_tx(&ctrl->full[s], P.stage_bytes);
+        if constexpr (kMode == kInput) {  // K runs over the gate's columns of dproj, then the up's
+          const int32_t plane = kb >= P.nkb / 2, k = (kb - (plane ? P.nkb / 2 : 0)) * 64;
+          tma_load_3d(smem_u32(st), &map_w, o0, k, plane, &ctrl->full[s]);
+          tma_load_3d(smem_u32(st + kAtom), &map_w, o0 + 64, k, plane, &ctrl->full[s]);
+          tma_load_3d(smem_u32(st + P.off_b), &map_x, k, plane, t0, &ctrl->full[s]);
+          if (++s == S) s = 0, phase ^= 1;
+          continue;
+        }
         tma_load_2d(smem_u32(st), &map_w, kb * elems, o0, &ctrl->full[s]);
         if (kMode == kGated) tma_load_2d(smem_u32(st + kWidth * kRowBytes), &map_w, kb * elems, E.d_out + o0, &ctrl->full[s]);
         tma_load_2d(smem_u32(st + P.off_b), &map_x, kb * elems, t0, &ctrl->full[s]);
@@ -533,8 +543,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == 9) {
     if (elect_one()) {
-      const uint32_t idesc = kFp8 ? idesc_e4m3_f32(kRows, (uint32_t)BN) : idesc_bf16_f32(kRows, (uint32_t)BN, false, false);
-      const uint64_t da = smem_desc(smem_u32(sm), 16, 1024, kSwizzle128B);
+      const uint32_t idesc = kFp8 ? idesc_e4m3_f32(kRows, (uint32_t)BN) : idesc_bf16_f32(kRows, (uint32_t)BN, kMode == kInput, false);
+      const uint64_t da = smem_desc(smem_u32(sm), kMode == kInput ? kAtom : 16, 1024, kSwizzle128B);
       const uint64_t db = smem_desc(smem_u32(sm + P.off_b), 16, 1024, kSwizzle128B);
       const uint32_t a_lo = (uint32_t)da, b_lo = (uint32_t)db, desc_hi = (uint32_t)(da >> 32);
       bool ok = true;
@@ -555,7 +565,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tc_fence_after();
           const uint32_t at = (uint32_t)s * (P.stage_bytes >> 4);
-          umma_stage<false, kFp8>(d, a_lo + at, b_lo + at, desc_hi, desc_hi, idesc, kb != first);
+          if constexpr (kMode == kInput)
+            umma_stage_steps<false>(d, a_lo + at, b_lo + at, desc_hi, desc_hi, idesc, kb != first, 16 * kRowBytes / 16, 2);
+          else
+            umma_stage<false, kFp8>(d, a_lo + at, b_lo + at, desc_hi, desc_hi, idesc, kb != first);
           umma_commit(&ctrl->empty[s]);
           if (++s == S) s = 0, phase ^= 1;
         }
@@ -618,7 +631,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // every MMA is done; the TMA warp has seen every load land
   have = mbar_wait(&ctrl->done, 0) && have && !*abort;
   __syncthreads();
-  ff_join<kMode, J >= 2 && kMode == kLinear ? 4 : 2>(E, sums, have, sm, C, rank, o0, t0, tokens, err_word);
+  ff_join<kMode == kInput ? kLinear : kMode, J >= 2 && kMode != kGated ? 4 : 2>(E, sums, have, sm, C, rank, o0, t0, tokens, err_word);
   if (warp == 9) {
     tc_fence_after();
     tmem_dealloc(tmem, P.tmem_cols);
@@ -678,22 +691,20 @@ cudaError_t launch_tc(const FeedForwardArgs& a, Mode mode, int BN, cudaStream_t 
   return mode == kSlopes ? go(ff_tc_kernel<kSlopes>, allowed[0]) : go(ff_tc_kernel<kGated>, allowed[1]);
 }
 
-cudaError_t launch_skinny(const FeedForwardArgs& a, const Resident& r, int BN, cudaStream_t stream) {
-  const FEpi e = ff_epilogue_of(a);
+// The plan of a product of o_tiles x 128 rows of W with N tokens, in tiles of BN tokens.
+FSkinnyPlan skinny_plan(const Resident& r, int64_t o_tiles, int64_t N, int nkb, int BN) {
   FSkinnyPlan p = {};
-  const int width = a.gated ? kRows / 2 : kRows;
   p.BN = BN;
-  p.nkb = ff_k_blocks(a);
-  p.o_tiles = (int32_t)(((int64_t)a.d_out + width - 1) / width);
-  p.t_tiles = (int32_t)((a.N + p.BN - 1) / p.BN);
-  const int64_t tiles = (int64_t)p.o_tiles * p.t_tiles;
-  p.C = split_of(r, tiles, p.nkb);
+  p.nkb = nkb;
+  p.o_tiles = (int32_t)o_tiles;
+  p.t_tiles = (int32_t)((N + BN - 1) / BN);
+  p.C = split_of(r, o_tiles * p.t_tiles, nkb);
   p.off_b = kRows * kRowBytes;
-  p.stage_bytes = p.off_b + (uint32_t)p.BN * kRowBytes;
-  p.tmem_cols = tmem_columns(2 * (uint32_t)p.BN);
+  p.stage_bytes = p.off_b + (uint32_t)BN * kRowBytes;
+  p.tmem_cols = tmem_columns(2 * (uint32_t)BN);
   const size_t fixed = sizeof(FCtrl) + kSmemSlack;
-  const size_t partial = (size_t)p.BN * kRows * sizeof(float);
-  const int need = (p.nkb + p.C - 1) / p.C;
+  const size_t partial = (size_t)BN * kRows * sizeof(float);
+  const int need = (nkb + p.C - 1) / p.C;
   p.S = (int)((kMaxSmem - fixed) / p.stage_bytes);
   if (p.S > kMaxStages) p.S = kMaxStages;
   if (p.S > need) p.S = need;
@@ -702,45 +713,66 @@ cudaError_t launch_skinny(const FeedForwardArgs& a, const Resident& r, int BN, c
   p.off_ctrl = (uint32_t)ring;
   p.smem = (uint32_t)(ring + fixed);
   if (p.smem < 116 * 1024) p.smem = 116 * 1024;  // no two CTAs that could wait for each other's TMEM share an SM (see linear.cu)
-  CUtensorMap mx, mw;
-  if (!ff_operand_map(&mx, a, a.x, a.N, (uint32_t)p.BN) || !ff_operand_map(&mw, a, a.W, ff_rows_of_w(a), (uint32_t)width))
-    return cudaErrorNotSupported;
-  auto go = [&](auto kernel, std::atomic<uint64_t>& allowed) {
-    const cudaError_t set = allow_smem(kernel, allowed, kMaxSmem);
+  return p;
+}
+
+template <bool kFp8, Mode kMode>
+cudaError_t launch_skinny_kernel(const FEpi& e, const FSkinnyPlan& p, int32_t* err_word, cudaStream_t stream, const CUtensorMap& mx,
+                                 const CUtensorMap& mw) {
+  static std::atomic<uint64_t> allowed[4];
+  auto go = [&](auto kernel, int n) {
+    const cudaError_t set = allow_smem(kernel, allowed[n], kMaxSmem);
     if (set != cudaSuccess) return set;
-    return launch_kernel(kernel, dim3((unsigned)(tiles * p.C)), dim3(kThreads), p.smem, stream, p.C, e, p, a.err_word, mx, mw);
-  };
-  static std::atomic<uint64_t> allowed[12];
-  const bool fp8 = a.dtype == MOLORA_E4M3;
-  auto pick = [&](auto j, int n) {
-    constexpr int J = decltype(j)::value;
-    return !fp8 ? go(ff_skinny_kernel<false, kGated, J>, allowed[3 * n])
-           : a.gated ? go(ff_skinny_kernel<true, kGated, J>, allowed[3 * n + 1])
-                     : go(ff_skinny_kernel<true, kLinear, J>, allowed[3 * n + 2]);
+    const int64_t ctas = (int64_t)p.o_tiles * p.t_tiles * p.C;
+    return launch_kernel(kernel, dim3((unsigned)ctas), dim3(kThreads), p.smem, stream, p.C, e, p, err_word, mx, mw);
   };
   switch (p.BN) {
     case 16:
     case 32:
-      return pick(std::integral_constant<int, 1>{}, 0);
+      return go(ff_skinny_kernel<kFp8, kMode, 1>, 0);
     case 64:
-      return pick(std::integral_constant<int, 2>{}, 1);
+      return go(ff_skinny_kernel<kFp8, kMode, 2>, 1);
     case 128:
-      return pick(std::integral_constant<int, 4>{}, 2);
+      return go(ff_skinny_kernel<kFp8, kMode, 4>, 2);
     default:
-      return pick(std::integral_constant<int, 8>{}, 3);
+      return go(ff_skinny_kernel<kFp8, kMode, 8>, 3);
   }
+}
+
+cudaError_t launch_skinny(const FeedForwardArgs& a, const Resident& r, int BN, cudaStream_t stream) {
+  const FEpi e = ff_epilogue_of(a);
+  const int width = a.gated ? kRows / 2 : kRows;
+  const FSkinnyPlan p = skinny_plan(r, ((int64_t)a.d_out + width - 1) / width, a.N, ff_k_blocks(a), BN);
+  CUtensorMap mx, mw;
+  if (!ff_operand_map(&mx, a, a.x, a.N, (uint32_t)p.BN) || !ff_operand_map(&mw, a, a.W, ff_rows_of_w(a), (uint32_t)width))
+    return cudaErrorNotSupported;
+  if (a.dtype != MOLORA_E4M3) return launch_skinny_kernel<false, kGated>(e, p, a.err_word, stream, mx, mw);
+  return a.gated ? launch_skinny_kernel<true, kGated>(e, p, a.err_word, stream, mx, mw)
+                 : launch_skinny_kernel<true, kLinear>(e, p, a.err_word, stream, mx, mw);
 }
 
 // Cycles that ff_skinny_kernel takes in tiles of BN tokens, and the pairs' kernels in tiles of BN rows of W: what a K block takes,
 // what ends a tile, and the way through.  Fitted to 130 sizes on GB300 (1 to 2048 tokens, d_in 1024 to 4096, 1024 to 12288
 // rows of W): the choice is 0.8% off the fastest on average, 15% at most.  With e4m3 a K block of many tokens takes
 // long, as its sums are scaled: 200 tokens of 1024 -> 1024 gated 6.1 us in tiles of 32, 7.7 in tiles of 128.
-int64_t skinny_cycles(const FeedForwardArgs& a, const Resident& r, int BN) {
-  const int64_t tiles = ((ff_rows_of_w(a) + kRows - 1) / kRows) * ((a.N + BN - 1) / BN);
-  const int nkb = ff_k_blocks(a), C = split_of(r, tiles, nkb);
+int64_t skinny_cycles(const Resident& r, int64_t rows_of_w, int64_t N, int nkb, bool fp8, int BN) {
+  const int64_t tiles = ((rows_of_w + kRows - 1) / kRows) * ((N + BN - 1) / BN);
+  const int C = split_of(r, tiles, nkb);
   const int64_t waves = (tiles + r.of[C] - 1) / r.of[C], blocks = (nkb + C - 1) / C;
-  if (a.dtype == MOLORA_E4M3) return 4000 + waves * (blocks * (450 + 5 * BN) + 60 * BN);
+  if (fp8) return 4000 + waves * (blocks * (450 + 5 * BN) + 60 * BN);
   return 6600 + waves * (blocks * (730 + BN * 3 / 5) + 38 * BN);
+}
+
+// The tile of the least cost.
+int best_skinny(const Resident& r, int64_t rows_of_w, int64_t N, int nkb, bool fp8, int64_t& cost) {
+  int best = 0;
+  cost = INT64_MAX;
+  for (int BN : {16, 32, 64, 128, 256}) {
+    if (BN > 16 && BN / 2 >= N) break;
+    const int64_t c = skinny_cycles(r, rows_of_w, N, nkb, fp8, BN);
+    if (c < cost) cost = c, best = BN;
+  }
+  return best;
 }
 
 int64_t tc_cycles(const FeedForwardArgs& a, const Resident& r, int BN) {
@@ -769,13 +801,8 @@ int best_tc(const FeedForwardArgs& a, const Resident& r, int64_t cost) {
 
 cudaError_t launch_feed_forward(const FeedForwardArgs& a, cudaStream_t stream) {
   const Resident r = resident_clusters();
-  int split = 0;
-  int64_t cost = INT64_MAX;
-  for (int BN : {16, 32, 64, 128, 256}) {
-    if (BN > 16 && BN / 2 >= a.N) break;
-    const int64_t c = skinny_cycles(a, r, BN);
-    if (c < cost) cost = c, split = BN;
-  }
+  int64_t cost;
+  int split = best_skinny(r, ff_rows_of_w(a), a.N, ff_k_blocks(a), a.dtype == MOLORA_E4M3, cost);
 #ifdef MOLORA_TUNING_ENV
   if (const char* g = getenv("MOLORA_FF_SKINNY")) split = atoi(g), cost = split ? 0 : INT64_MAX;
 #endif
@@ -788,6 +815,33 @@ cudaError_t launch_gated_slope(const GatedGradArgs& g, cudaStream_t stream) {
   const FeedForwardArgs a = {true, g.x, MOLORA_BF16, nullptr, g.N, g.d_in, g.W, nullptr, g.d_ff, nullptr, g.act, g.dh, g.dproj, true,
                              g.err_word};
   return launch_tc(a, kSlopes, best_tc(a, resident_clusters(), INT64_MAX), stream);
+}
+
+int64_t gated_input_cycles(const GatedGradArgs& a) {
+  int64_t cost;
+  best_skinny(resident_clusters(), a.d_in, a.N, 2 * (int)(((int64_t)a.d_ff + 63) / 64), false, cost);
+  return cost;
+}
+
+cudaError_t launch_gated_input(const GatedGradArgs& a, cudaStream_t stream) {
+  const Resident r = resident_clusters();
+  const uint64_t N = (uint64_t)a.N, F = (uint64_t)a.d_ff, D = (uint64_t)a.d_in, half = (F + 7) & ~uint64_t(7);
+  const int nkb = 2 * (int)((F + 63) / 64);
+  int64_t cost;
+  const int BN = best_skinny(r, a.d_in, a.N, nkb, false, cost);
+  FEpi e = {};
+  e.N = a.N;
+  e.d_out = a.d_in;
+  e.act = MOLORA_ACT_NONE;
+  e.y = a.dx;
+  e.y_bf16 = e.tma_y = true;
+  const auto BF = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const auto S128 = CU_TENSOR_MAP_SWIZZLE_128B;
+  CUtensorMap mx, mw;
+  if (!linear_map_3d(&mx, BF, a.dproj, {F, 2, N}, {2 * half, 4 * half}, {64, 1, (uint32_t)BN}, S128) ||
+      !linear_map_3d(&mw, BF, a.W, {D, F, 2}, {2 * D, 2 * F * D}, {64, 64, 1}, S128))
+    return cudaErrorNotSupported;
+  return launch_skinny_kernel<false, kInput>(e, skinny_plan(r, ((int64_t)a.d_in + kRows - 1) / kRows, a.N, nkb, BN), a.err_word, stream, mx, mw);
 }
 
 }  // namespace molora

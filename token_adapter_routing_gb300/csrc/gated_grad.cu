@@ -11,6 +11,9 @@
 #include <cudaTypedefs.h>
 
 #include <atomic>
+#ifdef MOLORA_TUNING_ENV
+#include <cstdlib>
+#endif
 
 #include "common.cuh"
 #include "kernels.h"
@@ -23,7 +26,6 @@ namespace {
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 32 * (kEpiWarps + 2);  // + TMA warp (8) + MMA warp (9)
 constexpr int kSets = 2;                        // staging boxes an epilogue warp
-constexpr uint32_t kAtom = 64 * kRowBytes;      // a box of 64 columns x 64 rows of K
 constexpr uint32_t kStageA = kRows * kRowBytes;
 
 struct __align__(8) GCtrl {
@@ -90,25 +92,6 @@ __device__ __forceinline__ bool tile_at(const GPlan& P, int32_t pair, int64_t j,
   t.n0 = (int32_t)(in / rows) * P.BN;
   t.kbs = t.x ? P.kb_x : P.kb_w;
   return true;
-}
-
-// The MMAs of one stage, as umma_stage, with the 16-byte units between the steps of A too.
-__device__ __forceinline__ void umma_stage_steps(uint32_t d, uint32_t a, uint32_t b, uint32_t a_hi, uint32_t b_hi, uint32_t idesc,
-                                                 uint32_t accumulate, uint32_t a_step, uint32_t b_step) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t.reg .b32 al, bl;\n\t"
-      "setp.ne.b32 p, %6, 0;\n\t"
-      "mov.b64 da, {%1, %3};\n\tmov.b64 db, {%2, %4};\n\t"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %5, p;\n\t"
-      "setp.eq.b32 p, 0, 0;\n\t"
-      "add.u32 al, %1, %7;\n\tadd.u32 bl, %2, %8;\n\tmov.b64 da, {al, %3};\n\tmov.b64 db, {bl, %4};\n\t"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %5, p;\n\t"
-      "add.u32 al, al, %7;\n\tadd.u32 bl, bl, %8;\n\tmov.b64 da, {al, %3};\n\tmov.b64 db, {bl, %4};\n\t"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %5, p;\n\t"
-      "add.u32 al, al, %7;\n\tadd.u32 bl, bl, %8;\n\tmov.b64 da, {al, %3};\n\tmov.b64 db, {bl, %4};\n\t"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %5, p;\n\t}" ::"r"(d),
-      "r"(a), "r"(b), "r"(a_hi), "r"(b_hi), "r"(idesc), "r"(accumulate), "r"(a_step), "r"(b_step)
-      : "memory");
 }
 
 }  // namespace
@@ -236,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tc_fence_after();
           const uint32_t at = (uint32_t)s * (P.stage_bytes >> 4);
-          umma_stage_steps(d, a_lo + at, m_lo + (kStageA >> 4) + at, hi, hi, idesc, kb != 0, a_step, 16 * kRowBytes / 16);
+          umma_stage_steps<true>(d, a_lo + at, m_lo + (kStageA >> 4) + at, hi, hi, idesc, kb != 0, a_step, 16 * kRowBytes / 16);
           umma_commit_pair(&ctrl->empty[s], both);
           if (++s == S) s = 0, phase ^= 1;
         }
@@ -324,13 +307,12 @@ cudaError_t launch_gated_grad(const GatedGradArgs& a, cudaStream_t stream) {
   p.kb_w = (int32_t)((N + 63) / 64);
   p.group = 8;
   const int64_t most = num_sms() / 2;
-  // The wider tiles where they are over first: a K block of a tile takes 600 cycles at 256 columns, 420 at 128.
-  // Returns those of the longest pair.
-  auto plan = [&](int BN) {
+  // A K block of a tile takes 600 cycles at 256 columns, 420 at 128.  Returns those of the longest pair.
+  auto plan = [&](int BN, bool with_x, bool with_w) {
     p.BN = BN;
     p.n_tiles = (int32_t)(((int64_t)a.d_in + BN - 1) / BN);
-    p.tiles_x = a.dx ? p.m_tiles_x * p.n_tiles : 0;
-    p.tiles_w = a.dW ? 2 * p.m_tiles_w * p.n_tiles : 0;
+    p.tiles_x = with_x ? p.m_tiles_x * p.n_tiles : 0;
+    p.tiles_w = with_w ? 2 * p.m_tiles_w * p.n_tiles : 0;
     const int64_t tiles = p.tiles_x + p.tiles_w;
     p.pairs = (int32_t)(tiles < most ? tiles : most);
     p.full = (int32_t)(p.tiles_x % p.pairs);
@@ -342,8 +324,23 @@ cudaError_t launch_gated_grad(const GatedGradArgs& a, cudaStream_t stream) {
     const int64_t of_others = all + (int64_t)p.ahead * p.kb_w + (extra ? p.kb_w : 0);
     return (of_full > of_others ? of_full : of_others) * (BN == 256 ? 600 : 420);
   };
-  const int64_t narrow = plan(128);
-  if (plan(256) > narrow) plan(128);
+  // The wider tiles where they are over first.
+  auto best = [&](bool with_x, bool with_w) {
+    const int64_t narrow = plan(128, with_x, with_w), wide = plan(256, with_x, with_w);
+    return wide > narrow ? plan(128, with_x, with_w) : wide;
+  };
+  // Few tokens' dx is a few tiles of long sums: its 2 d_ff split over clusters, in a launch of its own, where that is over
+  // before the tiles are (256 tokens, 1024 -> 4096: 21 us with dproj, 45 in tiles; dW too, 31 and 48).  Both uses, with dW
+  // and without, are counted whichever it is, so that dx has the same bits in either.
+  bool with_x = a.dx && 2 * gated_input_cycles(a) + best(false, true) >= best(true, false) + best(true, true);
+#ifdef MOLORA_TUNING_ENV
+  if (const char* g = getenv("MOLORA_FF_DX")) with_x = a.dx && atoi(g) != 0;
+#endif
+  if (a.dx && !with_x) {
+    const cudaError_t input = launch_gated_input(a, stream);
+    if (input != cudaSuccess || !a.dW) return input;
+  }
+  best(with_x, a.dW != nullptr);
   p.stage_bytes = kStageA + (uint32_t)(p.BN / 128) * kAtom;
   const uint32_t boxes = kEpiWarps * kSets * kBox;
   p.S = (int)((kMaxSmem - boxes - sizeof(GCtrl) - kSmemSlack) / p.stage_bytes);
@@ -354,7 +351,7 @@ cudaError_t launch_gated_grad(const GatedGradArgs& a, cudaStream_t stream) {
   const auto BF = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const auto S128 = CU_TENSOR_MAP_SWIZZLE_128B, S64 = CU_TENSOR_MAP_SWIZZLE_64B;
   CUtensorMap pk = {}, pm = {}, w = {}, x = {}, dx = {}, dw = {};
-  if (a.dx && (!linear_map_3d(&pk, BF, a.dproj, {F, 2, N}, {2 * half, 4 * half}, {64, 1, 128}, S128) ||
+  if (with_x && (!linear_map_3d(&pk, BF, a.dproj, {F, 2, N}, {2 * half, 4 * half}, {64, 1, 128}, S128) ||
                !linear_map_3d(&w, BF, a.W, {D, F, 2}, {2 * D, 2 * F * D}, {64, 64, 1}, S128) ||
                !linear_map_3d(&dx, BF, a.dx, {D, N, 1}, {2 * D, 2 * N * D}, {32, 32, 1}, S64)))
     return cudaErrorNotSupported;

@@ -177,6 +177,9 @@ struct GatedGradArgs {
   int32_t* err_word;
 };
 cudaError_t launch_gated_slope(const GatedGradArgs& a, cudaStream_t stream);  // dproj alone
+// dx alone from dproj, 2 d_ff split over clusters (few tokens), and the cycles that it takes.
+cudaError_t launch_gated_input(const GatedGradArgs& a, cudaStream_t stream);
+int64_t gated_input_cycles(const GatedGradArgs& a);
 cudaError_t launch_gated_grad(const GatedGradArgs& a, cudaStream_t stream);
 
 int num_sms();

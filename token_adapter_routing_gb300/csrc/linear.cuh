@@ -149,6 +149,34 @@ __device__ __forceinline__ void umma_stage(uint32_t d, uint32_t a, uint32_t b, u
 }
 #undef MOLORA_UMMA4
 
+// As umma_stage of bf16, with the 16-byte units between the steps of A too.
+#define MOLORA_UMMA4_STEPS(group)                                                                                        \
+  asm volatile(                                                                                                          \
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t.reg .b32 al, bl;\n\t"                                                  \
+      "setp.ne.b32 p, %6, 0;\n\t"                                                                                        \
+      "mov.b64 da, {%1, %3};\n\tmov.b64 db, {%2, %4};\n\t"                                                               \
+      "tcgen05.mma.cta_group::" group ".kind::f16 [%0], da, db, %5, p;\n\t"                                              \
+      "setp.eq.b32 p, 0, 0;\n\t"                                                                                         \
+      "add.u32 al, %1, %7;\n\tadd.u32 bl, %2, %8;\n\tmov.b64 da, {al, %3};\n\tmov.b64 db, {bl, %4};\n\t"                 \
+      "tcgen05.mma.cta_group::" group ".kind::f16 [%0], da, db, %5, p;\n\t"                                              \
+      "add.u32 al, al, %7;\n\tadd.u32 bl, bl, %8;\n\tmov.b64 da, {al, %3};\n\tmov.b64 db, {bl, %4};\n\t"                 \
+      "tcgen05.mma.cta_group::" group ".kind::f16 [%0], da, db, %5, p;\n\t"                                              \
+      "add.u32 al, al, %7;\n\tadd.u32 bl, bl, %8;\n\tmov.b64 da, {al, %3};\n\tmov.b64 db, {bl, %4};\n\t"                 \
+      "tcgen05.mma.cta_group::" group ".kind::f16 [%0], da, db, %5, p;\n\t}" ::"r"(d),                                   \
+      "r"(a), "r"(b), "r"(a_hi), "r"(b_hi), "r"(idesc), "r"(accumulate), "r"(a_step), "r"(b_step)                        \
+      : "memory")
+
+template <bool kPair>
+__device__ __forceinline__ void umma_stage_steps(uint32_t d, uint32_t a, uint32_t b, uint32_t a_hi, uint32_t b_hi, uint32_t idesc,
+                                                 uint32_t accumulate, uint32_t a_step, uint32_t b_step) {
+  if constexpr (kPair)
+    MOLORA_UMMA4_STEPS("2");
+  else
+    MOLORA_UMMA4_STEPS("1");
+}
+#undef MOLORA_UMMA4_STEPS
+
+constexpr uint32_t kAtom = 64 * 128;  // a box of 64 columns x 64 rows of K, of an operand that lies MN-major
 constexpr int kRows = 128;          // rows of a box of x (or of W in the skinny kernels) = TMEM lanes
 constexpr uint32_t kRowBytes = 128; // bytes of K per stage
 // More bytes in flight take longer to come: one token, 4096 x 4096 bf16 from HBM 9.4 us with 4 stages, 8.8
