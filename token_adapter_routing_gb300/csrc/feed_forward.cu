@@ -218,6 +218,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++used;
       return box;
     };
+    // rows of dh that start anywhere: a lane a column, into the same box
+    auto fetch = [&](int32_t col, int32_t row) {
+      __syncwarp();
+      uint8_t* box = in_box(asked);
+      const __nv_bfloat16* dh = static_cast<const __nv_bfloat16*>(E.res) + (int64_t)row * E.d_out + col + lane;
+      const bool in = col + lane < E.d_out;
+#pragma unroll
+      for (int r0 = 0; r0 < 32; r0 += 16) {  // (loads before stores: these could be to the same memory)
+        __nv_bfloat16 v[16];
+#pragma unroll
+        for (int r = 0; r < 16; ++r) v[r] = in && row + r0 + r < E.N ? dh[(int64_t)(r0 + r) * E.d_out] : __float2bfloat16_rn(0.f);
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          *reinterpret_cast<__nv_bfloat16*>(box + swz_offset((uint32_t)(r0 + r), (uint32_t)lane >> 3, 64) + (lane & 7) * 2) = v[r];
+      }
+      ++asked;
+    };
     const uint32_t tempty = dsmem_addr(smem_u32(&ctrl->tempty[0]), 0);
     bool ok = true;
     int32_t pt = pair;
@@ -242,12 +259,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < 32; ++i) turned[lane * 32 + (i ^ lane)] = v[i];
           __syncwarp();
           __nv_bfloat16* y = static_cast<__nv_bfloat16*>(E.y) + (int64_t)m0 * E.d_out + col + lane;
-          for (int q = 0; q < 32 && m0 + q < E.N; ++q)
-            if (col + lane < E.d_out) y[(int64_t)q * E.d_out] = __float2bfloat16_rn(turned[q * 32 + (lane ^ q)]);
+          if (col + lane < E.d_out) {
+            if (m0 + 32 <= E.N) {
+#pragma unroll 8
+              for (int q = 0; q < 32; ++q) y[(int64_t)q * E.d_out] = __float2bfloat16_rn(turned[q * 32 + (lane ^ q)]);
+            } else {
+              for (int q = 0; m0 + q < E.N; ++q) y[(int64_t)q * E.d_out] = __float2bfloat16_rn(turned[q * 32 + (lane ^ q)]);
+            }
+          }
         }
       };
-      if (E.tma_res)
+      if (E.tma_res) {
         for (int c = side; c < chunks; c += 2) ask(n0 + c * 32, m0);
+      } else if (kMode == kSlopes) {
+        for (int c = side; c < chunks; c += 2) fetch(n0 + c * 32, m0);
+      }
       ok = __all_sync(0xffffffffu, mbar_wait_spin(&ctrl->tfull[tc & 1], (uint32_t)(tc >> 1) & 1u, abort));
       if (!ok) break;
       tc_fence_after();
@@ -278,20 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint8_t* box = in_box(taken);
           if (E.tma_res) {
             if (!(ok = await())) break;
-          } else {  // rows of dh that start anywhere: a lane a column, turned into the same box
-            __syncwarp();
-            const __nv_bfloat16* dh = static_cast<const __nv_bfloat16*>(E.res) + (int64_t)m0 * E.d_out + col + lane;
-            const bool in = col + lane < E.d_out;
-#pragma unroll
-            for (int r0 = 0; r0 < 32; r0 += 16) {  // (loads before stores: these could be to the same memory)
-              __nv_bfloat16 v[16];
-#pragma unroll
-              for (int r = 0; r < 16; ++r)
-                v[r] = in && m0 + r0 + r < E.N ? dh[(int64_t)(r0 + r) * E.d_out] : __float2bfloat16_rn(0.f);
-#pragma unroll
-              for (int r = 0; r < 16; ++r)
-                *reinterpret_cast<__nv_bfloat16*>(box + swz_offset((uint32_t)(r0 + r), (uint32_t)lane >> 3, 64) + (lane & 7) * 2) = v[r];
-            }
+          } else {
             __syncwarp();
           }
 #pragma unroll
@@ -308,7 +321,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           ++taken;
-          if (!E.tma_res) ++asked;
           const uint8_t* from = stage(g);  // (after its __syncwarp every lane has read dh's box)
           if (lane == 0) {
             tma_store_3d(&map_y, smem_u32(from), col, 0, m0);
