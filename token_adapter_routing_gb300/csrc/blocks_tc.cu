@@ -15,12 +15,14 @@
 //   * no register spilled (a piece's columns by a constant offset, not a table): 121 -> 112 (103 without a residual)
 //   * the bias by way of shared memory, no work on pieces that are not there, kernels of their own for rows that TMA cannot
 //     write (nothing spilled): 113.8 -> 110.8; such rows 16 at a time without a branch for each: fp32 5000 x 2064 -> 4097
-//     145 -> 107; the first scales gathered by the eight warps that wait for them: 1024 x 4096 -> 1024 14.5 -> 13.8
+//     145 -> 107, those of the last tokens too: 1237 x 2064 -> 1541 19.4 -> 15.9; the first scales gathered by the eight
+//     warps that wait for them: 1024 x 4096 -> 1024 14.5 -> 13.8
 // A product without scales takes 76: the finishing of a tile (1 to 2 us, under which the next tile's first two K
 // blocks run, then the tensor cores wait) and the chain above are the difference.
 // Tried and left: four warps a scheduler with half the sums each (126); accumulators in halves of 128 columns, which the
-// tensor cores make less quickly (141); loads of 64 columns (118), the next K block's scales, or the look whether it is
-// there, before the last sums (123, 131: more registers than there are); the residual asked for in mid-tile (115).
+// tensor cores make less quickly (141); four accumulators with tiles of 128 columns (1024 x 4096 -> 1024 13.3 -> 13.9: it is
+// not the way to and fro); loads of 64 columns (118); the next K block's scales, or the look whether it is there, before the
+// last sums (123, 131: more registers than there are); the residual asked for in mid-tile (115).
 #include <cudaTypedefs.h>
 
 #include <atomic>
@@ -476,6 +478,20 @@ __global__ void __launch_bounds__(kThreadsB, 1)
             static_cast<float*>(E.y)[at] = v;
         };
         const bool res = !kGated && E.res;
+        auto write = [&](auto all, int64_t to) {
+#pragma unroll 1
+          for (int q0 = 0; q0 < rows; q0 += 16, to += 16 * (int64_t)E.d_out) {
+            auto in = [&](int q) { return decltype(all)::value || q0 + q < rows; };
+            float v[16];
+#pragma unroll
+            for (int q = 0; q < 16; ++q) v[q] = res && in(q) ? residual(to + q * (int64_t)E.d_out) : 0.f;
+#pragma unroll
+            for (int q = 0; q < 16; ++q) v[q] += turned[(q0 + q) * 32 + (lane ^ (q0 + q))];
+#pragma unroll
+            for (int q = 0; q < 16; ++q)
+              if (in(q)) put(to + q * (int64_t)E.d_out, v[q]);
+          }
+        };
 #pragma unroll
         for (int o = 0; o < kOut; ++o) {
           if (!there(o)) continue;
@@ -484,21 +500,13 @@ __global__ void __launch_bounds__(kThreadsB, 1)
           for (int i = 0; i < 32; ++i) turned[lane * 32 + (i ^ lane)] = acc[o][i];
           __syncwarp();
           if (column(o) + lane >= E.d_out) continue;
-          int64_t to = (int64_t)m0 * E.d_out + column(o) + lane;
-          if (rows == 32) {
-#pragma unroll 1
-            for (int q0 = 0; q0 < 32; q0 += 16, to += 16 * (int64_t)E.d_out) {
-              float v[16];
-#pragma unroll
-              for (int q = 0; q < 16; ++q) v[q] = res ? residual(to + q * (int64_t)E.d_out) : 0.f;
-#pragma unroll
-              for (int q = 0; q < 16; ++q) v[q] += turned[(q0 + q) * 32 + (lane ^ (q0 + q))];
-#pragma unroll
-              for (int q = 0; q < 16; ++q) put(to + q * (int64_t)E.d_out, v[q]);
-            }
-          } else {
-            for (int q = 0; q < rows; ++q, to += E.d_out) put(to, turned[q * 32 + (lane ^ q)] + (res ? residual(to) : 0.f));
-          }
+          const int64_t to = (int64_t)m0 * E.d_out + column(o) + lane;
+          if (rows == 32)
+            write(std::true_type{}, to);
+          else if (res)
+            write(std::false_type{}, to);
+          else
+            for (int q = 0; q < rows; ++q) put(to + q * (int64_t)E.d_out, turned[q * 32 + (lane ^ q)]);
         }
       }
     }

@@ -765,8 +765,9 @@ cudaError_t launch_skinny(const FeedForwardArgs& a, const Resident& r, int BN, c
 
 // Cycles that ff_skinny_kernel takes in tiles of BN tokens, and the pairs' kernels in tiles of BN rows of W: what a K block takes,
 // what ends a tile, and the way through.  Fitted to 130 sizes on GB300 (1 to 2048 tokens, d_in 1024 to 4096, 1024 to 12288
-// rows of W): the choice is 0.8% off the fastest on average, 15% at most.  With e4m3 a K block of many tokens takes
-// long, as its sums are scaled: 200 tokens of 1024 -> 1024 gated 6.1 us in tiles of 32, 7.7 in tiles of 128.
+// rows of W): the choice is 0.8% off the fastest on average, 15% at most; with e4m3 to 121 more (128 to 8192 tokens, each kind
+// of y, bias and residual): 0.7%, 11%.  With e4m3 a K block of many tokens takes long, as its sums are scaled: 200 tokens of
+// 1024 -> 1024 gated 6.1 us in tiles of 32, 7.7 in tiles of 128.
 int64_t skinny_cycles(const Resident& r, int64_t rows_of_w, int64_t N, int nkb, bool fp8, int BN) {
   const int64_t tiles = ((rows_of_w + kRows - 1) / kRows) * ((N + BN - 1) / BN);
   const int C = split_of(r, tiles, nkb);
@@ -791,7 +792,11 @@ int64_t tc_cycles(const FeedForwardArgs& a, const Resident& r, int BN) {
   const int width = a.gated ? BN / 2 : BN;
   const int64_t m_tiles = (a.N + 2 * kRows - 1) / (2 * kRows);
   const int64_t tiles = m_tiles * (((int64_t)a.d_out + width - 1) / width), waves = (tiles + r.of[2] - 1) / r.of[2];
-  if (a.dtype == MOLORA_E4M3) return 9200 + waves * (ff_k_blocks(a) * (200 + BN * 33 / 20) + 5400);
+  if (a.dtype == MOLORA_E4M3) {
+    // (rows of y that TMA cannot write: by the byte)
+    const int64_t by_lanes = ff_epilogue_of(a).tma_y ? 0 : 15 * width * (a.y_bf16 ? 2 : 4);
+    return 8000 + waves * (ff_k_blocks(a) * (150 + BN * 7 / 5) + 1000 + by_lanes);
+  }
   return 6300 + waves * (ff_k_blocks(a) * (160 + BN * 8 / 5) + 450);
 }
 
