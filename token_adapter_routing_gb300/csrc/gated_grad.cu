@@ -25,7 +25,8 @@ namespace {
 
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 32 * (kEpiWarps + 2);  // + TMA warp (8) + MMA warp (9)
-constexpr int kSets = 2;                        // staging boxes an epilogue warp
+constexpr int kSets = 2;                        // staging boxes an epilogue warp: all that it stores of a tile of 256 columns
+constexpr uint32_t kOutBox = 32 * kRowBytes;    // 32 rows of 64 columns
 constexpr uint32_t kStageA = kRows * kRowBytes;
 
 struct __align__(8) GCtrl {
@@ -230,42 +231,41 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else {
-    // epilogue: warps w and w + 4 share 32 rows and take chunks of 32 columns in turn
+    // epilogue: warps w and w + 4 share 32 rows and take chunks of 64 columns in turn
     const int quarter = warp & 3, side = warp >> 2;
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-    uint8_t* ring = sm + P.off_stage + (size_t)warp * kSets * kBox;
+    uint8_t* ring = sm + P.off_stage + (size_t)warp * kSets * kOutBox;
     int tc = 0, used = 0;
     bool ok = true;
     GTile t;
     for (int64_t i = 0; ok && tile_at(P, pair, i, rank, t); ++i) {
       const int32_t row = t.m0 + quarter * 32;
       const int64_t rows = t.x ? P.N : P.d_ff;
-      const int chunks = row < rows ? min(BN / 32, (P.d_in - t.n0 + 31) / 32) : 0;
+      const int chunks = row < rows ? min(BN / 64, (P.d_in - t.n0 + 63) / 64) : 0;
       ok = __all_sync(0xffffffffu, mbar_wait_spin(&ctrl->tfull[tc & 1], (uint32_t)(tc >> 1) & 1u, abort));
       if (!ok) break;
       tc_fence_after();
       const uint32_t base = tmem + lanes + (uint32_t)((tc & 1) * (P.tmem_cols / 2));
-      uint32_t r[32];
-      if (side < chunks) tmem_ld32_start(base + (uint32_t)(side * 32), r);
       for (int c = side; c < chunks; c += 2) {
-        tmem_ld_wait(r);
-        uint4 v[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          v[q] = make_uint4(pack_bf16(__uint_as_float(r[8 * q]), __uint_as_float(r[8 * q + 1])),
-                            pack_bf16(__uint_as_float(r[8 * q + 2]), __uint_as_float(r[8 * q + 3])),
-                            pack_bf16(__uint_as_float(r[8 * q + 4]), __uint_as_float(r[8 * q + 5])),
-                            pack_bf16(__uint_as_float(r[8 * q + 6]), __uint_as_float(r[8 * q + 7])));
-        if (c + 2 < chunks) tmem_ld32_start(base + (uint32_t)((c + 2) * 32), r);
-        uint8_t* box = ring + (size_t)(used & (kSets - 1)) * kBox;
+        uint32_t r[2][32];
+        tmem_ld32_start(base + (uint32_t)(c * 64), r[0]);
+        tmem_ld32_start(base + (uint32_t)(c * 64 + 32), r[1]);
+        uint8_t* box = ring + (size_t)(used & (kSets - 1)) * kOutBox;
         if (lane == 0) bulk_wait_read<kSets - 1>();  // the store that last left the box has read it
         __syncwarp();
+        tmem_ld_wait(r[0]);
+        tmem_ld_bind(r[1]);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) *reinterpret_cast<uint4*>(box + swz_offset((uint32_t)lane, (uint32_t)q, 64)) = v[q];
+        for (int q = 0; q < 8; ++q) {
+          const uint32_t(&v)[32] = r[q / 4];
+          const int i = 8 * (q & 3);
+          auto two = [&](int k) { return pack_bf16(__uint_as_float(v[i + k]), __uint_as_float(v[i + k + 1])); };
+          *reinterpret_cast<uint4*>(box + swz_offset((uint32_t)lane, (uint32_t)q, 128)) = make_uint4(two(0), two(2), two(4), two(6));
+        }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          tma_store_3d(t.x ? &map_dx : &map_dw, smem_u32(box), t.n0 + c * 32, row, t.plane);
+          tma_store_3d(t.x ? &map_dx : &map_dw, smem_u32(box), t.n0 + c * 64, row, t.plane);
           bulk_commit();
         }
         ++used;
@@ -342,22 +342,22 @@ cudaError_t launch_gated_grad(const GatedGradArgs& a, cudaStream_t stream) {
   }
   best(with_x, a.dW != nullptr);
   p.stage_bytes = kStageA + (uint32_t)(p.BN / 128) * kAtom;
-  const uint32_t boxes = kEpiWarps * kSets * kBox;
+  const uint32_t boxes = kEpiWarps * kSets * kOutBox;
   p.S = (int)((kMaxSmem - boxes - sizeof(GCtrl) - kSmemSlack) / p.stage_bytes);
   if (p.S > kMaxStages) p.S = kMaxStages;
   p.off_stage = (uint32_t)p.S * p.stage_bytes;
   p.off_ctrl = p.off_stage + boxes;
   p.tmem_cols = 2 * (uint32_t)p.BN;
   const auto BF = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  const auto S128 = CU_TENSOR_MAP_SWIZZLE_128B, S64 = CU_TENSOR_MAP_SWIZZLE_64B;
+  const auto S128 = CU_TENSOR_MAP_SWIZZLE_128B;
   CUtensorMap pk = {}, pm = {}, w = {}, x = {}, dx = {}, dw = {};
   if (with_x && (!linear_map_3d(&pk, BF, a.dproj, {F, 2, N}, {2 * half, 4 * half}, {64, 1, 128}, S128) ||
                !linear_map_3d(&w, BF, a.W, {D, F, 2}, {2 * D, 2 * F * D}, {64, 64, 1}, S128) ||
-               !linear_map_3d(&dx, BF, a.dx, {D, N, 1}, {2 * D, 2 * N * D}, {32, 32, 1}, S64)))
+               !linear_map_3d(&dx, BF, a.dx, {D, N, 1}, {2 * D, 2 * N * D}, {64, 32, 1}, S128)))
     return cudaErrorNotSupported;
   if (a.dW && (!linear_map_3d(&pm, BF, a.dproj, {F, 2, N}, {2 * half, 4 * half}, {64, 1, 64}, S128) ||
                !linear_map_3d(&x, BF, a.x, {D, N, 1}, {2 * D, 2 * N * D}, {64, 64, 1}, S128) ||
-               !linear_map_3d(&dw, BF, a.dW, {D, F, 2}, {2 * D, 2 * F * D}, {32, 32, 1}, S64)))
+               !linear_map_3d(&dw, BF, a.dW, {D, F, 2}, {2 * D, 2 * F * D}, {64, 32, 1}, S128)))
     return cudaErrorNotSupported;
   static std::atomic<uint64_t> allowed;
   const cudaError_t set = allow_smem(grad_tc_kernel, allowed, kMaxSmem);
