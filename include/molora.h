@@ -644,7 +644,7 @@ MOLORA_API molora_status molora_gated_linear(const void* x, molora_dtype dtype, 
  * [2 d_ff x d_in] or NULL (frozen weights, as when adapters are trained through them).  Outputs are overwritten, not added
  * to; N == 0 makes dW zero.  act' of RELU is 0 at 0.  Sums are fp32, outputs rounded once.  Sizes and alignment as for
  * molora_gated_linear; dproj, dx and dW are 16-byte aligned too.  No output shares memory with another array.  Results are
- * reproducible bit for bit.  Outputs that a wait that ran out left without their sums stay as they were.
+ * reproducible bit for bit.  Lost waits as for molora_linear_blocks.
  */
 MOLORA_API molora_status molora_gated_linear_backward(const void* x, molora_dtype dtype, int64_t N, int32_t d_in, const void* W,
                                            int32_t d_ff, molora_activation act, const void* dh, void* dproj, void* dx,

@@ -159,3 +159,32 @@ def test_backward_writes_nothing_wrong(libs, which, cta, warp):
         assert torch.isnan(out[2]).any() and torch.isnan(out[0]).any() and torch.isnan(out[1]).any()
     out, e = run(lost)
     assert e == 0 and all(torch.equal(w, v) for w, v in zip(want, out))
+
+
+@pytest.mark.parametrize("which", ["feed_forward", "gated_grad"])
+@pytest.mark.parametrize("cta, warp", [(1, 5), (0, 9), (0, 0)])
+def test_few_tokens_backward_loses_to_nan(libs, which, cta, warp):
+    """Few tokens' dx is a product of its own (csrc/feed_forward.cu), which makes NaN of what it loses."""
+    m, lib, lost = libs
+    g = gen(5)
+    N, d, F = 64, 512, 2048
+    x, _, W, _ = inputs(g, BF, N, d, 2 * F, 0)
+    dh = randn(g, N, F).to(BF)
+
+    def run(lib):
+        e = torch.zeros(1, dtype=torch.int32, device="cuda")
+        out = old(N, d), old(2 * F, d), old(N, 2, F)
+        call(lib.molora_gated_linear_backward, p(x), 1, N, d, p(W), F, 2, p(dh), p(out[2]), p(out[0]), p(out[1]), p(e))
+        return out, e.item()
+    want, e = run(lib)
+    assert e == 0
+    got = []
+    with_lost(libs, which, cta, warp, lambda lib: got.extend(run(lib)))
+    (out, e) = got
+    assert e == m.DEV_WAIT_TIMEOUT
+    if which == "gated_grad":  # dW's alone
+        assert torch.equal(out[0], want[0]) and torch.equal(out[2], want[2]) and ((out[1] == want[1]) | (out[1] == OLD)).all()
+    else:
+        assert all(((v == w) | torch.isnan(v)).all() for w, v in zip(want, out)) and torch.isnan(out[0]).any()
+    out, e = run(lost)
+    assert e == 0 and all(torch.equal(w, v) for w, v in zip(want, out))
