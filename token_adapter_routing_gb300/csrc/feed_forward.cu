@@ -736,6 +736,7 @@ cudaError_t launch_skinny_kernel(const FEpi& e, const FSkinnyPlan& p, int32_t* e
     const cudaError_t set = allow_smem(kernel, allowed[n], kMaxSmem);
     if (set != cudaSuccess) return set;
     const int64_t ctas = (int64_t)p.o_tiles * p.t_tiles * p.C;
+    if (ctas > INT32_MAX) return cudaErrorNotSupported;
     return launch_kernel(kernel, dim3((unsigned)ctas), dim3(kThreads), p.smem, stream, p.C, e, p, err_word, mx, mw);
   };
   switch (p.BN) {
