@@ -164,6 +164,22 @@ def blocks64(x, sx, W, sw, b, act, res):
 
 
 @pytest.mark.parametrize("y_dtype", [BF, F32])
+@pytest.mark.parametrize("d_in", [1024, 2304])
+@pytest.mark.parametrize("d_out", [2047, 2056])
+def test_linear_blocks_many_tiles_a_pair(m, y_dtype, d_in, d_out):
+    """More tiles than pairs of CTAs, of one span of scales and of two, with a bias for each column: every call the same bits."""
+    N, g = 3001, gen(d_in + d_out)
+    x, sx = e4m3(g, N, d_in, N)
+    W, sw = e4m3(g, d_out, d_in, blocks(d_out))
+    b, res = 100 * randn(g, d_out), (100 * randn(g, N, d_out)).to(y_dtype)
+    run = lambda: m.molora_linear_blocks(x, sx, W, sw, bias=beside_nan(b), act="silu", residual=res, out_dtype=y_dtype)  # noqa: E731
+    y = run()
+    want, tol = blocks64(x, sx, W, sw, b, "silu", res)
+    within(y, want, tol + (want.abs() + tol) * HALF[y_dtype])
+    assert all(torch.equal(run(), y) for _ in range(10))
+
+
+@pytest.mark.parametrize("y_dtype", [BF, F32])
 @pytest.mark.parametrize("N, d_in, d_out", [(1, 16, 1), (1, 4096, 512), (3, 128, 130), (16, 272, 64), (17, 2064, 257), (33, 512, 8),
                                             (64, 1024, 300), (100, 144, 1000), (129, 640, 384), (257, 256, 128), (300, 1040, 520),
                                             (512, 512, 2048), (1237, 2064, 1541), (2100, 384, 2304), (4096, 128, 1000), (5000, 48, 320)])
