@@ -1,0 +1,96 @@
+"""The feed-forward kernels at the ends of their ranges: activations over every gate, beside values that have none.
+
+Tolerances (u = 2^-24, half a step of fp32): an activation's exponent z, 126 at most before its power is flushed, is made with up to
+four roundings of it, so its power is off by 126 ln 2 * 4 u = 350 u; the power itself (4 u), the sum, the products and the
+reciprocal add fewer than 30: 384 u of the result.  Below 2^-126 powers are 0, where v / (1 + 2^z) is below 2^-119."""
+
+import math
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+BF, F32, FP8 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
+HALF = {BF: 2.0 ** -8, F32: U}
+ACTS = {"none": lambda v: v, "relu": torch.relu, "silu": lambda v: v * torch.sigmoid(v),
+        "gelu": lambda v: 0.5 * v * torch.erfc(-v / math.sqrt(2)),
+        "gelu_tanh": lambda v: v * torch.sigmoid(2 * math.sqrt(2 / math.pi) * (v + 0.044715 * v ** 3))}
+
+
+@pytest.fixture(scope="module")
+def m():
+    from token_adapter_routing_gb300 import build
+    build.build()
+    import token_adapter_routing_gb300 as mod
+    mod.load_library()
+    return mod
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def randn(g, *shape):
+    return torch.randn(*shape, generator=g, device="cuda")
+
+
+def within(got, want, tol):
+    over = (got.double() - want).abs() - tol
+    assert not torch.isnan(over).any(), "NaN"
+    i = int(over.argmax())
+    assert over.flatten()[i] <= 0, f"element {i}: got {got.double().flatten()[i].item()}, want {want.flatten()[i].item()}"
+
+
+# ---------------------------------------------------------------------------------------- activations
+@pytest.mark.parametrize("y_dtype", [F32, BF])
+@pytest.mark.parametrize("odd", [False, True])
+@pytest.mark.parametrize("N", [1, 32, 512])
+@pytest.mark.parametrize("act", ["relu", "silu", "gelu", "gelu_tanh"])
+def test_activations_over_the_whole_range(m, act, N, odd, y_dtype):
+    """act(bias) of every finite bf16 value through the block-scaled product of zeros (few tokens, many, rows that start
+    anywhere), in an order that puts values of all sizes beside one another."""
+    v = torch.arange(1 << 16, dtype=torch.int32, device="cuda").to(torch.int16).view(BF).float()
+    v = v[torch.isfinite(v)]
+    v = v[(v == 0) | (v.abs() >= 2.0 ** -118)]
+    v = torch.cat([v, v[torch.randperm(v.numel(), generator=gen(1), device="cuda")]])  # neighbours in size, then any
+    v = v[:v.numel() // 8 * 8 - odd]
+    x, W = torch.zeros(N, 16, device="cuda").to(FP8), torch.zeros(v.numel(), 16, device="cuda").to(FP8)
+    one = torch.ones(N, 1, device="cuda"), torch.ones(-(-v.numel() // 128), 1, device="cuda")
+    y = m.molora_linear_blocks(x, one[0], W, one[1], bias=v.clone(), act=act, out_dtype=y_dtype)
+    want = ACTS[act](v.double())
+    within(y, want.expand(N, -1), want.abs() * (384 * U + HALF[y_dtype]) + 2.0 ** -118)
+
+
+@pytest.mark.parametrize("N", [32, 4096])
+@pytest.mark.parametrize("act", ["relu", "silu", "gelu", "gelu_tanh"])
+def test_gates_over_the_whole_range(m, act, N):
+    """Every e4m3 value times scales of all sizes as the gate, each exact, through few tokens' kernel and many's."""
+    w = torch.arange(256, dtype=torch.int32, device="cuda").to(torch.uint8).view(FP8).float()
+    w = w[torch.isfinite(w)]
+    w = torch.cat([w, w[torch.randperm(w.numel(), generator=gen(2), device="cuda")]])
+    w = w.repeat(4)[:2032]
+    F = w.numel()
+    x, W = torch.zeros(N, 16, device="cuda"), torch.zeros(2 * F, 16, device="cuda")
+    x[:, 0], W[:F, 0], W[F:, 0] = 1, w, 1
+    sx = torch.exp2(torch.linspace(-24, 8, N, device="cuda"))
+    sw = torch.ones(2 * -(-F // 128), 1, device="cuda")
+    h = m.molora_gated_linear(x.to(FP8), W.to(FP8), act=act, x_scale=sx[:, None].contiguous(), w_scale=sw)
+    gate = sx.double()[:, None] * w.double()   # (rounds once to fp32, and act' is 1.13 at most, or what moves |z| ln 2 <= 88 by u)
+    want = ACTS[act](gate) * sx.double()[:, None]
+    within(h, want, want.abs() * (512 * U + HALF[BF]) + 2.0 ** -118 * sx.double()[:, None] + 2.0 ** -126)
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+@pytest.mark.parametrize("N", [8, 512])
+def test_activations_beside_nan_and_infinity(m, act, N):
+    """A NaN or an infinity in one column leaves those beside it within their own tolerance."""
+    g = gen(N)
+    v = 40 * randn(g, 4096)
+    v[1::7], v[3::11], v[5::13], v[8::17] = math.nan, math.inf, -math.inf, -3e38
+    x, W = torch.zeros(N, 16, device="cuda").to(FP8), torch.zeros(4096, 16, device="cuda").to(FP8)
+    y = m.molora_linear_blocks(x, torch.ones(N, 1, device="cuda"), W, torch.ones(32, 1, device="cuda"), bias=v, act=act)
+    assert torch.isnan(y[:, torch.isnan(v)]).all() and (y[:, v == math.inf] == math.inf).all()
+    want = ACTS[act](v.double())[torch.isfinite(v)]
+    within(y[:, torch.isfinite(v)], want.expand(N, -1), want.abs() * 385 * U + 2.0 ** -118)

@@ -83,23 +83,53 @@ __device__ __forceinline__ int piece_output(int side, int h) {
   return (side + kSides * (kGated ? h >> 1 : h)) * 32;
 }
 
-// SiLU, and the tanh form of GELU, of 32 values (see activate) with one reciprocal for two: 1 / a = b / (a b).  A tile's
-// activations are not under any MMA here, and their powers and reciprocals are what bounds them (gated 4096 x 2048 ->
-// 6144 96.0 -> 93.9 us).  Where 1 + 2^z passes 2^60 its reciprocal counts as 0, so that no product overflows.
+// max(a, b, c), NaN if any is
+__device__ __forceinline__ float max_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// SiLU, and the tanh form of GELU, of 32 values v / (1 + 2^z) (see activate) with one reciprocal for two: 1 / a = b / (a b).
+// A tile's activations are not under any MMA here, and their powers and reciprocals are what bounds them (gated 4096 x
+// 2048 -> 6144 96.0 -> 93.9 us).  A pair whose product passes 2^125 (SiLU: v that sum to less than -86) or is NaN has a
+// reciprocal each, in a branch of its own, which costs less than limits on every z (8192 x 1024 -> 1541 bf16, tanh, 54.8 -> 52.6
+// us; gated 8192 x 1024 -> 1024 24.4 -> 24.6).  A value's last bits depend on its pair, and on nothing else.
 __device__ __forceinline__ void activate_pairs(float (&v)[32], bool silu) {
+  constexpr float kMost = 0x1p125f;  // (its reciprocal is a normal number)
+  float d[32], p[16];
 #pragma unroll
-  for (int i = 0; i < 32; i += 2) {
-    float z[2], d[2], r;
+  for (int i = 0; i < 32; ++i) {
+    const float x = v[i], z = silu ? -1.4426950408889634f * x : x * fmaf(-0.10294324f * x, x, -2.3022082f);
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(d[i]) : "f"(z));
+    d[i] += 1.f;
+    if (i & 1) p[i / 2] = d[i - 1] * d[i];
+  }
+  auto over = [](float a) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(a));
+    return r;
+  };
+  float most[5];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const float x = v[i + j];
-      z[j] = silu ? -1.4426950408889634f * x : x * fmaf(-0.10294324f * x, x, -2.3022082f);
-      asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(d[j]) : "f"(fminf(z[j], 60.f)));
-      d[j] += 1.f;
+  for (int i = 0; i < 5; ++i) most[i] = max_nan(p[3 * i], p[3 * i + 1], p[3 * i + 2]);
+  most[0] = max_nan(most[0], most[1], most[2]);
+  most[0] = max_nan(most[0], max_nan(most[3], most[4], p[15]), most[0]);
+  if (most[0] < kMost) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float r = over(p[i]);
+      v[2 * i] *= r * d[2 * i + 1];
+      v[2 * i + 1] *= r * d[2 * i];
     }
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d[0] * d[1]));
-    v[i] *= z[0] > 60.f ? 0.f : r * d[1];
-    v[i + 1] *= z[1] > 60.f ? 0.f : r * d[0];
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const bool one = p[i] < kMost;
+      const float r0 = over(one ? p[i] : d[2 * i]), r1 = over(one ? p[i] : d[2 * i + 1]);
+      v[2 * i] *= one ? r0 * d[2 * i + 1] : r0;
+      v[2 * i + 1] *= one ? r1 * d[2 * i] : r1;
+    }
   }
 }
 
