@@ -642,9 +642,10 @@ MOLORA_API molora_status molora_gated_linear(const void* x, molora_dtype dtype, 
  * dh bf16 [N x d_ff];  dproj bf16 [N x 2 x roundup8(d_ff)]: dg and du, rounded, which the two products read, an output
  * (columns from d_ff on are unspecified);  dx bf16 [N x d_in] or NULL (the weights' gradient alone);  dW bf16
  * [2 d_ff x d_in] or NULL (frozen weights, as when adapters are trained through them).  Outputs are overwritten, not added
- * to; N == 0 makes dW zero.  act' of RELU is 0 at 0.  Sums are fp32, outputs rounded once.  Sizes and alignment as for
- * molora_gated_linear; dproj, dx and dW are 16-byte aligned too.  No output shares memory with another array.  Results are
- * reproducible bit for bit.  Lost waits as for molora_linear_blocks.
+ * to; N == 0 makes dW zero.  act' of RELU is 0 at 0.  Sums are fp32, on the tensor cores in chains of 8192 terms at most (their
+ * additions cut what they lose: sums of one sign come out up to 3e-5 short, whatever N and d_ff); outputs are rounded once.
+ * Sizes and alignment as for molora_gated_linear; dproj, dx and dW are 16-byte aligned too.  No output shares memory with
+ * another array.  Results are reproducible bit for bit.  Lost waits as for molora_linear_blocks.
  */
 MOLORA_API molora_status molora_gated_linear_backward(const void* x, molora_dtype dtype, int64_t N, int32_t d_in, const void* W,
                                            int32_t d_ff, molora_activation act, const void* dh, void* dproj, void* dx,

@@ -94,3 +94,61 @@ def test_activations_beside_nan_and_infinity(m, act, N):
     assert torch.isnan(y[:, torch.isnan(v)]).all() and (y[:, v == math.inf] == math.inf).all()
     want = ACTS[act](v.double())[torch.isfinite(v)]
     within(y[:, torch.isfinite(v)], want.expand(N, -1), want.abs() * 385 * U + 2.0 ** -118)
+
+
+# ---------------------------------------------------------------------------------------- long sums
+def positive(g, rows, cols, by_row=False):
+    """Values from 1/2 to 1, of columns (or rows) of different sizes: sums of them that fall anywhere between two bf16 values."""
+    s = torch.exp2(torch.rand((rows, 1) if by_row else (1, cols), generator=g, device="cuda"))
+    return ((0.5 + 0.5 * torch.rand(rows, cols, generator=g, device="cuda")) * s).to(BF)
+
+
+def drift(got, want):
+    """How far the outputs are off together, and what may be: 2^-15, a 128th of what bf16's rounding may do to each, for what a
+    tensor core's additions cut; the mean of that rounding (2^-8 at most of an output, 2^-8 / sqrt(3) at most on the root mean
+    square, either way: six deviations); 2^-20 for fp32's few additions.  An addition that cuts to fp32 loses half a step, 2^-25 of
+    the sum at least, on the mean: a single chain of n MMAs of 16 terms is 2^-25 sum_j j / n = 2^-26 n short at least, 1.2e-4 for
+    2^17 terms and 2.4e-4 for 2^18."""
+    off = ((got.double() - want) / want).mean().abs().item()
+    return off, 2.0 ** -15 + 6 * 2.0 ** -8 / math.sqrt(3 * want.numel()) + 2.0 ** -20
+
+
+def test_many_tokens_dw_does_not_drift(m):
+    """dW's sums run over the tokens, however many there are."""
+    g, N, d, F = gen(70), (1 << 18) + 77, 512, 256
+    x, W, dh = positive(g, N, d), positive(g, 2 * F, d), positive(g, N, F)
+    dx, dW, dproj = m.molora_gated_linear_backward(x, W, dh, act="none", want_dx=False)
+    want = torch.zeros(2 * F, d, dtype=torch.float64, device="cuda")
+    for t in range(0, N, 1 << 16):
+        want += dproj[t:t + (1 << 16)].view(-1, 2 * F).double().T @ x[t:t + (1 << 16)].double()
+    off, most = drift(dW, want)
+    assert off <= most, (off, most)
+
+
+def test_wide_blocks_dx_does_not_drift(m):
+    """dx's sums run over both projections' columns."""
+    g, N, d, F = gen(71), 8192, 512, 1 << 16
+    x, W, dh = (positive(g, N, d) / 512).to(BF), positive(g, 2 * F, d), positive(g, N, F, by_row=True)
+    dx, _, dproj = m.molora_gated_linear_backward(x, W, dh, act="none", want_dW=False)
+    want = torch.zeros(N, d, dtype=torch.float64, device="cuda")
+    for f in range(0, 2 * F, 1 << 14):
+        want += dproj.view(N, 2 * F)[:, f:f + (1 << 14)].double() @ W[f:f + (1 << 14)].double()
+    off, most = drift(dx, want)
+    assert off <= most, (off, most)
+
+
+@pytest.mark.parametrize("N, d, F", [(8192, 264, 130), (8193, 264, 130), (40000, 136, 65), (300, 520, 20000), (3000, 1032, 4100)])
+def test_gradients_of_long_sums(m, N, d, F):
+    """Sums of one chain of K blocks, one more, several, and of dx's and dW's different numbers of them, every output against the
+    64-bit sums of the same dproj (n additions each lose at most a step of a partial sum: 2 u n S), and the same bits again."""
+    g = gen(N + F)
+    x, W, dh = randn(g, N, d).to(BF), (randn(g, 2 * F, d) / math.sqrt(d)).to(BF), randn(g, N, F).to(BF)
+    e = torch.zeros(1, dtype=torch.int32, device="cuda")
+    dx, dW, dproj = m.molora_gated_linear_backward(x, W, dh, err_word=e)
+    assert e.item() == 0
+    dp = torch.cat([dproj[:, 0, :F], dproj[:, 1, :F]], dim=1).double()
+    for got, want, S, n in ((dx, dp @ W.double(), dp.abs() @ W.double().abs(), 2 * F), (dW, dp.T @ x.double(), dp.abs().T @ x.double().abs(), N)):
+        tol = 2 * U * n * S
+        within(got, want, tol + (want.abs() + tol) * HALF[BF] + 2.0 ** -118)
+    again = m.molora_gated_linear_backward(x, W, dh)
+    assert torch.equal(again[0], dx) and torch.equal(again[1], dW)

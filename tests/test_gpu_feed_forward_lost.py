@@ -188,3 +188,28 @@ def test_few_tokens_backward_loses_to_nan(libs, which, cta, warp):
         assert all(((v == w) | torch.isnan(v)).all() for w, v in zip(want, out)) and torch.isnan(out[0]).any()
     out, e = run(lost)
     assert e == 0 and all(torch.equal(w, v) for w, v in zip(want, out))
+
+
+@pytest.mark.parametrize("cta, warp", [(0, 0), (1, 5), (0, 9)])
+def test_chains_of_long_sums_write_nothing_wrong(libs, cta, warp):
+    """Sums of several chains of K blocks (over 9000 tokens, and over 2 x 4200 columns): a lost chain is a lost tile."""
+    m, lib, lost = libs
+    g = gen(6)
+    N, d, F = 9000, 256, 4200
+    x, _, W, _ = inputs(g, BF, N, d, 2 * F, 0)
+    dh = randn(g, N, F).to(BF)
+
+    def run(lib):
+        e = torch.zeros(1, dtype=torch.int32, device="cuda")
+        out = old(N, d), old(2 * F, d), old(N, 2, F)
+        call(lib.molora_gated_linear_backward, p(x), 1, N, d, p(W), F, 2, p(dh), p(out[2]), p(out[0]), p(out[1]), p(e))
+        return out, e.item()
+    want, e = run(lib)
+    assert e == 0
+    got = []
+    with_lost(libs, "gated_grad", cta, warp, lambda lib: got.extend(run(lib)))
+    (out, e) = got
+    assert e == m.DEV_WAIT_TIMEOUT
+    assert all(((v == w) | (v == OLD)).all() for w, v in zip(want, out))
+    out, e = run(lost)
+    assert e == 0 and all(torch.equal(w, v) for w, v in zip(want, out))

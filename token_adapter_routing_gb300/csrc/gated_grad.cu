@@ -103,6 +103,8 @@ __device__ __forceinline__ bool tile_at(const GPlan& P, int32_t pair, int64_t j,
 // map_pk, map_pm: dproj [N x 2 x d_ff] in boxes of 128 tokens x 64 columns (K-major rows of dx's product), and of 64
 // tokens x 64 (MN-major rows of dW's).  map_b[0], map_b[1]: W [2 x d_ff x d_in] and x [1 x N x d_in] in boxes of 64 x 64.
 // map_dx, map_dw: the outputs, [1 x N x d_in] and [2 x d_ff x d_in].
+// kLong: some tile has more than kChain K blocks, whose chains registers add.
+template <bool kLong>
 __global__ void __launch_bounds__(kThreads, 1)
     grad_tc_kernel(const GPlan P, int32_t* err_word, const __grid_constant__ CUtensorMap map_pk,
                    const __grid_constant__ CUtensorMap map_pm, const __grid_constant__ CUtensorMap map_w,
@@ -206,28 +208,32 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t phase = 0;
       bool ok = true;
       GTile t;
-      for (; ok && tile_at(P, pair, tc, rank, t); ++tc) {
+      for (int64_t i = 0; ok && tile_at(P, pair, i, rank, t); ++i) {
         const uint32_t idesc = idesc_bf16_f32(2 * kRows, (uint32_t)BN, !t.x, true);
         const uint32_t a_lo = t.x ? k_lo : m_lo, a_step = t.x ? 2 : 16 * kRowBytes / 16;
-        const int buf = tc & 1;
-        if (tc >= 2 && !mbar_wait_spin(&ctrl->tempty[buf], (uint32_t)((tc >> 1) - 1) & 1u, abort)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t d = tmem + (uint32_t)(buf * (P.tmem_cols / 2));
-        for (int kb = 0; kb < t.kbs; ++kb) {
-          if (!mbar_wait_spin(&ctrl->full[s], phase, abort)) {
+        for (int from = 0; ok && from < t.kbs; ++tc) {
+          const int to = kLong ? min(from + kChain, t.kbs) : t.kbs;
+          const int buf = tc & 1;
+          if (tc >= 2 && !mbar_wait_spin(&ctrl->tempty[buf], (uint32_t)((tc >> 1) - 1) & 1u, abort)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t at = (uint32_t)s * (P.stage_bytes >> 4);
-          umma_stage_steps<true>(d, a_lo + at, m_lo + (kStageA >> 4) + at, hi, hi, idesc, kb != 0, a_step, 16 * kRowBytes / 16);
-          umma_commit_pair(&ctrl->empty[s], both);
-          if (++s == S) s = 0, phase ^= 1;
+          const uint32_t d = tmem + (uint32_t)(buf * (P.tmem_cols / 2));
+          for (int kb = from; kb < to; ++kb) {
+            if (!mbar_wait_spin(&ctrl->full[s], phase, abort)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t at = (uint32_t)s * (P.stage_bytes >> 4);
+            umma_stage_steps<true>(d, a_lo + at, m_lo + (kStageA >> 4) + at, hi, hi, idesc, kb != from, a_step, 16 * kRowBytes / 16);
+            umma_commit_pair(&ctrl->empty[s], both);
+            if (++s == S) s = 0, phase ^= 1;
+          }
+          if (ok) umma_commit_pair(&ctrl->tfull[buf], both);
+          from = to;
         }
-        if (ok) umma_commit_pair(&ctrl->tfull[buf], both);
       }
       if (!ok) report(err_word, MOLORA_DEV_WAIT_TIMEOUT);
       umma_commit_pair(&ctrl->done, both);  // arrives in both CTAs once every MMA has completed
@@ -245,24 +251,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int32_t row = t.m0 + quarter * 32;
       const int64_t rows = t.x ? P.N : P.d_ff;
       const int chunks = row < rows ? min(BN / 64, (P.d_in - t.n0 + 63) / 64) : 0;
-      ok = __all_sync(0xffffffffu, mbar_wait_spin(&ctrl->tfull[tc & 1], (uint32_t)(tc >> 1) & 1u, abort));
-      if (!ok) break;
-      tc_fence_after();
-      const uint32_t base = tmem + lanes + (uint32_t)((tc & 1) * (P.tmem_cols / 2));
-      for (int c = side; c < chunks; c += 2) {
-        uint32_t r[2][32];
-        tmem_ld32_start(base + (uint32_t)(c * 64), r[0]);
-        tmem_ld32_start(base + (uint32_t)(c * 64 + 32), r[1]);
+      auto sums_ready = [&]() {
+        ok = __all_sync(0xffffffffu, mbar_wait_spin(&ctrl->tfull[tc & 1], (uint32_t)(tc >> 1) & 1u, abort));
+        if (ok) tc_fence_after();
+        return ok;
+      };
+      auto sums_taken = [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster_read(dsmem_addr(smem_u32(&ctrl->tempty[tc & 1]), 0));
+        ++tc;
+      };
+      // 64 columns of this warp's rows, sum(k) each, to the outputs
+      auto put = [&](int c, auto sum) {
         uint8_t* box = ring + (size_t)(used & (kSets - 1)) * kOutBox;
         if (lane == 0) bulk_wait_read<kSets - 1>();  // the store that last left the box has read it
         __syncwarp();
-        tmem_ld_wait(r[0]);
-        tmem_ld_bind(r[1]);
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
-          const uint32_t(&v)[32] = r[q / 4];
-          const int i = 8 * (q & 3);
-          auto two = [&](int k) { return pack_bf16(__uint_as_float(v[i + k]), __uint_as_float(v[i + k + 1])); };
+          auto two = [&](int k) { return pack_bf16(sum(8 * q + k), sum(8 * q + k + 1)); };
           *reinterpret_cast<uint4*>(box + swz_offset((uint32_t)lane, (uint32_t)q, 128)) = make_uint4(two(0), two(2), two(4), two(6));
         }
         fence_proxy_async_smem();
@@ -272,11 +279,43 @@ __global__ void __launch_bounds__(kThreads, 1)
           bulk_commit();
         }
         ++used;
+      };
+      if (kLong && t.kbs > kChain) {
+        float sums[2][64];  // of this warp's chunks
+#pragma unroll
+        for (int k = 0; k < 64; ++k) sums[0][k] = sums[1][k] = 0.f;
+        for (int left = t.kbs; left > 0 && sums_ready(); left -= kChain) {
+          const uint32_t base = tmem + lanes + (uint32_t)((tc & 1) * (P.tmem_cols / 2));
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            if (side + 2 * n >= chunks) continue;
+#pragma unroll
+            for (int h = 0; h < 64; h += 16) {
+              float r[16];
+              tmem_ld16(base + (uint32_t)((side + 2 * n) * 64 + h), r);
+#pragma unroll
+              for (int k = 0; k < 16; ++k) sums[n][h + k] += r[k];
+            }
+          }
+          sums_taken();
+        }
+        if (!ok) break;
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+          if (side + 2 * n < chunks) put(side + 2 * n, [&](int k) { return sums[n][k]; });
+      } else {
+        if (!sums_ready()) break;
+        const uint32_t base = tmem + lanes + (uint32_t)((tc & 1) * (P.tmem_cols / 2));
+        for (int c = side; c < chunks; c += 2) {
+          uint32_t r[2][32];
+          tmem_ld32_start(base + (uint32_t)(c * 64), r[0]);
+          tmem_ld32_start(base + (uint32_t)(c * 64 + 32), r[1]);
+          tmem_ld_wait(r[0]);
+          tmem_ld_bind(r[1]);
+          put(c, [&](int k) { return __uint_as_float(r[k / 32][k % 32]); });
+        }
+        sums_taken();
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster_read(dsmem_addr(smem_u32(&ctrl->tempty[tc & 1]), 0));
-      ++tc;
     }
     if (!ok) {
       *abort = 1;
@@ -362,12 +401,16 @@ cudaError_t launch_gated_grad(const GatedGradArgs& a, cudaStream_t stream) {
                !linear_map_3d(&x, BF, a.x, {D, N, 1}, {2 * D, 2 * N * D}, {64, 64, 1}, S128) ||
                !linear_map_3d(&dw, BF, a.dW, {D, F, 2}, {2 * D, 2 * F * D}, {64, 32, 1}, S128)))
     return cudaErrorNotSupported;
-  static std::atomic<uint64_t> allowed;
-  const cudaError_t set = allow_smem(grad_tc_kernel, allowed, kMaxSmem);
-  if (set != cudaSuccess) return set;
-  const dim3 grid((unsigned)(2 * p.pairs));
-  // one CTA an SM, alone: an allocation of TMEM never waits for another CTA's (see linear.cu)
-  return launch_kernel(grad_tc_kernel, grid, dim3(kThreads), kMaxSmem, stream, 2, p, a.err_word, pk, pm, w, x, dx, dw);
+  auto go = [&](auto kernel, std::atomic<uint64_t>& allowed) {
+    const cudaError_t set = allow_smem(kernel, allowed, kMaxSmem);
+    if (set != cudaSuccess) return set;
+    const dim3 grid((unsigned)(2 * p.pairs));
+    // one CTA an SM, alone: an allocation of TMEM never waits for another CTA's (see linear.cu)
+    return launch_kernel(kernel, grid, dim3(kThreads), kMaxSmem, stream, 2, p, a.err_word, pk, pm, w, x, dx, dw);
+  };
+  static std::atomic<uint64_t> allowed[2];
+  const bool longer = (p.tiles_x && p.kb_x > kChain) || (p.tiles_w && p.kb_w > kChain);
+  return longer ? go(grad_tc_kernel<true>, allowed[0]) : go(grad_tc_kernel<false>, allowed[1]);
 }
 
 }  // namespace molora

@@ -182,6 +182,12 @@ constexpr uint32_t kRowBytes = 128; // bytes of K per stage
 // More bytes in flight take longer to come: one token, 4096 x 4096 bf16 from HBM 9.4 us with 4 stages, 8.8
 // with 8, 10.0 with 12 (from L2 7.1, 7.4, 8.2).
 constexpr int kMaxStages = 8;
+// K blocks of 64 bf16 that many tokens' kernels with 16-bit outputs sum in TMEM before fp32 registers take over.  A tensor core's
+// additions cut what they lose, so sums of one sign come out short, the more the longer the chain: measured 1.0e-5 after 64
+// blocks, 2.9e-5 after 128, 7.5e-5 after 256, 1.6e-3 (four tenths of bf16's half step, for every output) after 4096, which 2^18
+// tokens' dW is.  At 128 taking the chains costs nothing that shows (16000 tokens, 4096 -> 8192 3709 us for both gradients, 3694
+// in one chain, 3747 in chains of 64).  Sums that are no longer, those of most calls, keep nothing in registers.
+constexpr int kChain = 128;
 constexpr uint32_t kTurn = 4096;    // 32 x 32 values of fp32 y
 constexpr size_t kMaxSmem = 227 * 1024;
 constexpr size_t kSmemSlack = 1024;
