@@ -621,7 +621,8 @@ MOLORA_API molora_status molora_linear_blocks(const void* x, const float* x_scal
  * x [N x d_in] and W [2 d_ff x d_in], the d_ff rows of Wg before those of Wu, share dtype: MOLORA_BF16, or MOLORA_E4M3
  * with a scale for each block of 128: x_scale fp32 [N x ceil(d_in / 128)] and w_scale fp32
  * [2 ceil(d_ff / 128) x ceil(d_in / 128)], Wg's blocks of rows before Wu's; both NULL with MOLORA_BF16.  h bf16 [N x d_ff].
- * g and u stay in fp32; h is made of them unrounded and rounded once.
+ * g and u stay in fp32 (with MOLORA_BF16 in chains of 8192 terms at most on the tensor cores, as molora_gated_linear_backward's
+ * sums); h is made of them unrounded and rounded once.
  * d_in is a multiple of 8 (MOLORA_BF16) or 16 (MOLORA_E4M3), else MOLORA_ERR_UNSUPPORTED; d_ff up to 2^30 - 512, N and d_in
  * up to 2^31 - 1024; x and W are 16-byte aligned, the other arrays start on a boundary of their element's size.  h shares no
  * memory with another array.  Results are reproducible bit for bit.  Lost waits as for molora_linear_blocks.

@@ -152,3 +152,45 @@ def test_gradients_of_long_sums(m, N, d, F):
         within(got, want, tol + (want.abs() + tol) * HALF[BF] + 2.0 ** -118)
     again = m.molora_gated_linear_backward(x, W, dh)
     assert torch.equal(again[0], dx) and torch.equal(again[1], dW)
+
+
+def wide_product(x, W):
+    return sum(x[:, c:c + (1 << 14)].double() @ W[:, c:c + (1 << 14)].double().T for c in range(0, x.shape[1], 1 << 14))
+
+
+def test_wide_inputs_do_not_drift(m):
+    """The projections' sums run over d_in, in the forward pass (h has two of them as factors) and in dproj."""
+    g, d = gen(72), 1 << 17
+    x, W = (positive(g, 8192, d, by_row=True) / 256).to(BF), positive(g, 1024, d, by_row=True)
+    h = m.molora_gated_linear(x, W, act="none")
+    p = wide_product(x, W)
+    off, most = drift(h, p[:, :512] * p[:, 512:])
+    assert off <= most + 2.0 ** -15, (off, most)
+    dh = positive(g, 2048, 512)
+    _, _, dproj = m.molora_gated_linear_backward(x[:2048], W, dh, act="none", want_dx=False, want_dW=False)
+    off, most = drift(dproj, torch.stack([p[:2048, 512:], p[:2048, :512]], dim=1) * dh.double()[:, None])
+    assert off <= most, (off, most)
+
+
+@pytest.mark.parametrize("N, d, F", [(9000, 8192, 264), (9000, 8200, 265), (9001, 20000, 250)])
+def test_projections_of_long_sums(m, N, d, F):
+    """d_in of one chain of K blocks, one more, several: g and u are within 2 u d S, S = sum |x w|, of their 64-bit sums, and
+    SiLU's slope is 1.1 at most."""
+    g = gen(d)
+    x, W, dh = randn(g, N, d).to(BF), (randn(g, 2 * F, d) / math.sqrt(d)).to(BF), randn(g, N, F).to(BF)
+    e = torch.zeros(1, dtype=torch.int32, device="cuda")
+    h = m.molora_gated_linear(x, W, err_word=e)
+    _, _, dproj = m.molora_gated_linear_backward(x, W, dh, want_dx=False, want_dW=False, err_word=e)
+    assert e.item() == 0
+    gate, up = wide_product(x, W).split(F, dim=1)
+    eg, eu = (2 * U * d * wide_product(x.abs(), W.abs())).split(F, dim=1)
+    p, dh = torch.sigmoid(gate), dh.double()
+    a, s = gate * p, p + gate * p * (1 - p)
+    want, tol = a * up, (1.1 * eg + 16 * U * gate.abs()) * (up.abs() + eu) + a.abs() * eu + 32 * U * (a * up).abs()
+    within(h, want, tol + (want.abs() + tol) * HALF[BF])
+    # (SiLU's second derivative is 1/2 at most; what rounds: the powers and factors, 256 u of each of two terms)
+    want, tol = dh * up * s, dh.abs() * (up.abs() * (768 * U + 0.5 * eg) + 1.1 * eu)
+    within(dproj[:, 0, :F], want, tol + (want.abs() + tol) * HALF[BF] + 2.0 ** -118)
+    want, tol = dh * a, dh.abs() * (1.1 * eg + 256 * U * a.abs())
+    within(dproj[:, 1, :F], want, tol + (want.abs() + tol) * HALF[BF] + 2.0 ** -118)
+    assert torch.equal(m.molora_gated_linear(x, W), h)

@@ -213,3 +213,30 @@ def test_chains_of_long_sums_write_nothing_wrong(libs, cta, warp):
     assert all(((v == w) | (v == OLD)).all() for w, v in zip(want, out))
     out, e = run(lost)
     assert e == 0 and all(torch.equal(w, v) for w, v in zip(want, out))
+
+
+@pytest.mark.parametrize("cta, warp", [(0, 0), (1, 5), (0, 9)])
+def test_chains_of_wide_inputs_write_nothing_wrong(libs, cta, warp):
+    """Projections of several chains of K blocks: a lost chain is a lost tile, of h as it was, of dproj NaN."""
+    m, lib, lost = libs
+    g = gen(7)
+    N, d, F = 9000, 8400, 264
+    x, _, W, _ = inputs(g, BF, N, d, 2 * F, 0)
+    dh = randn(g, N, F).to(BF)
+
+    def run(lib):
+        e = torch.zeros(1, dtype=torch.int32, device="cuda")
+        out = old(N, F), old(N, 2, F)
+        gated(lib, x, None, W, None, out[0], e)
+        call(lib.molora_gated_linear_backward, p(x), 1, N, d, p(W), F, 2, p(dh), p(out[1]), None, None, p(e))
+        return out, e.item()
+    want, e = run(lib)
+    assert e == 0
+    got = []
+    with_lost(libs, "feed_forward", cta, warp, lambda lib: got.extend(run(lib)))
+    (out, e) = got
+    assert e == m.DEV_WAIT_TIMEOUT
+    assert ((out[0] == want[0]) | (out[0] == OLD)).all() and ((out[1] == want[1]) | torch.isnan(out[1])).all()
+    assert (out[0] != want[0]).any() and torch.isnan(out[1]).any()
+    out, e = run(lost)
+    assert e == 0 and all(torch.equal(w, v) for w, v in zip(want, out))

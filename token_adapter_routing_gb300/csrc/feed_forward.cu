@@ -56,7 +56,8 @@ struct FPlan {
 
 }  // namespace
 
-template <Mode kMode>
+// kLong: d_in is more than kChain K blocks, whose chains registers add.
+template <Mode kMode, bool kLong>
 __global__ void __launch_bounds__(kThreads, 1)
     ff_tc_kernel(const FEpi E, const FPlan P, int32_t* err_word, const __grid_constant__ CUtensorMap map_x,
                  const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_y,
@@ -155,26 +156,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       int s = 0, tc = 0;
       uint32_t phase = 0;
       bool ok = true;
-      for (int32_t pt = pair; pt < P.tiles && ok; pt += pairs, ++tc) {
-        const int buf = tc & 1;
-        if (tc >= 2 && !mbar_wait_spin(&ctrl->tempty[buf], (uint32_t)((tc >> 1) - 1) & 1u, abort)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t d = tmem + (uint32_t)(buf * (P.tmem_cols / 2));
-        for (int kb = 0; kb < nkb; ++kb) {
-          if (!mbar_wait_spin(&ctrl->full[s], phase, abort)) {
+      for (int32_t pt = pair; pt < P.tiles && ok; pt += pairs) {
+        for (int from = 0; ok && from < nkb; ++tc) {
+          const int to = kLong ? min(from + kChain, nkb) : nkb;
+          const int buf = tc & 1;
+          if (tc >= 2 && !mbar_wait_spin(&ctrl->tempty[buf], (uint32_t)((tc >> 1) - 1) & 1u, abort)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t at = (uint32_t)s * (P.stage_bytes >> 4);
-          umma_stage<true, false>(d, a_lo + at, b_lo + at, desc_hi, desc_hi, idesc, kb != 0);
-          umma_commit_pair(&ctrl->empty[s], both);
-          if (++s == S) s = 0, phase ^= 1;
+          const uint32_t d = tmem + (uint32_t)(buf * (P.tmem_cols / 2));
+          for (int kb = from; kb < to; ++kb) {
+            if (!mbar_wait_spin(&ctrl->full[s], phase, abort)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t at = (uint32_t)s * (P.stage_bytes >> 4);
+            umma_stage<true, false>(d, a_lo + at, b_lo + at, desc_hi, desc_hi, idesc, kb != from);
+            umma_commit_pair(&ctrl->empty[s], both);
+            if (++s == S) s = 0, phase ^= 1;
+          }
+          if (ok) umma_commit_pair(&ctrl->tfull[buf], both);
+          from = to;
         }
-        if (ok) umma_commit_pair(&ctrl->tfull[buf], both);
       }
       if (!ok) report(err_word, MOLORA_DEV_WAIT_TIMEOUT);
       umma_commit_pair(&ctrl->done, both);  // arrives in both CTAs once every MMA has completed
@@ -274,26 +279,60 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else if (kMode == kSlopes) {
         for (int c = side; c < chunks; c += 2) fetch(n0 + c * 32, m0);
       }
-      ok = __all_sync(0xffffffffu, mbar_wait_spin(&ctrl->tfull[tc & 1], (uint32_t)(tc >> 1) & 1u, abort));
-      if (!ok) break;
-      tc_fence_after();
-      const uint32_t base = tmem + lanes + (uint32_t)((tc & 1) * (P.tmem_cols / 2));
+      auto sums_ready = [&]() {
+        ok = __all_sync(0xffffffffu, mbar_wait_spin(&ctrl->tfull[tc & 1], (uint32_t)(tc >> 1) & 1u, abort));
+        if (ok) tc_fence_after();
+        return ok;
+      };
       auto free_sums = [&]() {
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster_read(tempty + (tc & 1) * 8);
       };
-      if (side >= chunks) free_sums();
-      for (int c = side; c < chunks; c += 2) {
-        uint32_t rg[32], ru[32];
-        tmem_ld32_start(base + (uint32_t)(c * 32), rg);
-        tmem_ld32_start(base + (uint32_t)(width + c * 32), ru);
-        tmem_ld_wait(rg);
-        tmem_ld_bind(ru);
-        if (c + 2 >= chunks) free_sums();
-        float g[32], u[32];
+      float sums[kLong ? 2 : 1][64];  // kLong: of this warp's chunks, the gate's 32 columns and the up projection's
+      if constexpr (kLong) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) g[i] = __uint_as_float(rg[i]), u[i] = __uint_as_float(ru[i]);
+        for (int k = 0; k < 64; ++k) sums[0][k] = sums[1][k] = 0.f;
+        for (int left = nkb; left > 0 && sums_ready(); left -= kChain) {
+          const uint32_t base = tmem + lanes + (uint32_t)((tc & 1) * (P.tmem_cols / 2));
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            if (side + 2 * n >= chunks) continue;
+#pragma unroll
+            for (int h = 0; h < 64; h += 16) {
+              float r[16];
+              tmem_ld16(base + (uint32_t)((h < 32 ? 0 : width - 32) + (side + 2 * n) * 32 + h), r);
+#pragma unroll
+              for (int k = 0; k < 16; ++k) sums[n][h + k] += r[k];
+            }
+          }
+          free_sums();
+          ++tc;
+        }
+        if (!ok) break;
+      } else {
+        if (!sums_ready()) break;
+        if (side >= chunks) free_sums();
+      }
+      const uint32_t base = tmem + lanes + (uint32_t)((tc & 1) * (P.tmem_cols / 2));
+#pragma unroll(kLong ? 2 : 1)
+      for (int n = 0; n < 2; ++n) {  // (tiles of 256 rows of W at most: two chunks a warp)
+        const int c = side + 2 * n;
+        if (c >= chunks) break;
+        float g[32], u[32];
+        if constexpr (kLong) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) g[i] = sums[n][i], u[i] = sums[n][32 + i];
+        } else {
+          uint32_t rg[32], ru[32];
+          tmem_ld32_start(base + (uint32_t)(c * 32), rg);
+          tmem_ld32_start(base + (uint32_t)(width + c * 32), ru);
+          tmem_ld_wait(rg);
+          tmem_ld_bind(ru);
+          if (c + 2 >= chunks) free_sums();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) g[i] = __uint_as_float(rg[i]), u[i] = __uint_as_float(ru[i]);
+        }
         const int32_t col = n0 + c * 32;
         if constexpr (kMode == kGated) {
           apply_act(g, E.act);
@@ -333,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      ++tc;
+      if (!kLong) ++tc;
     }
     if (!ok) {
       for (; E.tma_res && taken < asked; ++taken) await();  // no copy is left in flight
@@ -699,8 +738,10 @@ cudaError_t launch_tc(const FeedForwardArgs& a, Mode mode, int BN, cudaStream_t 
     const dim3 grid((unsigned)(2 * (p.tiles < most ? p.tiles : most)));
     return launch_kernel(kernel, grid, dim3(kThreads), p.smem, stream, 2, e, p, a.err_word, mx, mw, my, mr);
   };
-  static std::atomic<uint64_t> allowed[2];
-  return mode == kSlopes ? go(ff_tc_kernel<kSlopes>, allowed[0]) : go(ff_tc_kernel<kGated>, allowed[1]);
+  static std::atomic<uint64_t> allowed[4];
+  if (p.nkb > kChain)
+    return mode == kSlopes ? go(ff_tc_kernel<kSlopes, true>, allowed[0]) : go(ff_tc_kernel<kGated, true>, allowed[1]);
+  return mode == kSlopes ? go(ff_tc_kernel<kSlopes, false>, allowed[2]) : go(ff_tc_kernel<kGated, false>, allowed[3]);
 }
 
 // The plan of a product of o_tiles x 128 rows of W with N tokens, in tiles of BN tokens.
