@@ -832,14 +832,14 @@ int best_skinny(const Resident& r, int64_t rows_of_w, int64_t N, int nkb, bool f
 
 int64_t tc_cycles(const FeedForwardArgs& a, const Resident& r, int BN) {
   const int width = a.gated ? BN / 2 : BN;
-  const int64_t m_tiles = (a.N + 2 * kRows - 1) / (2 * kRows);
+  const int64_t m_tiles = (a.N + 2 * kRows - 1) / (2 * kRows), blocks = ff_k_blocks(a);
   const int64_t tiles = m_tiles * (((int64_t)a.d_out + width - 1) / width), waves = (tiles + r.of[2] - 1) / r.of[2];
   if (a.dtype == MOLORA_E4M3) {
     // (rows of y that TMA cannot write: by the byte)
     const int64_t by_lanes = ff_epilogue_of(a).tma_y ? 0 : 15 * width * (a.y_bf16 ? 2 : 4);
-    return 8000 + waves * (ff_k_blocks(a) * (150 + BN * 7 / 5) + 1000 + by_lanes);
+    return 8000 + waves * (blocks * (150 + BN * 7 / 5) + 1000 + by_lanes);
   }
-  return 6300 + waves * (ff_k_blocks(a) * (160 + BN * 8 / 5) + 450);
+  return 6300 + waves * (blocks * (160 + BN * 8 / 5) + 450);
 }
 
 // The pairs' tile of the least cost, if that is below `cost`, else 0.
