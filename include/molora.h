@@ -582,7 +582,9 @@ MOLORA_API molora_status molora_norm_linear_lora_apply(
  * shorter): the x that molora_linear_blocks and molora_gated_linear read.
  *
  *   scale8[t,b] = max(max_{i in block b} |x[t,i]|, 2^-64) / 448
- *   out8[t,i]   = x[t,i] * (1 / scale8[t,b]), as molora_rmsnorm's out8
+ *   out8[t,i]   = x[t,i] / scale8[t,b]
+ *
+ * Both quotients round to fp32 as a division does, out8 then to e4m3 (the nearest, even on a tie; 448 at most).  -0 becomes 0.
  *
  * A NaN in a block makes its scale and all its values NaN; an infinity makes its scale infinite and itself NaN, the
  * block's other values 0.

@@ -1,4 +1,5 @@
-"""The feed-forward kernels at the ends of their ranges: activations over every gate, beside values that have none.
+"""The feed-forward kernels at the ends of their ranges: activations over every gate and beside values that have none, sums of
+many terms, quotients to the last bit.
 
 Tolerances (u = 2^-24, half a step of fp32): an activation's exponent z, 126 at most before its power is flushed, is made with up to
 four roundings of it, so its power is off by 126 ln 2 * 4 u = 350 u; the power itself (4 u), the sum, the products and the
@@ -194,3 +195,35 @@ def test_projections_of_long_sums(m, N, d, F):
     want, tol = dh * a, dh.abs() * (1.1 * eg + 256 * U * a.abs())
     within(dproj[:, 1, :F], want, tol + (want.abs() + tol) * HALF[BF] + 2.0 ** -118)
     assert torch.equal(m.molora_gated_linear(x, W), h)
+
+
+# ---------------------------------------------------------------------------------------- quantiser
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("N, d", [(4096, 4096), (700, 1030), (16, 70001), (5000, 64)])
+def test_quantised_values_are_the_quotients(m, dtype, N, d):
+    """scale8 is the quotient of the largest magnitude and 448, and out8 x / scale8, each rounded to fp32 once and out8 then to
+    e4m3, bit for bit (the expectation: IEEE divisions on the CPU), on values that are often halfway between two of e4m3."""
+    g = gen(d)
+    x = randn(g, N, d) * torch.exp2(torch.randint(-60, 60, (N, 1), generator=g, device="cuda").float())
+    x[::3] = (x[::3].to(BF).float().view(torch.int32) & ~0xfffff).view(F32)  # few bits: more of them halfway
+    x = x.to(dtype)
+    x[:, 5::9], x[:, 3::11] = 0.0, -0.0
+    out8, scale8 = m.molora_quantise_blocks(x)
+    c = torch.nn.functional.pad(x.float().cpu(), (0, -d % 128)).view(N, -1, 128)
+    scale = torch.div(c.abs().amax(2).clamp_min(2.0 ** -64), torch.full((1,), 448.0))
+    want = (torch.div(c, scale[:, :, None]) + torch.where(c == 0, 0.0, -0.0)).clamp(-448, 448).view(N, -1)[:, :d].to(FP8)  # (-0: 0)
+    assert torch.equal(scale8.cpu(), scale)
+    assert torch.equal(out8.cpu().view(torch.uint8), want.view(torch.uint8))
+
+
+def test_scales_of_every_largest_value(m):
+    """Blocks of one value each: every finite bf16 magnitude, and fp32 ones of all sizes."""
+    v = torch.arange(0x7f80, dtype=torch.int32).to(torch.int16).view(BF)
+    g = torch.Generator().manual_seed(4)
+    f = torch.randint(0, 0x7f800000, (1 << 18,), generator=g, dtype=torch.int32).view(F32)
+    for x in (v, f):
+        out8, scale8 = m.molora_quantise_blocks(x.view(-1, 1).cuda())
+        scale = torch.div(x.float().clamp_min(2.0 ** -64), torch.full((1,), 448.0))
+        assert torch.equal(scale8.cpu()[:, 0], scale)
+        want = torch.div(x.float(), scale).clamp(-448, 448).to(FP8)
+        assert torch.equal(out8.cpu()[:, 0].view(torch.uint8), want.view(torch.uint8))

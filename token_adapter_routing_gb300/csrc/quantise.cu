@@ -1,7 +1,9 @@
 // quantise.cu -- rows in e4m3 with a scale for each block of 128 columns, the x of molora_linear_blocks:
 //
-//   scale8[t,b] = max(max_{i in b} |x[t,i]|, 2^-64) / 448,    out8[t,i] = x[t,i] * (1 / scale8[t,b])
+//   scale8[t,b] = max(max_{i in b} |x[t,i]|, 2^-64) / 448,    out8[t,i] = x[t,i] / scale8[t,b]
 //
+// Both quotients round as fp32 divisions do: bf16's eight bits over a scale made of another eight often fall halfway between two
+// e4m3 values, where the product with a rounded reciprocal, a step of fp32 off, takes the other one (1 in 2000).
 // Bound by HBM: bf16 takes 3 bytes an element.  A block is 16 lanes of 8 elements, so a lane's elements are one
 // or two 16-byte loads and one 8-byte store, and the largest value takes 4 shuffles.  A warp takes kUnits pieces of two
 // blocks in a row, all of whose loads are in flight together.
@@ -24,6 +26,20 @@ __device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
+}
+
+// x / s from inv, 1 / s rounded, and minus = -s: the product with inv, corrected by what it leaves of x (Markstein, 1990); for two
+// x in one instruction each.  Three operations for a product's one, but with the scale made so too, in place of the compiler's
+// division, 8192 x 4096 bf16 takes 17.75 us where it took 18.5 (16384 x 512 6.3, 6.1).  -0 becomes 0.
+__device__ __forceinline__ float divide(float x, float inv, float minus) {
+  const float q = x * inv;
+  return fmaf(fmaf(q, minus, x), inv, q);
+}
+__device__ __forceinline__ void divide_pair(float& a, float& b, float inv, float minus) {
+  asm("{\n\t.reg .b64 x, i, m, q, r;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 i, {%2, %2};\n\tmov.b64 m, {%3, %3};\n\t"
+      "mul.rn.f32x2 q, x, i;\n\tfma.rn.f32x2 r, q, m, x;\n\tfma.rn.f32x2 q, r, i, q;\n\tmov.b64 {%0, %1}, q;\n\t}"
+      : "+f"(a), "+f"(b)
+      : "f"(inv), "f"(minus));
 }
 
 // Eight elements of a row: as they are loaded, their largest magnitude (over the 16 lanes of a block), and as floats.
@@ -104,15 +120,20 @@ __global__ void __launch_bounds__(kThreadsQ)
 #pragma unroll
   for (int k = 0; k < kUnits; ++k) {
     const int32_t col = col0 + k * 256;
-    const float scale = max_nan(e[k].largest(), 0x1p-64f) / 448.f, inv = 1.f / scale;
+    const float most = max_nan(e[k].largest(), 0x1p-64f);
+    const bool finite = most < __uint_as_float(0x7f800000u);  // (else there is nothing to correct by)
+    const float scale = finite ? divide(most, 1.f / 448.f, -448.f) : most, inv = 1.f / scale;
     if (col >= d) continue;  // (columns past 2^31 - 1 there are none: d is below 2^31 - 1023)
     if ((lane & 15) == 0) scale8[row * blocks + col / kBlock] = scale;
+    const float minus = finite ? -scale : 0.f;
     float v[8];
     e[k].values(v);
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) divide_pair(v[i], v[i + 1], inv, minus);
     uint32_t packed[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const float2 a = {v[4 * i] * inv, v[4 * i + 1] * inv}, b = {v[4 * i + 2] * inv, v[4 * i + 3] * inv};
+      const float2 a = {v[4 * i], v[4 * i + 1]}, b = {v[4 * i + 2], v[4 * i + 3]};
       packed[i] = __nv_cvt_float2_to_fp8x2(a, __NV_SATFINITE, __NV_E4M3) |
                   (uint32_t)__nv_cvt_float2_to_fp8x2(b, __NV_SATFINITE, __NV_E4M3) << 16;
     }
