@@ -616,7 +616,7 @@ MOLORA_API molora_status molora_linear_blocks(const void* x, const float* x_scal
 
 /*
  * molora_gated_linear -- the gated half of a feed-forward block: both projections, the activation and their product
- * in one kernel.
+ * in one kernel.  g and u never reach memory, so it is for blocks whose gate and up projections have no adapters.
  *
  *   g = x Wg^T,  u = x Wu^T,  h[t,f] = act(g[t,f]) * u[t,f]
  *

@@ -7,7 +7,8 @@
 //
 // Both projections of the gated block are one product: a tile's columns are as many rows of Wg as of Wu, so that the
 // sums of g[t,f] and u[t,f] meet in the registers of one thread and neither goes to memory.  The backward pass makes
-// them again: at 4096 x 2048 -> 6144 their 200 MB in fp32, written and read back, would take 85 us, the product takes 107.
+// them again, for the memory, not the time: at 4096 x 2048 -> 6144 they are 200 MB in fp32 that every layer would hold from
+// one pass to the other; writing and reading them back would take 60 us, part of it under the forward's MMAs, the product takes 107.
 //
 // ff_tc_kernel (bf16, many tokens): linear_tc_kernel's pipeline (linear.cu): persistent pairs of CTAs with tiles of 256 tokens x
 //   BN rows of W, a TMA warp and an MMA warp ahead of 8 epilogue warps by two TMEM accumulators.
@@ -865,6 +866,11 @@ cudaError_t launch_feed_forward(const FeedForwardArgs& a, cudaStream_t stream) {
 #ifdef MOLORA_TUNING_ENV
   if (const char* g = getenv("MOLORA_FF_SKINNY")) split = atoi(g), cost = split ? 0 : INT64_MAX;
 #endif
+  // Up to 32 tokens are bound by reading W, of which the costs, cycles of the tensor cores' side, say nothing: there clusters that
+  // split d_in read faster than the pairs, whatever their tiles.  Of 90 sizes (each of the three products; 1, 16 and 32 tokens;
+  // d_in 128 to 16384, 4096 to 65536 outputs) few tokens' kernel took 0.48 to 1.00 of the pairs' time at 73, 1.01 to 1.16 at 8 (wide
+  // W, short rows) and 1.04 to 1.59 at 128 -> 65536 (e4m3 blocks, 32 tokens, us: 4096 -> 4096 8.0 and 13.3, 1024 -> 28672 14.9
+  // and 12.9).
   const int pairs = a.N <= 32 && cost < INT64_MAX ? 0 : best_tc(a, r, cost);
   if (!pairs) return launch_skinny(a, r, split, stream);
   return a.dtype == MOLORA_E4M3 ? launch_blocks_tc(a, pairs, stream) : launch_tc(a, kGated, pairs, stream);

@@ -9,6 +9,7 @@
 // No operand is transposed in memory: what is not K-major (W in dx, both operands in dW) is read by the tensor
 // cores as it lies, MN-major, in boxes of 64 columns x 64 rows of K.  Bound by the tensor cores: 4096 x 2048 -> 6144, both
 // products, 250 us (1.65 PFLOP/s).
+// Sums of more than kChain K blocks (2 d_ff or N past 8192) are chains that registers add.
 // Few tokens leave most pairs without a tile of dx, and the others with sums of 2 d_ff terms: there ff_skinny_kernel
 // (feed_forward.cu) makes dx, d_ff split over clusters.
 #include <cudaTypedefs.h>
