@@ -606,7 +606,8 @@ MOLORA_API molora_status molora_quantise_blocks(const void* x, molora_dtype dtyp
  * A block's products are summed by the tensor cores, the scaled blocks in fp32 in order; the epilogue is fp32 and y is rounded
  * once.  d_in is a multiple of 16 (else MOLORA_ERR_UNSUPPORTED); N, d_in, d_out up to 2^31 - 1024; x and W are 16-byte aligned,
  * the other arrays start on a boundary of their element's size.  y shares no memory with another array but may be the
- * residual.  Results are reproducible bit for bit.  Outputs that a wait that ran out (MOLORA_DEV_WAIT_TIMEOUT) left without
+ * residual.  Results are reproducible bit for bit (by calls of the same sizes, types and alignment, which choose the kernel and
+ * with it the order of the sums).  Outputs that a wait that ran out (MOLORA_DEV_WAIT_TIMEOUT) left without
  * their sums are NaN, or stay as they were; the others are right.
  */
 MOLORA_API molora_status molora_linear_blocks(const void* x, const float* x_scale, int64_t N, int32_t d_in, const void* W,
@@ -627,7 +628,7 @@ MOLORA_API molora_status molora_linear_blocks(const void* x, const float* x_scal
  * sums); h is made of them unrounded and rounded once.
  * d_in is a multiple of 8 (MOLORA_BF16) or 16 (MOLORA_E4M3), else MOLORA_ERR_UNSUPPORTED; d_ff up to 2^30 - 512, N and d_in
  * up to 2^31 - 1024; x and W are 16-byte aligned, the other arrays start on a boundary of their element's size.  h shares no
- * memory with another array.  Results are reproducible bit for bit.  Lost waits as for molora_linear_blocks.
+ * memory with another array.  Reproducible bits and lost waits as for molora_linear_blocks.
  * The way back to the model's width is molora_linear (or molora_quantise_blocks and molora_linear_blocks) with the residual.
  */
 MOLORA_API molora_status molora_gated_linear(const void* x, molora_dtype dtype, const float* x_scale, int64_t N, int32_t d_in,
@@ -648,7 +649,7 @@ MOLORA_API molora_status molora_gated_linear(const void* x, molora_dtype dtype, 
  * to; N == 0 makes dW zero.  act' of RELU is 0 at 0.  Sums are fp32, on the tensor cores in chains of 8192 terms at most (their
  * additions cut what they lose: sums of one sign come out up to 3e-5 short, whatever N and d_ff); outputs are rounded once.
  * Sizes and alignment as for molora_gated_linear; dproj, dx and dW are 16-byte aligned too.  No output shares memory with
- * another array.  Results are reproducible bit for bit.  Lost waits as for molora_linear_blocks.
+ * another array.  Reproducible bits and lost waits as for molora_linear_blocks.
  */
 MOLORA_API molora_status molora_gated_linear_backward(const void* x, molora_dtype dtype, int64_t N, int32_t d_in, const void* W,
                                            int32_t d_ff, molora_activation act, const void* dh, void* dproj, void* dx,
